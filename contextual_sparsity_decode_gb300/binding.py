@@ -38,7 +38,8 @@ EXPORTS = (
     "dv_sparse_attn_workspace_size", "dv_sparse_attn", "dv_kv_repair",
     "dv_layernorm", "dv_positions_advance", "dv_set_launch_overlap", "dv_set_wait_limit_ns",
     "dv_kernel_launches", "dv_label_workspace_size", "dv_label_neurons", "dv_label_heads",
-    "dv_select_scores",
+    "dv_select_scores", "dv_tree_attn_workspace_size", "dv_tree_attn", "dv_kv_compact", "dv_kv_reorder",
+    "dv_beam_select_workspace_size", "dv_beam_select",
 )
 
 
@@ -97,6 +98,16 @@ _SIGS = {
                        _c_int),
     "dv_select_scores": ([_vp, _c_int, _c_int, _c_int, _c_int, _c_float, _vp, _c_int, _vp, _vp, _sz, _vp],
                          _c_int),
+    "dv_tree_attn_workspace_size": ([_c_int, _c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_sz)], _c_int),
+    "dv_tree_attn": ([_vp, _c_int, _c_int, _c_int, _c_int, _c_int, ctypes.POINTER(dv_kv), _vp, _vp, _vp, _c_int,
+                      _vp, _c_int, _vp, _c_float, _c_int, _vp, _vp, _sz, _vp], _c_int),
+    "dv_kv_compact": ([ctypes.POINTER(dv_kv), _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _vp,
+                       _c_int, _vp, _vp, _sz, _vp], _c_int),
+    "dv_kv_reorder": ([ctypes.POINTER(dv_kv), _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp,
+                       _c_int, _vp, _sz, _vp], _c_int),
+    "dv_beam_select_workspace_size": ([_c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_sz)], _c_int),
+    "dv_beam_select": ([_vp, _c_int, _c_int, _c_int, ctypes.c_longlong, _c_int, _vp, _vp, _c_int, _c_int, _vp,
+                        _vp, _vp, _vp, _sz, _vp], _c_int),
 }
 
 
@@ -270,7 +281,8 @@ def dv_sparse_mlp(y, W1n, W2n, idx, count, out, ws, accumulate=False, stream=Non
 
 class KV:
     """A batch's per-layer KV cache: K, V [B][h][n_max][d_h], X [B][n_max][d],
-    valid [B][h][n_max] (uint8)."""
+    valid [B][h][n_max] (uint8).  dv_tree_attn reads K and V alone: X and
+    valid may be None there."""
 
     def __init__(self, K, V, X, valid):
         self.K, self.V, self.X, self.valid = K, V, X, valid
@@ -284,8 +296,30 @@ class KV:
                    torch.zeros(B, h, n_max, dtype=torch.uint8, device=device))
 
     def c(self) -> dv_kv:
-        return dv_kv(self.K.data_ptr(), self.V.data_ptr(), self.X.data_ptr(),
-                     self.valid.data_ptr(), self.n_max)
+        return dv_kv(self.K.data_ptr(), self.V.data_ptr(),
+                     None if self.X is None else self.X.data_ptr(),
+                     None if self.valid is None else self.valid.data_ptr(), self.n_max)
+
+
+class KVLayers:
+    """The caches of a decoder's layers, all of one shape, as one argument of
+    dv_kv_compact and dv_kv_reorder (the descriptors are built once)."""
+
+    def __init__(self, kvs: Sequence[KV]):
+        self.kvs = list(kvs)
+        kv = self.kvs[0]
+        self.B, self.h, self.n_max, self.d_h = kv.K.shape
+        self.d, self.dt = kv.X.shape[2], _dt(kv.K)
+        for c in self.kvs:
+            for t, shape in ((c.K, kv.K.shape), (c.V, kv.K.shape), (c.X, (self.B, self.n_max, self.d))):
+                _laid_out(t, shape, kv.K.dtype, "KVLayers")
+            _laid_out(c.valid, kv.K.shape[:3], torch.uint8, "KVLayers")
+        self.array = (dv_kv * len(self.kvs))(*[c.c() for c in self.kvs])
+
+
+def _laid_out(t: torch.Tensor, shape, dtype, where: str) -> None:
+    if t.shape != torch.Size(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise DvError(1, where, f"a contiguous {tuple(shape)} tensor of {dtype} is wanted")
 
 
 def dv_sparse_attn_workspace_size(B, d, h, d_h, cap, n_max) -> int:
@@ -313,6 +347,76 @@ def dv_kv_repair(kv: KV, Wqkv, pos, head_idx, head_count, ws, stream=None):
     _ok(lib().dv_kv_repair(ctypes.byref(c), B, d, h, d_h, _ptr(Wqkv), _ptr(pos), _ptr(head_idx),
                            head_idx.shape[-1], _ptr(head_count), _dt(Wqkv), _ptr(ws), ws.numel(),
                            _stream(stream)), "dv_kv_repair")
+
+
+# --------------------------------------------------------------------- several candidates per sequence
+
+def dv_tree_attn_workspace_size(B: int, T: int, h: int, group: int, d_h: int) -> int:
+    n = ctypes.c_size_t(0)
+    _ok(lib().dv_tree_attn_workspace_size(B, T, h, group, d_h, ctypes.byref(n)), "dv_tree_attn_workspace_size")
+    return n.value
+
+
+def dv_tree_attn(q, kv: KV, pos, scale, out, ws, mask=None, nodes=None, head_idx=None, head_count=None, stream=None):
+    """q, out [B][T][h g][d_h]; mask [T][T] or [B][T][T], bool or uint8 (None:
+    a linear draft); see dv_tree_attn in dv.h."""
+    B, T, hq, d_h = q.shape
+    h = kv.K.shape[1]
+    where = "dv_tree_attn"
+    shape = (B, h, kv.n_max, d_h)
+    _laid_out(q, (B, T, hq, d_h), kv.K.dtype, where)
+    _laid_out(out, (B, T, hq, d_h), kv.K.dtype, where)
+    _laid_out(kv.K, shape, kv.K.dtype, where)
+    _laid_out(kv.V, shape, kv.K.dtype, where)
+    if hq % h:
+        raise DvError(1, where, f"{hq} query heads on {h} K/V heads")
+    batched = 0
+    if mask is not None:
+        batched = int(mask.dim() == 3)
+        _laid_out(mask, (B, T, T) if batched else (T, T), torch.bool if mask.dtype == torch.bool else torch.uint8, where)
+    c = kv.c()
+    _ok(lib().dv_tree_attn(_ptr(q), B, T, h, hq // h, d_h, ctypes.byref(c), _ptr(pos), _ptr(nodes), _ptr(mask),
+                           batched, _ptr(head_idx), 0 if head_idx is None else head_idx.shape[-1], _ptr(head_count),
+                           float(scale), _dt(q), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), where)
+
+
+def dv_kv_compact(layers: KVLayers, pos, idx, count, ws, new_pos=None, stream=None):
+    """Keep nodes idx[b][:count[b]] of each tree (see dv_kv_compact in dv.h)."""
+    _ok(lib().dv_kv_compact(layers.array, len(layers.array), layers.B, layers.d, layers.h, layers.d_h, _ptr(pos),
+                            _ptr(idx), idx.shape[-1], _ptr(count), layers.dt, _ptr(new_pos), _ptr(ws), ws.numel(),
+                            _stream(stream)), "dv_kv_compact")
+
+
+def dv_kv_reorder(layers: KVLayers, pos, parent, ws, start=None, stream=None):
+    """Beam w of sequence s (cache row s * width + w) continues beam
+    parent[s][w] (see dv_kv_reorder in dv.h)."""
+    n_seq, width = parent.shape
+    if n_seq * width != layers.B:
+        raise DvError(1, "dv_kv_reorder", f"{n_seq} x {width} beams on {layers.B} cache rows")
+    _ok(lib().dv_kv_reorder(layers.array, len(layers.array), n_seq, width, layers.d, layers.h, layers.d_h, _ptr(pos),
+                            _ptr(start), _ptr(parent), layers.dt, _ptr(ws), ws.numel(), _stream(stream)),
+        "dv_kv_reorder")
+
+
+def dv_beam_select_workspace_size(n_seq: int, width: int, V: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _ok(lib().dv_beam_select_workspace_size(n_seq, width, V, K, ctypes.byref(n)), "dv_beam_select_workspace_size")
+    return n.value
+
+
+def dv_beam_select(logits, cum, score, token, beam, ws, done=None, end_token=0, stream=None):
+    """logits [n_seq][width][V] (rows evenly spaced, tokens adjacent), cum
+    [n_seq][width]; score, token, beam [n_seq][K] (see dv_beam_select in dv.h)."""
+    S, W, V = logits.shape
+    K = score.shape[1]
+    s0, s1, s2 = logits.stride()
+    if W == 1:
+        s1 = s0 if S > 1 else V
+    if (V > 1 and s2 != 1) or (S > 1 and s0 != W * s1):
+        raise DvError(1, "dv_beam_select", "rows of logits evenly spaced, tokens adjacent")
+    _ok(lib().dv_beam_select(_ptr(logits), S, W, V, s1, _dt(logits), _ptr(cum), _ptr(done), int(end_token), K,
+                             _ptr(score), _ptr(token), _ptr(beam), _ptr(ws), ws.numel(), _stream(stream)),
+        "dv_beam_select")
 
 
 # --------------------------------------------------------------------- labels

@@ -176,6 +176,36 @@ LabelWs carve_label(Carver& c, int T, int N, int h, int d_h, bool heads) {
   return w;
 }
 
+struct TreeWs {
+  int32_t* ctr;
+  float2* ml;
+  float* part;
+};
+int tree_rows(int T, int group) { return T * group < kTreeRows ? T * group : kTreeRows; }
+TreeWs carve_tree(Carver& c, int T, int group, int d_h) {
+  TreeWs w{};
+  const size_t rows = (size_t)2 * kTreeCtas * tree_rows(T, group);
+  w.ctr = c.take<int32_t>(kTreeCtas);
+  w.ml = c.take<float2>(rows);
+  w.part = c.take<float>(rows * d_h);
+  return w;
+}
+
+struct BeamWs {
+  int32_t* ctr;
+  float2* stat;
+  int2* cand;
+};
+int beam_chunks(int V) { return (V + kBeamChunk - 1) / kBeamChunk; }
+BeamWs carve_beam(Carver& c, int n_seq, int width, int V, int K) {
+  BeamWs w{};
+  const size_t rows = (size_t)n_seq * width * beam_chunks(V);
+  w.ctr = c.take<int32_t>((size_t)n_seq);
+  w.stat = c.take<float2>(rows);
+  w.cand = c.take<int2>(rows * K);
+  return w;
+}
+
 // ---- validation ---------------------------------------------------------------------
 
 dv_status check_pred(const void* y, int B, int d, dv_dtype dt, const dv_predictor* preds,
@@ -506,6 +536,140 @@ dv_status dv_select_scores(const float* scores, int B, int N, dv_select mode, in
   if (mode == DV_TOPK && (k < 0 || k > N || k > cap)) return DV_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, sizeof(WsHeader))) return DV_ERR_WORKSPACE;
   cudaError_t e = launch_select(scores, B, N, (int)mode, k, t, idx, cap, count, static_cast<WsHeader*>(ws), stream);
+  return e == cudaSuccess ? DV_OK : cuda_fail(e);
+}
+
+// ---- several candidates per sequence --------------------------------------------------------------
+
+namespace {
+bool tree_shape_ok(int B, int T, int h, int group) {
+  return B >= 1 && B <= kTreeMaxB && T >= 1 && T <= 1024 && h >= 1 && h <= 1024 && group >= 1 && group <= 64;
+}
+
+// Caches of one shape, as dv_kv_compact and dv_kv_reorder take them.
+dv_status check_layers(const dv_kv* kv, int n_kv, int d, int h, int d_h, dv_dtype dt) {
+  if (!dtype_ok(dt)) return DV_ERR_DTYPE;
+  if (!kv || n_kv < 1 || n_kv > 1024 || d < 1 || d % vec_of(dt) || d_h < 1 || d_h % vec_of(dt) || h < 1 || h > 1024)
+    return DV_ERR_INVALID_ARG;
+  for (int l = 0; l < n_kv; ++l) {
+    const dv_kv& c = kv[l];
+    if (!c.K || !c.V || !c.X || !c.valid || !aligned16(c.K) || !aligned16(c.V) || !aligned16(c.X) ||
+        !aligned16(c.valid) || c.n_max < 1 || c.n_max > 1048576 || c.n_max != kv[0].n_max)
+      return DV_ERR_INVALID_ARG;
+  }
+  return DV_OK;
+}
+
+KvMove make_move(const dv_kv* kv, int n_kv, int B, int d, int h, int d_h, const int32_t* pos, dv_dtype dt) {
+  KvMove m{};
+  m.kv = kv; m.n_kv = n_kv; m.B = B; m.h = h; m.n_max = kv[0].n_max;
+  m.kv_chunks = d_h / vec_of(dt); m.x_chunks = d / vec_of(dt); m.pos = pos;
+  return m;
+}
+
+bool beam_shape_ok(int n_seq, int width, int V, int K) {
+  return n_seq >= 1 && n_seq <= 65535 && width >= 1 && width <= kBeamMaxWidth && V >= 1 && V <= 4194304 && K >= 1 &&
+         K <= kBeamMaxK && (long long)K <= (long long)width * V;
+}
+}  // namespace
+
+dv_status dv_tree_attn_workspace_size(int B, int T, int h, int group, int d_h, size_t* bytes) {
+  if (!bytes || !tree_shape_ok(B, T, h, group)) return DV_ERR_INVALID_ARG;
+  if (d_h != 64 && d_h != 128) return DV_ERR_UNSUPPORTED;
+  Carver c(nullptr);
+  carve_tree(c, T, group, d_h);
+  *bytes = c.size();
+  return DV_OK;
+}
+
+dv_status dv_tree_attn(const void* q, int B, int T, int h, int group, int d_h, const dv_kv* kv, const int32_t* pos,
+                       const int32_t* nodes, const uint8_t* mask, int mask_batched, const int32_t* head_idx, int cap,
+                       const int32_t* head_count, float scale, dv_dtype dt, void* out, void* ws, size_t ws_bytes,
+                       cudaStream_t stream) {
+  Range nvtx_range("dv_tree_attn");
+  if (!dtype_ok(dt)) return DV_ERR_DTYPE;
+  if (!q || !kv || !kv->K || !kv->V || !pos || !out || !head_idx != !head_count) return DV_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(kv->K) || !aligned16(kv->V) || !aligned16(out) || !aligned4(pos) ||
+      !aligned4(nodes) || !aligned4(head_idx) || !aligned4(head_count))
+    return DV_ERR_INVALID_ARG;
+  if (!tree_shape_ok(B, T, h, group)) return DV_ERR_INVALID_ARG;
+  if (d_h != 64 && d_h != 128) return DV_ERR_UNSUPPORTED;
+  if (head_idx && (cap < 1 || cap > h)) return DV_ERR_INVALID_ARG;
+  if (kv->n_max < 16 || kv->n_max > 1048576 || kv->n_max % 16) return DV_ERR_INVALID_ARG;
+  Carver meas(nullptr);
+  carve_tree(meas, T, group, d_h);
+  if (!ws_ok(ws, ws_bytes, meas.size())) return DV_ERR_WORKSPACE;
+  Carver c(ws);
+  const TreeWs w = carve_tree(c, T, group, d_h);
+  TreeLaunch L{};
+  L.q = q; L.out = out; L.K = kv->K; L.V = kv->V; L.n_max = kv->n_max;
+  L.pos = pos; L.nodes = nodes; L.mask = mask; L.mask_stride = mask_batched ? (long long)T * T : 0;
+  L.head_idx = head_idx; L.cap = cap; L.head_count = head_count;
+  L.B = B; L.T = T; L.h = h; L.g = group; L.d_h = d_h; L.scale = scale;
+  L.part = w.part; L.ml = w.ml; L.ctr = w.ctr; L.rows_pad = tree_rows(T, group);
+  cudaError_t e = launch_tree_attn(L, dt, static_cast<WsHeader*>(ws), num_sms_current(), stream);
+  return e == cudaSuccess ? DV_OK : cuda_fail(e);
+}
+
+dv_status dv_kv_compact(const dv_kv* kv, int n_kv, int B, int d, int h, int d_h, const int32_t* pos,
+                        const int32_t* idx, int cap, const int32_t* count, dv_dtype dt, int32_t* new_pos, void* ws,
+                        size_t ws_bytes, cudaStream_t stream) {
+  Range nvtx_range("dv_kv_compact");
+  dv_status st = check_layers(kv, n_kv, d, h, d_h, dt);
+  if (st != DV_OK) return st;
+  if (!pos || !idx || !count || !aligned4(pos) || !aligned4(idx) || !aligned4(count) || !aligned4(new_pos) ||
+      B < 1 || B > 65535 || cap < 1)
+    return DV_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, sizeof(WsHeader))) return DV_ERR_WORKSPACE;
+  cudaError_t e = launch_kv_compact(make_move(kv, n_kv, B, d, h, d_h, pos, dt), idx, cap, count, new_pos,
+                                    static_cast<WsHeader*>(ws), stream);
+  return e == cudaSuccess ? DV_OK : cuda_fail(e);
+}
+
+dv_status dv_kv_reorder(const dv_kv* kv, int n_kv, int n_seq, int width, int d, int h, int d_h, const int32_t* pos,
+                        const int32_t* start, const int32_t* parent, dv_dtype dt, void* ws, size_t ws_bytes,
+                        cudaStream_t stream) {
+  Range nvtx_range("dv_kv_reorder");
+  dv_status st = check_layers(kv, n_kv, d, h, d_h, dt);
+  if (st != DV_OK) return st;
+  if (!pos || !parent || !aligned4(pos) || !aligned4(start) || !aligned4(parent) || n_seq < 1 || n_seq > 1023 ||
+      width < 1 || width > 32)
+    return DV_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, sizeof(WsHeader))) return DV_ERR_WORKSPACE;
+  cudaError_t e = launch_kv_reorder(make_move(kv, n_kv, n_seq * width, d, h, d_h, pos, dt), width, start, parent,
+                                    static_cast<WsHeader*>(ws), stream);
+  return e == cudaSuccess ? DV_OK : cuda_fail(e);
+}
+
+dv_status dv_beam_select_workspace_size(int n_seq, int width, int V, int K, size_t* bytes) {
+  if (!bytes || !beam_shape_ok(n_seq, width, V, K)) return DV_ERR_INVALID_ARG;
+  Carver c(nullptr);
+  carve_beam(c, n_seq, width, V, K);
+  *bytes = c.size();
+  return DV_OK;
+}
+
+dv_status dv_beam_select(const void* logits, int n_seq, int width, int V, long long row_stride, dv_dtype dt,
+                         const float* cum, const uint8_t* done, int end_token, int K, float* score, int32_t* token,
+                         int32_t* beam, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  Range nvtx_range("dv_beam_select");
+  if (!dtype_ok(dt)) return DV_ERR_DTYPE;
+  if (!logits || !cum || !score || !token || !beam || !aligned4(cum) || !aligned4(score) || !aligned4(token) ||
+      !aligned4(beam) || (reinterpret_cast<uintptr_t>(logits) & (dt == DV_F32 ? 3u : 1u)))
+    return DV_ERR_INVALID_ARG;
+  if (!beam_shape_ok(n_seq, width, V, K) || row_stride < V) return DV_ERR_INVALID_ARG;
+  if (done && (end_token < 0 || end_token >= V)) return DV_ERR_INVALID_ARG;
+  Carver meas(nullptr);
+  carve_beam(meas, n_seq, width, V, K);
+  if (!ws_ok(ws, ws_bytes, meas.size())) return DV_ERR_WORKSPACE;
+  Carver c(ws);
+  const BeamWs w = carve_beam(c, n_seq, width, V, K);
+  BeamLaunch L{};
+  L.logits = logits; L.ld = row_stride; L.cum = cum; L.done = done; L.end = end_token;
+  L.S = n_seq; L.W = width; L.V = V; L.K = K; L.chunks = beam_chunks(V);
+  L.score = score; L.token = token; L.beam = beam;
+  L.stat = w.stat; L.cand = w.cand; L.ctr = w.ctr;
+  cudaError_t e = launch_beam_select(L, dt, stream);
   return e == cudaSuccess ? DV_OK : cuda_fail(e);
 }
 

@@ -279,6 +279,62 @@ struct CombineLaunch {
 };
 cudaError_t launch_rows_combine(const CombineLaunch& a, dv_dtype dt, cudaStream_t stream);
 
+// ---- several candidates per sequence -------------------------------------------
+
+// Attention of a drafted token tree over the KV cache (k_tree_attn.cu).
+constexpr int kTreeMaxB = 512;     // sequences (their lengths are staged in shared memory)
+constexpr int kTreeCtas = 152;     // CTAs of the persistent grid, at most
+constexpr int kTreeRows = 128;     // query rows of one unit, at most
+struct TreeLaunch {
+  const void* q; void* out;                  // [B][T][h g][d_h]
+  const void* K; const void* V; int n_max;   // [B][h][n_max][d_h]
+  const int32_t* pos; const int32_t* nodes;  // [B]; nodes may be null (T)
+  const uint8_t* mask; long long mask_stride;  // [T][T] per sequence (stride 0: shared), null: causal
+  const int32_t* head_idx; int cap; const int32_t* head_count;  // null: every head
+  int B, T, h, g, d_h;
+  float scale;
+  // scratch: partial results of units that several CTAs share
+  float* part;      // [2 kTreeCtas][d_h / 4][rows_pad][4]
+  float2* ml;       // [2 kTreeCtas][rows_pad] running maximum and sum
+  int* ctr;         // [kTreeCtas], zero between calls
+  int rows_pad;     // min(kTreeRows, T g)
+};
+cudaError_t launch_tree_attn(const TreeLaunch& a, dv_dtype dt, WsHeader* hdr, int num_sms, cudaStream_t stream);
+
+// Moving rows of the KV cache (k_kv_move.cu).
+constexpr int kKvLayers = 64;      // caches of one launch
+struct KvPtrs {
+  char* K; char* V; char* X; uint8_t* valid;
+};
+struct KvMove {
+  const dv_kv* kv; int n_kv;
+  int B, h, n_max;
+  int kv_chunks, x_chunks;         // 16-byte chunks of a K/V row and of an X row
+  const int32_t* pos;
+  KvPtrs kv_at(int l) const {
+    return KvPtrs{static_cast<char*>(kv[l].K), static_cast<char*>(kv[l].V), static_cast<char*>(kv[l].X), kv[l].valid};
+  }
+};
+cudaError_t launch_kv_compact(const KvMove& m, const int32_t* idx, int cap, const int32_t* count, int32_t* new_pos,
+                              WsHeader* hdr, cudaStream_t stream);
+cudaError_t launch_kv_reorder(const KvMove& m, int width, const int32_t* start, const int32_t* parent, WsHeader* hdr,
+                              cudaStream_t stream);
+
+// Beam selection (k_beam.cu).
+constexpr int kBeamChunk = 8192;   // tokens per CTA
+constexpr int kBeamMaxWidth = 32;
+constexpr int kBeamMaxK = 64;
+struct BeamLaunch {
+  const void* logits; long long ld;          // [S][W] rows of V, ld elements apart
+  const float* cum; const uint8_t* done; int end;
+  int S, W, V, K, chunks;
+  float* score; int32_t* token; int32_t* beam;  // [S][K]
+  float2* stat;    // [S W][chunks] maximum and sum of exponentials
+  int2* cand;      // [S W][chunks][K] (value bits, token)
+  int* ctr;        // [S], zero between calls
+};
+cudaError_t launch_beam_select(const BeamLaunch& a, dv_dtype dt, cudaStream_t stream);
+
 // ---- misc (k_misc.cu) --------------------------------------------------------
 
 cudaError_t launch_layernorm(const float* x, int B, int d, float eps, void* y,

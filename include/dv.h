@@ -294,6 +294,107 @@ dv_status dv_select_scores(const float* scores, int B, int N, dv_select mode,
                            int32_t* count, void* ws, size_t ws_bytes,
                            cudaStream_t stream);
 
+/* ------------------------------------------- several candidates per sequence */
+
+/* Workspace bytes of dv_tree_attn for trees of up to T nodes. */
+dv_status dv_tree_attn_workspace_size(int B, int T, int h, int group, int d_h,
+                                      size_t* bytes);
+
+/* Attention of a drafted token tree over the KV cache: the queries of T
+ * drafted tokens (nodes) per sequence against the committed positions and the
+ * nodes' own K/V, in one pass over the cache (the pages have no counterpart:
+ * a step there has one token).  The nodes of sequence b occupy the cache
+ * positions pos[b] .. pos[b] + nodes[b] - 1; write their embeddings into X
+ * there, clear their valid flags and let dv_kv_repair (with pos + nodes)
+ * compute their K/V together with whatever the selected heads had skipped:
+ * the valid flags themselves are not read here.
+ *     out[b][t][i g + e] = sum_j p_j V[b][i][j] / sum_j p_j,
+ *     p_j = exp(scale q[b][t][i g + e] . K[b][i][j]),   g = group, e < g,
+ * over j < pos[b] and j = pos[b] + u for the nodes u that t sees.
+ *  q, out [B][T][h g][d_h], storage type: g query heads share a K/V head
+ *     (g = 1: one each, as in dv_sparse_attn).  out must not overlap q.
+ *  nodes [B], or NULL: T nodes in every tree (0 <= nodes[b] <= T).
+ *  mask: bytes, [T][T] for every sequence (mask_batched = 0) or [B][T][T]
+ *     (1); node t sees node u where mask[t][u] != 0.  NULL: u <= t, a linear
+ *     draft or a chunk of a prompt.  K/V of a node that a row does not see do
+ *     not reach that row, whatever they hold.
+ *  head_idx [B][cap] with head_count [B]: the K/V heads of each sequence's
+ *     tree, as in dv_sparse_attn; both NULL: all h heads.
+ * Every row of out is written: those of other heads, of nodes behind
+ * nodes[b], and of nodes that see nothing are 0.  Maximum, sum and numerator
+ * are held in fp32, and results repeat bit for bit.
+ * Device errors: DV_ERR_POSITION (pos[b] < 0 or pos[b] + nodes[b] > n_max:
+ * the sequence's rows are 0), DV_ERR_INDEX_RANGE (head skipped: its rows are
+ * 0), DV_ERR_CAPACITY (count above cap, or nodes above T: cut off).
+ * Limits: B <= 512, T <= 1024, h <= 1024, group <= 64, d_h in {64, 128}
+ * (others DV_ERR_UNSUPPORTED), n_max <= 1048576, a multiple of 16. */
+dv_status dv_tree_attn(const void* q, int B, int T, int h, int group, int d_h,
+                       const dv_kv* kv, const int32_t* pos,
+                       const int32_t* nodes, const uint8_t* mask,
+                       int mask_batched, const int32_t* head_idx, int cap,
+                       const int32_t* head_count, float scale, dv_dtype dt,
+                       void* out, void* ws, size_t ws_bytes,
+                       cudaStream_t stream);
+
+/* Keep the accepted nodes of a drafted tree: in each of the n_kv caches (a
+ * decoder's layers) the rows of positions pos[b] + idx[b][k] move to
+ * pos[b] + k, k < count[b], in place -- K and V where the valid flag is set,
+ * X and the flags always.  idx [B][cap] is strictly ascending in every row
+ * (a path of the tree in the order of its nodes).  Nothing else changes: the
+ * flags behind the kept rows stay (they are cleared when the next tree's
+ * rows are written).  new_pos [B] = pos + count, unless NULL; it may be pos.
+ * Device errors: DV_ERR_INDEX_RANGE (a list that is negative or does not
+ * ascend) and DV_ERR_POSITION (a position outside the cache): nothing moves
+ * in that sequence, new_pos = pos; DV_ERR_CAPACITY: count cut off at cap.
+ * All caches have the same shape and n_max.  ws: at least 256 bytes,
+ * zero-filled once.  Limits: n_kv <= 1024, B <= 65535, h <= 1024. */
+dv_status dv_kv_compact(const dv_kv* kv, int n_kv, int B, int d, int h, int d_h,
+                        const int32_t* pos, const int32_t* idx, int cap,
+                        const int32_t* count, dv_dtype dt, int32_t* new_pos,
+                        void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Let beam w of each sequence continue beam parent[s][w]: in each of the n_kv
+ * caches, whose rows are s * width + w, positions start[s] .. pos - 1 of row w
+ * become those of row parent[s][w], all beams at once and in place, pos being
+ * that of the parent's row (pos [n_seq][width]: positions held).  K and V
+ * move where the parent's valid flag is set, X and the flags always; a beam
+ * that continues itself is left alone, and so are positions below start (a
+ * prompt that the beams share; NULL: 0) and behind.  pos itself is not
+ * changed: where a sequence's beams differ in length, gather it by parent.
+ * Device errors: DV_ERR_INDEX_RANGE (a parent outside [0, width)) and
+ * DV_ERR_POSITION (a pos outside [0, n_max]): that beam is left alone.
+ * ws: at least 256 bytes, zero-filled once.  Limits: n_kv <= 1024,
+ * n_seq <= 1023, width <= 32, h <= 1024. */
+dv_status dv_kv_reorder(const dv_kv* kv, int n_kv, int n_seq, int width, int d,
+                        int h, int d_h, const int32_t* pos,
+                        const int32_t* start, const int32_t* parent,
+                        dv_dtype dt, void* ws, size_t ws_bytes,
+                        cudaStream_t stream);
+
+/* Workspace bytes of dv_beam_select. */
+dv_status dv_beam_select_workspace_size(int n_seq, int width, int V, int K,
+                                        size_t* bytes);
+
+/* The K best continuations of each sequence over its beams and the vocabulary:
+ *     score(w, v) = cum[s][w] + logits[s][w][v] - log sum_u exp(logits[s][w][u]),
+ * by score descending, ties to the lower w V + v; into score (fp32), token and
+ * beam (the w it continues), each [n_seq][K].  K = width gives the next beams
+ * and their parents for dv_kv_reorder; a larger K leaves a choice.
+ *  logits [n_seq][width] rows of V, row_stride elements apart; any alignment.
+ *  done [n_seq][width], or NULL: a beam whose byte is not 0 has ended: it
+ *     offers end_token at score cum[s][w] and every other token at -inf.
+ * Beams that have not ended: a row whose log-sum-exp is not finite (a NaN, a
+ * +inf, or nothing above -inf) and a row whose cum is not finite offer every
+ * token at -inf.  Candidates are compared in double precision (sums in double
+ * over fp32 exponentials); results repeat bit for bit.
+ * Limits: n_seq <= 65535, width <= 32, V <= 4194304, 1 <= K <= 64 and
+ * K <= width V. */
+dv_status dv_beam_select(const void* logits, int n_seq, int width, int V,
+                         long long row_stride, dv_dtype dt, const float* cum,
+                         const uint8_t* done, int end_token, int K,
+                         float* score, int32_t* token, int32_t* beam,
+                         void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* ---------------------------------------------------- decoder-step helpers */
 
 /* y_b = LayerNorm(x_b) without affine terms (eps given), rounded to the
