@@ -15,9 +15,13 @@
 // numerator) per CTA, and the last CTA to finish joins them in tile order, so
 // results do not depend on timing.
 
+#include <cuda.h>
+
 #include <type_traits>
 
 #include "dv_kernels.h"
+#include "tc_common.cuh"
+#include "tma_map.h"
 
 namespace dv {
 namespace {
@@ -29,6 +33,7 @@ struct TreeArgs {
   TreeLaunch L;
   float scale_log2;            // scale log2(e): exponentials are taken to base 2
   WsHeader* hdr;
+  long long wait_ns;
 };
 
 // What every role of a CTA needs to walk its share of the tiles.
@@ -396,7 +401,503 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
   }
 }
 
+// ---- tensor cores (16-bit storage) ------------------------------------------------
+//
+// S = Q K^T and O += P V on tcgen05: M = 128 query rows (rows behind the unit's
+// last hold anything: a row of the product depends on its own row of Q and P
+// alone), 64 keys to a tile, fp32 accumulators in tensor memory.
+//   warp 8   one thread issues the TMA loads of K and V tiles into two rings
+//   warp 9   one thread issues the MMAs
+//   warps 10, 11  copy the next unit's query rows (swizzled, two buffers)
+//   warps 0-3 and 4-7  two softmax groups for the even and the odd tiles of a
+//            segment, a thread to a row: no value crosses threads.  Each
+//            group has its own maximum, sum and accumulator O, so the tiles of
+//            one overlap the other's products; they are joined at the end of
+//            the segment.
+// P goes back to tensor memory (the A operand of the second product) as the
+// sum of two 16-bit halves hi + lo: one rounding of P to bf16 would put as
+// large an error into O as the output's own rounding; the two halves leave
+// 2^-17, and the second MMA is hidden, since the kernel is bound by the reads
+// of K and V: a tile of 64 keys is 32 KB, about 1400 cycles at an SM's share
+// of the memory, and its products take about 400.
+// The reference maximum moves only when a tile's maximum exceeds it by 2^8
+// (P <= 2^14 with the 2^6 that keeps small weights out of f16's subnormals):
+// rescaling O is rare.
+
+constexpr int kTcThreads = 384;
+constexpr int kTcTmemCols = 512;
+// columns of group w: O at w DH, S at 256 + 64 w, P (two halves of 32) at 384 + 64 w
+constexpr uint32_t kColO = 0, kColS = 256, kColP = 384;
+constexpr float kShift = 6.f, kSlack = 8.f;
+constexpr long long kUnwindNs = 2000000000LL;
+
+template <int DH>
+struct TcSizes {
+  static constexpr int kStages = DH == 128 ? 4 : 6;
+  static constexpr uint32_t kQBytes = kTreeRows * DH * 2;
+  static constexpr uint32_t kTileBytes = kKeys * DH * 2;
+  static constexpr size_t kSmem = 1024 + 2 * kQBytes + 2 * kStages * kTileBytes;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A wait that ends: at its phase, when another wait of the CTA gave up, or at
+// the limit (recorded as DV_ERR_TIMEOUT; the CTA then unwinds, its results
+// being void).  Returns whether the phase was reached.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* stop, const TreeArgs& a,
+                                         int code) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (*stop) return false;
+    if ((long long)(globaltimer_ns() - t0) > a.wait_ns) {
+      *stop = 1;
+      set_error(a.hdr, DV_ERR_TIMEOUT, code);
+      return false;
+    }
+  }
+  return true;
+}
+
+template <int N>
+__device__ __forceinline__ void group_sync() {  // the eight softmax warps
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+
+template <typename T> struct Half2;
+template <> struct Half2<__half> {
+  static constexpr uint32_t kExp = 0x7c00u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 open(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+};
+template <> struct Half2<__nv_bfloat16> {
+  static constexpr uint32_t kExp = 0x7f80u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 open(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+};
+
+// Bit i: the row sees key j0 + i.  t: the row's node.
+__device__ __forceinline__ unsigned long long visible_keys(const TreeLaunch& L, const Seg& s, int j0, int t) {
+  const int u0 = j0 - s.pos;                                   // tree slot of the tile's first key
+  const int lo = min(max(-u0, 0), kKeys), hi = min(max(s.nodes - u0, 0), kKeys);
+  const unsigned long long below = lo >= 64 ? ~0ull : (1ull << lo) - 1;
+  if (!L.mask) {
+    const int top = min(max(t + 1 - u0, lo), hi);
+    return top >= 64 ? ~0ull : (1ull << top) - 1;
+  }
+  unsigned long long vis = below;
+  const uint8_t* row = L.mask + s.b * L.mask_stride + (size_t)t * L.T + u0;
+#pragma unroll 8
+  for (int i = lo; i < hi; ++i) vis |= (unsigned long long)(row[i] != 0) << i;
+  return vis;
+}
+
+// The V rows of a tile that not every row may see, in shared memory before the
+// product reads them: rows behind the last node become 0, and so do values of
+// tree nodes that are not finite (0 x inf would reach rows that do not see
+// them); returns whether there were any of those.
+template <typename T, int DH>
+__device__ __forceinline__ bool clean_v(uint8_t* v, const Seg& s, int j0, int tid) {
+  constexpr int kRowChunks = DH / 8;
+  bool found = false;
+  for (int i = tid; i < kKeys * kRowChunks; i += 128) {
+    const int r = i / kRowChunks, c = i % kRowChunks, j = j0 + r;
+    if (j < s.pos) continue;
+    uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    if (j >= s.n) {
+      *p = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint4 x = *p;
+    uint32_t* w = &x.x;
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      constexpr uint32_t lo = Half2<T>::kExp, hi = lo << 16;
+      if ((w[e] & lo) == lo) { w[e] &= 0xffff0000u; bad = true; }
+      if ((w[e] & hi) == hi) { w[e] &= 0x0000ffffu; bad = true; }
+    }
+    if (bad) *p = x;
+    found |= bad;
+  }
+  return found;
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                   const __grid_constant__ TreeArgs a) {
+  using Z = TcSizes<DH>;
+  constexpr int NS = Z::kStages, kBoxes = DH / 64;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TreePlan plan;
+  __shared__ uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], qfull[2], qempty[2], sfull[2], pready[2], ofull,
+      odone, done;
+  __shared__ float2 sml[2][2][kTreeRows];   // [segment parity][group][row] maximum and sum
+  __shared__ uint32_t tmem_base;
+  __shared__ int stop_s, bad_v[4], last;
+  const TreeLaunch& L = a.L;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + 2 * Z::kQBytes;
+  uint8_t* sV = sK + NS * Z::kTileBytes;
+  volatile int* stop = &stop_s;
+  const long long unwind_ns = a.wait_ns > kUnwindNs ? a.wait_ns : kUnwindNs;
+
+  if (tid == 0) {
+    for (int q = 0; q < NS; ++q) {
+      tc::mbar_init(&kfull[q], 1);
+      tc::mbar_init(&kempty[q], 1);
+      tc::mbar_init(&vfull[q], 1);
+      tc::mbar_init(&vempty[q], 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      tc::mbar_init(&qfull[q], 64);
+      tc::mbar_init(&qempty[q], 1);
+      tc::mbar_init(&sfull[q], 1);
+      tc::mbar_init(&pready[q], 128);
+    }
+    tc::mbar_init(&ofull, 1);
+    tc::mbar_init(&odone, 256);
+    tc::mbar_init(&done, 1);
+    tc::fence_mbar_init();
+    stop_s = 0;
+    bad_v[0] = bad_v[1] = bad_v[2] = bad_v[3] = 0;
+  }
+  if (warp == 9) tc::tmem_alloc(&tmem_base, kTcTmemCols);
+  tc::fence_before_sync();
+  tree_plan<kTcThreads>(a, &plan, kTreeRows);  // ends with a barrier
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_base;
+  Cursor cur(plan, L.B);
+  Seg s;
+
+  if (warp == 8) {
+    if (lane == 0) {  // TMA producer
+      int it = 0;
+      while (!*stop && cur.next(L, plan, kTreeRows, &s)) {
+        if (!s.ok) continue;
+        const int z = s.b * L.h + s.head;
+        for (int kt = s.k0; kt < s.k1; ++kt, ++it) {
+          const int st = it % NS, use = it / NS;
+          if (use) wait_bar(&kempty[st], (use - 1) & 1, stop, a, 31);
+          if (*stop) break;
+          tc::mbar_arrive_expect_tx(&kfull[st], Z::kTileBytes);
+#pragma unroll
+          for (int x = 0; x < kBoxes; ++x)
+            tc::tma_load_3d(sK + st * Z::kTileBytes + x * (kKeys * 128), &mapK, x * 64, kt * kKeys, z, &kfull[st]);
+          if (use) wait_bar(&vempty[st], (use - 1) & 1, stop, a, 32);
+          // (a V load of a stage whose K load went out is always issued, so
+          // that both rings count the same; its slot is free once the wait
+          // above returned without a stop)
+          if (*stop) {
+            tc::mbar_wait(&kfull[st], use & 1, unwind_ns);
+            break;
+          }
+          tc::mbar_arrive_expect_tx(&vfull[st], Z::kTileBytes);
+#pragma unroll
+          for (int x = 0; x < kBoxes; ++x)
+            tc::tma_load_3d(sV + st * Z::kTileBytes + x * (kKeys * 128), &mapV, x * 64, kt * kKeys, z, &vfull[st]);
+        }
+      }
+      // no copy into this CTA's shared memory may be in flight when it exits
+      for (int q = max(0, it - NS); q < it; ++q) {
+        if (!tc::mbar_wait(&kfull[q % NS], (q / NS) & 1, unwind_ns)) break;
+        if (!tc::mbar_wait(&vfull[q % NS], (q / NS) & 1, unwind_ns)) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0) {  // MMA issuer
+      constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+      const uint32_t idS = tc::idesc_f16(kTreeRows, kKeys, kBf16, false, false);
+      const uint32_t idO = tc::idesc_f16(kTreeRows, DH, kBf16, false, /*B MN-major*/ true);
+      int base = 0, sg = 0;
+      uint32_t pcount[2] = {0, 0};
+      while (!*stop && cur.next(L, plan, kTreeRows, &s)) {
+        if (!s.ok) continue;
+        const int nt = s.k1 - s.k0;
+        const uint32_t qb = tc::saddr(sQ + (sg & 1) * Z::kQBytes);
+        wait_bar(&qfull[sg & 1], (sg >> 1) & 1, stop, a, 33);
+        auto issue_s = [&](int j) {
+          const int it = base + j, st = it % NS;
+          wait_bar(&kfull[st], (it / NS) & 1, stop, a, 34);
+          if (*stop) return;
+          tc::fence_after_sync();
+          const uint32_t kb = tc::saddr(sK + st * Z::kTileBytes);
+#pragma unroll
+          for (int kk = 0; kk < DH / 16; ++kk) {
+            const uint64_t ad = tc::smem_desc(qb + (kk >> 2) * (kTreeRows * 128) + (kk & 3) * 32, 16, 1024, 2);
+            const uint64_t bd = tc::smem_desc(kb + (kk >> 2) * (kKeys * 128) + (kk & 3) * 32, 16, 1024, 2);
+            tc::mma_f16(tmem + kColS + (j & 1) * kKeys, ad, bd, idS, kk != 0);
+          }
+          tc::mma_commit(&sfull[j & 1]);
+          tc::mma_commit(&kempty[st]);
+        };
+        if (!*stop) issue_s(0);
+        if (nt > 1 && !*stop) issue_s(1);
+        // O is read to the end of the previous segment before it is begun anew
+        if (sg > 0) wait_bar(&odone, (sg - 1) & 1, stop, a, 35);
+        for (int j = 0; j < nt && !*stop; ++j) {
+          const int it = base + j, st = it % NS, w = j & 1;
+          wait_bar(&pready[w], pcount[w] & 1, stop, a, 36);
+          ++pcount[w];
+          wait_bar(&vfull[st], (it / NS) & 1, stop, a, 37);
+          if (*stop) break;
+          tc::fence_after_sync();
+          const uint32_t vb = tc::saddr(sV + st * Z::kTileBytes);
+          const uint32_t p = tmem + kColP + w * kKeys, o = tmem + kColO + w * DH;
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk) {
+            // V (MN-major): 16 keys = two 8-row groups (1024 B apart), the
+            // 64-column halves kKeys * 128 bytes apart
+            const uint64_t bd = tc::smem_desc(vb + kk * 2048, kKeys * 128, 1024, 2);
+            tc::mma_f16_ts(o, p + kk * 8, bd, idO, j >= 2 || kk != 0);
+            tc::mma_f16_ts(o, p + 32 + kk * 8, bd, idO, 1);
+          }
+          tc::mma_commit(&vempty[st]);
+          if (j + 2 < nt) issue_s(j + 2);
+        }
+        tc::mma_commit(&qempty[sg & 1]);
+        tc::mma_commit(&ofull);
+        base += nt;
+        ++sg;
+      }
+      tc::mma_commit(&done);  // arrives once every MMA issued above has completed
+      if (!tc::mbar_wait(&done, 0, unwind_ns)) set_error(a.hdr, DV_ERR_TIMEOUT, 38);
+    }
+    __syncwarp();
+  } else if (warp >= 10) {  // query rows, then the rows of out that no unit writes
+    constexpr int kRowChunks = DH / 8;
+    const int qt = tid - 320;
+    int sg = 0;
+    while (!*stop && cur.next(L, plan, kTreeRows, &s)) {
+      if (!s.ok) continue;
+      if (sg >= 2) wait_bar(&qempty[sg & 1], ((sg >> 1) - 1) & 1, stop, a, 39);
+      uint8_t* dst = sQ + (sg & 1) * Z::kQBytes;
+      if (!*stop) {
+        for (int i = qt; i < s.rows * kRowChunks; i += 64) {
+          const int r = i / kRowChunks, c = i % kRowChunks;
+          cp_async16(dst + (c >> 3) * (kTreeRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                     static_cast<const T*>(L.q) + row_offset(L, s, r, DH) + c * 8);
+        }
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      tc::fence_proxy_async();
+      tc::mbar_arrive(&qfull[sg & 1]);
+      ++sg;
+    }
+    __syncwarp();
+    zero_rows<T, DH>(L, plan, blockIdx.x * 2 + (warp - 10), gridDim.x * 2, lane, 32);
+  } else {  // softmax groups
+    const int w = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t tS = lanes + kColS + w * kKeys, tP = lanes + kColP + w * kKeys, tO = lanes + kColO + w * DH;
+    int base = 0, sg = 0;
+    uint32_t scount = 0;
+    while (cur.next(L, plan, kTreeRows, &s)) {
+      if (!s.ok) {
+        if (tid == 0) set_error(a.hdr, DV_ERR_INDEX_RANGE, s.head);
+        continue;
+      }
+      const int nt = s.k1 - s.k0;
+      const bool active = quad * 32 < s.rows;
+      const int t = min(s.row0 + row, s.row0 + s.rows - 1) / L.g;
+      float m = -INFINITY, l = 0.f;
+      for (int j = w; j < nt; j += 2) {
+        const int j0 = (s.k0 + j) * kKeys;
+        const bool edge = j0 + kKeys > s.pos;   // the tile holds tree nodes, or ends behind the last
+        bool there = true;
+        if (edge) {
+          const int it = base + j, st = it % NS;
+          there = wait_bar(&vfull[st], (it / NS) & 1, stop, a, 40);
+          if (clean_v<T, DH>(sV + st * Z::kTileBytes, s, j0, tid & 127)) bad_v[sg & 3] = 1;
+          tc::fence_proxy_async();
+        }
+        there &= wait_bar(&sfull[w], scount & 1, stop, a, 41);
+        ++scount;
+        if (!__all_sync(0xffffffffu, there)) break;  // the whole warp, or none of it
+        tc::fence_after_sync();
+        if (active) {
+          float v[kKeys];
+          tc::tmem_ld32(tS, v);
+          tc::tmem_ld32(tS + 32, v + 32);
+          tc::tmem_ld_wait();
+          float c = a.scale_log2;
+          if (c <= 0.f) {  // the maximum is taken before the scale
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) v[i] *= c;
+            c = 1.f;
+          }
+          if (edge) {
+            const unsigned long long vis = visible_keys(L, s, j0, t);
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) v[i] = (vis >> i) & 1 ? v[i] : -INFINITY;
+          }
+          float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int i = 4; i < kKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          const bool move = row < s.rows && top > m + kSlack;
+          if (__any_sync(0xffffffffu, move)) {
+            // a row whose maximum was -inf has sums of 0: nothing to rescale
+            const float alpha = move && m > -INFINITY ? ex2(m - top) : 1.f;
+            if (move) m = top;
+            l *= alpha;
+            if (j >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+              for (int cc = 0; cc < DH; cc += 32) {
+                float o[32];
+                tc::tmem_ld32(tO + cc, o);
+                tc::tmem_ld_wait();
+                uint32_t r[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i] * alpha);
+                tc::tmem_st32(tO + cc, r);
+              }
+            }
+          }
+          const float off = kShift - (m == -INFINITY ? 0.f : m);
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t hi[kKeys / 2], lo[kKeys / 2];
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 2) {
+            const float p0 = ex2(fmaf(v[i], c, off)), p1 = ex2(fmaf(v[i + 1], c, off));
+            sum[i & 3] += p0;
+            sum[(i + 1) & 3] += p1;
+            hi[i / 2] = Half2<T>::pack(p0, p1);
+            const float2 h = Half2<T>::open(hi[i / 2]);
+            lo[i / 2] = Half2<T>::pack(p0 - h.x, p1 - h.y);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tc::tmem_st32(tP, hi);
+          tc::tmem_st32(tP + 32, lo);
+          tc::tmem_st_wait();
+        }
+        tc::fence_before_sync();
+        tc::mbar_arrive(&pready[w]);
+      }
+      // the segment's end: both groups' results joined, a group to each half of the columns
+      sml[sg & 1][w][row] = make_float2(m, l);
+      if (tid == 0) bad_v[(sg + 2) & 3] = 0;
+      group_sync<256>();
+      wait_bar(&ofull, sg & 1, stop, a, 42);
+      tc::fence_after_sync();
+      __syncwarp();
+      const bool fix = bad_v[sg & 3] != 0;
+      const float2 A = sml[sg & 1][0][row], Bv = sml[sg & 1][1][row];
+      const float M = fmaxf(A.x, Bv.x);
+      const float wA = A.x == -INFINITY ? 0.f : ex2(A.x - M), wB = Bv.x == -INFINITY ? 0.f : ex2(Bv.x - M);
+      const float sum = fmaf(A.y, wA, Bv.y * wB);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a row that sees nothing is zero
+      const bool whole = s.pieces == 1;
+      const size_t slot = piece_slot(blockIdx.x, s.k0 == 0);
+#pragma unroll 1
+      for (int cc = w * (DH / 2); cc < (w + 1) * (DH / 2); cc += 32) {
+        if (!active) break;
+        float o[32];
+        {
+          float ob[32];
+          tc::tmem_ld32(lanes + kColO + cc, o);
+          if (nt > 1) tc::tmem_ld32(lanes + kColO + DH + cc, ob);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            o[i] *= wA;
+            if (nt > 1) o[i] = fmaf(ob[i], wB, o[i]);
+          }
+        }
+        if (row < s.rows) {
+          if (fix) {  // values that clean_v took out, for the rows that see them
+            const int f0 = max(s.k0 * kKeys - s.pos, 0), f1 = min(s.k1 * kKeys - s.pos, s.nodes);
+            for (int u = f0; u < f1; ++u) {
+              if (!sees(L, s, t, u)) continue;
+              const T* vr = static_cast<const T*>(L.V) +
+                            (((size_t)s.b * L.h + s.head) * L.n_max + s.pos + u) * DH + cc;
+  #pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float x = Elem<T>::to_f(vr[i]);
+                if (!(fabsf(x) < INFINITY)) o[i] += x;
+              }
+            }
+          }
+          if (whole) {
+            T* dst = static_cast<T*>(L.out) + row_offset(L, s, row, DH) + cc;
+  #pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              const uint4 x = make_uint4(Half2<T>::pack(o[i] * inv, o[i + 1] * inv),
+                                         Half2<T>::pack(o[i + 2] * inv, o[i + 3] * inv),
+                                         Half2<T>::pack(o[i + 4] * inv, o[i + 5] * inv),
+                                         Half2<T>::pack(o[i + 6] * inv, o[i + 7] * inv));
+              *reinterpret_cast<uint4*>(dst + i) = x;
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(L.part) + (slot * (DH / 4) + cc / 4) * L.rows_pad + row;
+  #pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              __stcg(dst + (size_t)(i / 4) * L.rows_pad, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+            if (cc == 0) __stcg(&L.ml[slot * L.rows_pad + row], make_float2(M, sum));
+          }
+        }
+        __syncwarp();
+      }
+      tc::fence_before_sync();
+      tc::mbar_arrive(&odone);
+      if (!whole) {
+        __threadfence();
+        group_sync<256>();
+        if (tid == 0) {
+          last = atomicAdd(&L.ctr[s.owner], 1) == s.pieces - 1;
+          if (last) L.ctr[s.owner] = 0;
+          __threadfence();
+        }
+        group_sync<256>();
+        if (last) join_unit<T, DH, 256>(L, s, tid);
+      }
+      base += nt;
+      ++sg;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 9) tc::tmem_dealloc(tmem, kTcTmemCols);
+}
+
 // ---- host ------------------------------------------------------------------------
+
+template <typename T, int DH>
+cudaError_t run_tc(const TreeArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  CUtensorMap mK, mV;
+  const uint64_t mats = (uint64_t)a.L.B * a.L.h;
+  if (!make_map_3d(&mK, a.L.K, DH, a.L.n_max, mats, kKeys, bf16) ||
+      !make_map_3d(&mV, a.L.V, DH, a.L.n_max, mats, kKeys, bf16))
+    return cudaErrorInvalidValue;
+  constexpr size_t smem = TcSizes<DH>::kSmem;
+  static PerDevice attr;  // function attributes are per device
+  const cudaError_t ea = (cudaError_t)attr.get(current_device(), [] {
+    return (int)cudaFuncSetAttribute(tree_tc_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (ea != cudaSuccess) return ea;
+  return launch_k(tree_tc_kernel<T, DH>, dim3(min(num_sms, kTreeCtas)), dim3(kTcThreads), smem, stream, false, 1, mK,
+                  mV, a);
+}
 
 template <typename T, int DH>
 cudaError_t run_simt(const TreeArgs& a, int num_sms, cudaStream_t stream) {
@@ -409,19 +910,16 @@ cudaError_t run_simt(const TreeArgs& a, int num_sms, cudaStream_t stream) {
   return launch_k(tree_simt_kernel<T, DH>, dim3(min(num_sms, kTreeCtas)), dim3(kSimtThreads), smem, stream, false, 1, a);
 }
 
-template <typename T>
-cudaError_t run_t(const TreeArgs& a, int num_sms, cudaStream_t stream) {
-  return a.L.d_h == 128 ? run_simt<T, 128>(a, num_sms, stream) : run_simt<T, 64>(a, num_sms, stream);
-}
-
 }  // namespace
 
 cudaError_t launch_tree_attn(const TreeLaunch& L, dv_dtype dt, WsHeader* hdr, int num_sms, cudaStream_t stream) {
-  TreeArgs a{L, L.scale * kLog2e, hdr};
+  const TreeArgs a{L, L.scale * kLog2e, hdr, wait_limit_ns()};
+  const bool wide = L.d_h == 128;
   switch (dt) {
-    case DV_F32: return run_t<float>(a, num_sms, stream);
-    case DV_F16: return run_t<__half>(a, num_sms, stream);
-    case DV_BF16: return run_t<__nv_bfloat16>(a, num_sms, stream);
+    case DV_F32: return wide ? run_simt<float, 128>(a, num_sms, stream) : run_simt<float, 64>(a, num_sms, stream);
+    case DV_F16: return wide ? run_tc<__half, 128>(a, num_sms, stream) : run_tc<__half, 64>(a, num_sms, stream);
+    case DV_BF16:
+      return wide ? run_tc<__nv_bfloat16, 128>(a, num_sms, stream) : run_tc<__nv_bfloat16, 64>(a, num_sms, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -45,6 +45,22 @@ inline bool make_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [mats][rows][cols] fp16 / bf16 matrices behind one another, box {64 columns,
+// box_rows, 1}, 128-byte swizzle, zero fill outside a matrix.
+inline bool make_map_3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t mats,
+                        uint32_t box_rows, bool bf16) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cols, rows, mats};
+  const cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // [rows][cols] row-major matrix of 2- or 4-byte elements read as plain
 // (unswizzled) row-major boxes of box_cols x box_rows, zero fill outside.
 inline bool make_map_rows(CUtensorMap* m, const void* base, int esize, bool bf16, uint64_t cols, uint64_t rows,

@@ -598,3 +598,24 @@ def test_beam_select_captured():
         graph.replay()
         _, rt, rb = _beam_ref(logits, cum, K)
         assert np.array_equal(token.cpu().numpy(), rt) and np.array_equal(beam.cpu().numpy(), rb)
+
+
+def test_tree_attention_waits_that_run_out_unwind():
+    """A 1 ns limit lets waits give up before their copies land (whether one
+    does depends on timing).  The call ends, the workspace stays usable, and
+    the next call is right."""
+    c = Case("f16", 128, [2000, 700], 16, 8, seed=41)
+    c.check()
+    want = c.out.clone()
+    prev = dv.dv_set_wait_limit_ns(1)
+    try:
+        for _ in range(3):
+            c.call()
+            st, _ = dv.dv_check(c.ws)
+            assert st in (0, 6)
+    finally:
+        dv.dv_set_wait_limit_ns(prev)
+    c.out.zero_()
+    c.call()
+    assert dv.dv_check(c.ws) == (0, 0)
+    assert torch.equal(c.out, want)
