@@ -192,15 +192,12 @@ TreeWs carve_tree(Carver& c, int T, int group, int d_h) {
 }
 
 struct BeamWs {
-  int32_t* ctr;
   float2* stat;
   int2* cand;
 };
-int beam_chunks(int V) { return (V + kBeamChunk - 1) / kBeamChunk; }
 BeamWs carve_beam(Carver& c, int n_seq, int width, int V, int K) {
   BeamWs w{};
-  const size_t rows = (size_t)n_seq * width * beam_chunks(V);
-  w.ctr = c.take<int32_t>((size_t)n_seq);
+  const size_t rows = (size_t)n_seq * width * ((V + kBeamTile - 1) / kBeamTile);
   w.stat = c.take<float2>(rows);
   w.cand = c.take<int2>(rows * K);
   return w;
@@ -568,7 +565,7 @@ KvMove make_move(const dv_kv* kv, int n_kv, int B, int d, int h, int d_h, const 
 }
 
 bool beam_shape_ok(int n_seq, int width, int V, int K) {
-  return n_seq >= 1 && n_seq <= 65535 && width >= 1 && width <= kBeamMaxWidth && V >= 1 && V <= 4194304 && K >= 1 &&
+  return n_seq >= 1 && width >= 1 && width <= kBeamMaxWidth && (long long)n_seq * width <= 65535 && V >= 1 && V <= 4194304 && K >= 1 &&
          K <= kBeamMaxK && (long long)K <= (long long)width * V;
 }
 }  // namespace
@@ -666,10 +663,10 @@ dv_status dv_beam_select(const void* logits, int n_seq, int width, int V, long l
   const BeamWs w = carve_beam(c, n_seq, width, V, K);
   BeamLaunch L{};
   L.logits = logits; L.ld = row_stride; L.cum = cum; L.done = done; L.end = end_token;
-  L.S = n_seq; L.W = width; L.V = V; L.K = K; L.chunks = beam_chunks(V);
+  L.S = n_seq; L.W = width; L.V = V; L.K = K;
   L.score = score; L.token = token; L.beam = beam;
-  L.stat = w.stat; L.cand = w.cand; L.ctr = w.ctr;
-  cudaError_t e = launch_beam_select(L, dt, stream);
+  L.stat = w.stat; L.cand = w.cand;
+  cudaError_t e = launch_beam_select(L, dt, num_sms_current(), stream);
   return e == cudaSuccess ? DV_OK : cuda_fail(e);
 }
 

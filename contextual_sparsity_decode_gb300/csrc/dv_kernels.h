@@ -321,19 +321,20 @@ cudaError_t launch_kv_reorder(const KvMove& m, int width, const int32_t* start, 
                               cudaStream_t stream);
 
 // Beam selection (k_beam.cu).
-constexpr int kBeamChunk = 8192;   // tokens per CTA
+constexpr int kBeamTile = 4096;    // tokens that a CTA takes at a time
 constexpr int kBeamMaxWidth = 32;
 constexpr int kBeamMaxK = 64;
 struct BeamLaunch {
   const void* logits; long long ld;          // [S][W] rows of V, ld elements apart
   const float* cum; const uint8_t* done; int end;
-  int S, W, V, K, chunks;
+  int S, W, V, K;
+  int parts, part_tiles;                     // set by the launcher: parts of a row, tiles of a part
   float* score; int32_t* token; int32_t* beam;  // [S][K]
-  float2* stat;    // [S W][chunks] maximum and sum of exponentials
-  int2* cand;      // [S W][chunks][K] (value bits, token)
-  int* ctr;        // [S], zero between calls
+  // room for a part per tile
+  float2* stat;    // [S W][parts] maximum and sum of exponentials
+  int2* cand;      // [S W][parts][K] (value bits, token)
 };
-cudaError_t launch_beam_select(const BeamLaunch& a, dv_dtype dt, cudaStream_t stream);
+cudaError_t launch_beam_select(const BeamLaunch& a, dv_dtype dt, int num_sms, cudaStream_t stream);
 
 // ---- misc (k_misc.cu) --------------------------------------------------------
 

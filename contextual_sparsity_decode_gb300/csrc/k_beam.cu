@@ -8,12 +8,27 @@
 // arithmetic; only the candidates of different beams are compared by score, in
 // double precision.
 //
-// One CTA takes kChunk consecutive tokens of a row into registers, reduces
-// their maximum and sum of exponentials and lists their K largest; the last
-// CTA of a sequence to finish joins the chunks (log-sum-exp in double, chunk
-// by chunk in order) and picks the K best of the listed candidates.  The
-// elements of a thread and the order of every sum depend on the token index
-// alone, so rows with equal logits get equal sums.
+// One pass over the logits (the floor: each is read once, which at 48 x 10 rows
+// of 128001 bf16 logits takes 18 us).
+//   scan  a CTA walks a part of a row in tiles of kBeamTile tokens, the next
+//         tile's loads in flight: a running maximum and sum of exponentials
+//         per thread, and the groups of 8 tokens whose maximum may be among
+//         the K largest: the K best groups, by maximum and then the lower
+//         token, hold the K best tokens (each group left out is preceded by K
+//         tokens of others).  The first tile gives a value tau that K maxima
+//         reach; of later groups only those above tau are listed (an equal
+//         one comes after K others), which are few; a list that grows long is
+//         cut back and tau raised.  At the part's end the K best groups'
+//         tokens are read again and ranked.  No sort, and no reduction over
+//         the block in the loop.
+//   join  one CTA per sequence, launched while the scan runs: log-sum-exp of
+//         the parts in double, then the K best of the parts' lists.
+// -inf tokens are never listed: a part with fewer than K others adds its
+// lowest ones, which lie among its first 2 K tokens.
+// The tokens of a thread and the order of every sum depend on the token index
+// alone, not on the row's address, so rows with equal logits get equal sums.
+
+#include <cfloat>
 
 #include "dv_kernels.h"
 
@@ -21,204 +36,619 @@ namespace dv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 32;                      // tokens per thread
-static_assert(kThreads * kPer == kBeamChunk, "tokens per CTA");
+constexpr int kWarps = kThreads / 32;
+constexpr int kGroups = 2;                    // groups of 8 tokens per thread and tile
+static_assert(kThreads * kGroups * 8 == kBeamTile, "tokens per tile");
+constexpr int kLong = 512;                    // a list longer than this is cut back
+constexpr int kListed = kLong + kBeamTile / 8;  // a tile's groups always fit behind it
+static_assert(kListed >= kBeamMaxK * 8, "the best groups' tokens fit too");
+constexpr int kFew = 256;                     // entries ranked against each other directly
+constexpr int kJoinListed = 1024;
+constexpr float kLog2e = 1.4426950408889634f;
 
-// Order-preserving map of a float to unsigned; NaN is treated elsewhere.
+typedef unsigned long long u64;
+
+// Order-preserving map of a float to unsigned (-0 as 0).
 __device__ __forceinline__ uint32_t ord32(float f) {
-  const uint32_t u = __float_as_uint(f);
+  const uint32_t u = __float_as_uint(f + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ float unord32(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
+__device__ __forceinline__ u64 key_of(float f, int v) { return ((u64)ord32(f) << 32) | (uint32_t)~v; }
 
-__device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = u > v ? u : v;
-  }
-  return v;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// A candidate of the join: score, then the lower flat index.
-struct Cand {
-  double s;
-  long long f;  // w V + v, or -1: none
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// (a0, a1) + (b, b) and (a0, a1) * (b, b): two fp32 operations an instruction
+__device__ __forceinline__ u64 pack2(float a, float b) {
+  u64 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void open2(u64 x, float* a, float* b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(x)); }
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// The r-th largest of a warp's values, equal ones counted singly; 0 where
+// fewer are not 0.
+__device__ __forceinline__ uint32_t warp_rth(uint32_t v, int r) {
+  for (;;) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, v);
+    r -= __popc(__ballot_sync(0xffffffffu, v == top));
+    if (r <= 0 || top == 0) return top;
+    if (v == top) v = 0;
+  }
+}
+// A value that at least r of the block's values reach, not far below the r-th
+// largest: each warp's share of r, the least over the warps.  One barrier; `red`
+// may be used again after the next.
+__device__ __forceinline__ uint32_t block_reached(uint32_t v, int r, uint32_t* red) {
+  const uint32_t t = warp_rth(v, (r + kWarps - 1) / kWarps);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
+  __syncthreads();
+  uint32_t least = red[0];
+#pragma unroll
+  for (int q = 1; q < kWarps; ++q) least = min(least, red[q]);
+  return least;
+}
+// The r-th largest of the block's values; 0 where fewer are not 0.  Starts and
+// ends with a barrier.
+template <typename U>
+__device__ __forceinline__ U block_rth(U v, int r, U* all, U* result) {
+  __syncthreads();
+  all[threadIdx.x] = v;
+  if (threadIdx.x == 0) *result = ~U(0);
+  __syncthreads();
+  int above = 0;
+#pragma unroll 8
+  for (int q = 0; q < kThreads; ++q) above += all[q] > v;
+  if (above < r) atomicMin(result, v);
+  __syncthreads();
+  return *result;
+}
+
+// Eight consecutive tokens of a row at any address: the aligned 16-byte
+// vectors that cover them, as they are loaded (the overlap with the next
+// group is an L1 hit).
+template <typename T>
+struct Raw8 {
+  static constexpr int kVecs = sizeof(T) * 8 / 16;
+  uint4 x[kVecs + 1];
+  // Whole vectors are read only within the logits' memory [first, last);
+  // groups at its ends, or at the row's, are read token by token.
+  static __device__ __forceinline__ bool whole(const T* row, int v, int V, const char* first, const char* last) {
+    const char* p = reinterpret_cast<const char*>(row + v);
+    const uint32_t off = reinterpret_cast<uintptr_t>(p) & 15u;
+    return v + 8 <= V && p - off >= first && (off == 0 || p - off + 16 * (kVecs + 1) <= last);
+  }
+  __device__ __forceinline__ void load(const T* row, int v) {
+    const char* p = reinterpret_cast<const char*>(row + v);
+    const uint32_t off = reinterpret_cast<uintptr_t>(p) & 15u;
+    const uint4* base = reinterpret_cast<const uint4*>(p - off);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) x[i] = __ldg(base + i);
+    if (off) x[kVecs] = __ldg(base + kVecs);
+  }
+  // the words from byte 4 WORDS + bits / 8 on
+  template <int WORDS>
+  __device__ __forceinline__ void cut(uint32_t bits, float* f) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+    uint32_t y[4 * kVecs];
+#pragma unroll
+    for (int i = 0; i < 4 * kVecs; ++i) y[i] = __funnelshift_r(w[i + WORDS], w[i + WORDS + 1 < 4 * kVecs + 4 ? i + WORDS + 1 : 0], bits);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      unpack<T>(make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]), f + i * Elem<T>::kVec);
+  }
+  // off: the row's offset from a 16-byte boundary (the same for all its groups)
+  __device__ __forceinline__ void open(uint32_t off, float* f) const {
+    const uint32_t bits = (off & 3u) * 8;
+    switch (off >> 2) {
+      case 0: cut<0>(bits, f); break;
+      case 1: cut<1>(bits, f); break;
+      case 2: cut<2>(bits, f); break;
+      default: cut<3>(bits, f); break;
+    }
+  }
 };
-__device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
-  if (b.f < 0) return a.f >= 0;
-  if (a.f < 0) return false;
-  return a.s > b.s || (a.s == b.s && a.f < b.f);
+
+// A candidate of the join: its score as an order-preserving integer, and where
+// it is.  Comparing integers keeps double-precision work, slow on this GPU, to
+// the few that are listed.
+struct Cand {
+  u64 key;
+  int w, v;  // v < 0: none
+};
+__device__ __forceinline__ u64 ord64(double d) {
+  const u64 u = (u64)__double_as_longlong(d + 0.0);
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
-__device__ __forceinline__ Cand warp_best(Cand c) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Cand d;
-    d.s = __shfl_xor_sync(0xffffffffu, c.s, o);
-    d.f = __shfl_xor_sync(0xffffffffu, c.f, o);
-    if (before(d, c)) c = d;
+__device__ __forceinline__ double unord64(u64 o) {
+  return __longlong_as_double((long long)((o >> 63) ? (o & 0x7fffffffffffffffull) : ~o));
+}
+__device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
+  if (a.key != b.key) return a.key > b.key;
+  return a.w != b.w ? a.w < b.w : a.v < b.v;
+}
+
+struct JoinRow {
+  double base;  // log-sum-exp; an ended beam's score
+  float cum;
+  int kind;     // 0: the listed tokens, 1: every token at -inf, 2: ended
+};
+
+// Entry i of the join, entry e of beam w's lists: its token (-1: none) and
+// logit.  A beam that lists nothing offers its K lowest tokens at -inf; an
+// ended beam's end token, at its score, takes its own place among them or that
+// of the last (*ends).
+__device__ __forceinline__ int join_entry(const BeamLaunch& a, const JoinRow* rows, int s, int i, int per_row, int* w,
+                                          float* x, bool* ends) {
+  *w = i / per_row;
+  const int e = i - *w * per_row, kind = rows[*w].kind;
+  *x = -INFINITY;
+  *ends = false;
+  if (kind == 0) {
+    const int2 p = __ldcg(&a.cand[(size_t)(s * a.W + *w) * per_row + e]);
+    *x = __int_as_float(p.x);
+    return p.y;
   }
-  return c;
+  if (e >= a.K) return -1;
+  if (kind == 2 && (e == a.end || (e == a.K - 1 && a.end >= a.K))) {
+    *ends = true;
+    return a.end;
+  }
+  return e < a.V ? e : -1;
+}
+
+// Bounds of an entry's score in fp32: the score lies in [lo, hi] (three
+// roundings of at most 2^-24 of the summed magnitudes).
+__device__ __forceinline__ void join_bounds(const JoinRow& r, float x, bool ends, float* lo, float* hi) {
+  if (ends) {
+    *lo = *hi = (float)r.base;
+  } else if (r.kind != 0 || x == -INFINITY) {
+    *lo = *hi = -INFINITY;
+  } else {
+    const float lse = (float)r.base, f = r.cum + (x - lse);
+    const float e = 0x1p-21f * (fabsf(r.cum) + fabsf(x) + fabsf(lse));
+    *lo = f - e;
+    *hi = f + e;
+  }
+}
+
+__device__ __forceinline__ void put(const BeamLaunch& a, int s, int k, const Cand& c) {
+  a.score[(size_t)s * a.K + k] = (float)unord64(c.key);
+  a.token[(size_t)s * a.K + k] = c.v;
+  a.beam[(size_t)s * a.K + k] = c.w;
+}
+
+// Cuts a list of n entries back to those that reach the K-th largest of the
+// thread maxima over it (the K-th largest entry where n <= kThreads); returns
+// the new length.
+__device__ __noinline__ int cut_back(u64* list, u64* kept, int n, int K, u64* all, u64* result, int* listed) {
+  u64 best = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) best = list[i] > best ? list[i] : best;
+  const u64 t = block_rth<u64>(best, K, all, result);
+  if (threadIdx.x == 0) *listed = 0;
+  __syncthreads();
+  if (best >= t)
+    for (int i = threadIdx.x; i < n; i += kThreads)
+      if (list[i] >= t) kept[atomicAdd(listed, 1)] = list[i];
+  __syncthreads();
+  n = *listed;
+  for (int i = threadIdx.x; i < n; i += kThreads) list[i] = kept[i];
+  __syncthreads();
+  return n;
+}
+
+// The same with a threshold that costs a tenth and keeps perhaps twice as many
+// (by value alone: runs of equal values stay); *t: the threshold.
+__device__ __forceinline__ int trim(u64* list, u64* kept, int n, int K, uint32_t* red, int* listed, uint32_t* t) {
+  const int i0 = (threadIdx.x & 31) * kWarps + (threadIdx.x >> 5);  // every warp gets its share of a short list
+  uint32_t best = 0;
+  for (int i = i0; i < n; i += kThreads) best = max(best, (uint32_t)(list[i] >> 32));
+  __syncthreads();
+  *t = block_reached(best, K, red);
+  if (threadIdx.x == 0) *listed = 0;
+  __syncthreads();
+  if (best >= *t)
+    for (int i = i0; i < n; i += kThreads)
+      if ((uint32_t)(list[i] >> 32) >= *t) kept[atomicAdd(listed, 1)] = list[i];
+  __syncthreads();
+  n = *listed;
+  for (int i = threadIdx.x; i < n; i += kThreads) list[i] = kept[i];
+  __syncthreads();
+  return n;
+}
+
+// The list's length brought down to near K (at most kFew).
+__device__ __forceinline__ int shorten(u64* list, u64* kept, int n, int K, uint32_t* red, u64* all, u64* result,
+                                       int* listed) {
+  uint32_t t;
+  if (n > 2 * K && n > 32) n = trim(list, kept, n, K, red, listed, &t);
+  while (n > kFew) n = cut_back(list, kept, n, K, all, result, listed);  // at most K ceil(n / kThreads) stay
+  return n;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_kernel(const BeamLaunch a) {
-  __shared__ float redf[kThreads / 32];
-  __shared__ unsigned long long red64[kThreads / 32];
-  __shared__ Cand redc[kThreads / 32];
-  __shared__ double base[kBeamMaxWidth];   // cum - lse of a row
-  __shared__ int kind[kBeamMaxWidth];      // 0: listed tokens, 1: every token at -inf, 2: ended
-  __shared__ int last;
-  const int chunk = blockIdx.x, w = blockIdx.y, s = blockIdx.z;
+__global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const BeamLaunch a) {
+  // keys (value, lower token first): of groups, by their maximum; of tokens
+  __shared__ u64 list[kListed], kept[kListed];
+  __shared__ u64 all[kThreads];
+  __shared__ u64 rth;
+  __shared__ uint32_t red[kWarps];
+  __shared__ float redm[kWarps], reds[kWarps];
+  __shared__ int listed;
+  const int part = blockIdx.x, row = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int row = s * a.W + w;
+  grid_dep_launch();
+  if (a.done && a.done[row]) return;  // an ended beam's logits are not read
   const T* x = static_cast<const T*>(a.logits) + (size_t)row * a.ld;
-  const int v0 = chunk * kBeamChunk;
+  const char* first = static_cast<const char*>(a.logits);
+  const char* last = first + ((size_t)(a.S * a.W - 1) * a.ld + a.V) * sizeof(T);
+  const uint32_t off = reinterpret_cast<uintptr_t>(x) & 15u;
+  const int lo = part * a.part_tiles * kBeamTile, hi = min(a.V, lo + a.part_tiles * kBeamTile);
 
-  float f[kPer];
-  float m = -INFINITY;
-  bool bad = false;
+  Raw8<T> raw[kGroups];
+  const auto fetch = [&](int v0) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int v = v0 + i * kThreads + tid;
-    f[i] = v < a.V ? Elem<T>::to_f(x[v]) : -INFINITY;
-    bad |= !(f[i] < INFINITY);   // NaN or +inf
-    m = fmaxf(m, f[i]);
-  }
-  m = warp_max(m);
-  if (lane == 0) redf[wid] = m;
-  bad = __syncthreads_or(bad);
+    for (int g = 0; g < kGroups; ++g) {
+      const int v = v0 + (g * kThreads + tid) * 8;
+      if (v < hi && Raw8<T>::whole(x, v, a.V, first, last)) raw[g].load(x, v);
+    }
+  };
+  fetch(lo);
+  if (tid == 0) listed = 0;
+  float m = -INFINITY, sum = 0.f, tau = -INFINITY;
+  for (int v0 = lo; v0 < hi; v0 += kBeamTile) {
+    float f[8 * kGroups];
 #pragma unroll
-  for (int q = 0; q < kThreads / 32; ++q) m = fmaxf(m, redf[q]);
-  __syncthreads();
-  float sum = 0.f;
-  if (m > -INFINITY) {
+    for (int g = 0; g < kGroups; ++g) {
+      const int v = v0 + (g * kThreads + tid) * 8;
+      if (v < hi && Raw8<T>::whole(x, v, a.V, first, last)) {
+        raw[g].open(off, f + 8 * g);
+      } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += expf(f[i] - m);
-  }
-  sum = warp_sum(sum);
-  if (lane == 0) redf[wid] = sum;
-  __syncthreads();
-  const size_t slot = (size_t)row * a.chunks + chunk;
-  if (tid == 0) {
-    double t = 0.0;
-    for (int q = 0; q < kThreads / 32; ++q) t += (double)redf[q];
-    a.stat[slot] = make_float2(bad ? NAN : m, (float)t);
-  }
-  // the K largest, by (value, lower index): one more each round
-  unsigned long long prev = ~0ull;
-  for (int k = 0; k < a.K; ++k) {
-    unsigned long long best = 0;
+        for (int e = 0; e < 8; ++e) f[8 * g + e] = v + e < hi ? Elem<T>::to_f(x[v + e]) : -INFINITY;
+      }
+    }
+    if (v0 + kBeamTile < hi) fetch(v0 + kBeamTile);
+    float g8[kGroups];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int v = v0 + i * kThreads + tid;
-      const unsigned long long key = ((unsigned long long)ord32(f[i]) << 32) | (uint32_t)~v;
-      if (v < a.V && key < prev && key > best) best = key;
+    for (int g = 0; g < kGroups; ++g) {
+      const float* x8 = f + 8 * g;
+      g8[g] = max3(max3(max3(x8[0], x8[1], x8[2]), x8[3], x8[4]), max3(x8[5], x8[6], x8[7]), -INFINITY);
     }
-    best = warp_max_u64(best);
-    if (lane == 0) red64[wid] = best;
-    __syncthreads();
+    const float top = fmaxf(g8[0], g8[1]);
+    // the sum is kept relative to the thread's maximum; a NaN or +inf among
+    // the tokens makes it a NaN
+    const float mn = fmaxf(m, top), ref = mn > -INFINITY ? mn : 0.f;
+    u64 part_sum = 0;
+    const u64 minus = pack2(-ref, -ref), scale = pack2(kLog2e, kLog2e);
 #pragma unroll
-    for (int q = 0; q < kThreads / 32; ++q) best = red64[q] > best ? red64[q] : best;
-    __syncthreads();
-    if (tid == 0) a.cand[slot * a.K + k] = make_int2(best ? __float_as_int(unord32(best >> 32)) : 0, best ? (int)~(uint32_t)best : -1);
-    prev = best;
-  }
-
-  // the sequence's last CTA joins
-  __syncthreads();
-  if (tid == 0) {
-    __threadfence();
-    last = atomicAdd(&a.ctr[s], 1) == a.W * a.chunks - 1;
-    if (last) {
-      a.ctr[s] = 0;
-      __threadfence();
+    for (int i = 0; i < 8 * kGroups; i += 2) {
+      float d0, d1;
+      open2(mul2(add2(pack2(f[i], f[i + 1]), minus), scale), &d0, &d1);
+      part_sum = add2(part_sum, pack2(ex2(d0), ex2(d1)));
     }
-  }
-  __syncthreads();
-  if (!last) return;
-  if (tid < a.W) {
-    const int r = s * a.W + tid;
-    float M = -INFINITY;
-    bool nan = false;
-    for (int c = 0; c < a.chunks; ++c) {
-      const float2 st = __ldcg(&a.stat[(size_t)r * a.chunks + c]);
-      nan |= st.x != st.x;
-      M = fmaxf(M, st.x);
+    float s0, s1;
+    open2(part_sum, &s0, &s1);
+    sum = fmaf(sum, m > -INFINITY ? ex2((m - ref) * kLog2e) : 1.f, s0 + s1);
+    m = mn;
+    bool over = false;
+    float least = tau;
+    if (v0 == lo) {
+      // the first tile: K maxima reach t, and those that do are listed
+      const uint32_t t = block_reached(top > -INFINITY ? ord32(top) : 0u, a.K, red);
+      if (t) tau = unord32(t);
+      least = t ? tau : -FLT_MAX;  // 0: fewer than K threads hold tokens
     }
-    double t = 0.0;
-    for (int c = 0; c < a.chunks; ++c) {
-      const float2 st = __ldcg(&a.stat[(size_t)r * a.chunks + c]);
-      if (st.y > 0.f) t += (double)st.y * exp((double)st.x - (double)M);
-    }
-    const float cum = a.cum[r];
-    const bool open = cum > -INFINITY && cum < INFINITY;   // NaN and +inf count as -inf
-    if (a.done && a.done[r]) {
-      kind[tid] = 2;
-      base[tid] = open ? (double)cum : -INFINITY;
-    } else if (nan || !(M > -INFINITY) || !open) {
-      kind[tid] = 1;
-    } else {
-      kind[tid] = 0;
-      base[tid] = (double)M + log(t);
-    }
-  }
-  __syncthreads();
-  const int per_row = a.chunks * a.K;
-  Cand prevc{INFINITY, -1};
-  for (int k = 0; k < a.K; ++k) {
-    Cand best{-INFINITY, -1};
-    for (int i = tid; i < a.W * per_row; i += kThreads) {
-      const int bw = i / per_row, e = i - bw * per_row;
-      Cand c{-INFINITY, -1};
-      if (kind[bw] == 0) {
-        const int2 p = __ldcg(&a.cand[(size_t)(s * a.W + bw) * per_row + e]);
-        if (p.y >= 0) {
-          c.s = (double)a.cum[s * a.W + bw] + ((double)__int_as_float(p.x) - base[bw]);
-          c.f = (long long)bw * a.V + p.y;
-        }
-      } else if (e < a.K) {
-        // the K lowest tokens at -inf; an ended beam's end token at its score
-        // takes the place of itself, or of the last of them
-        if (e < a.V) c.f = (long long)bw * a.V + e;
-        if (kind[bw] == 2 && (e == a.end || (e == a.K - 1 && a.end >= a.K))) {
-          c.f = (long long)bw * a.V + a.end;
-          c.s = base[bw];
+    if (top >= least) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        if (g8[g] > least || (v0 == lo && g8[g] == least)) {
+          const int at = atomicAdd(&listed, 1);
+          list[at] = key_of(g8[g], v0 + (g * kThreads + tid) * 8);
+          over |= at >= kLong;
         }
       }
-      if (c.f >= 0 && (prevc.f < 0 || before(prevc, c)) && before(c, best)) best = c;
     }
-    best = warp_best(best);
-    if (lane == 0) redc[wid] = best;
+    if (__syncthreads_or(over)) {
+      cut_back(list, kept, listed, a.K, all, &rth, &listed);
+      tau = fmaxf(tau, unord32((uint32_t)(rth >> 32)));
+    } else if (v0 == lo && lo + kBeamTile < hi) {
+      const int n = listed;
+      uint32_t t;
+      if (n > 2 * a.K) {
+        trim(list, kept, n, a.K, red, &listed, &t);
+        if (t) tau = fmaxf(tau, unord32(t));
+      }
+      __syncthreads();
+    }
+  }
+  // the part's maximum and sum
+  const float wm = warp_max(m);
+  const float ws = warp_sum(m > -INFINITY ? sum * ex2((m - wm) * kLog2e) : sum != sum ? sum : 0.f);
+  if (lane == 0) {
+    redm[wid] = wm;
+    reds[wid] = ws;
+  }
+  __syncthreads();
+  const size_t slot = (size_t)row * a.parts + part;
+  if (tid == 0) {
+    float top = -INFINITY;
+    for (int q = 0; q < kWarps; ++q) top = fmaxf(top, redm[q]);
+    double t = 0.0;
+    for (int q = 0; q < kWarps; ++q)
+      if (redm[q] > -INFINITY || reds[q] != reds[q])
+        t += (double)reds[q] * (double)(redm[q] > -INFINITY ? ex2((redm[q] - top) * kLog2e) : 1.f);
+    a.stat[slot] = make_float2(top, (float)t);
+  }
+  // the K best groups, then their tokens
+  int n = shorten(list, kept, listed, a.K, red, all, &rth, &listed);
+  __syncthreads();
+  if (n > a.K) {
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 key = list[i];
+      int rank = 0;
+#pragma unroll 8
+      for (int q = 0; q < n; ++q) rank += list[q] > key;
+      if (rank < a.K) kept[rank] = key;
+    }
     __syncthreads();
-    best = redc[0];
+    n = a.K;
+    for (int i = tid; i < n; i += kThreads) list[i] = kept[i];
+  }
+  if (tid == 0) listed = 0;
+  __syncthreads();
+  for (int i = tid; i < 8 * n; i += kThreads) {
+    const int v = (int)~(uint32_t)list[i >> 3] + (i & 7);
+    const float y = v < hi ? Elem<T>::to_f(x[v]) : -INFINITY;
+    if (y > -INFINITY) kept[atomicAdd(&listed, 1)] = key_of(y, v);
+  }
+  __syncthreads();
+  n = shorten(kept, list, listed, a.K, red, all, &rth, &listed);
+  int2* out = a.cand + slot * a.K;
+  for (int i = tid; i < n; i += kThreads) {
+    const u64 key = kept[i];
+    int rank = 0;
+#pragma unroll 8
+    for (int q = 0; q < n; ++q) rank += kept[q] > key;
+    if (rank < a.K) out[rank] = make_int2(__float_as_int(unord32(key >> 32)), (int)~(uint32_t)key);
+  }
+  if (n < a.K && wid == 0) {  // the lowest tokens at -inf
+    int k = n;
+    for (int c = lo; c < min(hi, lo + 2 * a.K) && k < a.K; c += 32) {
+      const int v = c + lane;
+      const bool is = v < hi && Elem<T>::to_f(x[v]) == -INFINITY;
+      const uint32_t ball = __ballot_sync(0xffffffffu, is);
+      const int at = k + __popc(ball & ((1u << lane) - 1));
+      if (is && at < a.K) out[at] = make_int2(__float_as_int(-INFINITY), v);
+      k += __popc(ball);
+    }
+    for (k += lane; k < a.K; k += 32) out[k] = make_int2(0, -1);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamLaunch a) {
+  __shared__ Cand list[kJoinListed];
+  __shared__ JoinRow rows[kBeamMaxWidth];
+  __shared__ float2 stat[kBeamMaxWidth];   // a row's maximum, and whether it holds a NaN or +inf
+  __shared__ double sums[kBeamMaxWidth];
+  __shared__ uint32_t all[kThreads];
+  __shared__ uint32_t rth;
+  __shared__ Cand redc[kWarps];
+  __shared__ int listed;
+  const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  grid_dep_wait();
+  if (tid == 0) listed = 0;
+  for (int q = wid; q < a.W; q += kWarps) {  // a warp to a row, a lane to a part
+    const float2* st = a.stat + (size_t)(s * a.W + q) * a.parts;
+    const float2 p0 = lane < a.parts ? __ldcg(&st[lane]) : make_float2(-INFINITY, 0.f);
+    float M = p0.x;
+    bool nan = p0.y != p0.y;
+    for (int c = lane + 32; c < a.parts; c += 32) {
+      const float2 p = __ldcg(&st[c]);
+      nan |= p.y != p.y;
+      M = fmaxf(M, p.x);
+    }
+    M = warp_max(M);
+    nan = __any_sync(0xffffffffu, nan);
+    double t = p0.y > 0.f ? (double)p0.y * (double)ex2((p0.x - M) * kLog2e) : 0.0;
+    for (int c = lane + 32; c < a.parts; c += 32) {
+      const float2 p = __ldcg(&st[c]);
+      if (p.y > 0.f) t += (double)p.y * (double)ex2((p.x - M) * kLog2e);
+    }
+    int span = 32;
+    while (span > 1 && span / 2 >= a.parts) span >>= 1;  // lanes that hold a part
+    for (int o = span >> 1; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) {
+      stat[q] = make_float2(M, nan ? 1.f : 0.f);
+      sums[q] = t;
+    }
+  }
+  __syncthreads();
+  if (tid < a.W) {
+    const int r = s * a.W + tid;
+    const float cum = a.cum[r];
+    const bool open = cum > -INFINITY && cum < INFINITY;   // NaN and +inf count as -inf
+    const float2 st = stat[tid];
+    JoinRow j{0.0, cum, 1};
+    if (a.done && a.done[r]) {
+      j.kind = 2;
+      j.base = open ? (double)cum : -INFINITY;
+    } else if (st.y == 0.f && st.x > -INFINITY && open) {
+      j.kind = 0;
+      j.base = (double)st.x + log(sums[tid]);
+    }
+    rows[tid] = j;
+  }
+  __syncthreads();
+  // K scores reach t, the K-th largest of the threads' best lower bounds, so
+  // none of the K best has an upper bound below it
+  const int per_row = a.parts * a.K, total = a.W * per_row;
+  constexpr int kHeld = 6;  // entries that a thread reads at once, and keeps if there are no more
+  int ew[kHeld], ev[kHeld];
+  float ex[kHeld];
+  bool ee[kHeld];
+  uint32_t best = 0;
 #pragma unroll
-    for (int q = 1; q < kThreads / 32; ++q)
-      if (before(redc[q], best)) best = redc[q];
-    __syncthreads();
-    if (tid == 0) {
-      a.score[(size_t)s * a.K + k] = (float)best.s;
-      a.token[(size_t)s * a.K + k] = (int)(best.f % a.V);
-      a.beam[(size_t)s * a.K + k] = (int)(best.f / a.V);
+  for (int k = 0; k < kHeld; ++k) {  // threads behind the last entry hold none
+    ew[k] = 0;
+    ev[k] = -1;
+    ex[k] = -INFINITY;
+    ee[k] = false;
+  }
+  for (int i0 = tid; i0 < total; i0 += kHeld * kThreads) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const int i = i0 + k * kThreads;
+      ev[k] = -1;
+      if (i < total) ev[k] = join_entry(a, rows, s, i, per_row, &ew[k], &ex[k], &ee[k]);
     }
-    prevc = best;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      float lo, hi;
+      if (ev[k] < 0) continue;
+      join_bounds(rows[ew[k]], ex[k], ee[k], &lo, &hi);
+      best = max(best, ord32(lo));
+    }
+  }
+  const uint32_t t = block_rth<uint32_t>(best, a.K, all, &rth);
+  // the candidate of an entry whose upper bound reaches t
+  const auto score = [&](int w, int v, float x, bool ends, Cand* c) {
+    if (v < 0) return false;
+    const JoinRow& r = rows[w];
+    float lo, hi;
+    join_bounds(r, x, ends, &lo, &hi);
+    if (ord32(hi) < t) return false;
+    c->key = ord64(ends ? r.base : r.kind != 0 ? -INFINITY : (double)r.cum + ((double)x - r.base));
+    c->w = w;
+    c->v = v;
+    return true;
+  };
+  const auto candidate = [&](int i, Cand* c) {
+    int w;
+    float x;
+    bool ends;
+    const int v = join_entry(a, rows, s, i, per_row, &w, &x, &ends);
+    return score(w, v, x, ends, c);
+  };
+  const auto add = [&](const Cand& c) {
+    const int at = atomicAdd(&listed, 1);
+    if (at < kJoinListed) list[at] = c;
+  };
+  if (total <= kHeld * kThreads) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      Cand c;
+      if (score(ew[k], ev[k], ex[k], ee[k], &c)) add(c);
+    }
+  } else {
+    for (int i = tid; i < total; i += kThreads) {
+      Cand c;
+      if (candidate(i, &c)) add(c);
+    }
+  }
+  __syncthreads();
+  const int n = listed;
+  if (n <= kJoinListed) {
+    for (int i = tid; i < n; i += kThreads) {
+      const Cand c = list[i];
+      int rank = 0;
+#pragma unroll 4
+      for (int q = 0; q < n; ++q) rank += before(list[q], c);
+      if (rank < a.K) put(a, s, rank, c);
+    }
+    return;
+  }
+  // more equal scores than the list holds: one more of the best each round
+  Cand prev{~0ull, -1, -1};
+  for (int k = 0; k < a.K; ++k) {
+    Cand top{0, kBeamMaxWidth, 0};
+    for (int i = tid; i < total; i += kThreads) {
+      Cand c;
+      if (candidate(i, &c) && before(prev, c) && before(c, top)) top = c;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Cand d;
+      d.key = __shfl_xor_sync(0xffffffffu, top.key, o);
+      d.w = __shfl_xor_sync(0xffffffffu, top.w, o);
+      d.v = __shfl_xor_sync(0xffffffffu, top.v, o);
+      if (before(d, top)) top = d;
+    }
+    if (lane == 0) redc[wid] = top;
+    __syncthreads();
+    top = redc[0];
+#pragma unroll
+    for (int q = 1; q < kWarps; ++q)
+      if (before(redc[q], top)) top = redc[q];
+    __syncthreads();
+    if (tid == 0) put(a, s, k, top);
+    prev = top;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_beam_select(const BeamLaunch& a, dv_dtype dt, cudaStream_t stream) {
-  const dim3 grid(a.chunks, a.W, a.S);
-  switch (dt) {
-    case DV_F32: beam_kernel<float><<<grid, kThreads, 0, stream>>>(a); break;
-    case DV_F16: beam_kernel<__half><<<grid, kThreads, 0, stream>>>(a); break;
-    case DV_BF16: beam_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a); break;
+namespace {
+
+// Parts of a row: as many CTAs as the GPU holds at once (four to an SM) or a
+// multiple of it, a part costing its tiles and about two more for its start
+// and end; a small problem gets a CTA per tile.
+int part_tiles(int rows, int V, int num_sms) {
+  const int tiles = (V + kBeamTile - 1) / kBeamTile, slots = 4 * num_sms;
+  int best = tiles;
+  long long least = -1;
+  for (int t = tiles; t >= 1; --t) {
+    const long long ctas = (long long)rows * ((tiles + t - 1) / t);
+    const long long cost = (ctas + slots - 1) / slots * (t + 2);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = t;
+    }
+    if (tiles > 64 && t > 64) t = t - t / 16;  // long rows: coarser steps
   }
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) count_launches(1);
-  return e;
+  return best;
+}
+
+template <typename T>
+cudaError_t run_beam(const BeamLaunch& a, cudaStream_t stream) {
+  const cudaError_t e = launch_k(beam_scan_kernel<T>, dim3(a.parts, a.S * a.W), dim3(kThreads), 0, stream, false, 1, a);
+  if (e != cudaSuccess) return e;
+  return launch_k(beam_join_kernel, dim3(a.S), dim3(kThreads), 0, stream, true, 1, a);
+}
+
+}  // namespace
+
+cudaError_t launch_beam_select(const BeamLaunch& L, dv_dtype dt, int num_sms, cudaStream_t stream) {
+  BeamLaunch a = L;
+  a.part_tiles = part_tiles(a.S * a.W, a.V, num_sms);
+  a.parts = ((a.V + kBeamTile - 1) / kBeamTile + a.part_tiles - 1) / a.part_tiles;
+  switch (dt) {
+    case DV_F32: return run_beam<float>(a, stream);
+    case DV_F16: return run_beam<__half>(a, stream);
+    case DV_BF16: return run_beam<__nv_bfloat16>(a, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace dv

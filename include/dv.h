@@ -387,7 +387,7 @@ dv_status dv_beam_select_workspace_size(int n_seq, int width, int V, int K,
  * +inf, or nothing above -inf) and a row whose cum is not finite offer every
  * token at -inf.  Candidates are compared in double precision (sums in double
  * over fp32 exponentials); results repeat bit for bit.
- * Limits: n_seq <= 65535, width <= 32, V <= 4194304, 1 <= K <= 64 and
+ * Limits: n_seq * width <= 65535, width <= 32, V <= 4194304, 1 <= K <= 64 and
  * K <= width V. */
 dv_status dv_beam_select(const void* logits, int n_seq, int width, int V,
                          long long row_stride, dv_dtype dt, const float* cum,

@@ -577,6 +577,31 @@ def test_beam_rows_without_finite_candidates(dt):
         _beam_check(x, cum, K, torch.ones(6, 3, dtype=torch.uint8, device="cuda"), end)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("K", [1, 5, 64])
+def test_beam_values_that_crowd_the_threshold(dt, K):
+    """Inputs that list many tokens: zeros of both signs, the best tokens of a
+    row in the hands of a few threads, rows of -inf but for a few tokens,
+    long runs of equal values, ascending and descending rows over several
+    chunks."""
+    V, inf = 20001, float("inf")
+    g = _gen(K)
+    cum = torch.tensor([[0.0, -0.25]], device="cuda")
+    x = torch.zeros(1, 2, V, device="cuda")
+    x[:, :, torch.rand(V, generator=g, device="cuda") < 0.5] = -0.0
+    _beam_check(x.to(DT[dt]), cum, K)
+    v = torch.arange(V, device="cuda")
+    few = torch.where((v // 8) % 256 < 9, 4.0 + torch.randn(1, 2, V, generator=g, device="cuda"), -4.0)
+    _beam_check(few.to(DT[dt]), cum, K)
+    holes = torch.full((1, 2, V), -inf, device="cuda")
+    holes[:, :, [7, 8190, 8191, 8192, 20000]] = torch.randn(1, 2, 5, generator=g, device="cuda")
+    _beam_check(holes.to(DT[dt]), cum, K)
+    runs = (v // 700 % 5).float().expand(1, 2, V).contiguous()
+    _beam_check(runs.to(DT[dt]), cum, K)
+    _beam_check((v / V).expand(1, 2, V).contiguous().to(DT[dt]), cum, K)
+    _beam_check((-v / V).expand(1, 2, V).contiguous().to(DT[dt]), cum, K)
+
+
 def test_beam_rows_with_a_stride_and_any_alignment():
     big = torch.randn(2 * 3 * 4099 + 8, generator=_gen(3), device="cuda").half()
     for off in range(8):
