@@ -25,23 +25,20 @@ namespace dv {
 namespace {
 
 constexpr int kMoveThreads = 256;
+constexpr int kMoveWarps = kMoveThreads / 32;
 
 __device__ __forceinline__ uint4 ld16(const void* p) { return __ldcg(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ void st16(void* p, const uint4& v) { __stcg(reinterpret_cast<uint4*>(p), v); }
 
-// Advances pos once every CTA has read it: the last CTA to finish writes
-// new_pos (which may be pos itself).
-__device__ __forceinline__ bool last_cta(int* ctr, int total) {
-  __shared__ int last;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    last = atomicAdd(ctr, 1) == total - 1;
-    if (last) *ctr = 0;
-  }
-  __syncthreads();
-  return last != 0;
-}
+// ---- compact ------------------------------------------------------------------
+//
+// A warp to a head's K, V and flags, or to 512 bytes of the X rows, of one
+// sequence and layer: eight rows at a time, their loads issued together.  What
+// bounds it is the chain of small reads (count and position, list, flags, rows,
+// stores: each a round trip), so all layers go in one launch and the rest is
+// left to the number of warps.
+
+constexpr int kRowsAtOnce = 8;
 
 struct CompactArgs {
   KvPtrs kv[kKvLayers];
@@ -54,77 +51,106 @@ struct CompactArgs {
   WsHeader* hdr;
 };
 
-// Number of accepted nodes of sequence b, or -1 when its list is refused.
-__device__ int compact_count(const CompactArgs& a, int b, int* pos_out, bool report) {
+// Accepted nodes of sequence b and its position, found by one warp; -1: the
+// list is refused.
+__device__ int compact_count(const CompactArgs& a, int b, int lane, bool report, int* pos_out) {
   int n = a.count[b];
-  if (n > a.cap) {
-    if (report) set_error(a.hdr, DV_ERR_CAPACITY, n);
-    n = a.cap;
-  }
   const int p = a.pos[b];
   *pos_out = p;
+  if (n > a.cap) {
+    if (report && lane == 0) set_error(a.hdr, DV_ERR_CAPACITY, n);
+    n = a.cap;
+  }
   if (n <= 0) return 0;
-  if (p < 0 || p >= a.n_max) {
-    if (report) set_error(a.hdr, DV_ERR_POSITION, p);
-    return -1;
-  }
-  int prev = -1;
-  for (int k = 0; k < n; ++k) {
-    const int u = a.idx[(size_t)b * a.cap + k];
-    if (u <= prev) {
-      if (report) set_error(a.hdr, DV_ERR_INDEX_RANGE, u);
-      return -1;
+  const bool outside = p < 0 || p >= a.n_max;
+  int bad = 0, what = 0, before = -1;
+  for (int k0 = 0; k0 < n && !outside && !bad; k0 += 32) {
+    const int k = k0 + lane;
+    const int u = k < n ? a.idx[(size_t)b * a.cap + k] : 0;
+    int prev = __shfl_up_sync(0xffffffffu, u, 1);
+    if (lane == 0) prev = before;
+    const int mine = k >= n ? 0 : u <= prev ? DV_ERR_INDEX_RANGE : u >= a.n_max - p ? DV_ERR_POSITION : 0;
+    const uint32_t ball = __ballot_sync(0xffffffffu, mine != 0);
+    if (ball) {
+      const int src = __ffs(ball) - 1;
+      bad = __shfl_sync(0xffffffffu, mine, src);
+      what = __shfl_sync(0xffffffffu, u, src);
     }
-    if (u >= a.n_max - p) {
-      if (report) set_error(a.hdr, DV_ERR_POSITION, p);
-      return -1;
-    }
-    prev = u;
+    before = __shfl_sync(0xffffffffu, u, 31);
   }
-  return n;
+  if (outside) bad = DV_ERR_POSITION;
+  if (bad && report && lane == 0) set_error(a.hdr, bad, bad == DV_ERR_POSITION ? p : what);
+  return bad ? -1 : n;
 }
 
-// grid (part, b, layer): part 0..h-1 a head's K and V rows, part h the X rows
+// grid (groups of eight warp items, b, layer)
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_constant__ CompactArgs a) {
-  const int part = blockIdx.x, b = blockIdx.y, layer = blockIdx.z;
+  __shared__ int last;
+  const int b = blockIdx.y, layer = blockIdx.z;
+  const int lane = threadIdx.x & 31, item = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
+  const bool first = blockIdx.x == 0 && layer == 0 && threadIdx.x < 32;
   int p;
-  const int n = compact_count(a, b, &p, part == 0 && layer == 0 && threadIdx.x == 0);
+  const int n = compact_count(a, b, lane, first, &p);
   const KvPtrs& kv = a.kv[layer];
   const int32_t* idx = a.idx + (size_t)b * a.cap;
-  if (n > 0) {
-    if (part < a.h) {
-      uint8_t* flags = kv.valid + ((size_t)b * a.h + part) * a.n_max + p;
-      char* rows[2] = {kv.K, kv.V};
-      const size_t pitch = (size_t)a.kv_chunks * 16;
-      const size_t base = (((size_t)b * a.h + part) * a.n_max + p) * pitch;
-      for (int c = threadIdx.x; c < 2 * a.kv_chunks; c += blockDim.x) {
-        char* row = rows[c >= a.kv_chunks] + base + (size_t)(c % a.kv_chunks) * 16;
-        for (int k = 0; k < n; ++k) {
-          const int u = idx[k];
-          if (u != k && flags[u]) st16(row + k * pitch, ld16(row + u * pitch));
-        }
+  const bool head = item < a.h;
+  const int x0 = (item - a.h) * 32;                       // first chunk of an X item
+  const int items = head ? 2 * a.kv_chunks : min(32, a.x_chunks - x0);
+  const size_t pitch = (size_t)(head ? a.kv_chunks : a.x_chunks) * 16;
+  const size_t row0 = head ? ((size_t)b * a.h + item) * a.n_max + p : (size_t)b * a.n_max + p;
+  uint8_t* flags = head ? kv.valid + row0 : nullptr;
+  for (int k0 = 0; k0 < n && items > 0; k0 += kRowsAtOnce) {
+    // lane k: slot and flag of row k0 + k
+    const bool live = lane < kRowsAtOnce && k0 + lane < n;
+    const int my_u = live ? idx[k0 + lane] : 0;
+    const uint8_t flag = live && head ? flags[my_u] : 0;
+    const uint32_t move = __ballot_sync(0xffffffffu, live && my_u != k0 + lane && (!head || flag));
+    for (int c = lane; c - lane < items; c += 32) {
+      char* col = nullptr;
+      if (c < items)
+        col = head ? (c < a.kv_chunks ? kv.K + c * 16 : kv.V + (c - a.kv_chunks) * 16) + row0 * pitch
+                   : kv.X + row0 * pitch + (size_t)(x0 + c) * 16;
+      uint4 v[kRowsAtOnce];
+#pragma unroll
+      for (int k = 0; k < kRowsAtOnce; ++k) {
+        const int u = __shfl_sync(0xffffffffu, my_u, k);
+        if (((move >> k) & 1) && col) v[k] = ld16(col + u * pitch);
       }
-      __syncthreads();
-      if (threadIdx.x == 0)
-        for (int k = 0; k < n; ++k) flags[k] = flags[idx[k]];
-    } else {
-      const size_t pitch = (size_t)a.x_chunks * 16;
-      char* base = kv.X + ((size_t)b * a.n_max + p) * pitch;
-      for (int c = threadIdx.x; c < a.x_chunks; c += blockDim.x)
-        for (int k = 0; k < n; ++k)
-          if (idx[k] != k) st16(base + k * pitch + (size_t)c * 16, ld16(base + idx[k] * pitch + (size_t)c * 16));
+#pragma unroll
+      for (int k = 0; k < kRowsAtOnce; ++k)
+        if (((move >> k) & 1) && col) st16(col + (k0 + k) * pitch, v[k]);
     }
+    if (live && head) flags[k0 + lane] = flag;
+    __syncwarp();
   }
-  if (a.new_pos) {
-    if (last_cta(&a.hdr->pad[0], gridDim.x * gridDim.y * gridDim.z)) {
-      for (int s = threadIdx.x; s < a.B; s += blockDim.x) {
-        int q;
-        const int m = compact_count(a, s, &q, false);
-        a.new_pos[s] = q + max(m, 0);
-      }
-    }
+  if (!a.new_pos) return;
+  if (a.new_pos != a.pos) {
+    if (first && lane == 0) a.new_pos[b] = p + max(n, 0);
+    return;
+  }
+  // in place: once every CTA has read pos, the last one advances it
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicAdd(&a.hdr->pad[0], 1) == (int)(gridDim.x * gridDim.y * gridDim.z) - 1;
+    if (last) a.hdr->pad[0] = 0;
+  }
+  __syncthreads();
+  if (!last) return;
+  for (int s = threadIdx.x >> 5; s < a.B; s += kMoveWarps) {
+    int q;
+    const int m = compact_count(a, s, lane, false, &q);
+    if (lane == 0) a.new_pos[s] = q + max(m, 0);
   }
 }
+
+// ---- reorder ------------------------------------------------------------------
+//
+// A CTA takes 64 positions of one head's K, V and flags, or of 512 bytes of the
+// X rows, of one sequence and layer.  Every parent that is taken is read once
+// and written to each of the beams that continue it.
+
+constexpr int kSpan = 64;      // positions of a CTA
 
 struct ReorderArgs {
   KvPtrs kv[kKvLayers];
@@ -135,108 +161,118 @@ struct ReorderArgs {
   WsHeader* hdr;
 };
 
-// grid (part, position block, layer * S + s)
+// grid (heads and X parts, position blocks, layer * S + s)
 template <int WM>
 __global__ void __launch_bounds__(kMoveThreads) reorder_kernel(const __grid_constant__ ReorderArgs a) {
-  __shared__ int par[WM], hi[WM];
+  __shared__ uint32_t heirs[WM];   // the beams that continue beam p, itself apart
+  __shared__ int upto[WM];         // positions held by beam p, 0 where it has no heirs
   __shared__ int lo_s;
   const int part = blockIdx.x, s = blockIdx.z % a.S, layer = blockIdx.z / a.S;
   const KvPtrs& kv = a.kv[layer];
-  if (threadIdx.x < WM) {
+  if (threadIdx.x < 32) {
     const int w = threadIdx.x;
-    int p = w, top = 0;
+    int p = w;
     if (w < a.W) {
       p = a.parent[s * a.W + w];
+      const bool report = part == 0 && layer == 0 && blockIdx.y == 0;
       if (p < 0 || p >= a.W) {
-        if (part == 0 && layer == 0 && blockIdx.y == 0) set_error(a.hdr, DV_ERR_INDEX_RANGE, p);
+        if (report) set_error(a.hdr, DV_ERR_INDEX_RANGE, p);
         p = w;
       }
-      top = a.pos[s * a.W + p];
+      int top = a.pos[s * a.W + w];
       if (top < 0 || top > a.n_max) {
-        if (part == 0 && layer == 0 && blockIdx.y == 0) set_error(a.hdr, DV_ERR_POSITION, top);
-        top = 0;
+        top = -1;  // an error only where another beam continues this one
       }
+      if (w < WM) upto[w] = top;
     }
-    par[w] = p;
-    hi[w] = p == w ? 0 : top;   // a beam that continues itself stays as it is
+    uint32_t mine = 0;
+    for (int q = 0; q < a.W; ++q) {
+      const int pq = __shfl_sync(0xffffffffu, p, q);
+      if (pq == w && q != w) mine |= 1u << q;
+    }
+    if (w < a.W) {
+      if (mine && upto[w] < 0 && part == 0 && layer == 0 && blockIdx.y == 0)
+        set_error(a.hdr, DV_ERR_POSITION, a.pos[s * a.W + w]);
+      heirs[w] = mine;
+      if (!mine || upto[w] < 0) upto[w] = 0;
+    } else if (w < WM) {
+      heirs[w] = 0;
+      upto[w] = 0;
+    }
     if (w == 0) lo_s = a.start ? max(a.start[s], 0) : 0;
   }
   __syncthreads();
   int top = 0;
-  for (int w = 0; w < a.W; ++w) top = max(top, hi[w]);
-  const bool is_x = part == a.h;
-  const int chunks = is_x ? a.x_chunks : a.kv_chunks;
-  const size_t pitch = (size_t)chunks * 16;
-  const int tensors = is_x ? 1 : 2;
+#pragma unroll
+  for (int p = 0; p < WM; ++p) top = max(top, upto[p]);
+  const int j0 = lo_s + blockIdx.y * kSpan, j1 = min(j0 + kSpan, top);
+  if (j0 < lo_s || j0 >= j1) return;   // (j0 < lo_s: a start near the largest integer)
+  const bool is_x = part >= a.h;
+  const int c_first = is_x ? (part - a.h) * 32 : 0;
+  const int chunks = is_x ? min(32, a.x_chunks - c_first) : a.kv_chunks;
+  const size_t pitch = (size_t)(is_x ? a.x_chunks : a.kv_chunks) * 16;
   const size_t row0 = (size_t)s * a.W;
-  const size_t beam_rows = is_x ? a.n_max : (size_t)a.h * a.n_max;       // rows between two beams
+  const size_t beam_rows = is_x ? (size_t)a.n_max : (size_t)a.h * a.n_max;  // rows between two beams
   const size_t first = is_x ? row0 * a.n_max : (row0 * a.h + part) * a.n_max;
-  const uint8_t* flags = kv.valid + (row0 * a.h + (is_x ? 0 : part)) * a.n_max;
-  const int per = kMoveThreads / chunks > 0 ? kMoveThreads / chunks : 1;  // positions a block handles at once
-  const int lanes = chunks < kMoveThreads ? chunks : kMoveThreads;
+  const size_t flag_beam = (size_t)a.h * a.n_max;
+  uint8_t* flags = is_x ? nullptr : kv.valid + first;
+  const int lanes = min(chunks, kMoveThreads), per = kMoveThreads / lanes;  // positions at once
   const int sub = threadIdx.x / lanes, c0 = threadIdx.x % lanes;
-  for (int j = lo_s + blockIdx.y * per + sub; j < top && sub < per; j += gridDim.y * per) {
-    for (int t = 0; t < tensors; ++t) {
-      char* base = (is_x ? kv.X : t ? kv.V : kv.K) + (first + j) * pitch;
+  if (sub < per) {
+    for (int j = j0 + sub; j < j1; j += per) {
+      uint32_t take = 0;
+#pragma unroll
+      for (int p = 0; p < WM; ++p)
+        if (j < upto[p] && (is_x || flags[p * flag_beam + j])) take |= 1u << p;
       for (int c = c0; c < chunks; c += lanes) {
-        uint4 v[WM];
-        bool take[WM];
+        const size_t at = (first + j) * pitch + (size_t)(c_first + c) * 16, step = beam_rows * pitch;
+        // up to eight beams: K and V together (128 bytes in flight a thread)
+        constexpr int kTogether = WM <= 8 ? 2 : 1;
+        const int tensors = is_x ? 1 : 2;
+        for (int t = 0; t < tensors; t += kTogether) {
+          char* b0 = (is_x ? kv.X : t ? kv.V : kv.K) + at;
+          char* b1 = kTogether == 2 && !is_x ? kv.V + at : nullptr;
+          uint4 v[WM], u[kTogether == 2 ? WM : 1];
 #pragma unroll
-        for (int w = 0; w < WM; ++w) {
-          const int p = par[w];
-          take[w] = j < hi[w] && (is_x || flags[(size_t)p * a.h * a.n_max + j]);
-          if (take[w]) v[w] = ld16(base + p * beam_rows * pitch + (size_t)c * 16);
+          for (int p = 0; p < WM; ++p) {
+            if ((take >> p) & 1) {
+              v[p] = ld16(b0 + p * step);
+              if (kTogether == 2 && b1) u[p % (kTogether == 2 ? WM : 1)] = ld16(b1 + p * step);
+            }
+          }
+#pragma unroll
+          for (int p = 0; p < WM; ++p) {
+            if ((take >> p) & 1) {
+              for (uint32_t m = heirs[p]; m; m &= m - 1) {
+                const size_t to = (__ffs(m) - 1) * step;
+                st16(b0 + to, v[p]);
+                if (kTogether == 2 && b1) st16(b1 + to, u[p % (kTogether == 2 ? WM : 1)]);
+              }
+            }
+          }
         }
-#pragma unroll
-        for (int w = 0; w < WM; ++w)
-          if (take[w]) st16(base + w * beam_rows * pitch + (size_t)c * 16, v[w]);
       }
     }
   }
-}
-
-// the flags move after the rows that they describe
-template <int WM>
-__global__ void __launch_bounds__(kMoveThreads) reorder_flags_kernel(const __grid_constant__ ReorderArgs a) {
-  __shared__ int par[WM], hi[WM];
-  const int i = blockIdx.x, s = blockIdx.y, layer = blockIdx.z;
-  if (threadIdx.x < WM) {
-    const int w = threadIdx.x;
-    int p = w, top = 0;
-    if (w < a.W) {
-      p = a.parent[s * a.W + w];
-      if (p < 0 || p >= a.W) p = w;
-      top = a.pos[s * a.W + p];
-      if (top < 0 || top > a.n_max) top = 0;
-    }
-    par[w] = p;
-    hi[w] = p == w ? 0 : top;
-  }
-  __syncthreads();
-  int top = 0;
-  for (int w = 0; w < a.W; ++w) top = max(top, hi[w]);
-  const int lo = a.start ? max(a.start[s], 0) : 0;
-  const size_t beam = (size_t)a.h * a.n_max;
-  uint8_t* flags = a.kv[layer].valid + ((size_t)s * a.W * a.h + i) * a.n_max;
-  for (int j = lo + threadIdx.x; j < top; j += blockDim.x) {
+  if (is_x) return;
+  __syncthreads();  // the flags of these positions are read
+  for (int j = j0 + threadIdx.x; j < j1; j += kMoveThreads) {
     uint8_t f[WM];
 #pragma unroll
-    for (int w = 0; w < WM; ++w) f[w] = j < hi[w] ? flags[par[w] * beam + j] : 0;
+    for (int p = 0; p < WM; ++p) f[p] = j < upto[p] ? flags[p * flag_beam + j] : 0;
 #pragma unroll
-    for (int w = 0; w < WM; ++w)
-      if (j < hi[w]) flags[w * beam + j] = f[w];
+    for (int p = 0; p < WM; ++p)
+      if (j < upto[p])
+        for (uint32_t m = heirs[p]; m; m &= m - 1) flags[(__ffs(m) - 1) * flag_beam + j] = f[p];
   }
 }
 
 template <int WM>
 cudaError_t run_reorder(const ReorderArgs& a, int n_kv, cudaStream_t stream) {
-  const int blocks = max(1, min(64, a.n_max / 16));
-  reorder_kernel<WM><<<dim3(a.h + 1, blocks, n_kv * a.S), kMoveThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  reorder_flags_kernel<WM><<<dim3(a.h, a.S, n_kv), kMoveThreads, 0, stream>>>(a);
-  e = cudaGetLastError();
-  if (e == cudaSuccess) count_launches(2);
+  const int parts = a.h + (a.x_chunks + 31) / 32, blocks = (a.n_max + kSpan - 1) / kSpan;
+  reorder_kernel<WM><<<dim3(parts, blocks, n_kv * a.S), kMoveThreads, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) count_launches(1);
   return e;
 }
 
@@ -251,7 +287,8 @@ cudaError_t launch_kv_compact(const KvMove& m, const int32_t* idx, int cap, cons
     a.B = m.B; a.h = m.h; a.n_max = m.n_max; a.kv_chunks = m.kv_chunks; a.x_chunks = m.x_chunks;
     a.pos = m.pos; a.idx = idx; a.cap = cap; a.count = count; a.hdr = hdr;
     a.new_pos = l0 + n == m.n_kv ? new_pos : nullptr;
-    compact_kernel<<<dim3(m.h + 1, m.B, n), kMoveThreads, 0, stream>>>(a);
+    const int items = m.h + (m.x_chunks + 31) / 32;
+    compact_kernel<<<dim3((items + kMoveWarps - 1) / kMoveWarps, m.B, n), kMoveThreads, 0, stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     count_launches(1);
