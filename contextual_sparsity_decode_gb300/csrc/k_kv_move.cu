@@ -54,6 +54,9 @@ struct CompactArgs {
 // Accepted nodes of sequence b and its position, found by one warp; -1: the
 // list is refused.
 __device__ int compact_count(const CompactArgs& a, int b, int lane, bool report, int* pos_out) {
+  // three reads at once: the list's first entries do not wait for its length
+  const int32_t* idx = a.idx + (size_t)b * a.cap;
+  const int u0 = lane < a.cap ? idx[lane] : 0;
   int n = a.count[b];
   const int p = a.pos[b];
   *pos_out = p;
@@ -66,7 +69,7 @@ __device__ int compact_count(const CompactArgs& a, int b, int lane, bool report,
   int bad = 0, what = 0, before = -1;
   for (int k0 = 0; k0 < n && !outside && !bad; k0 += 32) {
     const int k = k0 + lane;
-    const int u = k < n ? a.idx[(size_t)b * a.cap + k] : 0;
+    const int u = k0 == 0 ? u0 : k < n ? idx[k] : 0;
     int prev = __shfl_up_sync(0xffffffffu, u, 1);
     if (lane == 0) prev = before;
     const int mine = k >= n ? 0 : u <= prev ? DV_ERR_INDEX_RANGE : u >= a.n_max - p ? DV_ERR_POSITION : 0;
@@ -84,7 +87,7 @@ __device__ int compact_count(const CompactArgs& a, int b, int lane, bool report,
 }
 
 // grid (groups of eight warp items, b, layer)
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_constant__ CompactArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 4) compact_kernel(const __grid_constant__ CompactArgs a) {
   __shared__ int last;
   const int b = blockIdx.y, layer = blockIdx.z;
   const int lane = threadIdx.x & 31, item = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
@@ -146,15 +149,16 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_cons
 
 // ---- reorder ------------------------------------------------------------------
 //
-// A CTA takes 64 positions of one head's K, V and flags, or of 512 bytes of the
+// A CTA takes 128 positions of one head's K, V and flags, or of 512 bytes of the
 // X rows, of one sequence and layer.  Every parent that is taken is read once
 // and written to each of the beams that continue it.
 
-constexpr int kSpan = 64;      // positions of a CTA
+constexpr int kSpan = 128;     // positions of a CTA, at most
 
 struct ReorderArgs {
   KvPtrs kv[kKvLayers];
   int S, W, h, n_max, kv_chunks, x_chunks;
+  int span;                      // positions of a CTA
   const int32_t* pos;
   const int32_t* start;
   const int32_t* parent;
@@ -166,23 +170,38 @@ template <int WM>
 __global__ void __launch_bounds__(kMoveThreads) reorder_kernel(const __grid_constant__ ReorderArgs a) {
   __shared__ uint32_t heirs[WM];   // the beams that continue beam p, itself apart
   __shared__ int upto[WM];         // positions held by beam p, 0 where it has no heirs
-  __shared__ int lo_s;
+  __shared__ uint32_t there[kSpan];  // bit p: beam p's K/V at the position are present (and wanted)
   const int part = blockIdx.x, s = blockIdx.z % a.S, layer = blockIdx.z / a.S;
   const KvPtrs& kv = a.kv[layer];
+  const bool is_x = part >= a.h;
+  const size_t row0 = (size_t)s * a.W, flag_beam = (size_t)a.h * a.n_max;
+  const size_t first = is_x ? row0 * a.n_max : (row0 * a.h + part) * a.n_max;
+  uint8_t* flags = is_x ? nullptr : kv.valid + first;
+  const int lo = a.start ? max(a.start[s], 0) : 0;
+  if (lo >= a.n_max || lo + (int)blockIdx.y * a.span >= a.n_max) return;
+  const int j0 = lo + blockIdx.y * a.span;
+  if (threadIdx.x >= 128 && threadIdx.x < 128 + a.span) {  // the flags do not wait for the parents
+    const int j = j0 + threadIdx.x - 128;
+    uint32_t m = is_x ? ~0u : 0u;
+    if (!is_x && j < a.n_max) {
+#pragma unroll
+      for (int p = 0; p < WM; ++p)
+        if (p < a.W && flags[p * flag_beam + j]) m |= 1u << p;
+    }
+    there[threadIdx.x - 128] = m;
+  }
   if (threadIdx.x < 32) {
     const int w = threadIdx.x;
     int p = w;
     if (w < a.W) {
+      int top = a.pos[s * a.W + w];
       p = a.parent[s * a.W + w];
       const bool report = part == 0 && layer == 0 && blockIdx.y == 0;
       if (p < 0 || p >= a.W) {
         if (report) set_error(a.hdr, DV_ERR_INDEX_RANGE, p);
         p = w;
       }
-      int top = a.pos[s * a.W + w];
-      if (top < 0 || top > a.n_max) {
-        top = -1;  // an error only where another beam continues this one
-      }
+      if (top < 0 || top > a.n_max) top = -1;  // an error only where another beam continues this one
       if (w < WM) upto[w] = top;
     }
     uint32_t mine = 0;
@@ -199,31 +218,25 @@ __global__ void __launch_bounds__(kMoveThreads) reorder_kernel(const __grid_cons
       heirs[w] = 0;
       upto[w] = 0;
     }
-    if (w == 0) lo_s = a.start ? max(a.start[s], 0) : 0;
   }
   __syncthreads();
   int top = 0;
 #pragma unroll
   for (int p = 0; p < WM; ++p) top = max(top, upto[p]);
-  const int j0 = lo_s + blockIdx.y * kSpan, j1 = min(j0 + kSpan, top);
-  if (j0 < lo_s || j0 >= j1) return;   // (j0 < lo_s: a start near the largest integer)
-  const bool is_x = part >= a.h;
+  const int j1 = min(j0 + a.span, top);
+  if (j0 >= j1) return;
   const int c_first = is_x ? (part - a.h) * 32 : 0;
   const int chunks = is_x ? min(32, a.x_chunks - c_first) : a.kv_chunks;
   const size_t pitch = (size_t)(is_x ? a.x_chunks : a.kv_chunks) * 16;
-  const size_t row0 = (size_t)s * a.W;
-  const size_t beam_rows = is_x ? (size_t)a.n_max : (size_t)a.h * a.n_max;  // rows between two beams
-  const size_t first = is_x ? row0 * a.n_max : (row0 * a.h + part) * a.n_max;
-  const size_t flag_beam = (size_t)a.h * a.n_max;
-  uint8_t* flags = is_x ? nullptr : kv.valid + first;
+  const size_t beam_rows = is_x ? (size_t)a.n_max : flag_beam;  // rows between two beams
   const int lanes = min(chunks, kMoveThreads), per = kMoveThreads / lanes;  // positions at once
   const int sub = threadIdx.x / lanes, c0 = threadIdx.x % lanes;
   if (sub < per) {
     for (int j = j0 + sub; j < j1; j += per) {
-      uint32_t take = 0;
+      uint32_t take = there[j - j0];
 #pragma unroll
       for (int p = 0; p < WM; ++p)
-        if (j < upto[p] && (is_x || flags[p * flag_beam + j])) take |= 1u << p;
+        if (j >= upto[p]) take &= ~(1u << p);
       for (int c = c0; c < chunks; c += lanes) {
         const size_t at = (first + j) * pitch + (size_t)(c_first + c) * 16, step = beam_rows * pitch;
         // up to eight beams: K and V together (128 bytes in flight a thread)
@@ -268,9 +281,17 @@ __global__ void __launch_bounds__(kMoveThreads) reorder_kernel(const __grid_cons
 }
 
 template <int WM>
-cudaError_t run_reorder(const ReorderArgs& a, int n_kv, cudaStream_t stream) {
-  const int parts = a.h + (a.x_chunks + 31) / 32, blocks = (a.n_max + kSpan - 1) / kSpan;
-  reorder_kernel<WM><<<dim3(parts, blocks, n_kv * a.S), kMoveThreads, 0, stream>>>(a);
+cudaError_t run_reorder(const ReorderArgs& r, int n_kv, cudaStream_t stream) {
+  ReorderArgs a = r;
+  const int parts = a.h + (a.x_chunks + 31) / 32;
+  // Long spans spread a CTA's start (parents, flags) over more rows; a small
+  // problem is spread over the SMs instead (four beams of one layer, 112
+  // positions: 10.7 us with 128 positions a CTA, 5.1 with 16; eight beams of
+  // 56 heads: 454 us with 64, 370 with 128).
+  const auto blocks = [&](int span) { return (a.n_max + span - 1) / span; };
+  a.span = kSpan;
+  while (a.span > 16 && (long long)parts * blocks(a.span) * n_kv * a.S < 4 * num_sms_current()) a.span /= 2;
+  reorder_kernel<WM><<<dim3(parts, blocks(a.span), n_kv * a.S), kMoveThreads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) count_launches(1);
   return e;
