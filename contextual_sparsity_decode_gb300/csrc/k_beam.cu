@@ -44,8 +44,6 @@ constexpr int kListed = kLong + kBeamTile / 8;  // a tile's groups always fit be
 static_assert(kListed >= kBeamMaxK * 8, "the best groups' tokens fit too");
 constexpr int kFew = 256;                     // entries ranked against each other directly
 constexpr int kJoinListed = 1024;
-constexpr float kLog2e = 1.4426950408889634f;
-
 typedef unsigned long long u64;
 
 // Order-preserving map of a float to unsigned (-0 as 0).
@@ -57,35 +55,6 @@ __device__ __forceinline__ float unord32(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 __device__ __forceinline__ u64 key_of(float f, int v) { return ((u64)ord32(f) << 32) | (uint32_t)~v; }
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-// (a0, a1) + (b, b) and (a0, a1) * (b, b): two fp32 operations an instruction
-__device__ __forceinline__ u64 pack2(float a, float b) {
-  u64 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ void open2(u64 x, float* a, float* b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(x)); }
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-  u64 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-  u64 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 
 // The r-th largest of a warp's values, equal ones counted singly; 0 where
 // fewer are not 0.

@@ -26,8 +26,9 @@
 namespace dv {
 namespace {
 
+typedef unsigned long long u64;
+
 constexpr int kKeys = 64;      // keys per tile
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct TreeArgs {
   TreeLaunch L;
@@ -46,7 +47,6 @@ struct Seg {
   int b, head, row0, rows;       // rows row0 .. row0 + rows - 1 of the sequence's T g
   int pos, nodes, n;             // committed positions, tree nodes, their sum
   int k0, k1, tiles;             // tiles [k0, k1) of the unit's `tiles`
-  int owner, pieces;             // CTA of the unit's first tile, CTAs that share it
   bool ok;                       // the head index is in range
 };
 
@@ -104,16 +104,31 @@ __device__ void tree_plan(const TreeArgs& a, TreePlan* p, int rows_per_unit) {
   __syncthreads();
 }
 
-// Walks the segments of this CTA's share of the tiles.
+// a / b; short where both fit 32 bits, as they nearly always do
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
+// Walks the segments of this CTA's share of the tiles: of W tiles, the first
+// W % G of the G CTAs that take part get one more than W / G.
 struct Cursor {
-  long long t, t1, W;
-  int G, b;
+  long long t, t1;   // next tile, end of the share
+  long long q, r;    // W / G, W % G
+  int b;
   __device__ Cursor(const TreePlan& p, int B) {
-    W = p.pre[B];
-    G = (int)(W < (long long)gridDim.x ? W : (long long)gridDim.x);
+    const long long W = p.pre[B];
+    const long long G = W < (long long)gridDim.x ? W : (long long)gridDim.x;
     const int c = blockIdx.x;
-    t = c < G ? W * c / G : 0;
-    t1 = c < G ? W * (c + 1) / G : 0;
+    if (c >= G) {
+      t = t1 = q = r = 0;
+      b = 0;
+      return;
+    }
+    q = quot(W, G);
+    r = W - q * G;
+    t = c * q + min((long long)c, r);
+    t1 = t + q + (c < r);
     int lo = 0, hi = B;  // the last b with pre[b] <= t
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -121,6 +136,11 @@ struct Cursor {
       else hi = mid;
     }
     b = lo;
+  }
+  // The CTA whose share holds tile x.
+  __device__ int cta_of(long long x) const {
+    const long long wide = r * (q + 1);
+    return (int)(x < wide ? quot(x, q + 1) : r + quot(x - wide, q));
   }
   __device__ bool next(const TreeLaunch& L, const TreePlan& p, int rows_per_unit, Seg* s) {
     if (t >= t1) return false;
@@ -130,22 +150,35 @@ struct Cursor {
     s->nodes = p.nodes[b];
     s->n = s->pos + s->nodes;
     const int all_rows = s->nodes * L.g;
-    const int blocks = (all_rows + rows_per_unit - 1) / rows_per_unit;
     s->tiles = (s->n + kKeys - 1) / kKeys;
     const long long off = t - p.pre[b];
-    const long long unit = off / s->tiles;
+    const long long unit = quot(off, s->tiles);
     s->k0 = (int)(off - unit * s->tiles);
     s->k1 = (int)min((long long)s->tiles, s->k0 + (t1 - t));
-    const int slot = (int)(unit / blocks);
-    s->row0 = (int)(unit - (long long)slot * blocks) * rows_per_unit;
+    int slot = (int)unit;
+    s->row0 = 0;
+    if (all_rows > rows_per_unit) {
+      const int blocks = (all_rows + rows_per_unit - 1) / rows_per_unit;
+      slot = (int)quot(unit, blocks);
+      s->row0 = (int)(unit - (long long)slot * blocks) * rows_per_unit;
+    }
     s->rows = min(rows_per_unit, all_rows - s->row0);
     s->head = L.head_idx ? L.head_idx[(size_t)b * L.cap + slot] : slot;
     s->ok = s->head >= 0 && s->head < L.h;
-    const long long u0 = t - s->k0, u1 = u0 + s->tiles - 1;
-    s->owner = (int)(((u0 + 1) * G - 1) / W);
-    s->pieces = (int)(((u1 + 1) * G - 1) / W) - s->owner + 1;
     t += s->k1 - s->k0;
     return true;
+  }
+  // The CTAs that share the unit of the segment that next() gave last: the
+  // first and their number.
+  __device__ void pieces(const Seg& s, int* owner, int* count) const {
+    if (s.k0 == 0 && s.k1 == s.tiles) {
+      *owner = blockIdx.x;
+      *count = 1;
+      return;
+    }
+    const long long u0 = t - s.k1;
+    *owner = s.k0 == 0 ? (int)blockIdx.x : cta_of(u0);
+    *count = (s.k1 == s.tiles ? (int)blockIdx.x : cta_of(u0 + s.tiles - 1)) - *owner + 1;
   }
 };
 
@@ -184,26 +217,60 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* dst, float 
 }
 
 // Joins the partial results of a unit, in tile order, and writes its rows.
-// Called by NT threads of the CTA that finished last.
+// Called by NT threads of the CTA that finished last: a thread to a row and two
+// groups of four columns at a time, four pieces' loads in flight together.
 template <typename T, int DH, int NT>
-__device__ void join_unit(const TreeLaunch& L, const Seg& s, int tid) {
-  for (int i = tid; i < s.rows * (DH / 4); i += NT) {
-    const int r = i % s.rows, c4 = i / s.rows;
-    float M = -INFINITY;
-    for (int q = 0; q < s.pieces; ++q)
-      M = fmaxf(M, __ldcg(&L.ml[piece_slot(s.owner + q, q == 0) * L.rows_pad + r].x));
-    float l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-    for (int q = 0; q < s.pieces; ++q) {
-      const size_t slot = piece_slot(s.owner + q, q == 0);
-      const float2 ml = __ldcg(&L.ml[slot * L.rows_pad + r]);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(L.part) + (slot * (DH / 4) + c4) * L.rows_pad + r);
-      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      l = fmaf(ml.y, w, l);
-      o0 = fmaf(o.x, w, o0); o1 = fmaf(o.y, w, o1);
-      o2 = fmaf(o.z, w, o2); o3 = fmaf(o.w, w, o3);
+__device__ void join_unit(const TreeLaunch& L, const Seg& s, int owner, int pieces, int tid) {
+  constexpr int kP = 2, kC = 2;
+  const int groups = NT / s.rows, grp = tid / s.rows, r = tid - grp * s.rows;
+  if (grp >= groups) return;
+  T* dst = static_cast<T*>(L.out) + row_offset(L, s, r, DH);
+  for (int c0 = grp; c0 < DH / 4; c0 += kC * groups) {
+    float M = -INFINITY, l = 0.f;
+    float4 o[kC];
+#pragma unroll
+    for (int c = 0; c < kC; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q0 = 0; q0 < pieces; q0 += kP) {
+      float2 ml[kP];
+      float4 x[kP][kC];
+#pragma unroll
+      for (int q = 0; q < kP; ++q) {
+        ml[q] = make_float2(-INFINITY, 0.f);
+        if (q0 + q >= pieces) continue;
+        const size_t slot = piece_slot(owner + q0 + q, q0 + q == 0);
+        ml[q] = __ldcg(&L.ml[slot * L.rows_pad + r]);
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          if (c0 + c * groups < DH / 4)
+            x[q][c] = __ldcg(reinterpret_cast<const float4*>(L.part) + (slot * (DH / 4) + c0 + c * groups) * L.rows_pad + r);
+      }
+      float m = M;
+#pragma unroll
+      for (int q = 0; q < kP; ++q) m = fmaxf(m, ml[q].x);
+      const float keep = M == -INFINITY ? 0.f : ex2(M - m);
+      M = m;
+      l *= keep;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) { o[c].x *= keep; o[c].y *= keep; o[c].z *= keep; o[c].w *= keep; }
+#pragma unroll
+      for (int q = 0; q < kP; ++q) {
+        if (q0 + q >= pieces) continue;
+        // (a piece whose maximum is -inf has sums of 0, or a NaN)
+        const float w = ml[q].x == -INFINITY ? (ml[q].y == 0.f ? 0.f : 1.f) : ex2(ml[q].x - m);
+        l = fmaf(ml[q].y, w, l);
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          if (c0 + c * groups >= DH / 4) continue;
+          o[c].x = fmaf(x[q][c].x, w, o[c].x); o[c].y = fmaf(x[q][c].y, w, o[c].y);
+          o[c].z = fmaf(x[q][c].z, w, o[c].z); o[c].w = fmaf(x[q][c].w, w, o[c].w);
+        }
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing is zero
-    store4<T>(static_cast<T*>(L.out) + row_offset(L, s, r, DH) + 4 * c4, o0 * inv, o1 * inv, o2 * inv, o3 * inv);
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+      if (c0 + c * groups < DH / 4)
+        store4<T>(dst + 4 * (c0 + c * groups), o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv);
   }
 }
 
@@ -262,6 +329,8 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   constexpr int kVec = Elem<T>::kVec, kChunks = DH / kVec;
   constexpr int kCols = DH / 16;   // output columns of a thread
+  grid_dep_launch();
+  grid_dep_wait();
   tree_plan<kSimtThreads>(a, &sm.plan, kSimtRows);
   zero_rows<T, DH>(L, sm.plan, blockIdx.x * (kSimtThreads / 32) + wid, gridDim.x * (kSimtThreads / 32), lane, 32);
   Cursor cur(sm.plan, L.B);
@@ -371,7 +440,9 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
       }
     }
     const int r = tid / 16, c0 = (tid % 16) * 4;
-    if (s.pieces == 1) {
+    int owner, pieces;
+    cur.pieces(s, &owner, &pieces);
+    if (pieces == 1) {
       if (r < s.rows) {
         const float l = sm.l[r], inv = l == 0.f ? 0.f : 1.f / l;
         T* dst = static_cast<T*>(L.out) + row_offset(L, s, r, DH) + c0;
@@ -389,15 +460,15 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
         __stcg(dst + (size_t)((c0 + c * 16) / 4) * L.rows_pad, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
       if (c0 == 0) __stcg(&L.ml[slot * L.rows_pad + r], make_float2(sm.m[r], sm.l[r]));
     }
-    __threadfence();
     __syncthreads();
     if (tid == 0) {
-      sm.last = atomicAdd(&L.ctr[s.owner], 1) == s.pieces - 1;
-      if (sm.last) L.ctr[s.owner] = 0;
+      __threadfence();  // (the barrier before it makes it cover the CTA's stores)
+      sm.last = atomicAdd(&L.ctr[owner], 1) == pieces - 1;
+      if (sm.last) L.ctr[owner] = 0;
       __threadfence();
     }
     __syncthreads();
-    if (sm.last) join_unit<T, DH, kSimtThreads>(L, s, tid);
+    if (sm.last) join_unit<T, DH, kSimtThreads>(L, s, owner, pieces, tid);
   }
 }
 
@@ -408,7 +479,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
 // alone), 64 keys to a tile, fp32 accumulators in tensor memory.
 //   warp 8   one thread issues the TMA loads of K and V tiles into two rings
 //   warp 9   one thread issues the MMAs
-//   warps 10, 11  copy the next unit's query rows (swizzled, two buffers)
+//   warp 10  copies the next unit's query rows (swizzled, two buffers)
 //   warps 0-3 and 4-7  two softmax groups for the even and the odd tiles of a
 //            segment, a thread to a row: no value crosses threads.  Each
 //            group has its own maximum, sum and accumulator O, so the tiles of
@@ -424,7 +495,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
 // (P <= 2^14 with the 2^6 that keeps small weights out of f16's subnormals):
 // rescaling O is rare.
 
-constexpr int kTcThreads = 384;
+constexpr int kTcThreads = 352;
 constexpr int kTcTmemCols = 512;
 // columns of group w: O at w DH, S at 256 + 64 w, P (two halves of 32) at 384 + 64 w
 constexpr uint32_t kColO = 0, kColS = 256, kColP = 384;
@@ -438,12 +509,6 @@ struct TcSizes {
   static constexpr uint32_t kTileBytes = kKeys * DH * 2;
   static constexpr size_t kSmem = 1024 + 2 * kQBytes + 2 * kStages * kTileBytes;
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // A wait that ends: at its phase, when another wait of the CTA gave up, or at
 // the limit (recorded as DV_ERR_TIMEOUT; the CTA then unwinds, its results
@@ -489,7 +554,22 @@ template <> struct Half2<__nv_bfloat16> {
   }
 };
 
-// Bit i: the row sees key j0 + i.  t: the row's node.
+// Bit i: byte i of a 16-byte vector is not 0.
+__device__ __forceinline__ uint32_t nonzero16(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t top = ((((w[i] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w[i]) >> 7) & 0x01010101u;
+    bits |= ((top * 0x10204080u) >> 28) << (4 * i);
+  }
+  return bits;
+}
+
+// Bit i: the row sees key j0 + i.  t: the row's node.  The mask bytes come in
+// the aligned vectors that cover them, all in flight together (64 byte loads,
+// eight at a time, took 4500 cycles a tile); a vector that would reach outside
+// the mask is read byte by byte.
 __device__ __forceinline__ unsigned long long visible_keys(const TreeLaunch& L, const Seg& s, int j0, int t) {
   const int u0 = j0 - s.pos;                                   // tree slot of the tile's first key
   const int lo = min(max(-u0, 0), kKeys), hi = min(max(s.nodes - u0, 0), kKeys);
@@ -498,11 +578,32 @@ __device__ __forceinline__ unsigned long long visible_keys(const TreeLaunch& L, 
     const int top = min(max(t + 1 - u0, lo), hi);
     return top >= 64 ? ~0ull : (1ull << top) - 1;
   }
-  unsigned long long vis = below;
-  const uint8_t* row = L.mask + s.b * L.mask_stride + (size_t)t * L.T + u0;
-#pragma unroll 8
-  for (int i = lo; i < hi; ++i) vis |= (unsigned long long)(row[i] != 0) << i;
-  return vis;
+  if (hi <= lo) return below;
+  const uint8_t* first = L.mask;
+  const uint8_t* end = first + (L.mask_stride ? L.B * L.mask_stride : (long long)L.T * L.T);
+  const uint8_t* p = first + s.b * L.mask_stride + (long long)t * L.T + u0 + lo;
+  const int n = hi - lo, off = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint8_t* base = p - off;
+  uint4 v[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+    v[k] = make_uint4(0, 0, 0, 0);
+    const uint8_t* at = base + 16 * k;
+    if (16 * k < off + n && at >= first && at + 16 <= end) v[k] = __ldg(reinterpret_cast<const uint4*>(at));
+  }
+  unsigned long long bits = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) bits |= (unsigned long long)nonzero16(v[k]) << (16 * k);
+  bits >>= off;
+  if (off) bits |= (unsigned long long)nonzero16(v[4]) << (64 - off);
+  for (int k = 0; k < 5; ++k) {
+    const uint8_t* at = base + 16 * k;
+    if (16 * k >= off + n || (at >= first && at + 16 <= end)) continue;
+    for (int i = max(16 * k - off, 0); i < min(16 * k + 16 - off, n); ++i)
+      bits |= (unsigned long long)(p[i] != 0) << i;
+  }
+  if (n < 64) bits &= (1ull << n) - 1;
+  return below | (bits << lo);
 }
 
 // The V rows of a tile that not every row may see, in shared memory before the
@@ -544,8 +645,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int NS = Z::kStages, kBoxes = DH / 64;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TreePlan plan;
-  __shared__ uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], qfull[2], qempty[2], sfull[2], pready[2], ofull,
-      odone, done;
+  __shared__ uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], qfull[2], qempty[2], sfull[2], sfree[2], pready[2],
+      pdone[2], ofull, odone, done;
   __shared__ float2 sml[2][2][kTreeRows];   // [segment parity][group][row] maximum and sum
   __shared__ uint32_t tmem_base;
   __shared__ int stop_s, bad_v[4], last;
@@ -566,10 +667,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::mbar_init(&vempty[q], 1);
     }
     for (int q = 0; q < 2; ++q) {
-      tc::mbar_init(&qfull[q], 64);
+      tc::mbar_init(&qfull[q], 32);
       tc::mbar_init(&qempty[q], 1);
       tc::mbar_init(&sfull[q], 1);
+      tc::mbar_init(&sfree[q], 128);
       tc::mbar_init(&pready[q], 128);
+      tc::mbar_init(&pdone[q], 1);
     }
     tc::mbar_init(&ofull, 1);
     tc::mbar_init(&odone, 256);
@@ -578,7 +681,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     stop_s = 0;
     bad_v[0] = bad_v[1] = bad_v[2] = bad_v[3] = 0;
   }
+  if (tid == 256) {
+    tc::prefetch_map(&mapK);
+    tc::prefetch_map(&mapV);
+  }
   if (warp == 9) tc::tmem_alloc(&tmem_base, kTcTmemCols);
+  grid_dep_launch();
+  grid_dep_wait();  // no global memory is touched before
   tc::fence_before_sync();
   tree_plan<kTcThreads>(a, &plan, kTreeRows);  // ends with a barrier
   tc::fence_after_sync();
@@ -621,76 +730,99 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
-    if (lane == 0) {  // MMA issuer
-      constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-      const uint32_t idS = tc::idesc_f16(kTreeRows, kKeys, kBf16, false, false);
-      const uint32_t idO = tc::idesc_f16(kTreeRows, DH, kBf16, false, /*B MN-major*/ true);
-      int base = 0, sg = 0;
-      uint32_t pcount[2] = {0, 0};
-      while (!*stop && cur.next(L, plan, kTreeRows, &s)) {
-        if (!s.ok) continue;
-        const int nt = s.k1 - s.k0;
-        const uint32_t qb = tc::saddr(sQ + (sg & 1) * Z::kQBytes);
-        wait_bar(&qfull[sg & 1], (sg >> 1) & 1, stop, a, 33);
-        auto issue_s = [&](int j) {
-          const int it = base + j, st = it % NS;
-          wait_bar(&kfull[st], (it / NS) & 1, stop, a, 34);
-          if (*stop) return;
-          tc::fence_after_sync();
-          const uint32_t kb = tc::saddr(sK + st * Z::kTileBytes);
+  } else if (warp == 9) {  // MMA issuer
+    // The whole warp walks the loop and one lane issues, so that counters and
+    // descriptors are warp-uniform: issued from inside a one-lane branch, the
+    // 16 MMAs of a tile took 1200 cycles to issue and bounded the kernel.
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    const uint32_t idS = tc::idesc_f16(kTreeRows, kKeys, kBf16, false, false);
+    const uint32_t idO = tc::idesc_f16(kTreeRows, DH, kBf16, false, /*B MN-major*/ true);
+    const uint64_t qd0 = tc::smem_desc(tc::saddr(sQ), 16, 1024, 2), kd0 = tc::smem_desc(tc::saddr(sK), 16, 1024, 2);
+    // V (MN-major): 16 keys = two 8-row groups (1024 B apart), the 64-column
+    // halves kKeys * 128 bytes apart
+    const uint64_t vd0 = tc::smem_desc(tc::saddr(sV), kKeys * 128, 1024, 2);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    uint32_t ks = 0, kph = 0, vs = 0, vph = 0;   // ring stages and their phases
+    uint32_t s_used = 0, s_ph = 0, p_ph = 0;     // bit w: group w
+    int sg = 0;
+    while (cur.next(L, plan, kTreeRows, &s)) {
+      if (!s.ok) continue;
+      const int nt = __shfl_sync(0xffffffffu, s.k1 - s.k0, 0);
+      bool ok = wait_bar(&qfull[sg & 1], (sg >> 1) & 1, stop, a, 33);
+      const uint64_t qd = qd0 + (sg & 1) * (Z::kQBytes >> 4);
+      auto issue_s = [&](uint32_t w) {
+        if ((s_used >> w) & 1) {
+          ok &= wait_bar(&sfree[w], (s_ph >> w) & 1, stop, a, 43);
+          s_ph ^= 1u << w;
+        }
+        s_used |= 1u << w;
+        ok &= wait_bar(&kfull[ks], kph, stop, a, 34);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+          const uint64_t kd = kd0 + ks * (Z::kTileBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk) {
-            const uint64_t ad = tc::smem_desc(qb + (kk >> 2) * (kTreeRows * 128) + (kk & 3) * 32, 16, 1024, 2);
-            const uint64_t bd = tc::smem_desc(kb + (kk >> 2) * (kKeys * 128) + (kk & 3) * 32, 16, 1024, 2);
-            tc::mma_f16(tmem + kColS + (j & 1) * kKeys, ad, bd, idS, kk != 0);
-          }
-          tc::mma_commit(&sfull[j & 1]);
-          tc::mma_commit(&kempty[st]);
-        };
-        if (!*stop) issue_s(0);
-        if (nt > 1 && !*stop) issue_s(1);
-        // O is read to the end of the previous segment before it is begun anew
-        if (sg > 0) wait_bar(&odone, (sg - 1) & 1, stop, a, 35);
-        for (int j = 0; j < nt && !*stop; ++j) {
-          const int it = base + j, st = it % NS, w = j & 1;
-          wait_bar(&pready[w], pcount[w] & 1, stop, a, 36);
-          ++pcount[w];
-          wait_bar(&vfull[st], (it / NS) & 1, stop, a, 37);
-          if (*stop) break;
-          tc::fence_after_sync();
-          const uint32_t vb = tc::saddr(sV + st * Z::kTileBytes);
-          const uint32_t p = tmem + kColP + w * kKeys, o = tmem + kColO + w * DH;
+          for (int kk = 0; kk < DH / 16; ++kk)
+            tc::mma_f16(tm + kColS + w * kKeys, qd + ((kk >> 2) * (kTreeRows * 128) + (kk & 3) * 32) / 16,
+                        kd + ((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) / 16, idS, kk != 0);
+          tc::mma_commit(&sfull[w]);
+          tc::mma_commit(&kempty[ks]);
+        }
+        __syncwarp();
+        if (++ks == NS) { ks = 0; kph ^= 1; }
+      };
+      if (ok) issue_s(0);
+      if (nt > 1 && ok) issue_s(1);
+      // O is read to the end of the previous segment before it is begun anew
+      if (sg > 0) ok &= wait_bar(&odone, (sg - 1) & 1, stop, a, 35);
+      for (int j = 0; j < nt && ok; ++j) {
+        const uint32_t w = j & 1;
+        // S of the group's next tile while it works on this one
+        if (j + 2 < nt) issue_s(w);
+        ok &= wait_bar(&pready[w], (p_ph >> w) & 1, stop, a, 36);
+        p_ph ^= 1u << w;
+        ok &= wait_bar(&vfull[vs], vph, stop, a, 37);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+          const uint64_t vd = vd0 + vs * (Z::kTileBytes >> 4);
+          const uint32_t p = tm + kColP + w * kKeys, o = tm + kColO + w * DH;
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk) {
-            // V (MN-major): 16 keys = two 8-row groups (1024 B apart), the
-            // 64-column halves kKeys * 128 bytes apart
-            const uint64_t bd = tc::smem_desc(vb + kk * 2048, kKeys * 128, 1024, 2);
-            tc::mma_f16_ts(o, p + kk * 8, bd, idO, j >= 2 || kk != 0);
-            tc::mma_f16_ts(o, p + 32 + kk * 8, bd, idO, 1);
+            tc::mma_f16_ts(o, p + kk * 8, vd + kk * (2048 / 16), idO, j >= 2 || kk != 0);
+            tc::mma_f16_ts(o, p + 32 + kk * 8, vd + kk * (2048 / 16), idO, 1);
           }
-          tc::mma_commit(&vempty[st]);
-          if (j + 2 < nt) issue_s(j + 2);
+          tc::mma_commit(&vempty[vs]);
+          tc::mma_commit(&pdone[w]);
         }
+        __syncwarp();
+        if (++vs == NS) { vs = 0; vph ^= 1; }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (tc::elect_one()) {
         tc::mma_commit(&qempty[sg & 1]);
         tc::mma_commit(&ofull);
-        base += nt;
-        ++sg;
       }
+      __syncwarp();
+      if (!ok) break;
+      ++sg;
+    }
+    if (tc::elect_one()) {
       tc::mma_commit(&done);  // arrives once every MMA issued above has completed
       if (!tc::mbar_wait(&done, 0, unwind_ns)) set_error(a.hdr, DV_ERR_TIMEOUT, 38);
     }
     __syncwarp();
-  } else if (warp >= 10) {  // query rows, then the rows of out that no unit writes
+  } else if (warp == 10) {  // query rows, then the rows of out that no unit writes
     constexpr int kRowChunks = DH / 8;
-    const int qt = tid - 320;
     int sg = 0;
     while (!*stop && cur.next(L, plan, kTreeRows, &s)) {
       if (!s.ok) continue;
       if (sg >= 2) wait_bar(&qempty[sg & 1], ((sg >> 1) - 1) & 1, stop, a, 39);
       uint8_t* dst = sQ + (sg & 1) * Z::kQBytes;
       if (!*stop) {
-        for (int i = qt; i < s.rows * kRowChunks; i += 64) {
+        for (int i = lane; i < s.rows * kRowChunks; i += 32) {
           const int r = i / kRowChunks, c = i % kRowChunks;
           cp_async16(dst + (c >> 3) * (kTreeRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                      static_cast<const T*>(L.q) + row_offset(L, s, r, DH) + c * 8);
@@ -703,13 +835,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ++sg;
     }
     __syncwarp();
-    zero_rows<T, DH>(L, plan, blockIdx.x * 2 + (warp - 10), gridDim.x * 2, lane, 32);
+    zero_rows<T, DH>(L, plan, blockIdx.x, gridDim.x, lane, 32);
   } else {  // softmax groups
     const int w = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t tS = lanes + kColS + w * kKeys, tP = lanes + kColP + w * kKeys, tO = lanes + kColO + w * DH;
     int base = 0, sg = 0;
     uint32_t scount = 0;
+    bool done_p = false;
     while (cur.next(L, plan, kTreeRows, &s)) {
       if (!s.ok) {
         if (tid == 0) set_error(a.hdr, DV_ERR_INDEX_RANGE, s.head);
@@ -722,15 +855,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int j = w; j < nt; j += 2) {
         const int j0 = (s.k0 + j) * kKeys;
         const bool edge = j0 + kKeys > s.pos;   // the tile holds tree nodes, or ends behind the last
-        bool there = true;
+        u64 vis = ~0ull;
+        if (edge && active) vis = visible_keys(L, s, j0, t);
+        bool there = wait_bar(&sfull[w], scount & 1, stop, a, 41);
+        ++scount;
         if (edge) {
+          // S of this tile was issued behind the product that freed this stage
+          // for its V (NS tiles back), so the stage's barrier is at this tile's
+          // phase by now, for warps without rows too
           const int it = base + j, st = it % NS;
-          there = wait_bar(&vfull[st], (it / NS) & 1, stop, a, 40);
+          there &= wait_bar(&vfull[st], (it / NS) & 1, stop, a, 40);
           if (clean_v<T, DH>(sV + st * Z::kTileBytes, s, j0, tid & 127)) bad_v[sg & 3] = 1;
           tc::fence_proxy_async();
         }
-        there &= wait_bar(&sfull[w], scount & 1, stop, a, 41);
-        ++scount;
         if (!__all_sync(0xffffffffu, there)) break;  // the whole warp, or none of it
         tc::fence_after_sync();
         if (active) {
@@ -738,6 +875,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc::tmem_ld32(tS, v);
           tc::tmem_ld32(tS + 32, v + 32);
           tc::tmem_ld_wait();
+          tc::fence_before_sync();
+          tc::mbar_arrive(&sfree[w]);
           float c = a.scale_log2;
           if (c <= 0.f) {  // the maximum is taken before the scale
 #pragma unroll
@@ -745,14 +884,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             c = 1.f;
           }
           if (edge) {
-            const unsigned long long vis = visible_keys(L, s, j0, t);
 #pragma unroll
             for (int i = 0; i < kKeys; ++i) v[i] = (vis >> i) & 1 ? v[i] : -INFINITY;
           }
-          float mx[4] = {v[0], v[1], v[2], v[3]};
+          float mx[2] = {fmaxf(v[0], v[1]), fmaxf(v[2], v[3])};
 #pragma unroll
-          for (int i = 4; i < kKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          for (int i = 4; i < kKeys; i += 4) {
+            mx[0] = max3(mx[0], v[i], v[i + 1]);
+            mx[1] = max3(mx[1], v[i + 2], v[i + 3]);
+          }
+          const float top = fmaxf(mx[0], mx[1]) * c;
+          // P and O of the group's tile before are read and written
+          if (done_p) there &= wait_bar(&pdone[w], (scount - 2) & 1, stop, a, 44);
+          __syncwarp();
+          tc::fence_after_sync();
           const bool move = row < s.rows && top > m + kSlack;
           if (__any_sync(0xffffffffu, move)) {
             // a row whose maximum was -inf has sums of 0: nothing to rescale
@@ -773,22 +918,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           const float off = kShift - (m == -INFINITY ? 0.f : m);
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t hi[kKeys / 2], lo[kKeys / 2];
+          u64 sum[2] = {0, 0};
+          const u64 c2 = pack2(c, c), off2 = pack2(off, off), minus = pack2(-1.f, -1.f);
 #pragma unroll
-          for (int i = 0; i < kKeys; i += 2) {
-            const float p0 = ex2(fmaf(v[i], c, off)), p1 = ex2(fmaf(v[i + 1], c, off));
-            sum[i & 3] += p0;
-            sum[(i + 1) & 3] += p1;
-            hi[i / 2] = Half2<T>::pack(p0, p1);
-            const float2 h = Half2<T>::open(hi[i / 2]);
-            lo[i / 2] = Half2<T>::pack(p0 - h.x, p1 - h.y);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t hi[kKeys / 4], lo[kKeys / 4];
+#pragma unroll
+            for (int i = 0; i < kKeys / 2; i += 2) {
+              float p0, p1;
+              open2(fma2(pack2(v[half * 32 + i], v[half * 32 + i + 1]), c2, off2), &p0, &p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              const u64 p = pack2(p0, p1);
+              sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], p);
+              hi[i / 2] = Half2<T>::pack(p0, p1);
+              const float2 h = Half2<T>::open(hi[i / 2]);
+              float l0, l1;
+              open2(fma2(pack2(h.x, h.y), minus, p), &l0, &l1);
+              lo[i / 2] = Half2<T>::pack(l0, l1);
+            }
+            tc::tmem_st16(tP + half * 16, hi);
+            tc::tmem_st16(tP + 32 + half * 16, lo);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tc::tmem_st32(tP, hi);
-          tc::tmem_st32(tP + 32, lo);
+          float s0, s1;
+          open2(add2(sum[0], sum[1]), &s0, &s1);
+          l += s0 + s1;
           tc::tmem_st_wait();
+        } else {
+          // a warp without rows keeps step: it must not arrive for the next
+          // tile while the others are still at this one
+          tc::mbar_arrive(&sfree[w]);
+          if (done_p) wait_bar(&pdone[w], (scount - 2) & 1, stop, a, 44);
         }
+        done_p = true;
         tc::fence_before_sync();
         tc::mbar_arrive(&pready[w]);
       }
@@ -805,7 +967,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float wA = A.x == -INFINITY ? 0.f : ex2(A.x - M), wB = Bv.x == -INFINITY ? 0.f : ex2(Bv.x - M);
       const float sum = fmaf(A.y, wA, Bv.y * wB);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a row that sees nothing is zero
-      const bool whole = s.pieces == 1;
+      int owner, pieces;
+      cur.pieces(s, &owner, &pieces);
+      const bool whole = pieces == 1;
       const size_t slot = piece_slot(blockIdx.x, s.k0 == 0);
 #pragma unroll 1
       for (int cc = w * (DH / 2); cc < (w + 1) * (DH / 2); cc += 32) {
@@ -859,15 +1023,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::fence_before_sync();
       tc::mbar_arrive(&odone);
       if (!whole) {
-        __threadfence();
         group_sync<256>();
         if (tid == 0) {
-          last = atomicAdd(&L.ctr[s.owner], 1) == s.pieces - 1;
-          if (last) L.ctr[s.owner] = 0;
+          __threadfence();  // (the barrier before it makes it cover the CTA's stores)
+          last = atomicAdd(&L.ctr[owner], 1) == pieces - 1;
+          if (last) L.ctr[owner] = 0;
           __threadfence();
         }
         group_sync<256>();
-        if (last) join_unit<T, DH, 256>(L, s, tid);
+        if (last) join_unit<T, DH, 256>(L, s, owner, pieces, tid);
       }
       base += nt;
       ++sg;
@@ -895,7 +1059,7 @@ cudaError_t run_tc(const TreeArgs& a, int num_sms, cudaStream_t stream) {
     return (int)cudaFuncSetAttribute(tree_tc_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (ea != cudaSuccess) return ea;
-  return launch_k(tree_tc_kernel<T, DH>, dim3(min(num_sms, kTreeCtas)), dim3(kTcThreads), smem, stream, false, 1, mK,
+  return launch_k(tree_tc_kernel<T, DH>, dim3(min(num_sms, kTreeCtas)), dim3(kTcThreads), smem, stream, true, 1, mK,
                   mV, a);
 }
 
@@ -907,7 +1071,7 @@ cudaError_t run_simt(const TreeArgs& a, int num_sms, cudaStream_t stream) {
     return (int)cudaFuncSetAttribute(tree_simt_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (ea != cudaSuccess) return ea;
-  return launch_k(tree_simt_kernel<T, DH>, dim3(min(num_sms, kTreeCtas)), dim3(kSimtThreads), smem, stream, false, 1, a);
+  return launch_k(tree_simt_kernel<T, DH>, dim3(min(num_sms, kTreeCtas)), dim3(kSimtThreads), smem, stream, true, 1, a);
 }
 
 }  // namespace
