@@ -296,7 +296,6 @@ struct TreeLaunch {
   // scratch: partial results of units that several CTAs share
   float* part;      // [2 kTreeCtas][d_h / 4][rows_pad][4]
   float2* ml;       // [2 kTreeCtas][rows_pad] running maximum and sum
-  int* ctr;         // [kTreeCtas], zero between calls
   int rows_pad;     // min(kTreeRows, T g)
 };
 cudaError_t launch_tree_attn(const TreeLaunch& a, dv_dtype dt, WsHeader* hdr, int num_sms, cudaStream_t stream);

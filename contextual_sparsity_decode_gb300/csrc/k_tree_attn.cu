@@ -12,8 +12,9 @@
 // into tiles of 64 keys.  The grid is persistent, and every CTA takes an equal
 // share of all units' tiles, in order, whatever the sequences' lengths (read on
 // the device); a unit that crosses CTAs leaves a partial result (maximum, sum,
-// numerator) per CTA, and the last CTA to finish joins them in tile order, so
-// results do not depend on timing.
+// numerator) per CTA, and a second kernel, resident while the first runs, joins
+// them in tile order, so results do not depend on timing.  (Joined by the last
+// of its CTAs to finish, a unit of 125 rows over six CTAs took that CTA 30 us.)
 
 #include <cuda.h>
 
@@ -53,7 +54,7 @@ struct Seg {
 // One block-wide pass over the sequences: checks, lengths and the prefix sums
 // of their tiles.  NT threads; ends with a barrier.
 template <int NT>
-__device__ void tree_plan(const TreeArgs& a, TreePlan* p, int rows_per_unit) {
+__device__ void tree_plan(const TreeArgs& a, TreePlan* p, int rows_per_unit, bool report) {
   __shared__ long long warp_tot[NT / 32];
   const TreeLaunch& L = a.L;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -65,7 +66,6 @@ __device__ void tree_plan(const TreeArgs& a, TreePlan* p, int rows_per_unit) {
       const int n = L.pos[b];
       int nd = L.nodes ? L.nodes[b] : L.T;
       int cnt = L.head_idx ? L.head_count[b] : L.h;
-      const bool report = blockIdx.x == 0;
       if (nd > L.T) {
         if (report) set_error(a.hdr, DV_ERR_CAPACITY, nd);
         nd = L.T;
@@ -116,10 +116,9 @@ struct Cursor {
   long long t, t1;   // next tile, end of the share
   long long q, r;    // W / G, W % G
   int b;
-  __device__ Cursor(const TreePlan& p, int B) {
+  __device__ Cursor(const TreePlan& p, int B, int c, int ctas) {
     const long long W = p.pre[B];
-    const long long G = W < (long long)gridDim.x ? W : (long long)gridDim.x;
-    const int c = blockIdx.x;
+    const long long G = W < (long long)ctas ? W : (long long)ctas;
     if (c >= G) {
       t = t1 = q = r = 0;
       b = 0;
@@ -168,18 +167,6 @@ struct Cursor {
     t += s->k1 - s->k0;
     return true;
   }
-  // The CTAs that share the unit of the segment that next() gave last: the
-  // first and their number.
-  __device__ void pieces(const Seg& s, int* owner, int* count) const {
-    if (s.k0 == 0 && s.k1 == s.tiles) {
-      *owner = blockIdx.x;
-      *count = 1;
-      return;
-    }
-    const long long u0 = t - s.k1;
-    *owner = s.k0 == 0 ? (int)blockIdx.x : cta_of(u0);
-    *count = (s.k1 == s.tiles ? (int)blockIdx.x : cta_of(u0 + s.tiles - 1)) - *owner + 1;
-  }
 };
 
 // Query row r of unit (b, head): its offset in q and out.
@@ -214,64 +201,6 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* dst, float 
   const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
   *reinterpret_cast<uint2*>(dst) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-}
-
-// Joins the partial results of a unit, in tile order, and writes its rows.
-// Called by NT threads of the CTA that finished last: a thread to a row and two
-// groups of four columns at a time, four pieces' loads in flight together.
-template <typename T, int DH, int NT>
-__device__ void join_unit(const TreeLaunch& L, const Seg& s, int owner, int pieces, int tid) {
-  constexpr int kP = 2, kC = 2;
-  const int groups = NT / s.rows, grp = tid / s.rows, r = tid - grp * s.rows;
-  if (grp >= groups) return;
-  T* dst = static_cast<T*>(L.out) + row_offset(L, s, r, DH);
-  for (int c0 = grp; c0 < DH / 4; c0 += kC * groups) {
-    float M = -INFINITY, l = 0.f;
-    float4 o[kC];
-#pragma unroll
-    for (int c = 0; c < kC; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int q0 = 0; q0 < pieces; q0 += kP) {
-      float2 ml[kP];
-      float4 x[kP][kC];
-#pragma unroll
-      for (int q = 0; q < kP; ++q) {
-        ml[q] = make_float2(-INFINITY, 0.f);
-        if (q0 + q >= pieces) continue;
-        const size_t slot = piece_slot(owner + q0 + q, q0 + q == 0);
-        ml[q] = __ldcg(&L.ml[slot * L.rows_pad + r]);
-#pragma unroll
-        for (int c = 0; c < kC; ++c)
-          if (c0 + c * groups < DH / 4)
-            x[q][c] = __ldcg(reinterpret_cast<const float4*>(L.part) + (slot * (DH / 4) + c0 + c * groups) * L.rows_pad + r);
-      }
-      float m = M;
-#pragma unroll
-      for (int q = 0; q < kP; ++q) m = fmaxf(m, ml[q].x);
-      const float keep = M == -INFINITY ? 0.f : ex2(M - m);
-      M = m;
-      l *= keep;
-#pragma unroll
-      for (int c = 0; c < kC; ++c) { o[c].x *= keep; o[c].y *= keep; o[c].z *= keep; o[c].w *= keep; }
-#pragma unroll
-      for (int q = 0; q < kP; ++q) {
-        if (q0 + q >= pieces) continue;
-        // (a piece whose maximum is -inf has sums of 0, or a NaN)
-        const float w = ml[q].x == -INFINITY ? (ml[q].y == 0.f ? 0.f : 1.f) : ex2(ml[q].x - m);
-        l = fmaf(ml[q].y, w, l);
-#pragma unroll
-        for (int c = 0; c < kC; ++c) {
-          if (c0 + c * groups >= DH / 4) continue;
-          o[c].x = fmaf(x[q][c].x, w, o[c].x); o[c].y = fmaf(x[q][c].y, w, o[c].y);
-          o[c].z = fmaf(x[q][c].z, w, o[c].z); o[c].w = fmaf(x[q][c].w, w, o[c].w);
-        }
-      }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing is zero
-#pragma unroll
-    for (int c = 0; c < kC; ++c)
-      if (c0 + c * groups < DH / 4)
-        store4<T>(dst + 4 * (c0 + c * groups), o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv);
-  }
 }
 
 // Rows that no unit writes are zero: heads outside the list, nodes behind the
@@ -318,7 +247,6 @@ struct SimtSmem {
   float s[kSimtRows][kKeys + 1];   // scores, then p; -1 marks a masked key
   float alpha[kSimtRows];
   float m[kSimtRows], l[kSimtRows];
-  int last;
 };
 
 template <typename T, int DH>
@@ -329,11 +257,11 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   constexpr int kVec = Elem<T>::kVec, kChunks = DH / kVec;
   constexpr int kCols = DH / 16;   // output columns of a thread
-  grid_dep_launch();
   grid_dep_wait();
-  tree_plan<kSimtThreads>(a, &sm.plan, kSimtRows);
+  grid_dep_launch();  // after the wait: the join may read the lengths at once
+  tree_plan<kSimtThreads>(a, &sm.plan, kSimtRows, blockIdx.x == 0);
   zero_rows<T, DH>(L, sm.plan, blockIdx.x * (kSimtThreads / 32) + wid, gridDim.x * (kSimtThreads / 32), lane, 32);
-  Cursor cur(sm.plan, L.B);
+  Cursor cur(sm.plan, L.B, blockIdx.x, gridDim.x);
   Seg s;
   while (cur.next(L, sm.plan, kSimtRows, &s)) {
     if (!s.ok) {
@@ -440,9 +368,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
       }
     }
     const int r = tid / 16, c0 = (tid % 16) * 4;
-    int owner, pieces;
-    cur.pieces(s, &owner, &pieces);
-    if (pieces == 1) {
+    if (s.k1 - s.k0 == s.tiles) {
       if (r < s.rows) {
         const float l = sm.l[r], inv = l == 0.f ? 0.f : 1.f / l;
         T* dst = static_cast<T*>(L.out) + row_offset(L, s, r, DH) + c0;
@@ -460,15 +386,6 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
         __stcg(dst + (size_t)((c0 + c * 16) / 4) * L.rows_pad, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
       if (c0 == 0) __stcg(&L.ml[slot * L.rows_pad + r], make_float2(sm.m[r], sm.l[r]));
     }
-    __syncthreads();
-    if (tid == 0) {
-      __threadfence();  // (the barrier before it makes it cover the CTA's stores)
-      sm.last = atomicAdd(&L.ctr[owner], 1) == pieces - 1;
-      if (sm.last) L.ctr[owner] = 0;
-      __threadfence();
-    }
-    __syncthreads();
-    if (sm.last) join_unit<T, DH, kSimtThreads>(L, s, owner, pieces, tid);
   }
 }
 
@@ -649,7 +566,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       pdone[2], ofull, odone, done;
   __shared__ float2 sml[2][2][kTreeRows];   // [segment parity][group][row] maximum and sum
   __shared__ uint32_t tmem_base;
-  __shared__ int stop_s, bad_v[4], last;
+  __shared__ int stop_s, bad_v[4];
   const TreeLaunch& L = a.L;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -686,13 +603,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc::prefetch_map(&mapV);
   }
   if (warp == 9) tc::tmem_alloc(&tmem_base, kTcTmemCols);
-  grid_dep_launch();
-  grid_dep_wait();  // no global memory is touched before
+  grid_dep_wait();    // no global memory is touched before
+  grid_dep_launch();  // after the wait: the join may read the lengths at once
   tc::fence_before_sync();
-  tree_plan<kTcThreads>(a, &plan, kTreeRows);  // ends with a barrier
+  tree_plan<kTcThreads>(a, &plan, kTreeRows, blockIdx.x == 0);  // ends with a barrier
   tc::fence_after_sync();
   const uint32_t tmem = tmem_base;
-  Cursor cur(plan, L.B);
+  Cursor cur(plan, L.B, blockIdx.x, gridDim.x);
   Seg s;
 
   if (warp == 8) {
@@ -852,22 +769,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool active = quad * 32 < s.rows;
       const int t = min(s.row0 + row, s.row0 + s.rows - 1) / L.g;
       float m = -INFINITY, l = 0.f;
-      for (int j = w; j < nt; j += 2) {
+      // What an edge tile (one that holds tree nodes, or ends behind the last)
+      // needs besides its scores, made ready while the tile before it is in the
+      // products: the keys that the row sees, and clean V rows.  The V stage's
+      // barrier is at this tile's phase or the one before: the product that
+      // freed the stage was waited for.
+      bool there = true;
+      const auto prepare = [&](int j) -> u64 {
         const int j0 = (s.k0 + j) * kKeys;
-        const bool edge = j0 + kKeys > s.pos;   // the tile holds tree nodes, or ends behind the last
-        u64 vis = ~0ull;
-        if (edge && active) vis = visible_keys(L, s, j0, t);
-        bool there = wait_bar(&sfull[w], scount & 1, stop, a, 41);
+        if (j >= nt || j0 + kKeys <= s.pos) return ~0ull;
+        const u64 seen = active ? visible_keys(L, s, j0, t) : ~0ull;
+        const int it = base + j, st = it % NS;
+        there &= wait_bar(&vfull[st], (it / NS) & 1, stop, a, 40);
+        if (clean_v<T, DH>(sV + st * Z::kTileBytes, s, j0, tid & 127)) bad_v[sg & 3] = 1;
+        tc::fence_proxy_async();
+        return seen;
+      };
+      u64 vis = prepare(w);
+      for (int j = w; j < nt; j += 2) {
+        there &= wait_bar(&sfull[w], scount & 1, stop, a, 41);
         ++scount;
-        if (edge) {
-          // S of this tile was issued behind the product that freed this stage
-          // for its V (NS tiles back), so the stage's barrier is at this tile's
-          // phase by now, for warps without rows too
-          const int it = base + j, st = it % NS;
-          there &= wait_bar(&vfull[st], (it / NS) & 1, stop, a, 40);
-          if (clean_v<T, DH>(sV + st * Z::kTileBytes, s, j0, tid & 127)) bad_v[sg & 3] = 1;
-          tc::fence_proxy_async();
-        }
         if (!__all_sync(0xffffffffu, there)) break;  // the whole warp, or none of it
         tc::fence_after_sync();
         if (active) {
@@ -883,7 +804,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int i = 0; i < kKeys; ++i) v[i] *= c;
             c = 1.f;
           }
-          if (edge) {
+          if (__any_sync(0xffffffffu, vis != ~0ull)) {
 #pragma unroll
             for (int i = 0; i < kKeys; ++i) v[i] = (vis >> i) & 1 ? v[i] : -INFINITY;
           }
@@ -953,6 +874,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         done_p = true;
         tc::fence_before_sync();
         tc::mbar_arrive(&pready[w]);
+        vis = prepare(j + 2);
       }
       // the segment's end: both groups' results joined, a group to each half of the columns
       sml[sg & 1][w][row] = make_float2(m, l);
@@ -967,9 +889,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float wA = A.x == -INFINITY ? 0.f : ex2(A.x - M), wB = Bv.x == -INFINITY ? 0.f : ex2(Bv.x - M);
       const float sum = fmaf(A.y, wA, Bv.y * wB);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a row that sees nothing is zero
-      int owner, pieces;
-      cur.pieces(s, &owner, &pieces);
-      const bool whole = pieces == 1;
+      const bool whole = nt == s.tiles;
       const size_t slot = piece_slot(blockIdx.x, s.k0 == 0);
 #pragma unroll 1
       for (int cc = w * (DH / 2); cc < (w + 1) * (DH / 2); cc += 32) {
@@ -1022,17 +942,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       tc::fence_before_sync();
       tc::mbar_arrive(&odone);
-      if (!whole) {
-        group_sync<256>();
-        if (tid == 0) {
-          __threadfence();  // (the barrier before it makes it cover the CTA's stores)
-          last = atomicAdd(&L.ctr[owner], 1) == pieces - 1;
-          if (last) L.ctr[owner] = 0;
-          __threadfence();
-        }
-        group_sync<256>();
-        if (last) join_unit<T, DH, 256>(L, s, owner, pieces, tid);
-      }
       base += nt;
       ++sg;
     }
@@ -1043,7 +952,76 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 9) tc::tmem_dealloc(tmem, kTcTmemCols);
 }
 
+// ---- join ---------------------------------------------------------------------
+//
+// Block (c, part): the unit in which CTA c's share begins, if that is inside
+// the unit and no earlier share begins there; part of its rows.
+
+constexpr int kJoinThreads = 256, kJoinParts = 4;
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas,
+                                                                int rows_per_unit) {
+  __shared__ TreePlan plan;
+  const TreeLaunch& L = a.L;
+  const int tid = threadIdx.x, c = blockIdx.x + 1;
+  grid_dep_launch();
+  tree_plan<kJoinThreads>(a, &plan, rows_per_unit, false);
+  Cursor cur(plan, L.B, c, ctas);
+  Seg s{};
+  const bool some = cur.next(L, plan, rows_per_unit, &s);
+  const long long u0 = cur.t - s.k1;   // the unit's first tile
+  // the share before this one has to hold that tile
+  const bool mine = some && s.ok && s.k0 > 0 && cur.cta_of(u0) == c - 1;
+  const int owner = c - 1, pieces = mine ? cur.cta_of(u0 + s.tiles - 1) - owner + 1 : 0;
+  const int per = (s.rows + kJoinParts - 1) / kJoinParts, r0 = blockIdx.y * per, n = min(per, s.rows - r0);
+  grid_dep_wait();
+  if (!mine || n <= 0) return;
+  // a thread to a row and four columns; four pieces' loads in flight together
+  constexpr int kP = 4;
+  for (int i = tid; i < n * (DH / 4); i += kJoinThreads) {
+    const int r = r0 + i % n, c4 = i / n;
+    float M = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
+    for (int q0 = 0; q0 < pieces; q0 += kP) {
+      float2 ml[kP];
+      float4 x[kP];
+#pragma unroll
+      for (int q = 0; q < kP; ++q) {
+        ml[q] = make_float2(-INFINITY, 0.f);
+        x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q0 + q < pieces) {
+          const size_t slot = piece_slot(owner + q0 + q, q0 + q == 0);
+          ml[q] = __ldcg(&L.ml[slot * L.rows_pad + r]);
+          x[q] = __ldcg(reinterpret_cast<const float4*>(L.part) + (slot * (DH / 4) + c4) * L.rows_pad + r);
+        }
+      }
+      float m = M;
+#pragma unroll
+      for (int q = 0; q < kP; ++q) m = fmaxf(m, ml[q].x);
+      const float keep = M == -INFINITY ? 1.f : ex2(M - m);   // (sums of 0, or a NaN, where M is -inf)
+      M = m;
+      l *= keep; o0 *= keep; o1 *= keep; o2 *= keep; o3 *= keep;
+#pragma unroll
+      for (int q = 0; q < kP; ++q) {
+        const float w = ml[q].x == -INFINITY ? 1.f : ex2(ml[q].x - m);
+        l = fmaf(ml[q].y, w, l);
+        o0 = fmaf(x[q].x, w, o0); o1 = fmaf(x[q].y, w, o1);
+        o2 = fmaf(x[q].z, w, o2); o3 = fmaf(x[q].w, w, o3);
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing is zero
+    store4<T>(static_cast<T*>(L.out) + row_offset(L, s, r, DH) + 4 * c4, o0 * inv, o1 * inv, o2 * inv, o3 * inv);
+  }
+}
+
 // ---- host ------------------------------------------------------------------------
+
+template <typename T, int DH>
+cudaError_t run_join(const TreeArgs& a, int ctas, int rows_per_unit, cudaStream_t stream) {
+  if (ctas < 2) return cudaSuccess;
+  return launch_k(tree_join_kernel<T, DH>, dim3(ctas - 1, kJoinParts), dim3(kJoinThreads), 0, stream, true, 1, a, ctas,
+                  rows_per_unit);
+}
 
 template <typename T, int DH>
 cudaError_t run_tc(const TreeArgs& a, int num_sms, cudaStream_t stream) {
@@ -1059,8 +1037,9 @@ cudaError_t run_tc(const TreeArgs& a, int num_sms, cudaStream_t stream) {
     return (int)cudaFuncSetAttribute(tree_tc_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (ea != cudaSuccess) return ea;
-  return launch_k(tree_tc_kernel<T, DH>, dim3(min(num_sms, kTreeCtas)), dim3(kTcThreads), smem, stream, true, 1, mK,
-                  mV, a);
+  const int ctas = min(num_sms, kTreeCtas);
+  const cudaError_t e = launch_k(tree_tc_kernel<T, DH>, dim3(ctas), dim3(kTcThreads), smem, stream, true, 1, mK, mV, a);
+  return e == cudaSuccess ? run_join<T, DH>(a, ctas, kTreeRows, stream) : e;
 }
 
 template <typename T, int DH>
@@ -1071,7 +1050,9 @@ cudaError_t run_simt(const TreeArgs& a, int num_sms, cudaStream_t stream) {
     return (int)cudaFuncSetAttribute(tree_simt_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (ea != cudaSuccess) return ea;
-  return launch_k(tree_simt_kernel<T, DH>, dim3(min(num_sms, kTreeCtas)), dim3(kSimtThreads), smem, stream, true, 1, a);
+  const int ctas = min(num_sms, kTreeCtas);
+  const cudaError_t e = launch_k(tree_simt_kernel<T, DH>, dim3(ctas), dim3(kSimtThreads), smem, stream, true, 1, a);
+  return e == cudaSuccess ? run_join<T, DH>(a, ctas, kSimtRows, stream) : e;
 }
 
 }  // namespace
