@@ -393,15 +393,18 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
 //
 // S = Q K^T and O += P V on tcgen05: M = 128 query rows (rows behind the unit's
 // last hold anything: a row of the product depends on its own row of Q and P
-// alone), 64 keys to a tile, fp32 accumulators in tensor memory.
-//   warp 8   one thread issues the TMA loads of K and V tiles into two rings
-//   warp 9   one thread issues the MMAs
+// alone), fp32 accumulators in tensor memory.  Tiles go in pairs: one S of 128
+// keys (half as many reads of Q from shared memory as two of 64, and those
+// bound the product at N = 64), then one softmax group and one P V for each
+// tile of the pair.
+//   warp 8   one thread issues the TMA loads: K by pairs, V by tiles, two rings
+//   warp 9   issues the MMAs
 //   warp 10  copies the next unit's query rows (swizzled, two buffers)
-//   warps 0-3 and 4-7  two softmax groups for the even and the odd tiles of a
-//            segment, a thread to a row: no value crosses threads.  Each
-//            group has its own maximum, sum and accumulator O, so the tiles of
-//            one overlap the other's products; they are joined at the end of
-//            the segment.
+//   warps 0-3 and 4-7  the two softmax groups, a thread to a row: no value
+//            crosses threads.  Each group has its own maximum, sum and
+//            accumulator O; they are joined at the end of the segment.  S is
+//            read into registers at once, so that the next pair's S is
+//            computed while the groups work on this one's.
 // P goes back to tensor memory (the A operand of the second product) as the
 // sum of two 16-bit halves hi + lo: one rounding of P to bf16 would put as
 // large an error into O as the output's own rounding; the two halves leave
@@ -421,10 +424,10 @@ constexpr long long kUnwindNs = 2000000000LL;
 
 template <int DH>
 struct TcSizes {
-  static constexpr int kStages = DH == 128 ? 4 : 6;
+  static constexpr int kPairs = DH == 128 ? 2 : 4, kTiles = DH == 128 ? 5 : 8;   // ring depths: K pairs, V tiles
   static constexpr uint32_t kQBytes = kTreeRows * DH * 2;
-  static constexpr uint32_t kTileBytes = kKeys * DH * 2;
-  static constexpr size_t kSmem = 1024 + 2 * kQBytes + 2 * kStages * kTileBytes;
+  static constexpr uint32_t kTileBytes = kKeys * DH * 2, kPairBytes = 2 * kTileBytes;
+  static constexpr size_t kSmem = 1024 + 2 * kQBytes + kPairs * kPairBytes + kTiles * kTileBytes;
 };
 
 // A wait that ends: at its phase, when another wait of the CTA gave up, or at
@@ -559,10 +562,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                    const __grid_constant__ TreeArgs a) {
   using Z = TcSizes<DH>;
-  constexpr int NS = Z::kStages, kBoxes = DH / 64;
+  constexpr int NK = Z::kPairs, NV = Z::kTiles, kBoxes = DH / 64;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TreePlan plan;
-  __shared__ uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], qfull[2], qempty[2], sfull[2], sfree[2], pready[2],
+  __shared__ uint64_t kfull[NK], kempty[NK], vfull[NV], vempty[NV], qfull[2], qempty[2], sfull, sfree, pready[2],
       pdone[2], ofull, odone, done;
   __shared__ float2 sml[2][2][kTreeRows];   // [segment parity][group][row] maximum and sum
   __shared__ uint32_t tmem_base;
@@ -572,25 +575,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = smem + 2 * Z::kQBytes;
-  uint8_t* sV = sK + NS * Z::kTileBytes;
+  uint8_t* sV = sK + NK * Z::kPairBytes;
   volatile int* stop = &stop_s;
   const long long unwind_ns = a.wait_ns > kUnwindNs ? a.wait_ns : kUnwindNs;
 
   if (tid == 0) {
-    for (int q = 0; q < NS; ++q) {
+    for (int q = 0; q < NK; ++q) {
       tc::mbar_init(&kfull[q], 1);
       tc::mbar_init(&kempty[q], 1);
+    }
+    for (int q = 0; q < NV; ++q) {
       tc::mbar_init(&vfull[q], 1);
       tc::mbar_init(&vempty[q], 1);
     }
     for (int q = 0; q < 2; ++q) {
       tc::mbar_init(&qfull[q], 32);
       tc::mbar_init(&qempty[q], 1);
-      tc::mbar_init(&sfull[q], 1);
-      tc::mbar_init(&sfree[q], 128);
       tc::mbar_init(&pready[q], 128);
       tc::mbar_init(&pdone[q], 1);
     }
+    tc::mbar_init(&sfull, 1);
+    tc::mbar_init(&sfree, 256);
     tc::mbar_init(&ofull, 1);
     tc::mbar_init(&odone, 256);
     tc::mbar_init(&done, 1);
@@ -614,37 +619,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == 8) {
     if (lane == 0) {  // TMA producer
-      int it = 0;
+      int kp = 0, vt = 0;   // pairs and tiles issued
       while (!*stop && cur.next(L, plan, kTreeRows, &s)) {
         if (!s.ok) continue;
         const int z = s.b * L.h + s.head;
-        for (int kt = s.k0; kt < s.k1; ++kt, ++it) {
-          const int st = it % NS, use = it / NS;
-          if (use) wait_bar(&kempty[st], (use - 1) & 1, stop, a, 31);
-          if (*stop) break;
-          tc::mbar_arrive_expect_tx(&kfull[st], Z::kTileBytes);
+        for (int kt = s.k0; kt < s.k1 && !*stop; kt += 2) {
+          const int two = min(2, s.k1 - kt);
+          {
+            const int st = kp % NK, use = kp / NK;
+            if (use && !wait_bar(&kempty[st], (use - 1) & 1, stop, a, 31)) break;
+            tc::mbar_arrive_expect_tx(&kfull[st], two * Z::kTileBytes);
+            for (int h = 0; h < two; ++h)
 #pragma unroll
-          for (int x = 0; x < kBoxes; ++x)
-            tc::tma_load_3d(sK + st * Z::kTileBytes + x * (kKeys * 128), &mapK, x * 64, kt * kKeys, z, &kfull[st]);
-          if (use) wait_bar(&vempty[st], (use - 1) & 1, stop, a, 32);
-          // (a V load of a stage whose K load went out is always issued, so
-          // that both rings count the same; its slot is free once the wait
-          // above returned without a stop)
-          if (*stop) {
-            tc::mbar_wait(&kfull[st], use & 1, unwind_ns);
-            break;
+              for (int x = 0; x < kBoxes; ++x)
+                tc::tma_load_3d(sK + st * Z::kPairBytes + x * (2 * kKeys * 128) + h * (kKeys * 128), &mapK, x * 64,
+                                (kt + h) * kKeys, z, &kfull[st]);
+            ++kp;
           }
-          tc::mbar_arrive_expect_tx(&vfull[st], Z::kTileBytes);
+          for (int h = 0; h < two; ++h) {
+            const int st = vt % NV, use = vt / NV;
+            if (use && !wait_bar(&vempty[st], (use - 1) & 1, stop, a, 32)) break;
+            tc::mbar_arrive_expect_tx(&vfull[st], Z::kTileBytes);
 #pragma unroll
-          for (int x = 0; x < kBoxes; ++x)
-            tc::tma_load_3d(sV + st * Z::kTileBytes + x * (kKeys * 128), &mapV, x * 64, kt * kKeys, z, &vfull[st]);
+            for (int x = 0; x < kBoxes; ++x)
+              tc::tma_load_3d(sV + st * Z::kTileBytes + x * (kKeys * 128), &mapV, x * 64, (kt + h) * kKeys, z,
+                              &vfull[st]);
+            ++vt;
+          }
         }
       }
       // no copy into this CTA's shared memory may be in flight when it exits
-      for (int q = max(0, it - NS); q < it; ++q) {
-        if (!tc::mbar_wait(&kfull[q % NS], (q / NS) & 1, unwind_ns)) break;
-        if (!tc::mbar_wait(&vfull[q % NS], (q / NS) & 1, unwind_ns)) break;
-      }
+      for (int q = max(0, kp - NK); q < kp; ++q)
+        if (!tc::mbar_wait(&kfull[q % NK], (q / NK) & 1, unwind_ns)) break;
+      for (int q = max(0, vt - NV); q < vt; ++q)
+        if (!tc::mbar_wait(&vfull[q % NV], (q / NV) & 1, unwind_ns)) break;
     }
     __syncwarp();
   } else if (warp == 9) {  // MMA issuer
@@ -652,7 +660,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // descriptors are warp-uniform: issued from inside a one-lane branch, the
     // 16 MMAs of a tile took 1200 cycles to issue and bounded the kernel.
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    const uint32_t idS = tc::idesc_f16(kTreeRows, kKeys, kBf16, false, false);
+    const uint32_t idS1 = tc::idesc_f16(kTreeRows, kKeys, kBf16, false, false),
+                   idS2 = tc::idesc_f16(kTreeRows, 2 * kKeys, kBf16, false, false);
     const uint32_t idO = tc::idesc_f16(kTreeRows, DH, kBf16, false, /*B MN-major*/ true);
     const uint64_t qd0 = tc::smem_desc(tc::saddr(sQ), 16, 1024, 2), kd0 = tc::smem_desc(tc::saddr(sK), 16, 1024, 2);
     // V (MN-major): 16 keys = two 8-row groups (1024 B apart), the 64-column
@@ -660,43 +669,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint64_t vd0 = tc::smem_desc(tc::saddr(sV), kKeys * 128, 1024, 2);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     uint32_t ks = 0, kph = 0, vs = 0, vph = 0;   // ring stages and their phases
-    uint32_t s_used = 0, s_ph = 0, p_ph = 0;     // bit w: group w
-    int sg = 0;
+    uint32_t p_ph = 0;                           // bit w: group w
+    int sg = 0, pairs = 0;                       // segments begun, S issued
     while (cur.next(L, plan, kTreeRows, &s)) {
       if (!s.ok) continue;
       const int nt = __shfl_sync(0xffffffffu, s.k1 - s.k0, 0);
       bool ok = wait_bar(&qfull[sg & 1], (sg >> 1) & 1, stop, a, 33);
       const uint64_t qd = qd0 + (sg & 1) * (Z::kQBytes >> 4);
-      auto issue_s = [&](uint32_t w) {
-        if ((s_used >> w) & 1) {
-          ok &= wait_bar(&sfree[w], (s_ph >> w) & 1, stop, a, 43);
-          s_ph ^= 1u << w;
-        }
-        s_used |= 1u << w;
+      auto issue_s = [&](bool two) {
+        if (pairs) ok &= wait_bar(&sfree, (pairs - 1) & 1, stop, a, 43);
+        ++pairs;
         ok &= wait_bar(&kfull[ks], kph, stop, a, 34);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc::fence_after_sync();
         if (tc::elect_one()) {
-          const uint64_t kd = kd0 + ks * (Z::kTileBytes >> 4);
+          const uint64_t kd = kd0 + ks * (Z::kPairBytes >> 4);
+          const uint32_t id = two ? idS2 : idS1;
 #pragma unroll
           for (int kk = 0; kk < DH / 16; ++kk)
-            tc::mma_f16(tm + kColS + w * kKeys, qd + ((kk >> 2) * (kTreeRows * 128) + (kk & 3) * 32) / 16,
-                        kd + ((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) / 16, idS, kk != 0);
-          tc::mma_commit(&sfull[w]);
+            tc::mma_f16(tm + kColS, qd + ((kk >> 2) * (kTreeRows * 128) + (kk & 3) * 32) / 16,
+                        kd + ((kk >> 2) * (2 * kKeys * 128) + (kk & 3) * 32) / 16, id, kk != 0);
+          tc::mma_commit(&sfull);
           tc::mma_commit(&kempty[ks]);
         }
         __syncwarp();
-        if (++ks == NS) { ks = 0; kph ^= 1; }
+        if (++ks == NK) { ks = 0; kph ^= 1; }
       };
-      if (ok) issue_s(0);
-      if (nt > 1 && ok) issue_s(1);
+      if (ok) issue_s(nt > 1);
       // O is read to the end of the previous segment before it is begun anew
       if (sg > 0) ok &= wait_bar(&odone, (sg - 1) & 1, stop, a, 35);
       for (int j = 0; j < nt && ok; ++j) {
         const uint32_t w = j & 1;
-        // S of the group's next tile while it works on this one
-        if (j + 2 < nt) issue_s(w);
+        // S of the next pair while the groups work on this one
+        if (w == 0 && j + 2 < nt) issue_s(j + 3 < nt);
         ok &= wait_bar(&pready[w], (p_ph >> w) & 1, stop, a, 36);
         p_ph ^= 1u << w;
         ok &= wait_bar(&vfull[vs], vph, stop, a, 37);
@@ -715,7 +721,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc::mma_commit(&pdone[w]);
         }
         __syncwarp();
-        if (++vs == NS) { vs = 0; vph ^= 1; }
+        if (++vs == NV) { vs = 0; vph ^= 1; }
       }
       ok = __all_sync(0xffffffffu, ok);
       if (tc::elect_one()) {
@@ -758,8 +764,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t tS = lanes + kColS + w * kKeys, tP = lanes + kColP + w * kKeys, tO = lanes + kColO + w * DH;
     int base = 0, sg = 0;
-    uint32_t scount = 0;
-    bool done_p = false;
+    uint32_t scount = 0, pcount = 0;   // pairs seen, tiles worked on
     while (cur.next(L, plan, kTreeRows, &s)) {
       if (!s.ok) {
         if (tid == 0) set_error(a.hdr, DV_ERR_INDEX_RANGE, s.head);
@@ -779,17 +784,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int j0 = (s.k0 + j) * kKeys;
         if (j >= nt || j0 + kKeys <= s.pos) return ~0ull;
         const u64 seen = active ? visible_keys(L, s, j0, t) : ~0ull;
-        const int it = base + j, st = it % NS;
-        there &= wait_bar(&vfull[st], (it / NS) & 1, stop, a, 40);
+        const int it = base + j, st = it % NV;
+        there &= wait_bar(&vfull[st], (it / NV) & 1, stop, a, 40);
         if (clean_v<T, DH>(sV + st * Z::kTileBytes, s, j0, tid & 127)) bad_v[sg & 3] = 1;
         tc::fence_proxy_async();
         return seen;
       };
       u64 vis = prepare(w);
-      for (int j = w; j < nt; j += 2) {
-        there &= wait_bar(&sfull[w], scount & 1, stop, a, 41);
+      for (int j = w; j - w < nt; j += 2) {
+        there &= wait_bar(&sfull, scount & 1, stop, a, 41);
         ++scount;
         if (!__all_sync(0xffffffffu, there)) break;  // the whole warp, or none of it
+        if (j >= nt) {  // a pair of one tile, the other group's
+          tc::mbar_arrive(&sfree);
+          break;
+        }
         tc::fence_after_sync();
         if (active) {
           float v[kKeys];
@@ -797,7 +806,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc::tmem_ld32(tS + 32, v + 32);
           tc::tmem_ld_wait();
           tc::fence_before_sync();
-          tc::mbar_arrive(&sfree[w]);
+          tc::mbar_arrive(&sfree);
           float c = a.scale_log2;
           if (c <= 0.f) {  // the maximum is taken before the scale
 #pragma unroll
@@ -816,7 +825,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           const float top = fmaxf(mx[0], mx[1]) * c;
           // P and O of the group's tile before are read and written
-          if (done_p) there &= wait_bar(&pdone[w], (scount - 2) & 1, stop, a, 44);
+          if (pcount) there &= wait_bar(&pdone[w], (pcount - 1) & 1, stop, a, 44);
           __syncwarp();
           tc::fence_after_sync();
           const bool move = row < s.rows && top > m + kSlack;
@@ -868,10 +877,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         } else {
           // a warp without rows keeps step: it must not arrive for the next
           // tile while the others are still at this one
-          tc::mbar_arrive(&sfree[w]);
-          if (done_p) wait_bar(&pdone[w], (scount - 2) & 1, stop, a, 44);
+          tc::mbar_arrive(&sfree);
+          if (pcount) wait_bar(&pdone[w], (pcount - 1) & 1, stop, a, 44);
         }
-        done_p = true;
+        ++pcount;
         tc::fence_before_sync();
         tc::mbar_arrive(&pready[w]);
         vis = prepare(j + 2);
@@ -954,10 +963,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ---- join ---------------------------------------------------------------------
 //
-// Block (c, part): the unit in which CTA c's share begins, if that is inside
-// the unit and no earlier share begins there; part of its rows.
+// Block (c, part): the unit in which CTA c + 1's share begins, if that is inside
+// the unit and no earlier share begins there; 256 of its (row, four columns).
 
-constexpr int kJoinThreads = 256, kJoinParts = 4;
+constexpr int kJoinThreads = 256;
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas,
@@ -974,13 +983,12 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   // the share before this one has to hold that tile
   const bool mine = some && s.ok && s.k0 > 0 && cur.cta_of(u0) == c - 1;
   const int owner = c - 1, pieces = mine ? cur.cta_of(u0 + s.tiles - 1) - owner + 1 : 0;
-  const int per = (s.rows + kJoinParts - 1) / kJoinParts, r0 = blockIdx.y * per, n = min(per, s.rows - r0);
+  const int i = blockIdx.y * kJoinThreads + tid;
   grid_dep_wait();
-  if (!mine || n <= 0) return;
-  // a thread to a row and four columns; four pieces' loads in flight together
-  constexpr int kP = 4;
-  for (int i = tid; i < n * (DH / 4); i += kJoinThreads) {
-    const int r = r0 + i % n, c4 = i / n;
+  if (!mine || i >= s.rows * (DH / 4)) return;
+  constexpr int kP = 4;  // pieces whose loads are in flight together
+  {
+    const int r = i % s.rows, c4 = i / s.rows;
     float M = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
     for (int q0 = 0; q0 < pieces; q0 += kP) {
       float2 ml[kP];
@@ -1019,8 +1027,9 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
 template <typename T, int DH>
 cudaError_t run_join(const TreeArgs& a, int ctas, int rows_per_unit, cudaStream_t stream) {
   if (ctas < 2) return cudaSuccess;
-  return launch_k(tree_join_kernel<T, DH>, dim3(ctas - 1, kJoinParts), dim3(kJoinThreads), 0, stream, true, 1, a, ctas,
-                  rows_per_unit);
+  const int items = min(rows_per_unit, a.L.T * a.L.g) * (DH / 4);
+  return launch_k(tree_join_kernel<T, DH>, dim3(ctas - 1, (items + kJoinThreads - 1) / kJoinThreads),
+                  dim3(kJoinThreads), 0, stream, true, 1, a, ctas, rows_per_unit);
 }
 
 template <typename T, int DH>
