@@ -177,6 +177,7 @@ LabelWs carve_label(Carver& c, int T, int N, int h, int d_h, bool heads) {
 }
 
 struct TreeWs {
+  char* shared;
   float2* ml;
   float* part;
 };
@@ -184,6 +185,7 @@ int tree_rows(int T, int group) { return T * group < kTreeRows ? T * group : kTr
 TreeWs carve_tree(Carver& c, int T, int group, int d_h) {
   TreeWs w{};
   const size_t rows = (size_t)2 * kTreeCtas * tree_rows(T, group);
+  w.shared = c.take<char>((size_t)kTreeCtas * kTreeSharedBytes);
   w.ml = c.take<float2>(rows);
   w.part = c.take<float>(rows * d_h);
   return w;
@@ -601,7 +603,7 @@ dv_status dv_tree_attn(const void* q, int B, int T, int h, int group, int d_h, c
   L.pos = pos; L.nodes = nodes; L.mask = mask; L.mask_stride = mask_batched ? (long long)T * T : 0;
   L.head_idx = head_idx; L.cap = cap; L.head_count = head_count;
   L.B = B; L.T = T; L.h = h; L.g = group; L.d_h = d_h; L.scale = scale;
-  L.part = w.part; L.ml = w.ml; L.rows_pad = tree_rows(T, group);
+  L.part = w.part; L.ml = w.ml; L.shared = w.shared; L.rows_pad = tree_rows(T, group);
   cudaError_t e = launch_tree_attn(L, dt, static_cast<WsHeader*>(ws), num_sms_current(), stream);
   return e == cudaSuccess ? DV_OK : cuda_fail(e);
 }

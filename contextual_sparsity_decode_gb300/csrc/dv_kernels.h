@@ -285,6 +285,7 @@ cudaError_t launch_rows_combine(const CombineLaunch& a, dv_dtype dt, cudaStream_
 constexpr int kTreeMaxB = 512;     // sequences (their lengths are staged in shared memory)
 constexpr int kTreeCtas = 152;     // CTAs of the persistent grid, at most
 constexpr int kTreeRows = 128;     // query rows of one unit, at most
+constexpr int kTreeSharedBytes = 32;
 struct TreeLaunch {
   const void* q; void* out;                  // [B][T][h g][d_h]
   const void* K; const void* V; int n_max;   // [B][h][n_max][d_h]
@@ -296,6 +297,7 @@ struct TreeLaunch {
   // scratch: partial results of units that several CTAs share
   float* part;      // [2 kTreeCtas][d_h / 4][rows_pad][4]
   float2* ml;       // [2 kTreeCtas][rows_pad] running maximum and sum
+  void* shared;     // [kTreeCtas] kTreeSharedBytes: the units to join
   int rows_pad;     // min(kTreeRows, T g)
 };
 cudaError_t launch_tree_attn(const TreeLaunch& a, dv_dtype dt, WsHeader* hdr, int num_sms, cudaStream_t stream);

@@ -54,7 +54,8 @@ struct Seg {
 // One block-wide pass over the sequences: checks, lengths and the prefix sums
 // of their tiles.  NT threads; ends with a barrier.
 template <int NT>
-__device__ void tree_plan(const TreeArgs& a, TreePlan* p, int rows_per_unit, bool report) {
+__device__ void tree_plan(const TreeArgs& a, TreePlan* p, int rows_per_unit) {
+  const bool report = blockIdx.x == 0;
   __shared__ long long warp_tot[NT / 32];
   const TreeLaunch& L = a.L;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -110,6 +111,15 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
   return a / b;
 }
 
+// A unit that several CTAs share, as the join reads it: written by the CTA whose
+// share holds the unit's first tile (a share has at most one such unit, its
+// last); count 0: none.
+struct __align__(16) Shared {
+  int b, head, row0, rows;
+  int count, pad[3];
+};
+static_assert(sizeof(Shared) == kTreeSharedBytes, "workspace size");
+
 // Walks the segments of this CTA's share of the tiles: of W tiles, the first
 // W % G of the G CTAs that take part get one more than W / G.
 struct Cursor {
@@ -135,6 +145,17 @@ struct Cursor {
       else hi = mid;
     }
     b = lo;
+  }
+  // The shared unit that begins in this CTA's share, once its last segment s
+  // (the one that next() gave last) is done; called by one thread.
+  __device__ void describe(const Seg& s, bool any, Shared* out) const {
+    Shared d{};
+    if (any && s.ok && s.k0 == 0 && s.k1 < s.tiles) {
+      d.b = s.b; d.head = s.head; d.row0 = s.row0; d.rows = s.rows;
+      d.count = cta_of(t - s.k1 + s.tiles - 1) - (int)blockIdx.x + 1;
+    }
+    reinterpret_cast<int4*>(out)[0] = make_int4(d.b, d.head, d.row0, d.rows);
+    reinterpret_cast<int4*>(out)[1] = make_int4(d.count, 0, 0, 0);
   }
   // The CTA whose share holds tile x.
   __device__ int cta_of(long long x) const {
@@ -170,7 +191,8 @@ struct Cursor {
 };
 
 // Query row r of unit (b, head): its offset in q and out.
-__device__ __forceinline__ size_t row_offset(const TreeLaunch& L, const Seg& s, int r, int d_h) {
+template <typename Unit>
+__device__ __forceinline__ size_t row_offset(const TreeLaunch& L, const Unit& s, int r, int d_h) {
   const int rr = s.row0 + r, t = rr / L.g, e = rr - t * L.g;
   return (((size_t)s.b * L.T + t) * L.h * L.g + (size_t)s.head * L.g + e) * d_h;
 }
@@ -258,12 +280,14 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
   constexpr int kVec = Elem<T>::kVec, kChunks = DH / kVec;
   constexpr int kCols = DH / 16;   // output columns of a thread
   grid_dep_wait();
-  grid_dep_launch();  // after the wait: the join may read the lengths at once
-  tree_plan<kSimtThreads>(a, &sm.plan, kSimtRows, blockIdx.x == 0);
+  grid_dep_launch();
+  tree_plan<kSimtThreads>(a, &sm.plan, kSimtRows);
   zero_rows<T, DH>(L, sm.plan, blockIdx.x * (kSimtThreads / 32) + wid, gridDim.x * (kSimtThreads / 32), lane, 32);
   Cursor cur(sm.plan, L.B, blockIdx.x, gridDim.x);
   Seg s;
+  bool any = false;
   while (cur.next(L, sm.plan, kSimtRows, &s)) {
+    any = true;
     if (!s.ok) {
       if (tid == 0) set_error(a.hdr, DV_ERR_INDEX_RANGE, s.head);
       continue;
@@ -387,6 +411,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
       if (c0 == 0) __stcg(&L.ml[slot * L.rows_pad + r], make_float2(sm.m[r], sm.l[r]));
     }
   }
+  if (tid == 0) cur.describe(s, any, static_cast<Shared*>(L.shared) + blockIdx.x);
 }
 
 // ---- tensor cores (16-bit storage) ------------------------------------------------
@@ -608,10 +633,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc::prefetch_map(&mapV);
   }
   if (warp == 9) tc::tmem_alloc(&tmem_base, kTcTmemCols);
-  grid_dep_wait();    // no global memory is touched before
-  grid_dep_launch();  // after the wait: the join may read the lengths at once
+  grid_dep_wait();  // no global memory is touched before
+  grid_dep_launch();
   tc::fence_before_sync();
-  tree_plan<kTcThreads>(a, &plan, kTreeRows, blockIdx.x == 0);  // ends with a barrier
+  tree_plan<kTcThreads>(a, &plan, kTreeRows);  // ends with a barrier
   tc::fence_after_sync();
   const uint32_t tmem = tmem_base;
   Cursor cur(plan, L.B, blockIdx.x, gridDim.x);
@@ -765,7 +790,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t tS = lanes + kColS + w * kKeys, tP = lanes + kColP + w * kKeys, tO = lanes + kColO + w * DH;
     int base = 0, sg = 0;
     uint32_t scount = 0, pcount = 0;   // pairs seen, tiles worked on
+    bool any = false;
     while (cur.next(L, plan, kTreeRows, &s)) {
+      any = true;
       if (!s.ok) {
         if (tid == 0) set_error(a.hdr, DV_ERR_INDEX_RANGE, s.head);
         continue;
@@ -954,6 +981,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       base += nt;
       ++sg;
     }
+    if (tid == 0) cur.describe(s, any, static_cast<Shared*>(L.shared) + blockIdx.x);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -963,29 +991,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ---- join ---------------------------------------------------------------------
 //
-// Block (c, part): the unit in which CTA c + 1's share begins, if that is inside
-// the unit and no earlier share begins there; 256 of its (row, four columns).
+// Block (c, part): the shared unit that begins in CTA c's share, 256 of its
+// (row, four columns).
 
 constexpr int kJoinThreads = 256;
 
 template <typename T, int DH>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas,
-                                                                int rows_per_unit) {
-  __shared__ TreePlan plan;
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a) {
   const TreeLaunch& L = a.L;
-  const int tid = threadIdx.x, c = blockIdx.x + 1;
+  const int owner = blockIdx.x, i = blockIdx.y * kJoinThreads + threadIdx.x;
   grid_dep_launch();
-  tree_plan<kJoinThreads>(a, &plan, rows_per_unit, false);
-  Cursor cur(plan, L.B, c, ctas);
-  Seg s{};
-  const bool some = cur.next(L, plan, rows_per_unit, &s);
-  const long long u0 = cur.t - s.k1;   // the unit's first tile
-  // the share before this one has to hold that tile
-  const bool mine = some && s.ok && s.k0 > 0 && cur.cta_of(u0) == c - 1;
-  const int owner = c - 1, pieces = mine ? cur.cta_of(u0 + s.tiles - 1) - owner + 1 : 0;
-  const int i = blockIdx.y * kJoinThreads + tid;
   grid_dep_wait();
-  if (!mine || i >= s.rows * (DH / 4)) return;
+  const int4* d = reinterpret_cast<const int4*>(static_cast<const Shared*>(L.shared) + owner);
+  const int4 d0 = __ldcg(d);
+  const int pieces = __ldcg(d + 1).x;
+  const Shared s{d0.x, d0.y, d0.z, d0.w, pieces, {0, 0, 0}};
+  if (pieces < 2 || i >= s.rows * (DH / 4)) return;
   constexpr int kP = 4;  // pieces whose loads are in flight together
   {
     const int r = i % s.rows, c4 = i / s.rows;
@@ -1026,10 +1047,9 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
 
 template <typename T, int DH>
 cudaError_t run_join(const TreeArgs& a, int ctas, int rows_per_unit, cudaStream_t stream) {
-  if (ctas < 2) return cudaSuccess;
   const int items = min(rows_per_unit, a.L.T * a.L.g) * (DH / 4);
-  return launch_k(tree_join_kernel<T, DH>, dim3(ctas - 1, (items + kJoinThreads - 1) / kJoinThreads),
-                  dim3(kJoinThreads), 0, stream, true, 1, a, ctas, rows_per_unit);
+  return launch_k(tree_join_kernel<T, DH>, dim3(ctas, (items + kJoinThreads - 1) / kJoinThreads), dim3(kJoinThreads), 0,
+                  stream, true, 1, a);
 }
 
 template <typename T, int DH>
