@@ -12,9 +12,11 @@
 // into tiles of 64 keys.  The grid is persistent, and every CTA takes an equal
 // share of all units' tiles, in order, whatever the sequences' lengths (read on
 // the device); a unit that crosses CTAs leaves a partial result (maximum, sum,
-// numerator) per CTA, and a second kernel, resident while the first runs, joins
-// them in tile order, so results do not depend on timing.  (Joined by the last
-// of its CTAs to finish, a unit of 125 rows over six CTAs took that CTA 30 us.)
+// numerator) per CTA, and a second small kernel joins them in tile order, so
+// results do not depend on timing.  (Joined by the last of its CTAs to finish,
+// behind a fence and an atomic counter, one sequence of 8 nodes over 512
+// positions took 17.6 us instead of 13.2, and three of 125 rows over 32768
+// positions 98 instead of 83.)
 
 #include <cuda.h>
 
@@ -38,9 +40,10 @@ struct TreeArgs {
   long long wait_ns;
 };
 
-// What every role of a CTA needs to walk its share of the tiles.
+// What every role of a CTA needs to walk its share of the tiles.  Tile numbers
+// fit 32 bits: the host refuses shapes whose tiles might not.
 struct TreePlan {
-  long long pre[kTreeMaxB + 1];  // tiles of the sequences before b
+  uint32_t pre[kTreeMaxB + 1];   // tiles of the sequences before b
   int pos[kTreeMaxB], nodes[kTreeMaxB];
 };
 
@@ -51,64 +54,60 @@ struct Seg {
   bool ok;                       // the head index is in range
 };
 
-// One block-wide pass over the sequences: checks, lengths and the prefix sums
-// of their tiles.  NT threads; ends with a barrier.
-template <int NT>
-__device__ void tree_plan(const TreeArgs& a, TreePlan* p, int rows_per_unit) {
-  const bool report = blockIdx.x == 0;
-  __shared__ long long warp_tot[NT / 32];
+// Checks and lengths of sequence b; returns its tiles.
+__device__ __forceinline__ uint32_t plan_one(const TreeArgs& a, TreePlan* p, int b, int rows_per_unit) {
   const TreeLaunch& L = a.L;
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  long long carry = 0;
-  for (int b0 = 0; b0 < L.B; b0 += NT) {
-    const int b = b0 + tid;
-    long long work = 0;
-    if (b < L.B) {
-      const int n = L.pos[b];
-      int nd = L.nodes ? L.nodes[b] : L.T;
-      int cnt = L.head_idx ? L.head_count[b] : L.h;
-      if (nd > L.T) {
-        if (report) set_error(a.hdr, DV_ERR_CAPACITY, nd);
-        nd = L.T;
-      }
-      if (L.head_idx && cnt > L.cap) {
-        if (report) set_error(a.hdr, DV_ERR_CAPACITY, cnt);
-        cnt = L.cap;
-      }
-      if (nd > 0 && (n < 0 || n > L.n_max - nd)) {
-        if (report) set_error(a.hdr, DV_ERR_POSITION, n);
-        nd = 0;
-      }
-      nd = max(nd, 0);
-      if (nd > 0 && cnt > 0)
-        work = (long long)cnt * ((nd * L.g + rows_per_unit - 1) / rows_per_unit) * ((n + nd + kKeys - 1) / kKeys);
-      p->pos[b] = n;
-      p->nodes[b] = nd;
-    }
-    long long v = work;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) warp_tot[wid] = v;
-    __syncthreads();
-    long long before = carry;
-    for (int q = 0; q < wid; ++q) before += warp_tot[q];
-    if (b < L.B) p->pre[b + 1] = before + v;
-    long long all = carry;
-    for (int q = 0; q < NT / 32; ++q) all += warp_tot[q];
-    carry = all;
-    __syncthreads();
+  const bool report = blockIdx.x == 0;
+  const int n = L.pos[b];
+  int nd = L.nodes ? L.nodes[b] : L.T;
+  int cnt = L.head_idx ? L.head_count[b] : L.h;
+  if (nd > L.T) {
+    if (report) set_error(a.hdr, DV_ERR_CAPACITY, nd);
+    nd = L.T;
   }
-  if (tid == 0) p->pre[0] = 0;
-  __syncthreads();
+  if (L.head_idx && cnt > L.cap) {
+    if (report) set_error(a.hdr, DV_ERR_CAPACITY, cnt);
+    cnt = L.cap;
+  }
+  if (nd > 0 && (n < 0 || n > L.n_max - nd)) {
+    if (report) set_error(a.hdr, DV_ERR_POSITION, n);
+    nd = 0;
+  }
+  nd = max(nd, 0);
+  p->pos[b] = n;
+  p->nodes[b] = nd;
+  if (nd == 0 || cnt <= 0) return 0;
+  uint32_t work = (uint32_t)cnt * (uint32_t)((n + nd + kKeys - 1) / kKeys);
+  if (nd * L.g > rows_per_unit) work *= (uint32_t)((nd * L.g + rows_per_unit - 1) / rows_per_unit);
+  return work;
 }
 
-// a / b; short where both fit 32 bits, as they nearly always do
-__device__ __forceinline__ long long quot(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
+// Lengths of all sequences and the prefix sums of their tiles.  NT threads;
+// ends with a barrier (the only one up to 32 sequences, which one warp plans).
+template <int NT>
+__device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlan* p, int rows_per_unit) {
+  const int tid = threadIdx.x, B = a.L.B;
+  if (B > 32) {
+    for (int b = tid; b < B; b += NT) p->pre[b + 1] = plan_one(a, p, b, rows_per_unit);
+    __syncthreads();
+  }
+  if (tid < 32) {
+    uint32_t carry = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      const int b = b0 + tid;
+      uint32_t v = b >= B ? 0 : B > 32 ? p->pre[b + 1] : plan_one(a, p, b, rows_per_unit);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (tid >= o) v += u;
+      }
+      v += carry;
+      if (b < B) p->pre[b + 1] = v;
+      carry = __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (tid == 0) p->pre[0] = 0;
+  }
+  __syncthreads();
 }
 
 // A unit that several CTAs share, as the join reads it: written by the CTA whose
@@ -123,28 +122,54 @@ static_assert(sizeof(Shared) == kTreeSharedBytes, "workspace size");
 // Walks the segments of this CTA's share of the tiles: of W tiles, the first
 // W % G of the G CTAs that take part get one more than W / G.
 struct Cursor {
-  long long t, t1;   // next tile, end of the share
-  long long q, r;    // W / G, W % G
+  uint32_t t, t1;   // next tile, end of the share
+  uint32_t q, r;    // W / G, W % G
   int b;
-  __device__ Cursor(const TreePlan& p, int B, int c, int ctas) {
-    const long long W = p.pre[B];
-    const long long G = W < (long long)ctas ? W : (long long)ctas;
-    if (c >= G) {
-      t = t1 = q = r = 0;
-      b = 0;
-      return;
-    }
-    q = quot(W, G);
+  __device__ Cursor(const TreePlan& p, int B) {
+    const uint32_t W = p.pre[B], G = min(W, gridDim.x), c = blockIdx.x;
+    t = t1 = q = r = 0;
+    b = 0;
+    if (c >= G) return;
+    q = W / G;
     r = W - q * G;
-    t = c * q + min((long long)c, r);
+    t = c * q + min(c, r);
     t1 = t + q + (c < r);
-    int lo = 0, hi = B;  // the last b with pre[b] <= t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.pre[mid] <= t) lo = mid;
+    int hi = B;  // b: the last with pre[b] <= t
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
+      if (p.pre[mid] <= t) b = mid;
       else hi = mid;
     }
-    b = lo;
+  }
+  // The CTA whose share holds tile x.
+  __device__ int cta_of(uint32_t x) const {
+    const uint32_t wide = r * (q + 1);
+    return (int)(x < wide ? x / (q + 1) : r + (x - wide) / q);
+  }
+  __device__ __forceinline__ bool next(const TreeLaunch& L, const TreePlan& p, int rows_per_unit, Seg* s) {
+    if (t >= t1) return false;
+    while (p.pre[b + 1] <= t) ++b;
+    s->b = b;
+    s->pos = p.pos[b];
+    s->nodes = p.nodes[b];
+    s->n = s->pos + s->nodes;
+    const int all_rows = s->nodes * L.g;
+    s->tiles = (s->n + kKeys - 1) / kKeys;
+    const uint32_t off = t - p.pre[b];
+    uint32_t slot = off / (uint32_t)s->tiles;
+    s->k0 = (int)(off - slot * s->tiles);
+    s->k1 = (int)min((uint32_t)s->tiles, s->k0 + (t1 - t));
+    s->row0 = 0;
+    if (all_rows > rows_per_unit) {
+      const uint32_t blocks = (all_rows + rows_per_unit - 1) / rows_per_unit, unit = slot;
+      slot = unit / blocks;
+      s->row0 = (int)(unit - slot * blocks) * rows_per_unit;
+    }
+    s->rows = min(rows_per_unit, all_rows - s->row0);
+    s->head = L.head_idx ? L.head_idx[(size_t)b * L.cap + slot] : (int)slot;
+    s->ok = s->head >= 0 && s->head < L.h;
+    t += s->k1 - s->k0;
+    return true;
   }
   // The shared unit that begins in this CTA's share, once its last segment s
   // (the one that next() gave last) is done; called by one thread.
@@ -156,37 +181,6 @@ struct Cursor {
     }
     reinterpret_cast<int4*>(out)[0] = make_int4(d.b, d.head, d.row0, d.rows);
     reinterpret_cast<int4*>(out)[1] = make_int4(d.count, 0, 0, 0);
-  }
-  // The CTA whose share holds tile x.
-  __device__ int cta_of(long long x) const {
-    const long long wide = r * (q + 1);
-    return (int)(x < wide ? quot(x, q + 1) : r + quot(x - wide, q));
-  }
-  __device__ bool next(const TreeLaunch& L, const TreePlan& p, int rows_per_unit, Seg* s) {
-    if (t >= t1) return false;
-    while (p.pre[b + 1] <= t) ++b;
-    s->b = b;
-    s->pos = p.pos[b];
-    s->nodes = p.nodes[b];
-    s->n = s->pos + s->nodes;
-    const int all_rows = s->nodes * L.g;
-    s->tiles = (s->n + kKeys - 1) / kKeys;
-    const long long off = t - p.pre[b];
-    const long long unit = quot(off, s->tiles);
-    s->k0 = (int)(off - unit * s->tiles);
-    s->k1 = (int)min((long long)s->tiles, s->k0 + (t1 - t));
-    int slot = (int)unit;
-    s->row0 = 0;
-    if (all_rows > rows_per_unit) {
-      const int blocks = (all_rows + rows_per_unit - 1) / rows_per_unit;
-      slot = (int)quot(unit, blocks);
-      s->row0 = (int)(unit - (long long)slot * blocks) * rows_per_unit;
-    }
-    s->rows = min(rows_per_unit, all_rows - s->row0);
-    s->head = L.head_idx ? L.head_idx[(size_t)b * L.cap + slot] : slot;
-    s->ok = s->head >= 0 && s->head < L.h;
-    t += s->k1 - s->k0;
-    return true;
   }
 };
 
@@ -283,8 +277,8 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
   grid_dep_launch();
   tree_plan<kSimtThreads>(a, &sm.plan, kSimtRows);
   zero_rows<T, DH>(L, sm.plan, blockIdx.x * (kSimtThreads / 32) + wid, gridDim.x * (kSimtThreads / 32), lane, 32);
-  Cursor cur(sm.plan, L.B, blockIdx.x, gridDim.x);
-  Seg s;
+  Cursor cur(sm.plan, L.B);
+  Seg s{};
   bool any = false;
   while (cur.next(L, sm.plan, kSimtRows, &s)) {
     any = true;
@@ -639,8 +633,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tree_plan<kTcThreads>(a, &plan, kTreeRows);  // ends with a barrier
   tc::fence_after_sync();
   const uint32_t tmem = tmem_base;
-  Cursor cur(plan, L.B, blockIdx.x, gridDim.x);
-  Seg s;
+  Cursor cur(plan, L.B);
+  Seg s{};
 
   if (warp == 8) {
     if (lane == 0) {  // TMA producer
@@ -991,10 +985,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ---- join ---------------------------------------------------------------------
 //
-// Block (c, part): the shared unit that begins in CTA c's share, 256 of its
+// Block (c, part): the shared unit that begins in CTA c's share, kJoinThreads of its
 // (row, four columns).
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;   // fits beside a CTA of the first kernel, to wait for its end there
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a) {

@@ -327,7 +327,8 @@ dv_status dv_tree_attn_workspace_size(int B, int T, int h, int group, int d_h,
  * the sequence's rows are 0), DV_ERR_INDEX_RANGE (head skipped: its rows are
  * 0), DV_ERR_CAPACITY (count above cap, or nodes above T: cut off).
  * Limits: B <= 512, T <= 1024, h <= 1024, group <= 64, d_h in {64, 128}
- * (others DV_ERR_UNSUPPORTED), n_max <= 1048576, a multiple of 16. */
+ * (others DV_ERR_UNSUPPORTED), n_max <= 1048576, a multiple of 16, and
+ * B heads (T group / 16) (n_max / 64) below 2^32 (else DV_ERR_UNSUPPORTED). */
 dv_status dv_tree_attn(const void* q, int B, int T, int h, int group, int d_h,
                        const dv_kv* kv, const int32_t* pos,
                        const int32_t* nodes, const uint8_t* mask,
