@@ -249,7 +249,67 @@ __device__ void zero_rows(const TreeLaunch& L, const TreePlan& p, int worker, in
   }
 }
 
-// ---- CUDA cores ---------------------------------------------------------------
+// Bit i: byte i of a 16-byte vector is not 0.
+__device__ __forceinline__ uint32_t nonzero16(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t top = ((((w[i] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w[i]) >> 7) & 0x01010101u;
+    bits |= ((top * 0x10204080u) >> 28) << (4 * i);
+  }
+  return bits;
+}
+
+// Bit i: the row sees key j0 + i.  t: the row's node.  The mask bytes come in
+// the aligned vectors that cover them, all in flight together (64 byte loads,
+// eight at a time, took 4500 cycles a tile); a vector that would reach outside
+// the mask is read byte by byte.
+__device__ __forceinline__ unsigned long long visible_keys(const TreeLaunch& L, const Seg& s, int j0, int t) {
+  const int u0 = j0 - s.pos;                                   // tree slot of the tile's first key
+  const int lo = min(max(-u0, 0), kKeys), hi = min(max(s.nodes - u0, 0), kKeys);
+  const unsigned long long below = lo >= 64 ? ~0ull : (1ull << lo) - 1;
+  if (!L.mask) {
+    const int top = min(max(t + 1 - u0, lo), hi);
+    return top >= 64 ? ~0ull : (1ull << top) - 1;
+  }
+  if (hi <= lo) return below;
+  const uint8_t* first = L.mask;
+  const uint8_t* end = first + (L.mask_stride ? L.B * L.mask_stride : (long long)L.T * L.T);
+  const uint8_t* p = first + s.b * L.mask_stride + (long long)t * L.T + u0 + lo;
+  const int n = hi - lo, off = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint8_t* base = p - off;
+  uint4 v[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+    v[k] = make_uint4(0, 0, 0, 0);
+    const uint8_t* at = base + 16 * k;
+    if (16 * k < off + n && at >= first && at + 16 <= end) v[k] = __ldg(reinterpret_cast<const uint4*>(at));
+  }
+  unsigned long long bits = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) bits |= (unsigned long long)nonzero16(v[k]) << (16 * k);
+  bits >>= off;
+  if (off) bits |= (unsigned long long)nonzero16(v[4]) << (64 - off);
+  for (int k = 0; k < 5; ++k) {
+    const uint8_t* at = base + 16 * k;
+    if (16 * k >= off + n || (at >= first && at + 16 <= end)) continue;
+    for (int i = max(16 * k - off, 0); i < min(16 * k + 16 - off, n); ++i)
+      bits |= (unsigned long long)(p[i] != 0) << i;
+  }
+  if (n < 64) bits &= (1ull << n) - 1;
+  return below | (bits << lo);
+}
+
+// ---- CUDA cores (32-bit storage) ----------------------------------------------
+//
+// Units of 16 query rows.  K and V tiles come by cp.async into two buffers.
+//   scores      thread = one key, four rows
+//   softmax     a warp to two rows, a lane to two keys
+//   numerators  thread = four columns and a group of a tile's keys, all rows in
+//               registers over the whole segment (a key's V is read once, a
+//               weight once for four columns); the key groups are added at the
+//               segment's end.
 
 constexpr int kSimtRows = 16;
 constexpr int kSimtThreads = 256;
@@ -258,25 +318,26 @@ template <int DH>
 struct SimtSmem {
   TreePlan plan;
   alignas(16) float q[kSimtRows][DH];
-  alignas(16) float k[kKeys][DH + 4];
-  alignas(16) float v[kKeys][DH];
-  float s[kSimtRows][kKeys + 1];   // scores, then p; -1 marks a masked key
-  float alpha[kSimtRows];
-  float m[kSimtRows], l[kSimtRows];
+  alignas(16) float k[2][kKeys][DH + 4];       // at the segment's end: [8][kSimtRows][DH] partial numerators
+  alignas(16) float v[2][kKeys][DH];
+  alignas(16) float s[kSimtRows][kKeys + 4];   // scores, then weights
+  float alpha[kSimtRows], m[kSimtRows], l[kSimtRows];
+  u64 vis[kSimtRows];                          // edge tiles: the keys that a row sees
 };
 
-template <typename T, int DH>
+template <int DH>
 __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_constant__ TreeArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SimtSmem<DH>& sm = *reinterpret_cast<SimtSmem<DH>*>(smem_raw);
   const TreeLaunch& L = a.L;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  constexpr int kVec = Elem<T>::kVec, kChunks = DH / kVec;
-  constexpr int kCols = DH / 16;   // output columns of a thread
+  constexpr int kChunks = DH / 4, kGroups = kSimtThreads / kChunks, kMine = kKeys / kGroups;
+  constexpr int kCols = DH / 16;   // output columns of a thread at the end
+  static_assert(8 * kSimtRows * DH <= 2 * kKeys * (DH + 4), "the partial numerators fit into the K buffers");
   grid_dep_wait();
   grid_dep_launch();
   tree_plan<kSimtThreads>(a, &sm.plan, kSimtRows);
-  zero_rows<T, DH>(L, sm.plan, blockIdx.x * (kSimtThreads / 32) + wid, gridDim.x * (kSimtThreads / 32), lane, 32);
+  zero_rows<float, DH>(L, sm.plan, blockIdx.x * (kSimtThreads / 32) + wid, gridDim.x * (kSimtThreads / 32), lane, 32);
   Cursor cur(sm.plan, L.B);
   Seg s{};
   bool any = false;
@@ -286,53 +347,47 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
       if (tid == 0) set_error(a.hdr, DV_ERR_INDEX_RANGE, s.head);
       continue;
     }
-    __syncthreads();
-    for (int i = tid; i < kSimtRows * kChunks; i += kSimtThreads) {
-      const int r = i / kChunks, c = i % kChunks;
-      float f[kVec];
-      if (r < s.rows) {
-        unpack<T>(ld_cached(static_cast<const T*>(L.q) + row_offset(L, s, r, DH) + c * kVec), f);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) f[e] = 0.f;
+    const size_t kv0 = ((size_t)s.b * L.h + s.head) * L.n_max * DH;
+    const auto fetch = [&](int kt, int buf) {
+      const int j0 = kt * kKeys;
+      for (int i = tid; i < kKeys * kChunks; i += kSimtThreads) {
+        const int j = i / kChunks, c = (i % kChunks) * 4, there = j0 + j < s.n ? 16 : 0;
+        const size_t at = kv0 + (size_t)(there ? j0 + j : j0) * DH + c;
+        cp_async16_or_zero(&sm.k[buf][j][c], static_cast<const float*>(L.K) + at, there);
+        cp_async16_or_zero(&sm.v[buf][j][c], static_cast<const float*>(L.V) + at, there);
       }
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) sm.q[r][c * kVec + e] = f[e];
+    };
+    __syncthreads();  // the previous segment's shared memory is no longer read
+    fetch(s.k0, 0);
+    for (int i = tid; i < kSimtRows * kChunks; i += kSimtThreads) {
+      const int r = i / kChunks, c = (i % kChunks) * 4;
+      cp_async16_or_zero(&sm.q[r][c],
+                         static_cast<const float*>(L.q) + (r < s.rows ? row_offset(L, s, r, DH) + c : (size_t)0),
+                         r < s.rows ? 16 : 0);
     }
+    cp_async_commit();
     if (tid < kSimtRows) {
       sm.m[tid] = -INFINITY;
       sm.l[tid] = 0.f;
     }
-    float acc[kCols];
+    const int c4 = tid % kChunks, grp = tid / kChunks;
+    float acc[kSimtRows][4];
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-    const size_t kv0 = ((size_t)s.b * L.h + s.head) * L.n_max * DH;
+    for (int r = 0; r < kSimtRows; ++r) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.f;
     for (int kt = s.k0; kt < s.k1; ++kt) {
-      const int j0 = kt * kKeys, nk = min(kKeys, s.n - j0);
-      __syncthreads();   // the previous tile is no longer read
-      for (int i = tid; i < kKeys * kChunks; i += kSimtThreads) {
-        const int j = i / kChunks, c = i % kChunks;
-        float fk[kVec], fv[kVec];
-        if (j < nk) {
-          unpack<T>(ld_stream(static_cast<const T*>(L.K) + kv0 + (size_t)(j0 + j) * DH + c * kVec), fk);
-          unpack<T>(ld_stream(static_cast<const T*>(L.V) + kv0 + (size_t)(j0 + j) * DH + c * kVec), fv);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) fk[e] = fv[e] = 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          sm.k[j][c * kVec + e] = fk[e];
-          sm.v[j][c * kVec + e] = fv[e];
-        }
-      }
+      const int j0 = kt * kKeys, buf = (kt - s.k0) & 1;
+      const bool edge = j0 + kKeys > s.pos;   // the tile holds tree nodes, or ends behind the last
+      if (kt + 1 < s.k1) fetch(kt + 1, buf ^ 1);
+      cp_async_commit();
+      if (edge && tid < s.rows) sm.vis[tid] = visible_keys(L, s, j0, (s.row0 + tid) / L.g);
+      cp_async_wait<1>();
       __syncthreads();
-      {  // scores: thread = one key, four rows
-        const int j = tid & (kKeys - 1), r0 = (tid / kKeys) * 4;
+      const int j = tid & (kKeys - 1), r0 = (tid / kKeys) * 4;
+      if (r0 < s.rows) {  // scores
         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
         for (int c = 0; c < DH; c += 4) {
-          const float4 k4 = *reinterpret_cast<const float4*>(&sm.k[j][c]);
+          const float4 k4 = *reinterpret_cast<const float4*>(&sm.k[buf][j][c]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float4 q4 = *reinterpret_cast<const float4*>(&sm.q[r0 + r][c]);
@@ -340,17 +395,17 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
             d[r] = fmaf(q4.z, k4.z, d[r]); d[r] = fmaf(q4.w, k4.w, d[r]);
           }
         }
-        const int u = j0 + j - s.pos;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const bool vis = r0 + r < s.rows && j < nk && (u < 0 || sees(L, s, (s.row0 + r0 + r) / L.g, u));
-          sm.s[r0 + r][j] = vis ? d[r] * a.scale_log2 : -INFINITY;
+          const bool seen = r0 + r < s.rows && (!edge || ((sm.vis[r0 + r] >> j) & 1));
+          sm.s[r0 + r][j] = seen ? d[r] * a.scale_log2 : -INFINITY;
         }
       }
       __syncthreads();
 #pragma unroll
-      for (int rr = 0; rr < kSimtRows / 8; ++rr) {  // softmax: a warp takes two rows, a lane two keys
-        const int r = wid * (kSimtRows / 8) + rr;
+      for (int rr = 0; rr < kSimtRows / 8; ++rr) {  // softmax
+        const int r = wid + rr * 8;
+        if (r >= s.rows) continue;
         const float s0 = sm.s[r][lane], s1 = sm.s[r][lane + 32];
         const float mo = sm.m[r], mn = fmaxf(mo, warp_max(fmaxf(s0, s1)));
         const float mu = mn == -INFINITY ? 0.f : mn;
@@ -366,43 +421,68 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
         }
       }
       __syncthreads();
-      {  // numerators: thread = one row, kCols columns
-        const int r = tid / 16, c0 = (tid % 16) * 4;
-        const float al = sm.alpha[r];
-        const int t = (s.row0 + r) / L.g;
+      {  // numerators
+        float4 v[kMine];
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[c] *= al;
-        for (int j = 0; j < nk; ++j) {
-          const float p = sm.s[r][j];
-          // 0 x inf: a masked V row must not reach the sum, whatever it holds
-          if (p == 0.f && (r >= s.rows || (j0 + j >= s.pos && !sees(L, s, t, j0 + j - s.pos)))) continue;
+        for (int k = 0; k < kMine; ++k) v[k] = *reinterpret_cast<const float4*>(&sm.v[buf][grp * kMine + k][c4 * 4]);
 #pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 v4 = *reinterpret_cast<const float4*>(&sm.v[j][c0 + c * 16]);
-            acc[c] = fmaf(p, v4.x, acc[c]); acc[c + 1] = fmaf(p, v4.y, acc[c + 1]);
-            acc[c + 2] = fmaf(p, v4.z, acc[c + 2]); acc[c + 3] = fmaf(p, v4.w, acc[c + 3]);
+        for (int r = 0; r < kSimtRows; ++r) {
+          if (r >= s.rows) break;
+          const float al = sm.alpha[r];
+          float o0 = acc[r][0] * al, o1 = acc[r][1] * al, o2 = acc[r][2] * al, o3 = acc[r][3] * al;
+          // a V row that the row does not see must not reach it, whatever it
+          // holds (0 x inf)
+          const uint32_t seen = edge ? (uint32_t)(sm.vis[r] >> (grp * kMine)) : ~0u;
+#pragma unroll
+          for (int k = 0; k < kMine; k += 4) {
+            const float4 p = *reinterpret_cast<const float4*>(&sm.s[r][grp * kMine + k]);
+            const float pk[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              if (edge && !((seen >> (k + x)) & 1)) continue;
+              o0 = fmaf(pk[x], v[k + x].x, o0); o1 = fmaf(pk[x], v[k + x].y, o1);
+              o2 = fmaf(pk[x], v[k + x].z, o2); o3 = fmaf(pk[x], v[k + x].w, o3);
+            }
           }
+          acc[r][0] = o0; acc[r][1] = o1; acc[r][2] = o2; acc[r][3] = o3;
         }
       }
+      __syncthreads();  // the buffers are read
     }
-    const int r = tid / 16, c0 = (tid % 16) * 4;
-    if (s.k1 - s.k0 == s.tiles) {
-      if (r < s.rows) {
-        const float l = sm.l[r], inv = l == 0.f ? 0.f : 1.f / l;
-        T* dst = static_cast<T*>(L.out) + row_offset(L, s, r, DH) + c0;
+    // the key groups' numerators: lanes 16 apart first where a warp holds two
+    float* red = &sm.k[0][0][0];
 #pragma unroll
-        for (int c = 0; c < kCols; c += 4)
-          store4<T>(dst + c * 16, acc[c] * inv, acc[c + 1] * inv, acc[c + 2] * inv, acc[c + 3] * inv);
+    for (int r = 0; r < kSimtRows; ++r) {
+      if (r >= s.rows) break;
+      if (kGroups == 16) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[r][x] += __shfl_xor_sync(0xffffffffu, acc[r][x], 16);
       }
-      continue;
+      if (kGroups == 8 || lane < 16)
+        *reinterpret_cast<float4*>(red + (wid * kSimtRows + r) * DH + c4 * 4) =
+            make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
     }
-    const size_t slot = piece_slot(blockIdx.x, s.k0 == 0);
+    __syncthreads();
+    const int r = tid / 16, c0 = (tid % 16) * 4;
     if (r < s.rows) {
-      float4* dst = reinterpret_cast<float4*>(L.part) + slot * (DH / 4) * L.rows_pad + r;
+      const bool whole = s.k1 - s.k0 == s.tiles;
+      const float l = sm.l[r], inv = l == 0.f ? 0.f : 1.f / l;
+      const size_t slot = piece_slot(blockIdx.x, s.k0 == 0);
 #pragma unroll
-      for (int c = 0; c < kCols; c += 4)
-        __stcg(dst + (size_t)((c0 + c * 16) / 4) * L.rows_pad, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
-      if (c0 == 0) __stcg(&L.ml[slot * L.rows_pad + r], make_float2(sm.m[r], sm.l[r]));
+      for (int c = 0; c < kCols; c += 4) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float4 x = *reinterpret_cast<const float4*>(red + (g * kSimtRows + r) * DH + c0 + c * 16);
+          o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+        }
+        if (whole)
+          store4<float>(static_cast<float*>(L.out) + row_offset(L, s, r, DH) + c0 + c * 16, o.x * inv, o.y * inv,
+                        o.z * inv, o.w * inv);
+        else
+          __stcg(reinterpret_cast<float4*>(L.part) + (slot * (DH / 4) + (c0 + c * 16) / 4) * L.rows_pad + r, o);
+      }
+      if (!whole && c0 == 0) __stcg(&L.ml[slot * L.rows_pad + r], make_float2(sm.m[r], l));
     }
   }
   if (tid == 0) cur.describe(s, any, static_cast<Shared*>(L.shared) + blockIdx.x);
@@ -492,58 +572,6 @@ template <> struct Half2<__nv_bfloat16> {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   }
 };
-
-// Bit i: byte i of a 16-byte vector is not 0.
-__device__ __forceinline__ uint32_t nonzero16(const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t bits = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t top = ((((w[i] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w[i]) >> 7) & 0x01010101u;
-    bits |= ((top * 0x10204080u) >> 28) << (4 * i);
-  }
-  return bits;
-}
-
-// Bit i: the row sees key j0 + i.  t: the row's node.  The mask bytes come in
-// the aligned vectors that cover them, all in flight together (64 byte loads,
-// eight at a time, took 4500 cycles a tile); a vector that would reach outside
-// the mask is read byte by byte.
-__device__ __forceinline__ unsigned long long visible_keys(const TreeLaunch& L, const Seg& s, int j0, int t) {
-  const int u0 = j0 - s.pos;                                   // tree slot of the tile's first key
-  const int lo = min(max(-u0, 0), kKeys), hi = min(max(s.nodes - u0, 0), kKeys);
-  const unsigned long long below = lo >= 64 ? ~0ull : (1ull << lo) - 1;
-  if (!L.mask) {
-    const int top = min(max(t + 1 - u0, lo), hi);
-    return top >= 64 ? ~0ull : (1ull << top) - 1;
-  }
-  if (hi <= lo) return below;
-  const uint8_t* first = L.mask;
-  const uint8_t* end = first + (L.mask_stride ? L.B * L.mask_stride : (long long)L.T * L.T);
-  const uint8_t* p = first + s.b * L.mask_stride + (long long)t * L.T + u0 + lo;
-  const int n = hi - lo, off = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
-  const uint8_t* base = p - off;
-  uint4 v[5];
-#pragma unroll
-  for (int k = 0; k < 5; ++k) {
-    v[k] = make_uint4(0, 0, 0, 0);
-    const uint8_t* at = base + 16 * k;
-    if (16 * k < off + n && at >= first && at + 16 <= end) v[k] = __ldg(reinterpret_cast<const uint4*>(at));
-  }
-  unsigned long long bits = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) bits |= (unsigned long long)nonzero16(v[k]) << (16 * k);
-  bits >>= off;
-  if (off) bits |= (unsigned long long)nonzero16(v[4]) << (64 - off);
-  for (int k = 0; k < 5; ++k) {
-    const uint8_t* at = base + 16 * k;
-    if (16 * k >= off + n || (at >= first && at + 16 <= end)) continue;
-    for (int i = max(16 * k - off, 0); i < min(16 * k + 16 - off, n); ++i)
-      bits |= (unsigned long long)(p[i] != 0) << i;
-  }
-  if (n < 64) bits &= (1ull << n) - 1;
-  return below | (bits << lo);
-}
 
 // The V rows of a tile that not every row may see, in shared memory before the
 // product reads them: rows behind the last node become 0, and so do values of
@@ -1065,17 +1093,17 @@ cudaError_t run_tc(const TreeArgs& a, int num_sms, cudaStream_t stream) {
   return e == cudaSuccess ? run_join<T, DH>(a, ctas, kTreeRows, stream) : e;
 }
 
-template <typename T, int DH>
+template <int DH>
 cudaError_t run_simt(const TreeArgs& a, int num_sms, cudaStream_t stream) {
   constexpr size_t smem = sizeof(SimtSmem<DH>);
   static PerDevice attr;  // function attributes are per device
   const cudaError_t ea = (cudaError_t)attr.get(current_device(), [] {
-    return (int)cudaFuncSetAttribute(tree_simt_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return (int)cudaFuncSetAttribute(tree_simt_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (ea != cudaSuccess) return ea;
   const int ctas = min(num_sms, kTreeCtas);
-  const cudaError_t e = launch_k(tree_simt_kernel<T, DH>, dim3(ctas), dim3(kSimtThreads), smem, stream, true, 1, a);
-  return e == cudaSuccess ? run_join<T, DH>(a, ctas, kSimtRows, stream) : e;
+  const cudaError_t e = launch_k(tree_simt_kernel<DH>, dim3(ctas), dim3(kSimtThreads), smem, stream, true, 1, a);
+  return e == cudaSuccess ? run_join<float, DH>(a, ctas, kSimtRows, stream) : e;
 }
 
 }  // namespace
@@ -1084,7 +1112,7 @@ cudaError_t launch_tree_attn(const TreeLaunch& L, dv_dtype dt, WsHeader* hdr, in
   const TreeArgs a{L, L.scale * kLog2e, hdr, wait_limit_ns()};
   const bool wide = L.d_h == 128;
   switch (dt) {
-    case DV_F32: return wide ? run_simt<float, 128>(a, num_sms, stream) : run_simt<float, 64>(a, num_sms, stream);
+    case DV_F32: return wide ? run_simt<128>(a, num_sms, stream) : run_simt<64>(a, num_sms, stream);
     case DV_F16: return wide ? run_tc<__half, 128>(a, num_sms, stream) : run_tc<__half, 64>(a, num_sms, stream);
     case DV_BF16:
       return wide ? run_tc<__nv_bfloat16, 128>(a, num_sms, stream) : run_tc<__nv_bfloat16, 64>(a, num_sms, stream);
