@@ -669,7 +669,7 @@ dv_status dv_beam_select(const void* logits, int n_seq, int width, int V, long l
   L.S = n_seq; L.W = width; L.V = V; L.K = K;
   L.score = score; L.token = token; L.beam = beam;
   L.stat = w.stat; L.cand = w.cand;
-  cudaError_t e = launch_beam_select(L, dt, num_sms_current(), stream);
+  cudaError_t e = launch_beam_select(L, dt, static_cast<WsHeader*>(ws), num_sms_current(), stream);
   return e == cudaSuccess ? DV_OK : cuda_fail(e);
 }
 

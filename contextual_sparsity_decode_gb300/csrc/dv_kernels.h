@@ -334,8 +334,9 @@ struct BeamLaunch {
   // room for a part per tile
   float2* stat;    // [S W][parts] maximum and sum of exponentials
   int2* cand;      // [S W][parts][K] (value bits, token)
+  WsHeader* hdr; long long wait_ns;          // set by the launcher
 };
-cudaError_t launch_beam_select(const BeamLaunch& a, dv_dtype dt, int num_sms, cudaStream_t stream);
+cudaError_t launch_beam_select(const BeamLaunch& a, dv_dtype dt, WsHeader* hdr, int num_sms, cudaStream_t stream);
 
 // ---- misc (k_misc.cu) --------------------------------------------------------
 

@@ -10,8 +10,9 @@
 //
 // One pass over the logits (the floor: each is read once, which at 48 x 10 rows
 // of 128001 bf16 logits takes 18 us).
-//   scan  a CTA walks a part of a row in tiles of kBeamTile tokens, the next
-//         tile's loads in flight: a running maximum and sum of exponentials
+//   scan  a CTA walks a part of a row in tiles of kBeamTile tokens, which bulk
+//         copies bring into a ring of shared memory (register loads one tile
+//         ahead streamed 2.4 TB/s): a running maximum and sum of exponentials
 //         per thread, and the groups of 8 tokens whose maximum may be among
 //         the K largest: the K best groups, by maximum and then the lower
 //         token, hold the K best tokens (each group left out is preceded by K
@@ -31,6 +32,7 @@
 #include <cfloat>
 
 #include "dv_kernels.h"
+#include "tc_common.cuh"
 
 namespace dv {
 namespace {
@@ -94,47 +96,40 @@ __device__ __forceinline__ U block_rth(U v, int r, U* all, U* result) {
   return *result;
 }
 
-// Eight consecutive tokens of a row at any address: the aligned 16-byte
-// vectors that cover them, as they are loaded (the overlap with the next
-// group is an L1 hit).
+// Eight consecutive tokens that begin `off` bytes behind a 16-byte boundary of
+// shared memory, cut out of the aligned vectors that cover them.
 template <typename T>
 struct Raw8 {
   static constexpr int kVecs = sizeof(T) * 8 / 16;
-  uint4 x[kVecs + 1];
-  // Whole vectors are read only within the logits' memory [first, last);
-  // groups at its ends, or at the row's, are read token by token.
-  static __device__ __forceinline__ bool whole(const T* row, int v, int V, const char* first, const char* last) {
-    const char* p = reinterpret_cast<const char*>(row + v);
-    const uint32_t off = reinterpret_cast<uintptr_t>(p) & 15u;
-    return v + 8 <= V && p - off >= first && (off == 0 || p - off + 16 * (kVecs + 1) <= last);
-  }
-  __device__ __forceinline__ void load(const T* row, int v) {
-    const char* p = reinterpret_cast<const char*>(row + v);
-    const uint32_t off = reinterpret_cast<uintptr_t>(p) & 15u;
-    const uint4* base = reinterpret_cast<const uint4*>(p - off);
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) x[i] = __ldg(base + i);
-    if (off) x[kVecs] = __ldg(base + kVecs);
-  }
   // the words from byte 4 WORDS + bits / 8 on
   template <int WORDS>
-  __device__ __forceinline__ void cut(uint32_t bits, float* f) const {
+  static __device__ __forceinline__ void cut(const uint4* p, uint32_t bits, float* f) {
+    uint4 x[kVecs + 1];
+#pragma unroll
+    for (int i = 0; i <= kVecs; ++i) x[i] = p[i];
     const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
     uint32_t y[4 * kVecs];
 #pragma unroll
-    for (int i = 0; i < 4 * kVecs; ++i) y[i] = __funnelshift_r(w[i + WORDS], w[i + WORDS + 1 < 4 * kVecs + 4 ? i + WORDS + 1 : 0], bits);
+    for (int i = 0; i < 4 * kVecs; ++i)
+      y[i] = __funnelshift_r(w[i + WORDS], w[i + WORDS + 1 < 4 * kVecs + 4 ? i + WORDS + 1 : 0], bits);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
       unpack<T>(make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]), f + i * Elem<T>::kVec);
   }
-  // off: the row's offset from a 16-byte boundary (the same for all its groups)
-  __device__ __forceinline__ void open(uint32_t off, float* f) const {
+  static __device__ __forceinline__ void open(const uint4* p, uint32_t off, float* f) {
     const uint32_t bits = (off & 3u) * 8;
     switch (off >> 2) {
-      case 0: cut<0>(bits, f); break;
-      case 1: cut<1>(bits, f); break;
-      case 2: cut<2>(bits, f); break;
-      default: cut<3>(bits, f); break;
+      case 0:
+        if (bits == 0) {
+#pragma unroll
+          for (int i = 0; i < kVecs; ++i) unpack<T>(p[i], f + i * Elem<T>::kVec);
+        } else {
+          cut<0>(p, bits, f);
+        }
+        break;
+      case 1: cut<1>(p, bits, f); break;
+      case 2: cut<2>(p, bits, f); break;
+      default: cut<3>(p, bits, f); break;
     }
   }
 };
@@ -163,29 +158,6 @@ struct JoinRow {
   float cum;
   int kind;     // 0: the listed tokens, 1: every token at -inf, 2: ended
 };
-
-// Entry i of the join, entry e of beam w's lists: its token (-1: none) and
-// logit.  A beam that lists nothing offers its K lowest tokens at -inf; an
-// ended beam's end token, at its score, takes its own place among them or that
-// of the last (*ends).
-__device__ __forceinline__ int join_entry(const BeamLaunch& a, const JoinRow* rows, int s, int i, int per_row, int* w,
-                                          float* x, bool* ends) {
-  *w = i / per_row;
-  const int e = i - *w * per_row, kind = rows[*w].kind;
-  *x = -INFINITY;
-  *ends = false;
-  if (kind == 0) {
-    const int2 p = __ldcg(&a.cand[(size_t)(s * a.W + *w) * per_row + e]);
-    *x = __int_as_float(p.x);
-    return p.y;
-  }
-  if (e >= a.K) return -1;
-  if (kind == 2 && (e == a.end || (e == a.K - 1 && a.end >= a.K))) {
-    *ends = true;
-    return a.end;
-  }
-  return e < a.V ? e : -1;
-}
 
 // Bounds of an entry's score in fp32: the score lies in [lo, hi] (three
 // roundings of at most 2^-24 of the summed magnitudes).
@@ -257,48 +229,80 @@ __device__ __forceinline__ int shorten(u64* list, u64* kept, int n, int K, uint3
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const BeamLaunch a) {
+struct Ring {
+  static constexpr int kStages = sizeof(T) == 4 ? 3 : 4;
+  static constexpr uint32_t kBytes = kBeamTile * sizeof(T) + 32;   // a tile, from and to 16-byte boundaries
+};
+constexpr long long kUnwindNs = 2000000000LL;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_kernel(const BeamLaunch a) {
+  constexpr int ST = Ring<T>::kStages;
+  extern __shared__ __align__(16) uint8_t ring[];
   // keys (value, lower token first): of groups, by their maximum; of tokens
   __shared__ u64 list[kListed], kept[kListed];
   __shared__ u64 all[kThreads];
   __shared__ u64 rth;
+  __shared__ uint64_t full[ST];
   __shared__ uint32_t red[kWarps];
   __shared__ float redm[kWarps], reds[kWarps];
-  __shared__ int listed;
+  __shared__ int listed, stop[2];   // stop: by the tile's parity (a thread may be one barrier ahead)
   const int part = blockIdx.x, row = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  if (tid == 0) {
+    for (int q = 0; q < ST; ++q) tc::mbar_init(&full[q], 1);
+    tc::fence_mbar_init();
+    listed = stop[0] = stop[1] = 0;
+  }
+  grid_dep_wait();
   grid_dep_launch();
+  __syncthreads();
   if (a.done && a.done[row]) return;  // an ended beam's logits are not read
   const T* x = static_cast<const T*>(a.logits) + (size_t)row * a.ld;
   const char* first = static_cast<const char*>(a.logits);
   const char* last = first + ((size_t)(a.S * a.W - 1) * a.ld + a.V) * sizeof(T);
   const uint32_t off = reinterpret_cast<uintptr_t>(x) & 15u;
   const int lo = part * a.part_tiles * kBeamTile, hi = min(a.V, lo + a.part_tiles * kBeamTile);
-
-  Raw8<T> raw[kGroups];
-  const auto fetch = [&](int v0) {
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int v = v0 + (g * kThreads + tid) * 8;
-      if (v < hi && Raw8<T>::whole(x, v, a.V, first, last)) raw[g].load(x, v);
-    }
+  const int tiles = (hi - lo + kBeamTile - 1) / kBeamTile;
+  // Copies begin and end on 16-byte boundaries and stay within the logits'
+  // memory [first, last): groups of tokens outside [g_lo, g_hi), at its very
+  // ends or at the row's, are read token by token instead.
+  const char* begin = reinterpret_cast<const char*>(x) - off;
+  const int skip = begin < first ? 16 : 0;     // the first vector begins before the logits
+  const int g_lo = skip ? 8 : 0;
+  const long long room = (last - begin) & ~15LL;  // bytes of whole vectors from `begin` on
+  const int g_hi = min(hi, (int)min((long long)a.V, (room - (long long)off) / (long long)sizeof(T))) - 7;
+  const auto issue = [&](int k) {   // tile k's copy, by one thread
+    const long long b0 = (long long)(lo + k * kBeamTile) * sizeof(T);  // from `begin`: a multiple of 16
+    long long b1 = b0 + off + (long long)min(kBeamTile, hi - lo - k * kBeamTile) * sizeof(T);
+    b1 = min((b1 + 15) & ~15LL, room);
+    const int cut = b0 == 0 ? skip : 0;
+    const long long bytes = max(0LL, b1 - b0 - cut);
+    tc::mbar_arrive_expect_tx(&full[k % ST], (uint32_t)bytes);
+    if (bytes) tc::bulk_g2s(ring + (k % ST) * Ring<T>::kBytes + cut, begin + b0 + cut, (uint32_t)bytes, &full[k % ST]);
   };
-  fetch(lo);
-  if (tid == 0) listed = 0;
+  int issued = 0;
+  if (tid == 0)
+    while (issued < min(ST, tiles)) issue(issued++);
   float m = -INFINITY, sum = 0.f, tau = -INFINITY;
-  for (int v0 = lo; v0 < hi; v0 += kBeamTile) {
+  for (int k = 0; k < tiles; ++k) {
+    const int v0 = lo + k * kBeamTile;
+    if (!tc::mbar_try_wait(&full[k % ST], (k / ST) & 1) && !tc::mbar_wait(&full[k % ST], (k / ST) & 1, a.wait_ns)) {
+      stop[k & 1] = 1;
+      set_error(a.hdr, DV_ERR_TIMEOUT, 51);
+    }
+    const uint8_t* tile = ring + (k % ST) * Ring<T>::kBytes;
     float f[8 * kGroups];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const int v = v0 + (g * kThreads + tid) * 8;
-      if (v < hi && Raw8<T>::whole(x, v, a.V, first, last)) {
-        raw[g].open(off, f + 8 * g);
+      if (v >= g_lo && v < g_hi) {
+        Raw8<T>::open(reinterpret_cast<const uint4*>(tile + (size_t)(g * kThreads + tid) * 8 * sizeof(T)), off, f + 8 * g);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[8 * g + e] = v + e < hi ? Elem<T>::to_f(x[v + e]) : -INFINITY;
       }
     }
-    if (v0 + kBeamTile < hi) fetch(v0 + kBeamTile);
     float g8[kGroups];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
@@ -339,7 +343,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const BeamLaunch
         }
       }
     }
-    if (__syncthreads_or(over)) {
+    const bool full_list = __syncthreads_or(over);
+    // every thread has the tile in registers: its stage takes the next
+    if (stop[k & 1]) break;
+    if (tid == 0 && k + ST < tiles) issue(issued++);
+    if (full_list) {
       cut_back(list, kept, listed, a.K, all, &rth, &listed);
       tau = fmaxf(tau, unord32((uint32_t)(rth >> 32)));
     } else if (v0 == lo && lo + kBeamTile < hi) {
@@ -352,6 +360,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const BeamLaunch
       __syncthreads();
     }
   }
+  // no copy may be in flight when the CTA exits (all have landed already unless a wait gave up)
+  for (int k = max(0, issued - ST); k < issued; ++k)
+    if (!tc::mbar_wait(&full[k % ST], (k / ST) & 1, kUnwindNs > a.wait_ns ? kUnwindNs : a.wait_ns)) break;
   // the part's maximum and sum
   const float wm = warp_max(m);
   const float ws = warp_sum(m > -INFINITY ? sum * ex2((m - wm) * kLog2e) : sum != sum ? sum : 0.f);
@@ -421,13 +432,31 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamLaunch a)
   __shared__ JoinRow rows[kBeamMaxWidth];
   __shared__ float2 stat[kBeamMaxWidth];   // a row's maximum, and whether it holds a NaN or +inf
   __shared__ double sums[kBeamMaxWidth];
-  __shared__ uint32_t all[kThreads];
-  __shared__ uint32_t rth;
+  __shared__ uint32_t red[kWarps];
   __shared__ Cand redc[kWarps];
   __shared__ int listed;
   const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int per_row = a.parts * a.K, total = a.W * per_row;
+  constexpr int kHeld = 4;  // entries that a thread reads at once, and keeps if there are no more
+  // entries are dealt out so that every warp gets its share of a short list
+  const int first = lane * kWarps + wid;
   grid_dep_wait();
+  grid_dep_launch();
   if (tid == 0) listed = 0;
+  // one round of reads: the rows' sums, their scores so far, and the lists
+  float cum = 0.f;
+  int ended = 0;
+  if (tid < a.W) {
+    cum = a.cum[s * a.W + tid];
+    ended = a.done ? a.done[s * a.W + tid] : 0;
+  }
+  int2 held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = first + k * kThreads;
+    held[k] = make_int2(0, -1);
+    if (i < total) held[k] = __ldcg(&a.cand[(size_t)s * total + i]);
+  }
   for (int q = wid; q < a.W; q += kWarps) {  // a warp to a row, a lane to a part
     const float2* st = a.stat + (size_t)(s * a.W + q) * a.parts;
     const float2 p0 = lane < a.parts ? __ldcg(&st[lane]) : make_float2(-INFINITY, 0.f);
@@ -455,12 +484,10 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamLaunch a)
   }
   __syncthreads();
   if (tid < a.W) {
-    const int r = s * a.W + tid;
-    const float cum = a.cum[r];
     const bool open = cum > -INFINITY && cum < INFINITY;   // NaN and +inf count as -inf
     const float2 st = stat[tid];
     JoinRow j{0.0, cum, 1};
-    if (a.done && a.done[r]) {
+    if (ended) {
       j.kind = 2;
       j.base = open ? (double)cum : -INFINITY;
     } else if (st.y == 0.f && st.x > -INFINITY && open) {
@@ -470,72 +497,66 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamLaunch a)
     rows[tid] = j;
   }
   __syncthreads();
-  // K scores reach t, the K-th largest of the threads' best lower bounds, so
-  // none of the K best has an upper bound below it
-  const int per_row = a.parts * a.K, total = a.W * per_row;
-  constexpr int kHeld = 6;  // entries that a thread reads at once, and keeps if there are no more
-  int ew[kHeld], ev[kHeld];
-  float ex[kHeld];
-  bool ee[kHeld];
+  // Entry i, with what was read of it: its beam, its token (-1: none) and its
+  // logit.  A beam that lists nothing offers its K lowest tokens at -inf; an
+  // ended beam's end token, at its score, takes its own place among them or
+  // that of the last (*ends).
+  const auto entry = [&](int i, const int2& p, int* w, float* x, bool* ends) {
+    *w = i / per_row;
+    const int e = i - *w * per_row, kind = rows[*w].kind;
+    *x = -INFINITY;
+    *ends = false;
+    if (kind == 0) {
+      *x = __int_as_float(p.x);
+      return p.y;
+    }
+    if (e >= a.K) return -1;
+    if (kind == 2 && (e == a.end || (e == a.K - 1 && a.end >= a.K))) {
+      *ends = true;
+      return a.end;
+    }
+    return e < a.V ? e : -1;
+  };
+  const auto read = [&](int i, int k) {
+    return k < kHeld ? held[k < kHeld ? k : 0] : __ldcg(&a.cand[(size_t)s * total + i]);
+  };
+  // K scores reach t, so none of the K best has an upper bound below it
   uint32_t best = 0;
+  const auto bound = [&](int i, const int2& p) {
+    int w;
+    float x, lo, hi;
+    bool ends;
+    if (entry(i, p, &w, &x, &ends) < 0) return;
+    join_bounds(rows[w], x, ends, &lo, &hi);
+    best = max(best, ord32(lo));
+  };
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) {  // threads behind the last entry hold none
-    ew[k] = 0;
-    ev[k] = -1;
-    ex[k] = -INFINITY;
-    ee[k] = false;
-  }
-  for (int i0 = tid; i0 < total; i0 += kHeld * kThreads) {
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      const int i = i0 + k * kThreads;
-      ev[k] = -1;
-      if (i < total) ev[k] = join_entry(a, rows, s, i, per_row, &ew[k], &ex[k], &ee[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      float lo, hi;
-      if (ev[k] < 0) continue;
-      join_bounds(rows[ew[k]], ex[k], ee[k], &lo, &hi);
-      best = max(best, ord32(lo));
-    }
-  }
-  const uint32_t t = block_rth<uint32_t>(best, a.K, all, &rth);
+  for (int k = 0; k < kHeld; ++k)
+    if (first + k * kThreads < total) bound(first + k * kThreads, held[k]);
+  for (int i = first + kHeld * kThreads; i < total; i += kThreads) bound(i, read(i, kHeld));
+  const uint32_t t = block_reached(best, a.K, red);
   // the candidate of an entry whose upper bound reaches t
-  const auto score = [&](int w, int v, float x, bool ends, Cand* c) {
-    if (v < 0) return false;
-    const JoinRow& r = rows[w];
-    float lo, hi;
+  const auto candidate = [&](int i, const int2& p, Cand* c) {
+    float x, lo, hi;
+    bool ends;
+    c->v = entry(i, p, &c->w, &x, &ends);
+    if (c->v < 0) return false;
+    const JoinRow& r = rows[c->w];
     join_bounds(r, x, ends, &lo, &hi);
     if (ord32(hi) < t) return false;
     c->key = ord64(ends ? r.base : r.kind != 0 ? -INFINITY : (double)r.cum + ((double)x - r.base));
-    c->w = w;
-    c->v = v;
     return true;
   };
-  const auto candidate = [&](int i, Cand* c) {
-    int w;
-    float x;
-    bool ends;
-    const int v = join_entry(a, rows, s, i, per_row, &w, &x, &ends);
-    return score(w, v, x, ends, c);
-  };
-  const auto add = [&](const Cand& c) {
+  const auto add = [&](int i, const int2& p) {
+    Cand c;
+    if (!candidate(i, p, &c)) return;
     const int at = atomicAdd(&listed, 1);
     if (at < kJoinListed) list[at] = c;
   };
-  if (total <= kHeld * kThreads) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      Cand c;
-      if (score(ew[k], ev[k], ex[k], ee[k], &c)) add(c);
-    }
-  } else {
-    for (int i = tid; i < total; i += kThreads) {
-      Cand c;
-      if (candidate(i, &c)) add(c);
-    }
-  }
+  for (int k = 0; k < kHeld; ++k)
+    if (first + k * kThreads < total) add(first + k * kThreads, held[k]);
+  for (int i = first + kHeld * kThreads; i < total; i += kThreads) add(i, read(i, kHeld));
   __syncthreads();
   const int n = listed;
   if (n <= kJoinListed) {
@@ -554,7 +575,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamLaunch a)
     Cand top{0, kBeamMaxWidth, 0};
     for (int i = tid; i < total; i += kThreads) {
       Cand c;
-      if (candidate(i, &c) && before(prev, c) && before(c, top)) top = c;
+      if (candidate(i, read(i, kHeld), &c) && before(prev, c) && before(c, top)) top = c;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -580,37 +601,46 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamLaunch a)
 
 namespace {
 
-// Parts of a row: as many CTAs as the GPU holds at once (four to an SM) or a
-// multiple of it, a part costing its tiles and about two more for its start
-// and end; a small problem gets a CTA per tile.
-int part_tiles(int rows, int V, int num_sms) {
-  const int tiles = (V + kBeamTile - 1) / kBeamTile, slots = 4 * num_sms;
+// Tiles of a part.  Time is that of the tiles on the busiest SM, a part's start
+// and end costing about two more, and of a round's latency (about eight tiles)
+// for every time the GPU is filled (`per_sm` CTAs an SM); the least is taken,
+// fewer parts where equal.
+int part_tiles(int rows, int V, int num_sms, int per_sm) {
+  const int tiles = (V + kBeamTile - 1) / kBeamTile;
+  const long long slots = (long long)per_sm * num_sms;
   int best = tiles;
   long long least = -1;
-  for (int t = tiles; t >= 1; --t) {
+  for (int t = tiles; t >= 1; t -= 1 + t / 16) {  // long rows: coarser steps
     const long long ctas = (long long)rows * ((tiles + t - 1) / t);
-    const long long cost = (ctas + slots - 1) / slots * (t + 2);
+    const long long cost = (ctas + num_sms - 1) / num_sms * (t + 2) + 8 * ((ctas + slots - 1) / slots);
     if (least < 0 || cost < least) {
       least = cost;
       best = t;
     }
-    if (tiles > 64 && t > 64) t = t - t / 16;  // long rows: coarser steps
   }
   return best;
 }
 
 template <typename T>
 cudaError_t run_beam(const BeamLaunch& a, cudaStream_t stream) {
-  const cudaError_t e = launch_k(beam_scan_kernel<T>, dim3(a.parts, a.S * a.W), dim3(kThreads), 0, stream, false, 1, a);
+  constexpr size_t smem = Ring<T>::kStages * Ring<T>::kBytes;
+  static PerDevice attr;  // function attributes are per device
+  const cudaError_t ea = (cudaError_t)attr.get(current_device(), [] {
+    return (int)cudaFuncSetAttribute(beam_scan_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (ea != cudaSuccess) return ea;
+  const cudaError_t e = launch_k(beam_scan_kernel<T>, dim3(a.parts, a.S * a.W), dim3(kThreads), smem, stream, true, 1, a);
   if (e != cudaSuccess) return e;
   return launch_k(beam_join_kernel, dim3(a.S), dim3(kThreads), 0, stream, true, 1, a);
 }
 
 }  // namespace
 
-cudaError_t launch_beam_select(const BeamLaunch& L, dv_dtype dt, int num_sms, cudaStream_t stream) {
+cudaError_t launch_beam_select(const BeamLaunch& L, dv_dtype dt, WsHeader* hdr, int num_sms, cudaStream_t stream) {
   BeamLaunch a = L;
-  a.part_tiles = part_tiles(a.S * a.W, a.V, num_sms);
+  a.hdr = hdr;
+  a.wait_ns = wait_limit_ns();
+  a.part_tiles = part_tiles(a.S * a.W, a.V, num_sms, dt == DV_F32 ? 3 : 4);
   a.parts = ((a.V + kBeamTile - 1) / kBeamTile + a.part_tiles - 1) / a.part_tiles;
   switch (dt) {
     case DV_F32: return run_beam<float>(a, stream);
