@@ -16,20 +16,19 @@
 //         per thread, and the groups of 8 tokens whose maximum may be among
 //         the K largest: the K best groups, by maximum and then the lower
 //         token, hold the K best tokens (each group left out is preceded by K
-//         tokens of others).  The first tile gives a value tau that K maxima
-//         reach; of later groups only those above tau are listed (an equal
-//         one comes after K others), which are few; a list that grows long is
-//         cut back and tau raised.  At the part's end the K best groups'
-//         tokens are read again and ranked.  No sort, and no reduction over
-//         the block in the loop.
+//         tokens of others).  The threads' running maxima give a value tau
+//         that K groups reach, sharper with every tile; a group is listed if
+//         its maximum is above the tau before its tile (an equal one comes
+//         after K others) and reaches the one with it: about K / k groups of
+//         tile k.  A list that grows long all the same is cut back.  At the
+//         part's end the K best groups' tokens are read again and ranked.  No
+//         sort, and one barrier a tile.
 //   join  one CTA per sequence, launched while the scan runs: log-sum-exp of
 //         the parts in double, then the K best of the parts' lists.
 // -inf tokens are never listed: a part with fewer than K others adds its
 // lowest ones, which lie among its first 2 K tokens.
 // The tokens of a thread and the order of every sum depend on the token index
 // alone, not on the row's address, so rows with equal logits get equal sums.
-
-#include <cfloat>
 
 #include "dv_kernels.h"
 #include "tc_common.cuh"
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
   __shared__ u64 all[kThreads];
   __shared__ u64 rth;
   __shared__ uint64_t full[ST];
-  __shared__ uint32_t red[kWarps];
+  __shared__ uint32_t red[2][kWarps];
   __shared__ float redm[kWarps], reds[kWarps];
   __shared__ int listed, stop[2];   // stop: by the tile's parity (a thread may be one barrier ahead)
   const int part = blockIdx.x, row = blockIdx.y;
@@ -285,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
   if (tid == 0)
     while (issued < min(ST, tiles)) issue(issued++);
   float m = -INFINITY, sum = 0.f, tau = -INFINITY;
+  bool over = false;
   for (int k = 0; k < tiles; ++k) {
     const int v0 = lo + k * kBeamTile;
     if (!tc::mbar_try_wait(&full[k % ST], (k / ST) & 1) && !tc::mbar_wait(&full[k % ST], (k / ST) & 1, a.wait_ns)) {
@@ -325,24 +325,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     open2(part_sum, &s0, &s1);
     sum = fmaf(sum, m > -INFINITY ? ex2((m - ref) * kLog2e) : 1.f, s0 + s1);
     m = mn;
-    bool over = false;
-    float least = tau;
-    if (v0 == lo) {
-      // the first tile: K maxima reach t, and those that do are listed
-      const uint32_t t = block_reached(top > -INFINITY ? ord32(top) : 0u, a.K, red);
-      if (t) tau = unord32(t);
-      least = t ? tau : -FLT_MAX;  // 0: fewer than K threads hold tokens
-    }
-    if (top >= least) {
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        if (g8[g] > least || (v0 == lo && g8[g] == least)) {
-          const int at = atomicAdd(&listed, 1);
-          list[at] = key_of(g8[g], v0 + (g * kThreads + tid) * 8);
-          over |= at >= kLong;
-        }
-      }
-    }
+    const uint32_t wt = warp_rth(m > -INFINITY ? ord32(m) : 0u, (a.K + kWarps - 1) / kWarps);
+    if (lane == 0) red[k & 1][wid] = wt;
     const bool full_list = __syncthreads_or(over);
     // every thread has the tile in registers: its stage takes the next
     if (stop[k & 1]) break;
@@ -350,15 +334,23 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     if (full_list) {
       cut_back(list, kept, listed, a.K, all, &rth, &listed);
       tau = fmaxf(tau, unord32((uint32_t)(rth >> 32)));
-    } else if (v0 == lo && lo + kBeamTile < hi) {
-      const int n = listed;
-      uint32_t t;
-      if (n > 2 * a.K) {
-        trim(list, kept, n, a.K, red, &listed, &t);
-        if (t) tau = fmaxf(tau, unord32(t));
-      }
-      __syncthreads();
     }
+    uint32_t reached = red[k & 1][0];   // 0: fewer than K threads hold tokens
+#pragma unroll
+    for (int q = 1; q < kWarps; ++q) reached = min(reached, red[k & 1][q]);
+    const float now = reached ? fmaxf(tau, unord32(reached)) : tau;
+    over = false;
+    if (top > tau && top >= now) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        if (g8[g] > tau && g8[g] >= now) {
+          const int at = atomicAdd(&listed, 1);
+          list[at] = key_of(g8[g], v0 + (g * kThreads + tid) * 8);
+          over |= at >= kLong;
+        }
+      }
+    }
+    tau = now;
   }
   // no copy may be in flight when the CTA exits (all have landed already unless a wait gave up)
   for (int k = max(0, issued - ST); k < issued; ++k)
@@ -382,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     a.stat[slot] = make_float2(top, (float)t);
   }
   // the K best groups, then their tokens
-  int n = shorten(list, kept, listed, a.K, red, all, &rth, &listed);
+  int n = shorten(list, kept, listed, a.K, red[0], all, &rth, &listed);
   __syncthreads();
   if (n > a.K) {
     for (int i = tid; i < n; i += kThreads) {
@@ -404,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     if (y > -INFINITY) kept[atomicAdd(&listed, 1)] = key_of(y, v);
   }
   __syncthreads();
-  n = shorten(kept, list, listed, a.K, red, all, &rth, &listed);
+  n = shorten(kept, list, listed, a.K, red[0], all, &rth, &listed);
   int2* out = a.cand + slot * a.K;
   for (int i = tid; i < n; i += kThreads) {
     const u64 key = kept[i];
