@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
   __shared__ uint64_t full[ST];
   __shared__ uint32_t red[2][kWarps];
   __shared__ float redm[kWarps], reds[kWarps];
-  __shared__ int listed, stop[2];   // stop: by the tile's parity (a thread may be one barrier ahead)
+  __shared__ int listed, found, stop[2];   // stop: by the tile's parity (a thread may be one barrier ahead)
   const int part = blockIdx.x, row = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   if (tid == 0) {
@@ -325,8 +325,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     open2(part_sum, &s0, &s1);
     sum = fmaf(sum, m > -INFINITY ? ex2((m - ref) * kLog2e) : 1.f, s0 + s1);
     m = mn;
-    const uint32_t wt = warp_rth(m > -INFINITY ? ord32(m) : 0u, (a.K + kWarps - 1) / kWarps);
-    if (lane == 0) red[k & 1][wid] = wt;
+    const bool sharpen = k < 2 || (k & 3) == 0;   // (the maxima change ever more slowly)
+    if (sharpen) {
+      const uint32_t wt = warp_rth(m > -INFINITY ? ord32(m) : 0u, (a.K + kWarps - 1) / kWarps);
+      if (lane == 0) red[k & 1][wid] = wt;
+    }
     const bool full_list = __syncthreads_or(over);
     // every thread has the tile in registers: its stage takes the next
     if (stop[k & 1]) break;
@@ -335,10 +338,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
       cut_back(list, kept, listed, a.K, all, &rth, &listed);
       tau = fmaxf(tau, unord32((uint32_t)(rth >> 32)));
     }
-    uint32_t reached = red[k & 1][0];   // 0: fewer than K threads hold tokens
+    float now = tau;
+    if (sharpen) {
+      uint32_t reached = red[k & 1][0];   // 0: fewer than K threads hold tokens
 #pragma unroll
-    for (int q = 1; q < kWarps; ++q) reached = min(reached, red[k & 1][q]);
-    const float now = reached ? fmaxf(tau, unord32(reached)) : tau;
+      for (int q = 1; q < kWarps; ++q) reached = min(reached, red[k & 1][q]);
+      if (reached) now = fmaxf(tau, unord32(reached));
+    }
     over = false;
     if (top > tau && top >= now) {
 #pragma unroll
@@ -362,41 +368,60 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     redm[wid] = wm;
     reds[wid] = ws;
   }
+  if (tid == 0) found = 0;
   __syncthreads();
   const size_t slot = (size_t)row * a.parts + part;
-  if (tid == 0) {
-    float top = -INFINITY;
-    for (int q = 0; q < kWarps; ++q) top = fmaxf(top, redm[q]);
-    double t = 0.0;
-    for (int q = 0; q < kWarps; ++q)
-      if (redm[q] > -INFINITY || reds[q] != reds[q])
-        t += (double)reds[q] * (double)(redm[q] > -INFINITY ? ex2((redm[q] - top) * kLog2e) : 1.f);
-    a.stat[slot] = make_float2(top, (float)t);
+  if (wid == 0) {
+    const float pm = lane < kWarps ? redm[lane] : -INFINITY, ps = lane < kWarps ? reds[lane] : 0.f;
+    const float top = warp_max(pm);
+    double t = (double)(pm > -INFINITY ? ps * ex2((pm - top) * kLog2e) : ps != ps ? ps : 0.f);
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) a.stat[slot] = make_float2(top, (float)t);
   }
-  // the K best groups, then their tokens
-  int n = shorten(list, kept, listed, a.K, red[0], all, &rth, &listed);
+  // K groups reach tau, so the K best tokens do: those of the listed groups,
+  // read again
+  int n = listed;
+  for (int i = tid; i < 8 * n; i += kThreads) {
+    const u64 group = list[i >> 3];
+    if (unord32((uint32_t)(group >> 32)) < tau) continue;
+    const int v = (int)~(uint32_t)group + (i & 7);
+    const float y = v < hi ? Elem<T>::to_f(x[v]) : -INFINITY;
+    if (y > -INFINITY && y >= tau) {
+      const int at = atomicAdd(&found, 1);
+      if (at < kListed) kept[at] = key_of(y, v);
+    }
+  }
   __syncthreads();
-  if (n > a.K) {
-    for (int i = tid; i < n; i += kThreads) {
-      const u64 key = list[i];
-      int rank = 0;
+  if (found <= kFew) {
+    n = found;
+  } else {
+    // many equal values: the K best groups by value and then the lower token,
+    // then their tokens
+    n = shorten(list, kept, n, a.K, red[0], all, &rth, &listed);
+    __syncthreads();
+    if (n > a.K) {
+      for (int i = tid; i < n; i += kThreads) {
+        const u64 key = list[i];
+        int rank = 0;
 #pragma unroll 8
-      for (int q = 0; q < n; ++q) rank += list[q] > key;
-      if (rank < a.K) kept[rank] = key;
+        for (int q = 0; q < n; ++q) rank += list[q] > key;
+        if (rank < a.K) kept[rank] = key;
+      }
+      __syncthreads();
+      n = a.K;
+      for (int i = tid; i < n; i += kThreads) list[i] = kept[i];
+    }
+    if (tid == 0) listed = 0;
+    __syncthreads();
+    for (int i = tid; i < 8 * n; i += kThreads) {
+      const int v = (int)~(uint32_t)list[i >> 3] + (i & 7);
+      const float y = v < hi ? Elem<T>::to_f(x[v]) : -INFINITY;
+      if (y > -INFINITY) kept[atomicAdd(&listed, 1)] = key_of(y, v);
     }
     __syncthreads();
-    n = a.K;
-    for (int i = tid; i < n; i += kThreads) list[i] = kept[i];
+    n = shorten(kept, list, listed, a.K, red[0], all, &rth, &listed);
   }
-  if (tid == 0) listed = 0;
-  __syncthreads();
-  for (int i = tid; i < 8 * n; i += kThreads) {
-    const int v = (int)~(uint32_t)list[i >> 3] + (i & 7);
-    const float y = v < hi ? Elem<T>::to_f(x[v]) : -INFINITY;
-    if (y > -INFINITY) kept[atomicAdd(&listed, 1)] = key_of(y, v);
-  }
-  __syncthreads();
-  n = shorten(kept, list, listed, a.K, red[0], all, &rth, &listed);
   int2* out = a.cand + slot * a.K;
   for (int i = tid; i < n; i += kThreads) {
     const u64 key = kept[i];
