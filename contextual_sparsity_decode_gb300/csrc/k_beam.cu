@@ -67,17 +67,35 @@ __device__ __forceinline__ uint32_t warp_rth(uint32_t v, int r) {
     if (v == top) v = 0;
   }
 }
-// A value that at least r of the block's values reach, not far below the r-th
-// largest: each warp's share of r, the least over the warps.  One barrier; `red`
-// may be used again after the next.
-__device__ __forceinline__ uint32_t block_reached(uint32_t v, int r, uint32_t* red) {
-  const uint32_t t = warp_rth(v, (r + kWarps - 1) / kWarps);
+// A value that at least K of the block's values reach, not far below the K-th
+// largest, in two steps: each warp's r-th largest, and the j-th largest of
+// those, r j >= K.  With j near 2/3 of the warps about 1.7 K values of random
+// input reach it; the least of all warps' (j = their number) lets three times
+// as many through.
+struct Reach {
+  int r, j;
+  __device__ __forceinline__ explicit Reach(int K) {
+    constexpr int kMost = kWarps * 2 / 3;
+    r = (K + kMost - 1) / kMost;
+    j = (K + r - 1) / r;
+  }
+  // a warp's share, to be stored in red[] by lane 0 ...
+  __device__ __forceinline__ uint32_t share(uint32_t v) const { return warp_rth(v, r); }
+  // ... and the answer, after a barrier; 0 where fewer values are not 0
+  __device__ __forceinline__ uint32_t value(const uint32_t* red) const {
+    const uint32_t mine = red[threadIdx.x % kWarps];
+    int above = 0;
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) above += red[q] > mine;
+    return __reduce_min_sync(0xffffffffu, above < j ? mine : ~0u);
+  }
+};
+__device__ __forceinline__ uint32_t block_reached(uint32_t v, int K, uint32_t* red) {
+  const Reach reach(K);
+  const uint32_t t = reach.share(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
   __syncthreads();
-  uint32_t least = red[0];
-#pragma unroll
-  for (int q = 1; q < kWarps; ++q) least = min(least, red[q]);
-  return least;
+  return reach.value(red);
 }
 // The r-th largest of the block's values; 0 where fewer are not 0.  Starts and
 // ends with a barrier.
@@ -285,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     while (issued < min(ST, tiles)) issue(issued++);
   float m = -INFINITY, sum = 0.f, tau = -INFINITY;
   bool over = false;
+  const Reach reach(a.K);
   for (int k = 0; k < tiles; ++k) {
     const int v0 = lo + k * kBeamTile;
     if (!tc::mbar_try_wait(&full[k % ST], (k / ST) & 1) && !tc::mbar_wait(&full[k % ST], (k / ST) & 1, a.wait_ns)) {
@@ -310,24 +329,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
       g8[g] = max3(max3(max3(x8[0], x8[1], x8[2]), x8[3], x8[4]), max3(x8[5], x8[6], x8[7]), -INFINITY);
     }
     const float top = fmaxf(g8[0], g8[1]);
-    // the sum is kept relative to the thread's maximum; a NaN or +inf among
-    // the tokens makes it a NaN
+    // the sum is kept relative to the thread's maximum (the difference first: a
+    // logit may be the type's lowest value); a NaN or +inf among the tokens
+    // makes it a NaN
     const float mn = fmaxf(m, top), ref = mn > -INFINITY ? mn : 0.f;
-    u64 part_sum = 0;
-    const u64 minus = pack2(-ref, -ref), scale = pack2(kLog2e, kLog2e);
+    float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 8 * kGroups; i += 2) {
-      float d0, d1;
-      open2(mul2(add2(pack2(f[i], f[i + 1]), minus), scale), &d0, &d1);
-      part_sum = add2(part_sum, pack2(ex2(d0), ex2(d1)));
-    }
-    float s0, s1;
-    open2(part_sum, &s0, &s1);
-    sum = fmaf(sum, m > -INFINITY ? ex2((m - ref) * kLog2e) : 1.f, s0 + s1);
+    for (int i = 0; i < 8 * kGroups; ++i) s4[i & 3] += ex2((f[i] - ref) * kLog2e);
+    sum = fmaf(sum, m > -INFINITY ? ex2((m - ref) * kLog2e) : 1.f, (s4[0] + s4[1]) + (s4[2] + s4[3]));
     m = mn;
-    const bool sharpen = k < 2 || (k & 3) == 0;   // (the maxima change ever more slowly)
+    const bool sharpen = k < 4 || (k & 3) == 0;   // (the maxima change ever more slowly)
     if (sharpen) {
-      const uint32_t wt = warp_rth(m > -INFINITY ? ord32(m) : 0u, (a.K + kWarps - 1) / kWarps);
+      const uint32_t wt = reach.share(m > -INFINITY ? ord32(m) : 0u);
       if (lane == 0) red[k & 1][wid] = wt;
     }
     const bool full_list = __syncthreads_or(over);
@@ -340,21 +353,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     }
     float now = tau;
     if (sharpen) {
-      uint32_t reached = red[k & 1][0];   // 0: fewer than K threads hold tokens
-#pragma unroll
-      for (int q = 1; q < kWarps; ++q) reached = min(reached, red[k & 1][q]);
+      const uint32_t reached = reach.value(red[k & 1]);   // 0: fewer than K threads hold tokens
       if (reached) now = fmaxf(tau, unord32(reached));
     }
+    // one atomic for a warp's groups
     over = false;
-    if (top > tau && top >= now) {
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        if (g8[g] > tau && g8[g] >= now) {
-          const int at = atomicAdd(&listed, 1);
-          list[at] = key_of(g8[g], v0 + (g * kThreads + tid) * 8);
-          over |= at >= kLong;
-        }
-      }
+    static_assert(kGroups == 2, "two ballots");
+    const uint32_t hit0 = __ballot_sync(0xffffffffu, g8[0] > tau && g8[0] >= now);
+    const uint32_t hit1 = __ballot_sync(0xffffffffu, g8[1] > tau && g8[1] >= now);
+    if (hit0 | hit1) {
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&listed, __popc(hit0) + __popc(hit1));
+      at = __shfl_sync(0xffffffffu, at, 0);
+      const uint32_t below = (1u << lane) - 1;
+      const int at1 = at + __popc(hit0) + __popc(hit1 & below);
+      at += __popc(hit0 & below);
+      if ((hit0 >> lane) & 1) list[at] = key_of(g8[0], v0 + tid * 8);
+      if ((hit1 >> lane) & 1) list[at1] = key_of(g8[1], v0 + (kThreads + tid) * 8);
+      over = at1 >= kLong;   // (the warp's last entry is at or before its highest at1)
     }
     tau = now;
   }

@@ -573,6 +573,11 @@ def test_beam_rows_without_finite_candidates(dt):
     _beam_check(x, cum, K)
     x[5] = -inf                        # nothing at all
     _beam_check(x, cum, K)
+    low = x.clone()                    # masked with the type's lowest value instead, a whole row of it too
+    low[3, :, 3:] = torch.finfo(DT[dt]).min
+    low[2, 2] = torch.finfo(DT[dt]).min
+    low[1, 0, 7] = torch.finfo(DT[dt]).max / 2
+    _beam_check(low, cum, K)
     for end in (0, 7, 299):            # ended beams: one candidate each, then -inf from the lowest token on
         _beam_check(x, cum, K, torch.ones(6, 3, dtype=torch.uint8, device="cuda"), end)
 
