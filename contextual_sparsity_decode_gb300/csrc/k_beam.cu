@@ -13,10 +13,10 @@
 //   scan  a CTA walks a part of a row in tiles of kBeamTile tokens, which bulk
 //         copies bring into a ring of shared memory (register loads one tile
 //         ahead streamed 2.4 TB/s): a running maximum and sum of exponentials
-//         per thread, and the groups of 8 tokens whose maximum may be among
-//         the K largest: the K best groups, by maximum and then the lower
-//         token, hold the K best tokens (each group left out is preceded by K
-//         tokens of others).  The threads' running maxima give a value tau
+//         per thread, and the groups of 8 tokens (kThreads apart) whose maximum
+//         may be among the K largest: the K best groups, by maximum and then
+//         its lowest token, hold the K best tokens (each group left out is
+//         preceded by K tokens of others).  The threads' running maxima give a value tau
 //         that K groups reach, sharper with every tile; a group is listed if
 //         its maximum is above the tau before its tile (an equal one comes
 //         after K others) and reaches the one with it: about K / k groups of
@@ -40,9 +40,11 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroups = 2;                    // groups of 8 tokens per thread and tile
 static_assert(kThreads * kGroups * 8 == kBeamTile, "tokens per tile");
-constexpr int kLong = 512;                    // a list longer than this is cut back
-constexpr int kListed = kLong + kBeamTile / 8;  // a tile's groups always fit behind it
+constexpr int kLong = 64;                      // a warp's list longer than this: all are cut back
+constexpr int kMine = kLong + 32 * kGroups;    // a warp's list: a tile's groups always fit behind
+constexpr int kListed = kWarps * kMine;
 static_assert(kListed >= kBeamMaxK * 8, "the best groups' tokens fit too");
+static_assert(kBeamMaxK * kListed / kThreads <= 32 * kWarps, "what is left of a list is dealt out 32 to a warp");
 constexpr int kFew = 256;                     // entries ranked against each other directly
 constexpr int kJoinListed = 1024;
 typedef unsigned long long u64;
@@ -69,13 +71,12 @@ __device__ __forceinline__ uint32_t warp_rth(uint32_t v, int r) {
 }
 // A value that at least K of the block's values reach, not far below the K-th
 // largest, in two steps: each warp's r-th largest, and the j-th largest of
-// those, r j >= K.  With j near 2/3 of the warps about 1.7 K values of random
-// input reach it; the least of all warps' (j = their number) lets three times
-// as many through.
+// those, r j >= K (for K = 4 the fourth of the warps' maxima; the least of all
+// warps' would let ten times as many values through).
 struct Reach {
   int r, j;
   __device__ __forceinline__ explicit Reach(int K) {
-    constexpr int kMost = kWarps * 2 / 3;
+    constexpr int kMost = kWarps - 1;
     r = (K + kMost - 1) / kMost;
     j = (K + r - 1) / r;
   }
@@ -112,44 +113,6 @@ __device__ __forceinline__ U block_rth(U v, int r, U* all, U* result) {
   __syncthreads();
   return *result;
 }
-
-// Eight consecutive tokens that begin `off` bytes behind a 16-byte boundary of
-// shared memory, cut out of the aligned vectors that cover them.
-template <typename T>
-struct Raw8 {
-  static constexpr int kVecs = sizeof(T) * 8 / 16;
-  // the words from byte 4 WORDS + bits / 8 on
-  template <int WORDS>
-  static __device__ __forceinline__ void cut(const uint4* p, uint32_t bits, float* f) {
-    uint4 x[kVecs + 1];
-#pragma unroll
-    for (int i = 0; i <= kVecs; ++i) x[i] = p[i];
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
-    uint32_t y[4 * kVecs];
-#pragma unroll
-    for (int i = 0; i < 4 * kVecs; ++i)
-      y[i] = __funnelshift_r(w[i + WORDS], w[i + WORDS + 1 < 4 * kVecs + 4 ? i + WORDS + 1 : 0], bits);
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      unpack<T>(make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]), f + i * Elem<T>::kVec);
-  }
-  static __device__ __forceinline__ void open(const uint4* p, uint32_t off, float* f) {
-    const uint32_t bits = (off & 3u) * 8;
-    switch (off >> 2) {
-      case 0:
-        if (bits == 0) {
-#pragma unroll
-          for (int i = 0; i < kVecs; ++i) unpack<T>(p[i], f + i * Elem<T>::kVec);
-        } else {
-          cut<0>(p, bits, f);
-        }
-        break;
-      case 1: cut<1>(p, bits, f); break;
-      case 2: cut<2>(p, bits, f); break;
-      default: cut<3>(p, bits, f); break;
-    }
-  }
-};
 
 // A candidate of the join: its score as an order-preserving integer, and where
 // it is.  Comparing integers keeps double-precision work, slow on this GPU, to
@@ -197,18 +160,18 @@ __device__ __forceinline__ void put(const BeamLaunch& a, int s, int k, const Can
   a.beam[(size_t)s * a.K + k] = c.w;
 }
 
-// Cuts a list of n entries back to those that reach the K-th largest of the
-// thread maxima over it (the K-th largest entry where n <= kThreads); returns
-// the new length.
+// Cuts a list of n entries (0: none) back to those that reach the K-th largest
+// of the thread maxima over it (the K-th largest entry where n <= kThreads);
+// returns the new length, at most K ceil(n / kThreads).
 __device__ __noinline__ int cut_back(u64* list, u64* kept, int n, int K, u64* all, u64* result, int* listed) {
   u64 best = 0;
   for (int i = threadIdx.x; i < n; i += kThreads) best = list[i] > best ? list[i] : best;
   const u64 t = block_rth<u64>(best, K, all, result);
   if (threadIdx.x == 0) *listed = 0;
   __syncthreads();
-  if (best >= t)
+  if (best && best >= t)
     for (int i = threadIdx.x; i < n; i += kThreads)
-      if (list[i] >= t) kept[atomicAdd(listed, 1)] = list[i];
+      if (list[i] && list[i] >= t) kept[atomicAdd(listed, 1)] = list[i];
   __syncthreads();
   n = *listed;
   for (int i = threadIdx.x; i < n; i += kThreads) list[i] = kept[i];
@@ -216,33 +179,10 @@ __device__ __noinline__ int cut_back(u64* list, u64* kept, int n, int K, u64* al
   return n;
 }
 
-// The same with a threshold that costs a tenth and keeps perhaps twice as many
-// (by value alone: runs of equal values stay); *t: the threshold.
-__device__ __forceinline__ int trim(u64* list, u64* kept, int n, int K, uint32_t* red, int* listed, uint32_t* t) {
-  const int i0 = (threadIdx.x & 31) * kWarps + (threadIdx.x >> 5);  // every warp gets its share of a short list
-  uint32_t best = 0;
-  for (int i = i0; i < n; i += kThreads) best = max(best, (uint32_t)(list[i] >> 32));
-  __syncthreads();
-  *t = block_reached(best, K, red);
-  if (threadIdx.x == 0) *listed = 0;
-  __syncthreads();
-  if (best >= *t)
-    for (int i = i0; i < n; i += kThreads)
-      if ((uint32_t)(list[i] >> 32) >= *t) kept[atomicAdd(listed, 1)] = list[i];
-  __syncthreads();
-  n = *listed;
-  for (int i = threadIdx.x; i < n; i += kThreads) list[i] = kept[i];
-  __syncthreads();
-  return n;
-}
-
-// The list's length brought down to near K (at most kFew).
-__device__ __forceinline__ int shorten(u64* list, u64* kept, int n, int K, uint32_t* red, u64* all, u64* result,
-                                       int* listed) {
-  uint32_t t;
-  if (n > 2 * K && n > 32) n = trim(list, kept, n, K, red, listed, &t);
-  while (n > kFew) n = cut_back(list, kept, n, K, all, result, listed);  // at most K ceil(n / kThreads) stay
-  return n;
+// Token e of the group that token v (counted from the part's first) is in.
+__device__ __forceinline__ int group_token(int v, int e) {
+  constexpr int kSpan = 8 * kThreads;
+  return v / kSpan * kSpan + v % kThreads + e * kThreads;
 }
 
 template <typename T>
@@ -281,46 +221,48 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
   const uint32_t off = reinterpret_cast<uintptr_t>(x) & 15u;
   const int lo = part * a.part_tiles * kBeamTile, hi = min(a.V, lo + a.part_tiles * kBeamTile);
   const int tiles = (hi - lo + kBeamTile - 1) / kBeamTile;
-  // Copies begin and end on 16-byte boundaries and stay within the logits'
-  // memory [first, last): groups of tokens outside [g_lo, g_hi), at its very
-  // ends or at the row's, are read token by token instead.
+  // Rows begin at any address.  Copies begin and end on 16-byte boundaries and
+  // stay within the logits' memory [first, last); the few tokens at its very
+  // ends that they cannot bring are stored one by one.
   const char* begin = reinterpret_cast<const char*>(x) - off;
-  const int skip = begin < first ? 16 : 0;     // the first vector begins before the logits
-  const int g_lo = skip ? 8 : 0;
+  const int skip = begin < first ? 16 : 0;        // the first vector begins before the logits
   const long long room = (last - begin) & ~15LL;  // bytes of whole vectors from `begin` on
-  const int g_hi = min(hi, (int)min((long long)a.V, (room - (long long)off) / (long long)sizeof(T))) - 7;
-  const auto issue = [&](int k) {   // tile k's copy, by one thread
-    const long long b0 = (long long)(lo + k * kBeamTile) * sizeof(T);  // from `begin`: a multiple of 16
-    long long b1 = b0 + off + (long long)min(kBeamTile, hi - lo - k * kBeamTile) * sizeof(T);
-    b1 = min((b1 + 15) & ~15LL, room);
+  const auto issue = [&](int k) {                 // tile k, by one thread
+    const int t0 = lo + k * kBeamTile, n = min(kBeamTile, hi - t0);
+    const long long b0 = (long long)t0 * sizeof(T);  // from `begin`: a multiple of 16
+    const long long b1 = min((b0 + off + (long long)n * sizeof(T) + 15) & ~15LL, room);
     const int cut = b0 == 0 ? skip : 0;
-    const long long bytes = max(0LL, b1 - b0 - cut);
-    tc::mbar_arrive_expect_tx(&full[k % ST], (uint32_t)bytes);
-    if (bytes) tc::bulk_g2s(ring + (k % ST) * Ring<T>::kBytes + cut, begin + b0 + cut, (uint32_t)bytes, &full[k % ST]);
+    const uint32_t bytes = (uint32_t)max(0LL, b1 - b0 - cut);
+    uint8_t* stage = ring + (k % ST) * Ring<T>::kBytes;
+    T* tokens = reinterpret_cast<T*>(stage + off);
+    if (cut)
+      for (int e = 0; e < n && off + (e + 1) * sizeof(T) <= 16; ++e) tokens[e] = x[e];
+    for (int e = n - 1; e >= 0 && b0 + off + (long long)(e + 1) * sizeof(T) > b1; --e) tokens[e] = x[t0 + e];
+    tc::mbar_arrive_expect_tx(&full[k % ST], bytes);
+    if (bytes) tc::bulk_g2s(stage + cut, begin + b0 + cut, bytes, &full[k % ST]);
   };
   int issued = 0;
   if (tid == 0)
     while (issued < min(ST, tiles)) issue(issued++);
+  __syncthreads();  // (tokens stored one by one)
   float m = -INFINITY, sum = 0.f, tau = -INFINITY;
   bool over = false;
+  int mine = 0;   // entries of the warp's list
   const Reach reach(a.K);
   for (int k = 0; k < tiles; ++k) {
     const int v0 = lo + k * kBeamTile;
-    if (!tc::mbar_try_wait(&full[k % ST], (k / ST) & 1) && !tc::mbar_wait(&full[k % ST], (k / ST) & 1, a.wait_ns)) {
+    if (lane == 0 && !tc::mbar_wait_soon(&full[k % ST], (k / ST) & 1, a.wait_ns)) {  // one lane polls
       stop[k & 1] = 1;
       set_error(a.hdr, DV_ERR_TIMEOUT, 51);
     }
-    const uint8_t* tile = ring + (k % ST) * Ring<T>::kBytes;
-    float f[8 * kGroups];
+    __syncwarp();
+    const T* tile = reinterpret_cast<const T*>(ring + (k % ST) * Ring<T>::kBytes + off) + tid;
+    float f[8 * kGroups];   // tokens v0 + tid + i kThreads
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int v = v0 + (g * kThreads + tid) * 8;
-      if (v >= g_lo && v < g_hi) {
-        Raw8<T>::open(reinterpret_cast<const uint4*>(tile + (size_t)(g * kThreads + tid) * 8 * sizeof(T)), off, f + 8 * g);
-      } else {
+    for (int i = 0; i < 8 * kGroups; ++i) f[i] = Elem<T>::to_f(tile[i * kThreads]);
+    if (v0 + kBeamTile > hi) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[8 * g + e] = v + e < hi ? Elem<T>::to_f(x[v + e]) : -INFINITY;
-      }
+      for (int i = 0; i < 8 * kGroups; ++i) f[i] = v0 + tid + i * kThreads < hi ? f[i] : -INFINITY;
     }
     float g8[kGroups];
 #pragma unroll
@@ -348,35 +290,45 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     if (stop[k & 1]) break;
     if (tid == 0 && k + ST < tiles) issue(issued++);
     if (full_list) {
-      cut_back(list, kept, listed, a.K, all, &rth, &listed);
+      for (int i = mine + lane; i < kMine; i += 32) list[wid * kMine + i] = 0;
+      __syncthreads();
+      const int n = cut_back(list, kept, kListed, a.K, all, &rth, &listed);
       tau = fmaxf(tau, unord32((uint32_t)(rth >> 32)));
+      // dealt out again, 32 to a warp (n <= K kListed / kThreads)
+      __syncthreads();
+      mine = min(max(n - wid * 32, 0), 32);
+      if (lane < mine) list[wid * kMine + lane] = kept[wid * 32 + lane];
+      __syncwarp();
     }
     float now = tau;
     if (sharpen) {
       const uint32_t reached = reach.value(red[k & 1]);   // 0: fewer than K threads hold tokens
       if (reached) now = fmaxf(tau, unord32(reached));
     }
-    // one atomic for a warp's groups
-    over = false;
     static_assert(kGroups == 2, "two ballots");
     const uint32_t hit0 = __ballot_sync(0xffffffffu, g8[0] > tau && g8[0] >= now);
     const uint32_t hit1 = __ballot_sync(0xffffffffu, g8[1] > tau && g8[1] >= now);
     if (hit0 | hit1) {
-      int at = 0;
-      if (lane == 0) at = atomicAdd(&listed, __popc(hit0) + __popc(hit1));
-      at = __shfl_sync(0xffffffffu, at, 0);
+      u64* at = list + wid * kMine + mine;
       const uint32_t below = (1u << lane) - 1;
-      const int at1 = at + __popc(hit0) + __popc(hit1 & below);
-      at += __popc(hit0 & below);
-      if ((hit0 >> lane) & 1) list[at] = key_of(g8[0], v0 + tid * 8);
-      if ((hit1 >> lane) & 1) list[at1] = key_of(g8[1], v0 + (kThreads + tid) * 8);
-      over = at1 >= kLong;   // (the warp's last entry is at or before its highest at1)
+      int i0 = 7, i1 = 15;   // the lowest tokens that hold the maxima
+#pragma unroll
+      for (int i = 6; i >= 0; --i) {
+        if (f[i] == g8[0]) i0 = i;
+        if (f[8 + i] == g8[1]) i1 = 8 + i;
+      }
+      if ((hit0 >> lane) & 1) at[__popc(hit0 & below)] = key_of(g8[0], v0 + tid + i0 * kThreads);
+      if ((hit1 >> lane) & 1) at[__popc(hit0) + __popc(hit1 & below)] = key_of(g8[1], v0 + tid + i1 * kThreads);
+      mine += __popc(hit0) + __popc(hit1);
     }
+    over = mine > kLong;
     tau = now;
   }
-  // no copy may be in flight when the CTA exits (all have landed already unless a wait gave up)
-  for (int k = max(0, issued - ST); k < issued; ++k)
-    if (!tc::mbar_wait(&full[k % ST], (k / ST) & 1, kUnwindNs > a.wait_ns ? kUnwindNs : a.wait_ns)) break;
+  // No copy may be in flight when the CTA exits.  (Unless a wait gave up, all
+  // have been waited for.)
+  if (stop[0] | stop[1])
+    for (int k = max(0, issued - ST); k < issued; ++k)
+      if (!tc::mbar_wait(&full[k % ST], (k / ST) & 1, kUnwindNs > a.wait_ns ? kUnwindNs : a.wait_ns)) break;
   // the part's maximum and sum
   const float wm = warp_max(m);
   const float ws = warp_sum(m > -INFINITY ? sum * ex2((m - wm) * kLog2e) : sum != sum ? sum : 0.f);
@@ -390,18 +342,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
   if (wid == 0) {
     const float pm = lane < kWarps ? redm[lane] : -INFINITY, ps = lane < kWarps ? reds[lane] : 0.f;
     const float top = warp_max(pm);
-    double t = (double)(pm > -INFINITY ? ps * ex2((pm - top) * kLog2e) : ps != ps ? ps : 0.f);
+    float t = pm > -INFINITY ? ps * ex2((pm - top) * kLog2e) : ps != ps ? ps : 0.f;
 #pragma unroll
     for (int o = kWarps / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (lane == 0) a.stat[slot] = make_float2(top, (float)t);
+    if (lane == 0) a.stat[slot] = make_float2(top, t);
   }
   // K groups reach tau, so the K best tokens do: those of the listed groups,
-  // read again
-  int n = listed;
-  for (int i = tid; i < 8 * n; i += kThreads) {
-    const u64 group = list[i >> 3];
+  // read again, each warp its own
+  __syncwarp();
+  for (int i = lane; i < 8 * mine; i += 32) {
+    const u64 group = list[wid * kMine + (i >> 3)];
     if (unord32((uint32_t)(group >> 32)) < tau) continue;
-    const int v = (int)~(uint32_t)group + (i & 7);
+    const int v = group_token(~(uint32_t)group - lo, i & 7) + lo;
     const float y = v < hi ? Elem<T>::to_f(x[v]) : -INFINITY;
     if (y > -INFINITY && y >= tau) {
       const int at = atomicAdd(&found, 1);
@@ -409,34 +361,33 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     }
   }
   __syncthreads();
-  if (found <= kFew) {
-    n = found;
-  } else {
+  int n = found;
+  if (n > kFew) {
     // many equal values: the K best groups by value and then the lower token,
     // then their tokens
-    n = shorten(list, kept, n, a.K, red[0], all, &rth, &listed);
+    for (int i = mine + lane; i < kMine; i += 32) list[wid * kMine + i] = 0;
     __syncthreads();
-    if (n > a.K) {
-      for (int i = tid; i < n; i += kThreads) {
-        const u64 key = list[i];
-        int rank = 0;
+    n = cut_back(list, kept, kListed, a.K, all, &rth, &listed);
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 key = list[i];
+      int rank = 0;
 #pragma unroll 8
-        for (int q = 0; q < n; ++q) rank += list[q] > key;
-        if (rank < a.K) kept[rank] = key;
-      }
-      __syncthreads();
-      n = a.K;
-      for (int i = tid; i < n; i += kThreads) list[i] = kept[i];
+      for (int q = 0; q < n; ++q) rank += list[q] > key;
+      if (rank < a.K) kept[rank] = key;
     }
+    __syncthreads();
+    n = min(n, a.K);
+    for (int i = tid; i < n; i += kThreads) list[i] = kept[i];
     if (tid == 0) listed = 0;
     __syncthreads();
     for (int i = tid; i < 8 * n; i += kThreads) {
-      const int v = (int)~(uint32_t)list[i >> 3] + (i & 7);
+      const int v = group_token(~(uint32_t)list[i >> 3] - lo, i & 7) + lo;
       const float y = v < hi ? Elem<T>::to_f(x[v]) : -INFINITY;
       if (y > -INFINITY) kept[atomicAdd(&listed, 1)] = key_of(y, v);
     }
     __syncthreads();
-    n = shorten(kept, list, listed, a.K, red[0], all, &rth, &listed);
+    n = listed;
+    if (n > kFew) n = cut_back(kept, list, n, a.K, all, &rth, &listed);
   }
   int2* out = a.cand + slot * a.K;
   for (int i = tid; i < n; i += kThreads) {

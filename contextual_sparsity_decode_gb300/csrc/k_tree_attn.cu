@@ -531,20 +531,33 @@ struct TcSizes {
 
 // A wait that ends: at its phase, when another wait of the CTA gave up, or at
 // the limit (recorded as DV_ERR_TIMEOUT; the CTA then unwinds, its results
-// being void).  Returns whether the phase was reached.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* stop, const TreeArgs& a,
-                                         int code) {
-  if (tc::mbar_try_wait(bar, parity)) return true;
+// being void).  Returns whether the phase was reached.  Only the first try is
+// inlined: the loop's dozen waits are on the path of every tile, and with their
+// slow parts in line the kernel took 168 us instead of 160.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* stop, WsHeader* hdr,
+                                       long long wait_ns, int code) {
   const unsigned long long t0 = globaltimer_ns();
   while (!tc::mbar_try_wait(bar, parity)) {
     if (*stop) return false;
-    if ((long long)(globaltimer_ns() - t0) > a.wait_ns) {
+    if ((long long)(globaltimer_ns() - t0) > wait_ns) {
       *stop = 1;
-      set_error(a.hdr, DV_ERR_TIMEOUT, code);
+      set_error(hdr, DV_ERR_TIMEOUT, code);
       return false;
     }
   }
   return true;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* stop, const TreeArgs& a,
+                                         int code) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, stop, a.hdr, a.wait_ns, code);
+}
+// The same by a converged warp (lanes may differ in their answers).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* stop, const TreeArgs& a,
+                                          int code) {
+  const bool ok = wait_bar(bar, parity, stop, a, code);
+  __syncwarp();
+  return ok;
 }
 
 template <int N>
@@ -602,6 +615,22 @@ __device__ __forceinline__ bool clean_v(uint8_t* v, const Seg& s, int j0, int ti
     found |= bad;
   }
   return found;
+}
+
+// Makes an edge tile (tile j of the segment: it holds tree nodes, or ends behind
+// the last) ready: its V rows, which are there, clean; returns the keys that the
+// row sees.  By a softmax group.  The V stage's barrier was at this tile's phase
+// or the one before when it was waited for: the product that freed the stage
+// had been.
+template <typename T, int DH>
+__device__ __forceinline__ u64 prepare_edge(const TreeLaunch& L, int b, int pos, int nodes, uint8_t* v, int j0, int t,
+                                         bool active, int* bad) {
+  Seg s{};
+  s.b = b; s.pos = pos; s.nodes = nodes; s.n = pos + nodes;
+  const u64 seen = active ? visible_keys(L, s, j0, t) : ~0ull;
+  if (clean_v<T, DH>(v, s, j0, threadIdx.x & 127)) *bad = 1;
+  tc::fence_proxy_async();
+  return seen;
 }
 
 template <typename T, int DH>
@@ -697,9 +726,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       // no copy into this CTA's shared memory may be in flight when it exits
       for (int q = max(0, kp - NK); q < kp; ++q)
-        if (!tc::mbar_wait(&kfull[q % NK], (q / NK) & 1, unwind_ns)) break;
+        if (!tc::mbar_wait_soon(&kfull[q % NK], (q / NK) & 1, unwind_ns)) break;
       for (int q = max(0, vt - NV); q < vt; ++q)
-        if (!tc::mbar_wait(&vfull[q % NV], (q / NV) & 1, unwind_ns)) break;
+        if (!tc::mbar_wait_soon(&vfull[q % NV], (q / NV) & 1, unwind_ns)) break;
     }
     __syncwarp();
   } else if (warp == 9) {  // MMA issuer
@@ -721,12 +750,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     while (cur.next(L, plan, kTreeRows, &s)) {
       if (!s.ok) continue;
       const int nt = __shfl_sync(0xffffffffu, s.k1 - s.k0, 0);
-      bool ok = wait_bar(&qfull[sg & 1], (sg >> 1) & 1, stop, a, 33);
+      bool ok = wait_warp(&qfull[sg & 1], (sg >> 1) & 1, stop, a, 33);
       const uint64_t qd = qd0 + (sg & 1) * (Z::kQBytes >> 4);
       auto issue_s = [&](bool two) {
-        if (pairs) ok &= wait_bar(&sfree, (pairs - 1) & 1, stop, a, 43);
+        if (pairs) ok &= wait_warp(&sfree, (pairs - 1) & 1, stop, a, 43);
         ++pairs;
-        ok &= wait_bar(&kfull[ks], kph, stop, a, 34);
+        ok &= wait_warp(&kfull[ks], kph, stop, a, 34);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc::fence_after_sync();
@@ -745,14 +774,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       if (ok) issue_s(nt > 1);
       // O is read to the end of the previous segment before it is begun anew
-      if (sg > 0) ok &= wait_bar(&odone, (sg - 1) & 1, stop, a, 35);
+      if (sg > 0) ok &= wait_warp(&odone, (sg - 1) & 1, stop, a, 35);
       for (int j = 0; j < nt && ok; ++j) {
         const uint32_t w = j & 1;
         // S of the next pair while the groups work on this one
         if (w == 0 && j + 2 < nt) issue_s(j + 3 < nt);
-        ok &= wait_bar(&pready[w], (p_ph >> w) & 1, stop, a, 36);
+        ok &= wait_warp(&pready[w], (p_ph >> w) & 1, stop, a, 36);
         p_ph ^= 1u << w;
-        ok &= wait_bar(&vfull[vs], vph, stop, a, 37);
+        ok &= wait_warp(&vfull[vs], vph, stop, a, 37);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc::fence_after_sync();
@@ -781,17 +810,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (tc::elect_one()) {
       tc::mma_commit(&done);  // arrives once every MMA issued above has completed
-      if (!tc::mbar_wait(&done, 0, unwind_ns)) set_error(a.hdr, DV_ERR_TIMEOUT, 38);
+      if (!tc::mbar_wait_soon(&done, 0, unwind_ns)) set_error(a.hdr, DV_ERR_TIMEOUT, 38);
     }
     __syncwarp();
   } else if (warp == 10) {  // query rows, then the rows of out that no unit writes
     constexpr int kRowChunks = DH / 8;
     int sg = 0;
-    while (!*stop && cur.next(L, plan, kTreeRows, &s)) {
+    bool go = true;
+    while (go && cur.next(L, plan, kTreeRows, &s)) {
       if (!s.ok) continue;
-      if (sg >= 2) wait_bar(&qempty[sg & 1], ((sg >> 1) - 1) & 1, stop, a, 39);
+      if (sg >= 2) go = __all_sync(0xffffffffu, wait_warp(&qempty[sg & 1], ((sg >> 1) - 1) & 1, stop, a, 39));
       uint8_t* dst = sQ + (sg & 1) * Z::kQBytes;
-      if (!*stop) {
+      if (go) {
         for (int i = lane; i < s.rows * kRowChunks; i += 32) {
           const int r = i / kRowChunks, c = i % kRowChunks;
           cp_async16(dst + (c >> 3) * (kTreeRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
@@ -823,25 +853,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool active = quad * 32 < s.rows;
       const int t = min(s.row0 + row, s.row0 + s.rows - 1) / L.g;
       float m = -INFINITY, l = 0.f;
-      // What an edge tile (one that holds tree nodes, or ends behind the last)
-      // needs besides its scores, made ready while the tile before it is in the
-      // products: the keys that the row sees, and clean V rows.  The V stage's
-      // barrier is at this tile's phase or the one before: the product that
-      // freed the stage was waited for.
+      // what an edge tile needs besides its scores is made ready while the tile
+      // before it is in the products
       bool there = true;
       const auto prepare = [&](int j) -> u64 {
-        const int j0 = (s.k0 + j) * kKeys;
-        if (j >= nt || j0 + kKeys <= s.pos) return ~0ull;
-        const u64 seen = active ? visible_keys(L, s, j0, t) : ~0ull;
+        if (j >= nt || (s.k0 + j + 1) * kKeys <= s.pos) return ~0ull;
         const int it = base + j, st = it % NV;
-        there &= wait_bar(&vfull[st], (it / NV) & 1, stop, a, 40);
-        if (clean_v<T, DH>(sV + st * Z::kTileBytes, s, j0, tid & 127)) bad_v[sg & 3] = 1;
-        tc::fence_proxy_async();
-        return seen;
+        there &= wait_warp(&vfull[st], (it / NV) & 1, stop, a, 40);
+        return prepare_edge<T, DH>(L, s.b, s.pos, s.nodes, sV + st * Z::kTileBytes, (s.k0 + j) * kKeys, t, active,
+                                   &bad_v[sg & 3]);
       };
       u64 vis = prepare(w);
       for (int j = w; j - w < nt; j += 2) {
-        there &= wait_bar(&sfull, scount & 1, stop, a, 41);
+        there &= wait_warp(&sfull, scount & 1, stop, a, 41);
         ++scount;
         if (!__all_sync(0xffffffffu, there)) break;  // the whole warp, or none of it
         if (j >= nt) {  // a pair of one tile, the other group's
@@ -856,12 +880,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc::tmem_ld_wait();
           tc::fence_before_sync();
           tc::mbar_arrive(&sfree);
-          float c = a.scale_log2;
-          if (c <= 0.f) {  // the maximum is taken before the scale
-#pragma unroll
-            for (int i = 0; i < kKeys; ++i) v[i] *= c;
-            c = 1.f;
-          }
+          const float c = a.scale_log2;
           if (__any_sync(0xffffffffu, vis != ~0ull)) {
 #pragma unroll
             for (int i = 0; i < kKeys; ++i) v[i] = (vis >> i) & 1 ? v[i] : -INFINITY;
@@ -874,7 +893,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           const float top = fmaxf(mx[0], mx[1]) * c;
           // P and O of the group's tile before are read and written
-          if (pcount) there &= wait_bar(&pdone[w], (pcount - 1) & 1, stop, a, 44);
+          if (pcount) there &= wait_warp(&pdone[w], (pcount - 1) & 1, stop, a, 44);
           __syncwarp();
           tc::fence_after_sync();
           const bool move = row < s.rows && top > m + kSlack;
@@ -927,7 +946,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // a warp without rows keeps step: it must not arrive for the next
           // tile while the others are still at this one
           tc::mbar_arrive(&sfree);
-          if (pcount) wait_bar(&pdone[w], (pcount - 1) & 1, stop, a, 44);
+          if (pcount) wait_warp(&pdone[w], (pcount - 1) & 1, stop, a, 44);
         }
         ++pcount;
         tc::fence_before_sync();
@@ -938,7 +957,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sml[sg & 1][w][row] = make_float2(m, l);
       if (tid == 0) bad_v[(sg + 2) & 3] = 0;
       group_sync<256>();
-      wait_bar(&ofull, sg & 1, stop, a, 42);
+      wait_warp(&ofull, sg & 1, stop, a, 42);
       tc::fence_after_sync();
       __syncwarp();
       const bool fix = bad_v[sg & 3] != 0;

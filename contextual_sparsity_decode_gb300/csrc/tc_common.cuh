@@ -56,6 +56,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, long l
   return true;
 }
 
+// The same, with all but the first try out of line (the loops of long kernels
+// hold many waits, and a read of the global timer takes about 1000 cycles).
+inline __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, long long limit_ns) {
+  return mbar_wait(bar, parity, limit_ns);
+}
+__device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, long long limit_ns) {
+  return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity, limit_ns);
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;

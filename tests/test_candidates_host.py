@@ -18,10 +18,10 @@ def _vp(x):
 
 
 def _tree(q=FAKE, B=2, T=5, h=4, g=1, d_h=64, K=FAKE, V=FAKE, n_max=64, pos=FAKE, nodes=FAKE, mask=FAKE, idx=FAKE,
-          cap=4, count=FAKE, dt=dv.DV_F16, out=FAKE, ws=FAKE, ws_bytes=0):
+          cap=4, count=FAKE, dt=dv.DV_F16, out=FAKE, ws=FAKE, ws_bytes=0, scale=0.125):
     kv = dv.dv_kv(K, V, None, None, n_max)
     return dv.lib().dv_tree_attn(_vp(q), B, T, h, g, d_h, ctypes.byref(kv), _vp(pos), _vp(nodes), _vp(mask), 1,
-                                 _vp(idx), cap, _vp(count), 0.125, dt, _vp(out), _vp(ws), ws_bytes, _vp(0))
+                                 _vp(idx), cap, _vp(count), scale, dt, _vp(out), _vp(ws), ws_bytes, _vp(0))
 
 
 @pytest.mark.parametrize("kw", [
@@ -29,6 +29,7 @@ def _tree(q=FAKE, B=2, T=5, h=4, g=1, d_h=64, K=FAKE, V=FAKE, n_max=64, pos=FAKE
     dict(out=FAKE + 4), dict(pos=FAKE + 2), dict(nodes=FAKE + 1), dict(idx=FAKE + 2), dict(idx=None),
     dict(count=None), dict(cap=0), dict(cap=5), dict(B=0), dict(B=513), dict(T=0), dict(T=1025), dict(h=0),
     dict(h=1025), dict(g=0), dict(g=65), dict(n_max=0), dict(n_max=40), dict(n_max=1048592),
+    dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
 ])
 def test_tree_attention_refuses_bad_arguments(kw):
     assert _tree(ws_bytes=1 << 30, **kw) == INVALID
