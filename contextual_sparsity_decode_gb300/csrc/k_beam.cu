@@ -594,7 +594,8 @@ int part_tiles(int rows, int V, int num_sms, int per_sm) {
   const long long slots = (long long)per_sm * num_sms;
   int best = tiles;
   long long least = -1;
-  for (int t = tiles; t >= 1; t -= 1 + t / 16) {  // long rows: coarser steps
+  for (int parts = 1; parts <= tiles; parts += 1 + parts / 16) {  // long rows: coarser steps
+    const int t = (tiles + parts - 1) / parts;
     const long long ctas = (long long)rows * ((tiles + t - 1) / t);
     const long long cost = (ctas + num_sms - 1) / num_sms * (t + 2) + 8 * ((ctas + slots - 1) / slots);
     if (least < 0 || cost < least) {
