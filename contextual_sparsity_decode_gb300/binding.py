@@ -118,6 +118,8 @@ def lib_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load libdv.so (building it in-tree first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()
@@ -131,14 +133,21 @@ def lib() -> ctypes.CDLL:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# the current stream's handle without a Stream object around it (a third of the
+# host's time of a small call); torch.cuda.current_stream() otherwise
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and _current_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_current_device())
         stream = torch.cuda.current_stream()
-    h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    return ctypes.c_void_p(h)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _event(ev) -> ctypes.c_void_p:
@@ -318,7 +327,7 @@ class KVLayers:
 
 
 def _laid_out(t: torch.Tensor, shape, dtype, where: str) -> None:
-    if t.shape != torch.Size(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise DvError(1, where, f"a contiguous {tuple(shape)} tensor of {dtype} is wanted")
 
 
@@ -360,24 +369,28 @@ def dv_tree_attn_workspace_size(B: int, T: int, h: int, group: int, d_h: int) ->
 def dv_tree_attn(q, kv: KV, pos, scale, out, ws, mask=None, nodes=None, head_idx=None, head_count=None, stream=None):
     """q, out [B][T][h g][d_h]; mask [T][T] or [B][T][T], bool or uint8 (None:
     a linear draft); see dv_tree_attn in dv.h."""
-    B, T, hq, d_h = q.shape
-    h = kv.K.shape[1]
     where = "dv_tree_attn"
-    shape = (B, h, kv.n_max, d_h)
-    _laid_out(q, (B, T, hq, d_h), kv.K.dtype, where)
-    _laid_out(out, (B, T, hq, d_h), kv.K.dtype, where)
-    _laid_out(kv.K, shape, kv.K.dtype, where)
-    _laid_out(kv.V, shape, kv.K.dtype, where)
+    K, V = kv.K, kv.V
+    shape, cache, dtype = q.shape, K.shape, K.dtype
+    B, T, hq, d_h = shape
+    h = cache[1]
+    _laid_out(q, shape, dtype, where)
+    _laid_out(out, shape, dtype, where)
+    _laid_out(K, (B, h, kv.n_max, d_h), dtype, where)
+    _laid_out(V, cache, dtype, where)
     if hq % h:
         raise DvError(1, where, f"{hq} query heads on {h} K/V heads")
     batched = 0
     if mask is not None:
         batched = int(mask.dim() == 3)
         _laid_out(mask, (B, T, T) if batched else (T, T), torch.bool if mask.dtype == torch.bool else torch.uint8, where)
-    c = kv.c()
-    _ok(lib().dv_tree_attn(_ptr(q), B, T, h, hq // h, d_h, ctypes.byref(c), _ptr(pos), _ptr(nodes), _ptr(mask),
-                           batched, _ptr(head_idx), 0 if head_idx is None else head_idx.shape[-1], _ptr(head_count),
-                           float(scale), _dt(q), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), where)
+    st = (_lib or lib()).dv_tree_attn(
+        q.data_ptr(), B, T, h, hq // h, d_h, dv_kv(K.data_ptr(), V.data_ptr(), None, None, kv.n_max), pos.data_ptr(),
+        _ptr(nodes), _ptr(mask), batched, _ptr(head_idx), 0 if head_idx is None else head_idx.shape[-1],
+        _ptr(head_count), scale, _DT[dtype] if dtype in _DT else _dt(q), out.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream(stream))
+    if st:
+        _ok(st, where)
 
 
 def dv_kv_compact(layers: KVLayers, pos, idx, count, ws, new_pos=None, stream=None):
