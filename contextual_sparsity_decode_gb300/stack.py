@@ -12,7 +12,12 @@ Per layer l (main stream):
     r += MHA_{S_A}(y_a)              dv_sparse_attn (append, repair, attend)
     y_m = LN(r);  r += MLP_{S_M}(y_m)    dv_layernorm, dv_sparse_mlp
 The whole token (both streams) is captured once into a CUDA graph and
-replayed.  This module only orders calls; every step runs in libdv's kernels.
+replayed.  This module only orders calls; every step of a token runs in
+libdv's kernels.
+
+Several candidates per sequence: ``verify_tree`` runs a drafted token tree
+through the layers (dv_tree_attn over the cache), ``accept`` keeps a path of it
+(dv_kv_compact), and ``reorder`` lets beams continue others (dv_kv_reorder).
 """
 
 from __future__ import annotations
@@ -72,6 +77,9 @@ class SparseDecoder:
         self.ws_attn = dv.workspace(
             dv.dv_sparse_attn_workspace_size(B, d, self.h, self.d_h, k_heads, n_max), dev)
         self.ws_mlp = dv.workspace(dv.dv_sparse_mlp_workspace_size(B, d, self.N, k_neurons), dev)
+        self.kv_layers = dv.KVLayers(self.kv)
+        self.ws_move = dv.workspace(256, dev)
+        self._tree: Dict[int, dict] = {}    # buffers of verify_tree by tree size
         self.side = torch.cuda.Stream(device=dev)
         self.ev_y = [dv.make_event() for _ in layers]
         self.ev_pred = [dv.make_event() for _ in layers]
@@ -96,6 +104,7 @@ class SparseDecoder:
         self.ws_attn = dv.workspace(
             dv.dv_sparse_attn_workspace_size(B, self.d, self.h, self.d_h, k_heads, self.n_max), dev)
         self.ws_mlp = dv.workspace(dv.dv_sparse_mlp_workspace_size(B, self.d, self.N, k_neurons), dev)
+        self._tree = {}
         self.graph = None
 
     # ------------------------------------------------------------------ pieces
@@ -292,8 +301,98 @@ class SparseDecoder:
     def replay(self):
         self.graph.replay()
 
+    # ------------------------------------------- several candidates per sequence
+    def _tree_buffers(self, T: int) -> dict:
+        """Buffers and workspaces of verify_tree for trees of T nodes (made on
+        the first use of a size)."""
+        if T in self._tree:
+            return self._tree[T]
+        dev, B, d, h, d_h = self.device, self.B, self.d, self.h, self.d_h
+        rows = B * T
+        chunk = min(rows, 32)   # rows of one dv_predict / dv_sparse_mlp call
+        i32 = dict(dtype=torch.int32, device=dev)
+        t = dict(chunk=chunk, r=torch.zeros(rows, d, dtype=torch.float32, device=dev),
+                 y=torch.zeros(rows, d, dtype=self.dtype, device=dev),
+                 src=torch.zeros(rows, d, dtype=self.dtype, device=dev),
+                 y_root=torch.zeros(B, d, dtype=self.dtype, device=dev),
+                 out=torch.zeros(B, T, h, d_h, dtype=self.dtype, device=dev),
+                 head_idx=torch.zeros(B, self.k_heads, **i32), head_cnt=torch.zeros(B, **i32),
+                 neur_idx=torch.zeros(chunk, self.k_neurons, **i32), neur_cnt=torch.zeros(chunk, **i32),
+                 row=torch.arange(B, device=dev)[:, None], node=torch.arange(T, **i32)[None],
+                 ws_pred=dv.workspace(dv.dv_predict_workspace_size(max(chunk, min(B, 32)), 1, self.r, self.N), dev),
+                 ws_mlp=dv.workspace(dv.dv_sparse_mlp_workspace_size(chunk, d, self.N, self.k_neurons), dev),
+                 ws_tree=dv.workspace(dv.dv_tree_attn_workspace_size(B, T, h, 1, d_h), dev))
+        self._tree[T] = t
+        return t
+
+    def verify_tree(self, E: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                    nodes: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The residual streams [B][T][d] (fp32) that T drafted tokens per
+        sequence leave the last layer with, all nodes in one pass.
+
+        E [B][T][d] (fp32): the streams entering layer 0; mask and nodes as in
+        dv_tree_attn (None: a linear draft, full trees).  pos + T must be below
+        n_max.  The nodes' rows are written to the cache behind pos, which does
+        not move: ``accept`` keeps a path of them.  A tree's nodes share one set
+        of heads per layer, predicted from node 0; neurons are predicted node
+        by node, both from the same inputs as in a decode step (layer 0 from its
+        own attention input, layer l from layer l - 1's).  The query and output
+        projections are plain library GEMMs with 16-bit results for 16-bit
+        storage."""
+        B, T, d = E.shape
+        if B != self.B or d != self.d or E.dtype != torch.float32:
+            raise ValueError(f"E: fp32 [{self.B}][T][{self.d}]")
+        t = self._tree_buffers(T)
+        h, d_h, rows, chunk = self.h, self.d_h, B * T, t["chunk"]
+        r, y, src = t["r"], t["y"], t["src"]
+        r.copy_(E.reshape(rows, d))
+        # (a slot outside the cache is reported by the calls below; the copies
+        # here must not index outside it)
+        slots = (self.pos[:, None] + t["node"]).clamp(0, self.n_max - 1).long()
+        end = self.pos + (T if nodes is None else nodes)
+        for l in range(self.L):
+            W, kv = self.layers[l], self.kv[l]
+            dv.dv_layernorm(r, y, self.eps)
+            if l == 0:
+                src.copy_(y)
+            t["y_root"].copy_(src.view(B, T, d)[:, 0])
+            for b in range(0, B, 32):
+                e = min(b + 32, B)
+                dv.dv_predict(t["y_root"][b:e], [dv.Predictor(W["PA1t"], W["PA2t"], t["head_idx"][b:e],
+                                                             t["head_cnt"][b:e], dv.DV_TOPK, self.k_heads)],
+                              t["ws_pred"])
+            kv.X[t["row"], slots] = y.view(B, T, d)
+            kv.valid[t["row"], :, slots] = 0
+            dv.dv_kv_repair(kv, W["Wqkv"], end, t["head_idx"], t["head_cnt"], self.ws_attn)
+            q = torch.bmm(y.expand(h, rows, d), W["Wqkv"][:, 0].transpose(1, 2))         # [h][B T][d_h]
+            dv.dv_tree_attn(q.permute(1, 0, 2).contiguous().view(B, T, h, d_h), kv, self.pos, self.scale, t["out"],
+                            t["ws_tree"], mask=mask, nodes=nodes, head_idx=t["head_idx"], head_count=t["head_cnt"])
+            r += torch.mm(t["out"].view(rows, h * d_h), W["Wo"].view(h * d_h, d))
+            ya = y.clone()
+            dv.dv_layernorm(r, y, self.eps)
+            for i in range(0, rows, chunk):
+                e = min(i + chunk, rows)
+                idx, cnt = t["neur_idx"][:e - i], t["neur_cnt"][:e - i]
+                dv.dv_predict(src[i:e], [dv.Predictor(W["PM1t"], W["PM2t"], idx, cnt, dv.DV_TOPK, self.k_neurons)],
+                              t["ws_pred"])
+                dv.dv_sparse_mlp(y[i:e], W["W1n"], W["W2n"], idx, cnt, r[i:e], t["ws_mlp"], accumulate=True)
+            src.copy_(ya)
+        return r.view(B, T, d).clone()
+
+    def accept(self, idx: torch.Tensor, count: torch.Tensor):
+        """Keep nodes idx[b][0 .. count[b]) of the last verified tree of each
+        sequence (int32, ascending: a path of the tree) and advance pos."""
+        dv.dv_kv_compact(self.kv_layers, self.pos, idx, count, self.ws_move, new_pos=self.pos)
+
+    def reorder(self, parent: torch.Tensor, start: Optional[torch.Tensor] = None):
+        """Let beam w of sequence s (cache row s * width + w) continue beam
+        parent[s][w] (int32 [n_seq][width], n_seq * width = B; start as in
+        dv_kv_reorder).  The beams of a sequence have the same length."""
+        dv.dv_kv_reorder(self.kv_layers, self.pos, parent, self.ws_move, start=start)
+
     def check(self):
-        for ws in (self.ws_pred_main, self.ws_pred_side, self.ws_attn, self.ws_mlp):
+        for ws in (self.ws_pred_main, self.ws_pred_side, self.ws_attn, self.ws_mlp, self.ws_move,
+                   *(t[k] for t in self._tree.values() for k in ("ws_pred", "ws_mlp", "ws_tree"))):
             st, info = dv.dv_check(ws)
             if st != 0:
                 raise dv.DvError(st, "decode step", f"info={info}")

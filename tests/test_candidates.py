@@ -18,6 +18,7 @@ import pytest
 import torch
 
 from contextual_sparsity_decode_gb300 import binding as dv
+from test_guards import Guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -649,3 +650,51 @@ def test_tree_attention_waits_that_run_out_unwind():
     c.call()
     assert dv.dv_check(c.ws) == (0, 0)
     assert torch.equal(c.out, want)
+
+
+# ------------------------------------------------------------------ guard regions
+
+def _guarded_ws(nbytes):
+    w = Guarded((max(int(nbytes), 256),), torch.uint8)
+    dv.dv_workspace_init(w.t)
+    return w
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d_h,T,g", [(64, 5, 1), (128, 70, 2), (64, 1, 1)])
+def test_tree_attention_writes_stay_in_bounds(dt, d_h, T, g):
+    c = Case(dt, d_h, [300, 0, 77], T, 3, g=g, seed=51, n_max=(300 + T + 15) // 16 * 16)
+    out, ws = Guarded(tuple(c.out.shape), DT[dt]), _guarded_ws(dv.dv_tree_attn_workspace_size(3, T, 3, g, d_h))
+    c.call()
+    want, c.out, c.ws = c.out, out.t, ws.t
+    c.call()
+    assert dv.dv_check(ws.t) == (0, 0)
+    assert torch.equal(out.t, want) and out.intact() and ws.intact()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_cache_moves_stay_in_bounds(dt):
+    B, h, n_max, d_h = 4, 3, 32, 64
+    shapes = ((B, h, n_max, d_h), (B, h, n_max, d_h), (B, n_max, h * d_h))
+    parts = [Guarded(s, DT[dt], fill=1.0) for s in shapes] + [Guarded((B, h, n_max), torch.uint8, fill=1)]
+    layers, ws, new = dv.KVLayers([dv.KV(*(p.t for p in parts))]), _guarded_ws(256), Guarded((B,), torch.int32)
+    dv.dv_kv_compact(layers, _i32([0, 5, 30, 31]), _i32([[0, 3], [1, 26], [0, 1], [0, 0]]), _i32([2, 2, 2, 1]), ws.t,
+                     new_pos=new.t)
+    dv.dv_kv_reorder(layers, _i32([32, 32, 7, 0]), _i32([[1, 0, 3, 2]]), ws.t)
+    assert dv.dv_check(ws.t) == (0, 0)
+    assert all(p.intact() for p in parts) and ws.intact() and new.intact()
+    assert new.t.tolist() == [2, 7, 32, 32]
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+def test_beam_select_writes_stay_in_bounds(dt):
+    S, W, V, K = 3, 4, 9001, 8
+    logits = torch.randn(S, W, V, generator=_gen(5), device="cuda").to(DT[dt])
+    ws = _guarded_ws(dv.dv_beam_select_workspace_size(S, W, V, K))
+    score, token, beam = Guarded((S, K), torch.float32), Guarded((S, K), torch.int32), Guarded((S, K), torch.int32)
+    cum = torch.zeros(S, W, device="cuda")
+    dv.dv_beam_select(logits, cum, score.t, token.t, beam.t, ws.t)
+    assert dv.dv_check(ws.t) == (0, 0)
+    assert all(x.intact() for x in (ws, score, token, beam))
+    _, rt, rb = _beam_ref(logits, cum, K)
+    assert np.array_equal(token.t.cpu().numpy(), rt) and np.array_equal(beam.t.cpu().numpy(), rb)
