@@ -18,6 +18,12 @@
 // positions took 17.6 us instead of 13.2, and three of 125 rows over 32768
 // positions 98 instead of 83.)
 
+// Bound by the reads of K and V for trees of up to 128 rows a K/V head.  Measured
+// on GB300: 8 sequences of 64 nodes over 2047 positions of 96 heads of 128 (f16,
+// 855 MB): 160 us, 5.3 TB/s, 0.79 of a plain copy's rate; 3 of 25 x 5 rows over
+// up to 32768 positions of 8 heads (bf16, 398 MB): 82 us, 4.8 TB/s; one of 8
+// nodes over 512 positions of 32 heads of 64: 12 us, all latency.
+
 #include <cuda.h>
 
 #include <type_traits>
