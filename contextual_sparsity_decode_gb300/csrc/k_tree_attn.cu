@@ -513,9 +513,10 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
 // P goes back to tensor memory (the A operand of the second product) as the
 // sum of two 16-bit halves hi + lo: one rounding of P to bf16 would put as
 // large an error into O as the output's own rounding; the two halves leave
-// 2^-17, and the second MMA is hidden, since the kernel is bound by the reads
-// of K and V: a tile of 64 keys is 32 KB, about 1400 cycles at an SM's share
-// of the memory, and its products take about 400.
+// 2^-17.  The second MMA is not free: without it 8 x 64 nodes took 153 us
+// instead of 162.  A tile of 64 keys is 32 KB, about 1400 cycles at an SM's
+// share of the memory; its three products take about 770 (4096 products a
+// cycle), and the tensor pipe is busy 0.41 of the time.
 // The reference maximum moves only when a tile's maximum exceeds it by 2^8
 // (P <= 2^14 with the 2^6 that keeps small weights out of f16's subnormals):
 // rescaling O is rare.
