@@ -477,8 +477,11 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamLaunch a)
     const float2 st = stat[tid];
     JoinRow j{0.0, cum, 1};
     if (ended) {
-      j.kind = 2;
-      j.base = open ? (double)cum : -INFINITY;
+      // (at -inf its end token has no place before lower ones: kind 1)
+      if (open) {
+        j.kind = 2;
+        j.base = (double)cum;
+      }
     } else if (st.y == 0.f && st.x > -INFINITY && open) {
       j.kind = 0;
       j.base = (double)st.x + log(sums[tid]);

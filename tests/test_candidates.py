@@ -698,3 +698,16 @@ def test_beam_select_writes_stay_in_bounds(dt):
     assert all(x.intact() for x in (ws, score, token, beam))
     _, rt, rb = _beam_ref(logits, cum, K)
     assert np.array_equal(token.t.cpu().numpy(), rt) and np.array_equal(beam.t.cpu().numpy(), rb)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("W,K,end", [(1, 4, 10), (2, 2, 299), (2, 5, 4), (3, 12, 200), (2, 5, 0)])
+def test_ended_beams_of_score_minus_infinity(dt, W, K, end):
+    """An ended beam at -inf offers its end token at -inf as well: it takes no
+    place before lower tokens."""
+    logits = torch.randn(2, W, 300, generator=_gen(W + K), device="cuda").to(DT[dt])
+    cum = torch.full((2, W), float("-inf"), device="cuda")
+    done = torch.ones(2, W, dtype=torch.uint8, device="cuda")
+    _beam_check(logits, cum, K, done, end)
+    cum[1, W - 1] = -1.5               # one sequence with a candidate
+    _beam_check(logits, cum, K, done, end)
