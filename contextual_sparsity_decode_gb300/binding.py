@@ -326,6 +326,13 @@ class KVLayers:
         self.array = (dv_kv * len(self.kvs))(*[c.c() for c in self.kvs])
 
 
+def _counted(where: str, n: int, *tensors, dtype=torch.int32) -> None:
+    """Contiguous tensors of n elements: the library reads or writes that many."""
+    for t in tensors:
+        if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
+            raise DvError(1, where, f"contiguous tensors of {n} elements of {dtype} are wanted")
+
+
 def _laid_out(t: torch.Tensor, shape, dtype, where: str) -> None:
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise DvError(1, where, f"a contiguous {tuple(shape)} tensor of {dtype} is wanted")
@@ -384,6 +391,9 @@ def dv_tree_attn(q, kv: KV, pos, scale, out, ws, mask=None, nodes=None, head_idx
     if mask is not None:
         batched = int(mask.dim() == 3)
         _laid_out(mask, (B, T, T) if batched else (T, T), torch.bool if mask.dtype == torch.bool else torch.uint8, where)
+    _counted(where, B, pos, nodes, head_count)
+    if head_idx is not None:
+        _counted(where, B * head_idx.shape[-1], head_idx)
     st = (_lib or lib()).dv_tree_attn(
         q.data_ptr(), B, T, h, hq // h, d_h, dv_kv(K.data_ptr(), V.data_ptr(), None, None, kv.n_max), pos.data_ptr(),
         _ptr(nodes), _ptr(mask), batched, _ptr(head_idx), 0 if head_idx is None else head_idx.shape[-1],
@@ -395,6 +405,8 @@ def dv_tree_attn(q, kv: KV, pos, scale, out, ws, mask=None, nodes=None, head_idx
 
 def dv_kv_compact(layers: KVLayers, pos, idx, count, ws, new_pos=None, stream=None):
     """Keep nodes idx[b][:count[b]] of each tree (see dv_kv_compact in dv.h)."""
+    _counted("dv_kv_compact", layers.B, pos, count, new_pos)
+    _counted("dv_kv_compact", layers.B * idx.shape[-1], idx)
     _ok(lib().dv_kv_compact(layers.array, len(layers.array), layers.B, layers.d, layers.h, layers.d_h, _ptr(pos),
                             _ptr(idx), idx.shape[-1], _ptr(count), layers.dt, _ptr(new_pos), _ptr(ws), ws.numel(),
                             _stream(stream)), "dv_kv_compact")
@@ -406,6 +418,8 @@ def dv_kv_reorder(layers: KVLayers, pos, parent, ws, start=None, stream=None):
     n_seq, width = parent.shape
     if n_seq * width != layers.B:
         raise DvError(1, "dv_kv_reorder", f"{n_seq} x {width} beams on {layers.B} cache rows")
+    _counted("dv_kv_reorder", layers.B, pos, parent)
+    _counted("dv_kv_reorder", n_seq, start)
     _ok(lib().dv_kv_reorder(layers.array, len(layers.array), n_seq, width, layers.d, layers.h, layers.d_h, _ptr(pos),
                             _ptr(start), _ptr(parent), layers.dt, _ptr(ws), ws.numel(), _stream(stream)),
         "dv_kv_reorder")
@@ -427,6 +441,11 @@ def dv_beam_select(logits, cum, score, token, beam, ws, done=None, end_token=0, 
         s1 = s0 if S > 1 else V
     if (V > 1 and s2 != 1) or (S > 1 and s0 != W * s1):
         raise DvError(1, "dv_beam_select", "rows of logits evenly spaced, tokens adjacent")
+    _counted("dv_beam_select", S * W, cum, dtype=torch.float32)
+    _counted("dv_beam_select", S * K, score, dtype=torch.float32)
+    _counted("dv_beam_select", S * K, token, beam)
+    if done is not None:
+        _counted("dv_beam_select", S * W, done, dtype=torch.bool if done.dtype == torch.bool else torch.uint8)
     _ok(lib().dv_beam_select(_ptr(logits), S, W, V, s1, _dt(logits), _ptr(cum), _ptr(done), int(end_token), K,
                              _ptr(score), _ptr(token), _ptr(beam), _ptr(ws), ws.numel(), _stream(stream)),
         "dv_beam_select")

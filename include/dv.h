@@ -320,7 +320,7 @@ dv_status dv_tree_attn_workspace_size(int B, int T, int h, int group, int d_h,
  *     not reach that row, whatever they hold.
  *  scale > 0, finite.
  *  head_idx [B][cap] with head_count [B]: the K/V heads of each sequence's
- *     tree, as in dv_sparse_attn; both NULL: all h heads.
+ *     tree, as in dv_sparse_attn, each at most once; both NULL: all h heads.
  * Every row of out is written: those of other heads, of nodes behind
  * nodes[b], and of nodes that see nothing are 0.  Maximum, sum and numerator
  * are held in fp32, and results repeat bit for bit.

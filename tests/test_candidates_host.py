@@ -155,3 +155,67 @@ def test_binding_refuses_shapes_types_and_layouts():
     logits = torch.zeros(4, 2, 100).transpose(0, 1)
     with pytest.raises(dv.DvError):
         dv.dv_beam_select(logits, torch.zeros(2, 4), torch.zeros(2, 4), pos, pos, ws)
+
+
+def _beam_tensors(**kw):
+    i32 = dict(dtype=torch.int32)
+    t = dict(logits=torch.zeros(2, 3, 50), cum=torch.zeros(2, 3), score=torch.zeros(2, 4),
+             token=torch.zeros(2, 4, **i32), beam=torch.zeros(2, 4, **i32), ws=torch.zeros(1 << 16, dtype=torch.uint8),
+             done=torch.zeros(2, 3, dtype=torch.uint8))
+    t.update(kw)
+    dv.dv_beam_select(*(t[k] for k in ("logits", "cum", "score", "token", "beam", "ws")), done=t["done"])
+
+
+@pytest.mark.parametrize("kw", [
+    dict(token=torch.zeros(2, 3, dtype=torch.int32)), dict(beam=torch.zeros(1, 4, dtype=torch.int32)),
+    dict(token=torch.zeros(2, 4, dtype=torch.int16)), dict(score=torch.zeros(1, 4)),
+    dict(score=torch.zeros(2, 4, dtype=torch.float16)), dict(beam=torch.zeros(4, 2, dtype=torch.int32).t()),
+    dict(cum=torch.zeros(2, 2)), dict(cum=torch.zeros(2, 3, dtype=torch.float16)),
+    dict(done=torch.zeros(2, 2, dtype=torch.uint8)), dict(done=torch.zeros(2, 3, dtype=torch.int32)),
+])
+def test_beam_select_refuses_tensors_of_other_sizes(kw):
+    with pytest.raises(dv.DvError) as e:
+        _beam_tensors(**kw)
+    assert e.value.status == INVALID
+
+
+def _four_layers(B=4):
+    kv = dv.KV(*(torch.zeros(B, 2, 16, 8, dtype=torch.float16) for _ in range(2)),
+               torch.zeros(B, 16, 16, dtype=torch.float16), torch.zeros(B, 2, 16, dtype=torch.uint8))
+    return dv.KVLayers([kv])
+
+
+@pytest.mark.parametrize("kw", [
+    dict(pos=3), dict(idx=(3, 2)), dict(count=5), dict(new_pos=3), dict(dtype=torch.int64),
+])
+def test_compact_refuses_lists_of_other_sizes(kw):
+    i32 = dict(dtype=kw.get("dtype", torch.int32))
+    pos, count, new_pos = (torch.zeros(kw.get(k, 4), **i32) for k in ("pos", "count", "new_pos"))
+    with pytest.raises(dv.DvError) as e:
+        dv.dv_kv_compact(_four_layers(), pos, torch.zeros(kw.get("idx", (4, 2)), **i32), count,
+                         torch.zeros(256, dtype=torch.uint8), new_pos=new_pos)
+    assert e.value.status == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(pos=3), dict(start=1), dict(parent=(2, 3)), dict(dtype=torch.int64)])
+def test_reorder_refuses_lists_of_other_sizes(kw):
+    i32 = dict(dtype=kw.get("dtype", torch.int32))
+    with pytest.raises(dv.DvError) as e:
+        dv.dv_kv_reorder(_four_layers(), torch.zeros(kw.get("pos", 4), **i32), torch.zeros(kw.get("parent", (2, 2)), **i32),
+                         torch.zeros(256, dtype=torch.uint8), start=torch.zeros(kw.get("start", 2), **i32))
+    assert e.value.status == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(pos=1), dict(nodes=1), dict(count=3), dict(head_idx=(1, 2)), dict(dtype=torch.int64),
+])
+def test_tree_attention_refuses_lists_of_other_sizes(kw):
+    i32 = dict(dtype=kw.get("dtype", torch.int32))
+    q = torch.zeros(2, 3, 2, 64, dtype=torch.float16)
+    kv = dv.KV(*(torch.zeros(2, 2, 16, 64, dtype=torch.float16) for _ in range(2)), None, None)
+    with pytest.raises(dv.DvError) as e:
+        dv.dv_tree_attn(q, kv, torch.zeros(kw.get("pos", 2), **i32), 0.125, torch.zeros_like(q),
+                        torch.zeros(1 << 26, dtype=torch.uint8), nodes=torch.zeros(kw.get("nodes", 2), **i32),
+                        head_idx=torch.zeros(kw.get("head_idx", (2, 2)), **i32),
+                        head_count=torch.zeros(kw.get("count", 2), **i32))
+    assert e.value.status == INVALID
