@@ -31,9 +31,9 @@
 // alone, not on the row's address, so rows with equal logits get equal sums.
 
 // Measured on GB300, both kernels: 48 x 10 rows of 128001 bf16 logits, a fifth of
-// the beams done, 54 us (1.8 TB/s of the logits read; 20 instructions a token,
-// 0.65 of the issue slots of busy SMs, SMs busy 0.79 of the time); 8 x 8 of 50257
-// fp32 17 us, 4 of 32000 f16 7.7 us.
+// the beams done, 51.5 us (1.9 TB/s of the logits read; bound by instructions, 19
+// a token, and by uneven SMs: parts of 8, 11 and 32 tiles instead of 16 took
+// 57, 53 and 58); 8 x 8 of 50257 fp32 16.6 us, 4 of 32000 f16 7.6 us.
 
 #include "dv_kernels.h"
 #include "tc_common.cuh"
@@ -280,9 +280,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     // logit may be the type's lowest value); a NaN or +inf among the tokens
     // makes it a NaN
     const float mn = fmaxf(m, top), ref = mn > -INFINITY ? mn : 0.f;
-    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+    u64 s2[2] = {0, 0};   // (two tokens an instruction: 52.5 us instead of 54.4 at 48 x 10 rows)
+    const u64 minus_ref = pack2(-ref, -ref), log2e = pack2(kLog2e, kLog2e);
 #pragma unroll
-    for (int i = 0; i < 8 * kGroups; ++i) s4[i & 3] += ex2((f[i] - ref) * kLog2e);
+    for (int i = 0; i < 8 * kGroups; i += 2) {
+      float y0, y1;
+      open2(mul2(add2(pack2(f[i], f[i + 1]), minus_ref), log2e), &y0, &y1);
+      s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], pack2(ex2(y0), ex2(y1)));
+    }
+    float s4[4];
+    open2(s2[0], &s4[0], &s4[1]);
+    open2(s2[1], &s4[2], &s4[3]);
     sum = fmaf(sum, m > -INFINITY ? ex2((m - ref) * kLog2e) : 1.f, (s4[0] + s4[1]) + (s4[2] + s4[3]));
     m = mn;
     const bool sharpen = k < 4 || (k & 3) == 0;   // (the maxima change ever more slowly)
@@ -311,9 +319,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
       if (reached) now = fmaxf(tau, unord32(reached));
     }
     static_assert(kGroups == 2, "two ballots");
-    const uint32_t hit0 = __ballot_sync(0xffffffffu, g8[0] > tau && g8[0] >= now);
-    const uint32_t hit1 = __ballot_sync(0xffffffffu, g8[1] > tau && g8[1] >= now);
-    if (hit0 | hit1) {
+    if (__any_sync(0xffffffffu, top > tau && top >= now)) {
+      const uint32_t hit0 = __ballot_sync(0xffffffffu, g8[0] > tau && g8[0] >= now);
+      const uint32_t hit1 = __ballot_sync(0xffffffffu, g8[1] > tau && g8[1] >= now);
       u64* at = list + wid * kMine + mine;
       const uint32_t below = (1u << lane) - 1;
       int i0 = 7, i1 = 15;   // the lowest tokens that hold the maxima
