@@ -323,7 +323,8 @@ class KVLayers:
             for t, shape in ((c.K, kv.K.shape), (c.V, kv.K.shape), (c.X, (self.B, self.n_max, self.d))):
                 _laid_out(t, shape, kv.K.dtype, "KVLayers")
             _laid_out(c.valid, kv.K.shape[:3], torch.uint8, "KVLayers")
-        self.array = (dv_kv * len(self.kvs))(*[c.c() for c in self.kvs])
+        self.n = len(self.kvs)
+        self.array = (dv_kv * self.n)(*[c.c() for c in self.kvs])
 
 
 def _counted(where: str, n: int, *tensors, dtype=torch.int32) -> None:
@@ -407,9 +408,12 @@ def dv_kv_compact(layers: KVLayers, pos, idx, count, ws, new_pos=None, stream=No
     """Keep nodes idx[b][:count[b]] of each tree (see dv_kv_compact in dv.h)."""
     _counted("dv_kv_compact", layers.B, pos, count, new_pos)
     _counted("dv_kv_compact", layers.B * idx.shape[-1], idx)
-    _ok(lib().dv_kv_compact(layers.array, len(layers.array), layers.B, layers.d, layers.h, layers.d_h, _ptr(pos),
-                            _ptr(idx), idx.shape[-1], _ptr(count), layers.dt, _ptr(new_pos), _ptr(ws), ws.numel(),
-                            _stream(stream)), "dv_kv_compact")
+    st = (_lib or lib()).dv_kv_compact(
+        layers.array, layers.n, layers.B, layers.d, layers.h, layers.d_h, pos.data_ptr(), idx.data_ptr(),
+        idx.shape[-1], count.data_ptr(), layers.dt, None if new_pos is None else new_pos.data_ptr(), ws.data_ptr(),
+        ws.numel(), _stream(stream))
+    if st:
+        _ok(st, "dv_kv_compact")
 
 
 def dv_kv_reorder(layers: KVLayers, pos, parent, ws, start=None, stream=None):
@@ -419,10 +423,14 @@ def dv_kv_reorder(layers: KVLayers, pos, parent, ws, start=None, stream=None):
     if n_seq * width != layers.B:
         raise DvError(1, "dv_kv_reorder", f"{n_seq} x {width} beams on {layers.B} cache rows")
     _counted("dv_kv_reorder", layers.B, pos, parent)
-    _counted("dv_kv_reorder", n_seq, start)
-    _ok(lib().dv_kv_reorder(layers.array, len(layers.array), n_seq, width, layers.d, layers.h, layers.d_h, _ptr(pos),
-                            _ptr(start), _ptr(parent), layers.dt, _ptr(ws), ws.numel(), _stream(stream)),
-        "dv_kv_reorder")
+    if start is not None:
+        _counted("dv_kv_reorder", n_seq, start)
+    st = (_lib or lib()).dv_kv_reorder(
+        layers.array, layers.n, n_seq, width, layers.d, layers.h, layers.d_h, pos.data_ptr(),
+        None if start is None else start.data_ptr(), parent.data_ptr(), layers.dt, ws.data_ptr(), ws.numel(),
+        _stream(stream))
+    if st:
+        _ok(st, "dv_kv_reorder")
 
 
 def dv_beam_select_workspace_size(n_seq: int, width: int, V: int, K: int) -> int:
@@ -446,9 +454,12 @@ def dv_beam_select(logits, cum, score, token, beam, ws, done=None, end_token=0, 
     _counted("dv_beam_select", S * K, token, beam)
     if done is not None:
         _counted("dv_beam_select", S * W, done, dtype=torch.bool if done.dtype == torch.bool else torch.uint8)
-    _ok(lib().dv_beam_select(_ptr(logits), S, W, V, s1, _dt(logits), _ptr(cum), _ptr(done), int(end_token), K,
-                             _ptr(score), _ptr(token), _ptr(beam), _ptr(ws), ws.numel(), _stream(stream)),
-        "dv_beam_select")
+    st = (_lib or lib()).dv_beam_select(
+        logits.data_ptr(), S, W, V, s1, _dt(logits), cum.data_ptr(), None if done is None else done.data_ptr(),
+        int(end_token), K, score.data_ptr(), token.data_ptr(), beam.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream(stream))
+    if st:
+        _ok(st, "dv_beam_select")
 
 
 # --------------------------------------------------------------------- labels
