@@ -711,3 +711,29 @@ def test_ended_beams_of_score_minus_infinity(dt, W, K, end):
     _beam_check(logits, cum, K, done, end)
     cum[1, W - 1] = -1.5               # one sequence with a candidate
     _beam_check(logits, cum, K, done, end)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_beam_select_unwinds_when_its_waits_run_out(dt):
+    """With a wait limit of a nanosecond a scan may give up on a copy: the call
+    returns, reports it, writes nothing outside its outputs, and the next call
+    is right."""
+    S, W, V, K = 6, 8, 60001, 16
+    logits = torch.randn(S, W, V, generator=_gen(61), device="cuda").to(DT[dt])
+    cum = -torch.rand(S, W, generator=_gen(62), device="cuda")
+    score = Guarded((S, K), torch.float32)
+    token, beam = Guarded((S, K), torch.int32), Guarded((S, K), torch.int32)
+    ws = _guarded_ws(dv.dv_beam_select_workspace_size(S, W, V, K))
+    prev = dv.dv_set_wait_limit_ns(1)
+    try:
+        for _ in range(3):
+            dv.dv_beam_select(logits, cum, score.t, token.t, beam.t, ws.t)
+            st, _ = dv.dv_check(ws.t)
+            assert st in (0, 6)
+    finally:
+        dv.dv_set_wait_limit_ns(prev)
+    dv.dv_beam_select(logits, cum, score.t, token.t, beam.t, ws.t)
+    assert dv.dv_check(ws.t) == (0, 0)
+    assert score.intact() and token.intact() and beam.intact() and ws.intact()
+    _, rt, rb = _beam_ref(logits, cum, K, None, 0)
+    assert np.array_equal(token.t.cpu().numpy(), rt) and np.array_equal(beam.t.cpu().numpy(), rb)
