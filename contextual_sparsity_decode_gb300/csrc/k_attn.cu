@@ -918,6 +918,12 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_kernel(AttnArgs a) {
 // ---------------------------------------------------------------------------
 // standalone KV repair: tiled GEMM over the missing positions of a head
 
+// The end of the positions to repair (those before it): n_max, a full cache, is one.
+__device__ __forceinline__ int repair_end(const AttnArgs& a, int b) {
+  const int p = a.pos[b];
+  return (p >= 0 && p <= a.n_max) ? p : -1;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) kv_repair_gemm_kernel(AttnArgs a, int n_ct) {
   constexpr int V = Elem<T>::kVec;
@@ -934,7 +940,7 @@ __global__ void __launch_bounds__(256) kv_repair_gemm_kernel(AttnArgs a, int n_c
   const int cnt = max(0, min(a.head_count[b], a.cap));
   if (s >= cnt) return;
   const int i = a.head_idx[(size_t)b * a.cap + s];
-  const int p = row_pos(a, b);
+  const int p = repair_end(a, b);
   if (i < 0 || i >= a.h || p < 0) {
     if (tid == 0 && pt == 0 && ct == 0) set_error(a.hdr, p < 0 ? DV_ERR_POSITION : DV_ERR_INDEX_RANGE, p < 0 ? a.pos[b] : i);
     return;
@@ -1033,7 +1039,7 @@ __global__ void mark_valid_kernel(AttnArgs a) {
   const int cnt = max(0, min(a.head_count[b], a.cap));
   if (s >= cnt) return;
   const int i = a.head_idx[(size_t)b * a.cap + s];
-  const int p = row_pos(a, b);
+  const int p = repair_end(a, b);
   if (i < 0 || i >= a.h || p < 0) return;
   uint8_t* vr = a.valid + ((size_t)b * a.h + i) * a.n_max;
   for (int j = threadIdx.x; j < p; j += blockDim.x) vr[j] = 1;

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (s >= cnt) return;
   const int i = a.head_idx[(size_t)b * a.cap + s];
   const int p0 = a.pos[b];
-  const int p = (p0 >= 0 && p0 < a.n_max) ? p0 : -1;
+  const int p = (p0 >= 0 && p0 <= a.n_max) ? p0 : -1;  // positions before p: a full cache is fine
   if (i < 0 || i >= a.h || p < 0) {
     if (tid == 0 && pt == 0) set_error(a.hdr, p < 0 ? DV_ERR_POSITION : DV_ERR_INDEX_RANGE, p < 0 ? p0 : i);
     return;
@@ -237,7 +237,7 @@ __global__ void kv_mark_valid_kernel(KvTcArgs a) {
   if (s >= cnt) return;
   const int i = a.head_idx[(size_t)b * a.cap + s];
   const int p = a.pos[b];
-  if (i < 0 || i >= a.h || p < 0 || p >= a.n_max) return;
+  if (i < 0 || i >= a.h || p < 0 || p > a.n_max) return;
   uint8_t* vr = const_cast<uint8_t*>(a.valid) + ((size_t)b * a.h + i) * a.n_max;
   for (int j = threadIdx.x; j < p; j += blockDim.x) vr[j] = 1;
 }

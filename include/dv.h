@@ -247,7 +247,8 @@ dv_status dv_sparse_attn(const void* y, int B, int d, int h, int d_h,
  * selected head i of sequence b and every j < pos[b] with valid = 0,
  * recompute K/V[b][i][j] from X[b][j] and set valid = 1.  With every head
  * selected and valid all 0 this is a dense prefill of positions 0..pos-1.
- * Uses the dv_sparse_attn workspace. */
+ * 0 <= pos[b] <= n_max (else DV_ERR_POSITION, the row is left as it is): a
+ * full cache can be repaired.  Uses the dv_sparse_attn workspace. */
 dv_status dv_kv_repair(const dv_kv* kv, int B, int d, int h, int d_h,
                        const void* Wqkv, const int32_t* pos,
                        const int32_t* head_idx, int cap,
