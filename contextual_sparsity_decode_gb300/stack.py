@@ -318,7 +318,9 @@ class SparseDecoder:
                  out=torch.zeros(B, T, h, d_h, dtype=self.dtype, device=dev),
                  head_idx=torch.zeros(B, self.k_heads, **i32), head_cnt=torch.zeros(B, **i32),
                  neur_idx=torch.zeros(chunk, self.k_neurons, **i32), neur_cnt=torch.zeros(chunk, **i32),
-                 row=torch.arange(B, device=dev)[:, None], node=torch.arange(T, **i32)[None],
+                 full=torch.full((B,), T, **i32), node=torch.arange(T, **i32)[None],
+                 row=torch.arange(B, device=dev)[:, None],
+                 head=(torch.arange(B * h, device=dev) * self.n_max).view(B, 1, h),
                  ws_pred=dv.workspace(dv.dv_predict_workspace_size(max(chunk, min(B, 32)), 1, self.r, self.N), dev),
                  ws_mlp=dv.workspace(dv.dv_sparse_mlp_workspace_size(chunk, d, self.N, self.k_neurons), dev),
                  ws_tree=dv.workspace(dv.dv_tree_attn_workspace_size(B, T, h, 1, d_h), dev))
@@ -331,12 +333,14 @@ class SparseDecoder:
         sequence leave the last layer with, all nodes in one pass.
 
         E [B][T][d] (fp32): the streams entering layer 0; mask and nodes as in
-        dv_tree_attn (None: a linear draft, full trees).  pos + T must be below
-        n_max.  The nodes' rows are written to the cache behind pos, which does
-        not move: ``accept`` keeps a path of them.  A tree's nodes share one set
-        of heads per layer, predicted from node 0; neurons are predicted node
-        by node, both from the same inputs as in a decode step (layer 0 from its
-        own attention input, layer l from layer l - 1's).  The query and output
+        dv_tree_attn (None: a linear draft, full trees).  pos + nodes may be
+        n_max at most: a tree behind that changes no row of the cache, and
+        ``check`` reports it.  The live nodes' rows are written to the cache
+        behind pos, which does not move: ``accept`` keeps a path of them.  A
+        tree's nodes share one set of heads per layer, predicted from node 0;
+        neurons are predicted node by node, both from the same inputs as in a
+        decode step (layer 0 from its own attention input, layer l from layer
+        l - 1's).  The query and output
         projections are plain library GEMMs with 16-bit results for 16-bit
         storage."""
         B, T, d = E.shape
@@ -346,10 +350,22 @@ class SparseDecoder:
         h, d_h, rows, chunk = self.h, self.d_h, B * T, t["chunk"]
         r, y, src = t["r"], t["y"], t["src"]
         r.copy_(E.reshape(rows, d))
-        # (a slot outside the cache is reported by the calls below; the copies
-        # here must not index outside it)
-        slots = (self.pos[:, None] + t["node"]).clamp(0, self.n_max - 1).long()
-        end = self.pos + (T if nodes is None else nodes)
+        # Rows of the cache that the nodes take: those of live nodes alone, and
+        # none of a tree that does not fit (the calls below report it).  A node
+        # without a row of its own repeats its tree's last live one, or, where
+        # there is none, writes back what slot 0 holds: every index may be
+        # written, and equal ones get equal values.
+        live = t["full"] if nodes is None else nodes.clamp(0, T)
+        inside = (self.pos >= 0) & (self.pos <= self.n_max)
+        end = self.pos + live.where(inside, 0)
+        fits = (inside & (self.pos <= self.n_max - live) & (live > 0))[:, None]
+        node = torch.minimum(t["node"], live[:, None] - 1).clamp_(min=0)
+        slot = (self.pos[:, None] + node).where(fits, 0)
+        x_row = (t["row"] * self.n_max + slot).view(-1)
+        y_row = (t["row"] * T + node).view(-1)
+        x_new = fits.expand(B, T).reshape(rows, 1)
+        flag = (t["head"] + slot[:, :, None]).view(-1)
+        bound = (~fits).to(torch.uint8).mul_(255)[:, :, None].expand(B, T, h).reshape(-1)   # min: cleared, or as it is
         for l in range(self.L):
             W, kv = self.layers[l], self.kv[l]
             dv.dv_layernorm(r, y, self.eps)
@@ -361,8 +377,9 @@ class SparseDecoder:
                 dv.dv_predict(t["y_root"][b:e], [dv.Predictor(W["PA1t"], W["PA2t"], t["head_idx"][b:e],
                                                              t["head_cnt"][b:e], dv.DV_TOPK, self.k_heads)],
                               t["ws_pred"])
-            kv.X[t["row"], slots] = y.view(B, T, d)
-            kv.valid[t["row"], :, slots] = 0
+            X = kv.X.view(B * self.n_max, d)
+            X.index_copy_(0, x_row, y.index_select(0, y_row).where(x_new, X.index_select(0, x_row)))
+            kv.valid.view(-1).scatter_reduce_(0, flag, bound, "amin")
             dv.dv_kv_repair(kv, W["Wqkv"], end, t["head_idx"], t["head_cnt"], self.ws_attn)
             q = torch.bmm(y.expand(h, rows, d), W["Wqkv"][:, 0].transpose(1, 2))         # [h][B T][d_h]
             dv.dv_tree_attn(q.permute(1, 0, 2).contiguous().view(B, T, h, d_h), kv, self.pos, self.scale, t["out"],

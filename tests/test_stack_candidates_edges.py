@@ -1,0 +1,153 @@
+"""The verify pass where its nodes meet the cache's end, are padding, or share
+few heads and neurons; what it leaves alone, and what it keeps."""
+
+import pytest
+import torch
+
+from contextual_sparsity_decode_gb300 import binding as dv
+from test_stack_candidates import _close, _decoder, _inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _filled(B, pos, **kw):
+    """A decoder whose caches hold something in every slot, at positions pos."""
+    dec = _decoder(B, **kw)
+    g = torch.Generator(device="cuda").manual_seed(17)
+    for kv in dec.kv:
+        for t in (kv.K, kv.V, kv.X):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda").to(t.dtype))
+        kv.valid.fill_(1)
+    dec.pos.copy_(_i32(pos))
+    return dec
+
+
+def _tensors(dec):
+    return [[t.clone() for t in (kv.K, kv.V, kv.X, kv.valid)] for kv in dec.kv]
+
+
+def _unchanged(dec, old, b, lo, hi):
+    """Slots [lo, hi) of row b hold what they held, in every layer."""
+    for l, kv in enumerate(dec.kv):
+        for name, t, o in zip("KVXv", (kv.K, kv.V, kv.X, kv.valid), old[l]):
+            t, o = (x[b, lo:hi] if name == "X" else x[b, :, lo:hi] for x in (t, o))
+            assert torch.equal(t, o), (l, name)
+
+
+@pytest.mark.parametrize("pos", [64, 62, 70, -2, 2 ** 31 - 2])
+def test_a_tree_behind_the_cache_changes_no_row(pos):
+    """A tree that does not fit behind its sequence (or a position that is none)
+    is reported; no slot of the row changes, and the other row is served."""
+    E = _inputs(2, 5, 512, 31)
+    dec = _filled(2, [pos, 30])
+    old = _tensors(dec)
+    got = dec.verify_tree(E)
+    with pytest.raises(dv.DvError) as e:
+        dec.check()
+    assert e.value.status == 9
+    _unchanged(dec, old, 0, 0, 64)
+    _unchanged(dec, old, 1, 0, 30)
+    _unchanged(dec, old, 1, 35, 64)
+    ref = _filled(2, [30, 30])
+    want = ref.verify_tree(E)
+    ref.check()
+    _close(got[1], want[1])
+
+
+def test_padding_nodes_write_nothing():
+    """Nodes behind nodes[b] are padding: their slots keep what they hold, also
+    where they would lie behind the cache."""
+    E = _inputs(3, 5, 512, 32)
+    pos, nodes = [60, 40, 20], [2, 1, 0]
+    dec = _filled(3, pos)
+    old = _tensors(dec)
+    got = dec.verify_tree(E, nodes=_i32(nodes))
+    dec.check()
+    for b in range(3):
+        _unchanged(dec, old, b, 0, pos[b])
+        _unchanged(dec, old, b, pos[b] + nodes[b], 64)
+    for b, n in enumerate(nodes[:2]):
+        ref = _filled(3, pos)
+        want = ref.verify_tree(E[:, :n])
+        ref.check()
+        _close(got[b, :n], want[b])
+        for kv, k in zip(dec.kv, ref.kv):
+            _close(kv.X[b, pos[b]:pos[b] + n], k.X[b, pos[b]:pos[b] + n])
+            _close(kv.K[b, :, pos[b]:pos[b] + n], k.K[b, :, pos[b]:pos[b] + n])
+
+
+def test_more_nodes_than_the_tree_has_are_cut_off():
+    E = _inputs(1, 3, 512, 33)
+    dec, ref = _filled(1, [20]), _filled(1, [20])
+    for d in (dec, ref):
+        for kv in d.kv:
+            kv.valid[:, :, 20:] = 0
+    old = _tensors(dec)
+    got = dec.verify_tree(E, nodes=_i32([9]))
+    with pytest.raises(dv.DvError) as e:
+        dec.check()
+    assert e.value.status == 8
+    _unchanged(dec, old, 0, 23, 64)
+    want = ref.verify_tree(E)
+    ref.check()
+    _close(got, want)
+
+
+@pytest.mark.parametrize("T", [3, 5])
+def test_a_tree_that_ends_with_the_cache(T):
+    """Three nodes fill the last three slots (two more are padding): the same as
+    in a longer cache."""
+    E = _inputs(1, T, 512, 34)
+    dec, ref = _decoder(1), _decoder(1, n_max=80)
+    g = torch.Generator(device="cuda").manual_seed(35)
+    for a, b in zip(dec.kv, ref.kv):
+        X = torch.randn(61, 512, generator=g, device="cuda").to(a.X.dtype)
+        a.X[0, :61], b.X[0, :61] = X, X
+        a.valid.zero_(), b.valid.zero_()
+    dec.pos.fill_(61), ref.pos.fill_(61)
+    nodes = _i32([3])
+    got, want = dec.verify_tree(E, nodes=nodes), ref.verify_tree(E, nodes=nodes)
+    dec.check(), ref.check()
+    _close(got[:, :3], want[:, :3])
+    for a, b in zip(dec.kv, ref.kv):
+        assert a.valid.all()
+        _close(a.K, b.K[:, :, :64])
+        _close(a.X, b.X[:, :64])
+
+
+def test_verify_captured_and_replayed():
+    """One graph of the pass: streams, lengths and positions are read at replay,
+    a tree that does not fit among them."""
+    E, nodes = _inputs(2, 4, 512, 39), _i32([4, 2])
+    dec, ref = _filled(2, [20, 30]), _filled(2, [20, 30])
+    dec.verify_tree(E, nodes=nodes)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = dec.verify_tree(E, nodes=nodes)
+    for pos, n, status in (([25, 60], [3, 4], 0), ([0, 33], [0, 4], 0), ([61, 11], [4, 1], 9)):
+        for d in (dec, ref):
+            for kv, o in zip(d.kv, _filled(2, pos).kv):
+                for t, u in ((kv.K, o.K), (kv.V, o.V), (kv.X, o.X), (kv.valid, o.valid)):
+                    t.copy_(u)
+            d.pos.copy_(_i32(pos))
+        nodes.copy_(_i32(n))
+        E.copy_(_inputs(2, 4, 512, pos[0]))
+        graph.replay()
+        want = ref.verify_tree(E, nodes=nodes)
+        for d in (dec, ref):
+            if status:
+                with pytest.raises(dv.DvError) as e:
+                    d.check()
+                assert e.value.status == status
+            else:
+                d.check()
+        for b in range(2):
+            if pos[b] + n[b] <= 64:
+                _close(got[b, :n[b]], want[b, :n[b]]) if n[b] else None
+            for a, o in zip(dec.kv, ref.kv):
+                _close(a.X[b], o.X[b])
+                assert torch.equal(a.valid[b], o.valid[b])
