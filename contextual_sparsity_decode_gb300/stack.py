@@ -346,6 +346,13 @@ class SparseDecoder:
         B, T, d = E.shape
         if B != self.B or d != self.d or E.dtype != torch.float32:
             raise ValueError(f"E: fp32 [{self.B}][T][{self.d}]")
+        # before anything is written: the calls below would refuse these too late
+        if nodes is not None and (nodes.dtype != torch.int32 or nodes.shape != (B,) or not nodes.is_contiguous()
+                                  or nodes.device != self.pos.device):
+            raise ValueError(f"nodes: contiguous int32 [{B}] on {self.pos.device}")
+        if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or not mask.is_contiguous()
+                                 or mask.shape not in ((T, T), (B, T, T)) or mask.device != self.pos.device):
+            raise ValueError(f"mask: contiguous bool or uint8 [T][T] or [{B}][T][T] on {self.pos.device}")
         t = self._tree_buffers(T)
         h, d_h, rows, chunk = self.h, self.d_h, B * T, t["chunk"]
         r, y, src = t["r"], t["y"], t["src"]

@@ -151,3 +151,19 @@ def test_verify_captured_and_replayed():
             for a, o in zip(dec.kv, ref.kv):
                 _close(a.X[b], o.X[b])
                 assert torch.equal(a.valid[b], o.valid[b])
+
+
+@pytest.mark.parametrize("bad", [
+    dict(nodes=torch.tensor([3, 2])), dict(nodes=torch.tensor([[3], [2]], dtype=torch.int32)),
+    dict(nodes=torch.tensor([3], dtype=torch.int32)), dict(mask=torch.ones(3, 3)),
+    dict(mask=torch.ones(3, 4, dtype=torch.bool)), dict(mask=torch.ones(1, 3, 3, dtype=torch.bool)),
+    dict(mask=torch.ones(3, 3, dtype=torch.bool).t()), dict(mask=torch.ones(3, 3, dtype=torch.bool), cpu=True),
+])
+def test_verify_refuses_before_it_writes(bad):
+    dec = _filled(2, [30, 30])
+    old = _tensors(dec)
+    with pytest.raises(ValueError):
+        dec.verify_tree(_inputs(2, 3, 512, 36), **{k: t if "cpu" in bad else t.cuda() for k, t in bad.items() if k != "cpu"})
+    for b in range(2):
+        _unchanged(dec, old, b, 0, 64)
+    dec.check()
