@@ -353,6 +353,15 @@ class SparseDecoder:
         if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or not mask.is_contiguous()
                                  or mask.shape not in ((T, T), (B, T, T)) or mask.device != self.pos.device):
             raise ValueError(f"mask: contiguous bool or uint8 [T][T] or [{B}][T][T] on {self.pos.device}")
+        # the predictors here write their lists right before the calls that read them
+        prev = dv.dv_set_launch_overlap(0)
+        try:
+            return self._verify_ops(E, mask, nodes)
+        finally:
+            dv.dv_set_launch_overlap(prev)
+
+    def _verify_ops(self, E, mask, nodes):
+        B, T, d = E.shape
         t = self._tree_buffers(T)
         h, d_h, rows, chunk = self.h, self.d_h, B * T, t["chunk"]
         r, y, src = t["r"], t["y"], t["src"]

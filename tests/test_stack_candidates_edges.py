@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from contextual_sparsity_decode_gb300 import binding as dv
+from contextual_sparsity_decode_gb300 import stack
 from test_stack_candidates import _close, _decoder, _inputs
 
 pytestmark = pytest.mark.gpu
@@ -167,3 +168,32 @@ def test_verify_refuses_before_it_writes(bad):
     for b in range(2):
         _unchanged(dec, old, b, 0, 64)
     dec.check()
+
+
+def test_verify_does_not_inherit_the_launch_policy(monkeypatch):
+    """A call right after the predictor that writes its list must not start
+    early, whatever level the process is at; the level is left as it was."""
+    dec = _decoder(1)
+    seen = []
+
+    def level(fn):
+        def call(*a, **kw):
+            now = dv.dv_set_launch_overlap(0)
+            dv.dv_set_launch_overlap(now)
+            seen.append(now)
+            return fn(*a, **kw)
+        return call
+
+    monkeypatch.setattr(stack.dv, "dv_sparse_mlp", level(dv.dv_sparse_mlp))
+    prev = dv.dv_set_launch_overlap(1)
+    try:
+        dec.verify_tree(_inputs(1, 1, 512, 37))
+        dec.check()
+        after = dv.dv_set_launch_overlap(1)
+        monkeypatch.setattr(stack.dv, "dv_kv_repair", None)     # ... also when a call fails
+        with pytest.raises(TypeError):
+            dec.verify_tree(_inputs(1, 1, 512, 37))
+        failed = dv.dv_set_launch_overlap(1)
+    finally:
+        dv.dv_set_launch_overlap(prev)
+    assert seen == [0] * dec.L and after == 1 and failed == 1
