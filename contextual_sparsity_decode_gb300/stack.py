@@ -79,7 +79,7 @@ class SparseDecoder:
         self.ws_mlp = dv.workspace(dv.dv_sparse_mlp_workspace_size(B, d, self.N, k_neurons), dev)
         self.kv_layers = dv.KVLayers(self.kv)
         self.ws_move = dv.workspace(256, dev)
-        self._tree: Dict[int, dict] = {}    # buffers of verify_tree by tree size
+        self._tree: Dict[int, dict] = {}    # buffers of verify_tree by the nodes they hold
         self.side = torch.cuda.Stream(device=dev)
         self.ev_y = [dv.make_event() for _ in layers]
         self.ev_pred = [dv.make_event() for _ in layers]
@@ -303,28 +303,31 @@ class SparseDecoder:
 
     # ------------------------------------------- several candidates per sequence
     def _tree_buffers(self, T: int) -> dict:
-        """Buffers and workspaces of verify_tree for trees of T nodes (made on
-        the first use of a size)."""
-        if T in self._tree:
-            return self._tree[T]
+        """Buffers and workspaces of verify_tree for trees of T nodes: the
+        smallest set made so far that holds them, or a new one for the next
+        power of two (all sets together hold less than twice the largest).  A
+        set stays: captured graphs hold its addresses."""
+        size = min((n for n in self._tree if n >= T), default=0)
+        if size:
+            return self._tree[size]
+        size = 1 << (T - 1).bit_length()
         dev, B, d, h, d_h = self.device, self.B, self.d, self.h, self.d_h
-        rows = B * T
+        rows = B * size
         chunk = min(rows, 32)   # rows of one dv_predict / dv_sparse_mlp call
         i32 = dict(dtype=torch.int32, device=dev)
-        t = dict(chunk=chunk, r=torch.zeros(rows, d, dtype=torch.float32, device=dev),
+        t = dict(r=torch.zeros(rows, d, dtype=torch.float32, device=dev),
                  y=torch.zeros(rows, d, dtype=self.dtype, device=dev),
                  src=torch.zeros(rows, d, dtype=self.dtype, device=dev),
                  y_root=torch.zeros(B, d, dtype=self.dtype, device=dev),
-                 out=torch.zeros(B, T, h, d_h, dtype=self.dtype, device=dev),
+                 out=torch.zeros(rows, h * d_h, dtype=self.dtype, device=dev),
                  head_idx=torch.zeros(B, self.k_heads, **i32), head_cnt=torch.zeros(B, **i32),
                  neur_idx=torch.zeros(chunk, self.k_neurons, **i32), neur_cnt=torch.zeros(chunk, **i32),
-                 full=torch.full((B,), T, **i32), node=torch.arange(T, **i32)[None],
-                 row=torch.arange(B, device=dev)[:, None],
+                 node=torch.arange(size, **i32)[None], row=torch.arange(B, device=dev)[:, None],
                  head=(torch.arange(B * h, device=dev) * self.n_max).view(B, 1, h),
                  ws_pred=dv.workspace(dv.dv_predict_workspace_size(max(chunk, min(B, 32)), 1, self.r, self.N), dev),
                  ws_mlp=dv.workspace(dv.dv_sparse_mlp_workspace_size(chunk, d, self.N, self.k_neurons), dev),
-                 ws_tree=dv.workspace(dv.dv_tree_attn_workspace_size(B, T, h, 1, d_h), dev))
-        self._tree[T] = t
+                 ws_tree=dv.workspace(dv.dv_tree_attn_workspace_size(B, size, h, 1, d_h), dev))
+        self._tree[size] = t
         return t
 
     def verify_tree(self, E: torch.Tensor, mask: Optional[torch.Tensor] = None,
@@ -344,8 +347,8 @@ class SparseDecoder:
         projections are plain library GEMMs with 16-bit results for 16-bit
         storage."""
         B, T, d = E.shape
-        if B != self.B or d != self.d or E.dtype != torch.float32:
-            raise ValueError(f"E: fp32 [{self.B}][T][{self.d}]")
+        if B != self.B or T < 1 or d != self.d or E.dtype != torch.float32:
+            raise ValueError(f"E: fp32 [{self.B}][T][{self.d}], T >= 1")
         # before anything is written: the calls below would refuse these too late
         if nodes is not None and (nodes.dtype != torch.int32 or nodes.shape != (B,) or not nodes.is_contiguous()
                                   or nodes.device != self.pos.device):
@@ -363,19 +366,19 @@ class SparseDecoder:
     def _verify_ops(self, E, mask, nodes):
         B, T, d = E.shape
         t = self._tree_buffers(T)
-        h, d_h, rows, chunk = self.h, self.d_h, B * T, t["chunk"]
-        r, y, src = t["r"], t["y"], t["src"]
+        h, d_h, rows, chunk = self.h, self.d_h, B * T, min(B * T, 32)
+        r, y, src, out = (t[k][:rows] for k in ("r", "y", "src", "out"))
         r.copy_(E.reshape(rows, d))
         # Rows of the cache that the nodes take: those of live nodes alone, and
         # none of a tree that does not fit (the calls below report it).  A node
         # without a row of its own repeats its tree's last live one, or, where
         # there is none, writes back what slot 0 holds: every index may be
         # written, and equal ones get equal values.
-        live = t["full"] if nodes is None else nodes.clamp(0, T)
+        live = torch.full_like(self.pos, T) if nodes is None else nodes.clamp(0, T)
         inside = (self.pos >= 0) & (self.pos <= self.n_max)
         end = self.pos + live.where(inside, 0)
         fits = (inside & (self.pos <= self.n_max - live) & (live > 0))[:, None]
-        node = torch.minimum(t["node"], live[:, None] - 1).clamp_(min=0)
+        node = torch.minimum(t["node"][:, :T], live[:, None] - 1).clamp_(min=0)
         slot = (self.pos[:, None] + node).where(fits, 0)
         x_row = (t["row"] * self.n_max + slot).view(-1)
         y_row = (t["row"] * T + node).view(-1)
@@ -398,9 +401,10 @@ class SparseDecoder:
             kv.valid.view(-1).scatter_reduce_(0, flag, bound, "amin")
             dv.dv_kv_repair(kv, W["Wqkv"], end, t["head_idx"], t["head_cnt"], self.ws_attn)
             q = torch.bmm(y.expand(h, rows, d), W["Wqkv"][:, 0].transpose(1, 2))         # [h][B T][d_h]
-            dv.dv_tree_attn(q.permute(1, 0, 2).contiguous().view(B, T, h, d_h), kv, self.pos, self.scale, t["out"],
-                            t["ws_tree"], mask=mask, nodes=nodes, head_idx=t["head_idx"], head_count=t["head_cnt"])
-            r += torch.mm(t["out"].view(rows, h * d_h), W["Wo"].view(h * d_h, d))
+            dv.dv_tree_attn(q.permute(1, 0, 2).contiguous().view(B, T, h, d_h), kv, self.pos, self.scale,
+                            out.view(B, T, h, d_h), t["ws_tree"], mask=mask, nodes=nodes, head_idx=t["head_idx"],
+                            head_count=t["head_cnt"])
+            r += torch.mm(out, W["Wo"].view(h * d_h, d))
             ya = y.clone()
             dv.dv_layernorm(r, y, self.eps)
             for i in range(0, rows, chunk):

@@ -197,3 +197,35 @@ def test_verify_does_not_inherit_the_launch_policy(monkeypatch):
     finally:
         dv.dv_set_launch_overlap(prev)
     assert seen == [0] * dec.L and after == 1 and failed == 1
+
+
+def test_buffers_of_many_tree_sizes_stay_bounded():
+    """Trees of every size up to 24: what is kept for them is bounded by the
+    largest, not by how many sizes there were, and sizes that share buffers
+    give the same results."""
+    def kept(sizes):
+        dec = _decoder(1)
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        for T in sizes:
+            dec.verify_tree(_inputs(1, T, 512, T))
+        dec.check()
+        torch.cuda.synchronize()
+        return torch.cuda.memory_allocated() - before
+
+    one = kept([24])
+    assert kept([24] + list(range(1, 24))) <= 1.01 * one
+    assert kept(range(1, 25)) <= 3 * one
+    dec = _decoder(1)
+    dec.verify_tree(_inputs(1, 24, 512, 24))
+    for T in (1, 5, 16):
+        fresh = _decoder(1)
+        want, got = fresh.verify_tree(_inputs(1, T, 512, T)), dec.verify_tree(_inputs(1, T, 512, T))
+        dec.check(), fresh.check()
+        _close(got, want)
+
+
+def test_verify_refuses_no_nodes():
+    dec = _decoder(1)
+    with pytest.raises(ValueError):
+        dec.verify_tree(torch.zeros(1, 0, 512, device="cuda"))
