@@ -428,8 +428,11 @@ class SparseDecoder:
         dv.dv_kv_reorder(self.kv_layers, self.pos, parent, self.ws_move, start=start)
 
     def check(self):
-        for ws in (self.ws_pred_main, self.ws_pred_side, self.ws_attn, self.ws_mlp, self.ws_move,
-                   *(t[k] for t in self._tree.values() for k in ("ws_pred", "ws_mlp", "ws_tree"))):
-            st, info = dv.dv_check(ws)
+        """Raise the first error that any call has recorded since the last check
+        (all workspaces are read and cleared)."""
+        found = [dv.dv_check(ws) for ws in
+                 (self.ws_pred_main, self.ws_pred_side, self.ws_attn, self.ws_mlp, self.ws_move,
+                  *(t[k] for t in self._tree.values() for k in ("ws_pred", "ws_mlp", "ws_tree")))]
+        for st, info in found:
             if st != 0:
                 raise dv.DvError(st, "decode step", f"info={info}")

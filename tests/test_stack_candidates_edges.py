@@ -229,3 +229,14 @@ def test_verify_refuses_no_nodes():
     dec = _decoder(1)
     with pytest.raises(ValueError):
         dec.verify_tree(torch.zeros(1, 0, 512, device="cuda"))
+
+
+def test_check_reports_a_failure_once():
+    """A refused tree leaves an error in the repair's workspace and in the
+    attention's: one check reads and clears both."""
+    dec = _filled(1, [62])
+    dec.verify_tree(_inputs(1, 5, 512, 40))
+    with pytest.raises(dv.DvError) as e:
+        dec.check()
+    assert e.value.status == 9
+    dec.check()
