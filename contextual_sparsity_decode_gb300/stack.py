@@ -343,9 +343,10 @@ class SparseDecoder:
         tree's nodes share one set of heads per layer, predicted from node 0;
         neurons are predicted node by node, both from the same inputs as in a
         decode step (layer 0 from its own attention input, layer l from layer
-        l - 1's).  The query and output
-        projections are plain library GEMMs with 16-bit results for 16-bit
-        storage."""
+        l - 1's).  The query and output projections are plain library GEMMs
+        over every head.  q and the attention's result are rounded to the
+        storage type, which dv_tree_attn takes and gives (a decode step keeps
+        them in fp32); sums and streams are fp32."""
         B, T, d = E.shape
         if B != self.B or T < 1 or d != self.d or E.dtype != torch.float32:
             raise ValueError(f"E: fp32 [{self.B}][T][{self.d}], T >= 1")
@@ -385,6 +386,7 @@ class SparseDecoder:
         x_new = fits.expand(B, T).reshape(rows, 1)
         flag = (t["head"] + slot[:, :, None]).view(-1)
         bound = (~fits).to(torch.uint8).mul_(255)[:, :, None].expand(B, T, h).reshape(-1)   # min: cleared, or as it is
+        wide = {} if self.dtype == torch.float32 else dict(out_dtype=torch.float32)
         for l in range(self.L):
             W, kv = self.layers[l], self.kv[l]
             dv.dv_layernorm(r, y, self.eps)
@@ -404,7 +406,7 @@ class SparseDecoder:
             dv.dv_tree_attn(q.permute(1, 0, 2).contiguous().view(B, T, h, d_h), kv, self.pos, self.scale,
                             out.view(B, T, h, d_h), t["ws_tree"], mask=mask, nodes=nodes, head_idx=t["head_idx"],
                             head_count=t["head_cnt"])
-            r += torch.mm(out, W["Wo"].view(h * d_h, d))
+            r += torch.mm(out, W["Wo"].view(h * d_h, d), **wide)
             ya = y.clone()
             dv.dv_layernorm(r, y, self.eps)
             for i in range(0, rows, chunk):

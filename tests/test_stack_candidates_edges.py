@@ -240,3 +240,25 @@ def test_check_reports_a_failure_once():
         dec.check()
     assert e.value.status == 9
     dec.check()
+
+
+@pytest.mark.parametrize("keep_all", [True, False])
+def test_the_output_projection_keeps_its_bits(monkeypatch, keep_all):
+    """The streams behind the attention are what the attention gave times Wo, in
+    fp32 as in a decode step: 512 products (2^-24 each of the summed magnitudes)
+    and two roundings, not one to 16 bits."""
+    dec = _decoder(2, keep_all=keep_all)
+    E = _inputs(2, 7, 512, 41)
+    ln, tree = dv.dv_layernorm, dv.dv_tree_attn
+    streams, outs = [], []
+    monkeypatch.setattr(stack.dv, "dv_layernorm", lambda x, *a, **kw: (streams.append(x.clone()), ln(x, *a, **kw)))
+    monkeypatch.setattr(stack.dv, "dv_tree_attn",
+                        lambda *a, **kw: (tree(*a, **kw), outs.append(a[4].clone())))
+    dec.verify_tree(E)
+    dec.check()
+    for l in range(dec.L):
+        before, after = streams[2 * l].double(), streams[2 * l + 1].double()
+        out, Wo = outs[l].view(14, 512).double(), dec.layers[l]["Wo"].view(512, 512).double()
+        want = before + out @ Wo
+        tol = 512 * 2.0 ** -24 * (out.abs() @ Wo.abs()) + 2.0 ** -23 * (want.abs() + before.abs())
+        assert ((after - want).abs() <= tol).all()
