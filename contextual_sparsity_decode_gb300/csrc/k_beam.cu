@@ -196,6 +196,7 @@ struct Ring {
   static constexpr uint32_t kBytes = kBeamTile * sizeof(T) + 32;   // a tile, from and to 16-byte boundaries
 };
 constexpr long long kUnwindNs = 2000000000LL;
+constexpr float kSlack = 1.f;   // exponents up to 1.44: their rounding stays within 2^-24
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_kernel(const BeamLaunch a) {
@@ -250,7 +251,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
   if (tid == 0)
     while (issued < min(ST, tiles)) issue(issued++);
   __syncthreads();  // (tokens stored one by one)
-  float m = -INFINITY, sum = 0.f, tau = -INFINITY;
+  // the thread's maximum, and its sum of exponentials, sum - lost, relative to ref
+  // (as long as there is none, to from = 0)
+  float m = -INFINITY, ref = -INFINITY, from = 0.f, sum = 0.f, lost = 0.f, tau = -INFINITY;
   bool over = false;
   int mine = 0;   // entries of the warp's list
   const Reach reach(a.K);
@@ -276,12 +279,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
       g8[g] = max3(max3(max3(x8[0], x8[1], x8[2]), x8[3], x8[4]), max3(x8[5], x8[6], x8[7]), -INFINITY);
     }
     const float top = fmaxf(g8[0], g8[1]);
-    // the sum is kept relative to the thread's maximum (the difference first: a
-    // logit may be the type's lowest value); a NaN or +inf among the tokens
-    // makes it a NaN
-    const float mn = fmaxf(m, top), ref = mn > -INFINITY ? mn : 0.f;
+    // The sum is kept relative to a reference that follows the thread's maximum
+    // once it is kSlack above: scaled at every rise, the sum of a row that rises
+    // slowly would gather an error with every tile.  The difference is taken
+    // first: a logit may be the type's lowest value.  A NaN or +inf among the
+    // tokens makes the sum a NaN.
+    const float mn = fmaxf(m, top);
+    const bool moved = mn > ref + kSlack;
+    const float keep = moved ? ex2((ref - mn) * kLog2e) : 1.f;   // (0 from -inf: the sum was 0, or a NaN)
+    ref = moved ? mn : ref;
+    from = moved ? mn : from;
     u64 s2[2] = {0, 0};   // (two tokens an instruction: 52.5 us instead of 54.4 at 48 x 10 rows)
-    const u64 minus_ref = pack2(-ref, -ref), log2e = pack2(kLog2e, kLog2e);
+    const u64 minus_ref = pack2(-from, -from), log2e = pack2(kLog2e, kLog2e);
 #pragma unroll
     for (int i = 0; i < 8 * kGroups; i += 2) {
       float y0, y1;
@@ -291,7 +300,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     float s4[4];
     open2(s2[0], &s4[0], &s4[1]);
     open2(s2[1], &s4[2], &s4[3]);
-    sum = fmaf(sum, m > -INFINITY ? ex2((m - ref) * kLog2e) : 1.f, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+    // Compensated: a part may have 1024 tiles, and a plain fp32 sum of a flat row
+    // rounds the same way at each (1.2e-5 off in all); beams are compared by it.
+    const float add = __fmaf_rn(-lost, keep, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+    const float old = sum * keep, next = __fadd_rn(old, add);
+    lost = __fsub_rn(__fsub_rn(next, old), add);
+    sum = next;
     m = mn;
     const bool sharpen = k < 4 || (k & 3) == 0;   // (the maxima change ever more slowly)
     if (sharpen) {
@@ -344,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
       if (!tc::mbar_wait(&full[k % ST], (k / ST) & 1, kUnwindNs > a.wait_ns ? kUnwindNs : a.wait_ns)) break;
   // the part's maximum and sum
   const float wm = warp_max(m);
-  const float ws = warp_sum(m > -INFINITY ? sum * ex2((m - wm) * kLog2e) : sum != sum ? sum : 0.f);
+  sum -= lost;
+  const float ws = warp_sum(m > -INFINITY ? sum * ex2((ref - wm) * kLog2e) : sum != sum ? sum : 0.f);
   if (lane == 0) {
     redm[wid] = wm;
     reds[wid] = ws;

@@ -1,0 +1,90 @@
+"""Operators for several candidates per sequence at sizes that take their less
+common branches, against the same references in 64 bits.
+
+Relative error of a row's sum of exponentials, and so the error of its
+log-sum-exp, whatever the row (half-steps of 2^-24): the terms, and the scalings
+of a warp's, a block's and a part's sum are exponentials of 2^-22 each, 4 x 4; a
+thread's sum is scaled by one when the maximum rises by 1, at most 16 times
+before what it held is below the new maximum's term alone (e^-16 2^22 < 1), 5 with
+its product's rounding: 16 x 5; arguments, up to 22 in all (lower terms do not
+count), are rounded three times, 3 x 22; a tile's 16 terms take five additions,
+the running sum stays within 2, a part's 256 sums take eight: 15.  Together 177
+half-steps; a score is rounded once more."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from contextual_sparsity_decode_gb300 import binding as dv
+from test_candidates import DT, Case, _beam_ref, _cache, _compact_ref, _copy, _gen, _i32, _same
+from test_guards import Guarded
+
+pytestmark = pytest.mark.gpu
+
+TIMEOUT = 6
+LSE_TOL = 177 * 2.0 ** -24
+
+
+def _select(logits, cum, K, done=None, end=0):
+    S, W, V = logits.shape
+    ws = dv.workspace(dv.dv_beam_select_workspace_size(S, W, V, K))
+    score = torch.full((S, K), float("nan"), device="cuda")
+    token, beam = (torch.full((S, K), -1, dtype=torch.int32, device="cuda") for _ in range(2))
+    dv.dv_beam_select(logits, cum, score, token, beam, ws, done=done, end_token=end)
+    assert dv.dv_check(ws) == (0, 0)
+    return score, token, beam
+
+
+def _beam_check(logits, cum, K, done=None, end=0):
+    """Tokens and beams exactly, scores within LSE_TOL and their rounding."""
+    rs, rt, rb = _beam_ref(logits, cum, K, None if done is None else done.cpu().numpy(), end)
+    score, token, beam = _select(logits, cum, K, done, end)
+    assert np.array_equal(token.cpu().numpy(), rt) and np.array_equal(beam.cpu().numpy(), rb)
+    got = score.double().cpu().numpy()
+    fine = np.isfinite(rs)
+    assert np.array_equal(fine, np.isfinite(got)) and (got[~fine] == -np.inf).all()
+    assert (np.abs(got[fine] - rs[fine]) <= 2.0 ** -24 * np.abs(rs[fine]) + LSE_TOL).all()
+
+
+def test_beam_sums_do_not_lose_bits_with_the_vocabulary():
+    """304 rows of 2^22 tokens, one part each: 0 for the first 4096, then one
+    value -u for the rest, another for every row.  A running fp32 sum rounds the
+    same way at every step (up to 1e-5 in all).
+
+    Tolerance of a score: its own rounding, 2^-24 relative, and the
+    log-sum-exp's relative error: an exponential, 2^-22 (two units in the last
+    place), its argument, |u| <= 0.6, below 2^-24; a tile's 16 terms, five
+    additions; the running sum, kept to 2 x 2^-24; a part's 256 sums, eight
+    additions: 4 + 1 + 5 + 2 + 8 = 20 half-steps of 2^-24."""
+    S, W, V, K = 38, 8, 1 << 22, 8
+    u = torch.arange(1, S * W + 1, device="cuda").float().div(512).view(S, W)       # exact in f16
+    logits = (-u)[:, :, None].expand(S, W, V).to(torch.float16).contiguous()
+    logits[:, :, :4096] = 0
+    score, token, beam = _select(logits, torch.zeros(S, W, device="cuda"), K)
+    lse = (4096 + (V - 4096) * torch.exp(-u.double())).log()                        # descends with u
+    assert (beam == W - 1).all() and torch.equal(token, torch.arange(K, device="cuda").int().expand(S, K))
+    want = -lse[:, -1:]
+    err = (score.double() - want).abs() - (2.0 ** -24 * want.abs() + 20 * 2.0 ** -24)
+    assert err.max() <= 0, err.max()
+    # every row, as the only beam of its sequence
+    score, _, _ = _select(logits.view(S * W, 1, V), torch.zeros(S * W, 1, device="cuda"), 1)
+    want = -lse.view(-1, 1)
+    err = (score.double() - want).abs() - (2.0 ** -24 * want.abs() + 20 * 2.0 ** -24)
+    assert err.max() <= 0, err.max()
+
+
+def test_beam_sums_of_rows_that_rise():
+    """The maximum grows with every tile, a little or by much, and the sum has
+    to follow: logits a v / V for a = 0.01 ... 40."""
+    rows, V = 304, 1 << 18
+    a = torch.logspace(-2, math.log10(40), rows, device="cuda")
+    x = (a[:, None] * (torch.arange(V, device="cuda") / V)[None]).view(rows, 1, V).contiguous()
+    score, token, _ = _select(x, torch.zeros(rows, 1, device="cuda"), 1)
+    lse = torch.logsumexp(x.double(), 2)
+    top, at = x.max(2)
+    want = top.double() - lse
+    tol = 2.0 ** -24 * want.abs() + LSE_TOL
+    assert ((score.double() - want).abs() <= tol).all()
+    assert (x.gather(2, token.long()[:, :, None])[..., 0] == top).all()
