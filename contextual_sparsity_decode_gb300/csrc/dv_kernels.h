@@ -325,6 +325,7 @@ cudaError_t launch_kv_reorder(const KvMove& m, int width, const int32_t* start, 
 constexpr int kBeamTile = 4096;    // tokens that a CTA takes at a time
 constexpr int kBeamMaxWidth = 32;
 constexpr int kBeamMaxK = 64;
+constexpr int kBeamMaxV = 1 << 22;
 struct BeamLaunch {
   const void* logits; long long ld;          // [S][W] rows of V, ld elements apart
   const float* cum; const uint8_t* done; int end;

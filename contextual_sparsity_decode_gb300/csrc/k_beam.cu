@@ -6,7 +6,8 @@
 // Within a beam the order is that of the logits themselves (the log-sum-exp is
 // one number per row), so the selection inside a row is exact and needs no
 // arithmetic; only the candidates of different beams are compared by score, in
-// double precision.
+// double precision (and those of a beam whose scores round to the same double by
+// their logits).
 //
 // One pass over the logits of the beams that are not done (the floor: each is
 // read once; 48 x 10 rows of 128001 bf16 logits with a fifth of the beams done
@@ -122,10 +123,15 @@ __device__ __forceinline__ U block_rth(U v, int r, U* all, U* result) {
 // A candidate of the join: its score as an order-preserving integer, and where
 // it is.  Comparing integers keeps double-precision work, slow on this GPU, to
 // the few that are listed.
-struct Cand {
-  u64 key;
-  int w, v;  // v < 0: none
+// The tie orders equal scores: by beam, then by logit, larger first (scores that
+// are equal in double precision may differ), then by token.
+struct __align__(16) Cand {
+  u64 key, tie;
 };
+static_assert(kBeamMaxWidth <= 1 << 10 && kBeamMaxV <= 1 << 22, "a tie: 10 bits of beam, 32 of logit, 22 of token");
+__device__ __forceinline__ u64 tie_of(int w, float x, int v) {
+  return ((u64)w << 54) | ((u64)~ord32(x) << 22) | (uint32_t)v;
+}
 __device__ __forceinline__ u64 ord64(double d) {
   const u64 u = (u64)__double_as_longlong(d + 0.0);
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
@@ -134,8 +140,7 @@ __device__ __forceinline__ double unord64(u64 o) {
   return __longlong_as_double((long long)((o >> 63) ? (o & 0x7fffffffffffffffull) : ~o));
 }
 __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
-  if (a.key != b.key) return a.key > b.key;
-  return a.w != b.w ? a.w < b.w : a.v < b.v;
+  return a.key != b.key ? a.key > b.key : a.tie < b.tie;
 }
 
 struct JoinRow {
@@ -161,8 +166,8 @@ __device__ __forceinline__ void join_bounds(const JoinRow& r, float x, bool ends
 
 __device__ __forceinline__ void put(const BeamLaunch& a, int s, int k, const Cand& c) {
   a.score[(size_t)s * a.K + k] = (float)unord64(c.key);
-  a.token[(size_t)s * a.K + k] = c.v;
-  a.beam[(size_t)s * a.K + k] = c.w;
+  a.token[(size_t)s * a.K + k] = (int)(c.tie & ((1u << 22) - 1));
+  a.beam[(size_t)s * a.K + k] = (int)(c.tie >> 54);
 }
 
 // Cuts a list of n entries (0: none) back to those that reach the K-th largest
@@ -552,14 +557,16 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamLaunch a)
   const uint32_t t = block_reached(best, a.K, red);
   // the candidate of an entry whose upper bound reaches t
   const auto candidate = [&](int i, const int2& p, Cand* c) {
+    int w;
     float x, lo, hi;
     bool ends;
-    c->v = entry(i, p, &c->w, &x, &ends);
-    if (c->v < 0) return false;
-    const JoinRow& r = rows[c->w];
+    const int v = entry(i, p, &w, &x, &ends);
+    if (v < 0) return false;
+    const JoinRow& r = rows[w];
     join_bounds(r, x, ends, &lo, &hi);
     if (ord32(hi) < t) return false;
     c->key = ord64(ends ? r.base : r.kind != 0 ? -INFINITY : (double)r.cum + ((double)x - r.base));
+    c->tie = tie_of(w, x, v);
     return true;
   };
   const auto add = [&](int i, const int2& p) {
@@ -585,9 +592,9 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamLaunch a)
     return;
   }
   // more equal scores than the list holds: one more of the best each round
-  Cand prev{~0ull, -1, -1};
+  Cand prev{~0ull, 0};
   for (int k = 0; k < a.K; ++k) {
-    Cand top{0, kBeamMaxWidth, 0};
+    Cand top{0, ~0ull};
     for (int i = tid; i < total; i += kThreads) {
       Cand c;
       if (candidate(i, read(i, kHeld), &c) && before(prev, c) && before(c, top)) top = c;
@@ -596,8 +603,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamLaunch a)
     for (int o = 16; o > 0; o >>= 1) {
       Cand d;
       d.key = __shfl_xor_sync(0xffffffffu, top.key, o);
-      d.w = __shfl_xor_sync(0xffffffffu, top.w, o);
-      d.v = __shfl_xor_sync(0xffffffffu, top.v, o);
+      d.tie = __shfl_xor_sync(0xffffffffu, top.tie, o);
       if (before(d, top)) top = d;
     }
     if (lane == 0) redc[wid] = top;

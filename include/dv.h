@@ -388,7 +388,8 @@ dv_status dv_beam_select_workspace_size(int n_seq, int width, int V, int K,
  *     offers end_token at score cum[s][w] and every other token at -inf.
  * Beams that have not ended: a row whose log-sum-exp is not finite (a NaN, a
  * +inf, or nothing above -inf) and a row whose cum is not finite offer every
- * token at -inf.  Candidates are compared in double precision.  A row's
+ * token at -inf.  A beam's candidates are in the order of its logits, those of
+ * different beams are compared in double precision.  A row's
  * log-sum-exp is taken over fp32 exponentials, summed with compensation within
  * a part of the row, in fp32 over the part's threads and in double over parts:
  * about 2^-21.4 off at most in rows that were tried, 177 x 2^-24 in any row,

@@ -88,3 +88,21 @@ def test_beam_sums_of_rows_that_rise():
     tol = 2.0 ** -24 * want.abs() + LSE_TOL
     assert ((score.double() - want).abs() <= tol).all()
     assert (x.gather(2, token.long()[:, :, None])[..., 0] == top).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_a_beam_s_tokens_are_in_the_order_of_their_logits(dt):
+    """Logits so small that their scores are equal in double precision: whatever
+    K is, a beam's tokens come by logit, and equal ones by index."""
+    x = torch.zeros(1, 2, 40, device="cuda")
+    x[0, :, 0], x[0, :, 7], x[0, :, 30] = 1e-20, 2e-20, 3e-20
+    x[0, :, 1] = -1e-20
+    order = [30, 7, 0, 2, 3, 4]
+    for K in range(1, 7):
+        score, token, beam = _select(x.to(DT[dt]), torch.tensor([[0.0, -1.0]], device="cuda"), K)
+        assert token[0].tolist() == order[:K] and beam[0].tolist() == [0] * K
+    many = torch.zeros(1, 32, 100, device="cuda")      # ... and where the candidates do not fit a list
+    many[0, :, 0], many[0, :, 7] = 1e-20, 2e-20
+    cum = torch.zeros(1, 32, device="cuda")
+    _, token, beam = _select(many.to(DT[dt]), cum, 64)
+    assert token[0].tolist() == [7, 0] + [v for v in range(64) if v not in (0, 7)] and (beam == 0).all()
