@@ -565,9 +565,8 @@ KvMove make_move(const dv_kv* kv, int n_kv, int B, int d, int h, int d_h, const 
 }
 
 bool beam_shape_ok(int n_seq, int width, int V, int K) {
-  return n_seq >= 1 && width >= 1 && width <= kBeamMaxWidth && (long long)n_seq * width <= 65535 && V >= 1 && V <= kBeamMaxV &&
-         K >= 1 &&
-         K <= kBeamMaxK && (long long)K <= (long long)width * V;
+  return n_seq >= 1 && width >= 1 && width <= kBeamMaxWidth && (long long)n_seq * width <= 65535 && V >= 1 &&
+         V <= kBeamMaxV && K >= 1 && K <= kBeamMaxK && (long long)K <= (long long)width * V;
 }
 }  // namespace
 

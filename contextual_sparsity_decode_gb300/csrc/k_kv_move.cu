@@ -179,9 +179,10 @@ __global__ void __launch_bounds__(kMoveThreads) reorder_kernel(const __grid_cons
   const size_t row0 = (size_t)s * a.W, flag_beam = (size_t)a.h * a.n_max;
   const size_t first = is_x ? row0 * a.n_max : (row0 * a.h + part) * a.n_max;
   uint8_t* flags = is_x ? nullptr : kv.valid + first;
-  const int lo = a.start ? max(a.start[s], 0) : 0;
-  if (lo >= a.n_max || lo + (int)blockIdx.y * a.span >= a.n_max) return;
+  const int lo = a.start ? min(max(a.start[s], 0), a.n_max) : 0;
+  const bool report = part == 0 && layer == 0 && blockIdx.y == 0;   // this CTA's sequence, once, whatever moves
   const int j0 = lo + blockIdx.y * a.span;
+  if (j0 >= a.n_max && !report) return;
   if (threadIdx.x >= 128 && threadIdx.x < 128 + a.span) {  // the flags do not wait for the parents
     const int j = j0 + threadIdx.x - 128;
     uint32_t m = is_x ? ~0u : 0u;
@@ -198,7 +199,6 @@ __global__ void __launch_bounds__(kMoveThreads) reorder_kernel(const __grid_cons
     if (w < a.W) {
       int top = a.pos[s * a.W + w];
       p = a.parent[s * a.W + w];
-      const bool report = part == 0 && layer == 0 && blockIdx.y == 0;
       if (p < 0 || p >= a.W) {
         if (report) set_error(a.hdr, DV_ERR_INDEX_RANGE, p);
         p = w;
@@ -212,8 +212,7 @@ __global__ void __launch_bounds__(kMoveThreads) reorder_kernel(const __grid_cons
       if (pq == w && q != w) mine |= 1u << q;
     }
     if (w < a.W) {
-      if (mine && upto[w] < 0 && part == 0 && layer == 0 && blockIdx.y == 0)
-        set_error(a.hdr, DV_ERR_POSITION, a.pos[s * a.W + w]);
+      if (mine && upto[w] < 0 && report) set_error(a.hdr, DV_ERR_POSITION, a.pos[s * a.W + w]);
       heirs[w] = mine;
       if (!mine || upto[w] < 0) upto[w] = 0;
     } else if (w < WM) {

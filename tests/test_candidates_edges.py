@@ -106,3 +106,19 @@ def test_a_beam_s_tokens_are_in_the_order_of_their_logits(dt):
     cum = torch.zeros(1, 32, device="cuda")
     _, token, beam = _select(many.to(DT[dt]), cum, 64)
     assert token[0].tolist() == [7, 0] + [v for v in range(64) if v not in (0, 7)] and (beam == 0).all()
+
+
+@pytest.mark.parametrize("start", [16, 17, 2 ** 31 - 1])
+def test_reorder_reports_errors_behind_the_last_position(start):
+    """Nothing to move (the beams share everything): a parent that is none is
+    reported all the same, and nothing changes."""
+    kvs = _cache(2, 3, 2, 16, 64, "f16", 5)
+    want = _copy(kvs)
+    layers, ws = dv.KVLayers(kvs), dv.workspace(256)
+    dv.dv_kv_reorder(layers, _i32([16, 16, 16]), _i32([[1, 3, 0]]), ws, start=_i32([start]))
+    assert dv.dv_check(ws) == (5, 3)
+    dv.dv_kv_reorder(layers, _i32([16, 17, 16]), _i32([[1, 1, 2]]), ws, start=_i32([start]))
+    assert dv.dv_check(ws) == (9, 17)
+    dv.dv_kv_reorder(layers, _i32([16, 16, 16]), _i32([[1, 2, 0]]), ws, start=_i32([start]))
+    assert dv.dv_check(ws) == (0, 0)
+    _same(kvs, want)
