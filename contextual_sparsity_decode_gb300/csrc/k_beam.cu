@@ -249,6 +249,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) beam_scan_ke
     if (cut)
       for (int e = 0; e < n && off + (e + 1) * sizeof(T) <= 16; ++e) tokens[e] = x[e];
     for (int e = n - 1; e >= 0 && b0 + off + (long long)(e + 1) * sizeof(T) > b1; --e) tokens[e] = x[t0 + e];
+    // a stage that held tokens stored one by one, and was read by every thread
+    // before the last barrier, is written by a copy: order the two kinds of access
+    tc::fence_proxy_async();
     tc::mbar_arrive_expect_tx(&full[k % ST], bytes);
     if (bytes) tc::bulk_g2s(stage + cut, begin + b0 + cut, bytes, &full[k % ST]);
   };

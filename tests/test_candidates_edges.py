@@ -122,3 +122,13 @@ def test_reorder_reports_errors_behind_the_last_position(start):
     dv.dv_kv_reorder(layers, _i32([16, 16, 16]), _i32([[1, 2, 0]]), ws, start=_i32([start]))
     assert dv.dv_check(ws) == (0, 0)
     _same(kvs, want)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_beam_rows_off_a_boundary_over_many_tiles(dt):
+    """Rows that begin off a 16-byte boundary, the first and the last at the very
+    ends of their memory, and long enough that every stage of the ring is used
+    again after tokens were stored to it one by one."""
+    S, V, K = 304, 65537, 5
+    big = torch.randn(S * V + 1, generator=_gen(71), device="cuda").to(DT[dt])
+    _beam_check(big[1:].view(S, 1, V), -torch.rand(S, 1, generator=_gen(72), device="cuda"), K)
