@@ -132,3 +132,63 @@ def test_beam_rows_off_a_boundary_over_many_tiles(dt):
     S, V, K = 304, 65537, 5
     big = torch.randn(S * V + 1, generator=_gen(71), device="cuda").to(DT[dt])
     _beam_check(big[1:].view(S, 1, V), -torch.rand(S, 1, generator=_gen(72), device="cuda"), K)
+
+
+@pytest.mark.tc
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("d_h", [64, 128])
+def test_tree_attention_waits_give_up(dt, d_h):
+    """With a limit of a nanosecond the copies' producer gives up at a ring that
+    the products have not freed (a CTA has several dozen tiles), and every other
+    role behind it.  The call reports it, writes nothing outside its outputs,
+    and the next one is right, bit for bit."""
+    c = Case(dt, d_h, [4000] * 4, 64, 32, seed=41, n_max=4064)
+    c.call()
+    assert dv.dv_check(c.ws) == (0, 0)
+    want = c.out.clone()
+    out, ws = Guarded(tuple(c.out.shape), DT[dt]), Guarded((c.ws.numel(),), torch.uint8)
+    c.out, c.ws = out.t, ws.t
+    statuses = []
+    prev = dv.dv_set_wait_limit_ns(1)
+    try:
+        for _ in range(3):
+            c.call()
+            statuses.append(dv.dv_check(c.ws)[0])
+    finally:
+        dv.dv_set_wait_limit_ns(prev)
+    assert TIMEOUT in statuses and set(statuses) <= {0, TIMEOUT}, statuses
+    c.out.zero_()
+    c.call()
+    assert dv.dv_check(c.ws) == (0, 0)
+    assert torch.equal(c.out, want) and out.intact() and ws.intact()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_beam_scan_waits_give_up(dt):
+    """The same of the beam selection's scan: the logits are out of the L2 cache,
+    and its first copy is still on its way."""
+    big = torch.empty(1 << 29, dtype=torch.uint8, device="cuda")
+    S, W, V, K = 6, 8, 60001, 16
+    logits = torch.randn(S, W, V, generator=_gen(61), device="cuda").to(DT[dt])
+    cum = -torch.rand(S, W, generator=_gen(62), device="cuda")
+    ws = Guarded((dv.dv_beam_select_workspace_size(S, W, V, K),), torch.uint8)
+    score = Guarded((S, K), torch.float32)
+    token, beam = Guarded((S, K), torch.int32), Guarded((S, K), torch.int32)
+    call = lambda: dv.dv_beam_select(logits, cum, score.t, token.t, beam.t, ws.t)  # noqa: E731
+    call()
+    assert dv.dv_check(ws.t) == (0, 0)
+    want = [x.t.clone() for x in (score, token, beam)]
+    statuses = []
+    prev = dv.dv_set_wait_limit_ns(1)
+    try:
+        for _ in range(3):
+            big.fill_(1)
+            torch.cuda.synchronize()
+            call()
+            statuses.append(dv.dv_check(ws.t)[0])
+    finally:
+        dv.dv_set_wait_limit_ns(prev)
+    assert TIMEOUT in statuses and set(statuses) <= {0, TIMEOUT}, statuses
+    call()
+    assert dv.dv_check(ws.t) == (0, 0)
+    assert all(torch.equal(x.t, w) and x.intact() for x, w in zip((score, token, beam), want)) and ws.intact()
