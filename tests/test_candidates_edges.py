@@ -192,3 +192,85 @@ def test_beam_scan_waits_give_up(dt):
     call()
     assert dv.dv_check(ws.t) == (0, 0)
     assert all(torch.equal(x.t, w) and x.intact() for x, w in zip((score, token, beam), want)) and ws.intact()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("V", [100, 9001])
+def test_beam_more_equal_candidates_than_a_list_holds(dt, V):
+    """32 beams of equal logits, 64 wanted: more than 1024 candidates reach the
+    last place."""
+    x = torch.zeros(2, 32, V, device="cuda", dtype=DT[dt])
+    cum = torch.zeros(2, 32, device="cuda")
+    cum[1, 5:] = -0.5
+    _beam_check(x, cum, 64)
+    x[:, ::3, V // 2] = 1.0
+    done = torch.zeros(2, 32, dtype=torch.uint8, device="cuda")
+    done[:, 1::4] = 1
+    _beam_check(x, cum, 64, done, V // 3)
+
+
+@pytest.mark.parametrize("dt,S,W,V,K", [("f16", 1, 2, 300001, 16), ("f32", 1, 1, 1000003, 64), ("bf16", 2, 2, 262145, 5),
+                                        ("bf16", 1, 1, 4194304, 33)])
+def test_beam_rows_of_many_parts(dt, S, W, V, K):
+    """More parts a row than a warp has lanes."""
+    g = _gen(V)
+    x = (3 * torch.randn(S, W, V, generator=g, device="cuda")).to(DT[dt])
+    cum = -torch.rand(S, W, generator=g, device="cuda")
+    _beam_check(x, cum, K)
+    x[..., :] = (torch.arange(V, device="cuda") // 50000).float().to(DT[dt])       # runs over several parts
+    _beam_check(x, cum, K)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("K", [1, 7, 64])
+def test_beam_lists_cut_back_inside_a_part(dt, K):
+    """80 rows of 50003 tokens (parts of several tiles) that fill the lists of
+    groups: ascending, descending, in runs, ties of a few values, the best in the
+    hands of a few threads."""
+    S, V = 80, 50003
+    v = torch.arange(V, device="cuda")
+    g = _gen(K)
+    rows = torch.stack([
+        v / V, -v / V, (v // 700 % 5).float(), (v // 4096).float(), (v % 4096 // 16).float(),
+        torch.randint(0, 3, (V,), generator=g, device="cuda").float(),
+        torch.where((v // 8) % 256 < 9, 4.0 + torch.randn(V, generator=g, device="cuda"), torch.full((V,), -4.0, device="cuda")),
+        torch.where(v % 4096 > 2000, v / V, torch.full((V,), -float("inf"), device="cuda")),
+    ])
+    x = rows[torch.arange(S, device="cuda") % len(rows)][:, None].to(DT[dt]).contiguous()
+    _beam_check(x, -torch.rand(S, 1, generator=g, device="cuda"), K)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("B", [32, 33, 64, 70])
+def test_tree_attention_of_many_sequences(dt, B):
+    """Around and above the 32 sequences that a warp plans at once."""
+    Case(dt, 64, [(29 * b) % 190 for b in range(B)], 4, 2, nodes=[(b * 7 + 1) % 5 for b in range(B)], mask="tree", seed=B).check()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+def test_tree_attention_of_the_largest_batch(dt):
+    B = 512
+    Case(dt, 64, [(b * 37) % 90 for b in range(B)], 2, 1, nodes=[(b * 5 + 1) % 3 for b in range(B)], mask=None, seed=3,
+         heads=[[0] if b % 11 else [] for b in range(B)]).check()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_compact_of_long_lists(dt):
+    """Lists of more entries than a warp reads at once, kept in place and from
+    further back; lists that stop ascending where one read ends."""
+    B, cap, n_max = 6, 70, 160
+    up = list(range(0, 140, 2))
+    lists = [list(range(64)), up[:33], up, list(range(3, 67)), up[:32] + [62] + up[33:40], up[:31] + [58, 70]]
+    pos = [5, 0, 20, 90, 4, 6]
+    kvs = _cache(2, B, 2, n_max, 64, dt, 77)
+    want = _copy(kvs)
+    idx = torch.zeros(B, cap, dtype=torch.int32)
+    for b, x in enumerate(lists):
+        idx[b, :len(x)] = torch.tensor(x, dtype=torch.int32)
+    for b in range(4):
+        _compact_ref(want, b, pos[b], lists[b])
+    layers, ws, p = dv.KVLayers(kvs), dv.workspace(256), _i32(pos)
+    dv.dv_kv_compact(layers, p, idx.cuda(), _i32([len(x) for x in lists]), ws, new_pos=p)
+    assert dv.dv_check(ws)[0] == 5
+    _same(kvs, want)
+    assert p.tolist() == [a + len(x) for a, x in zip(pos[:4], lists)] + pos[4:]

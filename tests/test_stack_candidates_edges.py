@@ -1,12 +1,14 @@
 """The verify pass where its nodes meet the cache's end, are padding, or share
 few heads and neurons; what it leaves alone, and what it keeps."""
 
+import math
+
 import pytest
 import torch
 
 from contextual_sparsity_decode_gb300 import binding as dv
 from contextual_sparsity_decode_gb300 import stack
-from test_stack_candidates import _close, _decoder, _inputs
+from test_stack_candidates import N_PROMPT, TOL, _close, _decoder, _inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -262,3 +264,75 @@ def test_the_output_projection_keeps_its_bits(monkeypatch, keep_all):
         want = before + out @ Wo
         tol = 512 * 2.0 ** -24 * (out.abs() @ Wo.abs()) + 2.0 ** -23 * (want.abs() + before.abs())
         assert ((after - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("B,T,tree", [(1, 5, True), (2, 9, False), (3, 20, True)])
+def test_sparse_trees_of_several_nodes(monkeypatch, B, T, tree):
+    """Few heads and neurons kept, several nodes: the streams against the same
+    pass in 64 bits with the sets that the predictor gave.  The sets' inputs are
+    checked too: heads from node 0, neurons node by node, both from the layer
+    before (layer 0: its own attention input).
+
+    y is rounded to the storage type in both; the pass rounds q, the attention's
+    output and its projection as well (see TOL), and a y that falls across a
+    rounding moves by a step."""
+    dec = _decoder(B, keep_all=False)
+    E = _inputs(B, T, 512, 38)
+    mask = torch.ones(T, T, dtype=torch.bool).tril()
+    if tree:                                  # two chains that share node 0
+        odd = torch.arange(T) % 2
+        mask &= (odd[:, None] == odd[None, :]) | (torch.arange(T) == 0)[None, :]
+    sets = []
+    predict = dv.dv_predict
+
+    def spy(y, predictors, *a, **kw):
+        predict(y, predictors, *a, **kw)
+        (p,) = predictors
+        sets.append((y.clone(), p.idx.clone(), p.count.clone()))
+
+    monkeypatch.setattr(stack.dv, "dv_predict", spy)
+    got = dec.verify_tree(E, mask=mask.cuda() if tree else None)
+    dec.check()
+    monkeypatch.undo()
+    h, d_h, d = dec.h, dec.d_h, dec.d
+    chunks = (B * T + 31) // 32
+    assert len(sets) == dec.L * (1 + chunks)
+
+    def ln(r):
+        m = r.mean(-1, keepdim=True)
+        v = ((r - m) ** 2).mean(-1, keepdim=True)
+        return ((r - m) / (v + dec.eps).sqrt()).to(dec.dtype).double()
+
+    def near(y, want):                        # stored values: half a step each, and what came in
+        e = float((y.double() - want).norm() / want.norm())
+        assert e <= TOL, e
+
+    r, src = E.double().reshape(B * T, d), None
+    for l in range(dec.L):
+        W = {k: v.double() for k, v in dec.layers[l].items()}
+        y = ln(r)
+        src = y if l == 0 else src
+        calls = sets[l * (1 + chunks):(l + 1) * (1 + chunks)]
+        near(calls[0][0], src.view(B, T, d)[:, 0])
+        near(torch.cat([c[0] for c in calls[1:]]), src)
+        att = torch.zeros(B * T, d, dtype=torch.float64, device="cuda")
+        for b in range(B):
+            rows = y.view(B, T, d)[b]
+            X = torch.cat([dec.kv[l].X[b, :N_PROMPT].double(), rows])
+            see = torch.cat([torch.ones(T, N_PROMPT, dtype=torch.bool), mask], 1).cuda()
+            idx = calls[0][1][b, :int(calls[0][2][b])].tolist()
+            assert len(idx) == dec.k_heads < h
+            for i in idx:
+                q, k, v = (x @ W["Wqkv"][i, m].T for x, m in ((rows, 0), (X, 1), (X, 2)))
+                s = (q @ k.T * dec.scale).masked_fill(~see, -math.inf)
+                att.view(B, T, d)[b] += torch.softmax(s, 1) @ v @ W["Wo"][i]
+        r = r + att
+        ya, y = y, ln(r)
+        out = torch.zeros_like(r)
+        for n in range(B * T):
+            _, idx, cnt = calls[1 + n // 32]
+            j = idx[n % 32, :int(cnt[n % 32])].long()
+            assert len(j) == dec.k_neurons < dec.N
+            out[n] = torch.relu(W["W1n"][j] @ y[n]) @ W["W2n"][j]
+        r, src = r + out, ya
+    near(got.reshape(B * T, d), r)
