@@ -2,6 +2,7 @@
 // Every entry point checks its arguments on the host before launching
 // anything and never synchronises (except dv_check).
 
+#include <cfloat>
 #include <cstdint>
 #include <cstring>
 
@@ -592,7 +593,7 @@ dv_status dv_tree_attn(const void* q, int B, int T, int h, int group, int d_h, c
   if (!tree_shape_ok(B, T, h, group)) return DV_ERR_INVALID_ARG;
   if (d_h != 64 && d_h != 128) return DV_ERR_UNSUPPORTED;
   if (head_idx && (cap < 1 || cap > h)) return DV_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || scale > 3.4e38f) return DV_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale * kLog2e <= FLT_MAX)) return DV_ERR_INVALID_ARG;
   if (kv->n_max < 16 || kv->n_max > 1048576 || kv->n_max % 16) return DV_ERR_INVALID_ARG;
   // the kernels number the tiles of 64 keys (times 16 rows at least) in 32 bits
   if ((double)B * (head_idx ? cap : h) * ((T * group + 15) / 16) * (kv->n_max / 64 + 1) >= 4294967296.0)

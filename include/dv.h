@@ -319,7 +319,7 @@ dv_status dv_tree_attn_workspace_size(int B, int T, int h, int group, int d_h,
  *     (1); node t sees node u where mask[t][u] != 0.  NULL: u <= t, a linear
  *     draft or a chunk of a prompt.  K/V of a node that a row does not see do
  *     not reach that row, whatever they hold.
- *  scale > 0, finite.
+ *  scale > 0, scale log2(e) finite.
  *  head_idx [B][cap] with head_count [B]: the K/V heads of each sequence's
  *     tree, as in dv_sparse_attn, each at most once; both NULL: all h heads.
  * Every row of out is written: those of other heads, of nodes behind

@@ -219,3 +219,11 @@ def test_tree_attention_refuses_lists_of_other_sizes(kw):
                         head_idx=torch.zeros(kw.get("head_idx", (2, 2)), **i32),
                         head_count=torch.zeros(kw.get("count", 2), **i32))
     assert e.value.status == INVALID
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3.4e38, 3.4028235e38])
+def test_tree_attention_refuses_a_scale_that_overflows_to_base_two(scale):
+    """scale log2(e) multiplies the scores: infinite, it would make a NaN of 0."""
+    need = dv.dv_tree_attn_workspace_size(2, 5, 4, 1, 64)
+    assert _tree(ws_bytes=need, scale=scale) == INVALID
+    assert _tree(ws_bytes=need - 1, scale=2.3e38) == WORKSPACE      # (refused for its workspace only)
