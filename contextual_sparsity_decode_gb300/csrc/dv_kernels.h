@@ -35,9 +35,16 @@ void count_launches(int n);
 long long launches_total();
 
 // Launch with an optional programmatic dependency on the previous kernel of
-// the stream (see grid_dep_wait / grid_dep_launch).  Used only between the
-// kernels of one entry point, whose data dependencies are known; the first
-// kernel of every entry point is launched the ordinary way.
+// the stream (see grid_dep_wait / grid_dep_launch).  Used between the kernels of
+// one entry point, whose data dependencies are known, and for three first
+// kernels, those of dv_layernorm, dv_tree_attn and dv_beam_select, whatever
+// launch_overlap() is: they may start while the kernel before the call runs, so
+// they touch no global memory before grid_dep_wait().  Every other first kernel
+// is launched the ordinary way, but for batch-1 attention and MLP calls under
+// launch_overlap().  A kernel that lets its successor start before its own wait
+// (the layernorm, the tree attention's join) does so while the kernel before it
+// may still run: what a successor reads before it waits must be written by
+// neither of the two.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                      bool pdl, int cluster_x, Args&&... args) {

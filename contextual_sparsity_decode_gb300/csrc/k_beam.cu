@@ -625,10 +625,14 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamLaunch a)
 
 namespace {
 
-// Tiles of a part.  Time is that of the tiles on the busiest SM, a part's start
-// and end costing about two more, and of a round's latency (about eight tiles)
-// for every time the GPU is filled (`per_sm` CTAs an SM); the least is taken,
-// fewer parts where equal.
+// Tiles of a part.  Time is taken to be that of the tiles on the busiest SM, a
+// part's start and end costing about two more, and of a round's latency (about
+// eight tiles) for every time the GPU is filled (`per_sm` CTAs an SM); the least
+// is taken, fewer parts where equal.  The constants fit 480 rows of 128001 bf16
+// logits (parts of 8, 11 and 32 tiles: 57, 53 and 58 us; of 16: 51.6).  CTAs
+// that share an SM are counted as if they ran one after another, which is too
+// much below about four: 64 rows of 50257 get two parts each, and latency, not
+// the tiles, is what they take.
 int part_tiles(int rows, int V, int num_sms, int per_sm) {
   const int tiles = (V + kBeamTile - 1) / kBeamTile;
   const long long slots = (long long)per_sm * num_sms;

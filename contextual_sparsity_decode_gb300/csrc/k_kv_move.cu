@@ -288,7 +288,9 @@ cudaError_t run_reorder(const ReorderArgs& r, int n_kv, cudaStream_t stream) {
   // Long spans spread a CTA's start (parents, flags) over more rows; a small
   // problem is spread over the SMs instead (four beams of one layer, 112
   // positions: 10.7 us with 128 positions a CTA, 5.1 with 16; eight beams of
-  // 56 heads: 454 us with 64, 370 with 128).
+  // 56 heads: 454 us with 64, 370 with 128).  The host knows n_max, not the
+  // positions: in a cache that is mostly empty the blocks behind the last
+  // position are counted too, and read their flags before they leave.
   const auto blocks = [&](int span) { return (a.n_max + span - 1) / span; };
   a.span = kSpan;
   while (a.span > 16 && (long long)parts * blocks(a.span) * n_kv * a.S < 4 * num_sms_current()) a.span /= 2;

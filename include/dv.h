@@ -324,10 +324,14 @@ dv_status dv_tree_attn_workspace_size(int B, int T, int h, int group, int d_h,
  *     tree, as in dv_sparse_attn, each at most once; both NULL: all h heads.
  * Every row of out is written: those of other heads, of nodes behind
  * nodes[b], and of nodes that see nothing are 0.  Maximum, sum and numerator
- * are held in fp32, and results repeat bit for bit.
- * Device errors: DV_ERR_POSITION (pos[b] < 0 or pos[b] + nodes[b] > n_max:
- * the sequence's rows are 0), DV_ERR_INDEX_RANGE (head skipped: its rows are
- * 0), DV_ERR_CAPACITY (count above cap, or nodes above T: cut off).
+ * are held in fp32; for 16-bit storage the weights p_j enter the product with V
+ * as the sum of two values of the storage type (2^-17 relative for DV_BF16,
+ * 2^-22, or 2^-31 of the row's largest weight, for DV_F16).  Results repeat bit
+ * for bit.
+ * Device errors: DV_ERR_POSITION (nodes[b] > 0, and pos[b] < 0 or
+ * pos[b] + nodes[b] > n_max: the sequence's rows are 0), DV_ERR_INDEX_RANGE
+ * (head skipped: its rows are 0), DV_ERR_CAPACITY (count above cap, or nodes
+ * above T: cut off).
  * Limits: B <= 512, T <= 1024, h <= 1024, group <= 64, d_h in {64, 128}
  * (others DV_ERR_UNSUPPORTED), n_max <= 1048576, a multiple of 16, and
  * B heads (T group / 16) (n_max / 64) below 2^32 (else DV_ERR_UNSUPPORTED). */
@@ -364,8 +368,9 @@ dv_status dv_kv_compact(const dv_kv* kv, int n_kv, int B, int d, int h, int d_h,
  * that continues itself is left alone, and so are positions below start (a
  * prompt that the beams share; NULL: 0) and behind.  pos itself is not
  * changed: where a sequence's beams differ in length, gather it by parent.
- * Device errors: DV_ERR_INDEX_RANGE (a parent outside [0, width)) and
- * DV_ERR_POSITION (a pos outside [0, n_max]): that beam is left alone.
+ * Device errors: DV_ERR_INDEX_RANGE (a parent outside [0, width): that beam is
+ * left alone) and DV_ERR_POSITION (a parent whose pos is outside [0, n_max]: the
+ * beams that continue it are left alone).
  * ws: at least 256 bytes, zero-filled once.  Limits: n_kv <= 1024,
  * n_seq <= 1023, width <= 32, h <= 1024. */
 dv_status dv_kv_reorder(const dv_kv* kv, int n_kv, int n_seq, int width, int d,
@@ -389,11 +394,11 @@ dv_status dv_beam_select_workspace_size(int n_seq, int width, int V, int K,
  * Beams that have not ended: a row whose log-sum-exp is not finite (a NaN, a
  * +inf, or nothing above -inf) and a row whose cum is not finite offer every
  * token at -inf.  A beam's candidates are in the order of its logits, those of
- * different beams are compared in double precision.  A row's
- * log-sum-exp is taken over fp32 exponentials, summed with compensation within
- * a part of the row, in fp32 over the part's threads and in double over parts:
- * about 2^-21.4 off at most in rows that were tried, 177 x 2^-24 in any row,
- * whatever V.  Results repeat bit for bit.
+ * different beams are compared in double precision.  A row's log-sum-exp is
+ * taken over fp32 exponentials, summed with compensation by each thread of a
+ * part of the row, in fp32 over a part's threads and in double over parts:
+ * 4e-7 off at most in rows that were tried, 177 x 2^-24 in any row, whatever V.
+ * Results repeat bit for bit.
  * Limits: n_seq * width <= 65535, width <= 32, V <= 4194304, 1 <= K <= 64 and
  * K <= width V. */
 dv_status dv_beam_select(const void* logits, int n_seq, int width, int V,
@@ -415,7 +420,9 @@ dv_status dv_layernorm(const float* x, int B, int d, float eps,
 /* Launch policy (no counterpart in the pages; it changes timing, never
  * results).  Inside every entry point the later kernels start during the
  * earlier ones and read only data those do not write.  At level 0 (the
- * default) the first kernel of each call waits for everything before it.
+ * default) the first kernel of each call waits for everything before it
+ * (those of dv_layernorm, dv_tree_attn and dv_beam_select may be started
+ * earlier, at either level, and wait before they read or write anything).
  * At level 1, for batch 1, the first kernel of dv_sparse_attn and of
  * dv_sparse_mlp may also start while the kernel before the call is still
  * running, and reads before waiting for it: the head / neuron lists and
@@ -424,15 +431,18 @@ dv_status dv_layernorm(const float* x, int B, int d, float eps,
  * of those -- true when that kernel is the dv_layernorm producing the call's
  * y, as in a pre-LN decoder -- and neither does the kernel before that
  * layernorm, which lets its consumer start at once (in a pre-LN decoder it
- * is the previous block's dv_sparse_attn or dv_sparse_mlp).  Process-wide;
- * returns the previous level. */
+ * is the previous block's dv_sparse_attn or dv_sparse_mlp).  dv_tree_attn,
+ * too, lets the call after it start while both its kernels run; they write
+ * nothing but its out and its workspace.  Process-wide; returns the previous
+ * level. */
 int dv_set_launch_overlap(int level);
 
 /* Bound of every device-side wait (no counterpart in the pages): the
- * one-launch MLP's wait for its up-projection CTAs and the tensor-core
- * path's pipeline waits give up after `ns` nanoseconds of the GPU's global
- * timer, record DV_ERR_TIMEOUT in the workspace (read it with dv_check) and
- * unwind; the kernel still waits for its own tensor-core and copy work in
+ * one-launch MLP's wait for its up-projection CTAs, the tensor-core paths'
+ * pipeline waits (dv_tree_attn's among them) and the waits for copies of the
+ * streaming MLP and dv_beam_select give up after `ns` nanoseconds of the GPU's
+ * global timer, record DV_ERR_TIMEOUT in the workspace (read it with dv_check)
+ * and unwind; the kernel still waits for its own tensor-core and copy work in
  * flight before it exits.  ns <= 0 restores the default of one second.
  * Read at launch (a captured graph keeps the value it was captured with);
  * process-wide; returns the previous bound. */
