@@ -13,12 +13,13 @@
 // read once; 48 x 10 rows of 128001 bf16 logits with a fifth of the beams done
 // are 98 MB, 14.4 us).
 //   scan  a CTA walks a part of a row in tiles of kBeamTile tokens, which bulk
-//         copies bring into a ring of shared memory: a running maximum and sum of exponentials
-//         per thread, and the groups of 8 tokens (kThreads apart) whose maximum
-//         may be among the K largest: the K best groups, by maximum and then
-//         its lowest token, hold the K best tokens (each group left out is
-//         preceded by K tokens of others).  The threads' running maxima give a value tau
-//         that K groups reach, sharper with every tile; a group is listed if
+//         copies bring into a ring of shared memory: a running maximum and
+//         compensated sum of exponentials per thread, and the groups of 8 tokens
+//         (kThreads apart) whose maximum may be among the K largest: the K best
+//         groups, by maximum and then its lowest token, hold the K best tokens
+//         (each group left out is preceded by K tokens of others).  The threads'
+//         running maxima give a value tau that K groups reach, sharper with
+//         every tile; a group is listed if
 //         its maximum is above the tau before its tile (an equal one comes
 //         after K others) and reaches the one with it: about K / k groups of
 //         tile k.  A list that grows long all the same is cut back.  At the
@@ -32,9 +33,9 @@
 // alone, not on the row's address, so rows with equal logits get equal sums.
 
 // Measured on GB300, both kernels: 48 x 10 rows of 128001 bf16 logits, a fifth of
-// the beams done, 51.5 us (1.9 TB/s of the logits read; bound by instructions, 19
-// a token, and by uneven SMs: parts of 8, 11 and 32 tiles instead of 16 took
-// 57, 53 and 58); 8 x 8 of 50257 fp32 16.6 us, 4 of 32000 f16 7.6 us.
+// the beams done, 51.5 us (1.9 TB/s of the logits read; bound by instructions,
+// 19.5 a token, and by uneven SMs); 8 x 8 of 50257 fp32 15.5 us, 4 of 32000 f16
+// 7.5 us.
 
 #include "dv_kernels.h"
 #include "tc_common.cuh"
