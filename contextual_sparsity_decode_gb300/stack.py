@@ -306,10 +306,12 @@ class SparseDecoder:
         """Buffers and workspaces of verify_tree for trees of T nodes: the
         smallest set made so far that holds them, or a new one for the next
         power of two (all sets together hold less than twice the largest).  A
-        set stays: captured graphs hold its addresses."""
+        set stays until set_keep: captured graphs hold its addresses."""
         size = min((n for n in self._tree if n >= T), default=0)
         if size:
             return self._tree[size]
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError(f"verify_tree of {T} nodes: run it once before it is captured (its buffers are made then)")
         size = 1 << (T - 1).bit_length()
         dev, B, d, h, d_h = self.device, self.B, self.d, self.h, self.d_h
         rows = B * size
@@ -339,7 +341,9 @@ class SparseDecoder:
         dv_tree_attn (None: a linear draft, full trees).  pos + nodes may be
         n_max at most: a tree behind that changes no row of the cache, and
         ``check`` reports it.  The live nodes' rows are written to the cache
-        behind pos, which does not move: ``accept`` keeps a path of them.  A
+        behind pos, which does not move: ``accept`` keeps a path of them.  The
+        pass can be captured once a tree of its size has run (capture it again
+        after set_keep or prefill_dense, which make new buffers).  A
         tree's nodes share one set of heads per layer, predicted from node 0;
         neurons are predicted node by node, both from the same inputs as in a
         decode step (layer 0 from its own attention input, layer l from layer

@@ -8,7 +8,8 @@ import torch
 
 from contextual_sparsity_decode_gb300 import binding as dv
 from contextual_sparsity_decode_gb300 import stack
-from test_stack_candidates import N_PROMPT, TOL, _close, _decoder, _inputs
+from synth import Workload, embeddings, layer_weights
+from test_stack_candidates import N_PROMPT, TOL, _close, _decoder, _inputs, _step
 
 pytestmark = pytest.mark.gpu
 
@@ -336,3 +337,40 @@ def test_sparse_trees_of_several_nodes(monkeypatch, B, T, tree):
             out[n] = torch.relu(W["W1n"][j] @ y[n]) @ W["W2n"][j]
         r, src = r + out, ya
     near(got.reshape(B * T, d), r)
+
+
+def test_the_first_tree_of_a_size_is_not_captured():
+    """Buffers made inside a capture would hold nothing until the graph's first
+    replay: refused, and nothing is kept of the attempt."""
+    dec = _filled(1, [20])
+    E = _inputs(1, 3, 512, 42)
+    with pytest.raises(RuntimeError):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            dec.verify_tree(E)
+    want = _filled(1, [20]).verify_tree(E)
+    _close(dec.verify_tree(E), want)
+    dec.check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = dec.verify_tree(E)
+    graph.replay()
+    _close(got, want)
+
+
+@pytest.mark.parametrize("dtype,tol", [("f32", 1e-5), ("bf16", 8 * 2.0 ** -8)])
+def test_linear_draft_in_other_types(dtype, tol):
+    """As in f16: half-steps of the type per layer, fp32's own sums for f32."""
+    w = Workload("cand", 72, d=512, h=8, d_h=64, N=1024, r=64, dtype=dtype, layers=2, n_prompt=N_PROMPT)
+    layers = [layer_weights(w, l, device="cuda") for l in range(w.layers)]
+    decs = []
+    for _ in range(2):
+        dec = stack.SparseDecoder(layers, 2, 64, 8, w.N, 0.125)
+        dec.prefill([torch.stack([embeddings(w, N_PROMPT, f"X{l}/{b}", device="cuda") for b in range(2)])
+                     for l in range(w.layers)], N_PROMPT)
+        decs.append(dec)
+    E = _inputs(2, 5, 512, 43)
+    got = decs[0].verify_tree(E)
+    decs[0].check()
+    for t in range(5):
+        want = _step(decs[1], E[:, t])
+        assert float((got[:, t].double() - want.double()).norm() / want.double().norm()) <= tol
