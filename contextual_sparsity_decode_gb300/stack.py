@@ -319,7 +319,8 @@ class SparseDecoder:
         i32 = dict(dtype=torch.int32, device=dev)
         t = dict(r=torch.zeros(rows, d, dtype=torch.float32, device=dev),
                  y=torch.zeros(rows, d, dtype=self.dtype, device=dev),
-                 src=torch.zeros(rows, d, dtype=self.dtype, device=dev),
+                 y2=torch.zeros(rows, d, dtype=self.dtype, device=dev),
+                 y_mlp=torch.zeros(rows, d, dtype=self.dtype, device=dev),
                  y_root=torch.zeros(B, d, dtype=self.dtype, device=dev),
                  out=torch.zeros(rows, h * d_h, dtype=self.dtype, device=dev),
                  head_idx=torch.zeros(B, self.k_heads, **i32), head_cnt=torch.zeros(B, **i32),
@@ -372,7 +373,7 @@ class SparseDecoder:
         B, T, d = E.shape
         t = self._tree_buffers(T)
         h, d_h, rows, chunk = self.h, self.d_h, B * T, min(B * T, 32)
-        r, y, src, out = (t[k][:rows] for k in ("r", "y", "src", "out"))
+        r, y, before, y_mlp, out = (t[k][:rows] for k in ("r", "y", "y2", "y_mlp", "out"))
         r.copy_(E.reshape(rows, d))
         # Rows of the cache that the nodes take: those of live nodes alone, and
         # none of a tree that does not fit (the calls below report it).  A node
@@ -394,8 +395,7 @@ class SparseDecoder:
         for l in range(self.L):
             W, kv = self.layers[l], self.kv[l]
             dv.dv_layernorm(r, y, self.eps)
-            if l == 0:
-                src.copy_(y)
+            src = before if l else y          # what the predictors read
             t["y_root"].copy_(src.view(B, T, d)[:, 0])
             for b in range(0, B, 32):
                 e = min(b + 32, B)
@@ -411,15 +411,14 @@ class SparseDecoder:
                             out.view(B, T, h, d_h), t["ws_tree"], mask=mask, nodes=nodes, head_idx=t["head_idx"],
                             head_count=t["head_cnt"])
             r += torch.mm(out, W["Wo"].view(h * d_h, d), **wide)
-            ya = y.clone()
-            dv.dv_layernorm(r, y, self.eps)
+            dv.dv_layernorm(r, y_mlp, self.eps)
             for i in range(0, rows, chunk):
                 e = min(i + chunk, rows)
                 idx, cnt = t["neur_idx"][:e - i], t["neur_cnt"][:e - i]
                 dv.dv_predict(src[i:e], [dv.Predictor(W["PM1t"], W["PM2t"], idx, cnt, dv.DV_TOPK, self.k_neurons)],
                               t["ws_pred"])
-                dv.dv_sparse_mlp(y[i:e], W["W1n"], W["W2n"], idx, cnt, r[i:e], t["ws_mlp"], accumulate=True)
-            src.copy_(ya)
+                dv.dv_sparse_mlp(y_mlp[i:e], W["W1n"], W["W2n"], idx, cnt, r[i:e], t["ws_mlp"], accumulate=True)
+            y, before = before, y
         return r.view(B, T, d).clone()
 
     def accept(self, idx: torch.Tensor, count: torch.Tensor):
