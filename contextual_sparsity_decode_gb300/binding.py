@@ -40,6 +40,8 @@ EXPORTS = (
     "dv_kernel_launches", "dv_label_workspace_size", "dv_label_neurons", "dv_label_heads",
     "dv_select_scores", "dv_tree_attn_workspace_size", "dv_tree_attn", "dv_kv_compact", "dv_kv_reorder",
     "dv_beam_select_workspace_size", "dv_beam_select",
+    "dv_q4_quantize", "dv_q4_matvec_workspace_size", "dv_q4_matvec",
+    "dv_q4_sparse_mlp_workspace_size", "dv_q4_sparse_mlp",
 )
 
 
@@ -59,6 +61,10 @@ class dv_predictor(ctypes.Structure):
 class dv_kv(ctypes.Structure):
     _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("X", ctypes.c_void_p),
                 ("valid", ctypes.c_void_p), ("n_max", ctypes.c_int)]
+
+
+class dv_q4(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("group", ctypes.c_int)]
 
 
 _lib = None
@@ -108,6 +114,12 @@ _SIGS = {
     "dv_beam_select_workspace_size": ([_c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_sz)], _c_int),
     "dv_beam_select": ([_vp, _c_int, _c_int, _c_int, ctypes.c_longlong, _c_int, _vp, _vp, _c_int, _c_int, _vp,
                         _vp, _vp, _vp, _sz, _vp], _c_int),
+    "dv_q4_quantize": ([_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp], _c_int),
+    "dv_q4_matvec_workspace_size": ([_c_int, _c_int, _c_int, ctypes.POINTER(_sz)], _c_int),
+    "dv_q4_matvec": ([_vp, _c_int, _c_int, _c_int, ctypes.POINTER(dv_q4), _c_int, _vp, _c_int, _vp, _sz, _vp], _c_int),
+    "dv_q4_sparse_mlp_workspace_size": ([_c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_sz)], _c_int),
+    "dv_q4_sparse_mlp": ([_vp, _c_int, _c_int, _c_int, ctypes.POINTER(dv_q4), ctypes.POINTER(dv_q4), _vp, _c_int, _vp,
+                          _c_int, _vp, _c_int, _vp, _sz, _vp], _c_int),
 }
 
 
@@ -286,6 +298,90 @@ def dv_sparse_mlp(y, W1n, W2n, idx, count, out, ws, accumulate=False, stream=Non
                             ws.numel(), _stream(stream)), "dv_sparse_mlp")
 
 
+# --------------------------------------------------------------------- matrices in 4 bits
+
+class Q4:
+    """A matrix [N][d] in 4 bits with a scale for every `group` (64 or 128)
+    elements of a row (see dv_q4 in dv.h): q [N][64 ceil(d / 128)] uint8 and
+    scale [N][ceil(d / group)] in the storage type."""
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor, d: int, group: int):
+        self.q, self.scale, self.d, self.group = q, scale, int(d), int(group)
+        self.N, self.dtype = q.shape[0], scale.dtype
+        if self.group not in (64, 128):
+            raise DvError(7, "Q4", f"groups of {group}: 64 or 128")
+        _laid_out(q, (self.N, (self.d + 127) // 128 * 64), torch.uint8, "Q4")
+        _laid_out(scale, (self.N, -(-self.d // self.group)), scale.dtype, "Q4")
+        if scale.device != q.device:
+            raise DvError(1, "Q4", "codes and scales on one device")
+        self.dt = _dt(scale)
+        self.c = dv_q4(q.data_ptr(), scale.data_ptr(), self.group)
+
+    @classmethod
+    def empty(cls, N: int, d: int, dtype, group: int = 128, device="cuda") -> "Q4":
+        return cls(torch.zeros(N, (d + 127) // 128 * 64, dtype=torch.uint8, device=device),
+                   torch.zeros(N, -(-d // group), dtype=dtype, device=device), d, group)
+
+    @classmethod
+    def of(cls, W: torch.Tensor, group: int = 128, stream=None) -> "Q4":
+        """W [N][d] quantised (dv_q4_quantize)."""
+        out = cls.empty(W.shape[0], W.shape[1], W.dtype, group, W.device)
+        dv_q4_quantize(W, out, stream=stream)
+        return out
+
+
+def dv_q4_quantize(W: torch.Tensor, out: Q4, values: Optional[torch.Tensor] = None, stream=None):
+    """W [N][d] into out; values [N][d], unless None: what the codes stand for
+    (see dv_q4_quantize in dv.h)."""
+    for t in (W, values):
+        if t is not None:
+            _laid_out(t, (out.N, out.d), out.dtype, "dv_q4_quantize")
+    _here("dv_q4_quantize", W, out.q, values)
+    _ok(lib().dv_q4_quantize(_ptr(W), out.N, out.d, out.dt, out.group, _ptr(out.q), _ptr(out.scale), _ptr(values),
+                             _stream(stream)), "dv_q4_quantize")
+
+
+def dv_q4_matvec_workspace_size(B: int, d: int, N: int) -> int:
+    n = ctypes.c_size_t(0)
+    _ok(lib().dv_q4_matvec_workspace_size(B, d, N, ctypes.byref(n)), "dv_q4_matvec_workspace_size")
+    return n.value
+
+
+def dv_q4_matvec(y, W: Q4, out, ws, accumulate=False, stream=None):
+    """out [B][N] (+)= y [B][d] times the rows of W (see dv_q4_matvec in dv.h)."""
+    where, B = "dv_q4_matvec", y.shape[0]
+    _laid_out(y, (B, W.d), W.dtype, where)
+    _laid_out(out, (B, W.N), torch.float32, where)
+    _here(where, y, W.q, out, ws)
+    st = (_lib or lib()).dv_q4_matvec(y.data_ptr(), B, W.d, W.N, W.c, W.dt, out.data_ptr(), accumulate, ws.data_ptr(),
+                                      ws.numel(), _stream(stream))
+    if st:
+        _ok(st, where)
+
+
+def dv_q4_sparse_mlp_workspace_size(B: int, d: int, N: int, cap: int) -> int:
+    n = ctypes.c_size_t(0)
+    _ok(lib().dv_q4_sparse_mlp_workspace_size(B, d, N, cap, ctypes.byref(n)), "dv_q4_sparse_mlp_workspace_size")
+    return n.value
+
+
+def dv_q4_sparse_mlp(y, W1: Q4, W2: Q4, idx, count, out, ws, accumulate=False, stream=None):
+    """dv_sparse_mlp with 4-bit matrices (see dv_q4_sparse_mlp in dv.h)."""
+    where, B, cap = "dv_q4_sparse_mlp", y.shape[0], idx.shape[-1]
+    if W2.N != W1.N or W2.d != W1.d or W2.dt != W1.dt:
+        raise DvError(1, where, "W1 and W2 of one shape and type")
+    _laid_out(y, (B, W1.d), W1.dtype, where)
+    _laid_out(out, (B, W1.d), torch.float32, where)
+    _counted(where, B * cap, idx)
+    _counted(where, B, count)
+    _here(where, y, W1.q, W2.q, idx, count, out, ws)
+    st = (_lib or lib()).dv_q4_sparse_mlp(
+        y.data_ptr(), B, W1.d, W1.N, W1.c, W2.c, idx.data_ptr(), cap, count.data_ptr(), W1.dt, out.data_ptr(), accumulate,
+        ws.data_ptr(), ws.numel(), _stream(stream))
+    if st:
+        _ok(st, where)
+
+
 # --------------------------------------------------------------------- attention
 
 class KV:
@@ -337,6 +433,16 @@ def _counted(where: str, n: int, *tensors, dtype=torch.int32) -> None:
 def _laid_out(t: torch.Tensor, shape, dtype, where: str) -> None:
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise DvError(1, where, f"a contiguous {tuple(shape)} tensor of {dtype} is wanted")
+
+
+def _here(where: str, *tensors) -> None:
+    """Tensors on the current device (None: left out): the kernels run there."""
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != d:
+            d = -1
+    if d < 0 or d != (_current_device() if _current_device is not None else torch.cuda.current_device()):
+        raise DvError(1, where, "tensors on the current CUDA device are wanted")
 
 
 def dv_sparse_attn_workspace_size(B, d, h, d_h, cap, n_max) -> int:

@@ -204,6 +204,28 @@ BeamWs carve_beam(Carver& c, int n_seq, int width, int V, int K) {
   return w;
 }
 
+struct Q4Ws {
+  int32_t* U;
+  int32_t* U_count;
+  uint32_t* member;
+  float* act;
+  uint16_t* pieces;
+};
+size_t q4_piece_row(int d) { return (size_t)(d + 127) / 128 * 128; }
+// (room for the pieces of 32-bit vectors whatever the storage type: the size queries do not take it)
+Q4Ws carve_q4_mlp(Carver& c, int B, int d, int N, int cap) {
+  Q4Ws w{};
+  w.pieces = c.take<uint16_t>((size_t)3 * B * q4_piece_row(d));
+  w.act = c.take<float>((size_t)B * (B == 1 ? cap : mlp_union_cap(B, N, cap)));
+  if (B > 1) {
+    w.U = c.take<int32_t>((size_t)N);
+    w.U_count = c.take<int32_t>(4);
+    w.member = c.take<uint32_t>((size_t)B * ((N + 31) / 32));
+  }
+  return w;
+}
+uint16_t* carve_q4_matvec(Carver& c, int B, int d) { return c.take<uint16_t>((size_t)3 * B * q4_piece_row(d)); }
+
 // ---- validation ---------------------------------------------------------------------
 
 dv_status check_pred(const void* y, int B, int d, dv_dtype dt, const dv_predictor* preds,
@@ -412,6 +434,96 @@ dv_status dv_sparse_mlp(const void* y, int B, int d, int N, const void* W1n, con
   L.act_hi = w.act_hi; L.act_lo = w.act_lo; L.act = w.act; L.ctr = w.ctr;
   L.tc_part = w.tc_part; L.tc_sem = w.tc_sem;
   cudaError_t e = launch_sparse_mlp(L, dt, static_cast<WsHeader*>(ws), num_sms_current(), stream);
+  return e == cudaSuccess ? DV_OK : cuda_fail(e);
+}
+
+// ---- matrices in 4 bits -----------------------------------------------------------------
+
+namespace {
+constexpr int kQ4MaxD = 65536, kQ4MaxN = 1 << 24;
+
+dv_status check_q4(const dv_q4* W) {
+  if (!W || !W->q || !W->scale || !aligned16(W->q) || !aligned4(W->scale)) return DV_ERR_INVALID_ARG;
+  return W->group == 64 || W->group == 128 ? DV_OK : DV_ERR_UNSUPPORTED;
+}
+bool q4_shape_ok(int B, int d, int N, int most) {
+  return B >= 1 && B <= kMaxB && d >= 1 && d <= kQ4MaxD && N >= 1 && N <= most;
+}
+}  // namespace
+
+dv_status dv_q4_quantize(const void* W, int N, int d, dv_dtype dt, int group, void* q, void* scale, void* values,
+                         cudaStream_t stream) {
+  Range nvtx_range("dv_q4_quantize");
+  if (!dtype_ok(dt)) return DV_ERR_DTYPE;
+  if (!W || !aligned16(W) || (values && !aligned16(values))) return DV_ERR_INVALID_ARG;
+  const dv_q4 out{q, scale, group};
+  const dv_status st = check_q4(&out);
+  if (st != DV_OK) return st;
+  if (!q4_shape_ok(1, d, N, kQ4MaxN) || d % vec_of(dt)) return DV_ERR_INVALID_ARG;
+  cudaError_t e = launch_q4_quantize(W, N, d, dt, group, q, scale, values, num_sms_current(), stream);
+  return e == cudaSuccess ? DV_OK : cuda_fail(e);
+}
+
+dv_status dv_q4_matvec_workspace_size(int B, int d, int N, size_t* bytes) {
+  if (!bytes || !q4_shape_ok(B, d, N, kQ4MaxN)) return DV_ERR_INVALID_ARG;
+  Carver c(nullptr);
+  carve_q4_matvec(c, B, d);
+  *bytes = c.size();
+  return DV_OK;
+}
+
+dv_status dv_q4_matvec(const void* y, int B, int d, int N, const dv_q4* W, dv_dtype dt, float* out, int accumulate,
+                       void* ws, size_t ws_bytes, cudaStream_t stream) {
+  Range nvtx_range("dv_q4_matvec");
+  if (!dtype_ok(dt)) return DV_ERR_DTYPE;
+  if (!y || !aligned16(y) || !out || !aligned4(out)) return DV_ERR_INVALID_ARG;
+  const dv_status st = check_q4(W);
+  if (st != DV_OK) return st;
+  if (!q4_shape_ok(B, d, N, kQ4MaxN) || d % vec_of(dt)) return DV_ERR_INVALID_ARG;
+  Carver meas(nullptr);
+  carve_q4_matvec(meas, B, d);
+  if (!ws_ok(ws, ws_bytes, meas.size())) return DV_ERR_WORKSPACE;
+  Carver c(ws);
+  Q4MatvecLaunch L{};
+  L.y = y; L.B = B; L.d = d; L.N = N;
+  L.q = static_cast<const uint8_t*>(W->q); L.scale = W->scale; L.group = W->group;
+  L.out = out; L.accumulate = accumulate ? 1 : 0;
+  L.pieces = carve_q4_matvec(c, B, d);
+  cudaError_t e = launch_q4_matvec(L, dt, stream);
+  return e == cudaSuccess ? DV_OK : cuda_fail(e);
+}
+
+dv_status dv_q4_sparse_mlp_workspace_size(int B, int d, int N, int cap, size_t* bytes) {
+  if (!bytes || !q4_shape_ok(B, d, N, 65536) || cap < 1) return DV_ERR_INVALID_ARG;
+  Carver c(nullptr);
+  carve_q4_mlp(c, B, d, N, cap);
+  *bytes = c.size();
+  return DV_OK;
+}
+
+dv_status dv_q4_sparse_mlp(const void* y, int B, int d, int N, const dv_q4* W1, const dv_q4* W2, const int32_t* idx,
+                           int cap, const int32_t* count, dv_dtype dt, float* out, int accumulate, void* ws,
+                           size_t ws_bytes, cudaStream_t stream) {
+  Range nvtx_range("dv_q4_sparse_mlp");
+  if (!dtype_ok(dt)) return DV_ERR_DTYPE;
+  if (!y || !aligned16(y) || !idx || !count || !aligned4(idx) || !aligned4(count) || !out || !aligned4(out))
+    return DV_ERR_INVALID_ARG;
+  dv_status st = check_q4(W1);
+  if (st == DV_OK) st = check_q4(W2);
+  if (st != DV_OK) return st;
+  if (!q4_shape_ok(B, d, N, 65536) || d % vec_of(dt) || cap < 1) return DV_ERR_INVALID_ARG;
+  Carver meas(nullptr);
+  carve_q4_mlp(meas, B, d, N, cap);
+  if (!ws_ok(ws, ws_bytes, meas.size())) return DV_ERR_WORKSPACE;
+  Carver c(ws);
+  const Q4Ws w = carve_q4_mlp(c, B, d, N, cap);
+  Q4MlpLaunch L{};
+  L.y = y; L.B = B; L.d = d; L.N = N;
+  L.q1 = static_cast<const uint8_t*>(W1->q); L.s1 = W1->scale; L.group1 = W1->group;
+  L.q2 = static_cast<const uint8_t*>(W2->q); L.s2 = W2->scale; L.group2 = W2->group;
+  L.idx = idx; L.cap = cap; L.count = count; L.out = out; L.accumulate = accumulate ? 1 : 0;
+  L.U = w.U; L.U_count = w.U_count; L.member = w.member; L.act = w.act; L.pieces = w.pieces;
+  cudaError_t e = launch_q4_sparse_mlp(L, dt, static_cast<WsHeader*>(ws), stream);
   return e == cudaSuccess ? DV_OK : cuda_fail(e);
 }
 

@@ -346,6 +346,55 @@ struct BeamLaunch {
 };
 cudaError_t launch_beam_select(const BeamLaunch& a, dv_dtype dt, WsHeader* hdr, int num_sms, cudaStream_t stream);
 
+// ---- matrices in 4 bits (k_q4.cu) ------------------------------------------------
+
+constexpr int kQ4BlockBytes = 64;  // a block of 128 elements
+// First kind of product: rows of a matrix (all, or a list's) with vectors.
+struct Q4Rows {
+  const uint8_t* q; const void* scale; int group;
+  int B, d, N;                          // vectors, their length, rows of the matrix
+  const int32_t* list; const int32_t* count; int cap;  // listed rows, or null: all
+  const uint32_t* member; int words;    // [B][words] whose list a row is in, or null
+  float* act;                           // listed: max(0, product), [B][cap]
+  float* out; int accumulate;           // all rows: [B][N]
+  WsHeader* hdr;
+  int early;                            // list and weights are read before the wait
+  // set by the launcher: the vectors as columns of 16-bit values
+  const void* x; int cols, ldx, x_len;
+  int blocks, groups, kw;
+  size_t pitch;
+};
+// Second kind: sums of listed rows.
+struct Q4Cols {
+  const uint8_t* q; const void* scale; int group;
+  int B, d, N;
+  const int32_t* list; const int32_t* count; int cap;
+  const float* act;                     // [B][cap]
+  float* out; int accumulate;           // [B][d]
+  int groups, split;
+  size_t pitch;
+};
+struct Q4MatvecLaunch {
+  const void* y; int B, d, N;
+  const uint8_t* q; const void* scale; int group;
+  float* out; int accumulate;
+  void* pieces;                         // DV_F32: 3 B rows of whole blocks, 16 bits
+};
+struct Q4MlpLaunch {
+  const void* y; int B, d, N;
+  const uint8_t* q1; const void* s1; int group1;
+  const uint8_t* q2; const void* s2; int group2;
+  const int32_t* idx; int cap; const int32_t* count;
+  float* out; int accumulate;
+  int32_t* U; int32_t* U_count; uint32_t* member;  // B > 1
+  float* act;                           // [B][cap], B > 1: [B][mlp_union_cap]
+  void* pieces;
+};
+cudaError_t launch_q4_quantize(const void* W, int N, int d, dv_dtype dt, int group, void* q, void* scale, void* values,
+                               int num_sms, cudaStream_t stream);
+cudaError_t launch_q4_matvec(const Q4MatvecLaunch& L, dv_dtype dt, cudaStream_t stream);
+cudaError_t launch_q4_sparse_mlp(const Q4MlpLaunch& L, dv_dtype dt, WsHeader* hdr, cudaStream_t stream);
+
 // ---- misc (k_misc.cu) --------------------------------------------------------
 
 cudaError_t launch_layernorm(const float* x, int B, int d, float eps, void* y,

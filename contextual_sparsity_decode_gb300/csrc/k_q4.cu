@@ -1,0 +1,624 @@
+// Matrices in 4 bits with group scales, w[n][t] = (code[n][t] - 8) s[n][t / G]:
+// quantisation, products of 1..32 rows with all rows of a matrix, and the two
+// products of the sparse MLP over selected rows.
+//
+// Layout.  A row is blocks of 128 elements in 64 bytes.  Word w of a block
+// (g = w / 2, s = w % 2) holds elements 64 s + 8 g + e, e < 8, at bit
+// 4 (e / 2) + 16 (e % 2), so that
+//   - (word >> 4 i) & 0x000f000f are elements 2 i and 2 i + 1 side by side: one
+//     logic operation makes a pair of 16-bit floats of them;
+//   - the 16 bytes of chunk c (of 4) are elements 16 c .. 16 c + 15 of either
+//     half of the block: as the A operand of an m16n8k16 product, whose lane
+//     (g, c) holds four k of row g and of row g + 8, a 16-byte load is four
+//     k-steps, two of each half, and the vector's elements that go with it are
+//     contiguous;
+//   - 8 bytes at 8 g are elements 8 g .. 8 g + 7 of either half: with the roles
+//     of rows and elements exchanged (the second product of the MLP), lane
+//     (g, c) takes four matrix rows and 16 output elements.
+//
+// The codes less 8 are exact in both 16-bit types and every product of two of
+// them with a 16-bit factor is exact in fp32; sums are fp32 and the scale is
+// applied to the sum over a group (to the coefficient in the second product).
+// 32-bit factors (a DV_F32 vector, the activations) enter as three bf16 pieces
+// that add up to them, as further columns of the product.
+
+#include "dv_kernels.h"
+
+namespace dv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBlockBytes = kQ4BlockBytes;
+
+// ---- pairs of codes -------------------------------------------------------------
+
+template <typename P> struct Pairs;
+template <> struct Pairs<__half> {
+  // element pairs i = 0..3 of a word, less 8
+  static __device__ __forceinline__ void open(uint32_t w, uint32_t* p) {
+    const __half2 m1032 = __half2half2(__ushort_as_half(0xe408));           // -1032
+    const __half2 r16 = __half2half2(__ushort_as_half(0x2c00));             // 1/16
+    const __half2 m72 = __half2half2(__ushort_as_half(0xd480));             // -72
+    const uint32_t v = w >> 8;
+    const uint32_t a[4] = {(w & 0x000f000fu) | 0x64006400u, (w & 0x00f000f0u) | 0x64006400u,
+                           (v & 0x000f000fu) | 0x64006400u, (v & 0x00f000f0u) | 0x64006400u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = *reinterpret_cast<const __half2*>(&a[i]);
+      const __half2 r = (i & 1) ? __hfma2(h, r16, m72) : __hadd2(h, m1032);  // 1024 + 16 q, 1024 + q
+      p[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+};
+template <> struct Pairs<__nv_bfloat16> {
+  static __device__ __forceinline__ void open(uint32_t w, uint32_t* p) {
+    const __nv_bfloat162 m136 = __bfloat162bfloat162(__ushort_as_bfloat16(0xc308));  // -136
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;       // 128 + q
+      const __nv_bfloat162 r = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a), m136);
+      p[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+};
+
+// D += A B, m16n8k16: A 16 x 16 in four registers, B 16 x 8 in two.
+template <typename P>
+__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__half>(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An fp32 value as three bf16 pieces whose sum it is (24 bits of mantissa in
+// three of 8; a value that is not finite is its own first piece).
+__device__ __forceinline__ void pieces3(float v, __nv_bfloat16* p) {
+  p[0] = __float2bfloat16_rz(v);       // (towards zero: the largest values do not become infinite)
+  float r = v - __bfloat162float(p[0]);
+  r = fabsf(r) < INFINITY ? r : 0.f;   // (what is left of an infinity or a NaN is a NaN)
+  p[1] = __float2bfloat16_rn(r);
+  p[2] = __float2bfloat16_rn(r - __bfloat162float(p[1]));
+}
+
+template <typename S>
+__device__ __forceinline__ float ld_scale(const void* s, size_t i) {
+  return Elem<S>::to_f(__ldg(static_cast<const S*>(s) + i));
+}
+
+// ---- quantisation ------------------------------------------------------------------
+
+// One half-warp per block of 128 elements, a lane to a word: 8 elements in, one
+// word out.  Bound by memory: the matrix is read once and codes, scales and
+// values are written once.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) q4_quantize_kernel(const T* __restrict__ W, int d, int blocks,
+                                                              long long total, int group, uint32_t* __restrict__ q,
+                                                              T* __restrict__ scale, T* __restrict__ values) {
+  constexpr int kVecs = 8 / Elem<T>::kVec;   // 16-byte vectors of 8 elements
+  const int lane = threadIdx.x & 31, word = lane & 15;
+  const int s = word & 1, at = 64 * s + 8 * (word >> 1);
+  const int groups = (d + group - 1) / group;
+  const long long step = (long long)gridDim.x * (kThreads / 16);
+  // whole warps take part in the exchanges below: `total` is rounded up to two blocks
+  for (long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 4; i < ((total + 1) & ~1LL); i += step) {
+    const bool in = i < total;
+    const long long n = in ? i / blocks : 0;
+    const int b = in ? (int)(i - n * blocks) : 0, t = b * 128 + at;
+    float f[8];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      if (in && t + v * Elem<T>::kVec < d) {
+        unpack<T>(ld_stream(W + n * d + t + v * Elem<T>::kVec), f + v * Elem<T>::kVec);
+      } else {
+#pragma unroll
+        for (int e = 0; e < Elem<T>::kVec; ++e) f[v * Elem<T>::kVec + e] = 0.f;
+      }
+    }
+    // largest magnitude as an integer: a NaN's is above infinity's
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 2; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, top, 1);
+    if (group == 128) top = max(top, other);
+    const bool fine = top < 0x7f800000u;
+    // (a / 7 in fp32 and then in 16 bits is a / 7 rounded once: with at most 11 bits of a it is at least
+    // 2^-15 relative from a border of the 16-bit type)
+    const T sc = Elem<T>::from_f(fine ? __fdiv_rn(__uint_as_float(top), 7.f) : __int_as_float(0x7fc00000));
+    const float sf = Elem<T>::to_f(sc);
+    uint32_t code = 0;
+    float val[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      int c = 0;
+      if (fine && sf > 0.f) {
+        const float ratio = __fdiv_rn(f[e], sf);
+        float r = rintf(ratio);
+        // a quotient that was rounded onto a border between two codes is put on its side of it by the
+        // exact sign of f - ratio s
+        const float frac = ratio - truncf(ratio);
+        if (fabsf(frac) == 0.5f) {
+          const float rem = __fmaf_rn(-ratio, sf, f[e]);
+          if (rem > 0.f) r = ceilf(ratio);
+          if (rem < 0.f) r = floorf(ratio);
+        }
+        c = (int)fminf(fmaxf(r, -8.f), 7.f);
+      }
+      code |= (uint32_t)(c + 8) << (4 * (e >> 1) + 16 * (e & 1));
+      val[e] = fine ? (float)c * sf : __int_as_float(0x7fc00000);
+    }
+    if (!in) continue;
+    q[i * (kBlockBytes / 4) + word] = code;
+    if (t < d && (t % group) == 0) scale[n * groups + t / group] = sc;
+    if (values) {
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        if (t + v * Elem<T>::kVec >= d) continue;
+        uint4 o;
+        T* h = reinterpret_cast<T*>(&o);
+#pragma unroll
+        for (int e = 0; e < Elem<T>::kVec; ++e) h[e] = Elem<T>::from_f(val[v * Elem<T>::kVec + e]);
+        *reinterpret_cast<uint4*>(values + n * d + t + v * Elem<T>::kVec) = o;
+      }
+    }
+  }
+}
+
+// ---- products with rows of a matrix ----------------------------------------------------
+
+// Pieces of 32-bit vectors, rows of whole blocks, zero behind d: for every
+// kPieceRows vectors their first pieces, then their second, then their third.
+constexpr int kPieceRows = 10;   // 30 columns of a product
+
+__global__ void __launch_bounds__(kThreads) q4_pieces_kernel(const float* __restrict__ y, int B, int d, int ld,
+                                                            __nv_bfloat16* __restrict__ x) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int t = blockIdx.x * kThreads + threadIdx.x, b = blockIdx.y;
+  if (t >= ld) return;
+  const int b0 = b / kPieceRows * kPieceRows, rows = min(kPieceRows, B - b0);
+  __nv_bfloat16 p[3];
+  pieces3(t < d ? y[(size_t)b * d + t] : 0.f, p);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) x[((size_t)3 * b0 + k * rows + b - b0) * ld + t] = p[k];
+}
+
+// A CTA's eight warps are kRows row tiles of 16 by `kw` parts of the row's
+// blocks (part p takes blocks p, p + kw, ...).
+constexpr int kAhead = 4;   // blocks whose loads are issued before the first is used
+
+template <typename S, typename P, int NT, bool kList>
+__global__ void __launch_bounds__(kThreads) q4_rows_kernel(const Q4Rows a) {
+  __shared__ float red[kWarps][16][8 * NT + 1];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  const int tiles = kWarps / a.kw, tile = wid / a.kw, part = wid % a.kw;
+  const int u0 = (blockIdx.x * tiles + tile) * 16;
+  // at level 1 of the launch policy the list, its count and the weights are read
+  // before the wait
+  if (!a.early) grid_dep_wait();
+  if (!a.early) grid_dep_launch();
+  int row[2];
+  const int n = kList ? max(0, min(*a.count, a.cap)) : a.N;
+  if (kList && blockIdx.x == 0 && tid == 0 && *a.count > a.cap) set_error(a.hdr, DV_ERR_CAPACITY, *a.count);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int u = u0 + g + 8 * k;
+    row[k] = u < n ? u : -1;
+    if (kList && u < n) {
+      row[k] = a.list[u];
+      if (row[k] < 0 || row[k] >= a.N) {
+        if (c == 0 && part == 0) set_error(a.hdr, DV_ERR_INDEX_RANGE, row[k]);
+        row[k] = -1;
+      } else if (u > 0 && a.list[u - 1] == row[k]) {
+        row[k] = -1;   // listed twice: counts once
+      }
+    }
+  }
+  const uint8_t* q0 = a.q + (size_t)max(row[0], 0) * a.pitch + 16 * c;
+  const uint8_t* q1 = a.q + (size_t)max(row[1], 0) * a.pitch + 16 * c;
+  const size_t s0 = (size_t)max(row[0], 0) * a.groups, s1 = (size_t)max(row[1], 0) * a.groups;
+  const int halves = a.group == 64 ? 2 : 1;   // scales of a block
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+  const P* x = static_cast<const P*>(a.x);
+  bool waited = !a.early;
+  for (int k0 = part; k0 < a.blocks; k0 += a.kw * kAhead) {
+    uint4 w[kAhead][2];
+    float sc[kAhead][2][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int kb = k0 + i * a.kw;
+      w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+      if (kb < a.blocks) {
+        if (row[0] >= 0) w[i][0] = ld_stream(q0 + (size_t)kb * kBlockBytes);
+        if (row[1] >= 0) w[i][1] = ld_stream(q1 + (size_t)kb * kBlockBytes);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int kb = k0 + i * a.kw;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int gi = halves == 2 ? 2 * kb + h : kb;
+        const bool in = kb < a.blocks && gi < a.groups;
+        sc[i][h][0] = in && row[0] >= 0 ? ld_scale<S>(a.scale, s0 + gi) : 0.f;
+        sc[i][h][1] = in && row[1] >= 0 ? ld_scale<S>(a.scale, s1 + gi) : 0.f;
+      }
+    }
+    if (!waited) {
+      grid_dep_wait();
+      grid_dep_launch();
+      waited = true;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int kb = k0 + i * a.kw;
+      if (kb >= a.blocks) break;
+      const uint32_t w0[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w};
+      const uint32_t w1[4] = {w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
+      float d[NT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 0 || halves == 2) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d[t][r] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t p0[4], p1[4];
+          Pairs<P>::open(w0[2 * j + h], p0);
+          Pairs<P>::open(w1[2 * j + h], p1);
+          const int e = kb * 128 + 64 * h + 16 * c + 8 * j;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            // (plain loads: with a 32-bit vector the pieces are another kernel's output)
+            if (8 * t + g < a.cols && e < a.x_len) v = *reinterpret_cast<const uint4*>(x + (size_t)(8 * t + g) * a.ldx + e);
+            mma16816<P>(d[t], p0[0], p1[0], p0[1], p1[1], v.x, v.y);
+            mma16816<P>(d[t], p0[2], p1[2], p0[3], p1[3], v.z, v.w);
+          }
+        }
+        if (h == 1 || halves == 2) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(sc[i][h][r >> 1], d[t][r], acc[t][r]);
+        }
+      }
+    }
+  }
+  if (!waited) {
+    grid_dep_wait();
+    grid_dep_launch();
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) red[wid][g + 8 * (r >> 1)][8 * t + 2 * c + (r & 1)] = acc[t][r];
+  __syncthreads();
+  // sums over the parts (and a 32-bit vector's pieces), in a fixed order
+  for (int i = tid; i < tiles * 16 * a.B; i += kThreads) {
+    const int r = i % (tiles * 16), b = i / (tiles * 16), u = blockIdx.x * tiles * 16 + r;
+    if (u >= n) continue;
+    float sum = 0.f;
+    for (int p = 0; p < a.kw; ++p)
+      for (int col = b; col < a.cols; col += a.B) sum += red[(r >> 4) * a.kw + p][r & 15][col];
+    if (kList) {
+      const int j = a.list[u];
+      bool live = j >= 0 && j < a.N && !(u > 0 && a.list[u - 1] == j);
+      if (live && a.member) live = bit_test(a.member + (size_t)b * a.words, j);
+      a.act[(size_t)b * a.cap + u] = live ? (sum > 0.f || sum != sum ? sum : 0.f) : 0.f;
+    } else {
+      float* o = a.out + (size_t)b * a.N + u;
+      *o = a.accumulate ? *o + sum : sum;
+    }
+  }
+}
+
+// ---- second product of the MLP ----------------------------------------------------------
+
+// out[b][t] (+)= sum_u act[b][u] s[j_u][group of t] (code[j_u][t] - 8): the CTAs of
+// a cluster own one block of 128 output elements and a share of the list each; a
+// warp step is 16 listed rows by the 128 elements.  kCols: the three pieces of the
+// coefficients are columns of one product (3 B <= 8); otherwise three products.
+constexpr int kListed = 1024;   // list entries held at a time
+constexpr int kSteps = 2;       // warp steps whose loads are issued together
+
+template <typename S, int NT, bool kCols>
+__global__ void __launch_bounds__(kThreads) q4_cols_kernel(const Q4Cols a) {
+  extern __shared__ __align__(16) float red[];   // [128][B] the CTA's sums, then [kWarps - 1] more of them
+  __shared__ int id[kListed];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  const int kb = blockIdx.x / a.split, rank = blockIdx.x % a.split;
+  const int n = max(0, min(*a.count, a.cap));
+  const int share = ((n + a.split - 1) / a.split + 15) & ~15;
+  const int lo = min(n, rank * share), hi = min(n, lo + share);
+  const int halves = a.group == 64 ? 2 : 1;
+  float acc[2][4][NT][4];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[s][i][t][r] = 0.f;
+  bool waited = false;
+  const int gi0 = halves == 2 ? 2 * kb : kb, gi1 = halves == 2 ? min(2 * kb + 1, a.groups - 1) : kb;
+  for (int c0 = lo; c0 < hi; c0 += kListed) {
+    const int m = min(kListed, hi - c0);
+    __syncthreads();
+    for (int e = tid; e < ((m + 15) & ~15); e += kThreads) {
+      const int j = e < m ? a.list[c0 + e] : -1;
+      id[e] = j >= 0 && j < a.N ? j : -1;   // (reported, and given activation 0, by the first product)
+    }
+    __syncthreads();
+    for (int e0 = wid * 16; e0 < m; e0 += kWarps * 16 * kSteps) {
+      uint2 w[kSteps][4];
+      float sc[kSteps][2][4];
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int e = e0 + k * kWarps * 16 + 4 * c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = e < m ? id[e + i] : -1;
+          w[k][i] = make_uint2(0, 0);
+          sc[k][0][i] = sc[k][1][i] = 0.f;
+          if (j >= 0) {
+            w[k][i] = __ldg(reinterpret_cast<const uint2*>(a.q + (size_t)j * a.pitch + (size_t)kb * kBlockBytes + 8 * g));
+            sc[k][0][i] = ld_scale<S>(a.scale, (size_t)j * a.groups + gi0);
+            sc[k][1][i] = halves == 2 ? ld_scale<S>(a.scale, (size_t)j * a.groups + gi1) : sc[k][0][i];
+          }
+        }
+      }
+      if (!waited) {
+        grid_dep_wait();   // the activations
+        grid_dep_launch();
+        waited = true;
+      }
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int e = e0 + k * kWarps * 16 + 4 * c;
+        if (e0 + k * kWarps * 16 >= m) break;
+        // coefficients of this lane's four rows in its column(s): [half][piece][pair]
+        uint32_t cf[NT][2][3][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int b = kCols ? g % a.B : 8 * t + g;
+          float v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = (kCols ? g < 3 * a.B : b < a.B) && e + i < m ? __ldcg(a.act + (size_t)b * a.cap + c0 + e + i) : 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1 && halves == 1) break;
+            __nv_bfloat16 p[4][3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pieces3(v[i] == 0.f ? 0.f : v[i] * sc[k][h][i], p[i]);   // (0 adds nothing, whatever the row holds)
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                __nv_bfloat162 two;
+                if (kCols) {
+                  const int mine = g / a.B;
+                  two.x = mine == 0 ? p[2 * i][0] : mine == 1 ? p[2 * i][1] : p[2 * i][2];
+                  two.y = mine == 0 ? p[2 * i + 1][0] : mine == 1 ? p[2 * i + 1][1] : p[2 * i + 1][2];
+                } else {
+                  two.x = p[2 * i][q];
+                  two.y = p[2 * i + 1][q];
+                }
+                cf[t][h][q][i] = *reinterpret_cast<uint32_t*>(&two);
+              }
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint32_t r0 = s ? w[k][0].y : w[k][0].x, r1 = s ? w[k][1].y : w[k][1].x;
+          const uint32_t r2 = s ? w[k][2].y : w[k][2].x, r3 = s ? w[k][3].y : w[k][3].x;
+          // elements 2 i of two rows side by side, and elements 2 i + 1
+          uint32_t ev0[4], ev1[4], od0[4], od1[4];
+          Pairs<__nv_bfloat16>::open(__byte_perm(r0, r1, 0x5410), ev0);
+          Pairs<__nv_bfloat16>::open(__byte_perm(r0, r1, 0x7632), od0);
+          Pairs<__nv_bfloat16>::open(__byte_perm(r2, r3, 0x5410), ev1);
+          Pairs<__nv_bfloat16>::open(__byte_perm(r2, r3, 0x7632), od1);
+          const int h = halves == 2 ? s : 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+              for (int q = 0; q < (kCols ? 1 : 3); ++q) {
+                const uint32_t b0 = h ? cf[t][1][q][0] : cf[t][0][q][0], b1 = h ? cf[t][1][q][1] : cf[t][0][q][1];
+                mma16816<__nv_bfloat16>(acc[s][i][t], ev0[i], od0[i], ev1[i], od1[i], b0, b1);
+              }
+            }
+        }
+      }
+    }
+  }
+  if (!waited) {
+    grid_dep_wait();
+    grid_dep_launch();
+  }
+  // sums of the warps, warp by warp, then of the cluster's CTAs: a fixed order
+  const int cols = kCols ? 3 * a.B : a.B, ld = cols | 1;
+  for (int w = 0; w < kWarps; ++w) {
+    __syncthreads();
+    if (wid != w) continue;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int col = 8 * t + 2 * c + (r & 1), at = 64 * s + 8 * g + 2 * i + (r >> 1);
+            if (col < cols) red[at * ld + col] = w ? red[at * ld + col] + acc[s][i][t][r] : acc[s][i][t][r];
+          }
+  }
+  __syncthreads();
+  if (a.split > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  const int mine = 128 / a.split;   // elements that this CTA joins and writes
+  for (int i = tid; i < mine * a.B; i += kThreads) {
+    const int t = rank * mine + i % mine, b = i / mine;
+    if (kb * 128 + t >= a.d) continue;
+    float sum = 0.f;
+    for (int col = b; col < cols; col += a.B)
+      for (int r = 0; r < a.split; ++r) sum += a.split > 1 ? ld_dsmem_f32(red + t * ld + col, r) : red[t * ld + col];
+    float* o = a.out + (size_t)b * a.d + kb * 128 + t;
+    *o = a.accumulate ? *o + sum : sum;
+  }
+  if (a.split > 1) {   // no CTA leaves while its shared memory is read
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+template <typename S, typename P, int NT>
+cudaError_t run_rows(const Q4Rows& a, bool pdl, cudaStream_t stream) {
+  const int tiles = kWarps / a.kw;
+  const int rows = a.list ? a.cap : a.N;
+  const dim3 grid((rows + 16 * tiles - 1) / (16 * tiles));
+  return a.list ? launch_k(q4_rows_kernel<S, P, NT, true>, grid, dim3(kThreads), 0, stream, pdl, 1, a)
+                : launch_k(q4_rows_kernel<S, P, NT, false>, grid, dim3(kThreads), 0, stream, pdl, 1, a);
+}
+template <typename S, typename P>
+cudaError_t run_rows_nt(const Q4Rows& a, bool pdl, cudaStream_t stream) {
+  const int nt = (a.cols + 7) / 8;
+  if (nt <= 1) return run_rows<S, P, 1>(a, pdl, stream);
+  if (nt <= 2) return run_rows<S, P, 2>(a, pdl, stream);
+  return run_rows<S, P, 4>(a, pdl, stream);
+}
+
+// The first product: y in its storage type, or as pieces made by a kernel before it.
+cudaError_t launch_rows(Q4Rows a, const void* y, void* pieces, dv_dtype dt, bool pdl, cudaStream_t stream) {
+  a.blocks = (a.d + 127) / 128;
+  a.pitch = (size_t)a.blocks * kBlockBytes;
+  a.groups = (a.d + a.group - 1) / a.group;
+  a.kw = 8;
+  if (dt == DV_F32) {
+    const int ld = a.blocks * 128;
+    const cudaError_t e = launch_k(q4_pieces_kernel, dim3((ld + kThreads - 1) / kThreads, a.B), dim3(kThreads), 0, stream,
+                                   true, 1, static_cast<const float*>(y), a.B, a.d, ld, static_cast<__nv_bfloat16*>(pieces));
+    if (e != cudaSuccess) return e;
+    a.ldx = ld; a.x_len = ld; a.early = 0;
+    const int B = a.B;
+    for (int b0 = 0; b0 < B; b0 += kPieceRows) {
+      Q4Rows r = a;
+      r.B = B - b0 < kPieceRows ? B - b0 : kPieceRows;
+      r.cols = 3 * r.B;
+      r.x = static_cast<const __nv_bfloat16*>(pieces) + (size_t)3 * b0 * ld;
+      if (r.out) r.out += (size_t)b0 * r.N;
+      if (r.act) r.act += (size_t)b0 * r.cap;
+      if (r.member) r.member += (size_t)b0 * r.words;
+      const cudaError_t er = run_rows_nt<float, __nv_bfloat16>(r, true, stream);
+      if (er != cudaSuccess) return er;
+    }
+    return cudaSuccess;
+  }
+  a.x = y; a.cols = a.B; a.ldx = a.d; a.x_len = a.d;
+  return dt == DV_F16 ? run_rows_nt<__half, __half>(a, pdl, stream)
+                      : run_rows_nt<__nv_bfloat16, __nv_bfloat16>(a, pdl, stream);
+}
+
+template <typename S, int NT, bool kCols>
+cudaError_t run_cols(const Q4Cols& a, cudaStream_t stream) {
+  const int cols = kCols ? 3 * a.B : a.B;
+  const size_t smem = (size_t)128 * (cols | 1) * sizeof(float);
+  return launch_k(q4_cols_kernel<S, NT, kCols>, dim3((a.d + 127) / 128 * a.split), dim3(kThreads), smem, stream, true,
+                  a.split, a);
+}
+template <typename S>
+cudaError_t run_cols_nt(const Q4Cols& a, cudaStream_t stream) {
+  if (3 * a.B <= 8) return run_cols<S, 1, true>(a, stream);
+  if (a.B <= 8) return run_cols<S, 1, false>(a, stream);
+  if (a.B <= 16) return run_cols<S, 2, false>(a, stream);
+  return run_cols<S, 4, false>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_q4_quantize(const void* W, int N, int d, dv_dtype dt, int group, void* q, void* scale, void* values,
+                               int num_sms, cudaStream_t stream) {
+  const int blocks = (d + 127) / 128;
+  const long long total = (long long)N * blocks, per = kThreads / 16;
+  const long long ctas = (total + per - 1) / per, most = (long long)num_sms * 8;
+  const dim3 grid((unsigned)(ctas < most ? ctas : most));
+  const auto run = [&](auto* w) {
+    using T = std::remove_cv_t<std::remove_pointer_t<decltype(w)>>;
+    return launch_k(q4_quantize_kernel<T>, grid, dim3(kThreads), 0, stream, false, 1, static_cast<const T*>(w), d, blocks,
+                    total, group, static_cast<uint32_t*>(q), static_cast<T*>(scale), static_cast<T*>(values));
+  };
+  switch (dt) {
+    case DV_F32: return run(static_cast<const float*>(W));
+    case DV_F16: return run(static_cast<const __half*>(W));
+    case DV_BF16: return run(static_cast<const __nv_bfloat16*>(W));
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_q4_matvec(const Q4MatvecLaunch& L, dv_dtype dt, cudaStream_t stream) {
+  Q4Rows a{};
+  a.q = L.q; a.scale = L.scale; a.group = L.group; a.B = L.B; a.d = L.d; a.N = L.N;
+  a.out = L.out; a.accumulate = L.accumulate;
+  return launch_rows(a, L.y, L.pieces, dt, true, stream);
+}
+
+cudaError_t launch_q4_sparse_mlp(const Q4MlpLaunch& L, dv_dtype dt, WsHeader* hdr, cudaStream_t stream) {
+  Q4Rows a{};
+  a.q = L.q1; a.scale = L.s1; a.group = L.group1; a.B = L.B; a.d = L.d; a.N = L.N;
+  a.list = L.idx; a.count = L.count; a.cap = L.cap; a.act = L.act; a.hdr = hdr;
+  if (L.B > 1) {
+    const cudaError_t e =
+        launch_union(L.idx, L.cap, L.count, L.B, L.N, L.U, L.U_count, L.member, nullptr, hdr, stream);
+    if (e != cudaSuccess) return e;
+    a.list = L.U; a.count = L.U_count; a.cap = mlp_union_cap(L.B, L.N, L.cap);
+    a.member = L.member; a.words = (L.N + 31) / 32;
+  }
+  // batch 1 under the overlap policy: everything but y is read before the wait
+  a.early = launch_overlap() > 0 && L.B == 1 ? 1 : 0;
+  cudaError_t e = launch_rows(a, L.y, L.pieces, dt, a.early != 0, stream);
+  if (e != cudaSuccess) return e;
+  Q4Cols c{};
+  c.q = L.q2; c.scale = L.s2; c.group = L.group2; c.B = L.B; c.d = L.d; c.N = L.N;
+  c.list = a.list; c.count = a.count; c.cap = a.cap; c.act = L.act; c.out = L.out; c.accumulate = L.accumulate;
+  const int blocks = (L.d + 127) / 128;
+  c.pitch = (size_t)blocks * kBlockBytes;
+  c.groups = (L.d + L.group2 - 1) / L.group2;
+  c.split = 8;
+  switch (dt) {
+    case DV_F32: return run_cols_nt<float>(c, stream);
+    case DV_F16: return run_cols_nt<__half>(c, stream);
+    case DV_BF16: return run_cols_nt<__nv_bfloat16>(c, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace dv

@@ -117,6 +117,18 @@ typedef struct dv_kv {
   int n_max;        /* positions per sequence                                */
 } dv_kv;
 
+/* A matrix [N][d] in 4 bits with group scales (the pages have no counterpart:
+ * their weights are 16 bits wide): w[n][t] = (code[n][t] - 8) scale[n][t / group].
+ * A row is ceil(d / 128) blocks of 64 bytes.  The 32-bit word k of a block,
+ * g = k / 2 and s = k % 2, holds the codes of the elements 64 s + 8 g + e,
+ * e = 0..7, at bit 4 (e / 2) + 16 (e % 2).  What a block holds behind d does not
+ * matter (dv_q4_quantize writes 8). */
+typedef struct dv_q4 {
+  const void* q;      /* [N][64 ceil(d / 128)] bytes                          */
+  const void* scale;  /* [N][ceil(d / group)], storage type                   */
+  int group;          /* elements that share a scale: 64 or 128               */
+} dv_q4;
+
 /* ---------------------------------------------------------------- utility */
 
 const char* dv_status_str(dv_status s);
@@ -214,6 +226,55 @@ dv_status dv_sparse_mlp(const void* y, int B, int d, int N,
                         const int32_t* idx, int cap, const int32_t* count,
                         dv_dtype dt, float* out, int accumulate,
                         void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------ matrices in 4 bits */
+
+/* Quantise W [N][d] (dt, row lengths as everywhere) in groups of `group` (64 or
+ * 128) elements of a row, the last of a row as long as is left:
+ *     scale = max |w| / 7, rounded to the storage type,
+ *     code  = 8 + round-to-even(w / scale), kept within 0..15
+ * (8 where the scale is 0).  A group with a NaN or an infinity gets a NaN as its
+ * scale and codes 8: its products are NaNs.  q and scale as in dv_q4; values
+ * [N][d] (storage type), unless NULL: what the codes stand for, rounded once.
+ * Limits: N <= 16777216, d <= 65536; other groups return DV_ERR_UNSUPPORTED. */
+dv_status dv_q4_quantize(const void* W, int N, int d, dv_dtype dt, int group,
+                         void* q, void* scale, void* values,
+                         cudaStream_t stream);
+
+/* Workspace bytes of dv_q4_matvec. */
+dv_status dv_q4_matvec_workspace_size(int B, int d, int N, size_t* bytes);
+
+/* Products of B vectors with every row of a 4-bit matrix (an output head, a
+ * projection):
+ *     out[b][n] (+)= sum_t w[n][t] y[b][t],
+ * y [B][d] in the storage type of the scales, out [B][N] fp32, see
+ * dv_sparse_mlp for `accumulate`.  The weights enter as they are (no rounding),
+ * sums are fp32; results repeat bit for bit.  Like dv_layernorm's, its first
+ * kernel may be started before the kernel ahead of the call has ended and waits
+ * for it before it reads or writes anything.
+ * Limits: B <= 32, N <= 16777216, d <= 65536. */
+dv_status dv_q4_matvec(const void* y, int B, int d, int N, const dv_q4* W,
+                       dv_dtype dt, float* out, int accumulate,
+                       void* ws, size_t ws_bytes, cudaStream_t stream);
+
+dv_status dv_q4_sparse_mlp_workspace_size(int B, int d, int N, int cap,
+                                          size_t* bytes);
+
+/* dv_sparse_mlp with both matrices in 4 bits (their groups may differ):
+ *     out_b (+)= sum_{j in S_b} ReLU(y_b . W1[j]) W2[j],
+ * arguments as there.  An entry that a list holds twice counts once, and a
+ * neuron whose activation is 0 adds nothing, whatever its row of W2 holds.  The
+ * activations are fp32 and enter the second product as they are; every output
+ * has one writer and a fixed order of summation: results repeat bit for bit.
+ * dv_set_launch_overlap as for dv_sparse_mlp (16-bit storage).
+ * Device errors: DV_ERR_INDEX_RANGE (an entry outside [0, N) is skipped),
+ * DV_ERR_CAPACITY (a count above cap is cut off).
+ * Limits: B <= 32, N <= 65536, d <= 65536. */
+dv_status dv_q4_sparse_mlp(const void* y, int B, int d, int N, const dv_q4* W1,
+                           const dv_q4* W2, const int32_t* idx, int cap,
+                           const int32_t* count, dv_dtype dt, float* out,
+                           int accumulate, void* ws, size_t ws_bytes,
+                           cudaStream_t stream);
 
 /* ------------------------------------------------------------- attention */
 
