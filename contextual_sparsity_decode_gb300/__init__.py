@@ -10,6 +10,6 @@ from .binding import (  # noqa: F401
     dv_beam_select, dv_beam_select_workspace_size, dv_check, dv_kv_compact, dv_kv_reorder, dv_kv_repair,
     dv_layernorm, dv_lookahead, dv_positions_advance, dv_predict, dv_predict_workspace_size,
     dv_q4_matvec, dv_q4_matvec_workspace_size, dv_q4_quantize, dv_q4_sparse_mlp, dv_q4_sparse_mlp_workspace_size,
-    dv_sparse_attn, dv_sparse_attn_workspace_size, dv_sparse_mlp, dv_sparse_mlp_workspace_size,
+    dv_sample, dv_sample_workspace_size, dv_sparse_attn, dv_sparse_attn_workspace_size, dv_sparse_mlp, dv_sparse_mlp_workspace_size,
     dv_status_str, dv_tree_attn, dv_tree_attn_workspace_size, dv_version, dv_workspace_init, workspace,
 )

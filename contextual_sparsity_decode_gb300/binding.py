@@ -41,7 +41,7 @@ EXPORTS = (
     "dv_select_scores", "dv_tree_attn_workspace_size", "dv_tree_attn", "dv_kv_compact", "dv_kv_reorder",
     "dv_beam_select_workspace_size", "dv_beam_select",
     "dv_q4_quantize", "dv_q4_matvec_workspace_size", "dv_q4_matvec",
-    "dv_q4_sparse_mlp_workspace_size", "dv_q4_sparse_mlp",
+    "dv_q4_sparse_mlp_workspace_size", "dv_q4_sparse_mlp", "dv_sample_workspace_size", "dv_sample",
 )
 
 
@@ -120,6 +120,9 @@ _SIGS = {
     "dv_q4_sparse_mlp_workspace_size": ([_c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_sz)], _c_int),
     "dv_q4_sparse_mlp": ([_vp, _c_int, _c_int, _c_int, ctypes.POINTER(dv_q4), ctypes.POINTER(dv_q4), _vp, _c_int, _vp,
                           _c_int, _vp, _c_int, _vp, _sz, _vp], _c_int),
+    "dv_sample_workspace_size": ([_c_int, _c_int, ctypes.POINTER(_sz)], _c_int),
+    "dv_sample": ([_vp, _c_int, _c_int, ctypes.c_longlong, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+                  _c_int),
 }
 
 
@@ -566,6 +569,35 @@ def dv_beam_select(logits, cum, score, token, beam, ws, done=None, end_token=0, 
         _stream(stream))
     if st:
         _ok(st, "dv_beam_select")
+
+
+# --------------------------------------------------------------------- sampling
+
+def dv_sample_workspace_size(B: int, V: int) -> int:
+    n = ctypes.c_size_t(0)
+    _ok(lib().dv_sample_workspace_size(B, V, ctypes.byref(n)), "dv_sample_workspace_size")
+    return n.value
+
+
+def dv_sample(logits, u, token, ws, temperature=None, top_k=None, top_p=None, min_p=None, prob=None, stream=None):
+    """logits [B][V] (tokens adjacent), u [B]: token [B] int32 and prob [B],
+    unless None; temperature, top_p, min_p [B] fp32 and top_k [B] int32, or None
+    (see dv_sample in dv.h)."""
+    where = "dv_sample"
+    B, V = logits.shape
+    ld, adjacent = logits.stride()
+    if B == 1:
+        ld = V
+    if V > 1 and adjacent != 1:
+        raise DvError(1, where, "a row's logits adjacent")
+    _counted(where, B, u, temperature, top_p, min_p, prob, dtype=torch.float32)
+    _counted(where, B, top_k, token)
+    _here(where, logits, u, token, ws, temperature, top_k, top_p, min_p, prob)
+    st = (_lib or lib()).dv_sample(
+        logits.data_ptr(), B, V, ld, _dt(logits), u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+        token.data_ptr(), _ptr(prob), ws.data_ptr(), ws.numel(), _stream(stream))
+    if st:
+        _ok(st, where)
 
 
 # --------------------------------------------------------------------- labels

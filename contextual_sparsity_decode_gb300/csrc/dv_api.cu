@@ -787,6 +787,37 @@ dv_status dv_beam_select(const void* logits, int n_seq, int width, int V, long l
   return e == cudaSuccess ? DV_OK : cuda_fail(e);
 }
 
+// ---- sampling --------------------------------------------------------------------------------------
+
+namespace {
+bool sample_shape_ok(int B, int V) { return B >= 1 && B <= 65535 && V >= 1 && V <= kSampleMaxV; }
+}  // namespace
+
+dv_status dv_sample_workspace_size(int B, int V, size_t* bytes) {
+  if (!bytes || !sample_shape_ok(B, V)) return DV_ERR_INVALID_ARG;
+  *bytes = sizeof(WsHeader);
+  return DV_OK;
+}
+
+dv_status dv_sample(const void* logits, int B, int V, long long row_stride, dv_dtype dt, const float* u,
+                    const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                    int32_t* token, float* prob, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  Range nvtx_range("dv_sample");
+  if (!dtype_ok(dt)) return DV_ERR_DTYPE;
+  if (!logits || !u || !token || !aligned4(u) || !aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) ||
+      !aligned4(min_p) || !aligned4(token) || !aligned4(prob) ||
+      (reinterpret_cast<uintptr_t>(logits) & (dt == DV_F32 ? 3u : 1u)))
+    return DV_ERR_INVALID_ARG;
+  if (!sample_shape_ok(B, V) || row_stride < V) return DV_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, sizeof(WsHeader))) return DV_ERR_WORKSPACE;
+  SampleLaunch L{};
+  L.logits = logits; L.ld = row_stride; L.B = B; L.V = V;
+  L.u = u; L.temperature = temperature; L.top_k = top_k; L.top_p = top_p; L.min_p = min_p;
+  L.token = token; L.prob = prob;
+  cudaError_t e = launch_sample(L, dt, static_cast<WsHeader*>(ws), num_sms_current(), stream);
+  return e == cudaSuccess ? DV_OK : cuda_fail(e);
+}
+
 // ---- helpers ----------------------------------------------------------------------------------
 
 dv_status dv_layernorm(const float* x, int B, int d, float eps, void* y, dv_dtype dt,

@@ -395,6 +395,19 @@ cudaError_t launch_q4_quantize(const void* W, int N, int d, dv_dtype dt, int gro
 cudaError_t launch_q4_matvec(const Q4MatvecLaunch& L, dv_dtype dt, cudaStream_t stream);
 cudaError_t launch_q4_sparse_mlp(const Q4MlpLaunch& L, dv_dtype dt, WsHeader* hdr, cudaStream_t stream);
 
+// ---- sampling (k_sample.cu) --------------------------------------------------------
+
+constexpr int kSampleMaxV = 1 << 19;
+struct SampleLaunch {
+  const void* logits; long long ld; int B, V;   // B rows of V, ld elements apart
+  const float* u; const float* temperature; const int32_t* top_k; const float* top_p; const float* min_p;
+  int32_t* token; float* prob;
+  // set by the launcher: CTAs of a row, and each one's 16-byte vectors of it
+  int split, part_vecs;
+  WsHeader* hdr; long long wait_ns;
+};
+cudaError_t launch_sample(const SampleLaunch& a, dv_dtype dt, WsHeader* hdr, int num_sms, cudaStream_t stream);
+
 // ---- misc (k_misc.cu) --------------------------------------------------------
 
 cudaError_t launch_layernorm(const float* x, int B, int d, float eps, void* y,

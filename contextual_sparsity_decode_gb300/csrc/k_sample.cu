@@ -1,0 +1,767 @@
+// Sampling: one token of each row of logits, drawn with a given number u from
+// the softmax at temperature T, cut to the top k, to the nucleus of mass p and to
+// the tokens that have min_p of the best one's probability.
+//
+// Weights are integers, w(x) = 2^39 exp((x - max) / T) rounded, from arithmetic
+// that is exact to 2^-31 of the weight: sums of them are exact whatever their order, so that
+// the cut and the token are those of the definition unless u (or p) is within
+// about 1e-10 of a border, and results do not depend on how a row is split.
+// (With sums of 32-bit exponentials, 1e-6 off, one row in ten of a large
+// vocabulary would draw a neighbour.)
+//
+// One cluster per row: its CTAs hold the row in shared memory, brought once by
+// bulk copies, and every later pass reads it there.
+//   maximum     as the copies arrive; T = 0 ends with its lowest place.
+//   top k       a histogram of counts over kBins steps of x below the maximum, the
+//               bin that the k-th token falls into; k of a few hundred at most:
+//               the tokens down to that bin are listed and the first CTA does the
+//               rest on the list.  Otherwise the bin is refined until it holds a
+//               list of tokens or a single value.
+//   nucleus     the same with sums of weights; only tokens of more than
+//               (1 - p) / V of the mass are looked at (the others together
+//               are less than what is cut off).
+//   draw        sums of the kept tokens' weights by groups of 32 vectors, the
+//               CTA and the group that u falls into, the token within it.
+// Equal values are taken by their index where the cut passes among them.
+
+#include <cfloat>
+#include <climits>
+
+#include "dv_kernels.h"
+#include "tc_common.cuh"
+
+namespace dv {
+namespace {
+
+typedef unsigned long long u64;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 1024;
+constexpr int kList = 256;                 // tokens ranked against each other: one a thread
+constexpr int kChunks = 8;                 // bulk copies of a CTA's part of the row
+constexpr int kMaxCluster = 16;
+constexpr int kMaxGroups = kSampleMaxV * 4 / 16 / kMaxCluster / 32 + 2;   // groups of 32 vectors, at most
+constexpr int kUnit = 39;                  // a weight of 1 is 2^39
+constexpr float kReach = 28.5f;            // exp(-28.5) 2^39 < 1/4: nothing below weighs anything
+constexpr float kCold = 1e-30f, kHot = 1e30f;
+constexpr long long kUnwindNs = 2000000000LL;
+static_assert(kThreads == 256 && kList == 256, "a thread per table entry and per listed token");
+
+// 2^(39 + j / 256), rounded, from square roots of 2.
+struct Powers {
+  u64 v[256];
+};
+constexpr double root_of(double a) {
+  double x = 1.0 + (a - 1.0) / 2;
+  for (int i = 0; i < 40; ++i) x = (x + a / x) / 2;
+  return x;
+}
+constexpr Powers make_powers() {
+  Powers p{};
+  double root[8] = {};                     // 2^(1/2), 2^(1/4), ...
+  double a = 2.0;
+  for (int i = 0; i < 8; ++i) root[i] = a = root_of(a);
+  for (int j = 0; j < 256; ++j) {
+    double x = 549755813888.0;             // 2^39
+    for (int i = 0; i < 8; ++i)
+      if (j >> (7 - i) & 1) x *= root[i];
+    p.v[j] = (u64)(x + 0.5);
+  }
+  return p;
+}
+__device__ constexpr Powers kPowers = make_powers();
+
+__device__ __forceinline__ uint32_t ord32(float f) {
+  const uint32_t u = __float_as_uint(f + 0.f);   // (-0 as 0)
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float unord32(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+
+// The weight of x below the maximum m: y = (x - m) log2(e) / T as the sum of two
+// floats (exact difference, product with log2(e) / T in two floats), 2^y as a
+// table entry times 1 + z, |z| < 2^-9.5, and a shift.
+struct Scale {
+  float m, hi, lo;   // hi + lo = log2(e) / T
+  const u64* table;
+  __device__ __forceinline__ u64 operator()(float x) const {
+    const float d = __fsub_rn(x, m), b = __fsub_rn(d, x);
+    const float e = __fadd_rn(__fsub_rn(x, __fsub_rn(d, b)), __fsub_rn(-m, b));   // x - m = d + e
+    const float y = __fmul_rn(d, hi);
+    const float below = __fmaf_rn(d, lo, __fmaf_rn(e, hi, __fmaf_rn(d, hi, -y)));
+    constexpr float kMagic = 49152.f;               // 1.5 2^15: sums are multiples of 2^-8
+    const float t = __fadd_rn(fmaxf(y, -60.f), kMagic);
+    const int k = __float_as_int(t) - __float_as_int(kMagic);   // y = k / 256 + r, |r| <= 2^-9
+    const float r = __fsub_rn(y, __fsub_rn(t, kMagic));
+    const float q = __fmul_rn(r, 0.69314718056f);
+    const float s = __fmul_rn(__fmul_rn(q, q), __fmaf_rn(q, __fmaf_rn(q, 1.f / 24, 1.f / 6), 0.5f));
+    // r ln 2 in one product and the rest of it with the small terms: 2^-24 of 2^-9.5
+    const float z = __fmaf_rn(r, 0.69314718056f, __fmaf_rn(below, 0.69314718056f, __fmaf_rn(r, -1.9046542e-9f, s)));
+    const u64 base = table[k & 255];
+    const float near = __uint_as_float(0x3f800000u | ((uint32_t)(base >> 16) & 0x007fffffu));   // 2^(j/256)
+    const u64 w = base + (u64)(long long)__float2int_rn(__fmul_rn(z, __fmul_rn(near, 549755813888.f)));
+    const int shift = -(k >> 8);
+    const u64 out = (w + ((1ull << shift) >> 1)) >> shift;
+    return y > -40.5f ? out : 0;                    // (NaN: x is -inf, or so far below that y is)
+  }
+};
+
+// Where the order (x descending, then index) is cut: kept are tokens before and
+// at (key, index).
+struct Cut {
+  uint32_t key;
+  int index;   // in the row's vectors; a CTA's own where the cut is among equal values
+  __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= index); }
+};
+
+struct Shared {
+  u64 table[256];
+  u64 group[kMaxGroups];       // sums of 32 vectors
+  u64 box[2][kMaxCluster][2];  // what the cluster's CTAs tell each other
+  u64 answer[2][2];            // what one of them tells all
+  u64 list[kList];             // (key, lower index first)
+  u64 weight[kList], sorted[kList];
+  u64 bins[kBins];
+  uint32_t count[kBins], carry[kBins];
+  u64 scan[kWarps];
+  float redm[kWarps];
+  int redi[kWarps];
+  uint64_t full[kChunks];
+  u64 rest;
+  uint32_t listed;
+  int found, late;
+};
+
+__device__ __forceinline__ uint32_t remote(const void* local, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::saddr(local)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_remote(u64* local, uint32_t rank, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote(local, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_remote(const uint32_t* local, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(local, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t add_remote(uint32_t* local, uint32_t rank, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(remote(local, rank)), "r"(v) : "memory");
+  return old;
+}
+
+// All threads of the cluster meet, with what they have written to each other.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+}
+
+// Sum over a warp of values of 2^42 at most.
+__device__ __forceinline__ u64 warp_sum_u64(u64 v) {
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x1fffffu);
+  const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 21));
+  return ((u64)hi << 21) + lo;
+}
+// Inclusive sum over the block's threads; *total: all of it.  Two barriers.
+__device__ __forceinline__ u64 block_scan(u64 v, u64* tmp, u64* total) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 n = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += n;
+  }
+  __syncthreads();
+  if (lane == 31) tmp[wid] = v;
+  __syncthreads();
+  u64 before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < wid) before += tmp[w];
+    all += tmp[w];
+  }
+  *total = all;
+  return v + before;
+}
+
+template <typename T>
+struct Row {
+  static constexpr int E = 16 / sizeof(T);   // tokens of a vector
+  Shared& sh;
+  const uint8_t* part;     // the CTA's vectors
+  int v0, vecs;            // its first one, and how many
+  uint32_t rank, size;     // in the cluster
+  int turn = 0;            // exchanges so far
+
+  __device__ __forceinline__ void open(int v, float* f) const {
+    unpack<T>(*reinterpret_cast<const uint4*>(part + (size_t)v * 16), f);
+  }
+  // Every CTA's two values, in box[turn of this call].
+  __device__ __forceinline__ int exchange(u64 a, u64 b) {
+    const int t = turn++ & 1;
+    if (threadIdx.x < size) {
+      st_remote(&sh.box[t][rank][0], threadIdx.x, a);
+      st_remote(&sh.box[t][rank][1], threadIdx.x, b);
+    }
+    cluster_sync();
+    return t;
+  }
+  // f(key, index, x) of every token of the CTA above -inf
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    for (int v = threadIdx.x; v < vecs; v += kThreads) {
+      float x[E];
+      open(v, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (x[e] > -INFINITY) f(x[e], (v0 + v) * E + e);
+    }
+  }
+
+  // The bin that holds the `target`-th unit (of count or weight) of the
+  // histogram that all CTAs have filled: returns it, with what is before it and in
+  // it; kBins if there is less in all.  kMass: the sums are count + 2^32 carry.
+  template <bool kMass>
+  __device__ __forceinline__ int crossing(u64 target, u64* before, u64* inside) {
+    cluster_sync();   // the histograms are complete
+    const int mine = kBins / size;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {   // `size` lanes to a bin
+      const int b = rank * mine + i / size, src = i % size;
+      u64 v = ld_remote(&sh.count[b], src);
+      if (kMass) v += (u64)ld_remote(&sh.carry[b], src) << 32;
+      for (uint32_t o = size >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (src == 0) sh.bins[i / size] = v;
+    }
+    __syncthreads();
+    const int per = (mine + kThreads - 1) / kThreads, first = threadIdx.x * per;
+    u64 sum = 0, total;
+    for (int k = 0; k < per; ++k)
+      if (first + k < mine) sum += sh.bins[first + k];
+    const u64 upto = block_scan(sum, sh.scan, &total);
+    const int t = exchange(total, 0);
+    u64 ahead = 0, all = 0;
+    for (uint32_t r = 0; r < size; ++r) {
+      if (r < rank) ahead += sh.box[t][r][0];
+      all += sh.box[t][r][0];
+    }
+    if (all < target) return kBins;   // (the same in every CTA)
+    u64 at = ahead + upto - sum;
+    if (at < target && target <= at + sum) {   // one thread of the cluster
+      int k = 0;
+      while (at + sh.bins[first + k] < target) at += sh.bins[first + k++];
+      const u64 what = ((u64)(rank * mine + first + k) << 48), in = sh.bins[first + k];
+      for (uint32_t r = 0; r < size; ++r) {
+        st_remote(&sh.answer[0][0], r, at);
+        st_remote(&sh.answer[0][1], r, in);
+        st_remote(&sh.answer[1][0], r, what);
+      }
+    }
+    cluster_sync();
+    *before = sh.answer[0][0];
+    *inside = sh.answer[0][1];
+    return (int)(sh.answer[1][0] >> 48);
+  }
+  __device__ __forceinline__ void clear_bins() {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.count[i] = sh.carry[i] = 0;
+    __syncthreads();
+  }
+  template <bool kMass>
+  __device__ __forceinline__ void add_bin(int b, u64 w) {
+    if (!kMass) {
+      atomicAdd(&sh.count[b], 1u);
+    } else {
+      const uint32_t lo = (uint32_t)w, old = atomicAdd(&sh.count[b], lo);
+      const uint32_t up = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
+      if (up) atomicAdd(&sh.carry[b], up);
+    }
+  }
+  // Tokens that `take` into every CTA's list, their number into the first CTA's
+  // `listed`, which has been cleared, and a cluster barrier passed since.
+  template <typename F>
+  __device__ __forceinline__ void gather(F take) {
+    each([&](float x, int i) {
+      if (!take(x, i)) return;
+      const uint32_t at = add_remote(&sh.listed, 0, 1);
+      if (at < (uint32_t)kList)
+        for (uint32_t r = 0; r < size; ++r) st_remote(&sh.list[at], r, ((u64)ord32(x) << 32) | (uint32_t)~i);
+    });
+    cluster_sync();
+  }
+  // The group of 32 vectors, in order, that the sum `left` falls into: the first
+  // whose sum up to and with it is above `left`; *left becomes what is left in it.
+  // Some group's is.  Two barriers or more.
+  __device__ __forceinline__ int locate(u64* left) {
+    constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
+    const int groups = (vecs + 31) / 32;
+    u64 sum = 0, unused;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) sum += (int)threadIdx.x * kPer + q < groups ? sh.group[threadIdx.x * kPer + q] : 0;
+    const u64 upto = block_scan(sum, sh.scan, &unused);
+    if (upto > *left && upto - sum <= *left) {
+      u64 at = upto - sum;
+      int g = threadIdx.x * kPer;
+      while (at + sh.group[g] <= *left) at += sh.group[g++];
+      sh.found = g;
+      sh.rest = *left - at;
+    }
+    __syncthreads();
+    *left = sh.rest;
+    return sh.found;
+  }
+};
+
+__device__ __forceinline__ float listed_x(u64 entry) { return unord32((uint32_t)(entry >> 32)); }
+
+// The cut of the order at the `target`-th unit of count or weight among the tokens
+// that `have` keeps; `have` itself if they hold less.  `step`: bins per unit of x
+// below the maximum.  `first` (kBins: none): the first histogram's answer, if known.
+template <bool kMass, typename T>
+__device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut have, u64 target, float step,
+                                        u64 floor_weight, int b1, u64 before, u64 inside) {
+  Shared& sh = row.sh;
+  if (b1 < 0) {
+    row.clear_bins();
+    row.each([&](float x, int i) {
+      const uint32_t b = __float2uint_rz((weigh.m - x) * step);
+      if (b >= (uint32_t)kBins || !have.keeps(ord32(x), i)) return;
+      u64 w = 0;
+      if (kMass) {
+        w = weigh(x);
+        if (w < floor_weight) return;
+      }
+      row.template add_bin<kMass>((int)b, w);
+    });
+    b1 = row.template crossing<kMass>(target, &before, &inside);
+    if (b1 == kBins) return have;
+  }
+  // keys of the bin, a bin more on either side
+  const float top = b1 > 0 ? weigh.m - (float)(b1 - 1) / step : weigh.m;
+  const float low = fmaxf(weigh.m - (float)(b1 + 2) / step, -FLT_MAX);
+  uint32_t khi = ord32(fminf(top, weigh.m)), klo = ord32(low);
+  uint32_t done_lo = 0, done_hi = 0xffffffffu;   // refined: keys within
+  for (;;) {
+    const auto within = [&](float x, uint32_t k) {
+      return k >= done_lo && k <= done_hi && __float2uint_rz((weigh.m - x) * step) == (uint32_t)b1;
+    };
+    // how many tokens are left, at most: their weight over the least of them
+    const u64 least = kMass ? weigh(unord32(max(klo, done_lo))) : 1;
+    const bool few = least > 0 && inside <= (u64)kList * least;
+    if (few) {
+      if (threadIdx.x == 0) sh.listed = 0;
+      cluster_sync();
+      row.gather([&](float x, int i) {
+        return within(x, ord32(x)) && have.keeps(ord32(x), i) && (!kMass || weigh(x) >= floor_weight);
+      });
+      // (no CTA ends before the cluster's next barrier: the draw has one)
+      const int n = min((int)ld_remote(&sh.listed, 0), kList), i = threadIdx.x;
+      if (i < n) sh.weight[i] = kMass ? weigh(listed_x(sh.list[i])) : 1;
+      __syncthreads();
+      if (i < n) {
+        u64 at = before;
+        for (int j = 0; j < n; ++j)
+          if (sh.list[j] > sh.list[i]) at += sh.weight[j];
+        if (at < target && target <= at + sh.weight[i]) sh.sorted[0] = sh.list[i];
+      }
+      __syncthreads();
+      const u64 last = sh.sorted[0];
+      __syncthreads();
+      return Cut{(uint32_t)(last >> 32), (int)~(uint32_t)last};
+    }
+    if (klo == khi) break;   // one value
+    int shift = 0;
+    while ((khi - klo) >> shift >= (uint32_t)kBins) ++shift;
+    row.clear_bins();
+    row.each([&](float x, int i) {
+      const uint32_t k = ord32(x);
+      if (!within(x, k) || !have.keeps(k, i)) return;
+      u64 w = 0;
+      if (kMass) {
+        w = weigh(x);
+        if (w < floor_weight) return;
+      }
+      // (keys a rounding outside of the bin's edges count at its ends)
+      const uint32_t b = k >= khi ? 0 : min((khi - k) >> shift, (uint32_t)kBins - 1);
+      row.template add_bin<kMass>((int)b, w);
+    });
+    u64 ahead;
+    const int b = row.template crossing<kMass>(target - before, &ahead, &inside);
+    if (b == kBins) return have;
+    before += ahead;
+    done_hi = min(done_hi, khi - ((uint32_t)b << shift));
+    const uint32_t span = (1u << shift) - 1, upper = khi - ((uint32_t)b << shift);
+    done_lo = max(done_lo, upper - min(span, upper - klo));
+    klo = done_lo;
+    khi = done_hi;
+  }
+  // equal values: the first r of them, by index
+  const u64 one = kMass ? weigh(unord32(klo)) : 1;
+  const u64 r = (target - before + one - 1) / one;
+  u64 here = 0, total;
+  // (index order: a warp to a group of 32 vectors, as in the draw)
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, groups = (row.vecs + 31) / 32;
+  for (int g = wid; g < groups; g += kWarps) {
+    uint32_t n = 0;
+    const int v = g * 32 + lane;
+    if (v < row.vecs) {
+      float x[Row<T>::E];
+      row.open(v, x);
+#pragma unroll
+      for (int e = 0; e < Row<T>::E; ++e)
+        n += x[e] > -INFINITY && ord32(x[e]) == klo && have.keeps(klo, (row.v0 + v) * Row<T>::E + e);
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) sh.group[g] = n;
+    here += n;
+  }
+  (void)block_scan(lane == 0 ? here : 0, sh.scan, &total);
+  const int t = row.exchange(total, 0);
+  u64 ahead = 0;
+  for (uint32_t q = 0; q < row.rank; ++q) ahead += sh.box[t][q][0];
+  Cut cut{klo, -1};
+  if (ahead + total <= r) {
+    cut.index = INT_MAX;
+  } else if (ahead < r) {
+    // the CTA's own (r - ahead)-th of them
+    u64 left = r - ahead - 1;
+    const int v = row.locate(&left) * 32 + lane;
+    uint32_t n = 0, bits = 0;
+    if (v < row.vecs) {
+      float x[Row<T>::E];
+      row.open(v, x);
+#pragma unroll
+      for (int e = 0; e < Row<T>::E; ++e)
+        if (x[e] > -INFINITY && ord32(x[e]) == klo && have.keeps(klo, (row.v0 + v) * Row<T>::E + e)) bits |= 1u << e;
+    }
+    n = __popc(bits);
+    uint32_t upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t m = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += m;
+    }
+    int index = -1;
+    if (upto - n <= left && left < upto) {
+      for (uint32_t skip = (uint32_t)left - (upto - n); skip; --skip) bits &= bits - 1;
+      index = (row.v0 + v) * Row<T>::E + __ffs(bits) - 1;
+    }
+    cut.index = __reduce_max_sync(0xffffffffu, index);
+  }
+  // (a value equal to the cut's that `have` left out stays out: have's index is smaller there)
+  if (have.key == cut.key) cut.index = min(cut.index, have.index);
+  __syncthreads();
+  return cut;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a) {
+  extern __shared__ __align__(128) uint8_t part[];
+  __shared__ Shared sh;
+  constexpr int E = 16 / sizeof(T);
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const uint32_t rank = blockIdx.x % a.split;
+  const int b = blockIdx.x / a.split;
+  sh.table[tid] = kPowers.v[tid];
+  if (tid == 0) {
+    for (int q = 0; q < kChunks; ++q) tc::mbar_init(&sh.full[q], 1);
+    tc::fence_mbar_init();
+    sh.listed = 0;
+    sh.late = 0;
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  __syncthreads();
+  // The row as 16-byte vectors from the boundary at or below its first token on;
+  // the tokens of its first and last vector that are not the row's are -inf.
+  const T* x0 = static_cast<const T*>(a.logits) + (size_t)b * a.ld;
+  const int off = (int)((reinterpret_cast<uintptr_t>(x0) & 15u) / sizeof(T));
+  const int all = (off + a.V + E - 1) / E;
+  const char* base = reinterpret_cast<const char*>(x0 - off);
+  const int v0 = min((int)rank * a.part_vecs, all), v1 = min(v0 + a.part_vecs, all), vecs = v1 - v0;
+  const int whole0 = max(v0, off > 0 ? 1 : 0), whole1 = max(whole0, min(v1, (off + a.V) / E));  // copied
+  const int chunk = (a.part_vecs + kChunks - 1) / kChunks;
+  if (tid == 0)
+    for (int q = 0; q < kChunks; ++q) {
+      const int c0 = max(whole0, v0 + q * chunk), c1 = min(whole1, v0 + (q + 1) * chunk);
+      const uint32_t bytes = c1 > c0 ? (uint32_t)(c1 - c0) * 16 : 0;
+      tc::mbar_arrive_expect_tx(&sh.full[q], bytes);
+      if (bytes) tc::bulk_g2s(part + (size_t)(c0 - v0) * 16, base + (size_t)c0 * 16, bytes, &sh.full[q]);
+    }
+  for (int i = tid; i < 2 * E; i += kThreads) {   // the ends
+    const int v = i < E ? 0 : all - 1, t = v * E + i % E;   // token t - off
+    const bool edge = v < whole0 || v >= whole1;
+    if (v >= v0 && v < v1 && edge)
+      reinterpret_cast<T*>(part)[(size_t)(v - v0) * E + i % E] =
+          t >= off && t < off + a.V ? x0[t - off] : Elem<T>::from_f(-INFINITY);
+  }
+  const float temp = a.temperature ? a.temperature[b] : 1.f;
+  const float u = a.u[b];
+  const int k = a.top_k ? a.top_k[b] : 0;
+  const float p = a.top_p ? a.top_p[b] : 1.f;
+  const float min_p = a.min_p ? a.min_p[b] : 0.f;
+  __syncthreads();
+  Row<T> row{sh, part, v0, vecs, rank, (uint32_t)a.split};
+
+  // ---- maximum
+  float m = -INFINITY;
+  bool bad = false;
+  for (int q = 0; q < kChunks; ++q) {
+    if (lane == 0 && !tc::mbar_wait_soon(&sh.full[q], 0, a.wait_ns)) {
+      sh.late = 1;
+      set_error(a.hdr, DV_ERR_TIMEOUT, 61);
+    }
+    __syncwarp();
+    if (*reinterpret_cast<volatile int*>(&sh.late)) break;
+    const int c1 = min(vecs, (q + 1) * chunk);
+    for (int v = q * chunk + tid; v < c1; v += kThreads) {
+      float f[E];
+      row.open(v, f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        bad |= !(f[e] <= FLT_MAX);   // a NaN or +inf
+        m = fmaxf(m, f[e]);
+      }
+    }
+  }
+  m = warp_max(m);
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0) {
+    sh.redm[wid] = m;
+    sh.redi[wid] = bad;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    m = fmaxf(m, sh.redm[w]);
+    bad |= sh.redi[w] != 0;
+  }
+  bad |= sh.late != 0;
+  if (sh.late && tid == 0)   // no copy may be in flight when the CTA ends
+    for (int q = 0; q < kChunks; ++q)
+      if (!tc::mbar_wait(&sh.full[q], 0, kUnwindNs > a.wait_ns ? kUnwindNs : a.wait_ns)) break;
+  {
+    const int t = row.exchange(__float_as_uint(m), bad ? 1 : 0);
+    for (uint32_t r = 0; r < row.size; ++r) {
+      m = fmaxf(m, __uint_as_float((uint32_t)sh.box[t][r][0]));
+      bad |= sh.box[t][r][1] != 0;
+    }
+  }
+  // (temperatures beyond kCold and kHot: log2(e) / T or a difference of logits leaves the range of fp32)
+  bad |= !(m > -INFINITY) || !(temp == 0.f || (temp >= kCold && temp <= kHot)) || u != u || p != p || min_p != min_p;
+  if (bad) {   // the same in every CTA of the cluster
+    if (rank == 0 && tid == 0) {
+      a.token[b] = -1;
+      if (a.prob) a.prob[b] = 0.f;
+      set_error(a.hdr, DV_ERR_INVALID_ARG, b);
+    }
+    cluster_sync();
+    return;
+  }
+
+  if (temp == 0.f) {   // the best token, the first of equal ones
+    int first = INT_MAX;
+    row.each([&](float x, int i) {
+      if (x == m) first = min(first, i);
+    });
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) sh.redi[wid] = first;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) first = min(first, sh.redi[w]);
+    const int t = row.exchange((u64)(uint32_t)first, 0);
+    for (uint32_t r = 0; r < row.size; ++r) first = min(first, (int)(uint32_t)sh.box[t][r][0]);
+    if (rank == 0 && tid == 0) {
+      a.token[b] = first - off;
+      if (a.prob) a.prob[b] = 1.f;
+    }
+    cluster_sync();
+    return;
+  }
+
+  Scale weigh;
+  {
+    const double c = 1.4426950408889634 / (double)temp;
+    weigh.m = m;
+    weigh.hi = (float)c;
+    weigh.lo = (float)(c - (double)weigh.hi);
+    weigh.table = sh.table;
+  }
+  const float step = (float)kBins / (kReach * temp);
+  const u64 unit = 1ull << kUnit;
+  const u64 least = min_p > 0.f ? (u64)ceil(fmin((double)min_p, 1.0) * (double)unit) : 0;
+  const auto mass_target = [&](u64 mass) {   // tokens are kept while what is before them is below
+    return max((u64)ceil(fmax((double)p, 0.0) * (double)mass), (u64)1);
+  };
+  const auto draw_target = [&](u64 mass) {   // the token whose sum is the first above
+    const double t = floor(fmax((double)u, 0.0) * (double)mass);
+    return t < (double)mass ? (u64)t : mass - 1;
+  };
+  const auto put = [&](float x, int i, u64 mass) {
+    a.token[b] = i - off;
+    if (a.prob) {
+      const double y = ((double)x - (double)m) / (double)temp;
+      a.prob[b] = (float)(exp(y) * (double)unit / (double)mass);
+    }
+  };
+  Cut cut{0, INT_MAX};
+  const bool has_k = k > 0 && k < a.V, has_p = p < 1.f;
+
+  // ---- top k
+  if (has_k) {
+    row.clear_bins();
+    row.each([&](float x, int) {
+      const uint32_t bin = __float2uint_rz((m - x) * step);
+      if (bin < (uint32_t)kBins) row.template add_bin<false>((int)bin, 0);
+    });
+    u64 before, inside;
+    const int bin = row.template crossing<false>((u64)k, &before, &inside);
+    if (bin < kBins && before + inside <= (u64)kList) {
+      // the few best tokens: one CTA does the rest
+      row.gather([&](float x, int) { return __float2uint_rz((m - x) * step) <= (uint32_t)bin; });
+      if (rank != 0) return;
+      const int n = min((int)sh.listed, kList);
+      u64 mine = 0, w = 0;
+      int at = 0;
+      if (tid < n) {
+        mine = sh.list[tid];
+        for (int j = 0; j < n; ++j) at += sh.list[j] > mine;
+        w = weigh(listed_x(mine));
+      }
+      __syncthreads();
+      if (tid < n) {
+        sh.sorted[at] = mine;
+        sh.weight[at] = at < k ? w : 0;
+      }
+      __syncthreads();
+      u64 mass, v = tid < n ? sh.weight[tid] : 0;
+      const u64 upto = block_scan(v, sh.scan, &mass);
+      const bool keep = tid < n && tid < k && (!has_p || upto - v < mass_target(mass)) && v >= least;
+      __syncthreads();
+      if (tid < n) sh.weight[tid] = keep ? v : 0;
+      (void)block_scan(keep ? v : 0, sh.scan, &mass);
+      if (keep && v) {
+        mine = sh.sorted[tid];
+        u64 sum = 0;   // of the kept tokens up to this one by index
+        for (int j = 0; j < n; ++j) sum += (uint32_t)~sh.sorted[j] <= (uint32_t)~mine ? sh.weight[j] : 0;
+        const u64 t = draw_target(mass);
+        if (sum > t && sum - v <= t) put(listed_x(mine), (int)~(uint32_t)mine, mass);
+      }
+      return;
+    }
+    if (bin < kBins) cut = find_cut<false>(row, weigh, cut, (u64)k, step, 0, bin, before, inside);
+  }
+
+  // ---- sums of groups of 32 vectors: kept tokens that weigh `low` at least
+  const int groups = (vecs + 31) / 32;
+  const auto sums = [&](u64 low, u64* total) {
+    u64 mine = 0;
+    for (int g = wid; g < groups; g += kWarps) {
+      const int v = g * 32 + lane;
+      u64 w = 0;
+      if (v < vecs) {
+        float x[E];
+        row.open(v, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const u64 we = weigh(x[e]);
+          if (we >= low && cut.keeps(ord32(x[e]), (v0 + v) * E + e)) w += we;
+        }
+      }
+      w = warp_sum_u64(w);
+      if (lane == 0) sh.group[g] = w;
+      mine += w;
+    }
+    (void)block_scan(lane == 0 ? mine : 0, sh.scan, total);
+    __syncthreads();
+  };
+
+  // ---- nucleus
+  u64 total, mass = 0, ahead = 0;
+  if (has_p) {
+    sums(0, &total);
+    int t = row.exchange(total, 0);
+    for (uint32_t r = 0; r < row.size; ++r) mass += sh.box[t][r][0];
+    // tokens below this weight add up to less than what is cut off, even all V of them
+    const u64 low = (u64)fmax(0.0, floor((1.0 - fmax((double)p, 0.0)) * (double)mass / (double)a.V) - 1.0);
+    cut = find_cut<true>(row, weigh, cut, mass_target(mass), step, low, -1, 0, 0);
+  }
+
+  // ---- draw
+  sums(least, &total);
+  const int t = row.exchange(total, 0);
+  mass = 0;
+  for (uint32_t r = 0; r < row.size; ++r) {
+    if (r < rank) ahead += sh.box[t][r][0];
+    mass += sh.box[t][r][0];
+  }
+  const u64 aim = draw_target(mass);
+  if (aim < ahead || aim >= ahead + total) return;   // (nothing of this CTA is read by others any more)
+  u64 left = aim - ahead;
+  const int v = row.locate(&left) * 32 + lane;
+  if (wid != 0) return;
+  float x[E];
+  u64 we[E], w = 0;
+  if (v < vecs) row.open(v, x);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    we[e] = 0;
+    if (v < vecs) {
+      const u64 full = weigh(x[e]);
+      if (full >= least && cut.keeps(ord32(x[e]), (v0 + v) * E + e)) we[e] = full;
+    }
+    w += we[e];
+  }
+  u64 run = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 n = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += n;
+  }
+  if (run > left && run - w <= left) {
+    u64 at = run - w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (at <= left && left < at + we[e]) put(x[e], (v0 + v) * E + e, mass);
+      at += we[e];
+    }
+  }
+}
+
+template <typename T>
+cudaError_t run_sample(const SampleLaunch& a, cudaStream_t stream) {
+  static PerDevice attr;   // function attributes are per device
+  const cudaError_t ea = (cudaError_t)attr.get(current_device(), [] {
+    const cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return (int)e;
+    return (int)cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)(kSampleMaxV * sizeof(T) / kMaxCluster + 1024));
+  });
+  if (ea != cudaSuccess) return ea;
+  return launch_k(sample_kernel<T>, dim3((unsigned)a.B * a.split), dim3(kThreads), (size_t)a.part_vecs * 16, stream, true,
+                  a.split, a);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const SampleLaunch& L, dv_dtype dt, WsHeader* hdr, int num_sms, cudaStream_t stream) {
+  SampleLaunch a = L;
+  a.hdr = hdr;
+  a.wait_ns = wait_limit_ns();
+  const long long es = dt == DV_F32 ? 4 : 2, bytes = a.V * es;
+  int c = 1;
+  while (c < kMaxCluster && bytes > (long long)c * 32768) c *= 2;
+  while (c < kMaxCluster && (long long)a.B * c * 2 <= num_sms && a.V > c * 4096) c *= 2;
+  a.split = c;
+  const int E = (int)(16 / es), vecs = (a.V + 2 * E - 2) / E;
+  a.part_vecs = ((vecs + c - 1) / c + 31) / 32 * 32;
+  switch (dt) {
+    case DV_F32: return run_sample<float>(a, stream);
+    case DV_F16: return run_sample<__half>(a, stream);
+    case DV_BF16: return run_sample<__nv_bfloat16>(a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace dv

@@ -72,7 +72,8 @@ extern "C" {
 
 typedef enum dv_status {
   DV_OK = 0,
-  DV_ERR_INVALID_ARG = 1,  /* null pointer, bad size, misalignment, cap < k */
+  DV_ERR_INVALID_ARG = 1,  /* null pointer, bad size, misalignment, cap < k;
+                              device: a row that dv_sample cannot draw from  */
   DV_ERR_DTYPE = 2,        /* unsupported storage / output type            */
   DV_ERR_WORKSPACE = 3,    /* workspace missing or smaller than required   */
   DV_ERR_CUDA = 4,         /* a CUDA call failed: see dv_last_cuda_error() */
@@ -468,6 +469,44 @@ dv_status dv_beam_select(const void* logits, int n_seq, int width, int V,
                          float* score, int32_t* token, int32_t* beam,
                          void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------- sampling */
+
+/* Workspace bytes of dv_sample. */
+dv_status dv_sample_workspace_size(int B, int V, size_t* bytes);
+
+/* One token of each row, drawn with the caller's random number (the pages have
+ * no counterpart: they end with the logits).  For row b, x = logits[b],
+ *     w_i = exp((x_i - max x) / T),
+ * and the tokens in the order of x descending, of equal ones the lower index
+ * first, kept are
+ *   the first top_k (all if top_k <= 0);
+ *   of those, the ones before which less than top_p of their mass lies: the
+ *     smallest set that holds top_p of it (the first token always; all if
+ *     top_p >= 1);
+ *   of those, the ones with w_i >= min_p (min_p above 1 counts as 1).
+ * token[b] is the lowest kept i for which the kept w up to and with i add up to
+ * more than u of the sum of all kept w; prob[b], unless NULL, is w_i over that
+ * sum.  T = 0: the best token, prob 1; otherwise 1e-30 <= T <= 1e30.
+ *  logits: B rows of V, row_stride elements apart; any alignment.  -inf tokens
+ *     are never drawn.
+ *  u [B] in [0, 1) (below counts as 0, above as just below 1); temperature,
+ *     top_p, min_p [B] fp32, top_k [B] int32, each or NULL: 1, 1, 0, 0.
+ * Weights are held to 2^-31 of themselves or 2^-40 (1 being the best token's)
+ * and added without rounding: the token is the one of the formulas in exact
+ * arithmetic unless u or top_p lies that near to a border.  Results repeat bit for
+ * bit, whatever else is in the batch.
+ * A row without a distribution (a NaN or +inf, or nothing above -inf, among its
+ * logits; another temperature; a NaN as u, top_p or min_p)
+ * gets token -1 and prob 0 and is reported as DV_ERR_INVALID_ARG with b; other
+ * rows are not affected.
+ * ws: dv_sample_workspace_size bytes (the error word), zero-filled once.
+ * Limits: B <= 65535, V <= 524288. */
+dv_status dv_sample(const void* logits, int B, int V, long long row_stride,
+                    dv_dtype dt, const float* u, const float* temperature,
+                    const int32_t* top_k, const float* top_p, const float* min_p,
+                    int32_t* token, float* prob, void* ws, size_t ws_bytes,
+                    cudaStream_t stream);
+
 /* ---------------------------------------------------- decoder-step helpers */
 
 /* y_b = LayerNorm(x_b) without affine terms (eps given), rounded to the
@@ -482,10 +521,11 @@ dv_status dv_layernorm(const float* x, int B, int d, float eps,
  * results).  Inside every entry point the later kernels start during the
  * earlier ones and read only data those do not write.  At level 0 (the
  * default) the first kernel of each call waits for everything before it
- * (those of dv_layernorm, dv_tree_attn and dv_beam_select may be started
+ * (those of dv_layernorm, dv_tree_attn, dv_beam_select, dv_q4_matvec and
+ * dv_sample, and of dv_q4_sparse_mlp for one DV_F32 row, may be started
  * earlier, at either level, and wait before they read or write anything).
- * At level 1, for batch 1, the first kernel of dv_sparse_attn and of
- * dv_sparse_mlp may also start while the kernel before the call is still
+ * At level 1, for batch 1, the first kernel of dv_sparse_attn, dv_sparse_mlp and
+ * dv_q4_sparse_mlp may also start while the kernel before the call is still
  * running, and reads before waiting for it: the head / neuron lists and
  * counts, pos, the valid flags and the weights.  Enable it only when the
  * kernel issued just before each such call (on the same stream) writes none
@@ -501,7 +541,7 @@ int dv_set_launch_overlap(int level);
 /* Bound of every device-side wait (no counterpart in the pages): the
  * one-launch MLP's wait for its up-projection CTAs, the tensor-core paths'
  * pipeline waits (dv_tree_attn's among them) and the waits for copies of the
- * streaming MLP and dv_beam_select give up after `ns` nanoseconds of the GPU's
+ * streaming MLP, dv_beam_select and dv_sample give up after `ns` nanoseconds of the GPU's
  * global timer, record DV_ERR_TIMEOUT in the workspace (read it with dv_check)
  * and unwind; the kernel still waits for its own tensor-core and copy work in
  * flight before it exits.  ns <= 0 restores the default of one second.

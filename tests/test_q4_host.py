@@ -119,3 +119,38 @@ def test_binding_refuses_tensors_of_other_sizes_and_types():
     _refused(INVALID, dv.dv_q4_quantize, torch.zeros(6, 200, dtype=f16), Q)
     _refused(INVALID, dv.dv_q4_matvec, y, Q, out, ws)
     _refused(INVALID, dv.dv_q4_sparse_mlp, y, Q, Q, idx, cnt, o, ws)
+
+
+def _sample(logits=FAKE, B=2, V=100, ld=100, dt=dv.DV_F16, u=FAKE, T=FAKE, k=FAKE, p=FAKE, min_p=FAKE, token=FAKE,
+            prob=FAKE, ws=FAKE, ws_bytes=256):
+    return dv.lib().dv_sample(_vp(logits), B, V, ld, dt, _vp(u), _vp(T), _vp(k), _vp(p), _vp(min_p), _vp(token),
+                              _vp(prob), _vp(ws), ws_bytes, _vp(0))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(logits=None), INVALID), (dict(u=None), INVALID), (dict(token=None), INVALID), (dict(logits=FAKE + 1), INVALID),
+    (dict(logits=FAKE + 2, dt=dv.DV_F32), INVALID), (dict(u=FAKE + 2), INVALID), (dict(T=FAKE + 1), INVALID),
+    (dict(k=FAKE + 2), INVALID), (dict(p=FAKE + 3), INVALID), (dict(min_p=FAKE + 2), INVALID), (dict(token=FAKE + 2), INVALID),
+    (dict(prob=FAKE + 2), INVALID), (dict(B=0), INVALID), (dict(B=65536), INVALID), (dict(V=0), INVALID),
+    (dict(V=524289, ld=600000), INVALID), (dict(ld=99), INVALID), (dict(dt=4), DTYPE), (dict(ws=None), WORKSPACE),
+    (dict(ws_bytes=255), WORKSPACE), (dict(ws=FAKE + 8), WORKSPACE),
+])
+def test_sample_refuses_bad_arguments(kw, status):
+    assert _sample(**kw) == status
+
+
+def test_sample_binding_refuses_other_tensors():
+    f32, i32 = torch.float32, torch.int32
+    logits, u, token, ws = torch.zeros(2, 10), torch.zeros(2), torch.zeros(2, dtype=i32), torch.zeros(256, dtype=torch.uint8)
+    _refused(INVALID, dv.dv_sample, torch.zeros(2, 20)[:, ::2], u, token, ws)
+    _refused(INVALID, dv.dv_sample, logits, u.double(), token, ws)
+    _refused(INVALID, dv.dv_sample, logits, torch.zeros(3), token, ws)
+    _refused(INVALID, dv.dv_sample, logits, u, token.long(), ws)
+    for name, t in (("temperature", torch.zeros(1)), ("top_k", torch.zeros(2)), ("top_p", torch.zeros(2, dtype=torch.float16)),
+                    ("min_p", torch.zeros(4)[::2]), ("prob", torch.zeros(2, dtype=torch.float64))):
+        _refused(INVALID, dv.dv_sample, logits, u, token, ws, **{name: t})
+    _refused(INVALID, dv.dv_sample, logits, u, token, ws)   # on the host
+    for bad in ((0, 10), (65536, 10), (1, 0), (1, 524289)):
+        with pytest.raises(dv.DvError):
+            dv.dv_sample_workspace_size(*bad)
+    assert dv.dv_sample_workspace_size(65535, 524288) >= 256
