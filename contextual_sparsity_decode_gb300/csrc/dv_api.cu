@@ -209,14 +209,12 @@ struct Q4Ws {
   int32_t* U_count;
   uint32_t* member;
   float* act;
-  uint16_t* pieces;
+  uint8_t* pieces;
 };
-size_t q4_piece_row(int d) { return (size_t)(d + 127) / 128 * 128; }
-// (room for the pieces of 32-bit vectors whatever the storage type: the size queries do not take it)
 Q4Ws carve_q4_mlp(Carver& c, int B, int d, int N, int cap) {
   Q4Ws w{};
-  w.pieces = c.take<uint16_t>((size_t)3 * B * q4_piece_row(d));
-  w.act = c.take<float>((size_t)B * (B == 1 ? cap : mlp_union_cap(B, N, cap)));
+  w.pieces = c.take<uint8_t>((size_t)6 * B * ((d + 127) / 128 * 128));
+  w.act = c.take<float>((size_t)B * (((B == 1 ? cap : mlp_union_cap(B, N, cap)) + 3) & ~3) + 16);
   if (B > 1) {
     w.U = c.take<int32_t>((size_t)N);
     w.U_count = c.take<int32_t>(4);
@@ -224,7 +222,7 @@ Q4Ws carve_q4_mlp(Carver& c, int B, int d, int N, int cap) {
   }
   return w;
 }
-uint16_t* carve_q4_matvec(Carver& c, int B, int d) { return c.take<uint16_t>((size_t)3 * B * q4_piece_row(d)); }
+uint8_t* carve_q4_matvec(Carver& c, int B, int d) { return c.take<uint8_t>((size_t)6 * B * ((d + 127) / 128 * 128)); }
 
 // ---- validation ---------------------------------------------------------------------
 
@@ -440,7 +438,7 @@ dv_status dv_sparse_mlp(const void* y, int B, int d, int N, const void* W1n, con
 // ---- matrices in 4 bits -----------------------------------------------------------------
 
 namespace {
-constexpr int kQ4MaxD = 65536, kQ4MaxN = 1 << 24;
+constexpr int kQ4MaxD = 32768, kQ4MaxN = 1 << 24;
 
 dv_status check_q4(const dv_q4* W) {
   if (!W || !W->q || !W->scale || !aligned16(W->q) || !aligned4(W->scale)) return DV_ERR_INVALID_ARG;

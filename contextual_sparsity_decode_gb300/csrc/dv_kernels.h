@@ -355,21 +355,22 @@ struct Q4Rows {
   int B, d, N;                          // vectors, their length, rows of the matrix
   const int32_t* list; const int32_t* count; int cap;  // listed rows, or null: all
   const uint32_t* member; int words;    // [B][words] whose list a row is in, or null
-  float* act;                           // listed: max(0, product), [B][cap]
+  float* act; int ld_act;               // listed: max(0, product), B rows ld_act apart (a multiple of 4)
   float* out; int accumulate;           // all rows: [B][N]
   WsHeader* hdr;
   int early;                            // list and weights are read before the wait
-  // set by the launcher: the vectors as columns of 16-bit values
-  const void* x; int cols, ldx, x_len;
-  int blocks, groups, kw;
+  const void* y;                        // [B][d]
+  int blocks, groups;                   // of a row
   size_t pitch;
+  // B > 2, set by the launcher: the vectors as columns of 16-bit values
+  const void* x; int cols, ldx, x_len, kw;
 };
 // Second kind: sums of listed rows.
 struct Q4Cols {
-  const uint8_t* q; const void* scale; int group;
+  const uint8_t* q; const void* scale; int group, dt;
   int B, d, N;
   const int32_t* list; const int32_t* count; int cap;
-  const float* act;                     // [B][cap]
+  const float* act; int ld_act;         // as the first kind writes them
   float* out; int accumulate;           // [B][d]
   int groups, split;
   size_t pitch;
@@ -387,9 +388,13 @@ struct Q4MlpLaunch {
   const int32_t* idx; int cap; const int32_t* count;
   float* out; int accumulate;
   int32_t* U; int32_t* U_count; uint32_t* member;  // B > 1
-  float* act;                           // [B][cap], B > 1: [B][mlp_union_cap]
+  float* act;                           // B rows of cap (B > 1: mlp_union_cap), rounded up to 4, and 16 more
   void* pieces;
 };
+// One and two vectors (k_q4_vec.cu).
+bool q4_vec_supported(int B, int d);
+cudaError_t launch_q4_vec_rows(const Q4Rows& a, dv_dtype dt, bool pdl, cudaStream_t stream);
+cudaError_t launch_q4_vec_cols(const Q4Cols& a, cudaStream_t stream);
 cudaError_t launch_q4_quantize(const void* W, int N, int d, dv_dtype dt, int group, void* q, void* scale, void* values,
                                int num_sms, cudaStream_t stream);
 cudaError_t launch_q4_matvec(const Q4MatvecLaunch& L, dv_dtype dt, cudaStream_t stream);

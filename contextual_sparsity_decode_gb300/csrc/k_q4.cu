@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) q4_rows_kernel(const Q4Rows a) {
       const int j = a.list[u];
       bool live = j >= 0 && j < a.N && !(u > 0 && a.list[u - 1] == j);
       if (live && a.member) live = bit_test(a.member + (size_t)b * a.words, j);
-      a.act[(size_t)b * a.cap + u] = live ? (sum > 0.f || sum != sum ? sum : 0.f) : 0.f;
+      a.act[(size_t)b * a.ld_act + u] = live ? (sum > 0.f || sum != sum ? sum : 0.f) : 0.f;
     } else {
       float* o = a.out + (size_t)b * a.N + u;
       *o = a.accumulate ? *o + sum : sum;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads) q4_cols_kernel(const Q4Cols a) {
           float v[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            v[i] = (kCols ? g < 3 * a.B : b < a.B) && e + i < m ? __ldcg(a.act + (size_t)b * a.cap + c0 + e + i) : 0.f;
+            v[i] = (kCols ? g < 3 * a.B : b < a.B) && e + i < m ? __ldcg(a.act + (size_t)b * a.ld_act + c0 + e + i) : 0.f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h == 1 && halves == 1) break;
@@ -519,9 +519,11 @@ cudaError_t run_rows_nt(const Q4Rows& a, bool pdl, cudaStream_t stream) {
 
 // The first product: y in its storage type, or as pieces made by a kernel before it.
 cudaError_t launch_rows(Q4Rows a, const void* y, void* pieces, dv_dtype dt, bool pdl, cudaStream_t stream) {
+  a.y = y;
   a.blocks = (a.d + 127) / 128;
   a.pitch = (size_t)a.blocks * kBlockBytes;
   a.groups = (a.d + a.group - 1) / a.group;
+  if (q4_vec_supported(a.B, a.d)) return launch_q4_vec_rows(a, dt, pdl, stream);
   a.kw = 8;
   if (dt == DV_F32) {
     const int ld = a.blocks * 128;
@@ -536,7 +538,7 @@ cudaError_t launch_rows(Q4Rows a, const void* y, void* pieces, dv_dtype dt, bool
       r.cols = 3 * r.B;
       r.x = static_cast<const __nv_bfloat16*>(pieces) + (size_t)3 * b0 * ld;
       if (r.out) r.out += (size_t)b0 * r.N;
-      if (r.act) r.act += (size_t)b0 * r.cap;
+      if (r.act) r.act += (size_t)b0 * r.ld_act;
       if (r.member) r.member += (size_t)b0 * r.words;
       const cudaError_t er = run_rows_nt<float, __nv_bfloat16>(r, true, stream);
       if (er != cudaSuccess) return er;
@@ -602,16 +604,19 @@ cudaError_t launch_q4_sparse_mlp(const Q4MlpLaunch& L, dv_dtype dt, WsHeader* hd
     a.list = L.U; a.count = L.U_count; a.cap = mlp_union_cap(L.B, L.N, L.cap);
     a.member = L.member; a.words = (L.N + 31) / 32;
   }
+  a.ld_act = (a.cap + 3) & ~3;
   // batch 1 under the overlap policy: everything but y is read before the wait
   a.early = launch_overlap() > 0 && L.B == 1 ? 1 : 0;
   cudaError_t e = launch_rows(a, L.y, L.pieces, dt, a.early != 0, stream);
   if (e != cudaSuccess) return e;
   Q4Cols c{};
   c.q = L.q2; c.scale = L.s2; c.group = L.group2; c.B = L.B; c.d = L.d; c.N = L.N;
-  c.list = a.list; c.count = a.count; c.cap = a.cap; c.act = L.act; c.out = L.out; c.accumulate = L.accumulate;
+  c.list = a.list; c.count = a.count; c.cap = a.cap; c.act = L.act; c.ld_act = a.ld_act;
+  c.out = L.out; c.accumulate = L.accumulate; c.dt = dt;
   const int blocks = (L.d + 127) / 128;
   c.pitch = (size_t)blocks * kBlockBytes;
   c.groups = (L.d + L.group2 - 1) / L.group2;
+  if (L.B <= 2) return launch_q4_vec_cols(c, stream);
   c.split = 8;
   switch (dt) {
     case DV_F32: return run_cols_nt<float>(c, stream);

@@ -1,0 +1,578 @@
+// Matrices in 4 bits (layout: k_q4.cu) with one or two vectors: products with
+// rows of the matrix, and sums of listed rows, on the integer dot product of four
+// bytes (dp4a).
+//
+// A word of eight codes is two registers of four bytes by a mask, and a shift and
+// a mask.  Vectors and coefficients enter in fixed point below the largest of their group
+// (of the CTA's share): four signed digits of base 256, 30 bits.  So every sum of
+// products of codes and digits is a whole number that 32 bits hold, the offset of
+// 8 comes off exactly, and what is rounded is the fixed point (2^-31 of the
+// largest) and the sums over groups, in fp32.
+//
+// Both kernels read every selected byte once.  Integer products run at 64
+// lanes a cycle and SM: four digits of one vector take 1 a weight where 47 weights
+// a cycle and SM come from memory; logic and permutations (64 a cycle too, on
+// another pipe) take 0.4 and 0.7.  (With m16n8k16 products of opened codes the 50257 x
+// 5120 product took 68 us, however its loads were arranged: 3.5 cycles an SM each.)
+
+#include <climits>
+
+#include "dv_kernels.h"
+
+namespace dv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kDigits = 4;
+constexpr uint32_t kMagic = 0x4b400000u;   // 1.5 2^23 as a float: a whole number below 2^22 added to it is one in float
+constexpr float kMagicF = 12582912.f;
+
+// Elements (0, 4, 1, 5) and (2, 6, 3, 7) of a word as bytes.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) { return w & 0x0f0f0f0fu; }
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) { return (w >> 4) & 0x0f0f0f0fu; }
+__device__ __forceinline__ int high_of(int e) { return (e >> 1) & 1; }
+__device__ __forceinline__ int byte_of(int e) { return (e & 1) * 2 + (e >> 2); }
+
+__device__ __forceinline__ uint32_t ld_stream4(const void* p) {
+  uint32_t r;
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
+template <typename S>
+__device__ __forceinline__ uint32_t ld_raw(const void* p) {
+  if constexpr (sizeof(S) == 4) {
+    uint32_t v;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+  } else {
+    uint16_t h;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(h) : "l"(p));
+    return h;
+  }
+}
+template <typename S> __device__ __forceinline__ float of_raw(uint32_t r);
+template <> __device__ __forceinline__ float of_raw<float>(uint32_t r) { return __uint_as_float(r); }
+template <> __device__ __forceinline__ float of_raw<__half>(uint32_t r) {
+  return __half2float(__ushort_as_half((unsigned short)r));
+}
+template <> __device__ __forceinline__ float of_raw<__nv_bfloat16>(uint32_t r) { return __uint_as_float(r << 16); }
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// The exponent that brings values of at most `top` into [-2^30, 2^30].
+__device__ __forceinline__ int fixed_shift(uint32_t top) { return min(30 - ((int)(top >> 23) - 126), 126); }
+__device__ __forceinline__ int fixed(float v, int shift) {   // (two steps: 2^shift alone may be out of range)
+  return __float2int_rn(v * pow2(shift / 2) * pow2(shift - shift / 2));
+}
+// Digits of base 256, the highest first, each in [-128, 127].
+__device__ __forceinline__ void digits_of(int v, int* d) {
+#pragma unroll
+  for (int p = kDigits - 1; p > 0; --p) {
+    d[p] = (int)(signed char)(v & 255);
+    v = (v - d[p]) >> 8;
+  }
+  d[0] = v;
+}
+
+// ---- products with rows -----------------------------------------------------------------
+
+// Vectors in shared memory: digits of the 32 elements of chunk (16 bytes of a row)
+// k in the order of the chunk's codes, [vector][digit][half of it][chunk] of 16 bytes, and
+// a group's unit times 2^-20.
+struct VecLayout {
+  int chunks;   // a multiple of 32
+  int groups;
+  __host__ __device__ VecLayout(int blocks, int group) : chunks((blocks * 4 + 31) & ~31), groups(chunks * 32 / group) {}
+  __host__ __device__ size_t bytes(int B) const { return (size_t)B * (chunks * (kDigits * 32) + groups * 4); }
+};
+
+template <typename S>
+__device__ __forceinline__ void stage_group(const S* y, int d, int group, int gi, const VecLayout& v, uint8_t* xs,
+                                            float* unit) {
+  const int lane = threadIdx.x & 31;
+  float x[4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = gi * group + i * 32 + lane;
+    x[i] = i * 32 < group && t < d ? Elem<S>::to_f(y[t]) : 0.f;
+    top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  const int shift = fixed_shift(top);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i * 32 >= group) break;
+    const int t = gi * group + i * 32 + lane;
+    int dig[kDigits];
+    digits_of(top < 0x7f800000u ? fixed(x[i], shift) : 0, dig);
+    const int r = t & 63, chunk = (t >> 7) * 4 + (r >> 4), half = (r >> 3) & 1, e = t & 7;
+    uint8_t* at = xs + ((size_t)half * v.chunks + chunk) * 16 + ((t >> 6) & 1) * 8 + high_of(e) * 4 + byte_of(e);
+#pragma unroll
+    for (int p = 0; p < kDigits; ++p) at[(size_t)p * 2 * v.chunks * 16] = (uint8_t)dig[p];
+  }
+  // (an infinity or a NaN: every product a NaN)
+  if (lane == 0) *unit = top < 0x7f800000u ? pow2(-(shift / 2)) * pow2(-(shift - shift / 2) - 20) : __int_as_float(0x7fc00000);
+}
+
+// A warp takes kRows rows at a time, a lane one chunk of every 32 of a row;
+// kAhead steps (of 32 chunks) of the rows are loaded ahead.  The lane's part
+// of the vectors stays in registers for the rows.
+template <typename S, int B, int kRows, int kAhead, bool kList, bool two>
+__global__ void __launch_bounds__(kThreads, 2) q4_vec_rows_kernel(const Q4Rows a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const VecLayout v(a.blocks, a.group);
+  float* units = reinterpret_cast<float*>(smem + (size_t)B * v.chunks * kDigits * 32);   // [B][groups]
+  // at level 1 of the launch policy the list, its count and the weights are read
+  // before the wait
+  if (!a.early) grid_dep_wait();
+  if (!a.early) grid_dep_launch();
+  const int n = kList ? max(0, min(*a.count, a.cap)) : a.N;
+  if (kList && blockIdx.x == 0 && tid == 0 && *a.count > a.cap) set_error(a.hdr, DV_ERR_CAPACITY, *a.count);
+  const int tiles = (n + kRows - 1) / kRows, stride = gridDim.x * kWarps;
+  const int steps = v.chunks >> 5, last = a.blocks * 4 - 1;
+
+  constexpr int kNone = INT_MIN;
+  int row[kRows];
+  const auto rows_of = [&](int t) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int u = t * kRows + k;
+      row[k] = u < n ? u : kNone;
+      if (kList && u < n) {
+        const int r = max(a.list[u], kNone + 1);
+        row[k] = u > 0 && a.list[u - 1] == r ? kNone : r;   // (an entry listed twice counts once)
+        if (row[k] != kNone && (row[k] < 0 || row[k] >= a.N)) {
+          if (lane == 0) set_error(a.hdr, DV_ERR_INDEX_RANGE, row[k]);
+          row[k] = kNone;
+        }
+      }
+    }
+  };
+  uint4 w[kAhead][kRows];
+  uint32_t sc[kAhead][kRows][two ? 2 : 1];
+  // (where there is no row or no chunk another is read and not used)
+  const auto fetch = [&](int j, int s) {
+    const int chunk = min(s * 32 + lane, last), gi = two ? chunk >> 2 << 1 : chunk >> 2;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const size_t r = max(row[k], 0);
+      w[j][k] = ld_stream(a.q + r * a.pitch + chunk * 16);
+      const uint8_t* sp = static_cast<const uint8_t*>(a.scale) + r * a.groups * sizeof(S);
+      sc[j][k][0] = ld_raw<S>(sp + gi * (int)sizeof(S));
+      if (two) sc[j][k][two] = ld_raw<S>(sp + min(gi + 1, a.groups - 1) * (int)sizeof(S));
+    }
+  };
+  int t = blockIdx.x * kWarps + wid;
+  if (t < tiles) {
+    rows_of(t);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (j < steps) fetch(j, j);
+  }
+  if (a.early) {
+    grid_dep_wait();
+    grid_dep_launch();
+  }
+  for (int i = wid; i < v.groups * B; i += kWarps) {
+    const int b = i / v.groups, gi = i - b * v.groups;
+    stage_group<S>(static_cast<const S*>(a.y) + (size_t)b * a.d, a.d, a.group, gi, v, smem + (size_t)b * v.chunks * kDigits * 32,
+                   units + i);
+  }
+  __syncthreads();
+  while (t < tiles) {
+    float acc[kRows][B];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+#pragma unroll
+      for (int b = 0; b < B; ++b) acc[k][b] = 0.f;
+    for (int s0 = 0; s0 < steps; s0 += kAhead) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int s = s0 + j;
+        if (s >= steps) break;
+        const int chunk = s * 32 + lane;
+        const int gi = two ? chunk >> 2 << 1 : chunk >> 2;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          // [digit][word][low, high], and what the offset adds
+          uint32_t x[kDigits][8];
+          int base[kDigits][two ? 2 : 1];
+#pragma unroll
+          for (int p = 0; p < kDigits; ++p) {
+            const uint4* from = reinterpret_cast<const uint4*>(smem) + ((size_t)(b * kDigits + p) * 2) * v.chunks + chunk;
+            const uint4 lo = from[0], hi = from[v.chunks];
+            x[p][0] = lo.x; x[p][1] = lo.y; x[p][2] = lo.z; x[p][3] = lo.w;   // words 0 and 1
+            x[p][4] = hi.x; x[p][5] = hi.y; x[p][6] = hi.z; x[p][7] = hi.w;   // words 2 and 3
+            base[p][0] = base[p][two ? 1 : 0] = (int)kMagic;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              int& at = base[p][two ? (i >> 1) & 1 : 0];
+              at = __dp4a((int)x[p][i], (int)0xf8f8f8f8u, at);   // -8 each
+            }
+          }
+          const float u0 = units[b * v.groups + gi], u1 = two ? units[b * v.groups + gi + 1] : 0.f;
+#pragma unroll
+          for (int k = 0; k < kRows; ++k) {
+            const uint32_t ww[4] = {w[j][k].x, w[j][k].y, w[j][k].z, w[j][k].w};
+            int sum[kDigits][two ? 2 : 1];
+#pragma unroll
+            for (int p = 0; p < kDigits; ++p)
+#pragma unroll
+              for (int h = 0; h < (two ? 2 : 1); ++h) sum[p][h] = base[p][h];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {   // word i is of half i % 2
+              const int c0 = (int)low_codes(ww[i]), c1 = (int)high_codes(ww[i]), h = two ? i & 1 : 0;
+#pragma unroll
+              for (int p = 0; p < kDigits; ++p)
+                sum[p][h] = __dp4a(c1, (int)x[p][2 * i + 1], __dp4a(c0, (int)x[p][2 * i], sum[p][h]));
+            }
+#pragma unroll
+            for (int h = 0; h < (two ? 2 : 1); ++h) {
+              float f = __int_as_float(sum[0][h]) - kMagicF;   // exact, as is the next line's sum
+#pragma unroll
+              for (int p = 1; p < kDigits; ++p) f = fmaf(f, 256.f, __int_as_float(sum[p][h]) - kMagicF);
+              acc[k][b] = fmaf(f * (h ? u1 : u0), of_raw<S>(sc[j][k][h]) * 1048576.f, acc[k][b]);
+            }
+          }
+        }
+        if (s + kAhead < steps) fetch(j, s + kAhead);
+      }
+    }
+    int mine[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) mine[k] = row[k];
+    const int u0 = t * kRows;
+    t += stride;
+    if (t < tiles) {
+      rows_of(t);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (j < steps) fetch(j, j);
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const float sum = warp_sum(acc[k][b]);
+        if (lane != 0 || u0 + k >= n) continue;
+        if (kList) {
+          bool live = mine[k] != kNone;
+          if (live && a.member) live = bit_test(a.member + (size_t)b * a.words, mine[k]);
+          a.act[(size_t)b * a.ld_act + u0 + k] = live ? (sum > 0.f || sum != sum ? sum : 0.f) : 0.f;
+        } else {
+          float* o = a.out + (size_t)b * a.N + u0 + k;
+          *o = a.accumulate ? *o + sum : sum;
+        }
+      }
+  }
+}
+
+// ---- sums of listed rows ------------------------------------------------------------------
+
+// out[b][t] (+)= sum_u act[b][u] s[j_u][group of t] (code[j_u][t] - 8).  A CTA (of a
+// cluster of `split`) owns 256 elements, two blocks, and a share of the list; a lane
+// eight elements, a word; a step is four listed rows, whose codes of an element a 4 x
+// 4 transpose of bytes puts side by side.
+constexpr int kListed = 2048;              // list entries staged at a time
+constexpr int kColThreads = 512;
+constexpr int kColWarps = kColThreads / 32;
+constexpr int kColAhead = 6;               // steps loaded ahead
+
+__device__ __forceinline__ float ld_scale_dt(const void* s, size_t i, int dt) {
+  return dt == DV_F32 ? __ldg(static_cast<const float*>(s) + i)
+         : dt == DV_F16 ? __half2float(__ldg(static_cast<const __half*>(s) + i))
+                        : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(s) + i));
+}
+
+template <int B, bool two>
+__global__ void __launch_bounds__(kColThreads, 1) q4_vec_cols_kernel(const Q4Cols a) {
+  constexpr int kSets = two ? 4 : 2;        // groups among the CTA's elements
+  // [step][vector][set][digit] of four bytes, one a row; the warps' sums at the end
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int id[kListed];
+  __shared__ int digit_sum[B][kSets][kDigits];
+  __shared__ uint32_t top[B][kSets];
+  __shared__ float sums[B * 256];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int slab = blockIdx.x / a.split, rank = blockIdx.x % a.split;
+  const int blocks = (a.d + 127) >> 7;
+  const int n = max(0, min(*a.count, a.cap));
+  const int share = ((n + a.split - 1) / a.split + 3) & ~3;
+  const int lo = min(n, rank * share), hi = min(n, lo + share);
+  const int word = lane & 15, set = two ? (lane >> 4) * 2 + (word & 1) : lane >> 4;
+  const uint8_t* q = a.q + (size_t)min(2 * slab + (lane >> 4), blocks - 1) * kQ4BlockBytes + 4 * word;
+  if (tid < B * kSets * kDigits) (&digit_sum[0][0][0])[tid] = 0;
+  if (tid < B * kSets) (&top[0][0])[tid] = 0;
+
+  uint32_t w[kColAhead][4];
+  const auto stage_ids = [&](int c0, int m) {
+    for (int e = tid; e < ((m + 3) & ~3); e += kColThreads) {
+      const int j = e < m ? a.list[c0 + e] : 0;
+      // (an entry outside is reported, and has activation 0, from the first product on: row 0 is read)
+      id[e] = j >= 0 && j < a.N ? j : 0;
+    }
+  };
+  const auto fetch = [&](int k, int s) {   // rows of the warp's step s
+    const int4 j = *reinterpret_cast<const int4*>(&id[(s * kColWarps + wid) * 4]);
+    w[k][0] = ld_stream4(q + (size_t)j.x * a.pitch);
+    w[k][1] = ld_stream4(q + (size_t)j.y * a.pitch);
+    w[k][2] = ld_stream4(q + (size_t)j.z * a.pitch);
+    w[k][3] = ld_stream4(q + (size_t)j.w * a.pitch);
+  };
+  const auto steps_of = [&](int m) { return ((m + 3) / 4 - wid + kColWarps - 1) / kColWarps; };
+  const auto group_of = [&](int s) {
+    return min(two ? 4 * slab + s : 2 * slab + s, a.groups - 1);
+  };
+  const auto coefficient = [&](int b, int u, int j, int s) {   // (0 adds nothing, whatever the row holds)
+    const float x = __ldcg(a.act + (size_t)b * a.ld_act + u);
+    return x == 0.f ? 0.f : x * ld_scale_dt(a.scale, (size_t)j * a.groups + group_of(s), a.dt);
+  };
+
+  const int m0 = min(kListed, hi - lo);
+  stage_ids(lo, m0);
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kColAhead; ++k)
+    if (k < steps_of(m0)) fetch(k, k);
+  grid_dep_wait();   // the activations
+  grid_dep_launch();
+  // the largest coefficient of every vector and group: the unit of the fixed point
+  {
+    uint32_t most[B][kSets] = {};
+    for (int u = lo + tid; u < hi; u += kColThreads) {
+      const int l = u - lo < m0 ? id[u - lo] : a.list[u];
+      const int j = l >= 0 && l < a.N ? l : 0;
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) most[b][s] = max(most[b][s], __float_as_uint(fabsf(coefficient(b, u, j, s))));
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int s = 0; s < kSets; ++s) {
+        const uint32_t most_of = __reduce_max_sync(0xffffffffu, most[b][s]);
+        if (lane == 0 && most_of) atomicMax(&top[b][s], most_of);
+      }
+  }
+  __syncthreads();
+
+  int acc[B][8][kDigits];   // elements (0, 2), (4, 6), (1, 3), (5, 7) of the lane's word
+#pragma unroll
+  for (int b = 0; b < B; ++b)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int p = 0; p < kDigits; ++p) acc[b][i][p] = 0;
+  uint32_t* digits = reinterpret_cast<uint32_t*>(smem);
+  for (int c0 = lo; c0 < hi; c0 += kListed) {
+    const int m = min(kListed, hi - c0), padded = (m + 3) & ~3;
+    if (c0 > lo) {
+      __syncthreads();
+      stage_ids(c0, m);
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kColAhead; ++k)
+        if (k < steps_of(m)) fetch(k, k);
+    }
+    {
+      int mine[B][kSets][kDigits] = {};
+      for (int e = tid; e < padded; e += kColThreads)
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+          for (int s = 0; s < kSets; ++s) {
+            int dig[kDigits];
+            const bool fine = e < m && top[b][s] < 0x7f800000u;
+            digits_of(fine ? fixed(coefficient(b, c0 + e, id[e], s), fixed_shift(top[b][s])) : 0, dig);
+#pragma unroll
+            for (int p = 0; p < kDigits; ++p) {
+              reinterpret_cast<uint8_t*>(digits + (((size_t)(e >> 2) * B + b) * kSets + s) * kDigits + p)[e & 3] =
+                  (uint8_t)dig[p];
+              mine[b][s][p] += dig[p];
+            }
+          }
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int s = 0; s < kSets; ++s)
+#pragma unroll
+          for (int p = 0; p < kDigits; ++p) {
+            const int sum = __reduce_add_sync(0xffffffffu, mine[b][s][p]);
+            if (lane == 0 && sum) atomicAdd(&digit_sum[b][s][p], sum);
+          }
+    }
+    __syncthreads();
+    const int steps = steps_of(m);
+    for (int s0 = 0; s0 < steps; s0 += kColAhead) {
+#pragma unroll
+      for (int k = 0; k < kColAhead; ++k) {
+        if (s0 + k >= steps) break;
+        const int step = (s0 + k) * kColWarps + wid;
+        const uint32_t t0 = __byte_perm(w[k][0], w[k][1], 0x5140), t1 = __byte_perm(w[k][2], w[k][3], 0x5140);
+        const uint32_t t2 = __byte_perm(w[k][0], w[k][1], 0x7362), t3 = __byte_perm(w[k][2], w[k][3], 0x7362);
+        const uint32_t r[4] = {__byte_perm(t0, t1, 0x5410), __byte_perm(t0, t1, 0x7632), __byte_perm(t2, t3, 0x5410),
+                               __byte_perm(t2, t3, 0x7632)};
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const uint4 x = *reinterpret_cast<const uint4*>(digits + (((size_t)step * B + b) * kSets + set) * kDigits);
+          const uint32_t xx[kDigits] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int p = 0; p < kDigits; ++p) {
+              acc[b][2 * i][p] = __dp4a((int)low_codes(r[i]), (int)xx[p], acc[b][2 * i][p]);
+              acc[b][2 * i + 1][p] = __dp4a((int)high_codes(r[i]), (int)xx[p], acc[b][2 * i + 1][p]);
+            }
+        }
+        if (s0 + k + kColAhead < steps) fetch(k, s0 + k + kColAhead);
+      }
+    }
+  }
+  __syncthreads();
+  // the warps' whole numbers, in the digits' place, [warp][element]: their order does not matter
+  long long* red = reinterpret_cast<long long*>(smem);
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    if (b > 0) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // elements of register i: 0 2 4 6 1 3 5 7
+      const int e = (i & 3) * 2 + (i >> 2);
+      long long whole = 0;
+#pragma unroll
+      for (int p = 0; p < kDigits; ++p) whole = whole * 256 + acc[b][i][p];
+      red[wid * 256 + (lane >> 4) * 128 + 64 * (word & 1) + 8 * (word >> 1) + e] = whole;
+    }
+    __syncthreads();
+    if (tid < 256) {
+      const int s = two ? tid >> 6 : tid >> 7;
+      long long whole = 0, offset = 0;
+#pragma unroll
+      for (int k = 0; k < kColWarps; ++k) whole += red[k * 256 + tid];
+#pragma unroll
+      for (int p = 0; p < kDigits; ++p) offset = offset * 256 + digit_sum[b][s][p];
+      const int shift = fixed_shift(top[b][s]);
+      const float v = __ll2float_rn(whole - 8 * offset) * pow2(-(shift / 2)) * pow2(-(shift - shift / 2));
+      sums[b * 256 + tid] = top[b][s] < 0x7f800000u ? v : __int_as_float(0x7fc00000);
+    }
+  }
+  __syncthreads();
+  if (a.split > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  const int mine = (256 + a.split - 1) / a.split;   // elements that this CTA joins and writes
+  for (int i = tid; i < mine * B; i += kColThreads) {
+    const int b = i / mine, t = rank * mine + i - b * mine;
+    if (t >= 256 || slab * 256 + t >= a.d) continue;
+    float sum = 0.f;
+    for (int r = 0; r < a.split; ++r) sum += a.split > 1 ? ld_dsmem_f32(sums + b * 256 + t, r) : sums[b * 256 + t];
+    float* o = a.out + (size_t)b * a.d + slab * 256 + t;
+    *o = a.accumulate ? *o + sum : sum;
+  }
+  if (a.split > 1) {   // no CTA leaves while its shared memory is read
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+// ---- launches ------------------------------------------------------------------------------
+
+template <typename S, int B, int kRows, int kAhead, bool kList, bool two>
+cudaError_t run_rows(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
+  const size_t smem = VecLayout(a.blocks, a.group).bytes(B);
+  static PerDevice attr;   // function attributes are per device
+  const cudaError_t ea = (cudaError_t)attr.get(current_device(), [] {
+    return (int)cudaFuncSetAttribute(q4_vec_rows_kernel<S, B, kRows, kAhead, kList, two>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  });
+  if (ea != cudaSuccess) return ea;
+  const long long tiles = ((kList ? a.cap : a.N) + kRows - 1) / kRows, ctas = (tiles + kWarps - 1) / kWarps;
+  const long long most = 2LL * num_sms;
+  return launch_k(q4_vec_rows_kernel<S, B, kRows, kAhead, kList, two>, dim3((unsigned)(ctas < most ? ctas : most)),
+                  dim3(kThreads), smem, stream, pdl, 1, a);
+}
+// Rows at a time: four, which read a vector's digits once; one where that would leave
+// most of the GPU's warps (16 an SM) without rows.
+template <typename S, int B, bool kList, bool two>
+cudaError_t run_rows_shape(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
+  const int rows = kList ? a.cap : a.N;
+  return rows < 4 * num_sms * 16 ? run_rows<S, B, 1, 5, kList, two>(a, pdl, num_sms, stream)
+                                 : run_rows<S, B, 4, 2, kList, two>(a, pdl, num_sms, stream);
+}
+template <typename S>
+cudaError_t run_rows_of(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
+  const bool two = a.group == 64;
+  if (a.B == 1) {
+    if (a.list) return two ? run_rows_shape<S, 1, true, true>(a, pdl, num_sms, stream) : run_rows_shape<S, 1, true, false>(a, pdl, num_sms, stream);
+    return two ? run_rows_shape<S, 1, false, true>(a, pdl, num_sms, stream) : run_rows_shape<S, 1, false, false>(a, pdl, num_sms, stream);
+  }
+  if (a.list) return two ? run_rows_shape<S, 2, true, true>(a, pdl, num_sms, stream) : run_rows_shape<S, 2, true, false>(a, pdl, num_sms, stream);
+  return two ? run_rows_shape<S, 2, false, true>(a, pdl, num_sms, stream) : run_rows_shape<S, 2, false, false>(a, pdl, num_sms, stream);
+}
+
+// Clusters of `split` CTAs that run at once (a property of the device).
+template <int B, bool two>
+int clusters_at_once(int split, size_t smem) {
+  static PerDevice known[9];
+  return known[split].get(current_device(), [&] {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split);
+    cfg.blockDim = dim3(kColThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, q4_vec_cols_kernel<B, two>, &cfg) != cudaSuccess) n = 0;
+    (void)cudaGetLastError();
+    return n;
+  });
+}
+
+template <int B, bool two>
+cudaError_t run_cols(Q4Cols a, cudaStream_t stream) {
+  constexpr size_t digits = (size_t)kListed * B * (two ? 4 : 2) * kDigits, fold = (size_t)kColWarps * 256 * 8;
+  constexpr size_t smem = digits > fold ? digits : fold;
+  static PerDevice attr;   // function attributes are per device
+  const cudaError_t ea = (cudaError_t)attr.get(current_device(), [] {
+    return (int)cudaFuncSetAttribute(q4_vec_cols_kernel<B, two>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (ea != cudaSuccess) return ea;
+  // the largest clusters that still all run at once, with a step of four rows a warp at least
+  const int slabs = (a.d + 255) / 256;
+  a.split = 8;
+  while (a.split > 1 && (clusters_at_once<B, two>(a.split, smem) < slabs || (a.split - 1) * 4 * kColWarps >= a.cap))
+    --a.split;
+  return launch_k(q4_vec_cols_kernel<B, two>, dim3(slabs * a.split), dim3(kColThreads), smem, stream, true, a.split, a);
+}
+
+}  // namespace
+
+bool q4_vec_supported(int B, int d) {
+  return B <= 2 && VecLayout((d + 127) / 128, 64).bytes(B) <= 227 * 1024;
+}
+
+cudaError_t launch_q4_vec_rows(const Q4Rows& a, dv_dtype dt, bool pdl, cudaStream_t stream) {
+  const int num_sms = num_sms_current();
+  switch (dt) {
+    case DV_F32: return run_rows_of<float>(a, pdl, num_sms, stream);
+    case DV_F16: return run_rows_of<__half>(a, pdl, num_sms, stream);
+    case DV_BF16: return run_rows_of<__nv_bfloat16>(a, pdl, num_sms, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_q4_vec_cols(const Q4Cols& a, cudaStream_t stream) {
+  if (a.B == 1) return a.group == 64 ? run_cols<1, true>(a, stream) : run_cols<1, false>(a, stream);
+  return a.group == 64 ? run_cols<2, true>(a, stream) : run_cols<2, false>(a, stream);
+}
+
+}  // namespace dv

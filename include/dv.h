@@ -237,7 +237,7 @@ dv_status dv_sparse_mlp(const void* y, int B, int d, int N,
  * (8 where the scale is 0).  A group with a NaN or an infinity gets a NaN as its
  * scale and codes 8: its products are NaNs.  q and scale as in dv_q4; values
  * [N][d] (storage type), unless NULL: what the codes stand for, rounded once.
- * Limits: N <= 16777216, d <= 65536; other groups return DV_ERR_UNSUPPORTED. */
+ * Limits: N <= 16777216, d <= 32768; other groups return DV_ERR_UNSUPPORTED. */
 dv_status dv_q4_quantize(const void* W, int N, int d, dv_dtype dt, int group,
                          void* q, void* scale, void* values,
                          cudaStream_t stream);
@@ -253,7 +253,7 @@ dv_status dv_q4_matvec_workspace_size(int B, int d, int N, size_t* bytes);
  * sums are fp32; results repeat bit for bit.  Like dv_layernorm's, its first
  * kernel may be started before the kernel ahead of the call has ended and waits
  * for it before it reads or writes anything.
- * Limits: B <= 32, N <= 16777216, d <= 65536. */
+ * Limits: B <= 32, N <= 16777216, d <= 32768. */
 dv_status dv_q4_matvec(const void* y, int B, int d, int N, const dv_q4* W,
                        dv_dtype dt, float* out, int accumulate,
                        void* ws, size_t ws_bytes, cudaStream_t stream);
@@ -270,7 +270,7 @@ dv_status dv_q4_sparse_mlp_workspace_size(int B, int d, int N, int cap,
  * dv_set_launch_overlap as for dv_sparse_mlp (16-bit storage).
  * Device errors: DV_ERR_INDEX_RANGE (an entry outside [0, N) is skipped),
  * DV_ERR_CAPACITY (a count above cap is cut off).
- * Limits: B <= 32, N <= 65536, d <= 65536. */
+ * Limits: B <= 32, N <= 65536, d <= 32768. */
 dv_status dv_q4_sparse_mlp(const void* y, int B, int d, int N, const dv_q4* W1,
                            const dv_q4* W2, const int32_t* idx, int cap,
                            const int32_t* count, dv_dtype dt, float* out,

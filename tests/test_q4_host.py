@@ -28,7 +28,7 @@ def _quantize(W=FAKE, N=4, d=128, dt=dv.DV_F16, group=128, q=FAKE, scale=FAKE, v
     (dict(W=None), INVALID), (dict(W=FAKE + 8), INVALID), (dict(q=None), INVALID), (dict(q=FAKE + 8), INVALID),
     (dict(scale=None), INVALID), (dict(scale=FAKE + 2), INVALID), (dict(values=FAKE + 4), INVALID), (dict(N=0), INVALID),
     (dict(N=(1 << 24) + 1), INVALID), (dict(d=0), INVALID), (dict(d=100), INVALID), (dict(d=102, dt=dv.DV_F32), INVALID),
-    (dict(d=65544), INVALID), (dict(dt=3), DTYPE), (dict(group=32), UNSUPPORTED), (dict(group=0), UNSUPPORTED),
+    (dict(d=32776), INVALID), (dict(dt=3), DTYPE), (dict(group=32), UNSUPPORTED), (dict(group=0), UNSUPPORTED),
 ])
 def test_quantize_refuses_bad_arguments(kw, status):
     assert _quantize(**kw) == status
@@ -41,7 +41,7 @@ def _matvec(y=FAKE, B=2, d=128, N=10, W=None, dt=dv.DV_BF16, out=FAKE, ws=FAKE, 
 @pytest.mark.parametrize("kw,status", [
     (dict(y=None), INVALID), (dict(y=FAKE + 8), INVALID), (dict(out=None), INVALID), (dict(out=FAKE + 2), INVALID),
     (dict(B=0), INVALID), (dict(B=33), INVALID), (dict(d=0), INVALID), (dict(d=12), INVALID),
-    (dict(d=6, dt=dv.DV_F32), INVALID), (dict(d=65544), INVALID), (dict(N=0), INVALID), (dict(N=(1 << 24) + 1), INVALID),
+    (dict(d=6, dt=dv.DV_F32), INVALID), (dict(d=32776), INVALID), (dict(N=0), INVALID), (dict(N=(1 << 24) + 1), INVALID),
     (dict(W=_q4(q=None)), INVALID), (dict(W=_q4(scale=None)), INVALID), (dict(W=_q4(q=FAKE + 4)), INVALID),
     (dict(W=_q4(group=96)), UNSUPPORTED), (dict(dt=-1), DTYPE), (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 4), WORKSPACE),
     (dict(ws_bytes=255), WORKSPACE),
@@ -73,7 +73,7 @@ def test_workspace_queries():
     assert 0 < a < b
     a, b = dv.dv_q4_sparse_mlp_workspace_size(1, 5120, 20480, 1024), dv.dv_q4_sparse_mlp_workspace_size(4, 5120, 20480, 1024)
     assert 0 < a < b
-    for bad in ((0, 64, 10), (33, 64, 10), (1, 0, 10), (1, 65537, 10), (1, 64, 0)):
+    for bad in ((0, 64, 10), (33, 64, 10), (1, 0, 10), (1, 32769, 10), (1, 64, 0)):
         with pytest.raises(dv.DvError) as e:
             dv.dv_q4_matvec_workspace_size(*bad)
         assert e.value.status == INVALID
