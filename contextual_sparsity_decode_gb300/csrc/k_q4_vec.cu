@@ -78,13 +78,16 @@ __device__ __forceinline__ void digits_of(int v, int* d) {
 // ---- products with rows -----------------------------------------------------------------
 
 // Vectors in shared memory: digits of the 32 elements of chunk (16 bytes of a row)
-// k in the order of the chunk's codes, [vector][digit][half of it][chunk] of 16 bytes, and
-// a group's unit times 2^-20.
+// k in the order of the chunk's codes, [vector][digit][half of it][chunk] of 16 bytes; -8
+// times their sums, of either half of the block, [vector][chunk][half][digit]; and a
+// group's unit times 2^-20, [vector][group].
 struct VecLayout {
   int chunks;   // a multiple of 32
   int groups;
   __host__ __device__ VecLayout(int blocks, int group) : chunks((blocks * 4 + 31) & ~31), groups(chunks * 32 / group) {}
-  __host__ __device__ size_t bytes(int B) const { return (size_t)B * (chunks * (kDigits * 32) + groups * 4); }
+  __host__ __device__ size_t digit_bytes() const { return (size_t)chunks * (kDigits * 32); }
+  __host__ __device__ size_t offset_bytes() const { return (size_t)chunks * (kDigits * 8); }
+  __host__ __device__ size_t bytes(int B) const { return B * (digit_bytes() + offset_bytes() + groups * 4); }
 };
 
 template <typename S>
@@ -116,15 +119,15 @@ __device__ __forceinline__ void stage_group(const S* y, int d, int group, int gi
   if (lane == 0) *unit = top < 0x7f800000u ? pow2(-(shift / 2)) * pow2(-(shift - shift / 2) - 20) : __int_as_float(0x7fc00000);
 }
 
-// A warp takes kRows rows at a time, a lane one chunk of every 32 of a row;
-// kAhead steps (of 32 chunks) of the rows are loaded ahead.  The lane's part
-// of the vectors stays in registers for the rows.
+// A warp takes kRows rows at a time, a lane one chunk of every 32 of a row; the next
+// kAhead steps (of 32 chunks) of the rows are on their way while one is multiplied.
 template <typename S, int B, int kRows, int kAhead, bool kList, bool two>
 __global__ void __launch_bounds__(kThreads, 2) q4_vec_rows_kernel(const Q4Rows a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const VecLayout v(a.blocks, a.group);
-  float* units = reinterpret_cast<float*>(smem + (size_t)B * v.chunks * kDigits * 32);   // [B][groups]
+  const uint8_t* offsets = smem + B * v.digit_bytes();
+  float* units = reinterpret_cast<float*>(smem + B * (v.digit_bytes() + v.offset_bytes()));
   // at level 1 of the launch policy the list, its count and the weights are read
   // before the wait
   if (!a.early) grid_dep_wait();
@@ -136,6 +139,8 @@ __global__ void __launch_bounds__(kThreads, 2) q4_vec_rows_kernel(const Q4Rows a
 
   constexpr int kNone = INT_MIN;
   int row[kRows];
+  const uint8_t* q[kRows];
+  const uint8_t* sp[kRows];
   const auto rows_of = [&](int t) {
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
@@ -149,20 +154,23 @@ __global__ void __launch_bounds__(kThreads, 2) q4_vec_rows_kernel(const Q4Rows a
           row[k] = kNone;
         }
       }
+      const size_t r = max(row[k], 0);
+      q[k] = a.q + r * a.pitch;
+      sp[k] = static_cast<const uint8_t*>(a.scale) + r * a.groups * sizeof(S);
     }
   };
   uint4 w[kAhead][kRows];
   uint32_t sc[kAhead][kRows][two ? 2 : 1];
-  // (where there is no row or no chunk another is read and not used)
+  // (where there is no row or no chunk another is read and not used: a load under a condition
+  // is waited for at once)
   const auto fetch = [&](int j, int s) {
     const int chunk = min(s * 32 + lane, last), gi = two ? chunk >> 2 << 1 : chunk >> 2;
+    const int g1 = min(gi + 1, a.groups - 1);
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-      const size_t r = max(row[k], 0);
-      w[j][k] = ld_stream(a.q + r * a.pitch + chunk * 16);
-      const uint8_t* sp = static_cast<const uint8_t*>(a.scale) + r * a.groups * sizeof(S);
-      sc[j][k][0] = ld_raw<S>(sp + gi * (int)sizeof(S));
-      if (two) sc[j][k][two] = ld_raw<S>(sp + min(gi + 1, a.groups - 1) * (int)sizeof(S));
+      w[j][k] = ld_stream(q[k] + chunk * 16);
+      sc[j][k][0] = ld_raw<S>(sp[k] + gi * (int)sizeof(S));
+      if (two) sc[j][k][two] = ld_raw<S>(sp[k] + g1 * (int)sizeof(S));
     }
   };
   int t = blockIdx.x * kWarps + wid;
@@ -178,8 +186,20 @@ __global__ void __launch_bounds__(kThreads, 2) q4_vec_rows_kernel(const Q4Rows a
   }
   for (int i = wid; i < v.groups * B; i += kWarps) {
     const int b = i / v.groups, gi = i - b * v.groups;
-    stage_group<S>(static_cast<const S*>(a.y) + (size_t)b * a.d, a.d, a.group, gi, v, smem + (size_t)b * v.chunks * kDigits * 32,
-                   units + i);
+    stage_group<S>(static_cast<const S*>(a.y) + (size_t)b * a.d, a.d, a.group, gi, v, smem + b * v.digit_bytes(), units + i);
+  }
+  __syncthreads();
+  for (int i = tid; i < B * v.chunks * 2 * kDigits; i += kThreads) {
+    // -8 times the sum of one digit over one half of a chunk, with kMagic
+    const int p = i % kDigits, h = i / kDigits & 1, c = i / (2 * kDigits), b = c / v.chunks;
+    const uint8_t* from = smem + b * v.digit_bytes() + ((size_t)p * 2 * v.chunks + (c - b * v.chunks)) * 16 + h * 8;
+    int sum = (int)kMagic;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint2 x = *reinterpret_cast<const uint2*>(from + (size_t)k * v.chunks * 16);
+      sum = __dp4a((int)x.x, (int)0xf8f8f8f8u, __dp4a((int)x.y, (int)0xf8f8f8f8u, sum));
+    }
+    reinterpret_cast<int*>(smem + B * v.digit_bytes())[i] = sum;
   }
   __syncthreads();
   while (t < tiles) {
@@ -188,64 +208,69 @@ __global__ void __launch_bounds__(kThreads, 2) q4_vec_rows_kernel(const Q4Rows a
     for (int k = 0; k < kRows; ++k)
 #pragma unroll
       for (int b = 0; b < B; ++b) acc[k][b] = 0.f;
-    for (int s0 = 0; s0 < steps; s0 += kAhead) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int s = s0 + j;
-        if (s >= steps) break;
-        const int chunk = s * 32 + lane;
-        const int gi = two ? chunk >> 2 << 1 : chunk >> 2;
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-          // [digit][word][low, high], and what the offset adds
-          uint32_t x[kDigits][8];
-          int base[kDigits][two ? 2 : 1];
-#pragma unroll
-          for (int p = 0; p < kDigits; ++p) {
-            const uint4* from = reinterpret_cast<const uint4*>(smem) + ((size_t)(b * kDigits + p) * 2) * v.chunks + chunk;
-            const uint4 lo = from[0], hi = from[v.chunks];
-            x[p][0] = lo.x; x[p][1] = lo.y; x[p][2] = lo.z; x[p][3] = lo.w;   // words 0 and 1
-            x[p][4] = hi.x; x[p][5] = hi.y; x[p][6] = hi.z; x[p][7] = hi.w;   // words 2 and 3
-            base[p][0] = base[p][two ? 1 : 0] = (int)kMagic;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              int& at = base[p][two ? (i >> 1) & 1 : 0];
-              at = __dp4a((int)x[p][i], (int)0xf8f8f8f8u, at);   // -8 each
-            }
-          }
-          const float u0 = units[b * v.groups + gi], u1 = two ? units[b * v.groups + gi + 1] : 0.f;
-#pragma unroll
-          for (int k = 0; k < kRows; ++k) {
-            const uint32_t ww[4] = {w[j][k].x, w[j][k].y, w[j][k].z, w[j][k].w};
-            int sum[kDigits][two ? 2 : 1];
-#pragma unroll
-            for (int p = 0; p < kDigits; ++p)
-#pragma unroll
-              for (int h = 0; h < (two ? 2 : 1); ++h) sum[p][h] = base[p][h];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {   // word i is of half i % 2
-              const int c0 = (int)low_codes(ww[i]), c1 = (int)high_codes(ww[i]), h = two ? i & 1 : 0;
-#pragma unroll
-              for (int p = 0; p < kDigits; ++p)
-                sum[p][h] = __dp4a(c1, (int)x[p][2 * i + 1], __dp4a(c0, (int)x[p][2 * i], sum[p][h]));
-            }
-#pragma unroll
-            for (int h = 0; h < (two ? 2 : 1); ++h) {
-              float f = __int_as_float(sum[0][h]) - kMagicF;   // exact, as is the next line's sum
-#pragma unroll
-              for (int p = 1; p < kDigits; ++p) f = fmaf(f, 256.f, __int_as_float(sum[p][h]) - kMagicF);
-              acc[k][b] = fmaf(f * (h ? u1 : u0), of_raw<S>(sc[j][k][h]) * 1048576.f, acc[k][b]);
-            }
-          }
-        }
-        if (s + kAhead < steps) fetch(j, s + kAhead);
-      }
-    }
     int mine[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) mine[k] = row[k];
     const int u0 = t * kRows;
     t += stride;
+    for (int s0 = 0; s0 < steps; s0 += kAhead) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int s = s0 + j;
+        if (s >= steps) break;
+        const int chunk = s * 32 + lane, gi = two ? chunk >> 2 << 1 : chunk >> 2;
+        uint32_t code[kRows][8];   // [word][low, high]
+        float scale[kRows][two ? 2 : 1];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const uint32_t ww[4] = {w[j][k].x, w[j][k].y, w[j][k].z, w[j][k].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            code[k][2 * i] = low_codes(ww[i]);
+            code[k][2 * i + 1] = high_codes(ww[i]);
+          }
+#pragma unroll
+          for (int h = 0; h < (two ? 2 : 1); ++h) scale[k][h] = of_raw<S>(sc[j][k][h]) * 1048576.f;
+        }
+        // the slot takes the step after the ones ahead, of these rows or the warp's next
+        if (s + kAhead < steps) fetch(j, s + kAhead);
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const uint4* off = reinterpret_cast<const uint4*>(offsets) + ((size_t)b * v.chunks + chunk) * 2;
+          const uint4 o0 = off[0], o1 = off[1];
+          const int of0[kDigits] = {(int)o0.x, (int)o0.y, (int)o0.z, (int)o0.w};
+          const int of1[kDigits] = {(int)o1.x, (int)o1.y, (int)o1.z, (int)o1.w};
+          float f[kRows][two ? 2 : 1];
+#pragma unroll
+          for (int p = 0; p < kDigits; ++p) {
+            const uint4* from = reinterpret_cast<const uint4*>(smem) + (size_t)b * (v.chunks * kDigits * 2) +
+                                (size_t)p * 2 * v.chunks + chunk;
+            const uint4 lo = from[0], hi = from[v.chunks];
+            const int x[8] = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+              int sum[2] = {two ? of0[p] : of0[p] + (of1[p] - (int)kMagic), of1[p]};
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {   // registers 2 and 3 of every four are of the block's second half
+                int& at = sum[two ? (i >> 1) & 1 : 0];
+                at = __dp4a((int)code[k][i], x[i], at);
+              }
+#pragma unroll
+              for (int h = 0; h < (two ? 2 : 1); ++h) {
+                const float part = __int_as_float(sum[h]) - kMagicF;   // exact
+                f[k][h] = p == 0 ? part : fmaf(f[k][h], 256.f, part);
+              }
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < (two ? 2 : 1); ++h) {
+            const float unit = units[b * v.groups + gi + h];
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) acc[k][b] = fmaf(f[k][h] * unit, scale[k][h], acc[k][b]);
+          }
+        }
+      }
+    }
     if (t < tiles) {
       rows_of(t);
 #pragma unroll
@@ -276,7 +301,11 @@ __global__ void __launch_bounds__(kThreads, 2) q4_vec_rows_kernel(const Q4Rows a
 // cluster of `split`) owns 256 elements, two blocks, and a share of the list; a lane
 // eight elements, a word; a step is four listed rows, whose codes of an element a 4 x
 // 4 transpose of bytes puts side by side.
-constexpr int kListed = 2048;              // list entries staged at a time
+//
+// The list is taken kListed entries at a time.  Their coefficients act s, of every
+// group among the CTA's elements, go to shared memory once; the largest gives the unit of
+// the digits; a part's whole numbers become floats at its end.
+constexpr int kListed = 4096;
 constexpr int kColThreads = 512;
 constexpr int kColWarps = kColThreads / 32;
 constexpr int kColAhead = 6;               // steps loaded ahead
@@ -287,15 +316,25 @@ __device__ __forceinline__ float ld_scale_dt(const void* s, size_t i, int dt) {
                         : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(s) + i));
 }
 
-template <int B, bool two>
+template <bool two>
+struct ColLayout {
+  static constexpr int kSets = two ? 4 : 2;   // groups among the CTA's elements
+  // coefficients [set][kListed], digits [step][set][digit] of four bytes, one a row; the
+  // warps' sums take their place at the end
+  static constexpr size_t kCoefBytes = (size_t)kSets * kListed * 4;
+  static constexpr size_t kBytes = kCoefBytes + (size_t)kListed * kSets * kDigits;
+  static_assert(kBytes >= (size_t)kColWarps * 256 * 4, "the sums fit");
+};
+
+template <bool two>
 __global__ void __launch_bounds__(kColThreads, 1) q4_vec_cols_kernel(const Q4Cols a) {
-  constexpr int kSets = two ? 4 : 2;        // groups among the CTA's elements
-  // [step][vector][set][digit] of four bytes, one a row; the warps' sums at the end
+  constexpr int kSets = ColLayout<two>::kSets;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int id[kListed];
-  __shared__ int digit_sum[B][kSets][kDigits];
-  __shared__ uint32_t top[B][kSets];
-  __shared__ float sums[B * 256];
+  __shared__ uint32_t top[kSets];
+  __shared__ float sums[256];
+  float* coef = reinterpret_cast<float*>(smem);
+  uint32_t* digits = reinterpret_cast<uint32_t*>(smem + ColLayout<two>::kCoefBytes);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int slab = blockIdx.x / a.split, rank = blockIdx.x % a.split;
   const int blocks = (a.d + 127) >> 7;
@@ -304,8 +343,6 @@ __global__ void __launch_bounds__(kColThreads, 1) q4_vec_cols_kernel(const Q4Col
   const int lo = min(n, rank * share), hi = min(n, lo + share);
   const int word = lane & 15, set = two ? (lane >> 4) * 2 + (word & 1) : lane >> 4;
   const uint8_t* q = a.q + (size_t)min(2 * slab + (lane >> 4), blocks - 1) * kQ4BlockBytes + 4 * word;
-  if (tid < B * kSets * kDigits) (&digit_sum[0][0][0])[tid] = 0;
-  if (tid < B * kSets) (&top[0][0])[tid] = 0;
 
   uint32_t w[kColAhead][4];
   const auto stage_ids = [&](int c0, int m) {
@@ -314,6 +351,7 @@ __global__ void __launch_bounds__(kColThreads, 1) q4_vec_cols_kernel(const Q4Col
       // (an entry outside is reported, and has activation 0, from the first product on: row 0 is read)
       id[e] = j >= 0 && j < a.N ? j : 0;
     }
+    if (tid < kSets) top[tid] = 0;
   };
   const auto fetch = [&](int k, int s) {   // rows of the warp's step s
     const int4 j = *reinterpret_cast<const int4*>(&id[(s * kColWarps + wid) * 4]);
@@ -322,91 +360,78 @@ __global__ void __launch_bounds__(kColThreads, 1) q4_vec_cols_kernel(const Q4Col
     w[k][2] = ld_stream4(q + (size_t)j.z * a.pitch);
     w[k][3] = ld_stream4(q + (size_t)j.w * a.pitch);
   };
-  const auto steps_of = [&](int m) { return ((m + 3) / 4 - wid + kColWarps - 1) / kColWarps; };
-  const auto group_of = [&](int s) {
-    return min(two ? 4 * slab + s : 2 * slab + s, a.groups - 1);
-  };
-  const auto coefficient = [&](int b, int u, int j, int s) {   // (0 adds nothing, whatever the row holds)
-    const float x = __ldcg(a.act + (size_t)b * a.ld_act + u);
-    return x == 0.f ? 0.f : x * ld_scale_dt(a.scale, (size_t)j * a.groups + group_of(s), a.dt);
-  };
-
-  const int m0 = min(kListed, hi - lo);
-  stage_ids(lo, m0);
-  __syncthreads();
+  float out[8];   // elements (0, 2), (4, 6), (1, 3), (5, 7) of the lane's word
 #pragma unroll
-  for (int k = 0; k < kColAhead; ++k)
-    if (k < steps_of(m0)) fetch(k, k);
-  grid_dep_wait();   // the activations
-  grid_dep_launch();
-  // the largest coefficient of every vector and group: the unit of the fixed point
-  {
-    uint32_t most[B][kSets] = {};
-    for (int u = lo + tid; u < hi; u += kColThreads) {
-      const int l = u - lo < m0 ? id[u - lo] : a.list[u];
-      const int j = l >= 0 && l < a.N ? l : 0;
-#pragma unroll
-      for (int b = 0; b < B; ++b)
-#pragma unroll
-        for (int s = 0; s < kSets; ++s) most[b][s] = max(most[b][s], __float_as_uint(fabsf(coefficient(b, u, j, s))));
-    }
-#pragma unroll
-    for (int b = 0; b < B; ++b)
-#pragma unroll
-      for (int s = 0; s < kSets; ++s) {
-        const uint32_t most_of = __reduce_max_sync(0xffffffffu, most[b][s]);
-        if (lane == 0 && most_of) atomicMax(&top[b][s], most_of);
-      }
-  }
-  __syncthreads();
-
-  int acc[B][8][kDigits];   // elements (0, 2), (4, 6), (1, 3), (5, 7) of the lane's word
-#pragma unroll
-  for (int b = 0; b < B; ++b)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int p = 0; p < kDigits; ++p) acc[b][i][p] = 0;
-  uint32_t* digits = reinterpret_cast<uint32_t*>(smem);
+  for (int i = 0; i < 8; ++i) out[i] = 0.f;
+  bool waited = false;
   for (int c0 = lo; c0 < hi; c0 += kListed) {
-    const int m = min(kListed, hi - c0), padded = (m + 3) & ~3;
-    if (c0 > lo) {
-      __syncthreads();
-      stage_ids(c0, m);
-      __syncthreads();
+    const int m = min(kListed, hi - c0), quads = (m + 3) >> 2;
+    const int steps = (quads - wid + kColWarps - 1) / kColWarps;
+    __syncthreads();
+    stage_ids(c0, m);
+    __syncthreads();
 #pragma unroll
-      for (int k = 0; k < kColAhead; ++k)
-        if (k < steps_of(m)) fetch(k, k);
+    for (int k = 0; k < kColAhead; ++k)
+      if (k < steps) fetch(k, k);
+    if (!waited) {
+      grid_dep_wait();   // the activations
+      grid_dep_launch();
+      waited = true;
     }
-    {
-      int mine[B][kSets][kDigits] = {};
-      for (int e = tid; e < padded; e += kColThreads)
+    // coefficients, four entries a thread at a time, and the largest of them
+    uint32_t most[kSets] = {};
+    for (int e0 = tid; e0 < 4 * quads; e0 += 4 * kColThreads) {
+      float x[4], s[4][kSets];
 #pragma unroll
-        for (int b = 0; b < B; ++b)
+      for (int i = 0; i < 4; ++i) {
+        const int e = e0 + i * kColThreads;
+        x[i] = e < m ? __ldcg(a.act + c0 + e) : 0.f;
 #pragma unroll
-          for (int s = 0; s < kSets; ++s) {
-            int dig[kDigits];
-            const bool fine = e < m && top[b][s] < 0x7f800000u;
-            digits_of(fine ? fixed(coefficient(b, c0 + e, id[e], s), fixed_shift(top[b][s])) : 0, dig);
+        for (int g = 0; g < kSets; ++g) {
+          const int gi = min(two ? 4 * slab + g : 2 * slab + g, a.groups - 1);
+          s[i][g] = e < m ? ld_scale_dt(a.scale, (size_t)id[e] * a.groups + gi, a.dt) : 0.f;
+        }
+      }
 #pragma unroll
-            for (int p = 0; p < kDigits; ++p) {
-              reinterpret_cast<uint8_t*>(digits + (((size_t)(e >> 2) * B + b) * kSets + s) * kDigits + p)[e & 3] =
-                  (uint8_t)dig[p];
-              mine[b][s][p] += dig[p];
-            }
-          }
+      for (int i = 0; i < 4; ++i) {
+        const int e = e0 + i * kColThreads;
+        if (e >= 4 * quads) break;
 #pragma unroll
-      for (int b = 0; b < B; ++b)
+        for (int g = 0; g < kSets; ++g) {
+          const float c = x[i] == 0.f ? 0.f : x[i] * s[i][g];   // (0 adds nothing, whatever the row holds)
+          coef[g * kListed + e] = c;
+          most[g] = max(most[g], __float_as_uint(fabsf(c)));
+        }
+      }
+    }
 #pragma unroll
-        for (int s = 0; s < kSets; ++s)
-#pragma unroll
-          for (int p = 0; p < kDigits; ++p) {
-            const int sum = __reduce_add_sync(0xffffffffu, mine[b][s][p]);
-            if (lane == 0 && sum) atomicAdd(&digit_sum[b][s][p], sum);
-          }
+    for (int g = 0; g < kSets; ++g) {
+      const uint32_t all = __reduce_max_sync(0xffffffffu, most[g]);
+      if (lane == 0 && all) atomicMax(&top[g], all);
     }
     __syncthreads();
-    const int steps = steps_of(m);
+    // digits: a thread four rows, one group
+    for (int i = tid; i < quads * kSets; i += kColThreads) {
+      const int step = i / kSets, g = i % kSets, shift = fixed_shift(top[g]);
+      const bool fine = top[g] < 0x7f800000u;
+      uint32_t packed[kDigits] = {};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        int dig[kDigits];
+        digits_of(fine ? fixed(coef[g * kListed + 4 * step + r], shift) : 0, dig);
+#pragma unroll
+        for (int p = 0; p < kDigits; ++p) packed[p] |= (uint32_t)(dig[p] & 255) << (8 * r);
+      }
+      reinterpret_cast<uint4*>(digits)[i] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+    }
+    __syncthreads();
+    int acc[8][kDigits], offset[kDigits];
+#pragma unroll
+    for (int p = 0; p < kDigits; ++p) {
+      offset[p] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i][p] = 0;
+    }
     for (int s0 = 0; s0 < steps; s0 += kColAhead) {
 #pragma unroll
       for (int k = 0; k < kColAhead; ++k) {
@@ -414,64 +439,66 @@ __global__ void __launch_bounds__(kColThreads, 1) q4_vec_cols_kernel(const Q4Col
         const int step = (s0 + k) * kColWarps + wid;
         const uint32_t t0 = __byte_perm(w[k][0], w[k][1], 0x5140), t1 = __byte_perm(w[k][2], w[k][3], 0x5140);
         const uint32_t t2 = __byte_perm(w[k][0], w[k][1], 0x7362), t3 = __byte_perm(w[k][2], w[k][3], 0x7362);
+        if (s0 + k + kColAhead < steps) fetch(k, s0 + k + kColAhead);
         const uint32_t r[4] = {__byte_perm(t0, t1, 0x5410), __byte_perm(t0, t1, 0x7632), __byte_perm(t2, t3, 0x5410),
                                __byte_perm(t2, t3, 0x7632)};
+        const uint4 x = reinterpret_cast<const uint4*>(digits)[step * kSets + set];
+        const uint32_t xx[kDigits] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-          const uint4 x = *reinterpret_cast<const uint4*>(digits + (((size_t)step * B + b) * kSets + set) * kDigits);
-          const uint32_t xx[kDigits] = {x.x, x.y, x.z, x.w};
+        for (int p = 0; p < kDigits; ++p) offset[p] = __dp4a((int)xx[p], (int)0xf8f8f8f8u, offset[p]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+          const int c0i = (int)low_codes(r[i]), c1i = (int)high_codes(r[i]);
 #pragma unroll
-            for (int p = 0; p < kDigits; ++p) {
-              acc[b][2 * i][p] = __dp4a((int)low_codes(r[i]), (int)xx[p], acc[b][2 * i][p]);
-              acc[b][2 * i + 1][p] = __dp4a((int)high_codes(r[i]), (int)xx[p], acc[b][2 * i + 1][p]);
-            }
+          for (int p = 0; p < kDigits; ++p) {
+            acc[2 * i][p] = __dp4a(c0i, (int)xx[p], acc[2 * i][p]);
+            acc[2 * i + 1][p] = __dp4a(c1i, (int)xx[p], acc[2 * i + 1][p]);
+          }
         }
-        if (s0 + k + kColAhead < steps) fetch(k, s0 + k + kColAhead);
       }
     }
-  }
-  __syncthreads();
-  // the warps' whole numbers, in the digits' place, [warp][element]: their order does not matter
-  long long* red = reinterpret_cast<long long*>(smem);
-#pragma unroll
-  for (int b = 0; b < B; ++b) {
-    if (b > 0) __syncthreads();
+    // the part's sums: whole numbers, times the unit
+    const int shift = fixed_shift(top[set]);
+    const float u0 = pow2(-(shift / 2)), u1 = pow2(-(shift - shift / 2));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // elements of register i: 0 2 4 6 1 3 5 7
-      const int e = (i & 3) * 2 + (i >> 2);
       long long whole = 0;
 #pragma unroll
-      for (int p = 0; p < kDigits; ++p) whole = whole * 256 + acc[b][i][p];
-      red[wid * 256 + (lane >> 4) * 128 + 64 * (word & 1) + 8 * (word >> 1) + e] = whole;
+      for (int p = 0; p < kDigits; ++p) whole = whole * 256 + (acc[i][p] + offset[p]);
+      out[i] += __ll2float_rn(whole) * u0 * u1;
     }
-    __syncthreads();
-    if (tid < 256) {
-      const int s = two ? tid >> 6 : tid >> 7;
-      long long whole = 0, offset = 0;
+    if (top[set] >= 0x7f800000u) {   // an infinity or a NaN among the coefficients
 #pragma unroll
-      for (int k = 0; k < kColWarps; ++k) whole += red[k * 256 + tid];
-#pragma unroll
-      for (int p = 0; p < kDigits; ++p) offset = offset * 256 + digit_sum[b][s][p];
-      const int shift = fixed_shift(top[b][s]);
-      const float v = __ll2float_rn(whole - 8 * offset) * pow2(-(shift / 2)) * pow2(-(shift - shift / 2));
-      sums[b * 256 + tid] = top[b][s] < 0x7f800000u ? v : __int_as_float(0x7fc00000);
+      for (int i = 0; i < 8; ++i) out[i] = __int_as_float(0x7fc00000);
     }
+  }
+  if (!waited) {
+    grid_dep_wait();
+    grid_dep_launch();
+  }
+  __syncthreads();
+  // sums over the warps and the cluster's CTAs, in a fixed order
+  float* red = reinterpret_cast<float*>(smem);   // [warp][element]
+#pragma unroll
+  for (int i = 0; i < 8; ++i)   // register i holds element 0 2 4 6 1 3 5 7
+    red[wid * 256 + (lane >> 4) * 128 + 64 * (word & 1) + 8 * (word >> 1) + (i & 3) * 2 + (i >> 2)] = out[i];
+  __syncthreads();
+  if (tid < 256) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kColWarps; ++k) sum += red[k * 256 + tid];
+    sums[tid] = sum;
   }
   __syncthreads();
   if (a.split > 1) {
     cluster_arrive();
     cluster_wait();
   }
-  const int mine = (256 + a.split - 1) / a.split;   // elements that this CTA joins and writes
-  for (int i = tid; i < mine * B; i += kColThreads) {
-    const int b = i / mine, t = rank * mine + i - b * mine;
-    if (t >= 256 || slab * 256 + t >= a.d) continue;
+  const int mine = (256 + a.split - 1) / a.split, t = rank * mine + tid;   // elements that this CTA joins and writes
+  if (tid < mine && t < 256 && slab * 256 + t < a.d) {
     float sum = 0.f;
-    for (int r = 0; r < a.split; ++r) sum += a.split > 1 ? ld_dsmem_f32(sums + b * 256 + t, r) : sums[b * 256 + t];
-    float* o = a.out + (size_t)b * a.d + slab * 256 + t;
+    for (int r = 0; r < a.split; ++r) sum += a.split > 1 ? ld_dsmem_f32(sums + t, r) : sums[t];
+    float* o = a.out + slab * 256 + t;
     *o = a.accumulate ? *o + sum : sum;
   }
   if (a.split > 1) {   // no CTA leaves while its shared memory is read
@@ -502,7 +529,7 @@ template <typename S, int B, bool kList, bool two>
 cudaError_t run_rows_shape(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
   const int rows = kList ? a.cap : a.N;
   return rows < 4 * num_sms * 16 ? run_rows<S, B, 1, 5, kList, two>(a, pdl, num_sms, stream)
-                                 : run_rows<S, B, 4, 2, kList, two>(a, pdl, num_sms, stream);
+                                 : run_rows<S, B, 4, 1, kList, two>(a, pdl, num_sms, stream);
 }
 template <typename S>
 cudaError_t run_rows_of(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
@@ -516,14 +543,14 @@ cudaError_t run_rows_of(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t str
 }
 
 // Clusters of `split` CTAs that run at once (a property of the device).
-template <int B, bool two>
-int clusters_at_once(int split, size_t smem) {
+template <bool two>
+int clusters_at_once(int split) {
   static PerDevice known[9];
   return known[split].get(current_device(), [&] {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(split);
     cfg.blockDim = dim3(kColThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = ColLayout<two>::kBytes;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = split;
@@ -531,27 +558,33 @@ int clusters_at_once(int split, size_t smem) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, q4_vec_cols_kernel<B, two>, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, q4_vec_cols_kernel<two>, &cfg) != cudaSuccess) n = 0;
     (void)cudaGetLastError();
     return n;
   });
 }
 
-template <int B, bool two>
-cudaError_t run_cols(Q4Cols a, cudaStream_t stream) {
-  constexpr size_t digits = (size_t)kListed * B * (two ? 4 : 2) * kDigits, fold = (size_t)kColWarps * 256 * 8;
-  constexpr size_t smem = digits > fold ? digits : fold;
+template <bool two>
+cudaError_t run_cols(const Q4Cols& all, cudaStream_t stream) {
   static PerDevice attr;   // function attributes are per device
   const cudaError_t ea = (cudaError_t)attr.get(current_device(), [] {
-    return (int)cudaFuncSetAttribute(q4_vec_cols_kernel<B, two>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return (int)cudaFuncSetAttribute(q4_vec_cols_kernel<two>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)ColLayout<two>::kBytes);
   });
   if (ea != cudaSuccess) return ea;
   // the largest clusters that still all run at once, with a step of four rows a warp at least
+  Q4Cols a = all;
   const int slabs = (a.d + 255) / 256;
   a.split = 8;
-  while (a.split > 1 && (clusters_at_once<B, two>(a.split, smem) < slabs || (a.split - 1) * 4 * kColWarps >= a.cap))
-    --a.split;
-  return launch_k(q4_vec_cols_kernel<B, two>, dim3(slabs * a.split), dim3(kColThreads), smem, stream, true, a.split, a);
+  while (a.split > 1 && (clusters_at_once<two>(a.split) < slabs || (a.split - 1) * 4 * kColWarps >= a.cap)) --a.split;
+  for (int b = 0; b < all.B; ++b) {
+    const cudaError_t e = launch_k(q4_vec_cols_kernel<two>, dim3(slabs * a.split), dim3(kColThreads),
+                                   ColLayout<two>::kBytes, stream, true, a.split, a);
+    if (e != cudaSuccess) return e;
+    a.act += a.ld_act;
+    a.out += a.d;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -571,8 +604,7 @@ cudaError_t launch_q4_vec_rows(const Q4Rows& a, dv_dtype dt, bool pdl, cudaStrea
 }
 
 cudaError_t launch_q4_vec_cols(const Q4Cols& a, cudaStream_t stream) {
-  if (a.B == 1) return a.group == 64 ? run_cols<1, true>(a, stream) : run_cols<1, false>(a, stream);
-  return a.group == 64 ? run_cols<2, true>(a, stream) : run_cols<2, false>(a, stream);
+  return a.group == 64 ? run_cols<true>(a, stream) : run_cols<false>(a, stream);
 }
 
 }  // namespace dv
