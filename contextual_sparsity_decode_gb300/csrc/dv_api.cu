@@ -209,12 +209,14 @@ struct Q4Ws {
   int32_t* U_count;
   uint32_t* member;
   float* act;
+  float* part;
   uint8_t* pieces;
 };
 Q4Ws carve_q4_mlp(Carver& c, int B, int d, int N, int cap) {
   Q4Ws w{};
   w.pieces = c.take<uint8_t>((size_t)6 * B * ((d + 127) / 128 * 128));
   w.act = c.take<float>((size_t)B * (((B == 1 ? cap : mlp_union_cap(B, N, cap)) + 3) & ~3) + 16);
+  w.part = c.take<float>((size_t)kQ4Splits * ((d + 127) / 128 * 128));
   if (B > 1) {
     w.U = c.take<int32_t>((size_t)N);
     w.U_count = c.take<int32_t>(4);
@@ -520,7 +522,7 @@ dv_status dv_q4_sparse_mlp(const void* y, int B, int d, int N, const dv_q4* W1, 
   L.q1 = static_cast<const uint8_t*>(W1->q); L.s1 = W1->scale; L.group1 = W1->group;
   L.q2 = static_cast<const uint8_t*>(W2->q); L.s2 = W2->scale; L.group2 = W2->group;
   L.idx = idx; L.cap = cap; L.count = count; L.out = out; L.accumulate = accumulate ? 1 : 0;
-  L.U = w.U; L.U_count = w.U_count; L.member = w.member; L.act = w.act; L.pieces = w.pieces;
+  L.U = w.U; L.U_count = w.U_count; L.member = w.member; L.act = w.act; L.part = w.part; L.pieces = w.pieces;
   cudaError_t e = launch_q4_sparse_mlp(L, dt, static_cast<WsHeader*>(ws), stream);
   return e == cudaSuccess ? DV_OK : cuda_fail(e);
 }

@@ -349,6 +349,7 @@ cudaError_t launch_beam_select(const BeamLaunch& a, dv_dtype dt, WsHeader* hdr, 
 // ---- matrices in 4 bits (k_q4.cu) ------------------------------------------------
 
 constexpr int kQ4BlockBytes = 64;  // a block of 128 elements
+constexpr int kQ4Splits = 152;     // CTAs that share a list
 // First kind of product: rows of a matrix (all, or a list's) with vectors.
 struct Q4Rows {
   const uint8_t* q; const void* scale; int group;
@@ -372,7 +373,8 @@ struct Q4Cols {
   const int32_t* list; const int32_t* count; int cap;
   const float* act; int ld_act;         // as the first kind writes them
   float* out; int accumulate;           // [B][d]
-  int groups, split;
+  float* part;                          // kQ4Splits rows of whole blocks
+  int groups, split, blocks;
   size_t pitch;
 };
 struct Q4MatvecLaunch {
@@ -389,6 +391,7 @@ struct Q4MlpLaunch {
   float* out; int accumulate;
   int32_t* U; int32_t* U_count; uint32_t* member;  // B > 1
   float* act;                           // B rows of cap (B > 1: mlp_union_cap), rounded up to 4, and 16 more
+  float* part;                          // kQ4Splits rows of whole blocks
   void* pieces;
 };
 // One and two vectors (k_q4_vec.cu).

@@ -612,7 +612,7 @@ cudaError_t launch_q4_sparse_mlp(const Q4MlpLaunch& L, dv_dtype dt, WsHeader* hd
   Q4Cols c{};
   c.q = L.q2; c.scale = L.s2; c.group = L.group2; c.B = L.B; c.d = L.d; c.N = L.N;
   c.list = a.list; c.count = a.count; c.cap = a.cap; c.act = L.act; c.ld_act = a.ld_act;
-  c.out = L.out; c.accumulate = L.accumulate; c.dt = dt;
+  c.out = L.out; c.accumulate = L.accumulate; c.dt = dt; c.part = L.part;
   const int blocks = (L.d + 127) / 128;
   c.pitch = (size_t)blocks * kBlockBytes;
   c.groups = (L.d + L.group2 - 1) / L.group2;

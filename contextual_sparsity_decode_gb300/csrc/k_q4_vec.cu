@@ -297,78 +297,75 @@ __global__ void __launch_bounds__(kThreads, 2) q4_vec_rows_kernel(const Q4Rows a
 
 // ---- sums of listed rows ------------------------------------------------------------------
 
-// out[b][t] (+)= sum_u act[b][u] s[j_u][group of t] (code[j_u][t] - 8).  A CTA (of a
-// cluster of `split`) owns 256 elements, two blocks, and a share of the list; a lane
-// eight elements, a word; a step is four listed rows, whose codes of an element a 4 x
-// 4 transpose of bytes puts side by side.
+// out[b][t] (+)= sum_u act[b][u] s[j_u][group of t] (code[j_u][t] - 8).  A CTA owns a
+// share of the list and whole rows of it (128 bytes of every row to a CTA instead took 39
+// us for 53 MB: a row's memory page is opened once a CTA); a thread owns two words,
+// 8 g .. 8 g + 7 of either half of a block; a step is four rows, whose codes of an element a
+// 4 x 4 transpose of bytes puts side by side.  The CTAs' sums go to the workspace and
+// a second kernel adds them in order.
 //
-// The list is taken kListed entries at a time.  Their coefficients act s, of every
-// group among the CTA's elements, go to shared memory once; the largest gives the unit of
-// the digits; a part's whole numbers become floats at its end.
-constexpr int kListed = 4096;
-constexpr int kColThreads = 512;
-constexpr int kColWarps = kColThreads / 32;
-constexpr int kColAhead = 6;               // steps loaded ahead
+// The coefficients act s of as many steps as fit are staged together; the largest of a
+// group gives the unit of its digits, and a part's whole numbers become floats at its end.
+constexpr int kColThreads = 512;           // at most
+constexpr int kColAhead = 3;               // steps loaded ahead
+constexpr int kStaged = 4096;              // (step, group) pairs staged at a time
+constexpr int kMaxGroups = 512;            // rows of 32768, groups of 64
 
 __device__ __forceinline__ float ld_scale_dt(const void* s, size_t i, int dt) {
   return dt == DV_F32 ? __ldg(static_cast<const float*>(s) + i)
          : dt == DV_F16 ? __half2float(__ldg(static_cast<const __half*>(s) + i))
                         : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(s) + i));
 }
-
-template <bool two>
-struct ColLayout {
-  static constexpr int kSets = two ? 4 : 2;   // groups among the CTA's elements
-  // coefficients [set][kListed], digits [step][set][digit] of four bytes, one a row; the
-  // warps' sums take their place at the end
-  static constexpr size_t kCoefBytes = (size_t)kSets * kListed * 4;
-  static constexpr size_t kBytes = kCoefBytes + (size_t)kListed * kSets * kDigits;
-  static_assert(kBytes >= (size_t)kColWarps * 256 * 4, "the sums fit");
-};
+__device__ __forceinline__ uint2 ld_stream8(const void* p) {
+  uint2 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
 
 template <bool two>
 __global__ void __launch_bounds__(kColThreads, 1) q4_vec_cols_kernel(const Q4Cols a) {
-  constexpr int kSets = ColLayout<two>::kSets;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int id[kListed];
-  __shared__ uint32_t top[kSets];
-  __shared__ float sums[256];
-  float* coef = reinterpret_cast<float*>(smem);
-  uint32_t* digits = reinterpret_cast<uint32_t*>(smem + ColLayout<two>::kCoefBytes);
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int slab = blockIdx.x / a.split, rank = blockIdx.x % a.split;
-  const int blocks = (a.d + 127) >> 7;
+  extern __shared__ __align__(128) uint8_t smem[];   // coefficients of (step, group), four rows; then their digits
+  __shared__ uint32_t top[kMaxGroups];
+  __shared__ int id[kStaged / 2 * 4];
+  float4* coef = reinterpret_cast<float4*>(smem);
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
+  const int words = a.blocks * 16, pair = blockIdx.y * threads + tid;   // the thread's two words
+  const bool mine = 2 * pair < words;
+  const int block = min(pair >> 3, a.blocks - 1);
+  // groups of the CTA's words
+  const int first_block = (blockIdx.y * threads) >> 3;
+  const int per = two ? 2 : 1, g_first = first_block * per;
+  const int groups = min((threads + 7) / 8 * per, a.blocks * per - g_first);
+  const int set = (block - first_block) * per;
   const int n = max(0, min(*a.count, a.cap));
-  const int share = ((n + a.split - 1) / a.split + 3) & ~3;
-  const int lo = min(n, rank * share), hi = min(n, lo + share);
-  const int word = lane & 15, set = two ? (lane >> 4) * 2 + (word & 1) : lane >> 4;
-  const uint8_t* q = a.q + (size_t)min(2 * slab + (lane >> 4), blocks - 1) * kQ4BlockBytes + 4 * word;
+  const int quads_all = (n + 3) >> 2, share = (quads_all + gridDim.x - 1) / gridDim.x;
+  const int lo = min(quads_all, (int)blockIdx.x * share), hi = min(quads_all, lo + share);
+  const int at_once = min(kStaged / groups, kStaged / 2);
+  const uint8_t* q = a.q + (size_t)min(pair, words / 2 - 1) * 8;
 
-  uint32_t w[kColAhead][4];
-  const auto stage_ids = [&](int c0, int m) {
-    for (int e = tid; e < ((m + 3) & ~3); e += kColThreads) {
-      const int j = e < m ? a.list[c0 + e] : 0;
+  uint2 w[kColAhead][4];
+  const auto fetch = [&](int k, int s) {   // rows of step s
+    const int4 j = reinterpret_cast<const int4*>(id)[s];
+    w[k][0] = ld_stream8(q + (size_t)j.x * a.pitch);
+    w[k][1] = ld_stream8(q + (size_t)j.y * a.pitch);
+    w[k][2] = ld_stream8(q + (size_t)j.z * a.pitch);
+    w[k][3] = ld_stream8(q + (size_t)j.w * a.pitch);
+  };
+  float out[2][8];   // elements (0, 2), (4, 6), (1, 3), (5, 7) of either word
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[h][i] = 0.f;
+  bool waited = false;
+  for (int q0 = lo; q0 < hi; q0 += at_once) {
+    const int steps = min(at_once, hi - q0), m = min(4 * steps, n - 4 * q0);
+    __syncthreads();
+    for (int e = tid; e < 4 * steps; e += threads) {
+      const int j = e < m ? a.list[4 * q0 + e] : 0;
       // (an entry outside is reported, and has activation 0, from the first product on: row 0 is read)
       id[e] = j >= 0 && j < a.N ? j : 0;
     }
-    if (tid < kSets) top[tid] = 0;
-  };
-  const auto fetch = [&](int k, int s) {   // rows of the warp's step s
-    const int4 j = *reinterpret_cast<const int4*>(&id[(s * kColWarps + wid) * 4]);
-    w[k][0] = ld_stream4(q + (size_t)j.x * a.pitch);
-    w[k][1] = ld_stream4(q + (size_t)j.y * a.pitch);
-    w[k][2] = ld_stream4(q + (size_t)j.z * a.pitch);
-    w[k][3] = ld_stream4(q + (size_t)j.w * a.pitch);
-  };
-  float out[8];   // elements (0, 2), (4, 6), (1, 3), (5, 7) of the lane's word
-#pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = 0.f;
-  bool waited = false;
-  for (int c0 = lo; c0 < hi; c0 += kListed) {
-    const int m = min(kListed, hi - c0), quads = (m + 3) >> 2;
-    const int steps = (quads - wid + kColWarps - 1) / kColWarps;
-    __syncthreads();
-    stage_ids(c0, m);
+    for (int g = tid; g < groups; g += threads) top[g] = 0;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kColAhead; ++k)
@@ -378,133 +375,144 @@ __global__ void __launch_bounds__(kColThreads, 1) q4_vec_cols_kernel(const Q4Col
       grid_dep_launch();
       waited = true;
     }
-    // coefficients, four entries a thread at a time, and the largest of them
-    uint32_t most[kSets] = {};
-    for (int e0 = tid; e0 < 4 * quads; e0 += 4 * kColThreads) {
-      float x[4], s[4][kSets];
+    // coefficients, a row's groups by neighbouring threads, four entries of a thread at a time
+    const int items = 4 * steps * groups;
+    for (int i0 = tid; i0 < items; i0 += 4 * threads) {
+      float x[4], s[4];
+      int e[4], g[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = e0 + i * kColThreads;
-        x[i] = e < m ? __ldcg(a.act + c0 + e) : 0.f;
-#pragma unroll
-        for (int g = 0; g < kSets; ++g) {
-          const int gi = min(two ? 4 * slab + g : 2 * slab + g, a.groups - 1);
-          s[i][g] = e < m ? ld_scale_dt(a.scale, (size_t)id[e] * a.groups + gi, a.dt) : 0.f;
-        }
+      for (int k = 0; k < 4; ++k) {
+        const int i = min(i0 + k * threads, items - 1);
+        e[k] = i / groups;
+        g[k] = i - e[k] * groups;
+        x[k] = __ldcg(a.act + 4 * q0 + min(e[k], m - 1));
+        s[k] = ld_scale_dt(a.scale, (size_t)id[e[k]] * a.groups + min(g_first + g[k], a.groups - 1), a.dt);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = e0 + i * kColThreads;
-        if (e >= 4 * quads) break;
-#pragma unroll
-        for (int g = 0; g < kSets; ++g) {
-          const float c = x[i] == 0.f ? 0.f : x[i] * s[i][g];   // (0 adds nothing, whatever the row holds)
-          coef[g * kListed + e] = c;
-          most[g] = max(most[g], __float_as_uint(fabsf(c)));
-        }
+      for (int k = 0; k < 4; ++k) {
+        if (i0 + k * threads >= items) break;
+        const float c = x[k] == 0.f || e[k] >= m ? 0.f : x[k] * s[k];   // (0 adds nothing, whatever the row holds)
+        reinterpret_cast<float*>(coef + (size_t)(e[k] >> 2) * groups + g[k])[e[k] & 3] = c;
+        const uint32_t bits = __float_as_uint(fabsf(c));
+        if (bits) atomicMax(&top[g[k]], bits);
       }
-    }
-#pragma unroll
-    for (int g = 0; g < kSets; ++g) {
-      const uint32_t all = __reduce_max_sync(0xffffffffu, most[g]);
-      if (lane == 0 && all) atomicMax(&top[g], all);
     }
     __syncthreads();
-    // digits: a thread four rows, one group
-    for (int i = tid; i < quads * kSets; i += kColThreads) {
-      const int step = i / kSets, g = i % kSets, shift = fixed_shift(top[g]);
-      const bool fine = top[g] < 0x7f800000u;
+    for (int i = tid; i < steps * groups; i += threads) {
+      const uint32_t most = top[i % groups];
+      const int shift = fixed_shift(most);
+      const float4 c = coef[i];
+      const float cc[4] = {c.x, c.y, c.z, c.w};
       uint32_t packed[kDigits] = {};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         int dig[kDigits];
-        digits_of(fine ? fixed(coef[g * kListed + 4 * step + r], shift) : 0, dig);
+        digits_of(most < 0x7f800000u ? fixed(cc[r], shift) : 0, dig);
 #pragma unroll
         for (int p = 0; p < kDigits; ++p) packed[p] |= (uint32_t)(dig[p] & 255) << (8 * r);
       }
-      reinterpret_cast<uint4*>(digits)[i] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+      reinterpret_cast<uint4*>(coef)[i] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
     }
     __syncthreads();
-    int acc[8][kDigits], offset[kDigits];
+    int acc[2][8][kDigits], offset[two ? 2 : 1][kDigits];
 #pragma unroll
-    for (int p = 0; p < kDigits; ++p) {
-      offset[p] = 0;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i][p] = 0;
-    }
+      for (int p = 0; p < kDigits; ++p) {
+        offset[two && h][p] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[h][i][p] = 0;
+      }
     for (int s0 = 0; s0 < steps; s0 += kColAhead) {
 #pragma unroll
       for (int k = 0; k < kColAhead; ++k) {
         if (s0 + k >= steps) break;
-        const int step = (s0 + k) * kColWarps + wid;
-        const uint32_t t0 = __byte_perm(w[k][0], w[k][1], 0x5140), t1 = __byte_perm(w[k][2], w[k][3], 0x5140);
-        const uint32_t t2 = __byte_perm(w[k][0], w[k][1], 0x7362), t3 = __byte_perm(w[k][2], w[k][3], 0x7362);
+        uint32_t r[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w0 = h ? w[k][0].y : w[k][0].x, w1 = h ? w[k][1].y : w[k][1].x;
+          const uint32_t w2 = h ? w[k][2].y : w[k][2].x, w3 = h ? w[k][3].y : w[k][3].x;
+          const uint32_t t0 = __byte_perm(w0, w1, 0x5140), t1 = __byte_perm(w2, w3, 0x5140);
+          const uint32_t t2 = __byte_perm(w0, w1, 0x7362), t3 = __byte_perm(w2, w3, 0x7362);
+          r[h][0] = __byte_perm(t0, t1, 0x5410);
+          r[h][1] = __byte_perm(t0, t1, 0x7632);
+          r[h][2] = __byte_perm(t2, t3, 0x5410);
+          r[h][3] = __byte_perm(t2, t3, 0x7632);
+        }
         if (s0 + k + kColAhead < steps) fetch(k, s0 + k + kColAhead);
-        const uint32_t r[4] = {__byte_perm(t0, t1, 0x5410), __byte_perm(t0, t1, 0x7632), __byte_perm(t2, t3, 0x5410),
-                               __byte_perm(t2, t3, 0x7632)};
-        const uint4 x = reinterpret_cast<const uint4*>(digits)[step * kSets + set];
-        const uint32_t xx[kDigits] = {x.x, x.y, x.z, x.w};
+        const uint4* dig = reinterpret_cast<const uint4*>(coef) + (size_t)(s0 + k) * groups + set;
+        uint4 x[two ? 2 : 1];
+        x[0] = dig[0];
+        if (two) x[two] = dig[1];
 #pragma unroll
-        for (int p = 0; p < kDigits; ++p) offset[p] = __dp4a((int)xx[p], (int)0xf8f8f8f8u, offset[p]);
+        for (int h = 0; h < 2; ++h) {
+          const uint4 xh = x[two && h];
+          const int xx[kDigits] = {(int)xh.x, (int)xh.y, (int)xh.z, (int)xh.w};
+          if (h == 0 || two) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c0i = (int)low_codes(r[i]), c1i = (int)high_codes(r[i]);
+            for (int p = 0; p < kDigits; ++p) offset[two && h][p] = __dp4a(xx[p], (int)0xf8f8f8f8u, offset[two && h][p]);
+          }
 #pragma unroll
-          for (int p = 0; p < kDigits; ++p) {
-            acc[2 * i][p] = __dp4a(c0i, (int)xx[p], acc[2 * i][p]);
-            acc[2 * i + 1][p] = __dp4a(c1i, (int)xx[p], acc[2 * i + 1][p]);
+          for (int i = 0; i < 4; ++i) {
+            const int c0 = (int)low_codes(r[h][i]), c1 = (int)high_codes(r[h][i]);
+#pragma unroll
+            for (int p = 0; p < kDigits; ++p) {
+              acc[h][2 * i][p] = __dp4a(c0, xx[p], acc[h][2 * i][p]);
+              acc[h][2 * i + 1][p] = __dp4a(c1, xx[p], acc[h][2 * i + 1][p]);
+            }
           }
         }
       }
     }
     // the part's sums: whole numbers, times the unit
-    const int shift = fixed_shift(top[set]);
-    const float u0 = pow2(-(shift / 2)), u1 = pow2(-(shift - shift / 2));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      long long whole = 0;
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t most = top[set + (two && h)];
+      const int shift = fixed_shift(most);
+      const float u0 = pow2(-(shift / 2)), u1 = pow2(-(shift - shift / 2));
 #pragma unroll
-      for (int p = 0; p < kDigits; ++p) whole = whole * 256 + (acc[i][p] + offset[p]);
-      out[i] += __ll2float_rn(whole) * u0 * u1;
-    }
-    if (top[set] >= 0x7f800000u) {   // an infinity or a NaN among the coefficients
+      for (int i = 0; i < 8; ++i) {
+        long long whole = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) out[i] = __int_as_float(0x7fc00000);
+        for (int p = 0; p < kDigits; ++p) whole = whole * 256 + (acc[h][i][p] + offset[two && h][p]);
+        // (an infinity or a NaN among the coefficients)
+        out[h][i] = most < 0x7f800000u ? out[h][i] + __ll2float_rn(whole) * u0 * u1 : __int_as_float(0x7fc00000);
+      }
     }
   }
   if (!waited) {
     grid_dep_wait();
     grid_dep_launch();
   }
-  __syncthreads();
-  // sums over the warps and the cluster's CTAs, in a fixed order
-  float* red = reinterpret_cast<float*>(smem);   // [warp][element]
+  if (!mine) return;
+  // register i holds element 0 2 4 6 1 3 5 7
+  float* part = a.part + (size_t)blockIdx.x * a.blocks * 128 + (size_t)(pair >> 3) * 128 + 8 * (pair & 7);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)   // register i holds element 0 2 4 6 1 3 5 7
-    red[wid * 256 + (lane >> 4) * 128 + 64 * (word & 1) + 8 * (word >> 1) + (i & 3) * 2 + (i >> 2)] = out[i];
+  for (int h = 0; h < 2; ++h) {
+    float4* to = reinterpret_cast<float4*>(part + 64 * h);
+    to[0] = make_float4(out[h][0], out[h][4], out[h][1], out[h][5]);
+    to[1] = make_float4(out[h][2], out[h][6], out[h][3], out[h][7]);
+  }
+}
+
+// out[t] (+)= the sum over the CTAs of the kernel before: 32 elements a CTA, eight shares
+// of the sums, in a fixed order.
+__global__ void __launch_bounds__(256) q4_vec_join_kernel(const float* __restrict__ part, int parts, int ld, int d,
+                                                         float* __restrict__ out, int accumulate) {
+  __shared__ float red[8][32];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, t = blockIdx.x * 32 + lane;
+  grid_dep_wait();
+  grid_dep_launch();
+  float sum = 0.f;
+#pragma unroll 8
+  for (int r = wid; r < parts; r += 8) sum += __ldcg(part + (size_t)r * ld + t);   // (ld is a multiple of 128)
+  red[wid][lane] = sum;
   __syncthreads();
-  if (tid < 256) {
-    float sum = 0.f;
+  if (wid != 0 || t >= d) return;
+  sum = red[0][lane];
 #pragma unroll
-    for (int k = 0; k < kColWarps; ++k) sum += red[k * 256 + tid];
-    sums[tid] = sum;
-  }
-  __syncthreads();
-  if (a.split > 1) {
-    cluster_arrive();
-    cluster_wait();
-  }
-  const int mine = (256 + a.split - 1) / a.split, t = rank * mine + tid;   // elements that this CTA joins and writes
-  if (tid < mine && t < 256 && slab * 256 + t < a.d) {
-    float sum = 0.f;
-    for (int r = 0; r < a.split; ++r) sum += a.split > 1 ? ld_dsmem_f32(sums + t, r) : sums[t];
-    float* o = a.out + slab * 256 + t;
-    *o = a.accumulate ? *o + sum : sum;
-  }
-  if (a.split > 1) {   // no CTA leaves while its shared memory is read
-    cluster_arrive();
-    cluster_wait();
-  }
+  for (int k = 1; k < 8; ++k) sum += red[k][lane];
+  out[t] = accumulate ? out[t] + sum : sum;
 }
 
 // ---- launches ------------------------------------------------------------------------------
@@ -523,13 +531,14 @@ cudaError_t run_rows(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream
   return launch_k(q4_vec_rows_kernel<S, B, kRows, kAhead, kList, two>, dim3((unsigned)(ctas < most ? ctas : most)),
                   dim3(kThreads), smem, stream, pdl, 1, a);
 }
-// Rows at a time: four, which read a vector's digits once; one where that would leave
-// most of the GPU's warps (16 an SM) without rows.
+// Rows at a time: two (one: 55 us for 50257 x 5120, 30 for 14336 listed rows of 7168; two:
+// 35.8 and 21.6; four: 35.0 and 24.7); one where two would leave half of the GPU's
+// warps (16 an SM) without rows (1024 of 5120: 6.9 us, two: 7.2).
 template <typename S, int B, bool kList, bool two>
 cudaError_t run_rows_shape(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
   const int rows = kList ? a.cap : a.N;
-  return rows < 4 * num_sms * 16 ? run_rows<S, B, 1, 5, kList, two>(a, pdl, num_sms, stream)
-                                 : run_rows<S, B, 4, 1, kList, two>(a, pdl, num_sms, stream);
+  return rows < 8 * num_sms ? run_rows<S, B, 1, 5, kList, two>(a, pdl, num_sms, stream)
+                            : run_rows<S, B, 2, 4, kList, two>(a, pdl, num_sms, stream);
 }
 template <typename S>
 cudaError_t run_rows_of(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
@@ -542,44 +551,27 @@ cudaError_t run_rows_of(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t str
   return two ? run_rows_shape<S, 2, false, true>(a, pdl, num_sms, stream) : run_rows_shape<S, 2, false, false>(a, pdl, num_sms, stream);
 }
 
-// Clusters of `split` CTAs that run at once (a property of the device).
 template <bool two>
-int clusters_at_once(int split) {
-  static PerDevice known[9];
-  return known[split].get(current_device(), [&] {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(split);
-    cfg.blockDim = dim3(kColThreads);
-    cfg.dynamicSmemBytes = ColLayout<two>::kBytes;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, q4_vec_cols_kernel<two>, &cfg) != cudaSuccess) n = 0;
-    (void)cudaGetLastError();
-    return n;
-  });
-}
-
-template <bool two>
-cudaError_t run_cols(const Q4Cols& all, cudaStream_t stream) {
+cudaError_t run_cols(const Q4Cols& all, int num_sms, cudaStream_t stream) {
   static PerDevice attr;   // function attributes are per device
   const cudaError_t ea = (cudaError_t)attr.get(current_device(), [] {
-    return (int)cudaFuncSetAttribute(q4_vec_cols_kernel<two>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)ColLayout<two>::kBytes);
+    return (int)cudaFuncSetAttribute(q4_vec_cols_kernel<two>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStaged * 16);
   });
   if (ea != cudaSuccess) return ea;
-  // the largest clusters that still all run at once, with a step of four rows a warp at least
   Q4Cols a = all;
-  const int slabs = (a.d + 255) / 256;
-  a.split = 8;
-  while (a.split > 1 && (clusters_at_once<two>(a.split) < slabs || (a.split - 1) * 4 * kColWarps >= a.cap)) --a.split;
+  a.blocks = (a.d + 127) / 128;
+  // a thread to two words; rows of more than 8192 elements in equal slabs of whole blocks
+  const int slabs = (a.blocks * 8 + kColThreads - 1) / kColThreads;
+  const int threads = ((a.blocks + slabs - 1) / slabs * 8 + 31) / 32 * 32;
+  const int quads = (a.cap + 3) / 4;
+  int splits = num_sms < kQ4Splits ? num_sms : kQ4Splits;
+  splits = splits / slabs > 0 ? splits / slabs : 1;
+  if (splits > quads) splits = quads;
   for (int b = 0; b < all.B; ++b) {
-    const cudaError_t e = launch_k(q4_vec_cols_kernel<two>, dim3(slabs * a.split), dim3(kColThreads),
-                                   ColLayout<two>::kBytes, stream, true, a.split, a);
+    cudaError_t e = launch_k(q4_vec_cols_kernel<two>, dim3(splits, slabs), dim3(threads), kStaged * 16, stream, true, 1, a);
+    if (e != cudaSuccess) return e;
+    e = launch_k(q4_vec_join_kernel, dim3((a.d + 31) / 32), dim3(256), 0, stream, true, 1, (const float*)a.part, splits,
+                 a.blocks * 128, a.d, a.out, a.accumulate);
     if (e != cudaSuccess) return e;
     a.act += a.ld_act;
     a.out += a.d;
@@ -604,7 +596,8 @@ cudaError_t launch_q4_vec_rows(const Q4Rows& a, dv_dtype dt, bool pdl, cudaStrea
 }
 
 cudaError_t launch_q4_vec_cols(const Q4Cols& a, cudaStream_t stream) {
-  return a.group == 64 ? run_cols<true>(a, stream) : run_cols<false>(a, stream);
+  const int num_sms = num_sms_current();
+  return a.group == 64 ? run_cols<true>(a, num_sms, stream) : run_cols<false>(a, num_sms, stream);
 }
 
 }  // namespace dv
