@@ -18,6 +18,10 @@ libdv's kernels.
 Several candidates per sequence: ``verify_tree`` runs a drafted token tree
 through the layers (dv_tree_attn over the cache), ``accept`` keeps a path of it
 (dv_kv_compact), and ``reorder`` lets beams continue others (dv_kv_reorder).
+
+4 bits: a layer's MLP may be held in 4 bits (dv_q4_sparse_mlp in the place of
+dv_sparse_mlp), and ``sample`` draws the next tokens through a 4-bit output head
+(dv_layernorm, dv_q4_matvec, dv_sample).
 """
 
 from __future__ import annotations
@@ -29,11 +33,25 @@ import torch
 from . import binding as dv
 
 
+def quantize_mlp(layers: List[Dict[str, torch.Tensor]], group: int = 128) -> List[dict]:
+    """The same layers with their MLP in 4 bits (W1q and W2q in the place of
+    W1n and W2n; groups of 64 or 128 weights share a scale)."""
+    out = []
+    for W in layers:
+        W = dict(W)
+        if "W1n" in W:
+            W["W1q"], W["W2q"] = (dv.Q4.of(W.pop(k), group) for k in ("W1n", "W2n"))
+        out.append(W)
+    return out
+
+
 class SparseDecoder:
     """Device state of an L-layer sparse decoder for a batch of B sequences.
 
     layers: per layer a dict of weight tensors in the library layouts
             (Wqkv, Wo, W1n, W2n, PA1t, PA2t, PM1t, PM2t), all of one dtype.
+            A layer may hold its MLP in 4 bits, as W1q and W2q (binding.Q4)
+            in the place of W1n and W2n: see ``quantize_mlp``.
     trace:  keep a copy of the residual stream before layer 0 (r_in0) and
             after every block of every layer (r_mid[l] after the attention,
             r_out[l] after the MLP), so that each block can be checked on its
@@ -47,13 +65,15 @@ class SparseDecoder:
         self.layers = layers
         self.L = len(layers)
         self.h, _, self.d_h, self.d = W0["Wqkv"].shape
-        self.N = W0["W1n"].shape[0]
-        self.r = W0["PM1t"].shape[0]
+        self.N, self.r = W0["PM2t"].shape
         self.B, self.n_max = B, n_max
         self.k_heads, self.k_neurons = k_heads, k_neurons
         self.scale, self.eps = float(scale), float(eps)
-        self.dtype = W0["W1n"].dtype
-        dev = W0["W1n"].device
+        self.dtype = W0["Wqkv"].dtype
+        dev = W0["Wqkv"].device
+        for W in layers:
+            if "W1q" in W and any((q.N, q.d, q.dtype) != (self.N, self.d, self.dtype) for q in (W["W1q"], W["W2q"])):
+                raise ValueError(f"4-bit matrices of another shape or type than [{self.N}][{self.d}] of {self.dtype}")
         self.device = dev
         i32 = dict(dtype=torch.int32, device=dev)
         B, d = self.B, self.d
@@ -76,10 +96,11 @@ class SparseDecoder:
         self.ws_pred_side = dv.workspace(dv.dv_predict_workspace_size(B, 2, self.r, self.N), dev)
         self.ws_attn = dv.workspace(
             dv.dv_sparse_attn_workspace_size(B, d, self.h, self.d_h, k_heads, n_max), dev)
-        self.ws_mlp = dv.workspace(dv.dv_sparse_mlp_workspace_size(B, d, self.N, k_neurons), dev)
+        self.ws_mlp, self.ws_mlp_q4 = self._mlp_workspaces(B, k_neurons)
         self.kv_layers = dv.KVLayers(self.kv)
         self.ws_move = dv.workspace(256, dev)
         self._tree: Dict[int, dict] = {}    # buffers of verify_tree by the nodes they hold
+        self.head: Optional[dv.Q4] = None   # output head (set_head)
         self.side = torch.cuda.Stream(device=dev)
         self.ev_y = [dv.make_event() for _ in layers]
         self.ev_pred = [dv.make_event() for _ in layers]
@@ -103,11 +124,28 @@ class SparseDecoder:
         self.neur_cnt = [torch.zeros(B, **i32) for _ in self.layers]
         self.ws_attn = dv.workspace(
             dv.dv_sparse_attn_workspace_size(B, self.d, self.h, self.d_h, k_heads, self.n_max), dev)
-        self.ws_mlp = dv.workspace(dv.dv_sparse_mlp_workspace_size(B, self.d, self.N, k_neurons), dev)
+        self.ws_mlp, self.ws_mlp_q4 = self._mlp_workspaces(B, k_neurons)
         self._tree = {}
         self.graph = None
 
     # ------------------------------------------------------------------ pieces
+    def _mlp_workspaces(self, rows: int, k_neurons: int):
+        """For the layers whose MLP is in 16 (or 32) bits and for those in 4
+        (None where there are none): a workspace keeps state of its kind of
+        call, so the two do not share one."""
+        kinds = {"W1q" in W for W in self.layers}
+        size = (self.d, self.N, k_neurons)
+        return (dv.workspace(dv.dv_sparse_mlp_workspace_size(rows, *size), self.device) if False in kinds else None,
+                dv.workspace(dv.dv_q4_sparse_mlp_workspace_size(rows, *size), self.device) if True in kinds else None)
+
+    def _mlp(self, l: int, y, idx, cnt, out, ws, ws_q4):
+        """out += the sparse MLP of layer l."""
+        W = self.layers[l]
+        if "W1q" in W:
+            dv.dv_q4_sparse_mlp(y, W["W1q"], W["W2q"], idx, cnt, out, ws_q4, accumulate=True)
+        else:
+            dv.dv_sparse_mlp(y, W["W1n"], W["W2n"], idx, cnt, out, ws, accumulate=True)
+
     def predictors(self, l: int):
         W = self.layers[l]
         return [dv.Predictor(W["PA1t"], W["PA2t"], self.head_idx[l], self.head_cnt[l],
@@ -147,8 +185,8 @@ class SparseDecoder:
             if self.trace:
                 self.r_mid[l].copy_(self.r_stream)
             dv.dv_layernorm(self.r_stream, self.y_m[l], self.eps)
-            dv.dv_sparse_mlp(self.y_m[l], W["W1n"], W["W2n"], self.neur_idx[l], self.neur_cnt[l],
-                             self.r_stream, self.ws_mlp, accumulate=True)
+            self._mlp(l, self.y_m[l], self.neur_idx[l], self.neur_cnt[l], self.r_stream, self.ws_mlp,
+                      self.ws_mlp_q4)
             if self.trace:
                 self.r_out[l].copy_(self.r_stream)
 
@@ -267,8 +305,8 @@ class SparseDecoder:
             dv.dv_layernorm(self.r_stream, self.y_m[l], self.eps)
             self._time("ln")
             self._time("mlp")
-            dv.dv_sparse_mlp(self.y_m[l], W["W1n"], W["W2n"], self.neur_idx[l], self.neur_cnt[l],
-                             self.r_stream, self.ws_mlp, accumulate=True)
+            self._mlp(l, self.y_m[l], self.neur_idx[l], self.neur_cnt[l], self.r_stream, self.ws_mlp,
+                      self.ws_mlp_q4)
             self._time("mlp")
             if self.trace:
                 self.r_out[l].copy_(self.r_stream)
@@ -301,6 +339,33 @@ class SparseDecoder:
     def replay(self):
         self.graph.replay()
 
+    # ------------------------------------------------------------------ the next token
+    def set_head(self, head: dv.Q4):
+        """The output head of ``sample``: a 4-bit matrix [V][d] (its row v
+        scores token v), and the buffers that go with it."""
+        if head.d != self.d or head.dtype != self.dtype or head.q.device != self.device:
+            raise ValueError(f"a 4-bit matrix with rows of {self.d} of {self.dtype} on {self.device} is wanted")
+        dev, B = self.device, self.B
+        self.head = head
+        self.y_head = torch.zeros(B, self.d, dtype=self.dtype, device=dev)
+        self.logits = torch.zeros(B, head.N, dtype=torch.float32, device=dev)
+        self.token = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.prob = torch.zeros(B, dtype=torch.float32, device=dev)
+        self.ws_head = dv.workspace(dv.dv_q4_matvec_workspace_size(B, self.d, head.N), dev)
+        self.ws_sample = dv.workspace(dv.dv_sample_workspace_size(B, head.N), dev)
+
+    def sample(self, u, temperature=None, top_k=None, top_p=None, min_p=None):
+        """The next token of each sequence and its probability (``token`` and
+        ``prob``, [B]), drawn with the numbers u from the head's scores of the
+        residual stream that a step leaves: layer norm, ``logits``, dv_sample
+        (whose parameters these are).  Can be captured."""
+        if self.head is None:
+            raise ValueError("sample: set_head first")
+        dv.dv_layernorm(self.r_stream, self.y_head, self.eps)
+        dv.dv_q4_matvec(self.y_head, self.head, self.logits, self.ws_head)
+        dv.dv_sample(self.logits, u, self.token, self.ws_sample, temperature, top_k, top_p, min_p, prob=self.prob)
+        return self.token, self.prob
+
     # ------------------------------------------- several candidates per sequence
     def _tree_buffers(self, T: int) -> dict:
         """Buffers and workspaces of verify_tree for trees of T nodes: the
@@ -328,8 +393,8 @@ class SparseDecoder:
                  node=torch.arange(size, **i32)[None], row=torch.arange(B, device=dev)[:, None],
                  head=(torch.arange(B * h, device=dev) * self.n_max).view(B, 1, h),
                  ws_pred=dv.workspace(dv.dv_predict_workspace_size(max(chunk, min(B, 32)), 1, self.r, self.N), dev),
-                 ws_mlp=dv.workspace(dv.dv_sparse_mlp_workspace_size(chunk, d, self.N, self.k_neurons), dev),
                  ws_tree=dv.workspace(dv.dv_tree_attn_workspace_size(B, size, h, 1, d_h), dev))
+        t["ws_mlp"], t["ws_mlp_q4"] = self._mlp_workspaces(chunk, self.k_neurons)
         self._tree[size] = t
         return t
 
@@ -417,7 +482,7 @@ class SparseDecoder:
                 idx, cnt = t["neur_idx"][:e - i], t["neur_cnt"][:e - i]
                 dv.dv_predict(src[i:e], [dv.Predictor(W["PM1t"], W["PM2t"], idx, cnt, dv.DV_TOPK, self.k_neurons)],
                               t["ws_pred"])
-                dv.dv_sparse_mlp(y_mlp[i:e], W["W1n"], W["W2n"], idx, cnt, r[i:e], t["ws_mlp"], accumulate=True)
+                self._mlp(l, y_mlp[i:e], idx, cnt, r[i:e], t["ws_mlp"], t["ws_mlp_q4"])
             y, before = before, y
         return r.view(B, T, d).clone()
 
@@ -435,9 +500,12 @@ class SparseDecoder:
     def check(self):
         """Raise the first error that any call has recorded since the last check
         (all workspaces are read and cleared)."""
-        found = [dv.dv_check(ws) for ws in
-                 (self.ws_pred_main, self.ws_pred_side, self.ws_attn, self.ws_mlp, self.ws_move,
-                  *(t[k] for t in self._tree.values() for k in ("ws_pred", "ws_mlp", "ws_tree")))]
+        used = [self.ws_pred_main, self.ws_pred_side, self.ws_attn, self.ws_mlp, self.ws_mlp_q4, self.ws_move]
+        if self.head is not None:
+            used.append(self.ws_sample)
+        for t in self._tree.values():
+            used += [t[k] for k in ("ws_pred", "ws_mlp", "ws_mlp_q4", "ws_tree")]
+        found = [dv.dv_check(ws) for ws in used if ws is not None]
         for st, info in found:
             if st != 0:
                 raise dv.DvError(st, "decode step", f"info={info}")

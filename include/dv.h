@@ -267,7 +267,8 @@ dv_status dv_q4_sparse_mlp_workspace_size(int B, int d, int N, int cap,
  * neuron whose activation is 0 adds nothing, whatever its row of W2 holds.  The
  * activations are fp32 and enter the second product as they are; every output
  * has one writer and a fixed order of summation: results repeat bit for bit.
- * dv_set_launch_overlap as for dv_sparse_mlp (16-bit storage).
+ * Its workspace is not one of dv_sparse_mlp (which keeps counters there).
+ * dv_set_launch_overlap as for dv_sparse_mlp.
  * Device errors: DV_ERR_INDEX_RANGE (an entry outside [0, N) is skipped),
  * DV_ERR_CAPACITY (a count above cap is cut off).
  * Limits: B <= 32, N <= 65536, d <= 32768. */
@@ -522,8 +523,8 @@ dv_status dv_layernorm(const float* x, int B, int d, float eps,
  * earlier ones and read only data those do not write.  At level 0 (the
  * default) the first kernel of each call waits for everything before it
  * (those of dv_layernorm, dv_tree_attn, dv_beam_select, dv_q4_matvec and
- * dv_sample, and of dv_q4_sparse_mlp for one DV_F32 row, may be started
- * earlier, at either level, and wait before they read or write anything).
+ * dv_sample may be started earlier, at either level, and wait before they read
+ * or write anything).
  * At level 1, for batch 1, the first kernel of dv_sparse_attn, dv_sparse_mlp and
  * dv_q4_sparse_mlp may also start while the kernel before the call is still
  * running, and reads before waiting for it: the head / neuron lists and
