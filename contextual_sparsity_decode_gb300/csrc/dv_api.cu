@@ -489,6 +489,7 @@ dv_status dv_q4_matvec(const void* y, int B, int d, int N, const dv_q4* W, dv_dt
   L.q = static_cast<const uint8_t*>(W->q); L.scale = W->scale; L.group = W->group;
   L.out = out; L.accumulate = accumulate ? 1 : 0;
   L.pieces = carve_q4_matvec(c, B, d);
+  L.hdr = static_cast<WsHeader*>(ws);
   cudaError_t e = launch_q4_matvec(L, dt, stream);
   return e == cudaSuccess ? DV_OK : cuda_fail(e);
 }

@@ -358,7 +358,7 @@ struct Q4Rows {
   const uint32_t* member; int words;    // [B][words] whose list a row is in, or null
   float* act; int ld_act;               // listed: max(0, product), B rows ld_act apart (a multiple of 4)
   float* out; int accumulate;           // all rows: [B][N]
-  WsHeader* hdr;
+  WsHeader* hdr; long long wait_ns;
   int early;                            // list and weights are read before the wait
   const void* y;                        // [B][d]
   int blocks, groups;                   // of a row
@@ -382,6 +382,7 @@ struct Q4MatvecLaunch {
   const uint8_t* q; const void* scale; int group;
   float* out; int accumulate;
   void* pieces;                         // DV_F32: 3 B rows of whole blocks, 16 bits
+  WsHeader* hdr;
 };
 struct Q4MlpLaunch {
   const void* y; int B, d, N;
@@ -394,6 +395,9 @@ struct Q4MlpLaunch {
   float* part;                          // kQ4Splits rows of whole blocks
   void* pieces;
 };
+// Three and more vectors of a 16-bit type, the first kind of product (k_q4_tc.cu).
+bool q4_tc_supported(int B, int d, dv_dtype dt);
+cudaError_t launch_q4_tc_rows(const Q4Rows& a, dv_dtype dt, WsHeader* hdr, bool pdl, cudaStream_t stream);
 // One and two vectors (k_q4_vec.cu).
 bool q4_vec_supported(int B, int d);
 cudaError_t launch_q4_vec_rows(const Q4Rows& a, dv_dtype dt, bool pdl, cudaStream_t stream);

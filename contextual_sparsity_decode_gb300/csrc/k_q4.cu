@@ -524,6 +524,7 @@ cudaError_t launch_rows(Q4Rows a, const void* y, void* pieces, dv_dtype dt, bool
   a.pitch = (size_t)a.blocks * kBlockBytes;
   a.groups = (a.d + a.group - 1) / a.group;
   if (q4_vec_supported(a.B, a.d)) return launch_q4_vec_rows(a, dt, pdl, stream);
+  if (q4_tc_supported(a.B, a.d, dt)) return launch_q4_tc_rows(a, dt, a.hdr, pdl, stream);
   a.kw = 8;
   if (dt == DV_F32) {
     const int ld = a.blocks * 128;
@@ -589,7 +590,7 @@ cudaError_t launch_q4_quantize(const void* W, int N, int d, dv_dtype dt, int gro
 cudaError_t launch_q4_matvec(const Q4MatvecLaunch& L, dv_dtype dt, cudaStream_t stream) {
   Q4Rows a{};
   a.q = L.q; a.scale = L.scale; a.group = L.group; a.B = L.B; a.d = L.d; a.N = L.N;
-  a.out = L.out; a.accumulate = L.accumulate;
+  a.out = L.out; a.accumulate = L.accumulate; a.hdr = L.hdr;
   return launch_rows(a, L.y, L.pieces, dt, true, stream);
 }
 

@@ -1,0 +1,402 @@
+// Matrices in 4 bits (layout: k_q4.cu), three and more vectors of a 16-bit type: products
+// with rows of the matrix on the 5th-generation tensor cores.
+//
+// A tile is 128 rows; a product is a block of 128 elements of them (M = 128, K = 128)
+// with the vectors (N = 16 or 32).  The codes of a block go from registers to tensor
+// memory as 16-bit floats, a thread to a row (the A operand: shared memory would have
+// to take and give back four times the packed bytes); the vectors come by TMA; the
+// accumulator holds one group's sums, which the row's thread takes out, scales and
+// adds to its own in fp32 (a group's scale cannot be in the codes, which are
+// exact).
+//   warps 0-3, 4-7   two groups of 128 threads, a row each: every other block.  Open the
+//                    codes, store them to tensor memory, two blocks ahead of the sums
+//                    they take out.
+//   warps 8-11       packed rows into a ring of shared-memory stages (four blocks, 256
+//                    bytes of a row), cp.async, 16 lanes to a row
+//   warp 12          the vectors' tiles (TMA), warp 13 the products
+// Measured beside the m16n8k16 kernel of k_q4.cu in the table of cases.
+
+#include <climits>
+
+#include "dv_kernels.h"
+#include "tc_common.cuh"
+#include "tma_map.h"
+
+namespace dv {
+namespace {
+
+constexpr int kThreads = 448;
+constexpr int kRowsTile = 128;
+constexpr int kStageBlocks = 4;
+constexpr uint32_t kRowBytes = kStageBlocks * kQ4BlockBytes;   // of a stage
+constexpr uint32_t kWBytes = kRowsTile * kRowBytes;
+constexpr long long kUnwindNs = 2000000000LL;
+constexpr uint32_t kTmemCols = 512;
+
+template <int NB>
+struct Sizes {
+  static constexpr uint32_t kXBlock = 2 * NB * 128;             // the vectors' 128 elements
+  static constexpr uint32_t kXBytes = kStageBlocks * kXBlock;
+  static constexpr int kStages = NB == 32 ? 3 : 4;
+  static constexpr uint32_t kRedBytes = kRowsTile * (NB + 1) * 4;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * (kWBytes + kXBytes) + kRedBytes;
+  static_assert(kSmem + 1024 <= 227 * 1024, "fits an SM");
+};
+
+// Element pairs (2 i, 2 i + 1) of a word, less 8.
+template <typename T> struct Open;
+template <> struct Open<__half> {
+  static __device__ __forceinline__ void word(uint32_t w, uint32_t* p) {
+    const __half2 m1032 = __half2half2(__ushort_as_half(0xe408));           // -1032
+    const __half2 r16 = __half2half2(__ushort_as_half(0x2c00));             // 1/16
+    const __half2 m72 = __half2half2(__ushort_as_half(0xd480));             // -72
+    const uint32_t v = w >> 8;
+    const uint32_t a[4] = {(w & 0x000f000fu) | 0x64006400u, (w & 0x00f000f0u) | 0x64006400u,
+                           (v & 0x000f000fu) | 0x64006400u, (v & 0x00f000f0u) | 0x64006400u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = *reinterpret_cast<const __half2*>(&a[i]);
+      const __half2 r = (i & 1) ? __hfma2(h, r16, m72) : __hadd2(h, m1032);  // 1024 + 16 q, 1024 + q
+      p[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+};
+template <> struct Open<__nv_bfloat16> {
+  static __device__ __forceinline__ void word(uint32_t w, uint32_t* p) {
+    const __nv_bfloat162 m136 = __bfloat162bfloat162(__ushort_as_bfloat16(0xc308));  // -136
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;       // 128 + q
+      const __nv_bfloat162 r = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a), m136);
+      p[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+};
+
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* stop, WsHeader* hdr,
+                                       long long limit_ns, int code) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (*stop) return false;
+    if ((long long)(globaltimer_ns() - t0) > limit_ns) {
+      *stop = 1;
+      set_error(hdr, DV_ERR_TIMEOUT, code);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* stop, const Q4Rows& a, int code) {
+  return tc::mbar_try_wait(bar, parity) || wait_slow(bar, parity, stop, a.hdr, a.wait_ns, code);
+}
+// By a converged warp: the same answer in all lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* stop, const Q4Rows& a, int code) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, stop, a, code));
+}
+// Arrive on `bar` once this thread's copies so far have arrived.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::saddr(bar)) : "memory");
+}
+__device__ __forceinline__ void row_groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <typename T> __device__ __forceinline__ float scale_of(const void* s, size_t i) {
+  return Elem<T>::to_f(__ldg(static_cast<const T*>(s) + i));
+}
+
+// two: groups of 64, an accumulator to each half of a block.
+template <typename T, int NB, bool kList, bool two>
+__global__ void __launch_bounds__(kThreads, 1)
+    q4_tc_rows_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ Q4Rows a) {
+  using Z = Sizes<NB>;
+  constexpr int S = Z::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full_w[S], empty_w[S], full_x[S], empty_x[S], ready[2][2], done[2][2], fin;
+  __shared__ uint32_t tmem_base;
+  __shared__ int stop_s;
+  volatile int* stop = &stop_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sX = smem;
+  uint8_t* sW = smem + S * Z::kXBytes;
+  float* red = reinterpret_cast<float*>(sW + S * kWBytes);   // [row][NB + 1]
+  const long long unwind_ns = a.wait_ns > kUnwindNs ? a.wait_ns : kUnwindNs;
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      tc::mbar_init(&full_w[s], 128);
+      tc::mbar_init(&empty_w[s], 8);
+      tc::mbar_init(&full_x[s], 1);
+      tc::mbar_init(&empty_x[s], 1);
+    }
+    for (int g = 0; g < 2; ++g)
+      for (int q = 0; q < 2; ++q) {
+        tc::mbar_init(&ready[g][q], 128);
+        tc::mbar_init(&done[g][q], 1);
+      }
+    tc::mbar_init(&fin, 1);
+    tc::fence_mbar_init();
+    stop_s = 0;
+  }
+  if (warp == 13) tc::tmem_alloc(&tmem_base, kTmemCols);
+  grid_dep_wait();   // no global memory is touched before
+  grid_dep_launch();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_base;
+  const int n = kList ? max(0, min(*a.count, a.cap)) : a.N;
+  const int tiles = (n + kRowsTile - 1) / kRowsTile;
+  const int stages = (a.blocks + kStageBlocks - 1) / kStageBlocks;   // of a tile
+
+  if (warp < 8) {
+    // ---- codes to tensor memory, sums out of it
+    const int grp = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tA = tmem + grp * 256 + lanes, tD = tA + 128;
+    float acc[NB];
+    uint32_t made = 0, taken = 0;   // this group's blocks so far, and those whose sums are out
+    float s0[2] = {0.f, 0.f}, s1[2] = {0.f, 0.f};   // scales of the blocks under way
+    bool ok = true;
+    const auto take = [&] {   // the oldest block's sums
+      const int q = taken & 1;
+      if (!wait_warp(&done[grp][q], (taken >> 1) & 1, stop, a, 71)) return false;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int h = 0; h < (two ? 2 : 1); ++h) {
+        const float f = h ? (q ? s1[1] : s0[1]) : (q ? s1[0] : s0[0]);
+        float v[NB];
+        if constexpr (NB == 32) {
+          tc::tmem_ld32(tD + q * (two ? 2 * NB : NB) + h * NB, v);
+        } else {
+          tc::tmem_ld8(tD + q * (two ? 2 * NB : NB) + h * NB, v);
+          tc::tmem_ld8(tD + q * (two ? 2 * NB : NB) + h * NB + 8, v + 8);
+        }
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < NB; ++i) acc[i] = fmaf(f, v[i], acc[i]);
+      }
+      ++taken;
+      return true;
+    };
+    int st = 0;
+    // (all eight warps go through all tiles, also once a wait has given up: they meet at their end)
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+      const int u = tile * kRowsTile + r;
+      int row = u < n ? u : -1;
+      if (kList && u < n) {
+        row = a.list[u];
+        if (row < 0 || row >= a.N) {
+          if (grp == 0) set_error(a.hdr, DV_ERR_INDEX_RANGE, row);
+          row = -1;
+        }
+      }
+      const size_t scales = (size_t)max(row, 0) * a.groups;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) acc[i] = 0.f;
+      for (int k = 0; ok && k < stages; ++k, ++st) {
+        const int slot = st % S;
+        if (!wait_warp(&full_w[slot], (st / S) & 1, stop, a, 72)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* packed = sW + slot * kWBytes + r * kRowBytes;
+#pragma unroll
+        for (int j2 = 0; j2 < 2; ++j2) {
+          const int j = 2 * j2 + grp, kb = k * kStageBlocks + j;
+          if (kb >= a.blocks) continue;
+          if (made - taken == 2 && !take()) {
+            ok = false;
+            break;
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(w + 4 * c) =
+                *reinterpret_cast<const uint4*>(packed + (((4 * j + c) ^ (r & 7)) << 4));
+          const int q = made & 1;
+          const int gi = two ? 2 * kb : kb;
+          const float f0 = scale_of<T>(a.scale, scales + gi);
+          const float f1 = two ? scale_of<T>(a.scale, scales + min(gi + 1, a.groups - 1)) : 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {   // words h, h + 2, ... are the half's 32 pairs in order
+            uint32_t p[32];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) Open<T>::word(w[2 * g + h], p + 4 * g);
+            tc::tmem_st32(tA + q * 64 + h * 32, p);
+          }
+          (q ? s1[0] : s0[0]) = f0;
+          (q ? s1[1] : s0[1]) = f1;
+          tc::tmem_st_wait();
+          tc::fence_before_sync();
+          tc::mbar_arrive(&ready[grp][q]);
+          ++made;
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&empty_w[slot]);
+      }
+      while (ok && taken != made) ok = take();
+      if (grp == 1) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) red[r * (NB + 1) + i] = acc[i];
+      }
+      row_groups_sync();
+      if (grp == 0 && u < n && !*stop) {
+        for (int b = 0; b < a.B; ++b) {
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < NB; ++i) sum = i == b ? acc[i] : sum;   // (registers cannot be indexed)
+          sum += red[r * (NB + 1) + b];
+          if (kList) {
+            bool live = row >= 0;
+            if (live && a.member) live = bit_test(a.member + (size_t)b * a.words, row);
+            a.act[(size_t)b * a.ld_act + u] = live ? (sum > 0.f || sum != sum ? sum : 0.f) : 0.f;
+          } else {
+            float* o = a.out + (size_t)b * a.N + u;
+            *o = a.accumulate ? *o + sum : sum;
+          }
+        }
+      }
+      row_groups_sync();
+    }
+    tc::fence_before_sync();
+  } else if (warp < 12) {
+    // ---- packed rows: 16 lanes to a row's 256 bytes, chunk c of row r at c ^ (r % 8)
+    const int t = tid - 256, c = t & 15, r0 = t >> 4;
+    int st = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      int rows[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int u = min(tile * kRowsTile + r0 + 8 * q, n - 1);
+        const int l = kList ? a.list[u] : u;
+        rows[q] = l >= 0 && l < a.N ? l : 0;
+      }
+      for (int k = 0; k < stages; ++k, ++st) {
+        const int slot = st % S;
+        if (st >= S && !wait_bar(&empty_w[slot], ((st / S) - 1) & 1, stop, a, 73)) {
+          ok = false;
+          break;
+        }
+        uint8_t* base = sW + slot * kWBytes + r0 * kRowBytes + ((c ^ (r0 & 7)) << 4);
+        const uint32_t at = k * kRowBytes + c * 16;
+        if (at < a.pitch) {
+#pragma unroll
+          for (int q = 0; q < 16; ++q)   // (rows 8 apart: the same place in their 256 bytes)
+            cp_async16(base + q * 8 * kRowBytes, a.q + (size_t)rows[q] * a.pitch + at);
+        }
+        cp_async_arrive(&full_w[slot]);
+      }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();   // no copy is in flight when the CTA ends
+  } else if (warp == 12) {
+    // ---- the vectors' tiles
+    if (lane == 0) {
+      int st = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
+        for (int k = 0; k < stages; ++k, ++st) {
+          const int slot = st % S;
+          if (st >= S && !wait_bar(&empty_x[slot], ((st / S) - 1) & 1, stop, a, 74)) {
+            ok = false;
+            break;
+          }
+          const int here = min(kStageBlocks, a.blocks - k * kStageBlocks);
+          tc::mbar_arrive_expect_tx(&full_x[slot], here * Z::kXBlock);
+          for (int j = 0; j < 2 * here; ++j)
+            tc::tma_load_2d(sX + slot * Z::kXBytes + j * (Z::kXBlock / 2), &mapX, (k * kStageBlocks * 2 + j) * 64, 0,
+                            &full_x[slot]);
+        }
+      // no copy is in flight when the CTA ends
+      for (int s = max(0, st - S); s < st; ++s)
+        if (!tc::mbar_wait(&full_x[s % S], (s / S) & 1, unwind_ns)) break;
+    }
+    __syncwarp();
+  } else {
+    // ---- products
+    constexpr bool kBf16 = !std::is_same<T, __half>::value;
+    constexpr uint32_t idesc = tc::idesc_f16(kRowsTile, NB, kBf16, false, false);
+    uint32_t made[2] = {0, 0};
+    int st = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
+      for (int k = 0; ok && k < stages; ++k, ++st) {
+        const int slot = st % S;
+        if (!wait_warp(&full_x[slot], (st / S) & 1, stop, a, 75)) {
+          ok = false;
+          break;
+        }
+        const uint32_t x = tc::saddr(sX + slot * Z::kXBytes);
+        const int here = min(kStageBlocks, a.blocks - k * kStageBlocks);
+        for (int j = 0; j < here; ++j) {
+          const int grp = j & 1;
+          const uint32_t m = grp ? made[1] : made[0];
+          if (!wait_warp(&ready[grp][m & 1], (m >> 1) & 1, stop, a, 76)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            const uint32_t tA = tmem + grp * 256 + (m & 1) * 64, tD = tmem + grp * 256 + 128 + (m & 1) * (two ? 2 * NB : NB);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_f16_ts(tD + (two ? h * NB : 0), tA + h * 32 + kk * 8,
+                               tc::smem_desc(x + j * Z::kXBlock + h * (NB * 128) + kk * 32, 16, 1024, 2), idesc,
+                               kk != 0 || (h != 0 && !two));
+            tc::mma_commit(&done[grp][m & 1]);
+          }
+          __syncwarp();
+          if (grp) ++made[1]; else ++made[0];
+        }
+        if (!ok) break;
+        if (tc::elect_one()) tc::mma_commit(&empty_x[slot]);
+        __syncwarp();
+      }
+    // every product has ended before tensor memory is given back
+    if (tc::elect_one()) tc::mma_commit(&fin);
+    __syncwarp();
+    (void)tc::mbar_wait(&fin, 0, unwind_ns);
+    tc::fence_before_sync();
+  }
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 13) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <typename T, int NB, bool kList, bool two>
+cudaError_t run(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
+  static PerDevice attr;   // function attributes are per device
+  const cudaError_t ea = (cudaError_t)attr.get(current_device(), [] {
+    return (int)cudaFuncSetAttribute(q4_tc_rows_kernel<T, NB, kList, two>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)Sizes<NB>::kSmem);
+  });
+  if (ea != cudaSuccess) return ea;
+  CUtensorMap map;
+  if (!make_map(&map, a.y, (uint64_t)a.d, (uint64_t)a.B, NB, !std::is_same<T, __half>::value)) return cudaErrorInvalidValue;
+  const int tiles = ((kList ? a.cap : a.N) + kRowsTile - 1) / kRowsTile;
+  return launch_k(q4_tc_rows_kernel<T, NB, kList, two>, dim3(tiles < num_sms ? tiles : num_sms), dim3(kThreads),
+                  Sizes<NB>::kSmem, stream, pdl, 1, map, a);
+}
+template <typename T, int NB>
+cudaError_t run_nb(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
+  if (a.list) return a.group == 64 ? run<T, NB, true, true>(a, pdl, num_sms, stream) : run<T, NB, true, false>(a, pdl, num_sms, stream);
+  return a.group == 64 ? run<T, NB, false, true>(a, pdl, num_sms, stream) : run<T, NB, false, false>(a, pdl, num_sms, stream);
+}
+
+}  // namespace
+
+bool q4_tc_supported(int B, int d, dv_dtype dt) { return dt != DV_F32 && B >= 3 && B <= 32 && d >= 64; }
+
+cudaError_t launch_q4_tc_rows(const Q4Rows& L, dv_dtype dt, WsHeader* hdr, bool pdl, cudaStream_t stream) {
+  Q4Rows a = L;
+  a.hdr = hdr;
+  a.wait_ns = wait_limit_ns();
+  const int num_sms = num_sms_current();
+  if (dt == DV_F16) return a.B <= 16 ? run_nb<__half, 16>(a, pdl, num_sms, stream) : run_nb<__half, 32>(a, pdl, num_sms, stream);
+  return a.B <= 16 ? run_nb<__nv_bfloat16, 16>(a, pdl, num_sms, stream) : run_nb<__nv_bfloat16, 32>(a, pdl, num_sms, stream);
+}
+
+}  // namespace dv
