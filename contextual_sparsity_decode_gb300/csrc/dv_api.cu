@@ -216,7 +216,7 @@ Q4Ws carve_q4_mlp(Carver& c, int B, int d, int N, int cap) {
   Q4Ws w{};
   w.pieces = c.take<uint8_t>((size_t)6 * B * ((d + 127) / 128 * 128));
   w.act = c.take<float>((size_t)B * (((B == 1 ? cap : mlp_union_cap(B, N, cap)) + 3) & ~3) + 16);
-  w.part = c.take<float>((size_t)kQ4Splits * ((d + 127) / 128 * 128));
+  w.part = c.take<float>(q4_part_floats(B, d));
   if (B > 1) {
     w.U = c.take<int32_t>((size_t)N);
     w.U_count = c.take<int32_t>(4);

@@ -373,8 +373,8 @@ struct Q4Cols {
   const int32_t* list; const int32_t* count; int cap;
   const float* act; int ld_act;         // as the first kind writes them
   float* out; int accumulate;           // [B][d]
-  float* part;                          // kQ4Splits rows of whole blocks
-  int groups, split, blocks;
+  float* part;                          // q4_part_floats: the sums of shares of the list
+  int groups, blocks;
   size_t pitch;
 };
 struct Q4MatvecLaunch {
@@ -392,7 +392,7 @@ struct Q4MlpLaunch {
   float* out; int accumulate;
   int32_t* U; int32_t* U_count; uint32_t* member;  // B > 1
   float* act;                           // B rows of cap (B > 1: mlp_union_cap), rounded up to 4, and 16 more
-  float* part;                          // kQ4Splits rows of whole blocks
+  float* part;                          // q4_part_floats
   void* pieces;
 };
 // Three and more vectors of a 16-bit type, the first kind of product (k_q4_tc.cu).
@@ -402,6 +402,9 @@ cudaError_t launch_q4_tc_rows(const Q4Rows& a, dv_dtype dt, WsHeader* hdr, bool 
 bool q4_vec_supported(int B, int d);
 cudaError_t launch_q4_vec_rows(const Q4Rows& a, dv_dtype dt, bool pdl, cudaStream_t stream);
 cudaError_t launch_q4_vec_cols(const Q4Cols& a, cudaStream_t stream);
+// Adds the shares' sums [share][B][whole blocks] into out.
+cudaError_t launch_q4_join(const Q4Cols& a, int shares, cudaStream_t stream);
+size_t q4_part_floats(int B, int d);
 cudaError_t launch_q4_quantize(const void* W, int N, int d, dv_dtype dt, int group, void* q, void* scale, void* values,
                                int num_sms, cudaStream_t stream);
 cudaError_t launch_q4_matvec(const Q4MatvecLaunch& L, dv_dtype dt, cudaStream_t stream);

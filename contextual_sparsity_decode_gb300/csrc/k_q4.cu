@@ -338,24 +338,50 @@ __global__ void __launch_bounds__(kThreads) q4_rows_kernel(const Q4Rows a) {
 
 // ---- second product of the MLP ----------------------------------------------------------
 
-// out[b][t] (+)= sum_u act[b][u] s[j_u][group of t] (code[j_u][t] - 8): the CTAs of
-// a cluster own one block of 128 output elements and a share of the list each; a
-// warp step is 16 listed rows by the 128 elements.  kCols: the three pieces of the
-// coefficients are columns of one product (3 B <= 8); otherwise three products.
-constexpr int kListed = 1024;   // list entries held at a time
-constexpr int kSteps = 2;       // warp steps whose loads are issued together
+// out[b][t] (+)= sum_u act[b][u] s[j_u][group of t] (code[j_u][t] - 8): a CTA owns a
+// share of the list and up to eight blocks of its rows, one a warp; a step is 16 rows by the
+// 128 elements, elements as the A operand's rows.  The coefficients enter as three
+// pieces, a product each.  The CTAs' sums go to the workspace, and a second kernel adds
+// them in order.
+constexpr int kColWarps = 8;
 
-template <typename S, int NT, bool kCols>
-__global__ void __launch_bounds__(kThreads) q4_cols_kernel(const Q4Cols a) {
-  extern __shared__ __align__(16) float red[];   // [128][B] the CTA's sums, then [kWarps - 1] more of them
-  __shared__ int id[kListed];
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int g = lane >> 2, c = lane & 3;
-  const int kb = blockIdx.x / a.split, rank = blockIdx.x % a.split;
+template <typename S>
+__device__ __forceinline__ uint32_t ld_raw(const void* s, size_t i) {   // (volatile: not moved to its use)
+  if constexpr (sizeof(S) == 4) {
+    uint32_t v;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(static_cast<const float*>(s) + i));
+    return v;
+  } else {
+    uint16_t h;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(h) : "l"(static_cast<const uint16_t*>(s) + i));
+    return h;
+  }
+}
+template <typename S> __device__ __forceinline__ float of_raw(uint32_t r);
+template <> __device__ __forceinline__ float of_raw<float>(uint32_t r) { return __uint_as_float(r); }
+template <> __device__ __forceinline__ float of_raw<__half>(uint32_t r) {
+  return __half2float(__ushort_as_half((unsigned short)r));
+}
+template <> __device__ __forceinline__ float of_raw<__nv_bfloat16>(uint32_t r) { return __uint_as_float(r << 16); }
+__device__ __forceinline__ uint2 ld_stream8(const void* p) {
+  uint2 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
+
+template <typename S, int NT, bool two>
+__global__ void __launch_bounds__(32 * kColWarps, 1) q4_cols_kernel(const Q4Cols a) {
+  constexpr int kAhead = NT <= 2 ? 3 : 2;   // steps held in registers
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int kb = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  grid_dep_wait();
+  grid_dep_launch();
+  if (kb >= a.blocks) return;
   const int n = max(0, min(*a.count, a.cap));
-  const int share = ((n + a.split - 1) / a.split + 15) & ~15;
-  const int lo = min(n, rank * share), hi = min(n, lo + share);
-  const int halves = a.group == 64 ? 2 : 1;
+  const int all = (n + 15) >> 4, share = (all + gridDim.x - 1) / gridDim.x;
+  const int lo = min(all, (int)blockIdx.x * share), steps = min(all, lo + share) - lo;
+  const int g0 = two ? 2 * kb : kb, g1 = min(2 * kb + 1, a.groups - 1);
+  const uint8_t* q = a.q + (size_t)kb * kBlockBytes + 8 * g;
   float acc[2][4][NT][4];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
@@ -365,140 +391,112 @@ __global__ void __launch_bounds__(kThreads) q4_cols_kernel(const Q4Cols a) {
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[s][i][t][r] = 0.f;
-  bool waited = false;
-  const int gi0 = halves == 2 ? 2 * kb : kb, gi1 = halves == 2 ? min(2 * kb + 1, a.groups - 1) : kb;
-  for (int c0 = lo; c0 < hi; c0 += kListed) {
-    const int m = min(kListed, hi - c0);
-    __syncthreads();
-    for (int e = tid; e < ((m + 15) & ~15); e += kThreads) {
-      const int j = e < m ? a.list[c0 + e] : -1;
-      id[e] = j >= 0 && j < a.N ? j : -1;   // (reported, and given activation 0, by the first product)
+  uint2 w[kAhead][4];
+  uint32_t sc[kAhead][two ? 2 : 1][4];
+  float v[kAhead][NT][4];
+  // rows, scales and activations of step s (behind the list, and for entries outside,
+  // which have activation 0 from the first product on, another row is read)
+  const auto fetch = [&](int k, int s) {
+    const int e = (lo + s) * 16 + 4 * c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int l = a.list[min(e + i, n - 1)];
+      const size_t j = l >= 0 && l < a.N ? l : 0;
+      w[k][i] = ld_stream8(q + j * a.pitch);
+      sc[k][0][i] = ld_raw<S>(a.scale, j * a.groups + g0);
+      if (two) sc[k][two][i] = ld_raw<S>(a.scale, j * a.groups + g1);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        v[k][t][i] = __ldcg(a.act + (size_t)min(8 * t + g, a.B - 1) * a.ld_act + min(e + i, n - 1));
     }
-    __syncthreads();
-    for (int e0 = wid * 16; e0 < m; e0 += kWarps * 16 * kSteps) {
-      uint2 w[kSteps][4];
-      float sc[kSteps][2][4];
+  };
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const int e = e0 + k * kWarps * 16 + 4 * c;
+  for (int k = 0; k < kAhead; ++k)
+    if (k < steps) fetch(k, k);
+  for (int s0 = 0; s0 < steps; s0 += kAhead) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = e < m ? id[e + i] : -1;
-          w[k][i] = make_uint2(0, 0);
-          sc[k][0][i] = sc[k][1][i] = 0.f;
-          if (j >= 0) {
-            w[k][i] = __ldg(reinterpret_cast<const uint2*>(a.q + (size_t)j * a.pitch + (size_t)kb * kBlockBytes + 8 * g));
-            sc[k][0][i] = ld_scale<S>(a.scale, (size_t)j * a.groups + gi0);
-            sc[k][1][i] = halves == 2 ? ld_scale<S>(a.scale, (size_t)j * a.groups + gi1) : sc[k][0][i];
-          }
-        }
-      }
-      if (!waited) {
-        grid_dep_wait();   // the activations
-        grid_dep_launch();
-        waited = true;
-      }
+    for (int k = 0; k < kAhead; ++k) {
+      if (s0 + k >= steps) break;
+      const int e = (lo + s0 + k) * 16 + 4 * c;
+      // coefficients of this lane's four rows in its columns: [half][piece][pair]
+      uint32_t cf[NT][two ? 2 : 1][3][2];
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const int e = e0 + k * kWarps * 16 + 4 * c;
-        if (e0 + k * kWarps * 16 >= m) break;
-        // coefficients of this lane's four rows in its column(s): [half][piece][pair]
-        uint32_t cf[NT][2][3][2];
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int b = kCols ? g % a.B : 8 * t + g;
-          float v[4];
+        for (int h = 0; h < (two ? 2 : 1); ++h) {
+          __nv_bfloat16 p[4][3];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = (kCols ? g < 3 * a.B : b < a.B) && e + i < m ? __ldcg(a.act + (size_t)b * a.ld_act + c0 + e + i) : 0.f;
+          for (int i = 0; i < 4; ++i)   // (0 adds nothing, whatever the row holds; behind the list nothing counts)
+            pieces3(v[k][t][i] == 0.f || e + i >= n ? 0.f : v[k][t][i] * of_raw<S>(sc[k][h][i]), p[i]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == 1 && halves == 1) break;
-            __nv_bfloat16 p[4][3];
+          for (int z = 0; z < 3; ++z)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) pieces3(v[i] == 0.f ? 0.f : v[i] * sc[k][h][i], p[i]);   // (0 adds nothing, whatever the row holds)
-#pragma unroll
-            for (int q = 0; q < 3; ++q)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                __nv_bfloat162 two;
-                if (kCols) {
-                  const int mine = g / a.B;
-                  two.x = mine == 0 ? p[2 * i][0] : mine == 1 ? p[2 * i][1] : p[2 * i][2];
-                  two.y = mine == 0 ? p[2 * i + 1][0] : mine == 1 ? p[2 * i + 1][1] : p[2 * i + 1][2];
-                } else {
-                  two.x = p[2 * i][q];
-                  two.y = p[2 * i + 1][q];
-                }
-                cf[t][h][q][i] = *reinterpret_cast<uint32_t*>(&two);
-              }
-          }
+            for (int i = 0; i < 2; ++i) {
+              __nv_bfloat162 pair;
+              pair.x = p[2 * i][z];
+              pair.y = p[2 * i + 1][z];
+              cf[t][h][z][i] = *reinterpret_cast<uint32_t*>(&pair);
+            }
         }
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const uint32_t r0 = s ? w[k][0].y : w[k][0].x, r1 = s ? w[k][1].y : w[k][1].x;
-          const uint32_t r2 = s ? w[k][2].y : w[k][2].x, r3 = s ? w[k][3].y : w[k][3].x;
-          // elements 2 i of two rows side by side, and elements 2 i + 1
-          uint32_t ev0[4], ev1[4], od0[4], od1[4];
-          Pairs<__nv_bfloat16>::open(__byte_perm(r0, r1, 0x5410), ev0);
-          Pairs<__nv_bfloat16>::open(__byte_perm(r0, r1, 0x7632), od0);
-          Pairs<__nv_bfloat16>::open(__byte_perm(r2, r3, 0x5410), ev1);
-          Pairs<__nv_bfloat16>::open(__byte_perm(r2, r3, 0x7632), od1);
-          const int h = halves == 2 ? s : 0;
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t r0 = s ? w[k][0].y : w[k][0].x, r1 = s ? w[k][1].y : w[k][1].x;
+        const uint32_t r2 = s ? w[k][2].y : w[k][2].x, r3 = s ? w[k][3].y : w[k][3].x;
+        // elements 2 i of two rows side by side, and elements 2 i + 1
+        uint32_t ev0[4], ev1[4], od0[4], od1[4];
+        Pairs<__nv_bfloat16>::open(__byte_perm(r0, r1, 0x5410), ev0);
+        Pairs<__nv_bfloat16>::open(__byte_perm(r0, r1, 0x7632), od0);
+        Pairs<__nv_bfloat16>::open(__byte_perm(r2, r3, 0x5410), ev1);
+        Pairs<__nv_bfloat16>::open(__byte_perm(r2, r3, 0x7632), od1);
+#pragma unroll
+        for (int z = 0; z < 3; ++z)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-#pragma unroll
-              for (int q = 0; q < (kCols ? 1 : 3); ++q) {
-                const uint32_t b0 = h ? cf[t][1][q][0] : cf[t][0][q][0], b1 = h ? cf[t][1][q][1] : cf[t][0][q][1];
-                mma16816<__nv_bfloat16>(acc[s][i][t], ev0[i], od0[i], ev1[i], od1[i], b0, b1);
-              }
+              const uint32_t* x = cf[t][two && s][z];
+              mma16816<__nv_bfloat16>(acc[s][i][t], ev0[i], od0[i], ev1[i], od1[i], x[0], x[1]);
             }
-        }
       }
+      if (s0 + k + kAhead < steps) fetch(k, s0 + k + kAhead);
     }
   }
-  if (!waited) {
-    grid_dep_wait();
-    grid_dep_launch();
-  }
-  // sums of the warps, warp by warp, then of the cluster's CTAs: a fixed order
-  const int cols = kCols ? 3 * a.B : a.B, ld = cols | 1;
-  for (int w = 0; w < kWarps; ++w) {
-    __syncthreads();
-    if (wid != w) continue;
+  // [share][vector][element]
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int lo8 = 0; lo8 < 2; ++lo8) {
+      const int b = 8 * t + 2 * c + lo8;
+      if (b >= a.B) continue;
+      float* part = a.part + (((size_t)blockIdx.x * a.B + b) * a.blocks + kb) * 128 + 8 * g;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int col = 8 * t + 2 * c + (r & 1), at = 64 * s + 8 * g + 2 * i + (r >> 1);
-            if (col < cols) red[at * ld + col] = w ? red[at * ld + col] + acc[s][i][t][r] : acc[s][i][t][r];
-          }
-  }
+      for (int s = 0; s < 2; ++s) {
+        float4* to = reinterpret_cast<float4*>(part + 64 * s);
+        to[0] = make_float4(acc[s][0][t][lo8], acc[s][0][t][2 + lo8], acc[s][1][t][lo8], acc[s][1][t][2 + lo8]);
+        to[1] = make_float4(acc[s][2][t][lo8], acc[s][2][t][2 + lo8], acc[s][3][t][lo8], acc[s][3][t][2 + lo8]);
+      }
+    }
+}
+
+// out[b][t] (+)= the sum over the shares, [share][vector][ld]: 32 elements a CTA, eight warps
+// that take every eighth share, in a fixed order.
+__global__ void __launch_bounds__(256) q4_join_kernel(const float* __restrict__ part, int parts, int ld, int d,
+                                                     float* __restrict__ out, int accumulate) {
+  __shared__ float red[8][32];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, b = blockIdx.y, t = blockIdx.x * 32 + lane;
+  grid_dep_wait();
+  grid_dep_launch();
+  float sum = 0.f;
+#pragma unroll 10
+  for (int r = wid; r < parts; r += 8) sum += __ldcg(part + ((size_t)r * gridDim.y + b) * ld + t);   // (ld: whole blocks)
+  red[wid][lane] = sum;
   __syncthreads();
-  if (a.split > 1) {
-    cluster_arrive();
-    cluster_wait();
-  }
-  const int mine = 128 / a.split;   // elements that this CTA joins and writes
-  for (int i = tid; i < mine * a.B; i += kThreads) {
-    const int t = rank * mine + i % mine, b = i / mine;
-    if (kb * 128 + t >= a.d) continue;
-    float sum = 0.f;
-    for (int col = b; col < cols; col += a.B)
-      for (int r = 0; r < a.split; ++r) sum += a.split > 1 ? ld_dsmem_f32(red + t * ld + col, r) : red[t * ld + col];
-    float* o = a.out + (size_t)b * a.d + kb * 128 + t;
-    *o = a.accumulate ? *o + sum : sum;
-  }
-  if (a.split > 1) {   // no CTA leaves while its shared memory is read
-    cluster_arrive();
-    cluster_wait();
-  }
+  if (wid != 0 || t >= d) return;
+  sum = red[0][lane];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) sum += red[k][lane];
+  float* o = out + (size_t)b * d + t;
+  *o = accumulate ? *o + sum : sum;
 }
 
 template <typename S, typename P, int NT>
@@ -551,22 +549,46 @@ cudaError_t launch_rows(Q4Rows a, const void* y, void* pieces, dv_dtype dt, bool
                       : run_rows_nt<__nv_bfloat16, __nv_bfloat16>(a, pdl, stream);
 }
 
-template <typename S, int NT, bool kCols>
+// Shares of the list: CTAs for every SM, 16 listed rows each at least.
+int col_shares(const Q4Cols& a, int per_share, int slabs, int ctas) {
+  const int most = (a.cap + per_share - 1) / per_share;
+  int n = ctas / slabs;
+  n = n < 1 ? 1 : n;
+  return n < most ? n : most;
+}
+
+template <typename S, int NT, bool two>
 cudaError_t run_cols(const Q4Cols& a, cudaStream_t stream) {
-  const int cols = kCols ? 3 * a.B : a.B;
-  const size_t smem = (size_t)128 * (cols | 1) * sizeof(float);
-  return launch_k(q4_cols_kernel<S, NT, kCols>, dim3((a.d + 127) / 128 * a.split), dim3(kThreads), smem, stream, true,
-                  a.split, a);
+  const int slabs = (a.blocks + kColWarps - 1) / kColWarps, warps = (a.blocks + slabs - 1) / slabs;
+  const int shares = col_shares(a, 16, slabs, kQ4Splits);
+  const cudaError_t e = launch_k(q4_cols_kernel<S, NT, two>, dim3(shares, slabs), dim3(32 * warps), 0, stream, true, 1, a);
+  return e == cudaSuccess ? launch_q4_join(a, shares, stream) : e;
+}
+template <typename S, bool two>
+cudaError_t run_cols_nt(const Q4Cols& a, cudaStream_t stream) {
+  if (a.B <= 8) return run_cols<S, 1, two>(a, stream);
+  if (a.B <= 16) return run_cols<S, 2, two>(a, stream);
+  return run_cols<S, 4, two>(a, stream);
 }
 template <typename S>
-cudaError_t run_cols_nt(const Q4Cols& a, cudaStream_t stream) {
-  if (3 * a.B <= 8) return run_cols<S, 1, true>(a, stream);
-  if (a.B <= 8) return run_cols<S, 1, false>(a, stream);
-  if (a.B <= 16) return run_cols<S, 2, false>(a, stream);
-  return run_cols<S, 4, false>(a, stream);
+cudaError_t run_cols_group(const Q4Cols& a, cudaStream_t stream) {
+  return a.group == 64 ? run_cols_nt<S, true>(a, stream) : run_cols_nt<S, false>(a, stream);
 }
 
 }  // namespace
+
+cudaError_t launch_q4_join(const Q4Cols& a, int shares, cudaStream_t stream) {
+  return launch_k(q4_join_kernel, dim3((a.d + 31) / 32, a.B), dim3(256), 0, stream, true, 1, (const float*)a.part, shares,
+                  a.blocks * 128, a.d, a.out, a.accumulate);
+}
+
+size_t q4_part_floats(int B, int d) {
+  // shares of one vector's lists (k_q4_vec.cu), or B vectors' shares times slabs of
+  // eight blocks
+  const size_t blocks = (size_t)(d + 127) / 128;
+  const size_t one = kQ4Splits * blocks * 128, many = (kQ4Splits * kColWarps + blocks) * 128 * (size_t)B;
+  return many > one ? many : one;
+}
 
 cudaError_t launch_q4_quantize(const void* W, int N, int d, dv_dtype dt, int group, void* q, void* scale, void* values,
                                int num_sms, cudaStream_t stream) {
@@ -617,12 +639,12 @@ cudaError_t launch_q4_sparse_mlp(const Q4MlpLaunch& L, dv_dtype dt, WsHeader* hd
   const int blocks = (L.d + 127) / 128;
   c.pitch = (size_t)blocks * kBlockBytes;
   c.groups = (L.d + L.group2 - 1) / L.group2;
+  c.blocks = blocks;
   if (L.B <= 2) return launch_q4_vec_cols(c, stream);
-  c.split = 8;
   switch (dt) {
-    case DV_F32: return run_cols_nt<float>(c, stream);
-    case DV_F16: return run_cols_nt<__half>(c, stream);
-    case DV_BF16: return run_cols_nt<__nv_bfloat16>(c, stream);
+    case DV_F32: return run_cols_group<float>(c, stream);
+    case DV_F16: return run_cols_group<__half>(c, stream);
+    case DV_BF16: return run_cols_group<__nv_bfloat16>(c, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -495,26 +495,6 @@ __global__ void __launch_bounds__(kColThreads, 1) q4_vec_cols_kernel(const Q4Col
   }
 }
 
-// out[t] (+)= the sum over the CTAs of the kernel before: 32 elements a CTA, eight shares
-// of the sums, in a fixed order.
-__global__ void __launch_bounds__(256) q4_vec_join_kernel(const float* __restrict__ part, int parts, int ld, int d,
-                                                         float* __restrict__ out, int accumulate) {
-  __shared__ float red[8][32];
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, t = blockIdx.x * 32 + lane;
-  grid_dep_wait();
-  grid_dep_launch();
-  float sum = 0.f;
-#pragma unroll 8
-  for (int r = wid; r < parts; r += 8) sum += __ldcg(part + (size_t)r * ld + t);   // (ld is a multiple of 128)
-  red[wid][lane] = sum;
-  __syncthreads();
-  if (wid != 0 || t >= d) return;
-  sum = red[0][lane];
-#pragma unroll
-  for (int k = 1; k < 8; ++k) sum += red[k][lane];
-  out[t] = accumulate ? out[t] + sum : sum;
-}
-
 // ---- launches ------------------------------------------------------------------------------
 
 template <typename S, int B, int kRows, int kAhead, bool kList, bool two>
@@ -559,19 +539,18 @@ cudaError_t run_cols(const Q4Cols& all, int num_sms, cudaStream_t stream) {
   });
   if (ea != cudaSuccess) return ea;
   Q4Cols a = all;
-  a.blocks = (a.d + 127) / 128;
   // a thread to two words; rows of more than 8192 elements in equal slabs of whole blocks
   const int slabs = (a.blocks * 8 + kColThreads - 1) / kColThreads;
   const int threads = ((a.blocks + slabs - 1) / slabs * 8 + 31) / 32 * 32;
-  const int quads = (a.cap + 3) / 4;
-  int splits = num_sms < kQ4Splits ? num_sms : kQ4Splits;
-  splits = splits / slabs > 0 ? splits / slabs : 1;
-  if (splits > quads) splits = quads;
+  // shares: a CTA for every SM, of four steps each at least (1024 rows: the second kernel
+  // then has 64 sums to add)
+  const int most = (a.cap + 15) / 16;
+  int shares = (num_sms < kQ4Splits ? num_sms : kQ4Splits) / slabs;
+  shares = shares < 1 ? 1 : shares > most ? most : shares;
+  a.B = 1;
   for (int b = 0; b < all.B; ++b) {
-    cudaError_t e = launch_k(q4_vec_cols_kernel<two>, dim3(splits, slabs), dim3(threads), kStaged * 16, stream, true, 1, a);
-    if (e != cudaSuccess) return e;
-    e = launch_k(q4_vec_join_kernel, dim3((a.d + 31) / 32), dim3(256), 0, stream, true, 1, (const float*)a.part, splits,
-                 a.blocks * 128, a.d, a.out, a.accumulate);
+    cudaError_t e = launch_k(q4_vec_cols_kernel<two>, dim3(shares, slabs), dim3(threads), kStaged * 16, stream, true, 1, a);
+    if (e == cudaSuccess) e = launch_q4_join(a, shares, stream);
     if (e != cudaSuccess) return e;
     a.act += a.ld_act;
     a.out += a.d;
