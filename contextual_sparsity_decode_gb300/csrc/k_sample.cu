@@ -3,7 +3,7 @@
 // the tokens that have min_p of the best one's probability.
 //
 // Weights are integers, w(x) = 2^39 exp((x - max) / T) rounded, from arithmetic
-// that is exact to 2^-31 of the weight: sums of them are exact whatever their order, so that
+// that is exact to 2^-30 of the weight: sums of them are exact whatever their order, so that
 // the cut and the token are those of the definition unless u (or p) is within
 // about 1e-10 of a border, and results do not depend on how a row is split.
 // (With sums of 32-bit exponentials, 1e-6 off, one row in ten of a large
@@ -46,11 +46,12 @@ constexpr int kUnit = 39;                  // a weight of 1 is 2^39
 constexpr float kReach = 28.5f;            // exp(-28.5) 2^39 < 1/4: nothing below weighs anything
 constexpr float kCold = 1e-30f, kHot = 1e30f;
 constexpr long long kUnwindNs = 2000000000LL;
-static_assert(kThreads == 256 && kList == 256, "a thread per table entry and per listed token");
+static_assert(kList == kThreads, "a thread to a listed token");
 
-// 2^(39 + j / 256), rounded, from square roots of 2.
+// 2^(31 + j / 512), rounded, from square roots of 2.
+constexpr int kPowerCount = 512;
 struct Powers {
-  u64 v[256];
+  uint32_t v[kPowerCount];
 };
 constexpr double root_of(double a) {
   double x = 1.0 + (a - 1.0) / 2;
@@ -59,14 +60,14 @@ constexpr double root_of(double a) {
 }
 constexpr Powers make_powers() {
   Powers p{};
-  double root[8] = {};                     // 2^(1/2), 2^(1/4), ...
+  double root[9] = {};                     // 2^(1/2), 2^(1/4), ...
   double a = 2.0;
-  for (int i = 0; i < 8; ++i) root[i] = a = root_of(a);
-  for (int j = 0; j < 256; ++j) {
-    double x = 549755813888.0;             // 2^39
-    for (int i = 0; i < 8; ++i)
-      if (j >> (7 - i) & 1) x *= root[i];
-    p.v[j] = (u64)(x + 0.5);
+  for (int i = 0; i < 9; ++i) root[i] = a = root_of(a);
+  for (int j = 0; j < kPowerCount; ++j) {
+    double x = 2147483648.0;               // 2^31
+    for (int i = 0; i < 9; ++i)
+      if (j >> (8 - i) & 1) x *= root[i];
+    p.v[j] = (uint32_t)(x + 0.5);
   }
   return p;
 }
@@ -81,32 +82,71 @@ __device__ __forceinline__ float unord32(uint32_t o) {
 }
 
 // The weight of x below the maximum m: y = (x - m) log2(e) / T as the sum of two
-// floats (exact difference, product with log2(e) / T in two floats), 2^y as a
-// table entry times 1 + z, |z| < 2^-9.5, and a shift.
+// floats (exact difference, product with log2(e) / T in two floats), 2^y as a 32-bit
+// table entry times 1 + z, |z| < 2^-10.5, and a shift.
 struct Scale {
   float m, hi, lo;   // hi + lo = log2(e) / T
-  const u64* table;
-  __device__ __forceinline__ u64 operator()(float x) const {
+  const uint32_t* table;
+  // 2^31 times the mantissa of the weight, in [1, 2) but for rounding, and its shift
+  __device__ __forceinline__ uint32_t mantissa(float x, int* shift, float* at) const {
     const float d = __fsub_rn(x, m), b = __fsub_rn(d, x);
     const float e = __fadd_rn(__fsub_rn(x, __fsub_rn(d, b)), __fsub_rn(-m, b));   // x - m = d + e
     const float y = __fmul_rn(d, hi);
     const float below = __fmaf_rn(d, lo, __fmaf_rn(e, hi, __fmaf_rn(d, hi, -y)));
-    constexpr float kMagic = 49152.f;               // 1.5 2^15: sums are multiples of 2^-8
-    const float t = __fadd_rn(fmaxf(y, -60.f), kMagic);
-    const int k = __float_as_int(t) - __float_as_int(kMagic);   // y = k / 256 + r, |r| <= 2^-9
+    constexpr float kMagic = 24576.f;               // 1.5 2^14: sums are multiples of 2^-9
+    const float t = __fadd_rn(fmaxf(y, -41.f), kMagic);
+    const int k = __float_as_int(t) - __float_as_int(kMagic);   // y = k / 512 + r, |r| <= 2^-10
     const float r = __fsub_rn(y, __fsub_rn(t, kMagic));
     const float q = __fmul_rn(r, 0.69314718056f);
     const float s = __fmul_rn(__fmul_rn(q, q), __fmaf_rn(q, __fmaf_rn(q, 1.f / 24, 1.f / 6), 0.5f));
-    // r ln 2 in one product and the rest of it with the small terms: 2^-24 of 2^-9.5
+    // r ln 2 in one product and the rest of it with the small terms: 2^-24 of 2^-10.5
     const float z = __fmaf_rn(r, 0.69314718056f, __fmaf_rn(below, 0.69314718056f, __fmaf_rn(r, -1.9046542e-9f, s)));
-    const u64 base = table[k & 255];
-    const float near = __uint_as_float(0x3f800000u | ((uint32_t)(base >> 16) & 0x007fffffu));   // 2^(j/256)
-    const u64 w = base + (u64)(long long)__float2int_rn(__fmul_rn(z, __fmul_rn(near, 549755813888.f)));
-    const int shift = -(k >> 8);
-    const u64 out = (w + ((1ull << shift) >> 1)) >> shift;
-    return y > -40.5f ? out : 0;                    // (NaN: x is -inf, or so far below that y is)
+    const uint32_t base = table[k & (kPowerCount - 1)];
+    const float near = __uint_as_float(0x3f800000u | ((base >> 8) & 0x007fffffu));   // 2^(j/512)
+    // base (1 + z) as a whole number below 2^32 (the product, below 2^22, becomes one by 1.5 2^23)
+    constexpr float kWhole = 12582912.f;
+    const float zi = __fmaf_rn(__fmul_rn(z, 2147483648.f), near, kWhole);
+    const uint32_t w = base + (uint32_t)(__float_as_int(zi) - __float_as_int(kWhole));
+    *shift = -(k >> 9);
+    *at = y;
+    return w;
+  }
+  __device__ __forceinline__ u64 operator()(float x) const {
+    int shift;
+    float y;
+    const uint32_t w = mantissa(x, &shift, &y);
+    // w 2^8 >> shift, rounded
+    const u64 out = shift > 8 ? (u64)(((w >> min(shift - 9, 31)) + 1) >> 1) : (u64)w << (8 - shift);
+    return y >= -40.f ? out : 0;                    // (NaN: x is -inf, or so far below that y is)
+  }
+  // Nothing below this weighs `least` or more (1e-4 to the safe side).
+  __device__ __forceinline__ float floor_of(u64 least) const {
+    if (least == 0) return -INFINITY;
+    const float y = log2f(__ull2float_rn(least)) - (kUnit + 1e-3f);   // < 0
+    return m + (y * 1.0001f / hi - fabsf(m) * 1e-6f);
   }
 };
+
+// v f in whole numbers, f in [0, 1), rounded up or down: exact (double precision is slow
+// on this GPU: with targets, log2(e) / T and floors in it, by every thread, 192 rows
+// of 128001 took 310 us).
+__device__ __forceinline__ u64 times(u64 v, float f, bool up) {
+  if (!(f > 0.f)) return 0;
+  const uint32_t bits = __float_as_uint(f);
+  const int e = bits >> 23;
+  const uint32_t mant = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;   // f = mant 2^-shift
+  const int shift = 150 - (e ? e : 1);                                            // 24 to 149
+  const u64 lo = v * mant, hi = __umul64hi(v, mant);                              // hi below 2^24
+  u64 out, rest;
+  if (shift < 64) {
+    out = (hi << (64 - shift)) | (lo >> shift);
+    rest = lo << (64 - shift);
+  } else {
+    out = shift < 128 ? hi >> (shift - 64) : 0;
+    rest = lo | (shift < 128 ? hi & ((1ull << (shift - 64)) - 1) : hi);
+  }
+  return out + (up && rest ? 1 : 0);
+}
 
 // Where the order (x descending, then index) is cut: kept are tokens before and
 // at (key, index).
@@ -117,7 +157,7 @@ struct Cut {
 };
 
 struct Shared {
-  u64 table[256];
+  uint32_t table[kPowerCount];
   u64 group[kMaxGroups];       // sums of 32 vectors
   u64 box[2][kMaxCluster][2];  // what the cluster's CTAs tell each other
   u64 answer[2][2];            // what one of them tells all
@@ -125,6 +165,8 @@ struct Shared {
   u64 weight[kList], sorted[kList];
   u64 bins[kBins];
   uint32_t count[kBins], carry[kBins];
+  float dense[kWarps][256];    // a group's tokens that a pass looks at, and their places in it
+  uint8_t place[kWarps][256];
   u64 scan[kWarps];
   float redm[kWarps];
   int redi[kWarps];
@@ -209,18 +251,58 @@ struct Row {
     cluster_sync();
     return t;
   }
-  // f(key, index, x) of every token of the CTA above -inf
+  static __device__ __forceinline__ float largest(const float* x) {
+    float m = x[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) m = fmaxf(m, x[e]);
+    return m;
+  }
+  // Tokens of group g (of 32 vectors) above -inf and not below `floor`, side by side in the
+  // warp's buffer; returns their number.  What is done with a token costs 40 instructions,
+  // and a nucleus holds few of a group's: done where they are, every warp would run
+  // them for all.
+  __device__ __forceinline__ int pack(int g, float floor) const {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, v = g * 32 + lane;
+    float x[E];
+    const bool in = v < vecs;
+    if (in) open(v, x);
+    if (!__any_sync(0xffffffffu, in && largest(x) >= floor)) return 0;
+    int n = 0;
+    __syncwarp();   // (the buffer's last readers)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bool take = in && x[e] >= floor && x[e] > -INFINITY;
+      const uint32_t hit = __ballot_sync(0xffffffffu, take);
+      if (take) {
+        const int at = n + __popc(hit & ((1u << lane) - 1));
+        sh.dense[wid][at] = x[e];
+        sh.place[wid][at] = (uint8_t)(lane * E + e);
+      }
+      n += __popc(hit);
+    }
+    __syncwarp();
+    return n;
+  }
+  // f(x, index) of every token of the CTA above -inf and not below `floor`
   template <typename F>
-  __device__ __forceinline__ void each(F f) const {
+  __device__ __forceinline__ void each(float floor, F f) const {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    for (int g = wid; g * 32 < vecs; g += kWarps) {
+      const int n = pack(g, floor);
+      for (int i = lane; i < n; i += 32) f(sh.dense[wid][i], (v0 + g * 32) * E + sh.place[wid][i]);
+    }
+  }
+  // The same where nearly all tokens count and little is done with them.
+  template <typename F>
+  __device__ __forceinline__ void each_of_all(F f) const {
     for (int v = threadIdx.x; v < vecs; v += kThreads) {
       float x[E];
       open(v, x);
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (x[e] > -INFINITY) f(x[e], (v0 + v) * E + e);
+        if (x[e] > -INFINITY) f(x[e]);
     }
   }
-
   // The bin that holds the `target`-th unit (of count or weight) of the
   // histogram that all CTAs have filled: returns it, with what is before it and in
   // it; kBins if there is less in all.  kMass: the sums are count + 2^32 carry.
@@ -281,8 +363,8 @@ struct Row {
   // Tokens that `take` into every CTA's list, their number into the first CTA's
   // `listed`, which has been cleared, and a cluster barrier passed since.
   template <typename F>
-  __device__ __forceinline__ void gather(F take) {
-    each([&](float x, int i) {
+  __device__ __forceinline__ void gather(float floor, F take) {
+    each(floor, [&](float x, int i) {
       if (!take(x, i)) return;
       const uint32_t at = add_remote(&sh.listed, 0, 1);
       if (at < (uint32_t)kList)
@@ -322,9 +404,10 @@ template <bool kMass, typename T>
 __device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut have, u64 target, float step,
                                         u64 floor_weight, int b1, u64 before, u64 inside) {
   Shared& sh = row.sh;
+  const float least_x = fmaxf(kMass ? weigh.floor_of(floor_weight) : -INFINITY, have.key ? unord32(have.key) : -INFINITY);
   if (b1 < 0) {
     row.clear_bins();
-    row.each([&](float x, int i) {
+    row.each(least_x, [&](float x, int i) {
       const uint32_t b = __float2uint_rz((weigh.m - x) * step);
       if (b >= (uint32_t)kBins || !have.keeps(ord32(x), i)) return;
       u64 w = 0;
@@ -342,17 +425,18 @@ __device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut hav
   const float low = fmaxf(weigh.m - (float)(b1 + 2) / step, -FLT_MAX);
   uint32_t khi = ord32(fminf(top, weigh.m)), klo = ord32(low);
   uint32_t done_lo = 0, done_hi = 0xffffffffu;   // refined: keys within
-  for (;;) {
-    const auto within = [&](float x, uint32_t k) {
-      return k >= done_lo && k <= done_hi && __float2uint_rz((weigh.m - x) * step) == (uint32_t)b1;
-    };
+  const float low_x = fmaxf(low, least_x);
+  const auto within = [&](float x, uint32_t k) {
+    return k >= done_lo && k <= done_hi && __float2uint_rz((weigh.m - x) * step) == (uint32_t)b1;
+  };
+  for (bool exact = false;; exact = true) {
     // how many tokens are left, at most: their weight over the least of them
     const u64 least = kMass ? weigh(unord32(max(klo, done_lo))) : 1;
     const bool few = least > 0 && inside <= (u64)kList * least;
     if (few) {
       if (threadIdx.x == 0) sh.listed = 0;
       cluster_sync();
-      row.gather([&](float x, int i) {
+      row.gather(low_x, [&](float x, int i) {
         return within(x, ord32(x)) && have.keeps(ord32(x), i) && (!kMass || weigh(x) >= floor_weight);
       });
       // (no CTA ends before the cluster's next barrier: the draw has one)
@@ -370,11 +454,37 @@ __device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut hav
       __syncthreads();
       return Cut{(uint32_t)(last >> 32), (int)~(uint32_t)last};
     }
+    if (!exact) {   // the bin's own keys: often one (16-bit logits)
+      uint32_t k0 = 0xffffffffu, k1 = 0;
+      row.each(low_x, [&](float x, int i) {
+        const uint32_t k = ord32(x);
+        if (!within(x, k) || !have.keeps(k, i)) return;
+        k0 = min(k0, k);
+        k1 = max(k1, k);
+      });
+      k0 = __reduce_min_sync(0xffffffffu, k0);
+      k1 = __reduce_max_sync(0xffffffffu, k1);
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) sh.scan[threadIdx.x >> 5] = ((u64)k0 << 32) | k1;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        k0 = min(k0, (uint32_t)(sh.scan[w] >> 32));
+        k1 = max(k1, (uint32_t)sh.scan[w]);
+      }
+      const int t = row.exchange(k0, k1);
+      for (uint32_t r = 0; r < row.size; ++r) {
+        k0 = min(k0, (uint32_t)sh.box[t][r][0]);
+        k1 = max(k1, (uint32_t)sh.box[t][r][1]);
+      }
+      klo = k0;   // (the bin holds tokens)
+      khi = k1;
+    }
     if (klo == khi) break;   // one value
     int shift = 0;
     while ((khi - klo) >> shift >= (uint32_t)kBins) ++shift;
     row.clear_bins();
-    row.each([&](float x, int i) {
+    row.each(low_x, [&](float x, int i) {
       const uint32_t k = ord32(x);
       if (!within(x, k) || !have.keeps(k, i)) return;
       u64 w = 0;
@@ -399,6 +509,7 @@ __device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut hav
   // equal values: the first r of them, by index
   const u64 one = kMass ? weigh(unord32(klo)) : 1;
   const u64 r = (target - before + one - 1) / one;
+  const float value = unord32(klo);
   u64 here = 0, total;
   // (index order: a warp to a group of 32 vectors, as in the draw)
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, groups = (row.vecs + 31) / 32;
@@ -410,7 +521,7 @@ __device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut hav
       row.open(v, x);
 #pragma unroll
       for (int e = 0; e < Row<T>::E; ++e)
-        n += x[e] > -INFINITY && ord32(x[e]) == klo && have.keeps(klo, (row.v0 + v) * Row<T>::E + e);
+        n += x[e] == value && have.keeps(klo, (row.v0 + v) * Row<T>::E + e);
     }
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) sh.group[g] = n;
@@ -433,7 +544,7 @@ __device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut hav
       row.open(v, x);
 #pragma unroll
       for (int e = 0; e < Row<T>::E; ++e)
-        if (x[e] > -INFINITY && ord32(x[e]) == klo && have.keeps(klo, (row.v0 + v) * Row<T>::E + e)) bits |= 1u << e;
+        if (x[e] == value && have.keeps(klo, (row.v0 + v) * Row<T>::E + e)) bits |= 1u << e;
     }
     n = __popc(bits);
     uint32_t upto = n;
@@ -463,7 +574,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a) 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t rank = blockIdx.x % a.split;
   const int b = blockIdx.x / a.split;
-  sh.table[tid] = kPowers.v[tid];
+  for (int i = tid; i < kPowerCount; i += kThreads) sh.table[i] = kPowers.v[i];
   if (tid == 0) {
     for (int q = 0; q < kChunks; ++q) tc::mbar_init(&sh.full[q], 1);
     tc::fence_mbar_init();
@@ -562,7 +673,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a) 
 
   if (temp == 0.f) {   // the best token, the first of equal ones
     int first = INT_MAX;
-    row.each([&](float x, int i) {
+    row.each(m, [&](float x, int i) {
       if (x == m) first = min(first, i);
     });
     first = __reduce_min_sync(0xffffffffu, first);
@@ -581,28 +692,26 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a) 
   }
 
   Scale weigh;
-  {
-    const double c = 1.4426950408889634 / (double)temp;
-    weigh.m = m;
-    weigh.hi = (float)c;
-    weigh.lo = (float)(c - (double)weigh.hi);
-    weigh.table = sh.table;
-  }
+  weigh.m = m;
+  // log2(e) = 1.44269502 + 1.92596303e-8
+  weigh.hi = __fdiv_rn(1.44269502f, temp);
+  weigh.lo = __fdiv_rn(__fmaf_rn(-weigh.hi, temp, 1.44269502f) + 1.92596303e-8f, temp);
+  weigh.table = sh.table;
   const float step = (float)kBins / (kReach * temp);
-  const u64 unit = 1ull << kUnit;
-  const u64 least = min_p > 0.f ? (u64)ceil(fmin((double)min_p, 1.0) * (double)unit) : 0;
+  const u64 least = min_p > 0.f ? __float2ull_ru(fminf(min_p, 1.f) * (float)(1ull << kUnit)) : 0;
   const auto mass_target = [&](u64 mass) {   // tokens are kept while what is before them is below
-    return max((u64)ceil(fmax((double)p, 0.0) * (double)mass), (u64)1);
+    return max(times(mass, p, true), (u64)1);
   };
   const auto draw_target = [&](u64 mass) {   // the token whose sum is the first above
-    const double t = floor(fmax((double)u, 0.0) * (double)mass);
-    return t < (double)mass ? (u64)t : mass - 1;
+    return u < 1.f ? times(mass, u, false) : mass - 1;
   };
   const auto put = [&](float x, int i, u64 mass) {
     a.token[b] = i - off;
     if (a.prob) {
-      const double y = ((double)x - (double)m) / (double)temp;
-      a.prob[b] = (float)(exp(y) * (double)unit / (double)mass);
+      int shift;
+      float y;
+      const double w = (double)weigh.mantissa(x, &shift, &y) * __hiloint2double((1023 + kUnit - 31 - shift) << 20, 0);
+      a.prob[b] = (float)(w / (double)mass);
     }
   };
   Cut cut{0, INT_MAX};
@@ -611,7 +720,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a) 
   // ---- top k
   if (has_k) {
     row.clear_bins();
-    row.each([&](float x, int) {
+    row.each_of_all([&](float x) {
       const uint32_t bin = __float2uint_rz((m - x) * step);
       if (bin < (uint32_t)kBins) row.template add_bin<false>((int)bin, 0);
     });
@@ -619,7 +728,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a) 
     const int bin = row.template crossing<false>((u64)k, &before, &inside);
     if (bin < kBins && before + inside <= (u64)kList) {
       // the few best tokens: one CTA does the rest
-      row.gather([&](float x, int) { return __float2uint_rz((m - x) * step) <= (uint32_t)bin; });
+      row.gather(m - (float)(bin + 2) / step, [&](float x, int) { return __float2uint_rz((m - x) * step) <= (uint32_t)bin; });
       if (rank != 0) return;
       const int n = min((int)sh.listed, kList);
       u64 mine = 0, w = 0;
@@ -657,16 +766,24 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a) 
   const int groups = (vecs + 31) / 32;
   const auto sums = [&](u64 low, u64* total) {
     u64 mine = 0;
+    const float floor_x = fmaxf(weigh.floor_of(low), cut.key ? unord32(cut.key) : -INFINITY);
+    const bool every = floor_x == -INFINITY;
     for (int g = wid; g < groups; g += kWarps) {
-      const int v = g * 32 + lane;
       u64 w = 0;
-      if (v < vecs) {
-        float x[E];
-        row.open(v, x);
+      if (every) {
+        const int v = g * 32 + lane;
+        if (v < vecs) {
+          float x[E];
+          row.open(v, x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const u64 we = weigh(x[e]);
-          if (we >= low && cut.keeps(ord32(x[e]), (v0 + v) * E + e)) w += we;
+          for (int e = 0; e < E; ++e) w += weigh(x[e]);
+        }
+      } else {
+        const int n = row.pack(g, floor_x);
+        for (int i = lane; i < n; i += 32) {
+          const float x = sh.dense[wid][i];
+          const u64 we = weigh(x);
+          if (we >= low && cut.keeps(ord32(x), (v0 + g * 32) * E + sh.place[wid][i])) w += we;
         }
       }
       w = warp_sum_u64(w);
@@ -684,7 +801,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a) 
     int t = row.exchange(total, 0);
     for (uint32_t r = 0; r < row.size; ++r) mass += sh.box[t][r][0];
     // tokens below this weight add up to less than what is cut off, even all V of them
-    const u64 low = (u64)fmax(0.0, floor((1.0 - fmax((double)p, 0.0)) * (double)mass / (double)a.V) - 1.0);
+    const u64 low = __float2ull_rd(fmaxf((1.f - fmaxf(p, 0.f)) * 0.999f * __ull2float_rd(mass) / (float)a.V - 1.f, 0.f));
     cut = find_cut<true>(row, weigh, cut, mass_target(mass), step, low, -1, 0, 0);
   }
 

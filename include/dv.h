@@ -492,7 +492,7 @@ dv_status dv_sample_workspace_size(int B, int V, size_t* bytes);
  *     are never drawn.
  *  u [B] in [0, 1) (below counts as 0, above as just below 1); temperature,
  *     top_p, min_p [B] fp32, top_k [B] int32, each or NULL: 1, 1, 0, 0.
- * Weights are held to 2^-31 of themselves or 2^-40 (1 being the best token's)
+ * Weights are held to 2^-30 of themselves or 2^-40 (1 being the best token's)
  * and added without rounding: the token is the one of the formulas in exact
  * arithmetic unless u or top_p lies that near to a border.  Results repeat bit for
  * bit, whatever else is in the batch.

@@ -1,10 +1,10 @@
 """dv_sample against its definition in 64 bits, row by row.
 
-Tokens are equal.  (The kernel's weights are within 2^-31 of themselves or 2^-40,
+Tokens are equal.  (The kernel's weights are within 2^-30 of themselves or 2^-40,
 so a drawn u is on the other side of a border with a probability of about V times
 the error of a sum, below 1e-5 for every row here; borders are tested where all
 sums are exact.)  Probabilities: the chosen token's weight is taken in 64 bits and
-the sum of the others is within 2^-31 + V 2^-40 of its size, then one rounding to
+the sum of the others is within 2^-30 + V 2^-40 of its size, then one rounding to
 fp32: 2^-24 + 2^-30 + V 2^-40 relative."""
 
 import numpy as np
