@@ -287,3 +287,26 @@ def test_sparse_mlp_rows_keep_to_their_own_lists():
     out = torch.zeros(B, d, device="cuda")
     dv.dv_q4_sparse_mlp(y, W1, W2, idx.cuda(), cnt.cuda(), out, ws)
     assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_codes_beside_every_border(dt):
+    """Values at and next to (k + 1/2) s for scales of all kinds: the nearer code,
+    the even one in the middle."""
+    t, n = TORCH[dt], 64
+    scales = torch.tensor([1.0, 0.75, 3.3, 1e-3, 7e-4, 0.0199, 5e-6, 123.0, 1 / 3, 0.0625] +
+                          ([1e-30, 3e-32, 1e-38, 2e-41] if dt != "f16" else [6e-8, 3e-6]))
+    W = torch.zeros(len(scales), n, dtype=t)
+    for i, s in enumerate(scales):
+        top = (7 * s).to(t)
+        s = float((top.double() / 7).to(t))
+        v = torch.tensor([(k + 0.5) * s for k in range(-7, 7)], dtype=torch.float64).to(t)
+        up, down = torch.full_like(v, float("inf")), torch.full_like(v, float("-inf"))
+        near = torch.cat([v, torch.nextafter(v, up), torch.nextafter(v, down)])
+        W[i, 0], W[i, 1:1 + len(near)] = top, near
+        W[i] = torch.where(W[i].abs() > top, top, W[i])
+    Q = dv.Q4.of(W.cuda(), 64)
+    code, scale = plain_quantized(W, 64)
+    assert torch.equal(Q.scale.double().cpu(), scale)
+    assert np.array_equal(opened(Q.q, torch.ones_like(Q.scale), n, 64), code.numpy())
