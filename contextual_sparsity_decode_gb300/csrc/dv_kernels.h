@@ -363,8 +363,8 @@ struct Q4Rows {
   const void* y;                        // [B][d]
   int blocks, groups;                   // of a row
   size_t pitch;
-  // B > 2, set by the launcher: the vectors as columns of 16-bit values
-  const void* x; int cols, ldx, x_len, kw;
+  // k_q4.cu: the vectors as columns of 16-bit values
+  const void* x; int cols, ldx, x_len;
 };
 // Second kind: sums of listed rows.
 struct Q4Cols {

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) q4_quantize_kernel(const T* __restri
   const int groups = (d + group - 1) / group;
   // (whole warps take part in the exchanges below, also behind the last block; fewer than
   // 2^32 blocks: more would not fit the GPU, and 64-bit divisions took most of the time)
-  const uint32_t first = (blockIdx.x * kThreads + threadIdx.x) / 16, stride = gridDim.x * (kThreads / 16);
+  const uint32_t first = blockIdx.x * (kThreads / 16) + threadIdx.x / 16, stride = gridDim.x * (kThreads / 16);
   uint4 w[kItems][kVecs];
   uint32_t n_of[kItems];
   int t_of[kItems];
@@ -242,8 +242,9 @@ __global__ void __launch_bounds__(kThreads) q4_pieces_kernel(const float* __rest
   for (int k = 0; k < 3; ++k) x[((size_t)3 * b0 + k * rows + b - b0) * ld + t] = p[k];
 }
 
-// A CTA's eight warps are kRows row tiles of 16 by `kw` parts of the row's
-// blocks (part p takes blocks p, p + kw, ...).
+// A CTA takes 16 rows, its warp p the rows' blocks p, p + 8, ...  For what neither k_q4_vec.cu
+// nor k_q4_tc.cu takes: three and more 32-bit vectors, rows of less than 64 elements, and two
+// vectors of more than its shared memory holds.
 constexpr int kAhead = 4;   // blocks whose loads are issued before the first is used
 
 template <typename S, typename P, int NT, bool kList>
@@ -251,28 +252,15 @@ __global__ void __launch_bounds__(kThreads) q4_rows_kernel(const Q4Rows a) {
   __shared__ float red[kWarps][16][8 * NT + 1];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const int tiles = kWarps / a.kw, tile = wid / a.kw, part = wid % a.kw;
-  const int u0 = (blockIdx.x * tiles + tile) * 16;
-  // at level 1 of the launch policy the list, its count and the weights are read
-  // before the wait
-  if (!a.early) grid_dep_wait();
-  if (!a.early) grid_dep_launch();
+  const int u0 = blockIdx.x * 16;
+  grid_dep_wait();
+  grid_dep_launch();
   int row[2];
   const int n = kList ? max(0, min(*a.count, a.cap)) : a.N;
-  if (kList && blockIdx.x == 0 && tid == 0 && *a.count > a.cap) set_error(a.hdr, DV_ERR_CAPACITY, *a.count);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < 2; ++k) {   // (a list is a union: each of its rows once, and in range)
     const int u = u0 + g + 8 * k;
-    row[k] = u < n ? u : -1;
-    if (kList && u < n) {
-      row[k] = a.list[u];
-      if (row[k] < 0 || row[k] >= a.N) {
-        if (c == 0 && part == 0) set_error(a.hdr, DV_ERR_INDEX_RANGE, row[k]);
-        row[k] = -1;
-      } else if (u > 0 && a.list[u - 1] == row[k]) {
-        row[k] = -1;   // listed twice: counts once
-      }
-    }
+    row[k] = u >= n ? -1 : kList ? a.list[u] : u;
   }
   const uint8_t* q0 = a.q + (size_t)max(row[0], 0) * a.pitch + 16 * c;
   const uint8_t* q1 = a.q + (size_t)max(row[1], 0) * a.pitch + 16 * c;
@@ -284,13 +272,12 @@ __global__ void __launch_bounds__(kThreads) q4_rows_kernel(const Q4Rows a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
   const P* x = static_cast<const P*>(a.x);
-  bool waited = !a.early;
-  for (int k0 = part; k0 < a.blocks; k0 += a.kw * kAhead) {
+  for (int k0 = wid; k0 < a.blocks; k0 += kWarps * kAhead) {
     uint4 w[kAhead][2];
     float sc[kAhead][2][2];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int kb = k0 + i * a.kw;
+      const int kb = k0 + i * kWarps;
       w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
       if (kb < a.blocks) {
         if (row[0] >= 0) w[i][0] = ld_stream(q0 + (size_t)kb * kBlockBytes);
@@ -299,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) q4_rows_kernel(const Q4Rows a) {
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int kb = k0 + i * a.kw;
+      const int kb = k0 + i * kWarps;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int gi = halves == 2 ? 2 * kb + h : kb;
@@ -308,14 +295,9 @@ __global__ void __launch_bounds__(kThreads) q4_rows_kernel(const Q4Rows a) {
         sc[i][h][1] = in && row[1] >= 0 ? ld_scale<S>(a.scale, s1 + gi) : 0.f;
       }
     }
-    if (!waited) {
-      grid_dep_wait();
-      grid_dep_launch();
-      waited = true;
-    }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int kb = k0 + i * a.kw;
+      const int kb = k0 + i * kWarps;
       if (kb >= a.blocks) break;
       const uint32_t w0[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w};
       const uint32_t w1[4] = {w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
@@ -352,26 +334,20 @@ __global__ void __launch_bounds__(kThreads) q4_rows_kernel(const Q4Rows a) {
       }
     }
   }
-  if (!waited) {
-    grid_dep_wait();
-    grid_dep_launch();
-  }
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int r = 0; r < 4; ++r) red[wid][g + 8 * (r >> 1)][8 * t + 2 * c + (r & 1)] = acc[t][r];
   __syncthreads();
   // sums over the parts (and a 32-bit vector's pieces), in a fixed order
-  for (int i = tid; i < tiles * 16 * a.B; i += kThreads) {
-    const int r = i % (tiles * 16), b = i / (tiles * 16), u = blockIdx.x * tiles * 16 + r;
+  for (int i = tid; i < 16 * a.B; i += kThreads) {
+    const int r = i % 16, b = i / 16, u = u0 + r;
     if (u >= n) continue;
     float sum = 0.f;
-    for (int p = 0; p < a.kw; ++p)
-      for (int col = b; col < a.cols; col += a.B) sum += red[(r >> 4) * a.kw + p][r & 15][col];
+    for (int p = 0; p < kWarps; ++p)
+      for (int col = b; col < a.cols; col += a.B) sum += red[p][r][col];
     if (kList) {
-      const int j = a.list[u];
-      bool live = j >= 0 && j < a.N && !(u > 0 && a.list[u - 1] == j);
-      if (live && a.member) live = bit_test(a.member + (size_t)b * a.words, j);
+      const bool live = bit_test(a.member + (size_t)b * a.words, a.list[u]);
       a.act[(size_t)b * a.ld_act + u] = live ? (sum > 0.f || sum != sum ? sum : 0.f) : 0.f;
     } else {
       float* o = a.out + (size_t)b * a.N + u;
@@ -545,9 +521,7 @@ __global__ void __launch_bounds__(256) q4_join_kernel(const float* __restrict__ 
 
 template <typename S, typename P, int NT>
 cudaError_t run_rows(const Q4Rows& a, bool pdl, cudaStream_t stream) {
-  const int tiles = kWarps / a.kw;
-  const int rows = a.list ? a.cap : a.N;
-  const dim3 grid((rows + 16 * tiles - 1) / (16 * tiles));
+  const dim3 grid(((a.list ? a.cap : a.N) + 15) / 16);
   return a.list ? launch_k(q4_rows_kernel<S, P, NT, true>, grid, dim3(kThreads), 0, stream, pdl, 1, a)
                 : launch_k(q4_rows_kernel<S, P, NT, false>, grid, dim3(kThreads), 0, stream, pdl, 1, a);
 }
@@ -567,13 +541,12 @@ cudaError_t launch_rows(Q4Rows a, const void* y, void* pieces, dv_dtype dt, bool
   a.groups = (a.d + a.group - 1) / a.group;
   if (q4_vec_supported(a.B, a.d)) return launch_q4_vec_rows(a, dt, pdl, stream);
   if (q4_tc_supported(a.B, a.d, dt)) return launch_q4_tc_rows(a, dt, a.hdr, pdl, stream);
-  a.kw = 8;
   if (dt == DV_F32) {
     const int ld = a.blocks * 128;
     const cudaError_t e = launch_k(q4_pieces_kernel, dim3((ld + kThreads - 1) / kThreads, a.B), dim3(kThreads), 0, stream,
                                    true, 1, static_cast<const float*>(y), a.B, a.d, ld, static_cast<__nv_bfloat16*>(pieces));
     if (e != cudaSuccess) return e;
-    a.ldx = ld; a.x_len = ld; a.early = 0;
+    a.ldx = ld; a.x_len = ld;
     const int B = a.B;
     for (int b0 = 0; b0 < B; b0 += kPieceRows) {
       Q4Rows r = a;

@@ -34,11 +34,6 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w) { return (w >> 4) & 0
 __device__ __forceinline__ int high_of(int e) { return (e >> 1) & 1; }
 __device__ __forceinline__ int byte_of(int e) { return (e & 1) * 2 + (e >> 2); }
 
-__device__ __forceinline__ uint32_t ld_stream4(const void* p) {
-  uint32_t r;
-  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
-  return r;
-}
 template <typename S>
 __device__ __forceinline__ uint32_t ld_raw(const void* p) {
   if constexpr (sizeof(S) == 4) {
@@ -60,8 +55,9 @@ template <> __device__ __forceinline__ float of_raw<__nv_bfloat16>(uint32_t r) {
 
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-// The exponent that brings values of at most `top` into [-2^30, 2^30].
-__device__ __forceinline__ int fixed_shift(uint32_t top) { return min(30 - ((int)(top >> 23) - 126), 126); }
+// The exponent that brings values of at most `top` into [-2^30, 2^30] (2^-150 is finer than
+// the least of fp32).
+__device__ __forceinline__ int fixed_shift(uint32_t top) { return min(30 - ((int)(top >> 23) - 126), 150); }
 __device__ __forceinline__ int fixed(float v, int shift) {   // (two steps: 2^shift alone may be out of range)
   return __float2int_rn(v * pow2(shift / 2) * pow2(shift - shift / 2));
 }
@@ -80,7 +76,9 @@ __device__ __forceinline__ void digits_of(int v, int* d) {
 // Vectors in shared memory: digits of the 32 elements of chunk (16 bytes of a row)
 // k in the order of the chunk's codes, [vector][digit][half of it][chunk] of 16 bytes; -8
 // times their sums, of either half of the block, [vector][chunk][half][digit]; and a
-// group's unit times 2^-20, [vector][group].
+// the unit of a group's highest digit, [vector][group]: about its largest times 2^-6, so that
+// neither its product with a scale nor that with a sum of digits leaves the range of fp32
+// where products of weights and elements do not.
 struct VecLayout {
   int chunks;   // a multiple of 32
   int groups;
@@ -116,7 +114,7 @@ __device__ __forceinline__ void stage_group(const S* y, int d, int group, int gi
     for (int p = 0; p < kDigits; ++p) at[(size_t)p * 2 * v.chunks * 16] = (uint8_t)dig[p];
   }
   // (an infinity or a NaN: every product a NaN)
-  if (lane == 0) *unit = top < 0x7f800000u ? pow2(-(shift / 2)) * pow2(-(shift - shift / 2) - 20) : __int_as_float(0x7fc00000);
+  if (lane == 0) *unit = top < 0x7f800000u ? pow2(24 - shift) : __int_as_float(0x7fc00000);
 }
 
 // A warp takes kRows rows at a time, a lane one chunk of every 32 of a row; the next
@@ -230,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_vec_rows_kernel(const Q4Rows a
             code[k][2 * i + 1] = high_codes(ww[i]);
           }
 #pragma unroll
-          for (int h = 0; h < (two ? 2 : 1); ++h) scale[k][h] = of_raw<S>(sc[j][k][h]) * 1048576.f;
+          for (int h = 0; h < (two ? 2 : 1); ++h) scale[k][h] = of_raw<S>(sc[j][k][h]);
         }
         // the slot takes the step after the ones ahead, of these rows or the warp's next
         if (s + kAhead < steps) fetch(j, s + kAhead);
@@ -258,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_vec_rows_kernel(const Q4Rows a
 #pragma unroll
               for (int h = 0; h < (two ? 2 : 1); ++h) {
                 const float part = __int_as_float(sum[h]) - kMagicF;   // exact
-                f[k][h] = p == 0 ? part : fmaf(f[k][h], 256.f, part);
+                f[k][h] = p == 0 ? part : fmaf(part, 1.f / (1 << (8 * p)), f[k][h]);
               }
             }
           }
@@ -266,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_vec_rows_kernel(const Q4Rows a
           for (int h = 0; h < (two ? 2 : 1); ++h) {
             const float unit = units[b * v.groups + gi + h];
 #pragma unroll
-            for (int k = 0; k < kRows; ++k) acc[k][b] = fmaf(f[k][h] * unit, scale[k][h], acc[k][b]);
+            for (int k = 0; k < kRows; ++k) acc[k][b] = fmaf(f[k][h], scale[k][h] * unit, acc[k][b]);
           }
         }
       }
@@ -328,7 +326,7 @@ __global__ void __launch_bounds__(kColThreads, 1) q4_vec_cols_kernel(const Q4Col
   __shared__ uint32_t top[kMaxGroups];
   __shared__ int id[kStaged / 2 * 4];
   float4* coef = reinterpret_cast<float4*>(smem);
-  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
+  const int tid = threadIdx.x, threads = blockDim.x;
   const int words = a.blocks * 16, pair = blockIdx.y * threads + tid;   // the thread's two words
   const bool mine = 2 * pair < words;
   const int block = min(pair >> 3, a.blocks - 1);

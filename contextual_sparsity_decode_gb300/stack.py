@@ -502,7 +502,7 @@ class SparseDecoder:
         (all workspaces are read and cleared)."""
         used = [self.ws_pred_main, self.ws_pred_side, self.ws_attn, self.ws_mlp, self.ws_mlp_q4, self.ws_move]
         if self.head is not None:
-            used.append(self.ws_sample)
+            used += [self.ws_head, self.ws_sample]
         for t in self._tree.values():
             used += [t[k] for k in ("ws_pred", "ws_mlp", "ws_mlp_q4", "ws_tree")]
         found = [dv.dv_check(ws) for ws in used if ws is not None]

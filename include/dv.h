@@ -249,10 +249,14 @@ dv_status dv_q4_matvec_workspace_size(int B, int d, int N, size_t* bytes);
  * projection):
  *     out[b][n] (+)= sum_t w[n][t] y[b][t],
  * y [B][d] in the storage type of the scales, out [B][N] fp32, see
- * dv_sparse_mlp for `accumulate`.  The weights enter as they are (no rounding),
- * sums are fp32; results repeat bit for bit.  Like dv_layernorm's, its first
+ * dv_sparse_mlp for `accumulate`.  Codes and scales enter as they are.  For one
+ * and two vectors y enters in fixed point, 30 bits below the largest magnitude
+ * of each group of elements, for three and more as it is; sums are fp32 and
+ * results repeat bit for bit.  A NaN or an infinity in y makes the products of that
+ * vector NaN or infinite and no other's.  Like dv_layernorm's, its first
  * kernel may be started before the kernel ahead of the call has ended and waits
  * for it before it reads or writes anything.
+ * Device errors: DV_ERR_TIMEOUT (see dv_set_wait_limit_ns; three and more vectors).
  * Limits: B <= 32, N <= 16777216, d <= 32768. */
 dv_status dv_q4_matvec(const void* y, int B, int d, int N, const dv_q4* W,
                        dv_dtype dt, float* out, int accumulate,
@@ -263,14 +267,19 @@ dv_status dv_q4_sparse_mlp_workspace_size(int B, int d, int N, int cap,
 
 /* dv_sparse_mlp with both matrices in 4 bits (their groups may differ):
  *     out_b (+)= sum_{j in S_b} ReLU(y_b . W1[j]) W2[j],
- * arguments as there.  An entry that a list holds twice counts once, and a
+ * arguments as there.  An entry that a list holds twice counts once (for B = 1:
+ * if the two are neighbours, as in the ascending lists of dv_predict), and a
  * neuron whose activation is 0 adds nothing, whatever its row of W2 holds.  The
- * activations are fp32 and enter the second product as they are; every output
- * has one writer and a fixed order of summation: results repeat bit for bit.
+ * first product is dv_q4_matvec's.  The activations are fp32; times their rows'
+ * scales, rounded once, they enter the second product as they are for three and
+ * more vectors, and for one and two in fixed point, 30 bits below the largest of
+ * a share of the list.  Every output has one writer and a fixed order of
+ * summation: results repeat bit for bit.
  * Its workspace is not one of dv_sparse_mlp (which keeps counters there).
  * dv_set_launch_overlap as for dv_sparse_mlp.
  * Device errors: DV_ERR_INDEX_RANGE (an entry outside [0, N) is skipped),
- * DV_ERR_CAPACITY (a count above cap is cut off).
+ * DV_ERR_CAPACITY (a count above cap is cut off), DV_ERR_TIMEOUT as for
+ * dv_q4_matvec.
  * Limits: B <= 32, N <= 65536, d <= 32768. */
 dv_status dv_q4_sparse_mlp(const void* y, int B, int d, int N, const dv_q4* W1,
                            const dv_q4* W2, const int32_t* idx, int cap,
@@ -541,8 +550,8 @@ int dv_set_launch_overlap(int level);
 
 /* Bound of every device-side wait (no counterpart in the pages): the
  * one-launch MLP's wait for its up-projection CTAs, the tensor-core paths'
- * pipeline waits (dv_tree_attn's among them) and the waits for copies of the
- * streaming MLP, dv_beam_select and dv_sample give up after `ns` nanoseconds of the GPU's
+ * pipeline waits (those of dv_tree_attn, and of dv_q4_matvec and dv_q4_sparse_mlp
+ * for three and more vectors, among them) and the waits for copies of the streaming MLP, dv_beam_select and dv_sample give up after `ns` nanoseconds of the GPU's
  * global timer, record DV_ERR_TIMEOUT in the workspace (read it with dv_check)
  * and unwind; the kernel still waits for its own tensor-core and copy work in
  * flight before it exits.  ns <= 0 restores the default of one second.

@@ -7,7 +7,12 @@ An m16n8k16 product adds 17 numbers and may drop what is below 2^-24 of the
 largest of each: 17 x 2^-24 of the sum of magnitudes.  A group of 128 is a chain
 of 8 of them; then come one product with the scale and one sum per group (at most
 two groups a block), and 24 sums over warps and pieces, 2^-24 each:
-(136 + 4 blocks + 24) 2^-24 sum |w y|.  The second product of the MLP is a chain
+(136 + 4 blocks + 24) 2^-24 sum |w y|.  A product of 128 elements at once on the
+tensor cores' accumulators is the same chain of 8.  The integer products of one
+and two vectors are exact; their fixed point is off by 2^-31 of the largest of a
+group for each element, 2^-31 128 of the group's largest magnitude times its
+largest weight at most, which the normal vectors here stay far below 136 2^-24 of the
+sum with, and a conversion, a product and a sum a group are 4 2^-24 a block.  The second product of the MLP is a chain
 of three products for each 16 rows a warp meets (all of them, at most), one
 rounding of a_j s each, and sums over 8 warps, 8 CTAs and 3 pieces, on top of what
 its activations are off by."""
