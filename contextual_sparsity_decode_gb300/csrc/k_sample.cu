@@ -22,7 +22,7 @@
 //               tokens' weights by groups of 32 vectors, the group and the token.
 // Equal values are taken by their index where the cut passes among them.
 //
-// Measured on GB300: 192 rows of 128001 bf16 logits, nucleus of 0.95, 160 us (0.31 TB/s of the
+// Measured on GB300: 192 rows of 128001 bf16 logits, nucleus of 0.95, 158 us (0.31 TB/s of the
 // logits read; 24 us to the maximum, 40 for every token's weight and bin, the rest
 // in cluster barriers, the refined bin and the draw); 8 rows of 50257 fp32 without
 // filters 9.2 us, one of 32000 f16 with all 12.1: latency of the barriers.
@@ -254,27 +254,28 @@ struct Row {
     cluster_sync();
     return t;
   }
-  static __device__ __forceinline__ float largest(const float* x) {
-    float m = x[0];
-#pragma unroll
-    for (int e = 1; e < E; ++e) m = fmaxf(m, x[e]);
-    return m;
-  }
-  // Tokens of group g (of 32 vectors) above -inf and not below `floor`, side by side in the
+  // Tokens of group g (of 32 vectors) above -inf, from `floor` to `top`, side by side in the
   // warp's buffer; returns their number.  What is done with a token costs 40 instructions,
   // and a nucleus holds few of a group's: done where they are, every warp would run
   // them for all.
-  __device__ __forceinline__ int pack(int g, float floor) const {
+  __device__ __forceinline__ int pack(int g, float floor, float top) const {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, v = g * 32 + lane;
     float x[E];
-    const bool in = v < vecs;
-    if (in) open(v, x);
-    if (!__any_sync(0xffffffffu, in && largest(x) >= floor)) return 0;
+    uint32_t takes = 0;
+    if (v < vecs) {
+      open(v, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (x[e] >= floor && x[e] <= top && x[e] > -INFINITY) takes |= 1u << e;
+    }
+    const uint32_t any = __reduce_or_sync(0xffffffffu, takes);
+    if (!any) return 0;
     int n = 0;
     __syncwarp();   // (the buffer's last readers)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const bool take = in && x[e] >= floor && x[e] > -INFINITY;
+      if (!(any >> e & 1)) continue;
+      const bool take = takes >> e & 1;
       const uint32_t hit = __ballot_sync(0xffffffffu, take);
       if (take) {
         const int at = n + __popc(hit & ((1u << lane) - 1));
@@ -286,12 +287,12 @@ struct Row {
     __syncwarp();
     return n;
   }
-  // f(x, index) of every token of the CTA above -inf and not below `floor`
+  // f(x, index) of every token of the CTA above -inf, from `floor` to `top`
   template <typename F>
-  __device__ __forceinline__ void each(float floor, F f) const {
+  __device__ __forceinline__ void each(float floor, float top, F f) const {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     for (int g = wid; g * 32 < vecs; g += kWarps) {
-      const int n = pack(g, floor);
+      const int n = pack(g, floor, top);
       for (int i = lane; i < n; i += 32) f(sh.dense[wid][i], (v0 + g * 32) * E + sh.place[wid][i]);
     }
   }
@@ -307,8 +308,8 @@ struct Row {
     }
   }
   // The bin that holds the `target`-th unit (of count or weight) of the
-  // histogram that all CTAs have filled, what is before it and in it, and its keys; kBins if
-  // there is less in all.  Every CTA adds the cluster's bins for itself: one barrier.  No
+  // histogram that all CTAs have filled, what is before it and in it, and its keys (kKeys);
+  // kBins if there is less in all.  Every CTA adds the cluster's bins for itself: one barrier.  No
   // CTA may clear its bins before the cluster's next one.
   struct Found {
     int bin;
@@ -318,7 +319,7 @@ struct Row {
     u64 mine;     // this CTA's share of what is before
   };
   // target_of: the target, of the sum of all bins
-  template <bool kMass, typename F>
+  template <bool kMass, bool kKeys, typename F>
   __device__ __forceinline__ Found crossing(F target_of) {
     constexpr int kPer = kBins / kThreads;
     cluster_sync();   // the histograms are complete
@@ -350,9 +351,11 @@ struct Row {
     }
     __syncthreads();
     Found f{(int)sh.answer[0], sh.answer[1], sh.answer[2], 0, 0, target - sh.answer[1], 0};
-    const uint32_t r = threadIdx.x & 31;
-    f.klo = __reduce_min_sync(0xffffffffu, r < size ? ld_remote(&sh.kmin[f.bin], r) : 0xffffffffu);
-    f.khi = __reduce_max_sync(0xffffffffu, r < size ? ld_remote(&sh.kmax[f.bin], r) : 0u);
+    if (kKeys) {
+      const uint32_t r = threadIdx.x & 31;
+      f.klo = __reduce_min_sync(0xffffffffu, r < size ? ld_remote(&sh.kmin[f.bin], r) : 0xffffffffu);
+      f.khi = __reduce_max_sync(0xffffffffu, r < size ? ld_remote(&sh.kmax[f.bin], r) : 0u);
+    }
     sum = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
@@ -370,7 +373,7 @@ struct Row {
     __syncthreads();
   }
   template <bool kMass>
-  __device__ __forceinline__ void add_bin(int b, uint32_t key, u64 w) {
+  __device__ __forceinline__ void add_bin(int b, u64 w) {
     if (!kMass) {
       atomicAdd(&sh.count[b], 1u);
     } else {
@@ -378,14 +381,16 @@ struct Row {
       const uint32_t up = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
       if (up) atomicAdd(&sh.carry[b], up);
     }
+  }
+  __device__ __forceinline__ void add_key(int b, uint32_t key) {
     atomicMin(&sh.kmin[b], key);
     atomicMax(&sh.kmax[b], key);
   }
   // Tokens that `take` into every CTA's list, their number into the first CTA's
   // listed[which], 0 before.
   template <typename F>
-  __device__ __forceinline__ void gather(int which, float floor, F take) {
-    each(floor, [&](float x, int i) {
+  __device__ __forceinline__ void gather(int which, float floor, float top, F take) {
+    each(floor, top, [&](float x, int i) {
       if (!take(x, i)) return;
       const uint32_t at = add_remote(&sh.listed[which], 0, 1);
       if (at < (uint32_t)kList)
@@ -416,14 +421,25 @@ struct Row {
   }
 };
 
+// Bins of x below the maximum, `step` to a unit.
+struct Bins {
+  float m, step;
+  __device__ __forceinline__ uint32_t of(float x) const { return __float2uint_rz((m - x) * step); }
+  // Bounds of bin b's x: difference, product and quotient are rounded (2^-23 together, and the
+  // differences here outwards).
+  __device__ __forceinline__ float low(int b) const { return __fsub_rd(m, (float)(b + 1) / step * 1.000001f); }
+  __device__ __forceinline__ float high(int b) const { return b ? __fsub_ru(m, (float)b / step * 0.999999f) : m; }
+};
+
 __device__ __forceinline__ float listed_x(u64 entry) { return unord32((uint32_t)(entry >> 32)); }
 
 // The cut of the order at the unit of count or weight that `target_of` names, of the sum
-// of those that `have` keeps; `have` itself if they hold less.  `step`: bins per unit
-// of x below the maximum.  `first`: the answer of that histogram, if it is known.
+// of those that `have` keeps; `have` itself if they hold less.  `first`: the answer of the
+// histogram over `bins`, if it is known.  (Its bins have no keys: with two more atomic
+// operations a token 192 rows of 128001 took 160.6 us instead of 158.5.)
 // *mine: the weight of this CTA's tokens that the cut keeps (kMass).
 template <bool kMass, typename T, typename F>
-__device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut have, float step, F target_of,
+__device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut have, const Bins& bins, F target_of,
                                         const typename Row<T>::Found* first, u64* mine) {
   Shared& sh = row.sh;
   typename Row<T>::Found f;
@@ -431,20 +447,19 @@ __device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut hav
     f = *first;
   } else {
     row.clear_bins();
-    const auto count = [&](float x, uint32_t k) {
-      const uint32_t b = __float2uint_rz((weigh.m - x) * step);
+    const auto count = [&](float x) {
+      const uint32_t b = bins.of(x);
       const u64 w = kMass ? weigh(x) : 1;
-      if (b < (uint32_t)kBins && w) row.template add_bin<kMass>((int)b, k, w);
+      if (b < (uint32_t)kBins && w) row.template add_bin<kMass>((int)b, w);
     };
     if (have.key == 0) {
-      row.each_of_all([&](float x) { count(x, ord32(x)); });
+      row.each_of_all(count);
     } else {
-      row.each(unord32(have.key), [&](float x, int i) {
-        const uint32_t k = ord32(x);
-        if (have.keeps(k, i)) count(x, k);
+      row.each(unord32(have.key), weigh.m, [&](float x, int i) {
+        if (have.keeps(ord32(x), i)) count(x);
       });
     }
-    f = row.template crossing<kMass>(target_of);
+    f = row.template crossing<kMass, false>(target_of);
     if (f.bin == kBins) {   // (a weight's target is never above the sum)
       *mine = 0;
       return have;
@@ -453,15 +468,18 @@ __device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut hav
   u64 before = 0;             // of what is left
   const u64 target = f.target;
   *mine = f.mine;
-  // the tokens that are left: those `have` keeps with keys in [f.klo, f.khi]
-  for (;;) {
-    if (f.klo == f.khi) break;   // one value
+  // the tokens that are left: those `have` keeps in the bin, with keys in [f.klo, f.khi]
+  const uint32_t bin = f.bin;
+  f.klo = ord32(bins.low(bin));
+  f.khi = ord32(bins.high(bin));
+  for (bool exact = false;; exact = true) {
+    if (exact && f.klo == f.khi) break;   // one value
     const float low_x = unord32(f.klo), high_x = unord32(f.khi);
     // how many there are, at most: their weight over the least of them
     const u64 least = kMass ? weigh(low_x) : 1;
     if (least > 0 && f.inside <= (u64)kList * least) {
-      row.gather(kMass, low_x, [&](float x, int i) {
-        return x <= high_x && have.keeps(ord32(x), i) && (!kMass || weigh(x) != 0);
+      row.gather(kMass, low_x, high_x, [&](float x, int i) {
+        return bins.of(x) == bin && have.keeps(ord32(x), i) && (!kMass || weigh(x) != 0);
       });
       // (no CTA ends before the cluster's next barrier: the draw has one)
       const int n = min((int)ld_remote(&sh.listed[kMass], 0), kList), i = threadIdx.x;
@@ -491,14 +509,16 @@ __device__ __forceinline__ Cut find_cut(Row<T>& row, const Scale& weigh, Cut hav
     while ((f.khi - f.klo) >> shift >= (uint32_t)kBins) ++shift;
     cluster_sync();   // the last histogram has been read
     row.clear_bins();
-    row.each(low_x, [&](float x, int i) {
+    row.each(low_x, high_x, [&](float x, int i) {
       const uint32_t k = ord32(x);
-      if (x > high_x || !have.keeps(k, i)) return;
+      if (bins.of(x) != bin || !have.keeps(k, i)) return;
       const u64 w = kMass ? weigh(x) : 1;
-      if (w) row.template add_bin<kMass>((int)((f.khi - k) >> shift), k, w);
+      if (!w) return;
+      row.template add_bin<kMass>((int)((f.khi - k) >> shift), w);
+      row.add_key((int)((f.khi - k) >> shift), k);
     });
     const u64 left = target - before;
-    f = row.template crossing<kMass>([&](u64) { return left; });
+    f = row.template crossing<kMass, true>([&](u64) { return left; });
     if (f.bin == kBins) return have;
     before += f.before;
     *mine += f.mine;
@@ -672,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleLaunch 
 
   if (temp == 0.f) {   // the best token, the first of equal ones
     int first = INT_MAX;
-    row.each(m, [&](float x, int i) {
+    row.each(m, m, [&](float x, int i) {
       if (x == m) first = min(first, i);
     });
     first = __reduce_min_sync(0xffffffffu, first);
@@ -696,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleLaunch 
   weigh.hi = __fdiv_rn(1.44269502f, temp);
   weigh.lo = __fdiv_rn(__fmaf_rn(-weigh.hi, temp, 1.44269502f) + 1.92596303e-8f, temp);
   weigh.table = sh.table;
-  const float step = (float)kBins / (kReach * temp);
+  const Bins bins{m, (float)kBins / (kReach * temp)};
   const u64 least = min_p > 0.f ? __float2ull_ru(fminf(min_p, 1.f) * (float)(1ull << kUnit)) : 0;
   const auto mass_target = [&](u64 mass) {   // tokens are kept while what is before them is below
     return max(times(mass, p, true), (u64)1);
@@ -720,13 +740,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleLaunch 
   if (has_k) {
     row.clear_bins();
     row.each_of_all([&](float x) {
-      const uint32_t bin = __float2uint_rz((m - x) * step);
-      if (bin < (uint32_t)kBins) row.template add_bin<false>((int)bin, ord32(x), 0);
+      const uint32_t bin = bins.of(x);
+      if (bin < (uint32_t)kBins) row.template add_bin<false>((int)bin, 0);
     });
-    const auto found = row.template crossing<false>([&](u64) { return (u64)k; });
+    const auto found = row.template crossing<false, false>([&](u64) { return (u64)k; });
     if (found.bin < kBins && found.before + found.inside <= (u64)kList) {
       // the few best tokens: one CTA does the rest
-      row.gather(0, unord32(found.klo), [&](float x, int) { return __float2uint_rz((m - x) * step) <= (uint32_t)found.bin; });
+      row.gather(0, bins.low(found.bin), m, [&](float x, int) { return bins.of(x) <= (uint32_t)found.bin; });
       if (rank != 0) return;
       const int n = min((int)sh.listed[0], kList);
       u64 mine = 0, w = 0;
@@ -758,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleLaunch 
       return;
     }
     u64 unused;
-    if (found.bin < kBins) cut = find_cut<false>(row, weigh, cut, step, [](u64 all) { return all; }, &found, &unused);
+    if (found.bin < kBins) cut = find_cut<false>(row, weigh, cut, bins, [](u64 all) { return all; }, &found, &unused);
   }
 
   // ---- sums of groups of 32 vectors: kept tokens that weigh `low` at least
@@ -778,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleLaunch 
           for (int e = 0; e < E; ++e) w += weigh(x[e]);
         }
       } else {
-        const int n = row.pack(g, floor_x);
+        const int n = row.pack(g, floor_x, m);
         for (int i = lane; i < n; i += 32) {
           const float x = sh.dense[wid][i];
           const u64 we = weigh(x);
@@ -796,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleLaunch 
   // ---- nucleus
   u64 total, mass = 0, ahead = 0;
   if (has_p)
-    cut = find_cut<true>(row, weigh, cut, step, mass_target, (const typename Row<T>::Found*)nullptr, &total);
+    cut = find_cut<true>(row, weigh, cut, bins, mass_target, (const typename Row<T>::Found*)nullptr, &total);
 
   // ---- draw
   const bool summed = !has_p || least > 0;   // (the nucleus knows every CTA's weight already)
