@@ -376,6 +376,7 @@ struct Q4Cols {
   float* part;                          // q4_part_floats: the sums of shares of the list
   int groups, blocks;
   size_t pitch;
+  WsHeader* hdr; long long wait_ns;     // k_q4_tc_cols.cu
 };
 struct Q4MatvecLaunch {
   const void* y; int B, d, N;
@@ -397,6 +398,8 @@ struct Q4MlpLaunch {
 };
 // Three and more vectors of a 16-bit type, the first kind of product (k_q4_tc.cu).
 bool q4_tc_supported(int B, int d, dv_dtype dt);
+// The second kind for three and more vectors (k_q4_tc_cols.cu).
+cudaError_t launch_q4_tc_cols(const Q4Cols& a, cudaStream_t stream);
 cudaError_t launch_q4_tc_rows(const Q4Rows& a, dv_dtype dt, WsHeader* hdr, bool pdl, cudaStream_t stream);
 // One and two vectors (k_q4_vec.cu).
 bool q4_vec_supported(int B, int d);

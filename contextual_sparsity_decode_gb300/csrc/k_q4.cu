@@ -356,147 +356,7 @@ __global__ void __launch_bounds__(kThreads) q4_rows_kernel(const Q4Rows a) {
   }
 }
 
-// ---- second product of the MLP ----------------------------------------------------------
-
-// out[b][t] (+)= sum_u act[b][u] s[j_u][group of t] (code[j_u][t] - 8): a CTA owns a
-// share of the list and up to eight blocks of its rows, one a warp; a step is 16 rows by the
-// 128 elements, elements as the A operand's rows.  The coefficients enter as three
-// pieces, a product each.  The CTAs' sums go to the workspace, and a second kernel adds
-// them in order.
-constexpr int kColWarps = 8;
-
-template <typename S>
-__device__ __forceinline__ uint32_t ld_raw(const void* s, size_t i) {   // (volatile: not moved to its use)
-  if constexpr (sizeof(S) == 4) {
-    uint32_t v;
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(static_cast<const float*>(s) + i));
-    return v;
-  } else {
-    uint16_t h;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(h) : "l"(static_cast<const uint16_t*>(s) + i));
-    return h;
-  }
-}
-template <typename S> __device__ __forceinline__ float of_raw(uint32_t r);
-template <> __device__ __forceinline__ float of_raw<float>(uint32_t r) { return __uint_as_float(r); }
-template <> __device__ __forceinline__ float of_raw<__half>(uint32_t r) {
-  return __half2float(__ushort_as_half((unsigned short)r));
-}
-template <> __device__ __forceinline__ float of_raw<__nv_bfloat16>(uint32_t r) { return __uint_as_float(r << 16); }
-__device__ __forceinline__ uint2 ld_stream8(const void* p) {
-  uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
-}
-
-template <typename S, int NT, bool two>
-__global__ void __launch_bounds__(32 * kColWarps, 1) q4_cols_kernel(const Q4Cols a) {
-  constexpr int kAhead = NT <= 2 ? 3 : 2;   // steps held in registers
-  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int kb = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  grid_dep_wait();
-  grid_dep_launch();
-  if (kb >= a.blocks) return;
-  const int n = max(0, min(*a.count, a.cap));
-  const int all = (n + 15) >> 4, share = (all + gridDim.x - 1) / gridDim.x;
-  const int lo = min(all, (int)blockIdx.x * share), steps = min(all, lo + share) - lo;
-  const int g0 = two ? 2 * kb : kb, g1 = min(2 * kb + 1, a.groups - 1);
-  const uint8_t* q = a.q + (size_t)kb * kBlockBytes + 8 * g;
-  float acc[2][4][NT][4];
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[s][i][t][r] = 0.f;
-  uint2 w[kAhead][4];
-  uint32_t sc[kAhead][two ? 2 : 1][4];
-  float v[kAhead][NT][4];
-  // rows, scales and activations of step s (behind the list, and for entries outside,
-  // which have activation 0 from the first product on, another row is read)
-  const auto fetch = [&](int k, int s) {
-    const int e = (lo + s) * 16 + 4 * c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int l = a.list[min(e + i, n - 1)];
-      const size_t j = l >= 0 && l < a.N ? l : 0;
-      w[k][i] = ld_stream8(q + j * a.pitch);
-      sc[k][0][i] = ld_raw<S>(a.scale, j * a.groups + g0);
-      if (two) sc[k][two][i] = ld_raw<S>(a.scale, j * a.groups + g1);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        v[k][t][i] = __ldcg(a.act + (size_t)min(8 * t + g, a.B - 1) * a.ld_act + min(e + i, n - 1));
-    }
-  };
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k)
-    if (k < steps) fetch(k, k);
-  for (int s0 = 0; s0 < steps; s0 += kAhead) {
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (s0 + k >= steps) break;
-      const int e = (lo + s0 + k) * 16 + 4 * c;
-      // coefficients of this lane's four rows in its columns: [half][piece][pair]
-      uint32_t cf[NT][two ? 2 : 1][3][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int h = 0; h < (two ? 2 : 1); ++h) {
-          __nv_bfloat16 p[4][3];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)   // (0 adds nothing, whatever the row holds; behind the list nothing counts)
-            pieces3(v[k][t][i] == 0.f || e + i >= n ? 0.f : v[k][t][i] * of_raw<S>(sc[k][h][i]), p[i]);
-#pragma unroll
-          for (int z = 0; z < 3; ++z)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              __nv_bfloat162 pair;
-              pair.x = p[2 * i][z];
-              pair.y = p[2 * i + 1][z];
-              cf[t][h][z][i] = *reinterpret_cast<uint32_t*>(&pair);
-            }
-        }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t r0 = s ? w[k][0].y : w[k][0].x, r1 = s ? w[k][1].y : w[k][1].x;
-        const uint32_t r2 = s ? w[k][2].y : w[k][2].x, r3 = s ? w[k][3].y : w[k][3].x;
-        // elements 2 i of two rows side by side, and elements 2 i + 1
-        uint32_t ev0[4], ev1[4], od0[4], od1[4];
-        Pairs<__nv_bfloat16>::open(__byte_perm(r0, r1, 0x5410), ev0);
-        Pairs<__nv_bfloat16>::open(__byte_perm(r0, r1, 0x7632), od0);
-        Pairs<__nv_bfloat16>::open(__byte_perm(r2, r3, 0x5410), ev1);
-        Pairs<__nv_bfloat16>::open(__byte_perm(r2, r3, 0x7632), od1);
-#pragma unroll
-        for (int z = 0; z < 3; ++z)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint32_t* x = cf[t][two && s][z];
-              mma16816<__nv_bfloat16>(acc[s][i][t], ev0[i], od0[i], ev1[i], od1[i], x[0], x[1]);
-            }
-      }
-      if (s0 + k + kAhead < steps) fetch(k, s0 + k + kAhead);
-    }
-  }
-  // [share][vector][element]
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int lo8 = 0; lo8 < 2; ++lo8) {
-      const int b = 8 * t + 2 * c + lo8;
-      if (b >= a.B) continue;
-      float* part = a.part + (((size_t)blockIdx.x * a.B + b) * a.blocks + kb) * 128 + 8 * g;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        float4* to = reinterpret_cast<float4*>(part + 64 * s);
-        to[0] = make_float4(acc[s][0][t][lo8], acc[s][0][t][2 + lo8], acc[s][1][t][lo8], acc[s][1][t][2 + lo8]);
-        to[1] = make_float4(acc[s][2][t][lo8], acc[s][2][t][2 + lo8], acc[s][3][t][lo8], acc[s][3][t][2 + lo8]);
-      }
-    }
-}
+// ---- sums of the second product's shares ----------------------------------------------------
 
 // out[b][t] (+)= the sum over the shares, [share][vector][ld]: 32 elements a CTA, eight warps
 // that take every eighth share, in a fixed order.
@@ -566,32 +426,6 @@ cudaError_t launch_rows(Q4Rows a, const void* y, void* pieces, dv_dtype dt, bool
                       : run_rows_nt<__nv_bfloat16, __nv_bfloat16>(a, pdl, stream);
 }
 
-// Shares of the list: CTAs for every SM, 16 listed rows each at least.
-int col_shares(const Q4Cols& a, int per_share, int slabs, int ctas) {
-  const int most = (a.cap + per_share - 1) / per_share;
-  int n = ctas / slabs;
-  n = n < 1 ? 1 : n;
-  return n < most ? n : most;
-}
-
-template <typename S, int NT, bool two>
-cudaError_t run_cols(const Q4Cols& a, cudaStream_t stream) {
-  const int slabs = (a.blocks + kColWarps - 1) / kColWarps, warps = (a.blocks + slabs - 1) / slabs;
-  const int shares = col_shares(a, 16, slabs, kQ4Splits);
-  const cudaError_t e = launch_k(q4_cols_kernel<S, NT, two>, dim3(shares, slabs), dim3(32 * warps), 0, stream, true, 1, a);
-  return e == cudaSuccess ? launch_q4_join(a, shares, stream) : e;
-}
-template <typename S, bool two>
-cudaError_t run_cols_nt(const Q4Cols& a, cudaStream_t stream) {
-  if (a.B <= 8) return run_cols<S, 1, two>(a, stream);
-  if (a.B <= 16) return run_cols<S, 2, two>(a, stream);
-  return run_cols<S, 4, two>(a, stream);
-}
-template <typename S>
-cudaError_t run_cols_group(const Q4Cols& a, cudaStream_t stream) {
-  return a.group == 64 ? run_cols_nt<S, true>(a, stream) : run_cols_nt<S, false>(a, stream);
-}
-
 }  // namespace
 
 cudaError_t launch_q4_join(const Q4Cols& a, int shares, cudaStream_t stream) {
@@ -600,10 +434,10 @@ cudaError_t launch_q4_join(const Q4Cols& a, int shares, cudaStream_t stream) {
 }
 
 size_t q4_part_floats(int B, int d) {
-  // shares of one vector's lists (k_q4_vec.cu), or B vectors' shares times slabs of
-  // eight blocks
+  // shares of one vector's lists (k_q4_vec.cu), or B vectors' shares times slabs of at most
+  // eight blocks (k_q4_tc_cols.cu)
   const size_t blocks = (size_t)(d + 127) / 128;
-  const size_t one = kQ4Splits * blocks * 128, many = (kQ4Splits * kColWarps + blocks) * 128 * (size_t)B;
+  const size_t one = kQ4Splits * blocks * 128, many = (kQ4Splits * 8 + blocks) * 128 * (size_t)B;
   return many > one ? many : one;
 }
 
@@ -658,13 +492,8 @@ cudaError_t launch_q4_sparse_mlp(const Q4MlpLaunch& L, dv_dtype dt, WsHeader* hd
   c.pitch = (size_t)blocks * kBlockBytes;
   c.groups = (L.d + L.group2 - 1) / L.group2;
   c.blocks = blocks;
-  if (L.B <= 2) return launch_q4_vec_cols(c, stream);
-  switch (dt) {
-    case DV_F32: return run_cols_group<float>(c, stream);
-    case DV_F16: return run_cols_group<__half>(c, stream);
-    case DV_BF16: return run_cols_group<__nv_bfloat16>(c, stream);
-  }
-  return cudaErrorInvalidValue;
+  c.hdr = hdr;
+  return L.B <= 2 ? launch_q4_vec_cols(c, stream) : launch_q4_tc_cols(c, stream);
 }
 
 }  // namespace dv
