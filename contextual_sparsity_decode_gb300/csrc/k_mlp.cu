@@ -313,6 +313,10 @@ __device__ __forceinline__ uint32_t union_word(const uint32_t* member, int B, in
   return m;
 }
 
+// Every CTA finds all words' places, and writes those of every kUnionCtas-th pair of warps: one
+// CTA's scattered stores took 12.9 us for 16 rows whose union is 16050 entries.
+constexpr int kUnionCtas = 16;
+
 __global__ void __launch_bounds__(1024) union_list_kernel(const uint32_t* member, int B, int N, int32_t* U,
                                                           int32_t* U_count, int32_t* slot_of) {
   __shared__ int tmp[32];
@@ -328,6 +332,8 @@ __global__ void __launch_bounds__(1024) union_list_kernel(const uint32_t* member
   }
   int total;
   const int incl = block_inclusive_scan<1024>(mine, tmp, &total);
+  if (threadIdx.x == 0 && blockIdx.x == 0) *U_count = total;
+  if (threadIdx.x / 64 % kUnionCtas != blockIdx.x) return;
   int o = incl - mine;
 #pragma unroll
   for (int q = 0; q < kUnionMaxWW; ++q) {
@@ -340,7 +346,6 @@ __global__ void __launch_bounds__(1024) union_list_kernel(const uint32_t* member
       m &= m - 1;
     }
   }
-  if (threadIdx.x == 0) *U_count = total;
 }
 
 template <typename T, int BT>
@@ -452,7 +457,7 @@ cudaError_t launch_union(const int32_t* idx, int cap, const int32_t* count, int 
     union_rows_kernel<<<B, 1024, words * sizeof(uint32_t), stream>>>(idx, cap, count, N, member, hdr);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    union_list_kernel<<<1, 1024, 0, stream>>>(member, B, N, U, U_count, slot_of);
+    union_list_kernel<<<kUnionCtas, 1024, 0, stream>>>(member, B, N, U, U_count, slot_of);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(2);
     return e;
