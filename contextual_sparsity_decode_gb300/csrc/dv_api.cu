@@ -215,7 +215,7 @@ struct Q4Ws {
 Q4Ws carve_q4_mlp(Carver& c, int B, int d, int N, int cap) {
   Q4Ws w{};
   w.pieces = c.take<uint8_t>((size_t)6 * B * ((d + 127) / 128 * 128));
-  w.act = c.take<float>((size_t)B * (((B == 1 ? cap : mlp_union_cap(B, N, cap)) + 3) & ~3) + 16);
+  w.act = c.take<float>((size_t)B * (((size_t)(B == 1 ? cap : mlp_union_cap(B, N, cap)) + 3) & ~(size_t)3) + 16);
   w.part = c.take<float>(q4_part_floats(B, d));
   if (B > 1) {
     w.U = c.take<int32_t>((size_t)N);

@@ -19,7 +19,10 @@
 // The shares' sums go to the workspace and q4_join_kernel adds them in order.
 //
 // On m16n8k16 products (3.5 cycles an SM each, three for 16 rows by 16 elements by 8 vectors)
-// 16 vectors by 16050 of 28672 rows of 7168 took 68 us.
+// 16 vectors by 16050 of 28672 rows of 7168 took 68 us, here 59 (alone under a profiler; groups
+// of 64, which make the coefficients twice; 32 vectors with both products 245 and 187).  Bound
+// by the chain of a step (codes opened, coefficients made, products, their end): 1800 cycles,
+// of which the two are 900.  A list of 600 rows is 2 us slower than it was there: fewer and longer shares.
 
 #include <climits>
 
