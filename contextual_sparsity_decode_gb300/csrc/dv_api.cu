@@ -224,7 +224,11 @@ Q4Ws carve_q4_mlp(Carver& c, int B, int d, int N, int cap) {
   }
   return w;
 }
-uint8_t* carve_q4_matvec(Carver& c, int B, int d) { return c.take<uint8_t>((size_t)6 * B * ((d + 127) / 128 * 128)); }
+uint8_t* carve_q4_matvec(Carver& c, int B, int d, float** part) {
+  uint8_t* pieces = c.take<uint8_t>((size_t)6 * B * ((d + 127) / 128 * 128));
+  *part = c.take<float>(q4_tc_part_floats(B));
+  return pieces;
+}
 
 // ---- validation ---------------------------------------------------------------------
 
@@ -467,7 +471,8 @@ dv_status dv_q4_quantize(const void* W, int N, int d, dv_dtype dt, int group, vo
 dv_status dv_q4_matvec_workspace_size(int B, int d, int N, size_t* bytes) {
   if (!bytes || !q4_shape_ok(B, d, N, kQ4MaxN)) return DV_ERR_INVALID_ARG;
   Carver c(nullptr);
-  carve_q4_matvec(c, B, d);
+  float* part;
+  carve_q4_matvec(c, B, d, &part);
   *bytes = c.size();
   return DV_OK;
 }
@@ -480,15 +485,16 @@ dv_status dv_q4_matvec(const void* y, int B, int d, int N, const dv_q4* W, dv_dt
   const dv_status st = check_q4(W);
   if (st != DV_OK) return st;
   if (!q4_shape_ok(B, d, N, kQ4MaxN) || d % vec_of(dt)) return DV_ERR_INVALID_ARG;
+  float* part;
   Carver meas(nullptr);
-  carve_q4_matvec(meas, B, d);
+  carve_q4_matvec(meas, B, d, &part);
   if (!ws_ok(ws, ws_bytes, meas.size())) return DV_ERR_WORKSPACE;
   Carver c(ws);
   Q4MatvecLaunch L{};
   L.y = y; L.B = B; L.d = d; L.N = N;
   L.q = static_cast<const uint8_t*>(W->q); L.scale = W->scale; L.group = W->group;
   L.out = out; L.accumulate = accumulate ? 1 : 0;
-  L.pieces = carve_q4_matvec(c, B, d);
+  L.pieces = carve_q4_matvec(c, B, d, &L.part);
   L.hdr = static_cast<WsHeader*>(ws);
   cudaError_t e = launch_q4_matvec(L, dt, stream);
   return e == cudaSuccess ? DV_OK : cuda_fail(e);

@@ -359,6 +359,7 @@ struct Q4Rows {
   float* act; int ld_act;               // listed: max(0, product), B rows ld_act apart (a multiple of 4)
   float* out; int accumulate;           // all rows: [B][N]
   WsHeader* hdr; long long wait_ns;
+  float* part; int split;               // k_q4_tc.cu: q4_tc_part_floats, sums of cut tiles; all rows only
   int early;                            // list and weights are read before the wait
   const void* y;                        // [B][d]
   int blocks, groups;                   // of a row
@@ -383,6 +384,7 @@ struct Q4MatvecLaunch {
   const uint8_t* q; const void* scale; int group;
   float* out; int accumulate;
   void* pieces;                         // DV_F32: 3 B rows of whole blocks, 16 bits
+  float* part;                          // q4_tc_part_floats
   WsHeader* hdr;
 };
 struct Q4MlpLaunch {
@@ -397,7 +399,8 @@ struct Q4MlpLaunch {
   void* pieces;
 };
 // Three and more vectors of a 16-bit type, the first kind of product (k_q4_tc.cu).
-bool q4_tc_supported(int B, int d, dv_dtype dt);
+size_t q4_tc_part_floats(int B);
+bool q4_tc_takes(const Q4Rows& a, dv_dtype dt);
 // The second kind for three and more vectors (k_q4_tc_cols.cu).
 cudaError_t launch_q4_tc_cols(const Q4Cols& a, cudaStream_t stream);
 cudaError_t launch_q4_tc_rows(const Q4Rows& a, dv_dtype dt, WsHeader* hdr, bool pdl, cudaStream_t stream);

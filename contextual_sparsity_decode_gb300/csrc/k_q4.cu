@@ -2,7 +2,7 @@
 // quantisation, the choice among the kernels of both kinds of product, and the
 // m16n8k16 form of the first.
 //   with rows (all, or a list's)   one and two vectors: k_q4_vec.cu; three to 32 of a 16-bit
-//                                  type: k_q4_tc.cu; the rest here
+//                                  type, many rows: k_q4_tc.cu; the rest here
 //   sums of listed rows            one and two vectors: k_q4_vec.cu; more: k_q4_tc_cols.cu
 //
 // Layout.  A row is blocks of 128 elements in 64 bytes.  Word w of a block
@@ -249,8 +249,8 @@ __global__ void __launch_bounds__(kThreads) q4_pieces_kernel(const float* __rest
 }
 
 // A CTA takes 16 rows, its warp p the rows' blocks p, p + 8, ...  For what neither k_q4_vec.cu
-// nor k_q4_tc.cu takes: three and more 32-bit vectors, rows of less than 64 elements, and two
-// vectors of more than its shared memory holds.
+// nor k_q4_tc.cu takes: three and more vectors with few rows, or of 32 bits, or of less than 64
+// elements, and two vectors of more than its shared memory holds.
 constexpr int kAhead = 4;   // blocks whose loads are issued before the first is used
 
 template <typename S, typename P, int NT, bool kList>
@@ -406,7 +406,7 @@ cudaError_t launch_rows(Q4Rows a, const void* y, void* pieces, dv_dtype dt, bool
   a.pitch = (size_t)a.blocks * kBlockBytes;
   a.groups = (a.d + a.group - 1) / a.group;
   if (q4_vec_supported(a.B, a.d)) return launch_q4_vec_rows(a, dt, pdl, stream);
-  if (q4_tc_supported(a.B, a.d, dt)) return launch_q4_tc_rows(a, dt, a.hdr, pdl, stream);
+  if (q4_tc_takes(a, dt)) return launch_q4_tc_rows(a, dt, a.hdr, pdl, stream);
   if (dt == DV_F32) {
     const int ld = a.blocks * 128;
     const cudaError_t e = launch_k(q4_pieces_kernel, dim3((ld + kThreads - 1) / kThreads, a.B), dim3(kThreads), 0, stream,
@@ -470,7 +470,7 @@ cudaError_t launch_q4_quantize(const void* W, int N, int d, dv_dtype dt, int gro
 cudaError_t launch_q4_matvec(const Q4MatvecLaunch& L, dv_dtype dt, cudaStream_t stream) {
   Q4Rows a{};
   a.q = L.q; a.scale = L.scale; a.group = L.group; a.B = L.B; a.d = L.d; a.N = L.N;
-  a.out = L.out; a.accumulate = L.accumulate; a.hdr = L.hdr;
+  a.out = L.out; a.accumulate = L.accumulate; a.part = L.part; a.hdr = L.hdr;
   return launch_rows(a, L.y, L.pieces, dt, true, stream);
 }
 

@@ -56,6 +56,31 @@ template <typename T> __device__ __forceinline__ float of_raw(unsigned short h) 
   return Elem<T>::to_f(*reinterpret_cast<const T*>(&h));
 }
 
+// CTA c's part of the work: stages [c.lo, c.hi) of all tiles' stages in order, or whole tiles.
+// With `split`, tiles that parts meet inside are written to the workspace, at most
+// two a CTA, [CTA][its first or its last][vector][row], and q4_tc_join_kernel adds them in order.
+struct Part {
+  int lo, hi;   // (2^17 tiles of 64 stages at most, times 152: 32 bits)
+  __device__ Part(int c, int ctas, int tiles, int stages, int split) {
+    const int all = split ? tiles * stages : tiles, unit = split ? 1 : stages;
+    lo = all * c / ctas * unit;
+    hi = all * (c + 1) / ctas * unit;
+  }
+};
+// The next tile of a part: stages [k0, k1) of it.
+struct Walk {
+  int at, hi, stages, tile = 0, k0 = 0, k1 = 0;
+  __device__ Walk(const Part& p, int s) : at(p.lo), hi(p.hi), stages(s) {}
+  __device__ __forceinline__ bool next() {
+    if (at >= hi) return false;
+    tile = at / stages;
+    k0 = at - tile * stages;
+    k1 = min(stages, k0 + (hi - at));
+    at += k1 - k0;
+    return true;
+  }
+};
+
 // two: groups of 64, an accumulator to each half of a block.
 template <typename T, int NB, bool kList, bool two>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -100,6 +125,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = (n + kRowsTile - 1) / kRowsTile;
   const int stages = (a.blocks + kStageBlocks - 1) / kStageBlocks;   // of a tile
 
+  const Part own(blockIdx.x, gridDim.x, tiles, stages, a.split);
+  Walk walk(own, stages);
+
   if (warp < 8) {
     // ---- codes to tensor memory, sums out of it
     const int grp = warp >> 2, r = tid & 127;
@@ -132,8 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int st = 0;
     // (all eight warps go through all tiles, also once a wait has given up: they meet at their end)
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      const int u = tile * kRowsTile + r;
+    while (walk.next()) {
+      const int u = walk.tile * kRowsTile + r;
       int row = u < n ? u : -1;
       if (kList && u < n) {
         row = a.list[u];
@@ -155,10 +183,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (two) sc[j2][two] = ld_raw(a.scale, scales + min(gi + 1, a.groups - 1));
         }
       };
-      ask(0);
+      ask(walk.k0);
 #pragma unroll
       for (int i = 0; i < NB; ++i) acc[i] = 0.f;
-      for (int k = 0; ok && k < stages; ++k, ++st) {
+      for (int k = walk.k0; ok && k < walk.k1; ++k, ++st) {
         const int slot = st % S;
         if (!wait_warp(&full_w[slot], (st / S) & 1, stop, a, 72)) {
           ok = false;
@@ -209,16 +237,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < NB; ++i) red[r * (NB + 1) + i] = acc[i];
       }
       row_groups_sync();
-      if (grp == 0 && u < n && !*stop) {
-        for (int b = 0; b < a.B; ++b) {
-          float sum = 0.f;
+      const bool whole = walk.k1 - walk.k0 == stages;
+      if (grp == 0 && (u < n || !whole) && !*stop) {
+        float* part = a.part + (size_t)(2 * blockIdx.x + (walk.at - (walk.k1 - walk.k0) != own.lo)) * a.B * kRowsTile + r;
 #pragma unroll
-          for (int i = 0; i < NB; ++i) sum = i == b ? acc[i] : sum;   // (registers cannot be indexed)
-          sum += red[r * (NB + 1) + b];
+        for (int b = 0; b < NB; ++b) {   // (registers cannot be indexed: unrolled)
+          if (b >= a.B) break;
+          const float sum = acc[b] + red[r * (NB + 1) + b];
           if (kList) {
             bool live = row >= 0;
             if (live && a.member) live = bit_test(a.member + (size_t)b * a.words, row);
             a.act[(size_t)b * a.ld_act + u] = live ? (sum > 0.f || sum != sum ? sum : 0.f) : 0.f;
+          } else if (!whole) {
+            part[b * kRowsTile] = sum;
           } else {
             float* o = a.out + (size_t)b * a.N + u;
             *o = a.accumulate ? *o + sum : sum;
@@ -233,15 +264,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = tid - 256, c = t & 15, r0 = t >> 4;
     int st = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+    while (ok && walk.next()) {
       int rows[16];
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
-        const int u = min(tile * kRowsTile + r0 + 8 * q, n - 1);
+        const int u = min(walk.tile * kRowsTile + r0 + 8 * q, n - 1);
         const int l = kList ? a.list[u] : u;
         rows[q] = l >= 0 && l < a.N ? l : 0;
       }
-      for (int k = 0; k < stages; ++k, ++st) {
+      for (int k = walk.k0; k < walk.k1; ++k, ++st) {
         const int slot = st % S;
         if (st >= S && !wait_bar(&empty_w[slot], ((st / S) - 1) & 1, stop, a, 73)) {
           ok = false;
@@ -264,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int st = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
-        for (int k = 0; k < stages; ++k, ++st) {
+      while (ok && walk.next())
+        for (int k = walk.k0; k < walk.k1; ++k, ++st) {
           const int slot = st % S;
           if (st >= S && !wait_bar(&empty_x[slot], ((st / S) - 1) & 1, stop, a, 74)) {
             ok = false;
@@ -289,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t made[2] = {0, 0};
     int st = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
-      for (int k = 0; ok && k < stages; ++k, ++st) {
+    while (ok && walk.next())
+      for (int k = walk.k0; ok && k < walk.k1; ++k, ++st) {
         const int slot = st % S;
         if (!wait_warp(&full_x[slot], (st / S) & 1, stop, a, 75)) {
           ok = false;
@@ -335,6 +366,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 13) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
+// Tiles that parts meet inside: the sums of all their parts, in order.  A CTA to every border
+// between parts and every vector; the first border inside a tile does it.
+__global__ void __launch_bounds__(kRowsTile) q4_tc_join_kernel(const Q4Rows a, int ctas) {
+  const int tiles = (a.N + kRowsTile - 1) / kRowsTile, stages = (a.blocks + kStageBlocks - 1) / kStageBlocks;
+  const int c = blockIdx.x + 1, b = blockIdx.y, all = tiles * stages;
+  const int at = all * c / ctas, t = at / stages, begin = t * stages, before = all * (c - 1) / ctas;
+  const int row = t * kRowsTile + threadIdx.x;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (at == begin || before > begin || row >= a.N) return;
+  // (every CTA has a stage at least, and the tile's last is the last that begins in it)
+  const int end = min(ctas, ((begin + stages) * ctas + all - 1) / all);
+  const size_t pitch = (size_t)a.B * kRowsTile;
+  const float* part = a.part + (size_t)b * kRowsTile + threadIdx.x;
+  float sum = __ldcg(part + (2 * (c - 1) + (before != begin)) * pitch);
+#pragma unroll 4
+  for (int k = c; k < end; ++k) sum += __ldcg(part + 2 * k * pitch);
+  float* o = a.out + (size_t)b * a.N + row;
+  *o = a.accumulate ? *o + sum : sum;
+}
+
 template <typename T, int NB, bool kList, bool two>
 cudaError_t run(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
   static PerDevice attr;   // function attributes are per device
@@ -346,8 +398,12 @@ cudaError_t run(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
   CUtensorMap map;
   if (!make_map(&map, a.y, (uint64_t)a.d, (uint64_t)a.B, NB, !std::is_same<T, __half>::value)) return cudaErrorInvalidValue;
   const int tiles = ((kList ? a.cap : a.N) + kRowsTile - 1) / kRowsTile;
-  return launch_k(q4_tc_rows_kernel<T, NB, kList, two>, dim3(tiles < num_sms ? tiles : num_sms), dim3(kThreads),
-                  Sizes<NB>::kSmem, stream, pdl, 1, map, a);
+  const int units = a.split ? tiles * ((a.blocks + kStageBlocks - 1) / kStageBlocks) : tiles;
+  const int ctas = units < num_sms ? units : num_sms;
+  const cudaError_t e = launch_k(q4_tc_rows_kernel<T, NB, kList, two>, dim3(ctas), dim3(kThreads), Sizes<NB>::kSmem, stream,
+                                 pdl, 1, map, a);
+  if (e != cudaSuccess || !a.split || ctas == 1) return e;
+  return launch_k(q4_tc_join_kernel, dim3(ctas - 1, a.B), dim3(kRowsTile), 0, stream, true, 1, a, ctas);
 }
 template <typename T, int NB>
 cudaError_t run_nb(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
@@ -357,13 +413,31 @@ cudaError_t run_nb(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) 
 
 }  // namespace
 
-bool q4_tc_supported(int B, int d, dv_dtype dt) { return dt != DV_F32 && B >= 3 && B <= 32 && d >= 64; }
+size_t q4_tc_part_floats(int B) { return B < 3 ? 0 : (size_t)2 * kQ4Splits * B * kRowsTile; }
+
+// A step of a tile costs the same for 3 and for 16 vectors and takes a launch's setting up; m16n8k16
+// products cost by the vectors, 16 rows a CTA.  Rows of 5120 in groups of 128, bf16, us, here and there:
+//   vectors    2048 rows     5120          10240         40000
+//         8     9.0   5.6   12.5  11.9   17.8  17.7    43    51
+//        16     9.9   6.0   13.7  13.4   19.2  20.8    45    63
+//        32    13.2   7.8   18.0  22.1   23.3  37.1    51   123
+// (rows of 1024 change sides at about twice as many rows, of 12288 at half).  Tiles of a list are
+// not cut, and a list is mostly shorter than its bound.
+bool q4_tc_takes(const Q4Rows& a, dv_dtype dt) {
+  if (dt == DV_F32 || a.B < 3 || a.d < 64) return false;
+  const int rows = a.list ? a.cap : a.N, some = a.B <= 8 ? 54 : a.B <= 16 ? 34 : 24;   // rows for an SM
+  return rows >= num_sms_current() * (a.list ? some + some / 2 : some);
+}
 
 cudaError_t launch_q4_tc_rows(const Q4Rows& L, dv_dtype dt, WsHeader* hdr, bool pdl, cudaStream_t stream) {
   Q4Rows a = L;
   a.hdr = hdr;
   a.wait_ns = wait_limit_ns();
-  const int num_sms = num_sms_current();
+  const int sms = num_sms_current(), num_sms = sms < kQ4Splits ? sms : kQ4Splits;
+  // Tiles are cut where whole ones would leave the SMs idle for a sixth of the time or more (32 x 28672
+  // x 7168, 224 tiles: 59.5 us whole, 53.4 cut; 8 x 40000 x 5120, 313: 52 and 43)
+  const int tiles = (a.N + kRowsTile - 1) / kRowsTile, turns = (tiles + num_sms - 1) / num_sms;
+  a.split = !a.list && tiles * 20 < turns * num_sms * 17 ? 1 : 0;
   if (dt == DV_F16) return a.B <= 16 ? run_nb<__half, 16>(a, pdl, num_sms, stream) : run_nb<__half, 32>(a, pdl, num_sms, stream);
   return a.B <= 16 ? run_nb<__nv_bfloat16, 16>(a, pdl, num_sms, stream) : run_nb<__nv_bfloat16, 32>(a, pdl, num_sms, stream);
 }

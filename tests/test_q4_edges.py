@@ -334,3 +334,70 @@ def test_one_vectors_nan_is_its_own(B, dt):
     W2.scale[row] = 1.0   # (no list of the others names it)
     ref, tol = mlp_reference(y[others], W1, W2, idx[others], cnt[others])
     assert np.all(np.abs(out[others].double().cpu().numpy() - ref) <= tol)
+
+
+# ---- three and more vectors with many rows (tensor cores), in 64 bits on the GPU
+
+
+def opened_on_gpu(W):
+    return torch.cat([gpu_opened(W, torch.arange(n, min(W.N, n + 4096), device="cuda")) for n in range(0, W.N, 4096)])
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("B,N,d,group", [
+    (3, 8300, 64, 64), (3, 8300, 72, 128), (8, 8321, 512, 64), (5, 9000, 520, 128), (8, 19456, 1000, 128), (7, 19457, 136, 64),
+    (9, 5200, 1096, 64), (16, 5200, 128, 128), (16, 12345, 2056, 64), (17, 3700, 200, 64), (32, 3700, 1544, 128),
+    (32, 9999, 640, 64), (31, 39000, 328, 128), (20, 4000, 5000, 64)])
+def test_matvec_of_many_rows(dt, B, N, d, group):
+    W, y = matrix(N, d, dt, group, 1), vectors(B, d, dt)
+    ws = dv.workspace(dv.dv_q4_matvec_workspace_size(B, d, N))
+    out = torch.full((B, N), float("nan"), device="cuda")
+    dv.dv_q4_matvec(y, W, out, ws)
+    W64, y64, blocks = opened_on_gpu(W), y.double(), (d + 127) // 128
+    ref = y64 @ W64.T
+    # (a cut tile's parts are added in fp32, one rounding each: fewer than the blocks)
+    tol = (160 + 5 * blocks) * EPS * (y64.abs() @ W64.abs().T) + 1e-38
+    assert bool(((out.double() - ref).abs() <= tol).all())
+    again, more = torch.empty(B, N, device="cuda"), torch.ones(B, N, device="cuda")
+    dv.dv_q4_matvec(y, W, again, ws)
+    assert torch.equal(out, again)
+    dv.dv_q4_matvec(y, W, more, ws, accumulate=True)
+    assert torch.equal(more, out + 1)
+    assert dv.dv_check(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("B,N,d,k,groups", [(3, 20000, 328, 4200, (64, 128)), (8, 30000, 1024, 1600, (128, 64)), (16, 20000, 136, 500, (64, 64)),
+                                            (32, 16000, 520, 200, (128, 128)), (25, 9000, 64, 9000, (64, 128))])
+def test_mlp_of_many_rows(dt, B, N, d, k, groups):
+    W1, W2, y = matrix(N, d, dt, groups[0], 1), matrix(N, d, dt, groups[1], 2), vectors(B, d, dt)
+    idx, cnt = lists(B, N, k, counts=[0, k + 5] + [k - 3 * (b % 7) for b in range(B - 2)])
+    idx[2, 3] = N                                   # outside: skipped
+    ws = dv.workspace(dv.dv_q4_sparse_mlp_workspace_size(B, d, N, k))
+    out = torch.zeros(B, d, device="cuda")
+    dv.dv_q4_sparse_mlp(y, W1, W2, idx.cuda(), cnt.cuda(), out, ws)
+    status, _ = dv.dv_check(ws)
+    assert status != 0
+    A, C = opened_on_gpu(W1), opened_on_gpu(W2)
+    blocks, union = (d + 127) // 128, min(N, B * k)
+    for b in range(B):
+        rows = idx[b, :min(int(cnt[b]), k)].long()
+        rows = rows[rows < N].cuda()
+        x = y[b].double()
+        a = torch.relu(A[rows] @ x)
+        off = (160 + 4 * blocks) * EPS * (A[rows].abs() @ x.abs())
+        tol = off @ C[rows].abs() + (3 * 17 * (union // 16 + 1) + 32) * EPS * ((a + off) @ C[rows].abs()) + 1e-38
+        assert bool(((out[b].double() - a @ C[rows]).abs() <= tol).all())
+    assert bool((out[0] == 0).all())
+
+
+def test_one_vectors_nan_is_its_own_with_many_rows():
+    B, N, d = 12, 9001, 384
+    W, y = matrix(N, d, "bf16", 64), vectors(B, d, "bf16")
+    W.scale[4321] = float("nan")
+    y[5, 100] = float("inf")
+    out = torch.zeros(B, N, device="cuda")
+    dv.dv_q4_matvec(y, W, out, dv.workspace(dv.dv_q4_matvec_workspace_size(B, d, N)))
+    finite = torch.isfinite(out)
+    finite[5], finite[:, 4321] = True, True
+    assert bool(finite.all()) and bool(torch.isnan(out[:, 4321]).all()) and not bool(torch.isfinite(out[5]).any())
