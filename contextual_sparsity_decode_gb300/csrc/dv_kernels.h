@@ -364,7 +364,7 @@ struct Q4Rows {
   const void* y;                        // [B][d]
   int blocks, groups;                   // of a row
   size_t pitch;
-  // k_q4.cu: the vectors as columns of 16-bit values
+  // k_q4.cu, k_q4_tc.cu: the vectors as columns of 16-bit values
   const void* x; int cols, ldx, x_len;
 };
 // Second kind: sums of listed rows.
@@ -398,9 +398,9 @@ struct Q4MlpLaunch {
   float* part;                          // q4_part_floats
   void* pieces;
 };
-// Three and more vectors of a 16-bit type, the first kind of product (k_q4_tc.cu).
+// Several vectors by many rows, the first kind of product (k_q4_tc.cu).
 size_t q4_tc_part_floats(int B);
-bool q4_tc_takes(const Q4Rows& a, dv_dtype dt);
+bool q4_tc_takes(const Q4Rows& a);
 // The second kind for three and more vectors (k_q4_tc_cols.cu).
 cudaError_t launch_q4_tc_cols(const Q4Cols& a, cudaStream_t stream);
 cudaError_t launch_q4_tc_rows(const Q4Rows& a, dv_dtype dt, WsHeader* hdr, bool pdl, cudaStream_t stream);

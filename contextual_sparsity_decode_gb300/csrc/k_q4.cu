@@ -1,8 +1,8 @@
 // Matrices in 4 bits with group scales, w[n][t] = (code[n][t] - 8) s[n][t / G]:
 // quantisation, the choice among the kernels of both kinds of product, and the
 // m16n8k16 form of the first.
-//   with rows (all, or a list's)   one and two vectors: k_q4_vec.cu; three to 32 of a 16-bit
-//                                  type, many rows: k_q4_tc.cu; the rest here
+//   with rows (all, or a list's)   one and two vectors: k_q4_vec.cu; three to 32 by many
+//                                  rows: k_q4_tc.cu; the rest here
 //   sums of listed rows            one and two vectors: k_q4_vec.cu; more: k_q4_tc_cols.cu
 //
 // Layout.  A row is blocks of 128 elements in 64 bytes.  Word w of a block
@@ -249,8 +249,8 @@ __global__ void __launch_bounds__(kThreads) q4_pieces_kernel(const float* __rest
 }
 
 // A CTA takes 16 rows, its warp p the rows' blocks p, p + 8, ...  For what neither k_q4_vec.cu
-// nor k_q4_tc.cu takes: three and more vectors with few rows, or of 32 bits, or of less than 64
-// elements, and two vectors of more than its shared memory holds.
+// nor k_q4_tc.cu takes: three and more vectors with few rows or of less than 64 elements, and
+// two vectors of more than its shared memory holds with few rows.
 constexpr int kAhead = 4;   // blocks whose loads are issued before the first is used
 
 template <typename S, typename P, int NT, bool kList>
@@ -406,7 +406,6 @@ cudaError_t launch_rows(Q4Rows a, const void* y, void* pieces, dv_dtype dt, bool
   a.pitch = (size_t)a.blocks * kBlockBytes;
   a.groups = (a.d + a.group - 1) / a.group;
   if (q4_vec_supported(a.B, a.d)) return launch_q4_vec_rows(a, dt, pdl, stream);
-  if (q4_tc_takes(a, dt)) return launch_q4_tc_rows(a, dt, a.hdr, pdl, stream);
   if (dt == DV_F32) {
     const int ld = a.blocks * 128;
     const cudaError_t e = launch_k(q4_pieces_kernel, dim3((ld + kThreads - 1) / kThreads, a.B), dim3(kThreads), 0, stream,
@@ -422,12 +421,14 @@ cudaError_t launch_rows(Q4Rows a, const void* y, void* pieces, dv_dtype dt, bool
       if (r.out) r.out += (size_t)b0 * r.N;
       if (r.act) r.act += (size_t)b0 * r.ld_act;
       if (r.member) r.member += (size_t)b0 * r.words;
-      const cudaError_t er = run_rows_nt<float, __nv_bfloat16>(r, true, stream);
+      const cudaError_t er = q4_tc_takes(r) ? launch_q4_tc_rows(r, dt, r.hdr, true, stream)
+                                            : run_rows_nt<float, __nv_bfloat16>(r, true, stream);
       if (er != cudaSuccess) return er;
     }
     return cudaSuccess;
   }
   a.x = y; a.cols = a.B; a.ldx = a.d; a.x_len = a.d;
+  if (q4_tc_takes(a)) return launch_q4_tc_rows(a, dt, a.hdr, pdl, stream);
   return dt == DV_F16 ? run_rows_nt<__half, __half>(a, pdl, stream)
                       : run_rows_nt<__nv_bfloat16, __nv_bfloat16>(a, pdl, stream);
 }

@@ -1,5 +1,5 @@
-// Matrices in 4 bits (layout: k_q4.cu), three and more vectors of a 16-bit type: products
-// with rows of the matrix on the 5th-generation tensor cores.
+// Matrices in 4 bits (layout: k_q4.cu), several vectors (32-bit ones as three bf16 pieces): products
+// with many rows of the matrix on the 5th-generation tensor cores.
 //
 // A tile is 128 rows; a product is a block of 128 elements of them (M = 128, K = 128)
 // with the vectors (N = 16 or 32).  The codes of a block go from registers to tensor
@@ -47,14 +47,20 @@ struct Sizes {
 __device__ __forceinline__ void row_groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // A scale as it is stored (asked for here and not where it is used), and its value.
-__device__ __forceinline__ unsigned short ld_raw(const void* s, size_t i) {
+template <typename T> struct Raw {
   unsigned short h;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(h) : "l"(static_cast<const uint16_t*>(s) + i));
-  return h;
-}
-template <typename T> __device__ __forceinline__ float of_raw(unsigned short h) {
-  return Elem<T>::to_f(*reinterpret_cast<const T*>(&h));
-}
+  __device__ __forceinline__ void ask(const void* s, size_t i) {
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(h) : "l"(static_cast<const uint16_t*>(s) + i));
+  }
+  __device__ __forceinline__ float value() const { return Elem<T>::to_f(*reinterpret_cast<const T*>(&h)); }
+};
+template <> struct Raw<float> {
+  float f;
+  __device__ __forceinline__ void ask(const void* s, size_t i) {
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f) : "l"(static_cast<const float*>(s) + i));
+  }
+  __device__ __forceinline__ float value() const { return f; }
+};
 
 // CTA c's part of the work: stages [c.lo, c.hi) of all tiles' stages in order, or whole tiles.
 // With `split`, tiles that parts meet inside are written to the workspace, at most
@@ -81,12 +87,14 @@ struct Walk {
   }
 };
 
-// two: groups of 64, an accumulator to each half of a block.
-template <typename T, int NB, bool kList, bool two>
+// two: groups of 64, an accumulator to each half of a block.  S: the scales' type; float: T is
+// bf16 and the columns are the B vectors' first pieces, their second and their third.
+template <typename T, typename S_, int NB, bool kList, bool two>
 __global__ void __launch_bounds__(kThreads, 1)
     q4_tc_rows_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ Q4Rows a) {
   using Z = Sizes<NB>;
   constexpr int S = Z::kStages;
+  constexpr bool kPieces = sizeof(S_) == 4;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full_w[S], empty_w[S], full_x[S], empty_x[S], ready[2][2], done[2][2], fin;
   __shared__ uint32_t tmem_base;
@@ -174,13 +182,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // scales of the group's two blocks of a stage, asked for a stage ahead (at their block they
       // were waited for, since a select takes them to their slot's register: 61.5 us for 32 x
       // 28672 x 7168)
-      unsigned short sc[2][two ? 2 : 1];
+      Raw<S_> sc[2][two ? 2 : 1];
       const auto ask = [&](int k) {
 #pragma unroll
         for (int j2 = 0; j2 < 2; ++j2) {
           const int kb = min(k * kStageBlocks + 2 * j2 + grp, a.blocks - 1), gi = two ? 2 * kb : kb;
-          sc[j2][0] = ld_raw(a.scale, scales + gi);
-          if (two) sc[j2][two] = ld_raw(a.scale, scales + min(gi + 1, a.groups - 1));
+          sc[j2][0].ask(a.scale, scales + gi);
+          if (two) sc[j2][two].ask(a.scale, scales + min(gi + 1, a.groups - 1));
         }
       };
       ask(walk.k0);
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j2 = 0; j2 < 2; ++j2)
 #pragma unroll
-          for (int h = 0; h < (two ? 2 : 1); ++h) f[j2][h] = of_raw<T>(sc[j2][h]);
+          for (int h = 0; h < (two ? 2 : 1); ++h) f[j2][h] = sc[j2][h].value();
         ask(k + 1);
 #pragma unroll
         for (int j2 = 0; j2 < 2; ++j2) {
@@ -240,10 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = walk.k1 - walk.k0 == stages;
       if (grp == 0 && (u < n || !whole) && !*stop) {
         float* part = a.part + (size_t)(2 * blockIdx.x + (walk.at - (walk.k1 - walk.k0) != own.lo)) * a.B * kRowsTile + r;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {   // (registers cannot be indexed: unrolled)
-          if (b >= a.B) break;
-          const float sum = acc[b] + red[r * (NB + 1) + b];
+        const auto put = [&](int b, float sum) {
           if (kList) {
             bool live = row >= 0;
             if (live && a.member) live = bit_test(a.member + (size_t)b * a.words, row);
@@ -254,7 +259,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* o = a.out + (size_t)b * a.N + u;
             *o = a.accumulate ? *o + sum : sum;
           }
+        };
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {   // (registers cannot be indexed: unrolled)
+          if (b >= (kPieces ? 3 * a.B : a.B)) break;
+          float sum = acc[b] + red[r * (NB + 1) + b];
+          if (kPieces) {   // (a thread's own row: the least pieces' columns come last)
+            red[r * (NB + 1) + b] = sum;
+            continue;
+          }
+          put(b, sum);
         }
+        if (kPieces)
+          for (int b = 0; b < a.B; ++b) {
+            const float* p = red + r * (NB + 1) + b;
+            put(b, p[2 * a.B] + p[a.B] + p[0]);
+          }
       }
       row_groups_sync();
     }
@@ -387,33 +407,33 @@ __global__ void __launch_bounds__(kRowsTile) q4_tc_join_kernel(const Q4Rows a, i
   *o = a.accumulate ? *o + sum : sum;
 }
 
-template <typename T, int NB, bool kList, bool two>
+template <typename T, typename S, int NB, bool kList, bool two>
 cudaError_t run(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
   static PerDevice attr;   // function attributes are per device
   const cudaError_t ea = (cudaError_t)attr.get(current_device(), [] {
-    return (int)cudaFuncSetAttribute(q4_tc_rows_kernel<T, NB, kList, two>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return (int)cudaFuncSetAttribute(q4_tc_rows_kernel<T, S, NB, kList, two>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)Sizes<NB>::kSmem);
   });
   if (ea != cudaSuccess) return ea;
   CUtensorMap map;
-  if (!make_map(&map, a.y, (uint64_t)a.d, (uint64_t)a.B, NB, !std::is_same<T, __half>::value)) return cudaErrorInvalidValue;
+  if (!make_map(&map, a.x, (uint64_t)a.ldx, (uint64_t)a.cols, NB, !std::is_same<T, __half>::value)) return cudaErrorInvalidValue;
   const int tiles = ((kList ? a.cap : a.N) + kRowsTile - 1) / kRowsTile;
   const int units = a.split ? tiles * ((a.blocks + kStageBlocks - 1) / kStageBlocks) : tiles;
   const int ctas = units < num_sms ? units : num_sms;
-  const cudaError_t e = launch_k(q4_tc_rows_kernel<T, NB, kList, two>, dim3(ctas), dim3(kThreads), Sizes<NB>::kSmem, stream,
+  const cudaError_t e = launch_k(q4_tc_rows_kernel<T, S, NB, kList, two>, dim3(ctas), dim3(kThreads), Sizes<NB>::kSmem, stream,
                                  pdl, 1, map, a);
   if (e != cudaSuccess || !a.split || ctas == 1) return e;
   return launch_k(q4_tc_join_kernel, dim3(ctas - 1, a.B), dim3(kRowsTile), 0, stream, true, 1, a, ctas);
 }
-template <typename T, int NB>
+template <typename T, typename S, int NB>
 cudaError_t run_nb(const Q4Rows& a, bool pdl, int num_sms, cudaStream_t stream) {
-  if (a.list) return a.group == 64 ? run<T, NB, true, true>(a, pdl, num_sms, stream) : run<T, NB, true, false>(a, pdl, num_sms, stream);
-  return a.group == 64 ? run<T, NB, false, true>(a, pdl, num_sms, stream) : run<T, NB, false, false>(a, pdl, num_sms, stream);
+  if (a.list) return a.group == 64 ? run<T, S, NB, true, true>(a, pdl, num_sms, stream) : run<T, S, NB, true, false>(a, pdl, num_sms, stream);
+  return a.group == 64 ? run<T, S, NB, false, true>(a, pdl, num_sms, stream) : run<T, S, NB, false, false>(a, pdl, num_sms, stream);
 }
 
 }  // namespace
 
-size_t q4_tc_part_floats(int B) { return B < 3 ? 0 : (size_t)2 * kQ4Splits * B * kRowsTile; }
+size_t q4_tc_part_floats(int B) { return B < 2 ? 0 : (size_t)2 * kQ4Splits * B * kRowsTile; }
 
 // A step of a tile costs the same for 3 and for 16 vectors and takes a launch's setting up; m16n8k16
 // products cost by the vectors, 16 rows a CTA.  Rows of 5120 in groups of 128, bf16, us, here and there:
@@ -423,9 +443,10 @@ size_t q4_tc_part_floats(int B) { return B < 3 ? 0 : (size_t)2 * kQ4Splits * B *
 //        32    13.2   7.8   18.0  22.1   23.3  37.1    51   123
 // (rows of 1024 change sides at about twice as many rows, of 12288 at half).  Tiles of a list are
 // not cut, and a list is mostly shorter than its bound.
-bool q4_tc_takes(const Q4Rows& a, dv_dtype dt) {
-  if (dt == DV_F32 || a.B < 3 || a.d < 64) return false;
-  const int rows = a.list ? a.cap : a.N, some = a.B <= 8 ? 54 : a.B <= 16 ? 34 : 24;   // rows for an SM
+// 32-bit vectors count three times.
+bool q4_tc_takes(const Q4Rows& a) {
+  if (a.d < 64) return false;
+  const int rows = a.list ? a.cap : a.N, some = a.cols <= 8 ? 54 : a.cols <= 16 ? 34 : 24;   // rows for an SM
   return rows >= num_sms_current() * (a.list ? some + some / 2 : some);
 }
 
@@ -438,8 +459,13 @@ cudaError_t launch_q4_tc_rows(const Q4Rows& L, dv_dtype dt, WsHeader* hdr, bool 
   // x 7168, 224 tiles: 59.5 us whole, 53.4 cut; 8 x 40000 x 5120, 313: 52 and 43)
   const int tiles = (a.N + kRowsTile - 1) / kRowsTile, turns = (tiles + num_sms - 1) / num_sms;
   a.split = !a.list && tiles * 20 < turns * num_sms * 17 ? 1 : 0;
-  if (dt == DV_F16) return a.B <= 16 ? run_nb<__half, 16>(a, pdl, num_sms, stream) : run_nb<__half, 32>(a, pdl, num_sms, stream);
-  return a.B <= 16 ? run_nb<__nv_bfloat16, 16>(a, pdl, num_sms, stream) : run_nb<__nv_bfloat16, 32>(a, pdl, num_sms, stream);
+  const bool few = a.cols <= 16;
+  if (dt == DV_F32)
+    return few ? run_nb<__nv_bfloat16, float, 16>(a, pdl, num_sms, stream) : run_nb<__nv_bfloat16, float, 32>(a, pdl, num_sms, stream);
+  if (dt == DV_F16)
+    return few ? run_nb<__half, __half, 16>(a, pdl, num_sms, stream) : run_nb<__half, __half, 32>(a, pdl, num_sms, stream);
+  return few ? run_nb<__nv_bfloat16, __nv_bfloat16, 16>(a, pdl, num_sms, stream)
+             : run_nb<__nv_bfloat16, __nv_bfloat16, 32>(a, pdl, num_sms, stream);
 }
 
 }  // namespace dv

@@ -256,7 +256,7 @@ dv_status dv_q4_matvec_workspace_size(int B, int d, int N, size_t* bytes);
  * vector NaN or infinite and no other's.  Like dv_layernorm's, its first
  * kernel may be started before the kernel ahead of the call has ended and waits
  * for it before it reads or writes anything.
- * Device errors: DV_ERR_TIMEOUT (see dv_set_wait_limit_ns; three and more vectors).
+ * Device errors: DV_ERR_TIMEOUT (see dv_set_wait_limit_ns; two and more vectors).
  * Limits: B <= 32, N <= 16777216, d <= 32768. */
 dv_status dv_q4_matvec(const void* y, int B, int d, int N, const dv_q4* W,
                        dv_dtype dt, float* out, int accumulate,
@@ -550,9 +550,11 @@ int dv_set_launch_overlap(int level);
 
 /* Bound of every device-side wait (no counterpart in the pages): the
  * one-launch MLP's wait for its up-projection CTAs, the tensor-core paths'
- * pipeline waits (those of dv_tree_attn, and of dv_q4_matvec and dv_q4_sparse_mlp
- * for three and more vectors, among them) and the waits for copies of the streaming MLP, dv_beam_select and dv_sample give up after `ns` nanoseconds of the GPU's
- * global timer, record DV_ERR_TIMEOUT in the workspace (read it with dv_check)
+ * pipeline waits (those of dv_tree_attn, and of dv_q4_matvec and
+ * dv_q4_sparse_mlp for two and more vectors, among them) and the waits for
+ * copies of the streaming MLP, dv_beam_select and dv_sample give up after `ns`
+ * nanoseconds of the GPU's global timer, record DV_ERR_TIMEOUT in the
+ * workspace (read it with dv_check)
  * and unwind; the kernel still waits for its own tensor-core and copy work in
  * flight before it exits.  ns <= 0 restores the default of one second.
  * Read at launch (a captured graph keeps the value it was captured with);

@@ -343,9 +343,9 @@ def opened_on_gpu(W):
     return torch.cat([gpu_opened(W, torch.arange(n, min(W.N, n + 4096), device="cuda")) for n in range(0, W.N, 4096)])
 
 
-@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("B,N,d,group", [
-    (3, 8300, 64, 64), (3, 8300, 72, 128), (8, 8321, 512, 64), (5, 9000, 520, 128), (8, 19456, 1000, 128), (7, 19457, 136, 64),
+    (2, 8300, 20000, 64), (3, 8300, 64, 64), (3, 8300, 72, 128), (8, 8321, 512, 64), (5, 9000, 520, 128), (8, 19456, 1000, 128), (7, 19457, 136, 64),
     (9, 5200, 1096, 64), (16, 5200, 128, 128), (16, 12345, 2056, 64), (17, 3700, 200, 64), (32, 3700, 1544, 128),
     (32, 9999, 640, 64), (31, 39000, 328, 128), (20, 4000, 5000, 64)])
 def test_matvec_of_many_rows(dt, B, N, d, group):
