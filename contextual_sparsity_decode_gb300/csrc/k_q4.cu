@@ -183,14 +183,18 @@ __global__ void __launch_bounds__(kThreads) q4_quantize_kernel(const T* __restri
     const bool quick = fine && sf > 0x1p-100f;
     const float inv = quick ? __frcp_rn(sf) : 0.f, half = 0.5f * sf;
     constexpr float kWhole = 12582912.f;   // 1.5 2^23
-    float r[8];
+    float r[8], most = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       r[e] = __fsub_rn(__fadd_rn(__fmul_rn(f[e], inv), kWhole), kWhole);
-      const float left = __fmaf_rn(-r[e], sf, f[e]);
-      if (fabsf(left) >= half) {
+      most = fmaxf(most, fabsf(__fmaf_rn(-r[e], sf, f[e])));
+    }
+    if (most >= half) {   // (seldom: asked once for a lane's eight elements)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float left = __fmaf_rn(-r[e], sf, f[e]);
         const bool odd = __float_as_int(__fadd_rn(r[e], kWhole)) & 1;
-        if (fabsf(left) > half || odd) r[e] += copysignf(1.f, left);
+        if (fabsf(left) > half || (fabsf(left) == half && odd)) r[e] += copysignf(1.f, left);
       }
     }
     if (!quick) {   // (1 / s or s / 2 would leave the range of fp32, or the scale is 0 or a NaN)
