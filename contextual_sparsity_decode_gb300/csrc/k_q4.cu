@@ -26,7 +26,7 @@
 //
 // Measured on GB300: 5 fp32 vectors with 5001 rows of 5000 14.3 us (0.98 TB/s of codes and
 // scales: latency of two launches and of blocks loaded four ahead); quantisation of 20480 x
-// 5120 bf16 with values 135 us (3.5 TB/s, half of a copy's rate: instructions).
+// 5120 f16 with values 110 us (4.3 TB/s, 0.63 of a copy's rate: instructions).
 
 #include "dv_kernels.h"
 
@@ -120,6 +120,41 @@ __device__ __noinline__ float nearest(float f, float s) {
   return rintf(ratio);
 }
 
+// The largest magnitude among 8 elements as an integer (a NaN's is above infinity's), and 8
+// elements r s of the storage type (r whole, 4 bits: one rounding).
+__device__ __forceinline__ uint32_t top_of(const uint4* w, const float* f, float) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+  return top;
+}
+__device__ __forceinline__ void values_of(const float* r, float s, uint4* o) {
+  float* h = reinterpret_cast<float*>(o);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h[e] = r[e] * s;
+}
+template <typename P>
+__device__ __forceinline__ uint32_t top_of_pairs(const P* p) {
+  const P m = __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
+  return max(__float_as_uint(__low2float(m)), __float_as_uint(__high2float(m))) & 0x7fffffffu;
+}
+__device__ __forceinline__ uint32_t top_of(const uint4* w, const float*, __half) {
+  return top_of_pairs(reinterpret_cast<const __half2*>(w));
+}
+__device__ __forceinline__ uint32_t top_of(const uint4* w, const float*, __nv_bfloat16) {
+  return top_of_pairs(reinterpret_cast<const __nv_bfloat162*>(w));
+}
+__device__ __forceinline__ void values_of(const float* r, __half s, uint4* o) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<__half2*>(o)[i] = __hmul2(__floats2half2_rn(r[2 * i], r[2 * i + 1]), __half2half2(s));
+}
+__device__ __forceinline__ void values_of(const float* r, __nv_bfloat16 s, uint4* o) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<__nv_bfloat162*>(o)[i] = __hmul2(__floats2bfloat162_rn(r[2 * i], r[2 * i + 1]), __bfloat162bfloat162(s));
+}
+
 // One half-warp per block of 128 elements, a lane to a word: 8 elements in, one
 // word out; kItems blocks at a time, whose loads are issued together.  The matrix is read
 // once and codes, scales and values are written once.
@@ -158,16 +193,10 @@ __global__ void __launch_bounds__(kThreads) q4_quantize_kernel(const T* __restri
     float f[8];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
+      if (t + v * Elem<T>::kVec >= d) w[k][v] = make_uint4(0, 0, 0, 0);
       unpack<T>(w[k][v], f + v * Elem<T>::kVec);
-      if (t + v * Elem<T>::kVec >= d) {
-#pragma unroll
-        for (int e = 0; e < Elem<T>::kVec; ++e) f[v * Elem<T>::kVec + e] = 0.f;
-      }
     }
-    // largest magnitude as an integer: a NaN's is above infinity's
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+    uint32_t top = top_of(w[k], f, T());
 #pragma unroll
     for (int o = 2; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const uint32_t other = __shfl_xor_sync(0xffffffffu, top, 1);
@@ -179,14 +208,15 @@ __global__ void __launch_bounds__(kThreads) q4_quantize_kernel(const T* __restri
     const float sf = Elem<T>::to_f(sc);
     // round-to-even(f / s): the product with 1 / s, and a step where what it leaves, which is
     // exact, is more than half of s, or half of it and the code odd.  Codes are added up as floats, eight of them to two
-    // whole numbers of 16 bits.  (53 instructions an element took 182 us for 20480 x 5120.)
+    // whole numbers of 16 bits.  (With a division and a correction for every element 20480 x 5120 took 182 us, with the
+    // correction asked for by every element 135.)
     const bool quick = fine && sf > 0x1p-100f;
     const float inv = quick ? __frcp_rn(sf) : 0.f, half = 0.5f * sf;
     constexpr float kWhole = 12582912.f;   // 1.5 2^23
     float r[8], most = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      r[e] = __fsub_rn(__fadd_rn(__fmul_rn(f[e], inv), kWhole), kWhole);
+      r[e] = __fsub_rn(__fmaf_rn(f[e], inv, kWhole), kWhole);
       most = fmaxf(most, fabsf(__fmaf_rn(-r[e], sf, f[e])));
     }
     if (most >= half) {   // (seldom: asked once for a lane's eight elements)
@@ -206,29 +236,26 @@ __global__ void __launch_bounds__(kThreads) q4_quantize_kernel(const T* __restri
         for (int k = 0; k < 8; ++k) r[k] = k == e ? x : r[k];
       }
     }
+    if (!(sf > 0x1p-14f)) {   // (a scale of fewer bits may be far below max / 7: elsewhere |r| <= 7)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = fminf(fmaxf(r[e], -8.f), 7.f);
+    }
     float even = kWhole + 34952.f, odd = kWhole + 34952.f;   // 0x8888: 8 more for each
-    float val[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      r[e] = fminf(fmaxf(r[e], -8.f), 7.f);
       float& sum = e & 1 ? odd : even;
       sum = __fmaf_rn(r[e], (float)(1 << (4 * (e >> 1))), sum);
-      val[e] = fine ? r[e] * sf : __int_as_float(0x7fc00000);
     }
     const uint32_t code = __byte_perm(__float_as_uint(even), __float_as_uint(odd), 0x5410);
     if (!in) continue;
     q[(size_t)i * (kBlockBytes / 4) + word] = code;
     if (t < d && (t % group) == 0) scale[n * groups + t / group] = sc;
     if (values) {
+      uint4 o[kVecs];
+      values_of(r, sc, o);   // (a NaN as the scale: NaNs)
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        if (t + v * Elem<T>::kVec >= d) continue;
-        uint4 o;
-        T* h = reinterpret_cast<T*>(&o);
-#pragma unroll
-        for (int e = 0; e < Elem<T>::kVec; ++e) h[e] = Elem<T>::from_f(val[v * Elem<T>::kVec + e]);
-        *reinterpret_cast<uint4*>(values + n * d + t + v * Elem<T>::kVec) = o;
-      }
+      for (int v = 0; v < kVecs; ++v)
+        if (t + v * Elem<T>::kVec < d) *reinterpret_cast<uint4*>(values + n * d + t + v * Elem<T>::kVec) = o[v];
     }
   }
 }

@@ -14,9 +14,9 @@
 //   warps 8-11       packed rows into a ring of shared-memory stages (four blocks, 256
 //                    bytes of a row), cp.async, 16 lanes to a row
 //   warp 12          the vectors' tiles (TMA), warp 13 the products
-// Measured on GB300: 32 bf16 vectors with 28672 rows of 7168 59.5 us (1.9 TB/s of codes and
+// Measured on GB300: 32 bf16 vectors with 28672 rows of 7168 53.3 us (2.1 TB/s of codes and
 // scales; m16n8k16 products, which read them from registers, took 152).  A block costs a group
-// 1800 cycles, half of them the opening; 224 tiles are two on most of 152 SMs.
+// 1800 cycles, half of them the opening.
 
 #include <climits>
 
