@@ -401,3 +401,21 @@ def test_one_vectors_nan_is_its_own_with_many_rows():
     finite = torch.isfinite(out)
     finite[5], finite[:, 4321] = True, True
     assert bool(finite.all()) and bool(torch.isnan(out[:, 4321]).all()) and not bool(torch.isfinite(out[5]).any())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("counts", [(0, 0, 0, 0), (0, 1, 0, 0), (3, -5, 60, 0), (0, 0, 0, 4400)])
+def test_short_lists_under_a_large_bound(dt, counts):
+    """Lists that leave most CTAs of a grid sized for their bound without rows."""
+    B, N, d, k = 4, 20000, 264, 4400
+    W1, W2, y = matrix(N, d, dt, 64, 1), matrix(N, d, dt, 128, 2), vectors(B, d, dt)
+    idx, cnt = lists(B, N, k, counts=list(counts))
+    start = torch.randn(B, d, generator=torch.Generator().manual_seed(3)).cuda()
+    ws = dv.workspace(dv.dv_q4_sparse_mlp_workspace_size(B, d, N, k))
+    out, more = torch.full((B, d), float("nan"), device="cuda"), start.clone()
+    dv.dv_q4_sparse_mlp(y, W1, W2, idx.cuda(), cnt.cuda(), out, ws)
+    dv.dv_q4_sparse_mlp(y, W1, W2, idx.cuda(), cnt.cuda(), more, ws, accumulate=True)
+    ref, tol = mlp_reference(y, W1, W2, idx, cnt.clamp(min=0))
+    assert np.all(np.abs(out.double().cpu().numpy() - ref) <= tol)
+    assert torch.equal(more, start + out)
+    assert dv.dv_check(ws) == (0, 0)
