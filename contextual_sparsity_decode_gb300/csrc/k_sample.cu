@@ -405,6 +405,7 @@ struct Row {
     constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
     const int groups = (vecs + 31) / 32;
     u64 sum = 0, unused;
+    if (threadIdx.x == 0) sh.found = groups;   // (behind the last)
 #pragma unroll
     for (int q = 0; q < kPer; ++q) sum += (int)threadIdx.x * kPer + q < groups ? sh.group[threadIdx.x * kPer + q] : 0;
     const u64 upto = block_scan(sum, sh.scan, &unused);
@@ -603,6 +604,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleLaunch 
   grid_dep_wait();
   grid_dep_launch();
   __syncthreads();
+  cluster_arrive();   // the others may write here from now on (waited for before the first exchange)
   // The row as 16-byte vectors from the boundary at or below its first token on;
   // the tokens of its first and last vector that are not the row's are -inf.
   const T* x0 = static_cast<const T*>(a.logits) + (size_t)b * a.ld;
@@ -671,6 +673,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleLaunch 
   if (sh.late && tid == 0)   // no copy may be in flight when the CTA ends
     for (int q = 0; q < kChunks; ++q)
       if (!tc::mbar_wait(&sh.full[q], 0, kUnwindNs > a.wait_ns ? kUnwindNs : a.wait_ns)) break;
+  __syncwarp();
+  cluster_wait();   // every CTA of the cluster has begun
   {
     const int t = row.exchange(__float_as_uint(m), bad ? 1 : 0);
     for (uint32_t r = 0; r < row.size; ++r) {
@@ -778,7 +782,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleLaunch 
       return;
     }
     u64 unused;
-    if (found.bin < kBins) cut = find_cut<false>(row, weigh, cut, bins, [](u64 all) { return all; }, &found, &unused);
+    if (found.bin == kBins)
+      cluster_sync();   // fewer than k within reach: the bins have been read by all, and the nucleus may clear them
+    else
+      cut = find_cut<false>(row, weigh, cut, bins, [](u64 all) { return all; }, &found, &unused);
   }
 
   // ---- sums of groups of 32 vectors: kept tokens that weigh `low` at least
