@@ -22,10 +22,10 @@
 //               tokens' weights by groups of 32 vectors, the group and the token.
 // Equal values are taken by their index where the cut passes among them.
 //
-// Measured on GB300: 192 rows of 128001 bf16 logits, nucleus of 0.95, 158 us (0.31 TB/s of the
+// Measured on GB300: 192 rows of 128001 bf16 logits, nucleus of 0.95, 160 us (0.31 TB/s of the
 // logits read; 24 us to the maximum, 40 for every token's weight and bin, the rest
 // in cluster barriers, the refined bin and the draw); 8 rows of 50257 fp32 without
-// filters 9.2 us, one of 32000 f16 with all 12.1: latency of the barriers.
+// filters 9.5 us, one of 32000 f16 with all 12.1: latency of the barriers.
 
 #include <cfloat>
 #include <climits>
