@@ -250,8 +250,8 @@ dv_status dv_q4_matvec_workspace_size(int B, int d, int N, size_t* bytes);
  *     out[b][n] (+)= sum_t w[n][t] y[b][t],
  * y [B][d] in the storage type of the scales, out [B][N] fp32, see
  * dv_sparse_mlp for `accumulate`.  Codes and scales enter as they are.  For one
- * and two vectors y enters in fixed point, 30 bits below the largest magnitude
- * of each group of elements, for three and more as it is; sums are fp32 and
+ * vector, and for two of up to 22528 elements, y enters in fixed point, 30 bits
+ * below the largest magnitude of each group of elements, else as it is; sums are fp32 and
  * results repeat bit for bit.  A NaN or an infinity in y makes the products of that
  * vector NaN or infinite and no other's.  Like dv_layernorm's, its first
  * kernel may be started before the kernel ahead of the call has ended and waits
