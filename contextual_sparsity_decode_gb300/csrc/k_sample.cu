@@ -644,6 +644,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleLaunch 
       sh.late = 1;
       set_error(a.hdr, DV_ERR_TIMEOUT, 61);
     }
+    __syncwarp();   // the other lanes read behind the first one's wait (a shuffle orders no memory)
     // (the first lane's look at it, the warp's: lanes that saw different values would part)
     if (__shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sh.late), 0)) break;
     const int c1 = min(vecs, (q + 1) * chunk);
