@@ -327,9 +327,12 @@ class Q4:
 
     @classmethod
     def of(cls, W: torch.Tensor, group: int = 128, stream=None) -> "Q4":
-        """W [N][d] quantised (dv_q4_quantize)."""
-        out = cls.empty(W.shape[0], W.shape[1], W.dtype, group, W.device)
-        dv_q4_quantize(W, out, stream=stream)
+        """W [N][d] quantised (dv_q4_quantize).  With a stream the buffers are
+        allocated and zero-filled on it too (on the current one the fill could
+        come after the codes)."""
+        with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(_stream(stream))):
+            out = cls.empty(W.shape[0], W.shape[1], W.dtype, group, W.device)
+            dv_q4_quantize(W, out, stream=stream)
         return out
 
 
