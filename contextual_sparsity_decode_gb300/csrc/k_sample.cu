@@ -122,10 +122,11 @@ struct Scale {
     const u64 out = shift > 8 ? (u64)(((w >> min(shift - 9, 31)) + 1) >> 1) : (u64)w << (8 - shift);
     return y >= -40.f ? out : 0;                    // (NaN: x is -inf, or so far below that y is)
   }
-  // Nothing below this weighs `least` or more (1e-4 to the safe side).
+  // Nothing below this weighs `least` or more: what is rounded to it weighs least - 1/2 at
+  // least (1e-4 to the safe side).
   __device__ __forceinline__ float floor_of(u64 least) const {
     if (least == 0) return -INFINITY;
-    const float y = log2f(__ull2float_rn(least)) - (kUnit + 1e-3f);   // < 0
+    const float y = log2f(__ull2float_rn(2 * least - 1)) - (kUnit + 1 + 1e-3f);   // < 0
     return m + (y * 1.0001f / hi - fabsf(m) * 1e-6f);
   }
 };
