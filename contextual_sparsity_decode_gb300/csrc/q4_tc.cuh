@@ -42,7 +42,10 @@ template <> struct Open<__nv_bfloat16> {
 
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* stop, WsHeader* hdr,
                                        long long limit_ns, int code) {
-  for (int i = 0; i < 32; ++i) {   // (a read of the global timer takes about 1000 cycles)
+  // (a read of the global timer takes about 1000 cycles: tries that a limit of a millisecond
+  // and more does not see come first)
+  const int tries = limit_ns < 1000000 ? 0 : 32;
+  for (int i = 0; i < tries; ++i) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     if (*stop) return false;
   }
