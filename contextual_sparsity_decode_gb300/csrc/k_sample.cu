@@ -2,10 +2,12 @@
 // the softmax at temperature T, cut to the top k, to the nucleus of mass p and to
 // the tokens that have min_p of the best one's probability.
 //
-// Weights are integers, w(x) = 2^39 exp((x - max) / T) rounded, from arithmetic
-// that is exact to 2^-30 of the weight: sums of them are exact whatever their order, so that
-// the cut and the token are those of the definition unless u (or p) is within
-// about 1e-10 of a border, and results do not depend on how a row is split.
+// Weights are integers, w(x) = 2^39 exp((x - max) / T) rounded: off by half a unit, 2^-40
+// of the best token's weight, and by 2^-29 of themselves before that rounding (2^-31 near the
+// best token, 2^-30 down to 2^-10 of its weight).  Sums of them are exact whatever their order, so that
+// the cut and the token are those of the definition unless a weight is that near to
+// min_p, or a sum over n tokens within 2^-29 of itself and n 2^-40 of its border with u or p,
+// and results do not depend on how a row is split.
 // (With sums of 32-bit exponentials, 1e-6 off, one row in ten of a large
 // vocabulary would draw a neighbour.)
 //

@@ -501,10 +501,13 @@ dv_status dv_sample_workspace_size(int B, int V, size_t* bytes);
  *     are never drawn.
  *  u [B] in [0, 1) (below counts as 0, above as just below 1); temperature,
  *     top_p, min_p [B] fp32, top_k [B] int32, each or NULL: 1, 1, 0, 0.
- * Weights are held to 2^-30 of themselves or 2^-40 (1 being the best token's)
- * and added without rounding: the token is the one of the formulas in exact
- * arithmetic unless u or top_p lies that near to a border.  Results repeat bit for
- * bit, whatever else is in the batch.
+ * Weights are held to 2^-29 of themselves and 2^-40 (1 being the best token's;
+ * below 2^-40 they count as none) and added without rounding: a sum over n
+ * tokens is off by 2^-29 of itself and n 2^-40 at most (4.8e-7 of the best
+ * token's weight for 524288 of them; each is as likely to be up as down).  The
+ * token is the one of the formulas in exact arithmetic unless a border lies
+ * that near: a token's weight to min_p, a sum to its share top_p or u of
+ * another.  Results repeat bit for bit, whatever else is in the batch.
  * A row without a distribution (a NaN or +inf, or nothing above -inf, among its
  * logits; another temperature; a NaN as u, top_p or min_p)
  * gets token -1 and prob 0 and is reported as DV_ERR_INVALID_ARG with b; other
