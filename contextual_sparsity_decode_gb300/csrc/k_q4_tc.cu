@@ -441,7 +441,10 @@ size_t q4_tc_part_floats(int B) { return B < 2 ? 0 : (size_t)2 * kQ4Splits * B *
 //         8     9.0   5.6   12.5  11.9   17.8  17.7    43    51
 //        16     9.9   6.0   13.7  13.4   19.2  20.8    45    63
 //        32    13.2   7.8   18.0  22.1   23.3  37.1    51   123
-// (rows of 1024 change sides at about twice as many rows, of 12288 at half).  Tiles of a list are
+// The rule looks at rows and vectors alone, and the border moves with the rows' length: for 8, 16 and
+// 32 vectors it lies at 20000, 20000 and 5000 rows of 1024, and at 6000, 4000 and 3000 of 12288.  In
+// between the slower form is taken, by a fourth at most (8 vectors by 10240 rows of 1024: 8.9 here and 7.0
+// there; 32 by 3584 of 12288: 20.0 and 25.1).  Tiles of a list are
 // not cut, and a list is mostly shorter than its bound.
 // 32-bit vectors count three times.
 bool q4_tc_takes(const Q4Rows& a) {

@@ -35,7 +35,10 @@ from . import binding as dv
 
 def quantize_mlp(layers: List[Dict[str, torch.Tensor]], group: int = 128) -> List[dict]:
     """The same layers with their MLP in 4 bits (W1q and W2q in the place of
-    W1n and W2n; groups of 64 or 128 weights share a scale)."""
+    W1n and W2n; groups of 64 or 128 weights share a scale): a quarter of the
+    memory.  Steps over few neurons of one sequence are slower than in 16 bits
+    (40 layers of 5120, 5 % of 20480 neurons, groups of 128: 49 us a layer, 41 in
+    f16; 8 sequences 158 and 161)."""
     out = []
     for W in layers:
         W = dict(W)
@@ -342,7 +345,8 @@ class SparseDecoder:
     # ------------------------------------------------------------------ the next token
     def set_head(self, head: dv.Q4):
         """The output head of ``sample``: a 4-bit matrix [V][d] (its row v
-        scores token v), and the buffers that go with it."""
+        scores token v), and the buffers that go with it (a graph that has
+        captured ``sample`` is captured again after another head)."""
         if head.d != self.d or head.dtype != self.dtype or head.q.device != self.device:
             raise ValueError(f"a 4-bit matrix with rows of {self.d} of {self.dtype} on {self.device} is wanted")
         dev, B = self.device, self.B

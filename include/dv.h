@@ -251,8 +251,9 @@ dv_status dv_q4_matvec_workspace_size(int B, int d, int N, size_t* bytes);
  * y [B][d] in the storage type of the scales, out [B][N] fp32, see
  * dv_sparse_mlp for `accumulate`.  Codes and scales enter as they are.  For one
  * vector, and for two of up to 22528 elements, y enters in fixed point, 30 bits
- * below the largest magnitude of each group of elements, else as it is; sums are fp32 and
- * results repeat bit for bit.  A NaN or an infinity in y makes the products of that
+ * below the largest magnitude of each group of elements (a scale times that magnitude
+ * is taken in fp32: below 2^-120 it loses bits, above 2^127 a product may be a NaN),
+ * else as it is; sums are fp32 and results repeat bit for bit.  A NaN or an infinity in y makes the products of that
  * vector NaN or infinite and no other's.  Like dv_layernorm's, its first
  * kernel may be started before the kernel ahead of the call has ended and waits
  * for it before it reads or writes anything.
