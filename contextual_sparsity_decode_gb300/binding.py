@@ -165,6 +165,15 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _torch_stream(stream) -> Optional[torch.cuda.Stream]:
+    """What torch.cuda.stream takes for a stream argument (a Stream, a handle, None)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream)
+    # (an ExternalStream of handle 0 would be a new stream)
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
 def _event(ev) -> ctypes.c_void_p:
     if ev is None:
         return ctypes.c_void_p(0)
@@ -330,7 +339,7 @@ class Q4:
         """W [N][d] quantised (dv_q4_quantize).  With a stream the buffers are
         allocated and zero-filled on it too (on the current one the fill could
         come after the codes)."""
-        with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(_stream(stream))):
+        with torch.cuda.stream(_torch_stream(stream)):
             out = cls.empty(W.shape[0], W.shape[1], W.dtype, group, W.device)
             dv_q4_quantize(W, out, stream=stream)
         return out
